@@ -19,6 +19,8 @@ GS_OK, GS_ERR_INVALID_ARG, GS_ERR_UNSUPPORTED, GS_ERR_WORKSPACE, GS_ERR_HIP = ra
 GS_SH_F32, GS_SH_F16, GS_SH_Q8 = 0, 1, 2
 GS_ADAM_F32, GS_ADAM_Q8LOG = 0, 1
 GS_ADAM_DENSE, GS_ADAM_LAZY = 0, 1
+GS_DTYPE_F32, GS_DTYPE_F16, GS_DTYPE_BF16, GS_DTYPE_MXFP8 = 0, 1, 2, 3
+GS_ACT = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 SPLAT_FLOATS = 12          # gs_splat is 48 bytes
 
 
@@ -77,6 +79,45 @@ class GsShAdam(C.Structure):
                 ("m_bounds", C.c_void_p), ("v_bounds", C.c_void_p)]
 
 
+class GsRmsNorm(C.Structure):
+    _fields_ = [("m", C.c_int64), ("n", C.c_int32), ("dtype", C.c_int32), ("y_dtype", C.c_int32), ("eps", C.c_float),
+                ("x", C.c_void_p), ("x_stride", C.c_int64), ("residual", C.c_void_p), ("residual_stride", C.c_int64),
+                ("gamma", C.c_void_p), ("sum", C.c_void_p), ("sum_stride", C.c_int64), ("y", C.c_void_p),
+                ("y_stride", C.c_int64), ("y_scales", C.c_void_p), ("y_scales_stride", C.c_int64),
+                ("rstd", C.c_void_p)]
+
+
+class GsRmsNormGrads(C.Structure):
+    _fields_ = [("m", C.c_int64), ("n", C.c_int32), ("dtype", C.c_int32), ("sum", C.c_void_p),
+                ("sum_stride", C.c_int64), ("rstd", C.c_void_p), ("gamma", C.c_void_p), ("dy", C.c_void_p),
+                ("dy_stride", C.c_int64), ("dsum", C.c_void_p), ("dsum_stride", C.c_int64), ("dx", C.c_void_p),
+                ("dx_stride", C.c_int64), ("dgamma", C.c_void_p), ("accumulate", C.c_int32)]
+
+
+class GsLinear(C.Structure):
+    _fields_ = [("m", C.c_int64), ("n", C.c_int32), ("k", C.c_int32), ("dtype", C.c_int32), ("y_dtype", C.c_int32),
+                ("activation", C.c_int32), ("planes", C.c_int32), ("x", C.c_void_p), ("x_stride", C.c_int64),
+                ("w", C.c_void_p), ("w_stride", C.c_int64), ("x_scales", C.c_void_p), ("x_scales_stride", C.c_int64),
+                ("w_scales", C.c_void_p), ("w_scales_stride", C.c_int64), ("bias", C.c_void_p),
+                ("residual", C.c_void_p), ("residual_stride", C.c_int64), ("y", C.c_void_p), ("y_stride", C.c_int64),
+                ("z", C.c_void_p), ("z_stride", C.c_int64)]
+
+
+class GsLinearGrads(C.Structure):
+    _fields_ = [("dy", C.c_void_p), ("dy_stride", C.c_int64), ("dx", C.c_void_p), ("dx_stride", C.c_int64),
+                ("dw", C.c_void_p), ("dw_stride", C.c_int64), ("dw_dtype", C.c_int32), ("accumulate", C.c_int32),
+                ("db", C.c_void_p)]
+
+
+class GsMuon(C.Structure):
+    _fields_ = [("batch", C.c_int32), ("rows", C.c_int32), ("cols", C.c_int32), ("grad_dtype", C.c_int32),
+                ("out_dtype", C.c_int32), ("steps", C.c_int32), ("a", C.c_float), ("b", C.c_float), ("c", C.c_float),
+                ("eps", C.c_float), ("lr", C.c_float), ("beta", C.c_float), ("weight_decay", C.c_float),
+                ("scale", C.c_float), ("nesterov", C.c_int32), ("grad", C.c_void_p), ("out", C.c_void_p),
+                ("momentum", C.c_void_p), ("momentum_out", C.c_void_p), ("weight", C.c_void_p),
+                ("weight_out", C.c_void_p)]
+
+
 class GsError(RuntimeError):
     pass
 
@@ -89,7 +130,10 @@ SYMBOLS = ("gs_project", "gs_bin_sort_workspace_bytes", "gs_schedule_words", "gs
            "gs_render_bwd_workspace_bytes", "gs_render_bwd", "gs_render_bwd_screen_workspace_bytes",
            "gs_render_bwd_screen", "gs_project_bwd", "gs_project_bwd_binned", "gs_active_mask_workspace_bytes",
            "gs_active_mask", "gs_active_mask_static", "gs_active_mask_static_scratch_bytes",
-           "gs_sh_q8_bounds_floats", "gs_sh_quantize8", "gs_sh_adam_step", "gs_status_string",
+           "gs_sh_q8_bounds_floats", "gs_sh_quantize8", "gs_sh_adam_step", "gs_rms_norm_fwd",
+           "gs_rms_norm_bwd_workspace_bytes", "gs_rms_norm_bwd", "gs_mxfp8_quantize", "gs_linear_fwd_workspace_bytes",
+           "gs_linear_fwd", "gs_linear_bwd_workspace_bytes", "gs_linear_bwd", "gs_muon_workspace_bytes",
+           "gs_orthogonalize", "gs_muon_step", "gs_status_string",
            "gs_version")
 
 
@@ -146,6 +190,21 @@ def lib():
     L.gs_sh_q8_bounds_floats.restype = sz
     L.gs_sh_quantize8.argtypes = [vp, i64, C.c_int32, vp, vp, vp]
     L.gs_sh_adam_step.argtypes = [C.POINTER(GsShAdam), vp]
+    L.gs_rms_norm_fwd.argtypes = [C.POINTER(GsRmsNorm), vp]
+    L.gs_rms_norm_bwd_workspace_bytes.argtypes = [i64, C.c_int32]
+    L.gs_rms_norm_bwd_workspace_bytes.restype = sz
+    L.gs_rms_norm_bwd.argtypes = [C.POINTER(GsRmsNormGrads), vp, sz, vp]
+    L.gs_mxfp8_quantize.argtypes = [vp, C.c_int32, i64, C.c_int32, i64, vp, i64, vp, i64, vp]
+    L.gs_linear_fwd_workspace_bytes.argtypes = [C.POINTER(GsLinear)]
+    L.gs_linear_fwd_workspace_bytes.restype = sz
+    L.gs_linear_fwd.argtypes = [C.POINTER(GsLinear), vp, sz, vp]
+    L.gs_linear_bwd_workspace_bytes.argtypes = [C.POINTER(GsLinear), C.POINTER(GsLinearGrads)]
+    L.gs_linear_bwd_workspace_bytes.restype = sz
+    L.gs_linear_bwd.argtypes = [C.POINTER(GsLinear), C.POINTER(GsLinearGrads), vp, sz, vp]
+    L.gs_muon_workspace_bytes.argtypes = [C.POINTER(GsMuon)]
+    L.gs_muon_workspace_bytes.restype = sz
+    L.gs_orthogonalize.argtypes = [C.POINTER(GsMuon), vp, sz, vp]
+    L.gs_muon_step.argtypes = [C.POINTER(GsMuon), vp, sz, vp]
     L.gs_status_string.restype = C.c_char_p
     L.gs_status_string.argtypes = [C.c_int]
     L.gs_version.restype = C.c_int32
@@ -154,7 +213,8 @@ def lib():
                  "gs_render_bwd",
                  "gs_render_bwd_screen", "gs_render_bwd_screen_views",
                  "gs_project_bwd", "gs_project_bwd_binned", "gs_active_mask", "gs_active_mask_static",
-                 "gs_sh_quantize8"):
+                 "gs_sh_quantize8", "gs_rms_norm_fwd", "gs_rms_norm_bwd", "gs_mxfp8_quantize", "gs_linear_fwd",
+                 "gs_linear_bwd", "gs_orthogonalize", "gs_muon_step"):
         getattr(L, name).restype = C.c_int
     _lib = L
     return L
@@ -455,6 +515,204 @@ def active_mask_static(scores, n, keep, mask, stream=None):
     nothing allocated (n up to 2^30)."""
     _check(lib().gs_active_mask_static(_ptr(scores), int(n), int(keep), _ptr(mask), _stream(stream)),
            "gs_active_mask_static")
+
+
+# ---- a network head that predicts Gaussians ---------------------------------
+_DTYPES = {torch.float32: GS_DTYPE_F32, torch.float16: GS_DTYPE_F16, torch.bfloat16: GS_DTYPE_BF16,
+           torch.float8_e4m3fn: GS_DTYPE_MXFP8}
+_SCALES = (torch.uint8, torch.float8_e8m0fnu)
+
+
+def _dtype(t: torch.Tensor) -> int:
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        raise ValueError(f"unsupported element type {t.dtype}")
+    return d
+
+
+def _rows(t: Optional[torch.Tensor], rows: int, cols: int, what: str, dtype=None, device=None):
+    """(pointer, row stride) of an [rows][cols] tensor whose rows are
+    contiguous; (None, cols) for None."""
+    if t is None:
+        return None, cols
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{what}: expected [{rows}][{cols}], got {tuple(t.shape)}")
+    if dtype is not None and (t.dtype not in dtype if isinstance(dtype, tuple) else t.dtype != dtype):
+        raise ValueError(f"{what}: unexpected element type {t.dtype}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{what}: on {t.device}, expected {device}")
+    s = t.stride()
+    if (cols > 1 and s[1] != 1) or (rows > 1 and s[0] < cols):
+        raise ValueError(f"{what}: rows must be contiguous and must not overlap (strides {s})")
+    return t.data_ptr(), (s[0] if rows > 1 else cols)
+
+
+def _vector(t: Optional[torch.Tensor], n: int, what: str, device=None):
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous() or (device is not None and t.device != device):
+        raise ValueError(f"{what}: expected {n} contiguous float32 values on {device}")
+    return t.data_ptr()
+
+
+def rms_norm_fwd(x: torch.Tensor, y: torch.Tensor, gamma: Optional[torch.Tensor] = None,
+                 residual: Optional[torch.Tensor] = None, sum_out: Optional[torch.Tensor] = None,
+                 rstd: Optional[torch.Tensor] = None, y_scales: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 stream=None):
+    """gs_rms_norm_fwd over the rows of x [m][n] (float32, float16 or
+    bfloat16): y = (x + residual) * rstd * gamma in x's type, or
+    torch.float8_e4m3fn with y_scales [m][n / 32] (uint8 or float8_e8m0fnu)."""
+    m, n = x.shape
+    a = GsRmsNorm(m=m, n=n, dtype=_dtype(x), y_dtype=_dtype(y), eps=eps)
+    a.x, a.x_stride = _rows(x, m, n, "x")
+    a.residual, a.residual_stride = _rows(residual, m, n, "residual", x.dtype, x.device)
+    a.sum, a.sum_stride = _rows(sum_out, m, n, "sum_out", x.dtype, x.device)
+    a.y, a.y_stride = _rows(y, m, n, "y", (x.dtype, torch.float8_e4m3fn), x.device)
+    a.y_scales, a.y_scales_stride = _rows(y_scales, m, n // 32, "y_scales", _SCALES, x.device)
+    a.gamma, a.rstd = _vector(gamma, n, "gamma", x.device), _vector(rstd, m, "rstd", x.device)
+    _check(lib().gs_rms_norm_fwd(C.byref(a), _stream(stream)), "gs_rms_norm_fwd")
+
+
+def rms_norm_bwd_workspace_bytes(m: int, n: int) -> int:
+    return int(lib().gs_rms_norm_bwd_workspace_bytes(m, n))
+
+
+def rms_norm_bwd(sum_in: torch.Tensor, rstd: torch.Tensor, dy: torch.Tensor, dx: torch.Tensor,
+                 gamma: Optional[torch.Tensor] = None, dsum: Optional[torch.Tensor] = None,
+                 dgamma: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                 accumulate: bool = False, stream=None):
+    """gs_rms_norm_bwd: from the kept sum (x without a residual) and rstd, the
+    gradient dx of x and residual and, with dgamma and a workspace of
+    rms_norm_bwd_workspace_bytes(m, n), that of gamma."""
+    m, n = sum_in.shape
+    t, dev = sum_in.dtype, sum_in.device
+    a = GsRmsNormGrads(m=m, n=n, dtype=_dtype(sum_in), accumulate=1 if accumulate else 0)
+    a.sum, a.sum_stride = _rows(sum_in, m, n, "sum_in")
+    a.dy, a.dy_stride = _rows(dy, m, n, "dy", t, dev)
+    a.dsum, a.dsum_stride = _rows(dsum, m, n, "dsum", t, dev)
+    a.dx, a.dx_stride = _rows(dx, m, n, "dx", t, dev)
+    a.rstd, a.gamma = _vector(rstd, m, "rstd", dev), _vector(gamma, n, "gamma", dev)
+    a.dgamma = _vector(dgamma, n, "dgamma", dev)
+    _check(lib().gs_rms_norm_bwd(C.byref(a), _ptr(workspace), _nbytes(workspace), _stream(stream)), "gs_rms_norm_bwd")
+
+
+def mxfp8_quantize(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None):
+    """gs_mxfp8_quantize: x [m][n] -> codes float8_e4m3fn [m][n] and scales
+    [m][n / 32] (uint8 or float8_e8m0fnu)."""
+    m, n = x.shape
+    xp, xs = _rows(x, m, n, "x")
+    cp, cs = _rows(codes, m, n, "codes", torch.float8_e4m3fn, x.device)
+    sp, ss = _rows(scales, m, n // 32, "scales", _SCALES, x.device)
+    _check(lib().gs_mxfp8_quantize(xp, _dtype(x), m, n, xs, cp, cs, sp, ss, _stream(stream)), "gs_mxfp8_quantize")
+
+
+def linear_struct(x: torch.Tensor, w: torch.Tensor, y: Optional[torch.Tensor],
+                  bias: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+                  z: Optional[torch.Tensor] = None, act: str = "none", planes: bool = False,
+                  x_scales: Optional[torch.Tensor] = None, w_scales: Optional[torch.Tensor] = None) -> GsLinear:
+    """Descriptor of y = act(x w^T + bias) + residual: x [m][k] and w [n][k] of
+    one type; y [m][n], or with planes [n][m] (None for the backward alone);
+    z: the pre-activation kept for the backward, [m][n] of x's type."""
+    m, k = x.shape
+    n = w.shape[0]
+    a = GsLinear(m=m, n=n, k=k, dtype=_dtype(x), y_dtype=_dtype(x if y is None else y), activation=GS_ACT[act],
+                 planes=1 if planes else 0)
+    rows, cols = (n, m) if planes else (m, n)
+    a.x, a.x_stride = _rows(x, m, k, "x")
+    a.w, a.w_stride = _rows(w, n, k, "w", x.dtype, x.device)
+    if x.dtype == torch.float8_e4m3fn:
+        a.x_scales, a.x_scales_stride = _rows(x_scales, m, k // 32, "x_scales", _SCALES, x.device)
+        a.w_scales, a.w_scales_stride = _rows(w_scales, n, k // 32, "w_scales", _SCALES, x.device)
+    a.bias = _vector(bias, n, "bias", x.device)
+    a.y, a.y_stride = _rows(y, rows, cols, "y", None, x.device)
+    a.residual, a.residual_stride = _rows(residual, rows, cols, "residual", None if y is None else y.dtype, x.device)
+    a.z, a.z_stride = _rows(z, m, n, "z", x.dtype, x.device)
+    return a
+
+
+def linear_fwd_workspace_bytes(a: GsLinear) -> int:
+    return int(lib().gs_linear_fwd_workspace_bytes(C.byref(a)))
+
+
+def linear_fwd(a: GsLinear, workspace: Optional[torch.Tensor] = None, stream=None):
+    """gs_linear_fwd of a linear_struct; the tensors it was made from must be
+    alive."""
+    _check(lib().gs_linear_fwd(C.byref(a), _ptr(workspace), _nbytes(workspace), _stream(stream)), "gs_linear_fwd")
+
+
+def linear_grads_struct(a: GsLinear, dy: torch.Tensor, dx: Optional[torch.Tensor] = None,
+                        dw: Optional[torch.Tensor] = None, db: Optional[torch.Tensor] = None,
+                        accumulate: bool = False) -> GsLinearGrads:
+    """Descriptor of the gradients of a linear_struct: dy in y's layout; dx
+    [m][k] of x's type, dw [n][k] of float32 or x's type, db [n] float32, each
+    optional; accumulate adds to dw and db.  Sets the descriptor's y_dtype to
+    dy's."""
+    rows, cols = (a.n, a.m) if a.planes else (a.m, a.n)
+    a.y_dtype = _dtype(dy)
+    own = [t for t, d in _DTYPES.items() if d == a.dtype][0]
+    g = GsLinearGrads(accumulate=1 if accumulate else 0)
+    g.dy, g.dy_stride = _rows(dy, rows, cols, "dy")
+    g.dx, g.dx_stride = _rows(dx, a.m, a.k, "dx", own, dy.device)
+    g.dw, g.dw_stride = _rows(dw, a.n, a.k, "dw", (own, torch.float32), dy.device)
+    g.dw_dtype = GS_DTYPE_F32 if dw is None else _dtype(dw)
+    g.db = _vector(db, a.n, "db", dy.device)
+    return g
+
+
+def linear_bwd_workspace_bytes(a: GsLinear, g: GsLinearGrads) -> int:
+    return int(lib().gs_linear_bwd_workspace_bytes(C.byref(a), C.byref(g)))
+
+
+def linear_bwd(a: GsLinear, g: GsLinearGrads, workspace: Optional[torch.Tensor] = None, stream=None):
+    """gs_linear_bwd of a linear_struct and its linear_grads_struct."""
+    _check(lib().gs_linear_bwd(C.byref(a), C.byref(g), _ptr(workspace), _nbytes(workspace), _stream(stream)),
+           "gs_linear_bwd")
+
+
+def muon_struct(grad: torch.Tensor, out: Optional[torch.Tensor] = None, momentum: Optional[torch.Tensor] = None,
+                weight: Optional[torch.Tensor] = None, momentum_out: Optional[torch.Tensor] = None,
+                weight_out: Optional[torch.Tensor] = None, lr: float = 0.02, beta: float = 0.95,
+                weight_decay: float = 0.0, scale: float = 1.0, nesterov: bool = True, steps: int = 5,
+                coeffs: Sequence[float] = (3.4445, -4.7750, 2.0315), eps: float = 1e-7) -> GsMuon:
+    """Descriptor of gs_orthogonalize (grad and out) and gs_muon_step (grad,
+    momentum, weight; momentum_out and weight_out default to updating in
+    place): contiguous [rows][cols] or [batch][rows][cols] arrays, momentum
+    float32, the others float32, float16 or bfloat16."""
+    shape = grad.shape
+    if len(shape) not in (2, 3):
+        raise ValueError("grad: expected [rows][cols] or [batch][rows][cols]")
+    momentum_out = momentum if momentum_out is None else momentum_out
+    weight_out = weight if weight_out is None else weight_out
+    for t, what in ((grad, "grad"), (out, "out"), (momentum, "momentum"), (weight, "weight"),
+                    (momentum_out, "momentum_out"), (weight_out, "weight_out")):
+        if t is not None and (t.shape != shape or not t.is_contiguous() or t.device != grad.device):
+            raise ValueError(f"{what}: arrays must be contiguous, of one shape and on one device")
+    for t, what in ((momentum, "momentum"), (momentum_out, "momentum_out")):
+        if t is not None and t.dtype != torch.float32:
+            raise ValueError(f"{what}: expected float32")
+    if weight is not None and weight.dtype != weight_out.dtype:
+        raise ValueError("weight_out: expected weight's type")
+    a = GsMuon(batch=shape[0] if len(shape) == 3 else 1, rows=shape[-2], cols=shape[-1], grad_dtype=_dtype(grad),
+               out_dtype=_dtype(grad if out is None and weight is None else out if weight is None else weight),
+               steps=steps, a=coeffs[0], b=coeffs[1], c=coeffs[2], eps=eps, lr=lr, beta=beta,
+               weight_decay=weight_decay, scale=scale, nesterov=1 if nesterov else 0)
+    a.grad, a.out, a.momentum, a.momentum_out = _ptr(grad), _ptr(out), _ptr(momentum), _ptr(momentum_out)
+    a.weight, a.weight_out = _ptr(weight), _ptr(weight_out)
+    return a
+
+
+def muon_workspace_bytes(a: GsMuon) -> int:
+    return int(lib().gs_muon_workspace_bytes(C.byref(a)))
+
+
+def orthogonalize(a: GsMuon, workspace: torch.Tensor, stream=None):
+    """gs_orthogonalize: a's out receives the orthogonalised grad."""
+    _check(lib().gs_orthogonalize(C.byref(a), _ptr(workspace), _nbytes(workspace), _stream(stream)), "gs_orthogonalize")
+
+
+def muon_step(a: GsMuon, workspace: torch.Tensor, stream=None):
+    """gs_muon_step: momentum, orthogonalised update and weight decay."""
+    _check(lib().gs_muon_step(C.byref(a), _ptr(workspace), _nbytes(workspace), _stream(stream)), "gs_muon_step")
 
 
 # ---- buffers for one view ---------------------------------------------------

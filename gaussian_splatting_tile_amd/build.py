@@ -20,12 +20,15 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgs_hip.so")
-SOURCES = ["gs_api.hip", "gs_project.hip", "gs_sort.hip", "gs_render.hip", "gs_mask.hip", "gs_adam.hip"]
+SOURCES = ["gs_api.hip", "gs_project.hip", "gs_sort.hip", "gs_render.hip", "gs_mask.hip", "gs_adam.hip",
+           "gs_norm.hip", "gs_linear.hip", "gs_product_bf16.hip", "gs_product_f16.hip", "gs_product_f32.hip",
+           "gs_product_mx8.hip", "gs_muon.hip"]
 # the peak-rate microbenchmarks the roofline fractions are also taken against
 # (not part of the rasterizer's ABI)
 PEAKS_LIB = os.path.join(PKG, "libgs_peaks.so")
 PEAKS_SOURCES = ["peaks.hip"]
-HEADERS = [os.path.join(CSRC, "gs_internal.h"), os.path.join(CSRC, "gs_adam.h"), os.path.join(INCLUDE, "gs.h")]
+HEADERS = [os.path.join(CSRC, h) for h in ("gs_internal.h", "gs_adam.h", "gs_numeric.h", "gs_gemm.h", "gs_linear.h",
+                                           "gs_product_16.h")] + [os.path.join(INCLUDE, "gs.h")]
 ARCH = os.environ.get("GS_OFFLOAD_ARCH", "gfx950")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

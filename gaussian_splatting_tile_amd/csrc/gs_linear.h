@@ -1,0 +1,122 @@
+// Internal declarations of the linear layer: the epilogue of its products and
+// the launchers of each kind of operand (public interface: gs_linear_fwd and
+// gs_linear_bwd in include/gs.h).
+#pragma once
+
+#include "gs_gemm.h"
+
+namespace gsi {
+
+// What becomes of a product's sums.  With `partial` they are stored as they
+// are, one fp32 array [q][ld_partial] per split, and reduced by a second
+// kernel; otherwise
+//   z = sum + bias;  y = act(z) + residual (+ y if accumulate).
+struct LinearEpilogue {
+    struct Args {
+        float *partial;
+        int64_t ld_partial, split_stride;
+        const float *bias;
+        int bias_on_q;                  // bias[q] (planes) or bias[p]
+        int act, exact;                 // exact: fp32 results, library erf and exp
+        const void *residual;
+        int64_t ldr;
+        void *y;                        // residual and y: element q * ld + p
+        int64_t ldy;
+        int y_type, accumulate;
+        void *z;                        // element q * z_q + p * z_p
+        int64_t z_q, z_p;
+        int z_type;
+        int vec;                        // 8 consecutive p may be read and written as vectors
+    };
+
+    // One value, any layout.
+    __device__ static __forceinline__ void finish1(const Args &e, int p, int q, float v)
+    {
+        const int64_t at = (int64_t)q * e.ldy + p;
+        if (e.bias) v += e.bias[e.bias_on_q ? q : p];
+        if (e.z) store_from_float(e.z, e.z_type, (int64_t)q * e.z_q + (int64_t)p * e.z_p, v);
+        v = e.exact ? activate<true>(v, e.act) : activate<false>(v, e.act);
+        if (e.residual) v += load_as_float(e.residual, e.y_type, (int64_t)q * e.ldr + p);
+        if (e.accumulate) v += load_as_float(e.y, e.y_type, at);
+        store_from_float(e.y, e.y_type, at, v);
+    }
+
+    // Eight values p .. p + 7, vec set.
+    __device__ static __forceinline__ void finish8(const Args &e, int p, int q, float v[8])
+    {
+        const int64_t at = (int64_t)q * e.ldy + p;
+        if (e.bias) {
+            const float b = e.bias_on_q ? e.bias[q] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[i] += e.bias_on_q ? b : e.bias[p + i];
+        }
+        if (e.z) {
+            if (e.z_p == 1) {
+                store8_vec(e.z, e.z_type, (int64_t)q * e.z_q + p, v);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; i++) store_from_float(e.z, e.z_type, (int64_t)q * e.z_q + (int64_t)(p + i) * e.z_p, v[i]);
+            }
+        }
+        if (e.act != GS_ACT_NONE) {
+            if (e.exact) {
+#pragma unroll
+                for (int i = 0; i < 8; i++) v[i] = activate<true>(v[i], e.act);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; i++) v[i] = activate<false>(v[i], e.act);
+            }
+        }
+        float r[8];
+        if (e.residual) {
+            load8_vec(e.residual, e.y_type, (int64_t)q * e.ldr + p, r);
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[i] += r[i];
+        }
+        if (e.accumulate) {
+            load8_vec(e.y, e.y_type, at, r);
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[i] += r[i];
+        }
+        store8_vec(e.y, e.y_type, at, v);
+    }
+
+    __device__ static __forceinline__ void finish(const Args &e, int p, int q, int valid, const float *s)
+    {
+        if (e.vec && valid == 8) {
+            float v[8];
+            load8_vec(s, v);
+            finish8(e, p, q, v);
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < valid; i++) finish1(e, p + i, q, s[i]);
+        }
+    }
+
+    __device__ static __forceinline__ void store(const Args &e, int p, int q, int valid, const float *s, int, int split)
+    {
+        if (e.partial) {
+            float v[8];
+            load8_vec(s, v);                                    // rows of partial sums are padded to 8
+            store8_vec(e.partial + split * e.split_stride + (int64_t)q * e.ld_partial + p, v);
+            return;
+        }
+        finish(e, p, q, valid, s);
+    }
+};
+
+// One product of the linear layer: which operands are stored by columns,
+// which tile and how many splits of k.
+struct ProductPlan {
+    bool pt, qt;
+    bool staged;
+    int tile;                           // 0: 256 x 256, 1: 128 x 128, 2: 64 x 64 (staged: 1 and 2)
+    int splits;                         // of k, each with at least one tile of k
+};
+
+hipError_t launch_product_bf16(const gemm::Args &a, const LinearEpilogue::Args &e, const ProductPlan &plan, hipStream_t s);
+hipError_t launch_product_f16(const gemm::Args &a, const LinearEpilogue::Args &e, const ProductPlan &plan, hipStream_t s);
+hipError_t launch_product_f32(const gemm::Args &a, const LinearEpilogue::Args &e, const ProductPlan &plan, hipStream_t s);
+hipError_t launch_product_mx8(const gemm::Args &a, const LinearEpilogue::Args &e, const ProductPlan &plan, hipStream_t s);
+
+}  // namespace gsi

@@ -1,0 +1,516 @@
+// Linear layer: argument checks, choice of tile and split, and the passes
+// around its products (see gs_gemm.h for the products themselves).
+//
+// Forward: one product, out[q][p] with p the contiguous index of y: rows take
+// p = outputs (P = w, Q = x), planes take p = rows of x (P = x, Q = w), so both
+// layouts are written with full-width stores and neither is transposed.
+// Backward: dz = dy act'(z) and the partial sums of db in one pass over dy and
+// z (skipped when dz is dy as it stands), then dx[m][k] = dz w and
+// dw[n][k] = dz^T x, whose operands are read by columns where k is theirs.
+#include <string.h>
+
+#include "gs_linear.h"
+
+namespace gsi {
+namespace {
+
+constexpr int kThreads = 256;
+
+bool aligned_to(const void *p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
+bool float_type(int t) { return t == GS_DTYPE_F32 || t == GS_DTYPE_F16 || t == GS_DTYPE_BF16; }
+bool al16(const void *p) { return aligned_to(p, 16); }
+size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// ---- choice of tile and split -----------------------------------------------
+// Estimated time in microseconds of a tile choice: rounds of blocks over the
+// 256 CUs, each CU working through its resident blocks at `rate`, plus what a
+// split of k costs to reduce.  The rates are measured ones at full occupancy.
+struct TileRate { int size, resident; float mflop_us; };        // per CU
+
+double product_cost(const TileRate &t, int64_t P, int64_t Q, int64_t K, int splits, float work)
+{
+    const double blocks = (double)((P + t.size - 1) / t.size) * (double)((Q + t.size - 1) / t.size) * splits;
+    const double per_cu = ceil(blocks / 256.0);
+    // fewer blocks than the CU holds leave some of its rate unused
+    const double filled = per_cu < t.resident ? 0.5 + 0.5 * per_cu / t.resident : 1.0;
+    const double tile = 2e-6 * t.size * t.size * (ceil((double)K / splits) + 64.0) * work;
+    double us = per_cu * tile / (t.mflop_us * filled);
+    if (splits > 1) us += 4.0 + splits * (double)P * (double)Q * 8.0 / 4e6;
+    return us;
+}
+
+ProductPlan make_plan(int64_t P, int64_t Q, int64_t K, bool pt, bool qt, bool staged, int step_k, float work)
+{
+    static const TileRate direct[3] = {{256, 1, 5.0f}, {128, 2, 3.6f}, {64, 4, 1.8f}};
+    static const TileRate staged_[3] = {{256, 1, 0.0f}, {128, 1, 2.0f}, {64, 3, 1.2f}};
+    ProductPlan best{pt, qt, staged, 2, 1};
+    double least = 1e30;
+    const int64_t nt = (K + step_k - 1) / step_k;
+    for (int tile = staged ? 1 : 0; tile < 3; tile++) {
+        const TileRate &t = staged ? staged_[tile] : direct[tile];
+        for (int64_t want = 1; want <= 64 && want <= nt; want = want < 4 ? want + 1 : want * 2) {
+            const int64_t per = (nt + want - 1) / want;
+            const int splits = (int)((nt + per - 1) / per);
+            const double us = product_cost(t, P, Q, K, splits, work);
+            if (us < least * 0.98) {
+                least = us;
+                best.tile = tile;
+                best.splits = splits;
+            }
+        }
+    }
+    return best;
+}
+
+// One product with its plan; everything but the workspace address.
+struct Product {
+    gemm::Args a;
+    LinearEpilogue::Args e;
+    ProductPlan plan;
+    int kind;                           // gs_dtype of the operands
+    size_t partial_bytes;
+};
+
+bool vec_ok(const void *p, int type, int64_t ld) { return al16(p) && ld % (16 / dtype_bytes(type)) == 0; }
+
+void finish_plan(Product &r, bool direct)
+{
+    const int step = direct ? (r.kind == GS_DTYPE_MXFP8 ? 128 : 64) : 32;
+    r.a.p_vec = r.a.p_type != GS_DTYPE_MXFP8 && vec_ok(r.a.p, r.a.p_type, r.a.ldp);
+    r.a.q_vec = r.a.q_type != GS_DTYPE_MXFP8 && vec_ok(r.a.q, r.a.q_type, r.a.ldq);
+    const float work = r.kind == GS_DTYPE_F32 ? 6.0f : r.kind == GS_DTYPE_MXFP8 && direct ? 0.6f : 1.0f;
+    const bool pt = r.plan.pt, qt = r.plan.qt;
+    r.plan = make_plan(r.a.P, r.a.Q, r.a.K, pt, qt, !direct, step, work);
+    r.e.ld_partial = (r.a.P + 7) & ~7;
+    r.e.split_stride = r.e.ld_partial * r.a.Q;
+    r.partial_bytes = r.plan.splits > 1 ? (size_t)r.plan.splits * r.e.split_stride * 4 : 0;
+    r.e.vec = vec_ok(r.e.y, r.e.y_type, r.e.ldy) && (!r.e.residual || vec_ok(r.e.residual, r.e.y_type, r.e.ldr)) &&
+              (!r.e.z || r.e.z_p != 1 || vec_ok(r.e.z, r.e.z_type, r.e.z_q));
+    r.e.exact = r.e.y_type == GS_DTYPE_F32 || (r.e.z && r.e.z_type == GS_DTYPE_F32);
+}
+
+// Sum of the splits, then the epilogue: a thread per 8 consecutive p.
+__global__ __launch_bounds__(kThreads) void reduce_splits(LinearEpilogue::Args e, int P, int Q, int splits)
+{
+    __shared__ float sums[kThreads][12];        // 16-byte aligned rows
+    const int64_t groups = e.ld_partial / 8, id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (id >= groups * Q) return;
+    const int q = (int)(id / groups), p = (int)(id - q * groups) * 8;
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    const float *src = e.partial + (int64_t)q * e.ld_partial + p;
+    for (int s = 0; s < splits; s++) {
+        float w[8];
+        load8_vec(src + s * e.split_stride, w);
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[i] += w[i];
+    }
+    store8_vec(sums[threadIdx.x], v);           // read back by this thread alone
+    LinearEpilogue::finish(e, p, q, min(8, P - p), sums[threadIdx.x]);
+}
+
+hipError_t run_product(Product &r, void *partial, hipStream_t s)
+{
+    r.e.partial = r.plan.splits > 1 ? static_cast<float *>(partial) : nullptr;
+    hipError_t err;
+    if (r.kind == GS_DTYPE_MXFP8) err = launch_product_mx8(r.a, r.e, r.plan, s);
+    else if (r.kind == GS_DTYPE_F32) err = launch_product_f32(r.a, r.e, r.plan, s);
+    else if (r.kind == GS_DTYPE_F16) err = launch_product_f16(r.a, r.e, r.plan, s);
+    else err = launch_product_bf16(r.a, r.e, r.plan, s);
+    if (err != hipSuccess || r.plan.splits == 1) return err;
+    const int64_t n = r.e.ld_partial / 8 * r.a.Q;
+    reduce_splits<<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, s>>>(r.e, r.a.P, r.a.Q, r.plan.splits);
+    return hipGetLastError();
+}
+
+// ---- forward ------------------------------------------------------------------
+gs_status linear_ok(const gs_linear *l)
+{
+    if (!l) return GS_ERR_INVALID_ARG;
+    if (l->m < 0 || l->m > ((int64_t)1 << 30) || l->n < 1 || l->n > (1 << 20) || l->k < 1 || l->k > (1 << 20))
+        return GS_ERR_INVALID_ARG;
+    if (!float_type(l->dtype) && l->dtype != GS_DTYPE_MXFP8) return GS_ERR_INVALID_ARG;
+    if (l->y_dtype == GS_DTYPE_MXFP8) return GS_ERR_UNSUPPORTED;
+    if (!float_type(l->y_dtype)) return GS_ERR_INVALID_ARG;
+    if (l->activation < GS_ACT_NONE || l->activation > GS_ACT_GELU) return GS_ERR_INVALID_ARG;
+    if (l->dtype == GS_DTYPE_MXFP8 && (l->k % 32 != 0 || l->z)) return GS_ERR_UNSUPPORTED;
+    if ((l->m + 63) / 64 * ((l->n + 63) / 64) > INT32_MAX) return GS_ERR_UNSUPPORTED;
+    const int es = dtype_bytes(l->dtype);
+    if (l->x_stride < l->k || l->w_stride < l->k) return GS_ERR_INVALID_ARG;
+    if (l->m > 0 && (!l->x || !l->w)) return GS_ERR_INVALID_ARG;
+    if (!aligned_to(l->x, es) || !aligned_to(l->w, es) || !aligned_to(l->bias, 4)) return GS_ERR_INVALID_ARG;
+    if (l->dtype == GS_DTYPE_MXFP8 && ((l->m > 0 && (!l->x_scales || !l->w_scales)) || l->x_scales_stride < l->k / 32 ||
+                                       l->w_scales_stride < l->k / 32))
+        return GS_ERR_INVALID_ARG;
+    if (l->z && (l->z_stride < l->n || !aligned_to(l->z, es))) return GS_ERR_INVALID_ARG;
+    return GS_OK;
+}
+
+gs_status linear_fwd_ok(const gs_linear *l)
+{
+    const gs_status st = linear_ok(l);
+    if (st != GS_OK) return st;
+    const int64_t row = l->planes ? l->m : l->n;
+    const int ys = dtype_bytes(l->y_dtype);
+    if ((l->m > 0 && !l->y) || l->y_stride < row || !aligned_to(l->y, ys)) return GS_ERR_INVALID_ARG;
+    if (l->residual && (l->residual_stride < row || !aligned_to(l->residual, ys))) return GS_ERR_INVALID_ARG;
+    return GS_OK;
+}
+
+Product plan_fwd(const gs_linear &l)
+{
+    Product r;
+    memset(&r, 0, sizeof r);
+    const int es = dtype_bytes(l.dtype);
+    const bool px = l.planes != 0;              // the P operand is x
+    gemm::Args &a = r.a;
+    a.p = px ? l.x : l.w;
+    a.q = px ? l.w : l.x;
+    a.ldp = px ? l.x_stride : l.w_stride;
+    a.ldq = px ? l.w_stride : l.x_stride;
+    a.ps = px ? l.x_scales : l.w_scales;
+    a.qs = px ? l.w_scales : l.x_scales;
+    a.ldps = px ? l.x_scales_stride : l.w_scales_stride;
+    a.ldqs = px ? l.w_scales_stride : l.x_scales_stride;
+    a.P = a.Pl = (int)(px ? l.m : l.n);
+    a.Q = a.Ql = (int)(px ? l.n : l.m);
+    a.K = l.k;
+    a.p_type = a.q_type = l.dtype;
+    r.kind = l.dtype;
+    LinearEpilogue::Args &e = r.e;
+    e.bias = l.bias;
+    e.bias_on_q = px;
+    e.act = l.activation;
+    e.residual = l.residual;
+    e.ldr = l.residual_stride;
+    e.y = l.y;
+    e.ldy = l.y_stride;
+    e.y_type = l.y_dtype;
+    e.z = l.z;
+    e.z_type = l.dtype;
+    e.z_q = px ? 1 : l.z_stride;
+    e.z_p = px ? l.z_stride : 1;
+    // 8-bit matrix instructions only for 16-bit results: they keep fewer bits
+    // of a sum than fp32 holds
+    bool direct = l.dtype != GS_DTYPE_F32 && gemm::direct_ok(a.p, es, a.ldp, a.K) && gemm::direct_ok(a.q, es, a.ldq, a.K);
+    if (l.dtype == GS_DTYPE_MXFP8)
+        direct = direct && l.y_dtype != GS_DTYPE_F32 && a.ldps < (1 << 22) && a.ldqs < (1 << 22);
+    finish_plan(r, direct);
+    return r;
+}
+
+// ---- backward: dz and the sums of db -------------------------------------------
+struct DzArgs {
+    const void *dy, *z;
+    int64_t lddy, ldz;
+    int dy_type, type, act, exact;
+    void *dz;                           // [m][ld_dz] of `type`, zeros past n; NULL: not wanted
+    int64_t ld_dz;
+    float *part;                        // [row blocks][n] partial sums of db, or NULL
+    int64_t m;
+    int n, rows_per_block;
+    int vec;
+};
+
+// dy in rows.  A block takes `rows_per_block` rows of up to 512 columns: a
+// thread owns 8 columns and every (256 / groups)-th row.
+__global__ __launch_bounds__(kThreads) void dz_rows(DzArgs d, int groups)
+{
+    __shared__ float sums[kThreads][8];
+    const int cg = threadIdx.x % groups, rl = threadIdx.x / groups, lanes = kThreads / groups;
+    const int c0 = (blockIdx.x * groups + cg) * 8, valid = max(0, min(8, d.n - c0));
+    const int64_t r0 = (int64_t)blockIdx.y * d.rows_per_block, r1 = min(d.m, r0 + d.rows_per_block);
+    const int room = d.dz ? (int)max((int64_t)0, min((int64_t)8, d.ld_dz - c0)) : 0;
+    float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int64_t r = r0 + rl; r < r1; r += lanes) {
+        float v[8];
+        load8(d.dy, d.dy_type, r * d.lddy + c0, valid, d.vec, v);
+        if (d.act != GS_ACT_NONE) {
+            float z[8];
+            load8(d.z, d.type, r * d.ldz + c0, valid, d.vec, z);
+            if (d.exact) {
+#pragma unroll
+                for (int i = 0; i < 8; i++) v[i] = i < valid ? v[i] * activate_slope<true>(z[i], d.act) : 0.0f;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; i++) v[i] = i < valid ? v[i] * activate_slope<false>(z[i], d.act) : 0.0f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; i++) acc[i] += v[i];
+        if (room == 8) store8_vec(d.dz, d.type, r * d.ld_dz + c0, v);        // ld_dz is a multiple of 8
+    }
+    if (!d.part) return;
+#pragma unroll
+    for (int i = 0; i < 8; i++) sums[threadIdx.x][i] = acc[i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < groups * 8; i += kThreads) {
+        const int c = blockIdx.x * groups * 8 + i;
+        float s = 0.0f;
+        for (int l = 0; l < lanes; l++) s += sums[l * groups + i / 8][i % 8];
+        if (c < d.n) d.part[(int64_t)blockIdx.y * d.n + c] = s;
+    }
+}
+
+// dy in planes [n][m]: tiles of 64 columns x 64 rows turned round in LDS.
+__global__ __launch_bounds__(kThreads) void dz_planes(DzArgs d)
+{
+    __shared__ float tile[64][65];
+    const int c0 = blockIdx.x * 64, tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
+    const int64_t r0 = (int64_t)blockIdx.y * d.rows_per_block, r1 = min(d.m, r0 + d.rows_per_block);
+    const int c = c0 + tx;                      // this thread's column of dz
+    float acc = 0.0f;
+    for (int64_t r = r0; r < r1; r += 64) {
+#pragma unroll 4
+        for (int i = ty; i < 64; i += 4)
+            tile[i][tx] = c0 + i < d.n && r + tx < r1 ? load_as_float(d.dy, d.dy_type, (int64_t)(c0 + i) * d.lddy + r + tx)
+                                                      : 0.0f;
+        __syncthreads();
+        for (int i = ty; i < 64 && r + i < r1; i += 4) {
+            float v = tile[tx][i];
+            if (d.act != GS_ACT_NONE && c < d.n) {
+                const float z = load_as_float(d.z, d.type, (r + i) * d.ldz + c);
+                v *= d.exact ? activate_slope<true>(z, d.act) : activate_slope<false>(z, d.act);
+            }
+            acc += v;
+            if (d.dz && c < d.ld_dz) store_from_float(d.dz, d.type, (r + i) * d.ld_dz + c, v);
+        }
+        __syncthreads();
+    }
+    if (!d.part) return;
+    tile[ty][tx] = acc;
+    __syncthreads();
+    if (ty == 0 && c < d.n) d.part[(int64_t)blockIdx.y * d.n + c] = tile[0][tx] + tile[1][tx] + tile[2][tx] + tile[3][tx];
+}
+
+// db from the partial sums of `blocks` row blocks: 64 columns a block, four
+// lanes of rows.
+__global__ __launch_bounds__(kThreads) void sum_partials(const float *part, float *out, int n, int blocks, int accumulate)
+{
+    __shared__ float sums[4][64];
+    const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6, c = blockIdx.x * 64 + tx;
+    float s = 0.0f;
+    if (c < n)
+        for (int b = ty; b < blocks; b += 4) s += part[(int64_t)b * n + c];
+    sums[ty][tx] = s;
+    __syncthreads();
+    if (ty == 0 && c < n) {
+        s = sums[0][tx] + sums[1][tx] + sums[2][tx] + sums[3][tx];
+        out[c] = accumulate ? out[c] + s : s;
+    }
+}
+
+// Everything a backward call does, with its places in the workspace.
+struct BwdPlan {
+    bool own_dz;                        // dz is written to the workspace (else dz is dy)
+    bool pass;                          // the dz / db pass runs
+    int row_blocks, rows_per_block;
+    int64_t ld_dz;
+    size_t dz_at, part_at, dx_at, dw_at, bytes;
+    Product dx, dw;
+};
+
+BwdPlan plan_bwd(const gs_linear &l, const gs_linear_grads &g)
+{
+    BwdPlan b;
+    memset(&b, 0, sizeof b);
+    const int es = dtype_bytes(l.dtype);
+    const bool products = g.dx || g.dw;
+    // dz is dy itself when nothing has to be done to it and it can be loaded
+    // as it stands
+    const bool same = l.activation == GS_ACT_NONE && !l.planes && l.y_dtype == l.dtype;
+    b.own_dz = products && !(same && (l.dtype == GS_DTYPE_F32 || gemm::direct_ok(g.dy, es, g.dy_stride, l.n)));
+    b.pass = b.own_dz || g.db;
+    b.ld_dz = ((int64_t)l.n + 7) & ~(int64_t)7;
+    // row blocks of the pass: enough for the device, at most 1024 (the partial
+    // sums are read once more)
+    const int64_t cols = l.planes ? (l.n + 63) / 64 : (l.n + 511) / 512;
+    int64_t want = 2048 / cols;
+    want = want < 1 ? 1 : want > 1024 ? 1024 : want;
+    int64_t per = (l.m + want - 1) / want;
+    per = (per + 63) & ~(int64_t)63;
+    if (per < 64) per = 64;
+    b.rows_per_block = (int)per;
+    b.row_blocks = (int)((l.m + per - 1) / per);
+    size_t at = 0;
+    b.dz_at = at;
+    if (b.own_dz) at += round256((size_t)l.m * b.ld_dz * es);
+    b.part_at = at;
+    if (g.db) at += round256((size_t)b.row_blocks * l.n * 4);
+
+    auto common = [&](Product &r) {
+        r.kind = l.dtype;
+        r.a.p_type = r.a.q_type = l.dtype;
+        r.a.q = b.own_dz ? nullptr : g.dy;              // with own_dz: the workspace, 256-byte aligned
+        r.a.ldq = b.own_dz ? b.ld_dz : g.dy_stride;
+        r.plan.pt = true;
+        r.a.P = r.a.Pl = l.k;
+    };
+    const int64_t n_read = b.own_dz ? b.ld_dz : l.n;    // columns of dz that may be read
+    const bool w16 = l.dtype != GS_DTYPE_F32;
+    if (g.dx) {
+        Product &r = b.dx;
+        common(r);
+        r.a.p = l.w;
+        r.a.ldp = l.w_stride;
+        r.a.Q = r.a.Ql = (int)l.m;
+        r.a.K = l.n;
+        r.e.y = g.dx;
+        r.e.ldy = g.dx_stride;
+        r.e.y_type = l.dtype;
+        finish_plan(r, w16 && gemm::direct_ok(l.w, es, l.w_stride, l.k) &&
+                           gemm::direct_ok(r.a.q, es, r.a.ldq, n_read));
+        b.dx_at = at;
+    }
+    if (g.dw) {
+        Product &r = b.dw;
+        common(r);
+        r.plan.qt = true;
+        r.a.p = l.x;
+        r.a.ldp = l.x_stride;
+        r.a.Q = l.n;
+        r.a.Ql = (int)n_read;
+        r.a.K = (int)l.m;
+        r.e.y = g.dw;
+        r.e.ldy = g.dw_stride;
+        r.e.y_type = g.dw_dtype;
+        r.e.accumulate = g.accumulate != 0;
+        finish_plan(r, w16 && gemm::direct_ok(l.x, es, l.x_stride, l.k) &&
+                           gemm::direct_ok(r.a.q, es, r.a.ldq, n_read));
+        b.dw_at = at;
+    }
+    // the two products run one after the other and share their partial sums' place
+    const size_t parts = b.dx.partial_bytes > b.dw.partial_bytes ? b.dx.partial_bytes : b.dw.partial_bytes;
+    b.bytes = at + round256(parts);
+    return b;
+}
+
+gs_status linear_bwd_ok(const gs_linear *l, const gs_linear_grads *g)
+{
+    const gs_status st = linear_ok(l);
+    if (st != GS_OK) return st;
+    if (!g) return GS_ERR_INVALID_ARG;
+    if (l->dtype == GS_DTYPE_MXFP8) return GS_ERR_UNSUPPORTED;
+    if (l->activation != GS_ACT_NONE && l->m > 0 && !l->z) return GS_ERR_INVALID_ARG;
+    const int es = dtype_bytes(l->dtype);
+    if ((l->m > 0 && !g->dy) || g->dy_stride < (l->planes ? l->m : l->n) || !aligned_to(g->dy, dtype_bytes(l->y_dtype)))
+        return GS_ERR_INVALID_ARG;
+    if (g->dx && (g->dx_stride < l->k || !aligned_to(g->dx, es))) return GS_ERR_INVALID_ARG;
+    if (g->dw && ((g->dw_dtype != GS_DTYPE_F32 && g->dw_dtype != l->dtype) || g->dw_stride < l->k ||
+                  !aligned_to(g->dw, dtype_bytes(g->dw_dtype))))
+        return GS_ERR_INVALID_ARG;
+    if (!aligned_to(g->db, 4)) return GS_ERR_INVALID_ARG;
+    return GS_OK;
+}
+
+__global__ __launch_bounds__(kThreads) void zero_rows(void *p, int type, int64_t ld, int rows, int cols)
+{
+    const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (id >= (int64_t)rows * cols) return;
+    store_from_float(p, type, id / cols * ld + id % cols, 0.0f);
+}
+
+hipError_t run_bwd(const gs_linear &l, const gs_linear_grads &g, BwdPlan &b, char *ws, hipStream_t s)
+{
+    hipError_t err = hipSuccess;
+    if (l.m == 0) {                             // sums over no rows
+        if (g.dw && !g.accumulate) {
+            const int64_t blocks = ((int64_t)l.n * l.k + kThreads - 1) / kThreads;
+            zero_rows<<<(unsigned)blocks, kThreads, 0, s>>>(g.dw, g.dw_dtype, g.dw_stride, l.n, l.k);
+            if ((err = hipGetLastError()) != hipSuccess) return err;
+        }
+        if (g.db && !g.accumulate) {
+            zero_rows<<<(unsigned)((l.n + kThreads - 1) / kThreads), kThreads, 0, s>>>(g.db, GS_DTYPE_F32, l.n, 1, l.n);
+            err = hipGetLastError();
+        }
+        return err;
+    }
+    if (b.pass) {
+        DzArgs d;
+        d.dy = g.dy;
+        d.z = l.z;
+        d.lddy = g.dy_stride;
+        d.ldz = l.z_stride;
+        d.dy_type = l.y_dtype;
+        d.type = l.dtype;
+        d.act = l.activation;
+        d.exact = l.dtype == GS_DTYPE_F32;
+        d.dz = b.own_dz ? ws + b.dz_at : nullptr;
+        d.ld_dz = b.ld_dz;
+        d.part = g.db ? reinterpret_cast<float *>(ws + b.part_at) : nullptr;
+        d.m = l.m;
+        d.n = l.n;
+        d.rows_per_block = b.rows_per_block;
+        d.vec = vec_ok(g.dy, l.y_dtype, g.dy_stride) && (l.activation == GS_ACT_NONE || vec_ok(l.z, l.dtype, l.z_stride));
+        if (l.planes) {
+            dz_planes<<<dim3((unsigned)((l.n + 63) / 64), (unsigned)b.row_blocks), kThreads, 0, s>>>(d);
+        } else {
+            int groups = 1;                     // of 8 columns: a power of two, at most 64
+            while (groups < 64 && groups * 8 < l.n) groups *= 2;
+            dz_rows<<<dim3((unsigned)((l.n + groups * 8 - 1) / (groups * 8)), (unsigned)b.row_blocks), kThreads, 0, s>>>(d, groups);
+        }
+        if ((err = hipGetLastError()) != hipSuccess) return err;
+        if (g.db) {
+            sum_partials<<<(unsigned)((l.n + 63) / 64), kThreads, 0, s>>>(d.part, g.db, l.n, b.row_blocks, g.accumulate);
+            if ((err = hipGetLastError()) != hipSuccess) return err;
+        }
+    }
+    if (g.dx) {
+        if (b.own_dz) b.dx.a.q = ws + b.dz_at;
+        b.dx.a.q_vec = b.own_dz ? 1 : b.dx.a.q_vec;
+        if ((err = run_product(b.dx, ws + b.dx_at, s)) != hipSuccess) return err;
+    }
+    if (g.dw) {
+        if (b.own_dz) b.dw.a.q = ws + b.dz_at;
+        b.dw.a.q_vec = b.own_dz ? 1 : b.dw.a.q_vec;
+        if ((err = run_product(b.dw, ws + b.dw_at, s)) != hipSuccess) return err;
+    }
+    return hipSuccess;
+}
+
+gs_status from_hip(hipError_t e) { return e == hipSuccess ? GS_OK : GS_ERR_HIP; }
+
+}  // namespace
+}  // namespace gsi
+
+using namespace gsi;
+
+extern "C" {
+
+size_t gs_linear_fwd_workspace_bytes(const gs_linear *l)
+{
+    if (linear_fwd_ok(l) != GS_OK || l->m == 0) return 0;
+    return plan_fwd(*l).partial_bytes;
+}
+
+gs_status gs_linear_fwd(const gs_linear *l, void *workspace, size_t workspace_bytes, void *stream)
+{
+    const gs_status st = linear_fwd_ok(l);
+    if (st != GS_OK) return st;
+    if (l->m == 0) return GS_OK;
+    Product r = plan_fwd(*l);
+    if (r.partial_bytes > 0) {
+        if (workspace_bytes < r.partial_bytes) return GS_ERR_WORKSPACE;
+        if (!workspace || !al16(workspace)) return GS_ERR_INVALID_ARG;
+    }
+    return from_hip(run_product(r, workspace, (hipStream_t)stream));
+}
+
+size_t gs_linear_bwd_workspace_bytes(const gs_linear *l, const gs_linear_grads *g)
+{
+    if (linear_bwd_ok(l, g) != GS_OK || l->m == 0) return 0;
+    return plan_bwd(*l, *g).bytes;
+}
+
+gs_status gs_linear_bwd(const gs_linear *l, const gs_linear_grads *g, void *workspace, size_t workspace_bytes, void *stream)
+{
+    const gs_status st = linear_bwd_ok(l, g);
+    if (st != GS_OK) return st;
+    BwdPlan b = plan_bwd(*l, *g);
+    if (l->m > 0 && b.bytes > 0) {
+        if (workspace_bytes < b.bytes) return GS_ERR_WORKSPACE;
+        if (!workspace || !al16(workspace)) return GS_ERR_INVALID_ARG;
+    }
+    return from_hip(run_bwd(*l, *g, b, static_cast<char *>(workspace), (hipStream_t)stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,551 @@
+// Root-mean-square norm with the residual's addition, output in the input's
+// type or in 8-bit blocks, and its backward; 8-bit quantisation of a matrix.
+//
+// HBM-bound: the forward reads x and the residual and writes the sum and y
+// once, the backward reads the sum, dy and dsum and writes dx.  A row is held
+// in registers between its reduction and its outputs, 8 consecutive elements
+// (16 bytes of a 16-bit type) per lane and access: rows of up to 2048 by one
+// wave (4 rows per workgroup, no barrier), up to 8192 by a workgroup, longer
+// ones in two passes.  An 8-bit block of 32 values is 4 neighbouring lanes.
+#include "gs_numeric.h"
+
+#include <math.h>
+
+namespace gsi {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxRegRow = 8192;
+
+bool aligned_to(const void *p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
+bool float_type(int t) { return t == GS_DTYPE_F32 || t == GS_DTYPE_F16 || t == GS_DTYPE_BF16; }
+bool vec_ok(const void *p, int type, int64_t ld) { return aligned_to(p, 16) && ld % (16 / dtype_bytes(type)) == 0; }
+gs_status from_hip(hipError_t e) { return e == hipSuccess ? GS_OK : GS_ERR_HIP; }
+
+template <typename T> constexpr int type_of();
+template <> constexpr int type_of<float>() { return GS_DTYPE_F32; }
+template <> constexpr int type_of<_Float16>() { return GS_DTYPE_F16; }
+template <> constexpr int type_of<__bf16>() { return GS_DTYPE_BF16; }
+
+template <typename T> __device__ __forceinline__ void load_chunk(const T *p, int64_t i, int valid, bool vec, float v[8])
+{
+    if (vec && valid == 8) {
+        load8_vec(p + i, v);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j++) v[j] = j < valid ? (float)p[i + j] : 0.0f;
+}
+template <typename T> __device__ __forceinline__ void store_chunk(T *p, int64_t i, int valid, bool vec, const float v[8])
+{
+    if (vec && valid == 8) {
+        store8_vec(p + i, v);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j++)
+        if (j < valid) p[i + j] = (T)v[j];
+}
+
+__device__ __forceinline__ float wave_sum(float x)
+{
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);
+    return x;
+}
+// Sum over the LANES threads of a row: a wave, or the workgroup by LDS.
+template <int LANES> __device__ __forceinline__ float row_sum(float x, float *lds)
+{
+    x = wave_sum(x);
+    if constexpr (LANES > 64) {
+        __syncthreads();                        // the last use of lds is over
+        if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
+        __syncthreads();
+        x = 0.0f;
+#pragma unroll
+        for (int w = 0; w < LANES / 64; w++) x += lds[w];
+    }
+    return x;
+}
+
+// One chunk of an 8-bit block row: the scale is shared by 4 neighbouring lanes
+// (all of them in the call).  The exponent is the smallest that leaves the
+// block's largest magnitude, 1.m x 2^E, at most 448 = 1.75 x 2^8: E - 8, or
+// E - 7 where 1.m > 1.75.
+__device__ __forceinline__ void quantize_chunk(const float v[8], uint8_t *codes, bool vec, uint8_t *scale)
+{
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < 8; j++) top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+    top = max(top, (uint32_t)__shfl_xor((int)top, 1));
+    top = max(top, (uint32_t)__shfl_xor((int)top, 2));
+    const bool finite = top < 0x7F800000u;
+    int s = (int)(top >> 23) - 8 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    s = finite ? max(s, 0) : 255;
+    const float inv = finite ? __uint_as_float((uint32_t)(254 - s) << 23) : 0.0f;      // 2^(127 - s), exact
+    int w[2];
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        int x = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h] * inv, v[4 * h + 1] * inv, 0, false);
+        w[h] = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h + 2] * inv, v[4 * h + 3] * inv, x, true);
+    }
+    if (vec) {
+        *reinterpret_cast<int2 *>(codes) = make_int2(w[0], w[1]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++) codes[j] = (uint8_t)(w[j >> 2] >> (8 * (j & 3)));
+    }
+    if (scale) *scale = (uint8_t)s;
+}
+
+struct NormArgs {
+    const void *x, *residual;
+    const float *gamma;
+    void *sum, *y;
+    uint8_t *scales;
+    float *rstd;
+    int64_t m, ldx, ldr, lds, ldy, ldsc;
+    int n, vec, gamma_vec, q8, norm;            // norm 0: y is x (quantisation alone)
+    float eps;
+};
+
+__device__ __forceinline__ float inverse_rms(float sum_sq, int n, float eps) { return 1.0f / sqrtf(sum_sq / (float)n + eps); }
+
+template <typename T>
+__device__ __forceinline__ void emit(const NormArgs &a, int64_t row, int c, int valid, float v[8], float rstd)
+{
+    if (a.norm) {
+        float g[8];
+        if (a.gamma) load_chunk(a.gamma, c, valid, a.gamma_vec, g);
+#pragma unroll
+        for (int j = 0; j < 8; j++) v[j] = a.gamma ? v[j] * rstd * g[j] : v[j] * rstd;
+    }
+    if (a.q8)
+        quantize_chunk(v, static_cast<uint8_t *>(a.y) + row * a.ldy + c, a.vec,
+                       (threadIdx.x & 3) == 0 ? a.scales + row * a.ldsc + (c >> 5) : nullptr);
+    else
+        store_chunk(static_cast<T *>(a.y), row * a.ldy + c, valid, a.vec, v);
+}
+
+// Rows of up to LANES * 8 * V elements.
+template <typename T, int LANES, int V> __global__ __launch_bounds__(kThreads) void norm_rows(NormArgs a)
+{
+    __shared__ float lds[kThreads / 64];
+    const int lane = threadIdx.x % LANES;
+    const int64_t row = (int64_t)blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
+    if (row >= a.m) return;                     // whole waves; a workgroup's single row is always there
+    float v[V][8], sq = 0.0f;
+#pragma unroll
+    for (int k = 0; k < V; k++) {
+        const int c = (k * LANES + lane) * 8, valid = max(0, min(8, a.n - c));
+        load_chunk(static_cast<const T *>(a.x), row * a.ldx + c, valid, a.vec, v[k]);
+        if (a.residual) {
+            float r[8];
+            load_chunk(static_cast<const T *>(a.residual), row * a.ldr + c, valid, a.vec, r);
+#pragma unroll
+            for (int j = 0; j < 8; j++) v[k][j] += r[j];
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < V; k++)
+#pragma unroll
+        for (int j = 0; j < 8; j++) sq = fmaf(v[k][j], v[k][j], sq);
+    const float rstd = inverse_rms(row_sum<LANES>(sq, lds), a.n, a.eps);
+    if (a.rstd && lane == 0) a.rstd[row] = rstd;
+#pragma unroll
+    for (int k = 0; k < V; k++) {
+        const int c = (k * LANES + lane) * 8, valid = max(0, min(8, a.n - c));
+        if (valid == 0) continue;               // whole 8-bit blocks: n is a multiple of 32 there
+        if (a.sum) store_chunk(static_cast<T *>(a.sum), row * a.lds + c, valid, a.vec, v[k]);
+        emit<T>(a, row, c, valid, v[k], rstd);
+    }
+}
+
+// Rows of any length, a workgroup each, read twice.
+template <typename T> __global__ __launch_bounds__(kThreads) void norm_long(NormArgs a)
+{
+    __shared__ float lds[kThreads / 64];
+    const int64_t row = blockIdx.x;
+    auto sum_at = [&](int c, int valid, float v[8]) {
+        load_chunk(static_cast<const T *>(a.x), row * a.ldx + c, valid, a.vec, v);
+        if (a.residual) {
+            float r[8];
+            load_chunk(static_cast<const T *>(a.residual), row * a.ldr + c, valid, a.vec, r);
+#pragma unroll
+            for (int j = 0; j < 8; j++) v[j] += r[j];
+        }
+    };
+    float sq = 0.0f, rstd = 0.0f;
+    if (a.norm) {
+        for (int c = threadIdx.x * 8; c < a.n; c += kThreads * 8) {
+            float v[8];
+            sum_at(c, min(8, a.n - c), v);
+#pragma unroll
+            for (int j = 0; j < 8; j++) sq = fmaf(v[j], v[j], sq);
+        }
+        rstd = inverse_rms(row_sum<kThreads>(sq, lds), a.n, a.eps);
+        if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
+    }
+    for (int c = threadIdx.x * 8; c < a.n; c += kThreads * 8) {
+        const int valid = min(8, a.n - c);
+        float v[8];
+        sum_at(c, valid, v);
+        if (a.sum) store_chunk(static_cast<T *>(a.sum), row * a.lds + c, valid, a.vec, v);
+        emit<T>(a, row, c, valid, v, rstd);
+    }
+}
+
+template <typename T> hipError_t launch_norm(const NormArgs &a, hipStream_t s)
+{
+    const unsigned rows4 = (unsigned)((a.m + 3) / 4), rows1 = (unsigned)a.m;
+    if (a.n <= 512) norm_rows<T, 64, 1><<<rows4, kThreads, 0, s>>>(a);
+    else if (a.n <= 1024) norm_rows<T, 64, 2><<<rows4, kThreads, 0, s>>>(a);
+    else if (a.n <= 2048) norm_rows<T, 64, 4><<<rows4, kThreads, 0, s>>>(a);
+    else if (a.n <= 4096) norm_rows<T, 256, 2><<<rows1, kThreads, 0, s>>>(a);
+    else if (a.n <= kMaxRegRow) norm_rows<T, 256, 4><<<rows1, kThreads, 0, s>>>(a);
+    else norm_long<T><<<rows1, kThreads, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_norm(const NormArgs &a, int dtype, hipStream_t s)
+{
+    if (dtype == GS_DTYPE_F32) return launch_norm<float>(a, s);
+    if (dtype == GS_DTYPE_F16) return launch_norm<_Float16>(a, s);
+    return launch_norm<__bf16>(a, s);
+}
+
+// ---- backward -------------------------------------------------------------------
+struct GradArgs {
+    const void *sum, *dy, *dsum;
+    const float *rstd, *gamma;
+    void *dx;
+    float *part;                                // [grid][n] partial sums of dgamma, or NULL
+    int64_t m, lds, ldy, ldds, ldx;
+    int n, vec, gamma_vec;
+};
+
+// Each workgroup strides over the rows; a thread keeps the dgamma sums of its
+// columns in registers and the workgroup writes one partial row at the end.
+template <typename T, int LANES, int V> __global__ __launch_bounds__(kThreads) void grad_rows(GradArgs a)
+{
+    constexpr int kRows = kThreads / LANES;
+    __shared__ float lds[kThreads / 64];
+    __shared__ float turn[LANES == 64 ? kThreads : 1][8];
+    const int lane = threadIdx.x % LANES, sub = threadIdx.x / LANES;
+    float dg[V][8];
+#pragma unroll
+    for (int k = 0; k < V; k++)
+#pragma unroll
+        for (int j = 0; j < 8; j++) dg[k][j] = 0.0f;
+    for (int64_t row = (int64_t)blockIdx.x * kRows + sub; row < a.m; row += (int64_t)gridDim.x * kRows) {
+        const float rstd = a.rstd[row];
+        float h[V][8], g[V][8], dot = 0.0f;
+#pragma unroll
+        for (int k = 0; k < V; k++) {
+            const int c = (k * LANES + lane) * 8, valid = max(0, min(8, a.n - c));
+            load_chunk(static_cast<const T *>(a.sum), row * a.lds + c, valid, a.vec, h[k]);
+            load_chunk(static_cast<const T *>(a.dy), row * a.ldy + c, valid, a.vec, g[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < V; k++) {
+            const int c = (k * LANES + lane) * 8, valid = max(0, min(8, a.n - c));
+            float w[8];
+            if (a.gamma) load_chunk(a.gamma, c, valid, a.gamma_vec, w);
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                h[k][j] *= rstd;
+                dg[k][j] = fmaf(g[k][j], h[k][j], dg[k][j]);
+                if (a.gamma) g[k][j] *= w[j];
+                dot = fmaf(g[k][j], h[k][j], dot);
+            }
+        }
+        dot = row_sum<LANES>(dot, lds) / (float)a.n;
+#pragma unroll
+        for (int k = 0; k < V; k++) {
+            const int c = (k * LANES + lane) * 8, valid = max(0, min(8, a.n - c));
+            if (valid == 0) continue;
+            float d[8];
+            if (a.dsum) load_chunk(static_cast<const T *>(a.dsum), row * a.ldds + c, valid, a.vec, d);
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const float v = rstd * fmaf(-h[k][j], dot, g[k][j]);
+                d[j] = a.dsum ? v + d[j] : v;
+            }
+            store_chunk(static_cast<T *>(a.dx), row * a.ldx + c, valid, a.vec, d);
+        }
+    }
+    if (!a.part) return;
+    float *out = a.part + (int64_t)blockIdx.x * a.n;
+#pragma unroll
+    for (int k = 0; k < V; k++) {
+        const int c = (k * LANES + lane) * 8;
+        if constexpr (LANES == 64) {            // the four waves' sums of a column, in order
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < 8; j++) turn[threadIdx.x][j] = dg[k][j];
+            __syncthreads();
+            for (int i = threadIdx.x; i < 512; i += kThreads) {
+                const int l = i / 8, j = i % 8, col = k * 512 + i;
+                if (col < a.n) out[col] = turn[l][j] + turn[64 + l][j] + turn[128 + l][j] + turn[192 + l][j];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                if (c + j < a.n) out[c + j] = dg[k][j];
+        }
+    }
+}
+
+// Rows of any length: dx, a workgroup each.
+template <typename T> __global__ __launch_bounds__(kThreads) void grad_long(GradArgs a)
+{
+    __shared__ float lds[kThreads / 64];
+    const int64_t row = blockIdx.x;
+    const float rstd = a.rstd[row];
+    float dot = 0.0f;
+    auto at = [&](int c, int valid, float h[8], float g[8]) {
+        float w[8];
+        load_chunk(static_cast<const T *>(a.sum), row * a.lds + c, valid, a.vec, h);
+        load_chunk(static_cast<const T *>(a.dy), row * a.ldy + c, valid, a.vec, g);
+        if (a.gamma) load_chunk(a.gamma, c, valid, a.gamma_vec, w);
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            h[j] *= rstd;
+            if (a.gamma) g[j] *= w[j];
+        }
+    };
+    for (int c = threadIdx.x * 8; c < a.n; c += kThreads * 8) {
+        float h[8], g[8];
+        at(c, min(8, a.n - c), h, g);
+#pragma unroll
+        for (int j = 0; j < 8; j++) dot = fmaf(g[j], h[j], dot);
+    }
+    dot = row_sum<kThreads>(dot, lds) / (float)a.n;
+    for (int c = threadIdx.x * 8; c < a.n; c += kThreads * 8) {
+        const int valid = min(8, a.n - c);
+        float h[8], g[8], d[8];
+        at(c, valid, h, g);
+        if (a.dsum) load_chunk(static_cast<const T *>(a.dsum), row * a.ldds + c, valid, a.vec, d);
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            const float v = rstd * fmaf(-h[j], dot, g[j]);
+            d[j] = a.dsum ? v + d[j] : v;
+        }
+        store_chunk(static_cast<T *>(a.dx), row * a.ldx + c, valid, a.vec, d);
+    }
+}
+
+// Rows of any length: partial sums of dgamma, 2048 columns by every grid.y-th row.
+template <typename T> __global__ __launch_bounds__(kThreads) void dgamma_long(GradArgs a)
+{
+    const int c = (blockIdx.x * kThreads + threadIdx.x) * 8, valid = max(0, min(8, a.n - c));
+    float dg[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int64_t row = blockIdx.y; row < a.m; row += gridDim.y) {
+        float h[8], g[8];
+        load_chunk(static_cast<const T *>(a.sum), row * a.lds + c, valid, a.vec, h);
+        load_chunk(static_cast<const T *>(a.dy), row * a.ldy + c, valid, a.vec, g);
+        const float rstd = a.rstd[row];
+#pragma unroll
+        for (int j = 0; j < 8; j++) dg[j] = fmaf(g[j], h[j] * rstd, dg[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j++)
+        if (j < valid) a.part[(int64_t)blockIdx.y * a.n + c + j] = dg[j];
+}
+
+__global__ __launch_bounds__(kThreads) void sum_dgamma(const float *part, float *out, int n, int blocks, int accumulate)
+{
+    __shared__ float sums[4][64];
+    const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6, c = blockIdx.x * 64 + tx;
+    float s = 0.0f;
+    if (c < n)
+        for (int b = ty; b < blocks; b += 4) s += part[(int64_t)b * n + c];
+    sums[ty][tx] = s;
+    __syncthreads();
+    if (ty == 0 && c < n) {
+        s = sums[0][tx] + sums[1][tx] + sums[2][tx] + sums[3][tx];
+        out[c] = accumulate ? out[c] + s : s;
+    }
+}
+
+// Workgroups of the backward, each with one partial row of dgamma.
+int grad_blocks(int64_t m, int n)
+{
+    if (n > kMaxRegRow) return (int)(m < 64 ? m : 64);
+    const int64_t rows = n <= 2048 ? 4 : 1, want = (m + rows - 1) / rows;
+    return (int)(want < 1024 ? want : 1024);
+}
+
+template <typename T> hipError_t launch_grad(const GradArgs &a, hipStream_t s)
+{
+    const unsigned g = (unsigned)grad_blocks(a.m, a.n);
+    if (a.n <= 512) grad_rows<T, 64, 1><<<g, kThreads, 0, s>>>(a);
+    else if (a.n <= 1024) grad_rows<T, 64, 2><<<g, kThreads, 0, s>>>(a);
+    else if (a.n <= 2048) grad_rows<T, 64, 4><<<g, kThreads, 0, s>>>(a);
+    else if (a.n <= 4096) grad_rows<T, 256, 2><<<g, kThreads, 0, s>>>(a);
+    else if (a.n <= kMaxRegRow) grad_rows<T, 256, 4><<<g, kThreads, 0, s>>>(a);
+    else {
+        // dgamma first: dx may be written over dy
+        if (a.part) dgamma_long<T><<<dim3((unsigned)((a.n + 2047) / 2048), g), kThreads, 0, s>>>(a);
+        grad_long<T><<<(unsigned)a.m, kThreads, 0, s>>>(a);
+    }
+    return hipGetLastError();
+}
+
+gs_status norm_ok(const gs_rms_norm *a)
+{
+    if (!a) return GS_ERR_INVALID_ARG;
+    if (a->m < 0 || a->m > ((int64_t)1 << 30) || a->n < 1 || a->n > (1 << 20)) return GS_ERR_INVALID_ARG;
+    if (!float_type(a->dtype)) return GS_ERR_INVALID_ARG;
+    if (a->y_dtype != a->dtype && a->y_dtype != GS_DTYPE_MXFP8) return GS_ERR_UNSUPPORTED;
+    const bool q8 = a->y_dtype == GS_DTYPE_MXFP8;
+    if (q8 && a->n % 32 != 0) return GS_ERR_INVALID_ARG;
+    if (!isfinite(a->eps) || a->eps < 0.0f) return GS_ERR_INVALID_ARG;
+    const int es = dtype_bytes(a->dtype), ys = dtype_bytes(a->y_dtype);
+    if (a->m > 0 && (!a->x || !a->y || (q8 && !a->y_scales))) return GS_ERR_INVALID_ARG;
+    if (a->x_stride < a->n || a->y_stride < a->n || (a->residual && a->residual_stride < a->n) ||
+        (a->sum && a->sum_stride < a->n) || (q8 && a->y_scales_stride < a->n / 32))
+        return GS_ERR_INVALID_ARG;
+    if (!aligned_to(a->x, es) || !aligned_to(a->residual, es) || !aligned_to(a->sum, es) || !aligned_to(a->y, ys) ||
+        !aligned_to(a->gamma, 4) || !aligned_to(a->rstd, 4))
+        return GS_ERR_INVALID_ARG;
+    return GS_OK;
+}
+
+gs_status grads_ok(const gs_rms_norm_grads *a)
+{
+    if (!a) return GS_ERR_INVALID_ARG;
+    if (a->m < 0 || a->m > ((int64_t)1 << 30) || a->n < 1 || a->n > (1 << 20)) return GS_ERR_INVALID_ARG;
+    if (!float_type(a->dtype)) return GS_ERR_INVALID_ARG;
+    const int es = dtype_bytes(a->dtype);
+    if (a->m > 0 && (!a->sum || !a->rstd || !a->dy || !a->dx)) return GS_ERR_INVALID_ARG;
+    if (a->sum_stride < a->n || a->dy_stride < a->n || a->dx_stride < a->n || (a->dsum && a->dsum_stride < a->n))
+        return GS_ERR_INVALID_ARG;
+    if (!aligned_to(a->sum, es) || !aligned_to(a->dy, es) || !aligned_to(a->dsum, es) || !aligned_to(a->dx, es) ||
+        !aligned_to(a->rstd, 4) || !aligned_to(a->gamma, 4) || !aligned_to(a->dgamma, 4))
+        return GS_ERR_INVALID_ARG;
+    return GS_OK;
+}
+
+__global__ __launch_bounds__(kThreads) void zero_floats(float *p, int n)
+{
+    const int i = blockIdx.x * kThreads + threadIdx.x;
+    if (i < n) p[i] = 0.0f;
+}
+
+}  // namespace
+}  // namespace gsi
+
+using namespace gsi;
+
+extern "C" {
+
+gs_status gs_rms_norm_fwd(const gs_rms_norm *p, void *stream)
+{
+    const gs_status st = norm_ok(p);
+    if (st != GS_OK) return st;
+    if (p->m == 0) return GS_OK;
+    const bool q8 = p->y_dtype == GS_DTYPE_MXFP8;
+    NormArgs a;
+    a.x = p->x;
+    a.residual = p->residual;
+    a.gamma = p->gamma;
+    a.sum = p->sum;
+    a.y = p->y;
+    a.scales = p->y_scales;
+    a.rstd = p->rstd;
+    a.m = p->m;
+    a.ldx = p->x_stride;
+    a.ldr = p->residual_stride;
+    a.lds = p->sum_stride;
+    a.ldy = p->y_stride;
+    a.ldsc = p->y_scales_stride;
+    a.n = p->n;
+    a.vec = vec_ok(p->x, p->dtype, p->x_stride) && (!p->residual || vec_ok(p->residual, p->dtype, p->residual_stride)) &&
+            (!p->sum || vec_ok(p->sum, p->dtype, p->sum_stride)) &&
+            (q8 ? aligned_to(p->y, 8) && p->y_stride % 8 == 0 : vec_ok(p->y, p->dtype, p->y_stride));
+    a.gamma_vec = aligned_to(p->gamma, 16);
+    a.q8 = q8;
+    a.norm = 1;
+    a.eps = p->eps;
+    return from_hip(launch_norm(a, p->dtype, (hipStream_t)stream));
+}
+
+gs_status gs_mxfp8_quantize(const void *x, int32_t dtype, int64_t m, int32_t n, int64_t x_stride, uint8_t *codes,
+                            int64_t codes_stride, uint8_t *scales, int64_t scales_stride, void *stream)
+{
+    gs_rms_norm p = {};
+    p.m = m;
+    p.n = n;
+    p.dtype = dtype;
+    p.y_dtype = GS_DTYPE_MXFP8;
+    p.x = x;
+    p.x_stride = x_stride;
+    p.y = codes;
+    p.y_stride = codes_stride;
+    p.y_scales = scales;
+    p.y_scales_stride = scales_stride;
+    const gs_status st = norm_ok(&p);
+    if (st != GS_OK) return st;
+    if (m == 0) return GS_OK;
+    NormArgs a = {};
+    a.x = x;
+    a.y = codes;
+    a.scales = scales;
+    a.m = m;
+    a.ldx = x_stride;
+    a.ldy = codes_stride;
+    a.ldsc = scales_stride;
+    a.n = n;
+    a.vec = vec_ok(x, dtype, x_stride) && aligned_to(codes, 8) && codes_stride % 8 == 0;
+    a.q8 = 1;
+    return from_hip(launch_norm(a, dtype, (hipStream_t)stream));
+}
+
+size_t gs_rms_norm_bwd_workspace_bytes(int64_t m, int32_t n)
+{
+    if (m <= 0 || m > ((int64_t)1 << 30) || n < 1 || n > (1 << 20)) return 0;
+    return (size_t)grad_blocks(m, n) * n * 4;
+}
+
+gs_status gs_rms_norm_bwd(const gs_rms_norm_grads *p, void *workspace, size_t workspace_bytes, void *stream)
+{
+    const gs_status st = grads_ok(p);
+    if (st != GS_OK) return st;
+    hipStream_t s = (hipStream_t)stream;
+    if (p->m == 0) {
+        if (!p->dgamma || p->accumulate) return GS_OK;
+        zero_floats<<<(p->n + kThreads - 1) / kThreads, kThreads, 0, s>>>(p->dgamma, p->n);
+        return from_hip(hipGetLastError());
+    }
+    if (p->dgamma) {
+        if (workspace_bytes < gs_rms_norm_bwd_workspace_bytes(p->m, p->n)) return GS_ERR_WORKSPACE;
+        if (!workspace || !aligned_to(workspace, 16)) return GS_ERR_INVALID_ARG;
+    }
+    GradArgs a;
+    a.sum = p->sum;
+    a.dy = p->dy;
+    a.dsum = p->dsum;
+    a.rstd = p->rstd;
+    a.gamma = p->gamma;
+    a.dx = p->dx;
+    a.part = p->dgamma ? static_cast<float *>(workspace) : nullptr;
+    a.m = p->m;
+    a.lds = p->sum_stride;
+    a.ldy = p->dy_stride;
+    a.ldds = p->dsum_stride;
+    a.ldx = p->dx_stride;
+    a.n = p->n;
+    a.vec = vec_ok(p->sum, p->dtype, p->sum_stride) && vec_ok(p->dy, p->dtype, p->dy_stride) &&
+            (!p->dsum || vec_ok(p->dsum, p->dtype, p->dsum_stride)) && vec_ok(p->dx, p->dtype, p->dx_stride);
+    a.gamma_vec = aligned_to(p->gamma, 16);
+    hipError_t e = p->dtype == GS_DTYPE_F32 ? launch_grad<float>(a, s)
+                   : p->dtype == GS_DTYPE_F16 ? launch_grad<_Float16>(a, s) : launch_grad<__bf16>(a, s);
+    if (e == hipSuccess && p->dgamma) {
+        sum_dgamma<<<(unsigned)((p->n + 63) / 64), kThreads, 0, s>>>(a.part, p->dgamma, p->n, grad_blocks(p->m, p->n), p->accumulate);
+        e = hipGetLastError();
+    }
+    return from_hip(e);
+}
+
+}  // extern "C"

@@ -1,0 +1,149 @@
+// Number formats and elementwise functions shared by the norm, the matrix
+// products and the orthogonalised update (internal).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "gs.h"
+
+namespace gsi {
+
+__host__ __device__ constexpr int dtype_bytes(int t) { return t == GS_DTYPE_F32 ? 4 : t == GS_DTYPE_MXFP8 ? 1 : 2; }
+
+// Four or eight consecutive values as one vector access; T: float, _Float16, __bf16.
+template <typename T, int N> struct alignas(sizeof(T) * N > 16 ? 16 : sizeof(T) * N) Vec { T v[N]; };
+
+template <typename T> __device__ __forceinline__ float to_float(T x) { return (float)x; }
+template <typename T> __device__ __forceinline__ T from_float(float x) { return (T)x; }     // rounds to nearest even
+
+// Element i of an array of type t (not GS_DTYPE_MXFP8).
+__device__ __forceinline__ float load_as_float(const void *p, int t, int64_t i)
+{
+    if (t == GS_DTYPE_F32) return static_cast<const float *>(p)[i];
+    if (t == GS_DTYPE_F16) return (float)static_cast<const _Float16 *>(p)[i];
+    return (float)static_cast<const __bf16 *>(p)[i];
+}
+__device__ __forceinline__ void store_from_float(void *p, int t, int64_t i, float x)
+{
+    if (t == GS_DTYPE_F32) static_cast<float *>(p)[i] = x;
+    else if (t == GS_DTYPE_F16) static_cast<_Float16 *>(p)[i] = (_Float16)x;
+    else static_cast<__bf16 *>(p)[i] = (__bf16)x;
+}
+
+template <typename T> __device__ __forceinline__ void load8_vec(const T *p, float v[8])
+{
+    const Vec<T, 8> w = *reinterpret_cast<const Vec<T, 8> *>(p);
+#pragma unroll
+    for (int i = 0; i < 8; i++) v[i] = (float)w.v[i];
+}
+template <typename T> __device__ __forceinline__ void store8_vec(T *p, const float v[8])
+{
+    Vec<T, 8> w;
+#pragma unroll
+    for (int i = 0; i < 8; i++) w.v[i] = (T)v[i];
+    *reinterpret_cast<Vec<T, 8> *>(p) = w;
+}
+// Elements i .. i + 7 of an array of type t, i * size a multiple of 16 bytes
+// from an aligned base.
+__device__ __forceinline__ void load8_vec(const void *p, int t, int64_t i, float v[8])
+{
+    if (t == GS_DTYPE_F32) load8_vec(static_cast<const float *>(p) + i, v);
+    else if (t == GS_DTYPE_F16) load8_vec(static_cast<const _Float16 *>(p) + i, v);
+    else load8_vec(static_cast<const __bf16 *>(p) + i, v);
+}
+__device__ __forceinline__ void store8_vec(void *p, int t, int64_t i, const float v[8])
+{
+    if (t == GS_DTYPE_F32) store8_vec(static_cast<float *>(p) + i, v);
+    else if (t == GS_DTYPE_F16) store8_vec(static_cast<_Float16 *>(p) + i, v);
+    else store8_vec(static_cast<__bf16 *>(p) + i, v);
+}
+// The same without alignment; elements past the first `valid` do not exist and
+// read as 0.
+__device__ __forceinline__ void load8(const void *p, int t, int64_t i, int valid, bool vec, float v[8])
+{
+    if (vec && valid >= 8) {
+        load8_vec(p, t, i, v);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j++) v[j] = j < valid ? load_as_float(p, t, i + j) : 0.0f;
+}
+
+// x = limb 0 + limb 1 + limb 2, each what is left rounded to bf16 (8 bits): a
+// rounded limb leaves a remainder of either sign, so three hold all 24 bits
+// and what a product of limbs drops does not pile up on one side.  A finite x
+// that would round to an infinity is truncated instead; an infinity or NaN
+// stays alone in the first limb.  Limbs below the smallest bf16 vanish, so
+// values under 2^-110 keep fewer bits.
+template <int NL> __device__ __forceinline__ void split_limbs(float x, uint16_t limb[NL])
+{
+    limb[0] = __builtin_bit_cast(uint16_t, (__bf16)x);
+    float head = __uint_as_float((uint32_t)limb[0] << 16);
+    if (!(fabsf(head) < INFINITY) && fabsf(x) < INFINITY) {
+        head = __uint_as_float(__float_as_uint(x) & 0xFFFF0000u);
+        limb[0] = (uint16_t)(__float_as_uint(head) >> 16);
+    }
+    float rest = fabsf(x) < INFINITY ? x - head : 0.0f;
+#pragma unroll
+    for (int l = 1; l < NL; l++) {
+        limb[l] = __builtin_bit_cast(uint16_t, (__bf16)rest);
+        rest -= __uint_as_float((uint32_t)limb[l] << 16);
+    }
+}
+__device__ __forceinline__ float limb_value(uint16_t l) { return __uint_as_float((uint32_t)l << 16); }
+
+// e4m3 (1 sign, 4 exponent, 3 mantissa bits, bias 7, no infinities, 0x7F NaN).
+__device__ __forceinline__ float e4m3_value(uint8_t b)
+{
+    return __builtin_amdgcn_cvt_f32_fp8((int)b, 0);
+}
+// 2^(s - 127); 255 is NaN, 0 is 2^-127.
+__device__ __forceinline__ float e8m0_value(uint32_t s)
+{
+    return s == 255u ? NAN : s == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(s << 23);
+}
+
+// ---- activations -------------------------------------------------------------
+// Standard normal distribution function.  For results rounded to 16 bits: the
+// five-term rational approximation of Abramowitz and Stegun 7.1.26 (absolute
+// error 7.5e-8), one reciprocal and one exponential; the library's erf takes
+// about three times as long and made up most of the epilogue of a GELU layer.
+template <bool EXACT> __device__ __forceinline__ float normal_cdf(float z)
+{
+    if constexpr (EXACT) return 0.5f * erfcf(-0.70710678118654752f * z);
+    const float x = fabsf(z) * 0.70710678118654752f;
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.0f));
+    const float p = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
+                             0.254829592f);
+    const float h = 0.5f * p * __builtin_amdgcn_exp2f(x * x * -1.4426950408889634f);
+    return z >= 0.0f ? 1.0f - h : h;
+}
+template <bool EXACT> __device__ __forceinline__ float logistic(float z)
+{
+    if constexpr (EXACT) return 1.0f / (1.0f + expf(-z));
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
+}
+template <bool EXACT> __device__ __forceinline__ float activate(float z, int act)
+{
+    if (act == GS_ACT_RELU) return z < 0.0f ? 0.0f : z;               // a NaN stays one
+    if (act == GS_ACT_SILU) return z * logistic<EXACT>(z);
+    if (act == GS_ACT_GELU) return z * normal_cdf<EXACT>(z);
+    return z;
+}
+template <bool EXACT> __device__ __forceinline__ float activate_slope(float z, int act)
+{
+    if (act == GS_ACT_RELU) return z > 0.0f ? 1.0f : z == z ? 0.0f : z;
+    if (act == GS_ACT_SILU) {
+        const float s = logistic<EXACT>(z);
+        return s * fmaf(z, 1.0f - s, 1.0f);
+    }
+    if (act == GS_ACT_GELU) {
+        const float e = EXACT ? expf(-0.5f * z * z) : __builtin_amdgcn_exp2f(z * z * -0.72134752044448170f);
+        return normal_cdf<EXACT>(z) + z * 0.39894228040143268f * e;
+    }
+    return 1.0f;
+}
+
+}  // namespace gsi

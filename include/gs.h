@@ -587,6 +587,212 @@ gs_status gs_active_mask_static(const float *scores, int64_t n, int64_t keep,
                                 uint8_t *mask, void *stream);
 size_t gs_active_mask_static_scratch_bytes(void);
 
+/* ---------------------------------------------------------------------- */
+/* A network head that predicts Gaussians (the GlobalSplat page, step (4) of
+ * its pipeline: heads that turn scene tokens into position, scale, rotation,
+ * opacity and SH colour).  Residual blocks of a root-mean-square norm and two
+ * matrix products, and a last product that writes one plane per Gaussian
+ * parameter, the [rows][n] layout of gs_gaussians and gs_grads; their
+ * gradients; the weights' orthogonalised momentum step; and an 8-bit form
+ * for serving.  All matrices are row-major device memory with a row stride in
+ * elements; every product and sum is accumulated in fp32. */
+
+/* Element types.  GS_DTYPE_MXFP8 is a block format: e4m3 values (largest 448)
+ * with one e8m0 scale 2^(s-127) per 32 consecutive values of a row, held in a
+ * second array; the value is the product of the two.  A block is written with
+ * the smallest exponent in -127..127 that leaves no value above 448, values
+ * rounded to nearest even; a block with an infinity or NaN gets the scale 255
+ * (NaN) and reads back as NaN throughout. */
+typedef enum gs_dtype { GS_DTYPE_F32 = 0, GS_DTYPE_F16 = 1, GS_DTYPE_BF16 = 2, GS_DTYPE_MXFP8 = 3 } gs_dtype;
+
+/* relu max(z, 0); silu z / (1 + exp(-z)); gelu z Phi(z) with the normal
+ * distribution function Phi. */
+typedef enum gs_activation { GS_ACT_NONE = 0, GS_ACT_RELU = 1, GS_ACT_SILU = 2, GS_ACT_GELU = 3 } gs_activation;
+
+/* Root-mean-square norm of the rows of x + residual:
+ *     s = x + residual,  rstd = (mean_j s_j^2 + eps)^(-1/2),  y_j = s_j rstd gamma_j
+ * in fp32 from the unrounded s; sum receives s rounded to `dtype`.  A row of
+ * zeros gives zeros.  y may be x or residual, sum may be x or residual
+ * (each element is read before it is written) with the same stride, unless
+ * y is 8-bit.  Strides are in elements (of the scales: bytes). */
+typedef struct gs_rms_norm {
+    int64_t m;                  /* rows, 0 .. 2^30                             */
+    int32_t n;                  /* row length, 1 .. 2^20; y_dtype MXFP8: a
+                                   multiple of 32                              */
+    int32_t dtype;              /* gs_dtype of x, residual, sum: F32, F16, BF16 */
+    int32_t y_dtype;            /* of y: `dtype` or GS_DTYPE_MXFP8              */
+    float eps;                  /* >= 0, finite                                */
+    const void *x;              /* [m][n]                                      */
+    int64_t x_stride;
+    const void *residual;       /* [m][n] or NULL: none                        */
+    int64_t residual_stride;
+    const float *gamma;         /* [n] or NULL: ones                           */
+    void *sum;                  /* [m][n] or NULL: not kept                    */
+    int64_t sum_stride;
+    void *y;                    /* [m][n]                                      */
+    int64_t y_stride;
+    uint8_t *y_scales;          /* MXFP8: [m][n / 32]                          */
+    int64_t y_scales_stride;
+    float *rstd;                /* [m] or NULL: not kept                       */
+} gs_rms_norm;
+
+/* Errors: GS_ERR_INVALID_ARG (NULL descriptor or arrays with m > 0, sizes or
+ * strides out of range, an unknown type, a misaligned pointer, eps negative
+ * or not finite), GS_ERR_UNSUPPORTED (a y_dtype that is neither). */
+gs_status gs_rms_norm_fwd(const gs_rms_norm *norm /* host */, void *stream);
+
+/* Backward of gs_rms_norm_fwd from the kept sum (x itself without a residual)
+ * and rstd, for the gradient dy of y and, optionally, the gradient dsum that
+ * reaches the sum along the residual stream:
+ *     g = dy gamma,  h = s rstd,  dx = rstd (g - h mean_j(g_j h_j)) + dsum
+ *     dgamma_j (+)= sum over rows of dy_j h_j
+ * dx is the gradient of x and of residual alike.  dx may be dy or dsum (same
+ * stride).  dgamma is reduced in a fixed order (bit-reproducible). */
+typedef struct gs_rms_norm_grads {
+    int64_t m;
+    int32_t n;
+    int32_t dtype;              /* of sum, dy, dsum, dx: F32, F16, BF16        */
+    const void *sum;
+    int64_t sum_stride;
+    const float *rstd;          /* [m]                                         */
+    const float *gamma;         /* [n] or NULL: ones                           */
+    const void *dy;
+    int64_t dy_stride;
+    const void *dsum;           /* [m][n] or NULL                              */
+    int64_t dsum_stride;
+    void *dx;
+    int64_t dx_stride;
+    float *dgamma;              /* [n] or NULL: not wanted                     */
+    int32_t accumulate;         /* nonzero: dgamma += (else dgamma =)          */
+} gs_rms_norm_grads;
+
+/* Workspace of gs_rms_norm_bwd, in bytes (0 without dgamma). */
+size_t gs_rms_norm_bwd_workspace_bytes(int64_t m, int32_t n);
+
+/* Errors: as gs_rms_norm_fwd; GS_ERR_WORKSPACE. */
+gs_status gs_rms_norm_bwd(const gs_rms_norm_grads *grads /* host */, void *workspace, size_t workspace_bytes,
+                          void *stream);
+
+/* Quantises x [m][n] (F32, F16 or BF16) to GS_DTYPE_MXFP8: codes [m][n] and
+ * scales [m][n / 32] (weights of the 8-bit product, or activations that no
+ * norm produced).  Errors: as gs_rms_norm_fwd. */
+gs_status gs_mxfp8_quantize(const void *x, int32_t dtype, int64_t m, int32_t n, int64_t x_stride, uint8_t *codes,
+                            int64_t codes_stride, uint8_t *scales, int64_t scales_stride, void *stream);
+
+/* Linear layer:  z = x w^T + bias,  y = act(z) + residual.
+ * y and residual are [m][n] rows, or with `planes` [n][m] (one plane of m
+ * values per output, e.g. per Gaussian parameter).
+ * fp32 operands are multiplied as three bf16 limbs each (six products), which
+ * keeps fp32's accuracy; values under 2^-110 lose low bits, and an infinity
+ * or NaN in an operand makes the sums it enters infinite or NaN.  8-bit
+ * operands with an fp32 y are widened and multiplied in bf16, exactly; with a
+ * 16-bit y by 8-bit matrix instructions, whose sums keep fewer bits than
+ * fp32. */
+typedef struct gs_linear {
+    int64_t m;                  /* rows of x, 0 .. 2^30                        */
+    int32_t n, k;               /* outputs and inputs, 1 .. 2^20; MXFP8: k a
+                                   multiple of 32                              */
+    int32_t dtype;              /* of x and w: any gs_dtype                    */
+    int32_t y_dtype;            /* of y and residual: F32, F16 or BF16          */
+    int32_t activation;         /* gs_activation                               */
+    int32_t planes;             /* nonzero: y, residual (and dy) are [n][m]    */
+    const void *x;              /* [m][k]                                      */
+    int64_t x_stride;
+    const void *w;              /* [n][k]                                      */
+    int64_t w_stride;
+    const uint8_t *x_scales;    /* MXFP8: [m][k / 32]                          */
+    int64_t x_scales_stride;
+    const uint8_t *w_scales;    /* MXFP8: [n][k / 32]                          */
+    int64_t w_scales_stride;
+    const float *bias;          /* [n] or NULL                                 */
+    const void *residual;       /* y's layout, or NULL; may be y itself        */
+    int64_t residual_stride;
+    void *y;
+    int64_t y_stride;
+    void *z;                    /* [m][n] of `dtype` (F32, F16, BF16) for the
+                                   backward, or NULL: not kept                 */
+    int64_t z_stride;
+} gs_linear;
+
+/* Workspace of gs_linear_fwd, in bytes (often 0). */
+size_t gs_linear_fwd_workspace_bytes(const gs_linear *linear /* host */);
+
+/* Errors: GS_ERR_INVALID_ARG (NULL descriptor or arrays with m > 0, sizes or
+ * strides out of range, an unknown type or activation, a misaligned pointer),
+ * GS_ERR_UNSUPPORTED (MXFP8 with z kept, or k no multiple of 32; an 8-bit y),
+ * GS_ERR_WORKSPACE. */
+gs_status gs_linear_fwd(const gs_linear *linear /* host */, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Gradients of the linear layer, for the gradient dy of y (y's layout and
+ * y_dtype).  With an activation z must be the one the forward kept:
+ *     dz = dy act'(z),  dx = dz w,  dw (+)= dz^T x,  db (+)= sum over rows of dz
+ * (the residual's gradient is dy itself).  For 16-bit operands dz is rounded
+ * to `dtype` for the two products; db sums it unrounded.  NULL outputs are
+ * not computed.  Sums over rows are reduced in a fixed order.  The outputs
+ * must not overlap the inputs. */
+typedef struct gs_linear_grads {
+    const void *dy;
+    int64_t dy_stride;
+    void *dx;                   /* [m][k] of `dtype`, or NULL                  */
+    int64_t dx_stride;
+    void *dw;                   /* [n][k] of dw_dtype, or NULL                 */
+    int64_t dw_stride;
+    int32_t dw_dtype;           /* F32 or `dtype`                              */
+    int32_t accumulate;         /* nonzero: dw += and db += (else =)           */
+    float *db;                  /* [n], or NULL                                */
+} gs_linear_grads;
+
+/* Workspace of gs_linear_bwd, in bytes. */
+size_t gs_linear_bwd_workspace_bytes(const gs_linear *linear /* host */, const gs_linear_grads *grads /* host */);
+
+/* Uses m, n, k, dtype, y_dtype, activation, planes, x, w and z of `linear`.
+ * Errors: as gs_linear_fwd; GS_ERR_INVALID_ARG for an activation without z;
+ * GS_ERR_UNSUPPORTED for 8-bit operands. */
+gs_status gs_linear_bwd(const gs_linear *linear /* host */, const gs_linear_grads *grads /* host */, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
+/* Orthogonalised update of `batch` weight matrices of one shape (the Muon
+ * optimiser's step).  From an update U [rows][cols], Newton-Schulz iterations
+ *     X = U / (|U|_F + eps);  steps times:  A = X X^T,  X = a X + (b A + c A^2) X
+ * (on U^T when rows > cols) drive every singular value of U towards 1; O is
+ * the last X.
+ *   gs_orthogonalize  U = grad, out = O
+ *   gs_muon_step      momentum_out = beta momentum + grad
+ *                     U = grad + beta momentum_out (nesterov) or momentum_out
+ *                     weight_out = weight (1 - lr weight_decay) - lr scale O
+ * Products of fp32 results use three bf16 limbs per operand, of 16-bit
+ * results two (see gs_linear), sums are fp32 throughout.  A matrix of zeros
+ * gives O = 0.  momentum_out may be momentum, weight_out may be weight, out
+ * may be grad. */
+typedef struct gs_muon {
+    int32_t batch;              /* matrices, 0 .. 65535                        */
+    int32_t rows, cols;         /* 1 .. 16384 each                             */
+    int32_t grad_dtype;         /* F32, F16 or BF16                            */
+    int32_t out_dtype;          /* of out, or of weight and weight_out: F32,
+                                   F16 or BF16                                 */
+    int32_t steps;              /* 1 .. 64 iterations                          */
+    float a, b, c;              /* coefficients (3.4445, -4.7750, 2.0315 reach
+                                   singular values of about 0.7 .. 1.2 in 5)   */
+    float eps;                  /* > 0                                         */
+    float lr, beta, weight_decay, scale;        /* gs_muon_step only, finite   */
+    int32_t nesterov;
+    const void *grad;           /* [batch][rows][cols], as every array here    */
+    void *out;                  /* gs_orthogonalize                            */
+    const float *momentum;      /* gs_muon_step ...                            */
+    float *momentum_out;
+    const void *weight;
+    void *weight_out;
+} gs_muon;
+
+/* Workspace of gs_orthogonalize and gs_muon_step, in bytes. */
+size_t gs_muon_workspace_bytes(const gs_muon *muon /* host */);
+
+/* Errors: GS_ERR_INVALID_ARG (NULL descriptor or arrays with batch > 0, sizes
+ * or types out of range, eps <= 0, a coefficient that is not finite, a
+ * misaligned pointer), GS_ERR_WORKSPACE. */
+gs_status gs_orthogonalize(const gs_muon *muon /* host */, void *workspace, size_t workspace_bytes, void *stream);
+gs_status gs_muon_step(const gs_muon *muon /* host */, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Static description of a status code. */
 const char *gs_status_string(gs_status status);
 
