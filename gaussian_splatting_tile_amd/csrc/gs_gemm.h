@@ -47,6 +47,7 @@ struct Args {
     int64_t ldps, ldqs;
     int tiles_p, tiles_q;
     int k_split;                                       // k range of one split (a multiple of the k tile), grid.y splits
+    int symmetric;                                     // the result is: only tiles with p tile <= q tile are formed
 };
 
 typedef float f4 __attribute__((ext_vector_type(4)));
@@ -124,6 +125,32 @@ template <int BX, int BK, bool T> struct Tile {
 // size, which reads as zeros.
 constexpr uint32_t kBufferBytes = 0x80000000u;          // of every buffer descriptor: offsets stay below
 
+// The descriptor's words: base, no stride, size, 32-bit raw data.
+__device__ __forceinline__ i4 buffer_at(const void *base)
+{
+    const uint64_t b = (uint64_t)(uintptr_t)base;
+    return i4{(int)__builtin_amdgcn_readfirstlane((int)b), (int)__builtin_amdgcn_readfirstlane((int)(b >> 32) & 0xFFFF),
+              (int)kBufferBytes, 0x00020000};
+}
+// 64 lanes' pieces of 16 bytes, or bytes widened to words, to consecutive
+// places from `lds` (the same in all lanes) on.  Written as assembly because the
+// compiler cannot tell which stage a transposing LDS read touches and would
+// wait for every load in flight before each; the loads have no result
+// registers, and stage_barrier waits for them.  (m0 cannot be named as
+// clobbered: it is reserved.  Nothing else in these kernels uses it.)
+__device__ __forceinline__ void load_lds16(i4 buffer, uint32_t off, const char *lds)
+{
+    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char *)lds);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(off), "s"(buffer)
+                 : "memory");
+}
+__device__ __forceinline__ void load_lds1(i4 buffer, uint32_t off, const char *lds)
+{
+    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char *)lds);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ubyte %1, %2, 0 offen lds" ::"s"(at), "v"(off), "s"(buffer)
+                 : "memory");
+}
+
 template <class TL, int THREADS, bool T, int ES> struct Direct {
     static constexpr int kLoads = TL::kChunks / THREADS;
     static_assert(TL::kChunks % THREADS == 0, "tile and block size");
@@ -149,14 +176,36 @@ template <class TL, int THREADS, bool T, int ES> struct Direct {
     // left: k values from the tile's base to the end
     __device__ __forceinline__ void issue(const char *base, char *lds, int left, int wave) const
     {
-        const __amdgpu_buffer_rsrc_t rsrc =
-            __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(base), 0, (int)kBufferBytes, 0x00020000);
+        const i4 buffer = buffer_at(base);
 #pragma unroll
         for (int j = 0; j < kLoads; j++) {
             const int k = T ? k0 + j * kLineStep : k0;
             const uint32_t o = k < left ? off[j] : kBufferBytes;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rsrc, (__attribute__((address_space(3))) void *)(lds + (j * THREADS + wave * 64) * 16), 16, o, 0, 0, 0);
+            load_lds16(buffer, o, lds + (j * THREADS + wave * 64) * 16);
+        }
+    }
+};
+
+// Scale bytes of a kMX8 tile: 4 blocks of 32 k per row, each widened to a word
+// in LDS, [BX][4].  Blocks past the end of k read as 0, a finite scale.
+template <int BX, int THREADS> struct Scales {
+    static constexpr int kLoads = BX * 4 / THREADS;
+    static_assert(BX * 4 % THREADS == 0, "tile and block size");
+    uint32_t off[kLoads];
+
+    __device__ __forceinline__ void init(int x0, int X, int64_t ld, int tid)
+    {
+#pragma unroll
+        for (int j = 0; j < kLoads; j++)
+            off[j] = (uint32_t)min((j * THREADS + tid) >> 2, X - 1 - x0) * (uint32_t)ld + (tid & 3);
+    }
+    __device__ __forceinline__ void issue(const uint8_t *base, char *lds, int blocks, int wave) const
+    {
+        const i4 buffer = buffer_at(base);
+#pragma unroll
+        for (int j = 0; j < kLoads; j++) {
+            const uint32_t o = (int)(threadIdx.x & 3) < blocks ? off[j] : kBufferBytes;
+            load_lds1(buffer, o, lds + (j * THREADS + wave * 64) * 4);
         }
     }
 };
@@ -228,6 +277,23 @@ __device__ __forceinline__ void tile_of(int b, int tiles_p, int tiles_q, int &tp
     tq = g * 8 + r - tp * h;
 }
 
+// The b-th tile of the triangle tp <= tq, row by row.
+__device__ __forceinline__ void triangle_of(int b, int &tp, int &tq)
+{
+    tq = (int)((sqrtf(8.0f * (float)b + 1.0f) - 1.0f) * 0.5f);
+    while ((tq + 1) * (tq + 2) / 2 <= b) tq++;
+    while (tq * (tq + 1) / 2 > b) tq--;
+    tp = b - tq * (tq + 1) / 2;
+}
+
+// Waits until at most LEFT of the wave's loads are outstanding and its LDS
+// reads are done, then for the other waves.
+template <int LEFT> __device__ __forceinline__ void stage_barrier()
+{
+    static_assert(LEFT >= 0 && LEFT < 64, "vmcnt");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LEFT) : "memory");
+}
+
 // Orders a wave's own LDS writes and reads across its lanes (the lanes run in
 // lockstep and LDS serves a wave in order: only the compiler has to be held).
 __device__ __forceinline__ void wave_fence()
@@ -237,9 +303,17 @@ __device__ __forceinline__ void wave_fence()
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// EPI::store(e, p, q, valid, v, batch, split): v[0 .. valid - 1] (LDS, 16-byte
-// aligned) are the sums of p .. at q.
-template <int KIND, int NL, int BK, int BP, int BQ, int WP, int WQ, bool PT, bool QT, bool STAGED, class EPI>
+// Fragments along p that the waves can turn at once within `bytes` of LDS.
+constexpr int turn_part(int fp, int waves, int bytes)
+{
+    while (fp > 1 && waves * 16 * (fp * 16 + 4) * 4 > bytes) fp /= 2;
+    return fp;
+}
+
+// The epilogue takes 8 sums of consecutive p at a time where EPI::vec(e) allows,
+// EPI::store8(e, p, q, v, batch, split, mirror), else single ones,
+// EPI::store1.  mirror: the tile also stands for its transpose.
+template <int KIND, int NL, int NS, int BK, int BP, int BQ, int WP, int WQ, bool PT, bool QT, bool STAGED, class EPI>
 __global__ __launch_bounds__(WP *WQ * 64, NL == 3 && BP == 128 ? 1 : 2) void product_kernel(Args a, typename EPI::Args e)
 {
     constexpr int kThreads = WP * WQ * 64;
@@ -249,16 +323,23 @@ __global__ __launch_bounds__(WP *WQ * 64, NL == 3 && BP == 128 ? 1 : 2) void pro
     static_assert(KIND != kMX8 || (!PT && !QT && !STAGED && NL == 1 && BK == 64), "8-bit operands");
     using TP = Tile<BP, BK, PT>;
     using TQ = Tile<BQ, BK, QT>;
-    constexpr int kStage = NL * (TP::kBytes + TQ::kBytes);
-    // after the last product each wave turns its sums round in LDS, 16 q at a time
-    constexpr int kTurnLd = FP * 16 + 4, kTurn = WP * WQ * 16 * kTurnLd * 4;
-    __shared__ __align__(128) char lds0[kStage > kTurn ? kStage : kTurn];
+    constexpr int kScaleAt = NL * (TP::kBytes + TQ::kBytes);
+    constexpr int kStage = kScaleAt + (KIND == kMX8 ? (BP + BQ) * 16 : 0);
+    // after the last product each wave turns its sums round in a stage's place,
+    // 16 q by as many p as fit there at a time
+    constexpr int kPart = turn_part(FP, WP * WQ, kStage), kTurnLd = kPart * 16 + 4;
+    __shared__ __align__(128) char lds0[kStage];
     __shared__ __align__(128) char lds1[kStage];
+    __shared__ __align__(128) char lds2[NS > 2 ? kStage : 16];
+    __shared__ __align__(128) char lds3[NS > 3 ? kStage : 16];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wp = wave / WQ, wq = wave % WQ;
     int tp, tq;
-    tile_of(blockIdx.x, a.tiles_p, a.tiles_q, tp, tq);
+    if (a.symmetric)
+        triangle_of(blockIdx.x, tp, tq);
+    else
+        tile_of(blockIdx.x, a.tiles_p, a.tiles_q, tp, tq);
     const int p0 = tp * BP, q0 = tq * BQ;
     const int kbeg = blockIdx.y * a.k_split, kend = min(a.K, kbeg + a.k_split);
     const char *pb = static_cast<const char *>(a.p), *qb = static_cast<const char *>(a.q);
@@ -269,8 +350,16 @@ __global__ __launch_bounds__(WP *WQ * 64, NL == 3 && BP == 128 ? 1 : 2) void pro
 #pragma unroll
         for (int j = 0; j < FQ; j++) acc[i][j] = f4{0, 0, 0, 0};
 
-    auto compute = [&](const char *s, const int *sp, const int *sq) {
+    // issue() starts the next tile's loads once the first fragments are on their
+    // way: the wave's LDS reads do not queue behind them
+    auto compute = [&](const char *s, auto &&issue) {
         if constexpr (KIND == kMX8) {
+            const int *sp = reinterpret_cast<const int *>(s + kScaleAt) + (wp * FP * 16 + (lane & 15)) * 4 + (lane >> 4);
+            const int *sq = reinterpret_cast<const int *>(s + kScaleAt + BP * 16) + (wq * FQ * 16 + (lane & 15)) * 4 + (lane >> 4);
+            int sqv[FQ];
+#pragma unroll
+            for (int j = 0; j < FQ; j++) sqv[j] = sq[j * 64];
+            bool issued = false;
             i4 qf[FQ][2];
 #pragma unroll
             for (int j = 0; j < FQ; j++)
@@ -279,8 +368,10 @@ __global__ __launch_bounds__(WP *WQ * 64, NL == 3 && BP == 128 ? 1 : 2) void pro
 #pragma unroll
             for (int i = 0; i < FP; i++) {
                 const i4 lo = TP::frag(s, wp * FP * 16, i, 0, lane), hi = TP::frag(s, wp * FP * 16, i, 1, lane);
+                if (!issued) issue();
+                issued = true;
 #pragma unroll
-                for (int j = 0; j < FQ; j++) acc[i][j] = mfma_mx(lo, hi, sp[i], qf[j][0], qf[j][1], sq[j], acc[i][j]);
+                for (int j = 0; j < FQ; j++) acc[i][j] = mfma_mx(lo, hi, sp[i * 64], qf[j][0], qf[j][1], sqv[j], acc[i][j]);
             }
         } else {
 #pragma unroll
@@ -295,6 +386,7 @@ __global__ __launch_bounds__(WP *WQ * 64, NL == 3 && BP == 128 ? 1 : 2) void pro
                     for (int j = 0; j < FQ; j++)
                         qf[l][j] = TQ::frag(s + NL * TP::kBytes + l * TQ::kBytes, wq * FQ * 16, j, kk, lane);
                 }
+                if (kk == 0) issue();
 #pragma unroll
                 for (int order = NL - 1; order >= 0; order--)
 #pragma unroll
@@ -313,48 +405,21 @@ __global__ __launch_bounds__(WP *WQ * 64, NL == 3 && BP == 128 ? 1 : 2) void pro
         qb += (int64_t)blockIdx.z * a.batch_q * ES;
         Direct<TP, kThreads, PT, ES> dp;
         Direct<TQ, kThreads, QT, ES> dq;
+        Scales<BP, kThreads> cp;
+        Scales<BQ, kThreads> cq;
         dp.init(p0, a.Pl, a.ldp, tid);
         dq.init(q0, a.Ql, a.ldq, tid);
+        if constexpr (KIND == kMX8) {
+            cp.init(p0, a.P, a.ldps, tid);
+            cq.init(q0, a.Q, a.ldqs, tid);
+        }
+        constexpr int kLoadsPerTile = NL * (dp.kLoads + dq.kLoads) + (KIND == kMX8 ? cp.kLoads + cq.kLoads : 0);
         // first elements of the tile at k = kbeg, and the step to the next
         pb += (PT ? (int64_t)kbeg * a.ldp + p0 : (int64_t)p0 * a.ldp + kbeg) * ES;
         qb += (QT ? (int64_t)kbeg * a.ldq + q0 : (int64_t)q0 * a.ldq + kbeg) * ES;
         const int64_t step_p = (PT ? a.ldp : 1) * (int64_t)kStepK * ES, step_q = (QT ? a.ldq : 1) * (int64_t)kStepK * ES;
         const int nt = (kend - kbeg + kStepK - 1) / kStepK;
 
-        // scale bytes of a lane's rows, by buffers that start at the tile's rows
-        constexpr int NS = KIND == kMX8 ? 1 : 0;
-        int sp0[NS ? FP : 1], sq0[NS ? FQ : 1], sp1[NS ? FP : 1], sq1[NS ? FQ : 1];
-        uint32_t sp_off[NS ? FP : 1], sq_off[NS ? FQ : 1];
-        if constexpr (NS) {
-#pragma unroll
-            for (int i = 0; i < FP; i++)
-                sp_off[i] = (uint32_t)min((wp * FP + i) * 16 + (lane & 15), a.P - 1 - p0) * (uint32_t)a.ldps;
-#pragma unroll
-            for (int j = 0; j < FQ; j++)
-                sq_off[j] = (uint32_t)min((wq * FQ + j) * 16 + (lane & 15), a.Q - 1 - q0) * (uint32_t)a.ldqs;
-        }
-        auto scales = [&](int t, int *sp, int *sq) {
-            if constexpr (NS) {
-                const __amdgpu_buffer_rsrc_t rp = __builtin_amdgcn_make_buffer_rsrc(
-                    const_cast<uint8_t *>(a.ps + p0 * a.ldps), 0, (int)kBufferBytes, 0x00020000);
-                const __amdgpu_buffer_rsrc_t rq = __builtin_amdgcn_make_buffer_rsrc(
-                    const_cast<uint8_t *>(a.qs + q0 * a.ldqs), 0, (int)kBufferBytes, 0x00020000);
-                // blocks past the end of k: their values are 0, any finite scale does
-                const int b = kbeg / 32 + t * 4 + (lane >> 4);
-                const uint32_t bo = (uint32_t)min(b, (a.K >> 5) - 1);
-                const bool in = b < (a.K >> 5);
-#pragma unroll
-                for (int i = 0; i < FP; i++) {
-                    const int v = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rp, sp_off[i] + bo, 0, 0);
-                    sp[i] = in ? v : 127;
-                }
-#pragma unroll
-                for (int j = 0; j < FQ; j++) {
-                    const int v = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rq, sq_off[j] + bo, 0, 0);
-                    sq[j] = in ? v : 127;
-                }
-            }
-        };
         auto issue = [&](int t, char *s) {
             const int left = kend - kbeg - t * kStepK;
             const char *pt = pb + t * step_p, *qt = qb + t * step_q;
@@ -363,25 +428,31 @@ __global__ __launch_bounds__(WP *WQ * 64, NL == 3 && BP == 128 ? 1 : 2) void pro
                 dp.issue(pt + l * a.plane_p * ES, s + l * TP::kBytes, left, wave);
                 dq.issue(qt + l * a.plane_q * ES, s + NL * TP::kBytes + l * TQ::kBytes, left, wave);
             }
+            if constexpr (KIND == kMX8) {
+                const int b = kbeg / 32 + t * 4, blocks = (a.K >> 5) - b;
+                cp.issue(a.ps + (int64_t)p0 * a.ldps + b, s + kScaleAt, blocks, wave);
+                cq.issue(a.qs + (int64_t)q0 * a.ldqs + b, s + kScaleAt + BP * 16, blocks, wave);
+            }
         };
-        // two LDS stages: while one is multiplied the next is on its way
-        issue(0, lds0);
-        scales(0, sp0, sq0);
+        // NS stages in LDS: tile t is multiplied while the next NS - 1 are on
+        // their way.  A wave's loads land in order, so waiting until only the
+        // later tiles' are outstanding leaves tile t complete; the barrier then
+        // makes it so for every wave, and frees the stage of tile t - 1.  Every
+        // tile counts the same loads: past the end they read zeros.
+        auto turn_stage = [&](int t, char *now, char *next) {
+            stage_barrier<kLoadsPerTile *(NS - 2)>();
+            compute(now, [&] { issue(t + NS - 1, next); });
+        };
+        char *const stage[4] = {lds0, lds1, lds2, lds3};
+#pragma unroll
+        for (int t = 0; t < NS - 1; t++) issue(t, stage[t]);
         int t = 0;
-        for (; t + 1 < nt; t += 2) {
-            __syncthreads();                            // stage 0 has landed, stage 1 is free
-            issue(t + 1, lds1);
-            scales(t + 1, sp1, sq1);
-            compute(lds0, sp0, sq0);
-            __syncthreads();
-            issue(t + 2, lds0);                         // zeros when there is no such tile
-            scales(t + 2, sp0, sq0);
-            compute(lds1, sp1, sq1);
-        }
-        if (t < nt) {
-            __syncthreads();
-            compute(lds0, sp0, sq0);
-        }
+        for (; t + NS <= nt; t += NS)
+#pragma unroll
+            for (int i = 0; i < NS; i++) turn_stage(t + i, stage[i], stage[(i + NS - 1) % NS]);
+        if (t < nt) turn_stage(t, stage[0], stage[NS - 1]);
+        if (NS > 2 && t + 1 < nt) turn_stage(t + 1, stage[1], stage[0]);
+        if (NS > 3 && t + 2 < nt) turn_stage(t + 2, stage[2], stage[1]);
     } else {
         Staged<TP, kThreads, PT, NL, KIND> sp;
         Staged<TQ, kThreads, QT, NL, KIND> sq;
@@ -398,27 +469,53 @@ __global__ __launch_bounds__(WP *WQ * 64, NL == 3 && BP == 128 ? 1 : 2) void pro
             sq.write(s + NL * TP::kBytes, tid);
             __syncthreads();                            // also: every wave is done with this stage's last use
             if (k0 + kStepK < kend) load(k0 + kStepK);
-            compute(s, nullptr, nullptr);
+            compute(s, [] {});
         }
     }
 
     // sums to the epilogue, 8 consecutive p at a time; a lane's accumulator holds
     // p = 16 i + 4 g + (0..3) at q = 16 j + r
-    __syncthreads();
+    stage_barrier<0>();
     float *turn = reinterpret_cast<float *>(lds0) + wave * (16 * kTurnLd);
-    constexpr int kLanesP = FP * 2, kRowsQ = 64 / kLanesP;      // lanes along p, q rows at a time
-#pragma unroll
-    for (int j = 0; j < FQ; j++) {
-#pragma unroll
-        for (int i = 0; i < FP; i++)
-            *reinterpret_cast<f4 *>(turn + (lane & 15) * kTurnLd + i * 16 + (lane >> 4) * 4) = acc[i][j];
-        wave_fence();
+    constexpr int kLanesP = kPart * 2, kRowsQ = 64 / kLanesP;   // lanes along p, q rows at a time
+    constexpr int kParts = FQ * (FP / kPart);
 #pragma unroll 1
-        for (int h = 0; h < 16; h += kRowsQ) {
-            const int qr = h + lane / kLanesP, pr = lane % kLanesP * 8;
-            const int p = p0 + wp * FP * 16 + pr, q = q0 + (wq * FQ + j) * 16 + qr;
-            if (p >= a.P || q >= a.Q) continue;
-            EPI::store(e, p, q, min(8, a.P - p), turn + qr * kTurnLd + pr, blockIdx.z, blockIdx.y);
+    for (int u = 0; u < kParts; u++) {
+        const int j = u / (FP / kPart), i0 = u % (FP / kPart) * kPart;
+        // accumulators have no run-time index: one of kParts branches
+#pragma unroll
+        for (int c = 0; c < kParts; c++)
+            if (u == c) {
+#pragma unroll
+                for (int i = 0; i < kPart; i++)
+                    *reinterpret_cast<f4 *>(turn + (lane & 15) * kTurnLd + i * 16 + (lane >> 4) * 4) =
+                        acc[c % (FP / kPart) * kPart + i][c / (FP / kPart)];
+            }
+        wave_fence();
+        const int pb0 = p0 + (wp * FP + i0) * 16, qb0 = q0 + (wq * FQ + j) * 16;
+        const bool mirror = a.symmetric && tp != tq;
+        if (EPI::vec(e)) {
+#pragma unroll 1
+            for (int h = 0; h < 16; h += kRowsQ) {
+                const int qr = h + lane / kLanesP, pr = lane % kLanesP * 8;
+                const int p = pb0 + pr, q = qb0 + qr;
+                if (qr >= 16 || q >= a.Q) continue;     // two lanes a row would reach 32 rows
+                if (p + 8 <= a.P) {
+                    float v[8];
+                    load8_vec(turn + qr * kTurnLd + pr, v);
+                    EPI::store8(e, p, q, v, blockIdx.z, blockIdx.y, mirror);
+                } else {
+#pragma unroll 1
+                    for (int i = 0; i < a.P - p; i++) EPI::store1(e, p + i, q, turn[qr * kTurnLd + pr + i], blockIdx.z, blockIdx.y);
+                }
+            }
+        } else {
+#pragma unroll 2
+            for (int x = lane; x < 256 * kPart; x += 64) {
+                const int p = pb0 + x % (16 * kPart), q = qb0 + x / (16 * kPart);
+                if (p < a.P && q < a.Q)
+                    EPI::store1(e, p, q, turn[x / (16 * kPart) * kTurnLd + x % (16 * kPart)], blockIdx.z, blockIdx.y);
+            }
         }
         wave_fence();
     }
@@ -435,7 +532,7 @@ inline bool direct_ok(const void *p, int es, int64_t ld, int64_t extent)
     return al16(p) && ld % per == 0 && extent % per == 0 && ld * es < (1 << 23);
 }
 
-template <int KIND, int NL, int BK, int BP, int BQ, int WP, int WQ, bool PT, bool QT, bool STAGED, class EPI>
+template <int KIND, int NL, int NS, int BK, int BP, int BQ, int WP, int WQ, bool PT, bool QT, bool STAGED, class EPI>
 hipError_t launch(Args a, const typename EPI::Args &e, int splits, int batch, hipStream_t s)
 {
     constexpr int kStepK = KIND == kMX8 ? 2 * BK : BK;
@@ -444,8 +541,9 @@ hipError_t launch(Args a, const typename EPI::Args &e, int splits, int batch, hi
     const int nt = (a.K + kStepK - 1) / kStepK, per = (nt + splits - 1) / splits;
     if ((nt + per - 1) / per != splits) return hipErrorInvalidValue;       // every split has at least one tile
     a.k_split = per * kStepK;
-    const dim3 grid((unsigned)(a.tiles_p * a.tiles_q), (unsigned)splits, (unsigned)batch);
-    product_kernel<KIND, NL, BK, BP, BQ, WP, WQ, PT, QT, STAGED, EPI><<<grid, WP * WQ * 64, 0, s>>>(a, e);
+    const int tiles = a.symmetric ? a.tiles_p * (a.tiles_p + 1) / 2 : a.tiles_p * a.tiles_q;
+    const dim3 grid((unsigned)tiles, (unsigned)splits, (unsigned)batch);
+    product_kernel<KIND, NL, NS, BK, BP, BQ, WP, WQ, PT, QT, STAGED, EPI><<<grid, WP * WQ * 64, 0, s>>>(a, e);
     return hipGetLastError();
 }
 

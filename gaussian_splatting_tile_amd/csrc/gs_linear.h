@@ -46,9 +46,16 @@ struct LinearEpilogue {
     {
         const int64_t at = (int64_t)q * e.ldy + p;
         if (e.bias) {
-            const float b = e.bias_on_q ? e.bias[q] : 0.0f;
+            if (e.bias_on_q) {
+                const float b = e.bias[q];
 #pragma unroll
-            for (int i = 0; i < 8; i++) v[i] += e.bias_on_q ? b : e.bias[p + i];
+                for (int i = 0; i < 8; i++) v[i] += b;
+            } else {
+                float b[8];
+                load8_vec(e.bias + p, b);
+#pragma unroll
+                for (int i = 0; i < 8; i++) v[i] += b[i];
+            }
         }
         if (e.z) {
             if (e.z_p == 1) {
@@ -81,27 +88,21 @@ struct LinearEpilogue {
         store8_vec(e.y, e.y_type, at, v);
     }
 
-    __device__ static __forceinline__ void finish(const Args &e, int p, int q, int valid, const float *s)
-    {
-        if (e.vec && valid == 8) {
-            float v[8];
-            load8_vec(s, v);
-            finish8(e, p, q, v);
-        } else {
-#pragma unroll 1
-            for (int i = 0; i < valid; i++) finish1(e, p + i, q, s[i]);
-        }
-    }
+    __device__ static __forceinline__ bool vec(const Args &e) { return e.partial || e.vec; }
 
-    __device__ static __forceinline__ void store(const Args &e, int p, int q, int valid, const float *s, int, int split)
+    __device__ static __forceinline__ void store8(const Args &e, int p, int q, float v[8], int, int split, bool)
     {
-        if (e.partial) {
-            float v[8];
-            load8_vec(s, v);                                    // rows of partial sums are padded to 8
+        if (e.partial)                                          // rows of partial sums are padded to 8
             store8_vec(e.partial + split * e.split_stride + (int64_t)q * e.ld_partial + p, v);
-            return;
-        }
-        finish(e, p, q, valid, s);
+        else
+            finish8(e, p, q, v);
+    }
+    __device__ static __forceinline__ void store1(const Args &e, int p, int q, float v, int, int split)
+    {
+        if (e.partial)
+            e.partial[split * e.split_stride + (int64_t)q * e.ld_partial + p] = v;
+        else
+            finish1(e, p, q, v);
     }
 };
 
@@ -113,6 +114,9 @@ struct ProductPlan {
     int tile;                           // 0: 256 x 256, 1: 128 x 128, 2: 64 x 64 (staged: 1 and 2)
     int splits;                         // of k, each with at least one tile of k
 };
+
+// out[c] (+)= sum over rows r of part[r][c], in a fixed order (gs_norm.hip).
+hipError_t launch_sum_rows(const float *part, float *out, int n, int rows, int accumulate, hipStream_t s);
 
 hipError_t launch_product_bf16(const gemm::Args &a, const LinearEpilogue::Args &e, const ProductPlan &plan, hipStream_t s);
 hipError_t launch_product_f16(const gemm::Args &a, const LinearEpilogue::Args &e, const ProductPlan &plan, hipStream_t s);

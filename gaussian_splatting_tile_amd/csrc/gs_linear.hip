@@ -41,14 +41,14 @@ double product_cost(const TileRate &t, int64_t P, int64_t Q, int64_t K, int spli
 
 ProductPlan make_plan(int64_t P, int64_t Q, int64_t K, bool pt, bool qt, bool staged, int step_k, float work)
 {
-    static const TileRate direct[3] = {{256, 1, 5.0f}, {128, 2, 3.6f}, {64, 4, 1.8f}};
+    static const TileRate direct[3] = {{256, 1, 4.6f}, {128, 2, 4.1f}, {64, 3, 2.4f}};
     static const TileRate staged_[3] = {{256, 1, 0.0f}, {128, 1, 2.0f}, {64, 3, 1.2f}};
     ProductPlan best{pt, qt, staged, 2, 1};
     double least = 1e30;
     const int64_t nt = (K + step_k - 1) / step_k;
     for (int tile = staged ? 1 : 0; tile < 3; tile++) {
         const TileRate &t = staged ? staged_[tile] : direct[tile];
-        for (int64_t want = 1; want <= 64 && want <= nt; want = want < 4 ? want + 1 : want * 2) {
+        for (int64_t want = 1; want <= 16 && want <= nt; want = want < 4 ? want + 1 : want * 2) {
             const int64_t per = (nt + want - 1) / want;
             const int splits = (int)((nt + per - 1) / per);
             const double us = product_cost(t, P, Q, K, splits, work);
@@ -84,28 +84,37 @@ void finish_plan(Product &r, bool direct)
     r.e.ld_partial = (r.a.P + 7) & ~7;
     r.e.split_stride = r.e.ld_partial * r.a.Q;
     r.partial_bytes = r.plan.splits > 1 ? (size_t)r.plan.splits * r.e.split_stride * 4 : 0;
-    r.e.vec = vec_ok(r.e.y, r.e.y_type, r.e.ldy) && (!r.e.residual || vec_ok(r.e.residual, r.e.y_type, r.e.ldr)) &&
+    r.e.vec = (r.e.bias_on_q || al16(r.e.bias)) && vec_ok(r.e.y, r.e.y_type, r.e.ldy) && (!r.e.residual || vec_ok(r.e.residual, r.e.y_type, r.e.ldr)) &&
               (!r.e.z || r.e.z_p != 1 || vec_ok(r.e.z, r.e.z_type, r.e.z_q));
     r.e.exact = r.e.y_type == GS_DTYPE_F32 || (r.e.z && r.e.z_type == GS_DTYPE_F32);
 }
 
-// Sum of the splits, then the epilogue: a thread per 8 consecutive p.
-__global__ __launch_bounds__(kThreads) void reduce_splits(LinearEpilogue::Args e, int P, int Q, int splits)
+// Sum of the splits in their order, then the epilogue: a thread per 8
+// consecutive p, or per one where the result's layout allows no vectors.
+constexpr int kReduceThreads = 64;              // a wave a block: the few threads of a small result on many CUs
+
+template <bool VEC> __global__ __launch_bounds__(kReduceThreads) void reduce_splits(LinearEpilogue::Args e, int P, int Q, int splits)
 {
-    __shared__ float sums[kThreads][12];        // 16-byte aligned rows
-    const int64_t groups = e.ld_partial / 8, id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    const int64_t groups = VEC ? P / 8 : P, id = (int64_t)blockIdx.x * kReduceThreads + threadIdx.x;
     if (id >= groups * Q) return;
-    const int q = (int)(id / groups), p = (int)(id - q * groups) * 8;
-    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    const int q = (int)(id / groups), p = (int)(id - q * groups) * (VEC ? 8 : 1);
     const float *src = e.partial + (int64_t)q * e.ld_partial + p;
-    for (int s = 0; s < splits; s++) {
-        float w[8];
-        load8_vec(src + s * e.split_stride, w);
+    if constexpr (VEC) {
+        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 4
+        for (int s = 0; s < splits; s++) {
+            float w[8];
+            load8_vec(src + s * e.split_stride, w);
 #pragma unroll
-        for (int i = 0; i < 8; i++) v[i] += w[i];
+            for (int i = 0; i < 8; i++) v[i] += w[i];
+        }
+        LinearEpilogue::finish8(e, p, q, v);
+    } else {
+        float v = 0.0f;
+#pragma unroll 8
+        for (int s = 0; s < splits; s++) v += src[s * e.split_stride];
+        LinearEpilogue::finish1(e, p, q, v);
     }
-    store8_vec(sums[threadIdx.x], v);           // read back by this thread alone
-    LinearEpilogue::finish(e, p, q, min(8, P - p), sums[threadIdx.x]);
 }
 
 hipError_t run_product(Product &r, void *partial, hipStream_t s)
@@ -117,8 +126,11 @@ hipError_t run_product(Product &r, void *partial, hipStream_t s)
     else if (r.kind == GS_DTYPE_F16) err = launch_product_f16(r.a, r.e, r.plan, s);
     else err = launch_product_bf16(r.a, r.e, r.plan, s);
     if (err != hipSuccess || r.plan.splits == 1) return err;
-    const int64_t n = r.e.ld_partial / 8 * r.a.Q;
-    reduce_splits<<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, s>>>(r.e, r.a.P, r.a.Q, r.plan.splits);
+    const bool vec = r.e.vec && r.a.P % 8 == 0;
+    const int64_t n = (int64_t)(vec ? r.a.P / 8 : r.a.P) * r.a.Q;
+    const unsigned blocks = (unsigned)((n + kReduceThreads - 1) / kReduceThreads);
+    if (vec) reduce_splits<true><<<blocks, kReduceThreads, 0, s>>>(r.e, r.a.P, r.a.Q, r.plan.splits);
+    else reduce_splits<false><<<blocks, kReduceThreads, 0, s>>>(r.e, r.a.P, r.a.Q, r.plan.splits);
     return hipGetLastError();
 }
 
@@ -260,10 +272,14 @@ __global__ __launch_bounds__(kThreads) void dz_planes(DzArgs d)
     const int c = c0 + tx;                      // this thread's column of dz
     float acc = 0.0f;
     for (int64_t r = r0; r < r1; r += 64) {
-#pragma unroll 4
-        for (int i = ty; i < 64; i += 4)
-            tile[i][tx] = c0 + i < d.n && r + tx < r1 ? load_as_float(d.dy, d.dy_type, (int64_t)(c0 + i) * d.lddy + r + tx)
-                                                      : 0.0f;
+        float in[16];                           // all loads under way at once
+#pragma unroll
+        for (int k = 0; k < 16; k++) {
+            const int i = ty + 4 * k;
+            in[k] = c0 + i < d.n && r + tx < r1 ? load_as_float(d.dy, d.dy_type, (int64_t)(c0 + i) * d.lddy + r + tx) : 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < 16; k++) tile[ty + 4 * k][tx] = in[k];
         __syncthreads();
         for (int i = ty; i < 64 && r + i < r1; i += 4) {
             float v = tile[tx][i];
@@ -280,23 +296,6 @@ __global__ __launch_bounds__(kThreads) void dz_planes(DzArgs d)
     tile[ty][tx] = acc;
     __syncthreads();
     if (ty == 0 && c < d.n) d.part[(int64_t)blockIdx.y * d.n + c] = tile[0][tx] + tile[1][tx] + tile[2][tx] + tile[3][tx];
-}
-
-// db from the partial sums of `blocks` row blocks: 64 columns a block, four
-// lanes of rows.
-__global__ __launch_bounds__(kThreads) void sum_partials(const float *part, float *out, int n, int blocks, int accumulate)
-{
-    __shared__ float sums[4][64];
-    const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6, c = blockIdx.x * 64 + tx;
-    float s = 0.0f;
-    if (c < n)
-        for (int b = ty; b < blocks; b += 4) s += part[(int64_t)b * n + c];
-    sums[ty][tx] = s;
-    __syncthreads();
-    if (ty == 0 && c < n) {
-        s = sums[0][tx] + sums[1][tx] + sums[2][tx] + sums[3][tx];
-        out[c] = accumulate ? out[c] + s : s;
-    }
 }
 
 // Everything a backward call does, with its places in the workspace.
@@ -450,8 +449,7 @@ hipError_t run_bwd(const gs_linear &l, const gs_linear_grads &g, BwdPlan &b, cha
         }
         if ((err = hipGetLastError()) != hipSuccess) return err;
         if (g.db) {
-            sum_partials<<<(unsigned)((l.n + 63) / 64), kThreads, 0, s>>>(d.part, g.db, l.n, b.row_blocks, g.accumulate);
-            if ((err = hipGetLastError()) != hipSuccess) return err;
+            if ((err = launch_sum_rows(d.part, g.db, l.n, b.row_blocks, g.accumulate, s)) != hipSuccess) return err;
         }
     }
     if (g.dx) {

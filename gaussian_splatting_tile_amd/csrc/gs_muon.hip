@@ -3,7 +3,7 @@
 //
 // With r = min(rows, cols) and f = max, X is [r][f] (U^T when U is tall) and
 // an iteration is three products: A = X X^T, B = b A + c A A^T (A is
-// symmetric) and X' = a X + B X, 2 r^2 (2 f + r) multiply-adds.  X, A and B
+// symmetric) and X' = a X + B X.  A and B are formed on one side of the diagonal.  X, A and B
 // live in the workspace as bf16 limbs, padded with zeros to multiples of 32,
 // and every epilogue writes its result as limbs, so no product converts
 // anything: B X reads X by columns, and a tall U is turned round once at each
@@ -18,7 +18,7 @@ namespace gsi {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kNormBlocks = 64;                 // partial sums of squares per matrix
+constexpr int kMaxNormBlocks = 512;             // partial sums of squares per matrix
 
 bool aligned_to(const void *p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
 bool float_type(int t) { return t == GS_DTYPE_F32 || t == GS_DTYPE_F16 || t == GS_DTYPE_BF16; }
@@ -30,8 +30,26 @@ struct Update {
     float *momentum_out;
     int grad_type, nesterov;
     float beta;
+    int vec;                                    // size and alignments are multiples of 4 elements
     int64_t size;                               // rows * cols
 };
+
+__device__ __forceinline__ void load4(const void *p, int t, int64_t i, float v[4])
+{
+    if (t == GS_DTYPE_F32) {
+        const Vec<float, 4> w = *reinterpret_cast<const Vec<float, 4> *>(static_cast<const float *>(p) + i);
+#pragma unroll
+        for (int k = 0; k < 4; k++) v[k] = w.v[k];
+    } else if (t == GS_DTYPE_F16) {
+        const Vec<_Float16, 4> w = *reinterpret_cast<const Vec<_Float16, 4> *>(static_cast<const _Float16 *>(p) + i);
+#pragma unroll
+        for (int k = 0; k < 4; k++) v[k] = (float)w.v[k];
+    } else {
+        const Vec<__bf16, 4> w = *reinterpret_cast<const Vec<__bf16, 4> *>(static_cast<const __bf16 *>(p) + i);
+#pragma unroll
+        for (int k = 0; k < 4; k++) v[k] = (float)w.v[k];
+    }
+}
 
 // Element i of U once momentum_out is written.
 __device__ __forceinline__ float update_at(const Update &u, int64_t i)
@@ -41,38 +59,63 @@ __device__ __forceinline__ float update_at(const Update &u, int64_t i)
     return u.nesterov ? fmaf(u.beta, m, load_as_float(u.grad, u.grad_type, i)) : m;
 }
 
-// Momentum and the sums of squares of U, kNormBlocks workgroups per matrix.
+// Momentum and the sums of squares of U, one partial sum per workgroup.
 // The norm scales every singular value alike and the iterations' polynomial is
 // steep between its plateaus, so it is kept in fp64: an fp32 norm's error was
 // the largest part of the fp32 result's.
 __global__ __launch_bounds__(kThreads) void momentum_and_norm(Update u, double *part)
 {
+    // 4 consecutive elements a thread and pass where the matrices allow it
     __shared__ double lds[kThreads / 64];
-    const int64_t base = (int64_t)blockIdx.y * u.size;
+    const int64_t base = (int64_t)blockIdx.y * u.size, stride = (int64_t)gridDim.x * kThreads;
     double sq = 0.0;
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < u.size; i += (int64_t)kNormBlocks * kThreads) {
-        if (u.momentum)
-            u.momentum_out[base + i] = fmaf(u.beta, u.momentum[base + i], load_as_float(u.grad, u.grad_type, base + i));
-        const double x = update_at(u, base + i);
-        sq = fma(x, x, sq);
+    if (u.vec) {
+        for (int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4; i < u.size; i += stride * 4) {
+            float g[4];
+            load4(u.grad, u.grad_type, base + i, g);
+            if (u.momentum) {
+                float m[4];
+                load4(u.momentum, GS_DTYPE_F32, base + i, m);
+#pragma unroll
+                for (int k = 0; k < 4; k++) m[k] = fmaf(u.beta, m[k], g[k]);
+                *reinterpret_cast<Vec<float, 4> *>(u.momentum_out + base + i) = Vec<float, 4>{{m[0], m[1], m[2], m[3]}};
+#pragma unroll
+                for (int k = 0; k < 4; k++) g[k] = u.nesterov ? fmaf(u.beta, m[k], g[k]) : m[k];
+            }
+#pragma unroll
+            for (int k = 0; k < 4; k++) sq = fma((double)g[k], (double)g[k], sq);
+        }
+    } else {
+        for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < u.size; i += stride) {
+            if (u.momentum)
+                u.momentum_out[base + i] = fmaf(u.beta, u.momentum[base + i], load_as_float(u.grad, u.grad_type, base + i));
+            const double x = update_at(u, base + i);
+            sq = fma(x, x, sq);
+        }
     }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) sq += __shfl_xor(sq, o);
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = sq;
     __syncthreads();
-    if (threadIdx.x == 0) part[blockIdx.y * kNormBlocks + blockIdx.x] = lds[0] + lds[1] + lds[2] + lds[3];
+    if (threadIdx.x == 0) part[blockIdx.y * gridDim.x + blockIdx.x] = lds[0] + lds[1] + lds[2] + lds[3];
 }
 
 // X = U / (|U| + eps) as limbs [r_pad][f_pad], zeros in the padding; tiles of
 // 32 x 32 turned round in LDS when U is tall.
 template <int NL>
-__global__ __launch_bounds__(kThreads) void normalised_limbs(Update u, const double *part, float eps, int rows, int cols, int tall,
+__global__ __launch_bounds__(kThreads) void normalised_limbs(Update u, const double *part, int parts, float eps, int rows, int cols, int tall,
                                                              uint16_t *x, int64_t ldx, int64_t plane, int64_t batch)
 {
     __shared__ float tile[32][33];
+    __shared__ double lds[kThreads / 64];
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     double sq = 0.0;
-    for (int i = 0; i < kNormBlocks; i++) sq += part[blockIdx.z * kNormBlocks + i];
+    for (int i = threadIdx.x; i < parts; i += kThreads) sq += part[blockIdx.z * parts + i];
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) sq += __shfl_xor(sq, o);
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = sq;
+    __syncthreads();
+    sq = lds[0] + lds[1] + lds[2] + lds[3];
     const double inv = 1.0 / (sqrt(sq) + (double)eps);
     const int64_t base = (int64_t)blockIdx.z * u.size;
     const int f0 = blockIdx.x * 32, r0 = blockIdx.y * 32;
@@ -98,6 +141,9 @@ __global__ __launch_bounds__(kThreads) void normalised_limbs(Update u, const dou
 // result.
 template <int NL> struct NsEpilogue {
     struct Args {
+        float *partial;                         // [batch][splits][q][ld_partial], or NULL: one split
+        int64_t ld_partial, split_stride;
+        int splits;
         float alpha, beta;
         const uint16_t *c;                      // limbs at q * ld + p, or NULL
         uint16_t *o;
@@ -109,38 +155,43 @@ template <int NL> struct NsEpilogue {
         float decay, rate;                      // weight * decay - rate * v
     };
 
-    __device__ static __forceinline__ void store(const Args &e, int p, int q, int, const float *s, int batch, int)
+    __device__ static __forceinline__ bool vec(const Args &) { return true; }   // everything is padded
+
+    __device__ static __forceinline__ void write_limbs(const Args &e, int p, int q, const float v[8], int batch)
     {
-        float v[8];
-        load8_vec(s, v);
+        Vec<uint16_t, 8> h[NL];
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            uint16_t limb[NL];
+            split_limbs<NL>(v[i], limb);
+#pragma unroll
+            for (int l = 0; l < NL; l++) h[l].v[i] = limb[l];
+        }
+        uint16_t *o = e.o + batch * e.batch_o + (int64_t)q * e.ldo + p;
+#pragma unroll
+        for (int l = 0; l < NL; l++) *reinterpret_cast<Vec<uint16_t, 8> *>(o + l * e.plane_o) = h[l];
+    }
+
+    // v = alpha sum + beta C, in place
+    __device__ static __forceinline__ void combine(const Args &e, int p, int q, float v[8], int batch)
+    {
 #pragma unroll
         for (int i = 0; i < 8; i++) v[i] *= e.alpha;
-        if (e.c) {
-            const uint16_t *c = e.c + batch * e.batch_c + (int64_t)q * e.ldc + p;
-            float w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (!e.c) return;
+        const uint16_t *c = e.c + batch * e.batch_c + (int64_t)q * e.ldc + p;
+        float w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-            for (int l = NL - 1; l >= 0; l--) {
-                const Vec<uint16_t, 8> h = *reinterpret_cast<const Vec<uint16_t, 8> *>(c + l * e.plane_c);
+        for (int l = NL - 1; l >= 0; l--) {
+            const Vec<uint16_t, 8> h = *reinterpret_cast<const Vec<uint16_t, 8> *>(c + l * e.plane_c);
 #pragma unroll
-                for (int i = 0; i < 8; i++) w[i] += limb_value(h.v[i]);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; i++) v[i] = fmaf(e.beta, w[i], v[i]);
+            for (int i = 0; i < 8; i++) w[i] += limb_value(h.v[i]);
         }
-        if (!e.out) {
-            Vec<uint16_t, 8> h[NL];
 #pragma unroll
-            for (int i = 0; i < 8; i++) {
-                uint16_t limb[NL];
-                split_limbs<NL>(v[i], limb);
-#pragma unroll
-                for (int l = 0; l < NL; l++) h[l].v[i] = limb[l];
-            }
-            uint16_t *o = e.o + batch * e.batch_o + (int64_t)q * e.ldo + p;
-#pragma unroll
-            for (int l = 0; l < NL; l++) *reinterpret_cast<Vec<uint16_t, 8> *>(o + l * e.plane_o) = h[l];
-            return;
-        }
+        for (int i = 0; i < 8; i++) v[i] = fmaf(e.beta, w[i], v[i]);
+    }
+
+    __device__ static __forceinline__ void write_result(const Args &e, int p, int q, const float v[8], int batch)
+    {
         const int64_t base = (int64_t)batch * e.rows * e.cols;
 #pragma unroll
         for (int i = 0; i < 8; i++) {
@@ -152,13 +203,96 @@ template <int NL> struct NsEpilogue {
             store_from_float(e.out, e.out_type, at, x);
         }
     }
+
+    __device__ static __forceinline__ void store8(const Args &e, int p, int q, float v[8], int batch, int split, bool mirror)
+    {
+        if (e.partial) {
+            store8_vec(e.partial + ((int64_t)batch * e.splits + split) * e.split_stride + (int64_t)q * e.ld_partial + p, v);
+            return;
+        }
+        combine(e, p, q, v, batch);
+        if (e.out) {
+            write_result(e, p, q, v, batch);
+            return;
+        }
+        write_limbs(e, p, q, v, batch);
+        if (mirror) {
+            // the transposed tile, 2 bytes at a time: a few per cent of a
+            // triangle's time, where forming it would double it
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                uint16_t limb[NL];
+                split_limbs<NL>(v[i], limb);
+#pragma unroll
+                for (int l = 0; l < NL; l++) e.o[batch * e.batch_o + l * e.plane_o + (int64_t)(p + i) * e.ldo + q] = limb[l];
+            }
+        }
+    }
+    __device__ static __forceinline__ void store1(const Args &, int, int, float, int, int) {}  // never: 8 | P
 };
+
+// Sum of the splits of k in their order and the epilogue, a 64 x 64 tile a
+// workgroup; a symmetric result is summed on one side of the diagonal and
+// turned round in LDS for the other.
+template <int NL>
+__global__ __launch_bounds__(kThreads) void reduce_splits(typename NsEpilogue<NL>::Args e, int P, int Q, int symmetric)
+{
+    using E = NsEpilogue<NL>;
+    __shared__ float tile[64][65];
+    int tp, tq;
+    const int tiles_p = (P + 63) / 64;
+    if (symmetric) {
+        gemm::triangle_of(blockIdx.x, tp, tq);
+    } else {
+        tp = blockIdx.x % tiles_p;
+        tq = blockIdx.x / tiles_p;
+    }
+    const float *part = e.partial + (int64_t)blockIdx.y * e.splits * e.split_stride;
+    const int pl = threadIdx.x % 8 * 8;
+#pragma unroll
+    for (int h = 0; h < 64; h += 32) {
+        const int ql = h + threadIdx.x / 8, p = tp * 64 + pl, q = tq * 64 + ql;
+        if (p >= P || q >= Q) continue;
+        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 4
+        for (int s = 0; s < e.splits; s++) {
+            float w[8];
+            load8_vec(part + s * e.split_stride + (int64_t)q * e.ld_partial + p, w);
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[i] += w[i];
+        }
+        E::combine(e, p, q, v, blockIdx.y);
+        if (e.out) E::write_result(e, p, q, v, blockIdx.y);
+        else E::write_limbs(e, p, q, v, blockIdx.y);
+#pragma unroll
+        for (int i = 0; i < 8; i++) tile[ql][pl + i] = v[i];
+    }
+    if (!symmetric || tp == tq) return;
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 64; h += 32) {
+        const int ql = h + threadIdx.x / 8, p = tq * 64 + pl, q = tp * 64 + ql;     // the mirrored tile's
+        if (p >= P || q >= Q) continue;
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[i] = tile[pl + i][ql];
+        E::write_limbs(e, p, q, v, blockIdx.y);
+    }
+}
+
+// Tile and splits of one product of a batch.
+struct NsProduct {
+    int tile;                                   // 128 or 64
+    int splits;
+};
+NsProduct choose(int P, int Q, int K, int batch, bool symmetric, int nl);
 
 struct MuonPlan {
     int r, f;                                   // padded
     int nl;
     int64_t x_size, a_size;                     // elements of one limb plane
-    size_t part_at, x_at[2], a_at, b_at, bytes;
+    int norm_blocks;
+    size_t part_at, x_at[2], a_at, b_at, split_at, bytes;
 };
 
 MuonPlan plan_muon(const gs_muon &m)
@@ -176,23 +310,72 @@ MuonPlan plan_muon(const gs_muon &m)
         at += round256(bytes);
         return here;
     };
-    p.part_at = take((size_t)m.batch * kNormBlocks * sizeof(double));
+    // a workgroup per 4096 elements of a matrix
+    const int64_t blocks = ((int64_t)m.rows * m.cols + 4095) / 4096;
+    p.norm_blocks = (int)(blocks < kMaxNormBlocks ? blocks : kMaxNormBlocks);
+    p.part_at = take((size_t)m.batch * p.norm_blocks * sizeof(double));
     const size_t xb = (size_t)m.batch * p.nl * p.x_size * 2, ab = (size_t)m.batch * p.nl * p.a_size * 2;
     p.x_at[0] = take(xb);
     p.x_at[1] = take(xb);
     p.a_at = take(ab);
     p.b_at = take(ab);
+    // sums of split products, one product at a time
+    const NsProduct g[3] = {choose(p.r, p.r, p.f, m.batch, true, p.nl), choose(p.r, p.r, p.r, m.batch, true, p.nl),
+                            choose(p.f, p.r, p.r, m.batch, false, p.nl)};
+    size_t most = 0;
+    for (int i = 0; i < 3; i++) {
+        const size_t b = g[i].splits > 1 ? (size_t)m.batch * g[i].splits * (i == 2 ? p.x_size : p.a_size) * 4 : 0;
+        most = b > most ? b : most;
+    }
+    p.split_at = take(most);
     p.bytes = at;
     return p;
 }
 
+// Estimated time in microseconds.  A 128 tile of 8 waves takes about 0.42 us
+// per 32 k with three products and twice that with six, a 64 tile 0.19 alone on
+// its CU and 0.10 (0.2) with others beside it; a split costs a launch and its
+// sums' way to memory and back.
+NsProduct choose(int P, int Q, int K, int batch, bool symmetric, int nl)
+{
+    NsProduct best{64, 1};
+    double least = 1e30;
+    const int nt = (K + 31) / 32;
+    for (int tile = 128; tile >= 64; tile /= 2) {
+        const int tp = (P + tile - 1) / tile, tq = (Q + tile - 1) / tile;
+        const double tiles = (double)(symmetric ? tp * (tp + 1) / 2 : tp * tq) * batch;
+        for (int want = 1; want <= 8 && want <= nt; want++) {
+            const int per = (nt + want - 1) / want, splits = (nt + per - 1) / per;
+            const double rounds = ceil(tiles * splits / 256.0);
+            const double step = nl == 3 ? (tile == 128 ? 0.84 : rounds > 1 ? 0.2 : 0.26) : tile == 128 ? 0.42 : rounds > 1 ? 0.1 : 0.19;
+            double us = rounds * per * step + 2.0;
+            if (splits > 1) us += 5.0 + tiles * splits * tile * tile * 8.0 / 6e6;
+            if (us < least * 0.97) {
+                least = us;
+                best.tile = tile;
+                best.splits = splits;
+            }
+        }
+    }
+    return best;
+}
+
 template <int NL, bool PT>
-hipError_t launch_product(const gemm::Args &a, const typename NsEpilogue<NL>::Args &e, int batch, hipStream_t s)
+hipError_t launch_product(gemm::Args a, typename NsEpilogue<NL>::Args e, float *partial, int batch, bool symmetric, hipStream_t s)
 {
     using E = NsEpilogue<NL>;
-    const int64_t blocks = (int64_t)((a.P + 127) / 128) * ((a.Q + 127) / 128) * batch;
-    if (blocks >= 192) return gemm::launch<gemm::kBF16, NL, 32, 128, 128, 2, 2, PT, false, false, E>(a, e, 1, batch, s);
-    return gemm::launch<gemm::kBF16, NL, 32, 64, 64, 2, 2, PT, false, false, E>(a, e, 1, batch, s);
+    const NsProduct c = choose(a.P, a.Q, a.K, batch, symmetric, NL);
+    a.symmetric = symmetric;
+    e.splits = c.splits;
+    e.partial = c.splits > 1 ? partial : nullptr;
+    e.ld_partial = a.P;
+    e.split_stride = (int64_t)a.P * a.Q;
+    hipError_t err = c.tile == 128 ? gemm::launch<gemm::kBF16, NL, NL == 3 ? 2 : 3, 32, 128, 128, 2, 4, PT, false, false, E>(a, e, c.splits, batch, s)
+                                   : gemm::launch<gemm::kBF16, NL, 3, 32, 64, 64, 2, 2, PT, false, false, E>(a, e, c.splits, batch, s);
+    if (err != hipSuccess || c.splits == 1) return err;
+    const int tp = (a.P + 63) / 64, tq = (a.Q + 63) / 64;
+    reduce_splits<NL><<<dim3((unsigned)(symmetric ? tp * (tp + 1) / 2 : tp * tq), (unsigned)batch), kThreads, 0, s>>>(e, a.P, a.Q, symmetric);
+    return hipGetLastError();
 }
 
 template <int NL> hipError_t run_muon(const gs_muon &m, bool step, char *ws, hipStream_t s)
@@ -201,6 +384,7 @@ template <int NL> hipError_t run_muon(const gs_muon &m, bool step, char *ws, hip
     const bool tall = m.rows > m.cols;
     double *part = reinterpret_cast<double *>(ws + p.part_at);
     uint16_t *x[2] = {reinterpret_cast<uint16_t *>(ws + p.x_at[0]), reinterpret_cast<uint16_t *>(ws + p.x_at[1])};
+    float *split = reinterpret_cast<float *>(ws + p.split_at);
     uint16_t *A = reinterpret_cast<uint16_t *>(ws + p.a_at), *B = reinterpret_cast<uint16_t *>(ws + p.b_at);
     Update u;
     u.grad = m.grad;
@@ -210,11 +394,13 @@ template <int NL> hipError_t run_muon(const gs_muon &m, bool step, char *ws, hip
     u.nesterov = m.nesterov;
     u.beta = m.beta;
     u.size = (int64_t)m.rows * m.cols;
-    momentum_and_norm<<<dim3(kNormBlocks, (unsigned)m.batch), kThreads, 0, s>>>(u, part);
+    const int es = dtype_bytes(m.grad_dtype) * 4;
+    u.vec = u.size % 4 == 0 && aligned_to(m.grad, es) && (!step || (aligned_to(m.momentum, 16) && aligned_to(m.momentum_out, 16)));
+    momentum_and_norm<<<dim3((unsigned)p.norm_blocks, (unsigned)m.batch), kThreads, 0, s>>>(u, part);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
     normalised_limbs<NL><<<dim3((unsigned)(p.f / 32), (unsigned)(p.r / 32), (unsigned)m.batch), kThreads, 0, s>>>(
-        u, part, m.eps, m.rows, m.cols, tall, x[0], p.f, p.x_size, NL * p.x_size);
+        u, part, p.norm_blocks, m.eps, m.rows, m.cols, tall, x[0], p.f, p.x_size, NL * p.x_size);
     if ((err = hipGetLastError()) != hipSuccess) return err;
 
     // products of limb arrays: [r][f] for X, [r][r] for A and B
@@ -243,7 +429,7 @@ template <int NL> hipError_t run_muon(const gs_muon &m, bool step, char *ws, hip
         e.ldo = p.r;
         e.plane_o = p.a_size;
         e.batch_o = NL * p.a_size;
-        if ((err = launch_product<NL, false>(args(X, p.f, p.x_size, X, p.f, p.x_size, p.r, p.f), e, m.batch, s)) != hipSuccess) return err;
+        if ((err = launch_product<NL, false>(args(X, p.f, p.x_size, X, p.f, p.x_size, p.r, p.f), e, split, m.batch, true, s)) != hipSuccess) return err;
         e.alpha = m.c;
         e.beta = m.b;
         e.c = A;
@@ -251,7 +437,7 @@ template <int NL> hipError_t run_muon(const gs_muon &m, bool step, char *ws, hip
         e.plane_c = p.a_size;
         e.batch_c = NL * p.a_size;
         e.o = B;
-        if ((err = launch_product<NL, false>(args(A, p.r, p.a_size, A, p.r, p.a_size, p.r, p.r), e, m.batch, s)) != hipSuccess) return err;
+        if ((err = launch_product<NL, false>(args(A, p.r, p.a_size, A, p.r, p.a_size, p.r, p.r), e, split, m.batch, true, s)) != hipSuccess) return err;
         e.alpha = 1.0f;
         e.beta = m.a;
         e.c = X;
@@ -272,7 +458,7 @@ template <int NL> hipError_t run_muon(const gs_muon &m, bool step, char *ws, hip
             e.decay = 1.0f - m.lr * m.weight_decay;
             e.rate = m.lr * m.scale;
         }
-        if ((err = launch_product<NL, true>(args(X, p.f, p.x_size, B, p.r, p.a_size, p.f, p.r), e, m.batch, s)) != hipSuccess) return err;
+        if ((err = launch_product<NL, true>(args(X, p.f, p.x_size, B, p.r, p.a_size, p.f, p.r), e, split, m.batch, false, s)) != hipSuccess) return err;
     }
     return hipSuccess;
 }

@@ -7,7 +7,7 @@
 // (16 bytes of a 16-bit type) per lane and access: rows of up to 2048 by one
 // wave (4 rows per workgroup, no barrier), up to 8192 by a workgroup, longer
 // ones in two passes.  An 8-bit block of 32 values is 4 neighbouring lanes.
-#include "gs_numeric.h"
+#include "gs_linear.h"
 
 #include <math.h>
 
@@ -353,19 +353,26 @@ template <typename T> __global__ __launch_bounds__(kThreads) void dgamma_long(Gr
         if (j < valid) a.part[(int64_t)blockIdx.y * a.n + c + j] = dg[j];
 }
 
-__global__ __launch_bounds__(kThreads) void sum_dgamma(const float *part, float *out, int n, int blocks, int accumulate)
+// Column sums of partial rows: 16 columns (64 bytes) a block, 64 lanes of rows
+// with 8 loads under way each, then a tree over the lanes.
+constexpr int kSumThreads = 1024;
+
+__global__ __launch_bounds__(kSumThreads) void sum_rows(const float *part, float *out, int n, int rows, int accumulate)
 {
-    __shared__ float sums[4][64];
-    const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6, c = blockIdx.x * 64 + tx;
+    __shared__ float sums[64][17];
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, c = blockIdx.x * 16 + tx;
     float s = 0.0f;
-    if (c < n)
-        for (int b = ty; b < blocks; b += 4) s += part[(int64_t)b * n + c];
-    sums[ty][tx] = s;
-    __syncthreads();
-    if (ty == 0 && c < n) {
-        s = sums[0][tx] + sums[1][tx] + sums[2][tx] + sums[3][tx];
-        out[c] = accumulate ? out[c] + s : s;
+    if (c < n) {
+#pragma unroll 8
+        for (int r = ty; r < rows; r += 64) s += part[(int64_t)r * n + c];
     }
+    sums[ty][tx] = s;
+#pragma unroll
+    for (int h = 32; h > 0; h >>= 1) {
+        __syncthreads();
+        if (ty < h) sums[ty][tx] += sums[ty + h][tx];
+    }
+    if (ty == 0 && c < n) out[c] = accumulate ? out[c] + sums[0][tx] : sums[0][tx];
 }
 
 // Workgroups of the backward, each with one partial row of dgamma.
@@ -373,7 +380,7 @@ int grad_blocks(int64_t m, int n)
 {
     if (n > kMaxRegRow) return (int)(m < 64 ? m : 64);
     const int64_t rows = n <= 2048 ? 4 : 1, want = (m + rows - 1) / rows;
-    return (int)(want < 1024 ? want : 1024);
+    return (int)(want < 512 ? want : 512);
 }
 
 template <typename T> hipError_t launch_grad(const GradArgs &a, hipStream_t s)
@@ -434,6 +441,13 @@ __global__ __launch_bounds__(kThreads) void zero_floats(float *p, int n)
 }
 
 }  // namespace
+
+hipError_t launch_sum_rows(const float *part, float *out, int n, int rows, int accumulate, hipStream_t s)
+{
+    sum_rows<<<(unsigned)((n + 15) / 16), kSumThreads, 0, s>>>(part, out, n, rows, accumulate);
+    return hipGetLastError();
+}
+
 }  // namespace gsi
 
 using namespace gsi;
@@ -542,8 +556,7 @@ gs_status gs_rms_norm_bwd(const gs_rms_norm_grads *p, void *workspace, size_t wo
     hipError_t e = p->dtype == GS_DTYPE_F32 ? launch_grad<float>(a, s)
                    : p->dtype == GS_DTYPE_F16 ? launch_grad<_Float16>(a, s) : launch_grad<__bf16>(a, s);
     if (e == hipSuccess && p->dgamma) {
-        sum_dgamma<<<(unsigned)((p->n + 63) / 64), kThreads, 0, s>>>(a.part, p->dgamma, p->n, grad_blocks(p->m, p->n), p->accumulate);
-        e = hipGetLastError();
+        e = launch_sum_rows(a.part, p->dgamma, p->n, grad_blocks(p->m, p->n), p->accumulate, s);
     }
     return from_hip(e);
 }

@@ -106,19 +106,18 @@ __device__ __forceinline__ float e8m0_value(uint32_t s)
 }
 
 // ---- activations -------------------------------------------------------------
-// Standard normal distribution function.  For results rounded to 16 bits: the
-// five-term rational approximation of Abramowitz and Stegun 7.1.26 (absolute
-// error 7.5e-8), one reciprocal and one exponential; the library's erf takes
-// about three times as long and made up most of the epilogue of a GELU layer.
-template <bool EXACT> __device__ __forceinline__ float normal_cdf(float z)
+// Phi(-|z|) of the standard normal distribution, for results rounded to 16
+// bits: the five-term approximation of Abramowitz and Stegun 7.1.26 (absolute
+// error 7.5e-8), one reciprocal and one exponential, e = exp(-z^2 / 2); the
+// library's erf takes about three times as long and made up most of the
+// epilogue of a GELU layer.
+__device__ __forceinline__ float normal_tail(float z, float &e)
 {
-    if constexpr (EXACT) return 0.5f * erfcf(-0.70710678118654752f * z);
-    const float x = fabsf(z) * 0.70710678118654752f;
-    const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.0f));
-    const float p = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
-                             0.254829592f);
-    const float h = 0.5f * p * __builtin_amdgcn_exp2f(x * x * -1.4426950408889634f);
-    return z >= 0.0f ? 1.0f - h : h;
+    const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(z), 0.3275911f * 0.70710678118654752f, 1.0f));
+    const float p = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 0.5f * 1.061405429f, -0.5f * 1.453152027f), 0.5f * 1.421413741f),
+                                     -0.5f * 0.284496736f), 0.5f * 0.254829592f);
+    e = __builtin_amdgcn_exp2f(z * z * -0.72134752044448170f);
+    return p * e;
 }
 template <bool EXACT> __device__ __forceinline__ float logistic(float z)
 {
@@ -129,7 +128,14 @@ template <bool EXACT> __device__ __forceinline__ float activate(float z, int act
 {
     if (act == GS_ACT_RELU) return z < 0.0f ? 0.0f : z;               // a NaN stays one
     if (act == GS_ACT_SILU) return z * logistic<EXACT>(z);
-    if (act == GS_ACT_GELU) return z * normal_cdf<EXACT>(z);
+    if (act == GS_ACT_GELU) {
+        if constexpr (EXACT) return z * (0.5f * erfcf(-0.70710678118654752f * z));
+        // z Phi(z) = max(z, 0) - |z| Phi(-|z|); the bound keeps an infinite z from
+        // meeting the tail's 0
+        float e;
+        const float h = normal_tail(z, e);
+        return fmaf(-fminf(fabsf(z), 64.0f), h, fmaxf(z, 0.0f));
+    }
     return z;
 }
 template <bool EXACT> __device__ __forceinline__ float activate_slope(float z, int act)
@@ -140,8 +146,10 @@ template <bool EXACT> __device__ __forceinline__ float activate_slope(float z, i
         return s * fmaf(z, 1.0f - s, 1.0f);
     }
     if (act == GS_ACT_GELU) {
-        const float e = EXACT ? expf(-0.5f * z * z) : __builtin_amdgcn_exp2f(z * z * -0.72134752044448170f);
-        return normal_cdf<EXACT>(z) + z * 0.39894228040143268f * e;
+        if constexpr (EXACT) return 0.5f * erfcf(-0.70710678118654752f * z) + z * 0.39894228040143268f * expf(-0.5f * z * z);
+        float e;
+        const float h = normal_tail(z, e);
+        return fmaf(z * 0.39894228040143268f, e, z >= 0.0f ? 1.0f - h : h);
     }
     return 1.0f;
 }

@@ -8,8 +8,8 @@ template <bool PT, bool QT>
 static hipError_t launch_tiles(const gemm::Args &a, const LinearEpilogue::Args &e, const ProductPlan &plan, hipStream_t s)
 {
     using E = LinearEpilogue;
-    if (plan.tile == 1) return gemm::launch<gemm::kBF16, 3, 32, 128, 128, 2, 2, PT, QT, true, E>(a, e, plan.splits, 1, s);
-    return gemm::launch<gemm::kBF16, 3, 32, 64, 64, 2, 2, PT, QT, true, E>(a, e, plan.splits, 1, s);
+    if (plan.tile == 1) return gemm::launch<gemm::kBF16, 3, 2, 32, 128, 128, 2, 2, PT, QT, true, E>(a, e, plan.splits, 1, s);
+    return gemm::launch<gemm::kBF16, 3, 2, 32, 64, 64, 2, 2, PT, QT, true, E>(a, e, plan.splits, 1, s);
 }
 
 hipError_t launch_product_f32(const gemm::Args &a, const LinearEpilogue::Args &e, const ProductPlan &plan, hipStream_t s)
