@@ -35,7 +35,8 @@ struct LinearEpilogue {
         const int64_t at = (int64_t)q * e.ldy + p;
         if (e.bias) v += e.bias[e.bias_on_q ? q : p];
         if (e.z) store_from_float(e.z, e.z_type, (int64_t)q * e.z_q + (int64_t)p * e.z_p, v);
-        v = e.exact ? activate<true>(v, e.act) : activate<false>(v, e.act);
+        if (e.exact) activate_all<1, true>(&v, e.act);
+        else activate_all<1, false>(&v, e.act);
         if (e.residual) v += load_as_float(e.residual, e.y_type, (int64_t)q * e.ldr + p);
         if (e.accumulate) v += load_as_float(e.y, e.y_type, at);
         store_from_float(e.y, e.y_type, at, v);
@@ -65,15 +66,8 @@ struct LinearEpilogue {
                 for (int i = 0; i < 8; i++) store_from_float(e.z, e.z_type, (int64_t)q * e.z_q + (int64_t)(p + i) * e.z_p, v[i]);
             }
         }
-        if (e.act != GS_ACT_NONE) {
-            if (e.exact) {
-#pragma unroll
-                for (int i = 0; i < 8; i++) v[i] = activate<true>(v[i], e.act);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; i++) v[i] = activate<false>(v[i], e.act);
-            }
-        }
+        if (e.exact) activate_all<8, true>(v, e.act);
+        else activate_all<8, false>(v, e.act);
         float r[8];
         if (e.residual) {
             load8_vec(e.residual, e.y_type, (int64_t)q * e.ldr + p, r);
@@ -111,7 +105,7 @@ struct LinearEpilogue {
 struct ProductPlan {
     bool pt, qt;
     bool staged;
-    int tile;                           // 0: 256 x 256, 1: 128 x 128, 2: 64 x 64 (staged: 1 and 2)
+    int tile;                           // 0: 256 x 256, 1: 128 x 128, 2: 64 x 64 (staged: 2; fp32: 1 and 2)
     int splits;                         // of k, each with at least one tile of k
 };
 

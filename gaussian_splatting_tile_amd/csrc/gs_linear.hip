@@ -7,6 +7,15 @@
 // Backward: dz = dy act'(z) and the partial sums of db in one pass over dy and
 // z (skipped when dz is dy as it stands), then dx[m][k] = dz w and
 // dw[n][k] = dz^T x, whose operands are read by columns where k is theirs.
+//
+// Operands that cannot be loaded into LDS as they stand (fp32, odd sizes,
+// strides or alignments, 8-bit values for an fp32 result) go one of two ways.
+// A result of at most 64 columns or rows reads its long operand once, so the
+// product converts while loading ("staged").  A wider one would convert each
+// element once per tile across it; there one pass first writes both operands
+// as padded 16-bit planes (three bf16 limbs of fp32).  At 692x4032x384 in fp32
+// the backward took 111 us staged and XX packed; at 18846x64x832 the forward
+// takes YY staged and ZZ packed.
 #include <string.h>
 
 #include "gs_linear.h"
@@ -39,15 +48,17 @@ double product_cost(const TileRate &t, int64_t P, int64_t Q, int64_t K, int spli
     return us;
 }
 
-ProductPlan make_plan(int64_t P, int64_t Q, int64_t K, bool pt, bool qt, bool staged, int step_k, float work)
+ProductPlan make_plan(int64_t P, int64_t Q, int64_t K, bool pt, bool qt, bool staged, bool f32, int step_k, float work)
 {
     static const TileRate direct[3] = {{256, 1, 4.6f}, {128, 2, 4.1f}, {64, 3, 2.4f}};
-    static const TileRate staged_[3] = {{256, 1, 0.0f}, {128, 1, 2.0f}, {64, 3, 1.2f}};
+    static const TileRate limbs[3] = {{256, 1, 0.0f}, {128, 1, 4.1f}, {64, 2, 3.0f}};
+    static const TileRate staged_[3] = {{256, 1, 0.0f}, {128, 1, 0.0f}, {64, 3, 1.2f}};
     ProductPlan best{pt, qt, staged, 2, 1};
     double least = 1e30;
     const int64_t nt = (K + step_k - 1) / step_k;
-    for (int tile = staged ? 1 : 0; tile < 3; tile++) {
-        const TileRate &t = staged ? staged_[tile] : direct[tile];
+    // three limbs of a 256 tile exceed the LDS
+    for (int tile = staged ? 2 : f32 ? 1 : 0; tile < 3; tile++) {
+        const TileRate &t = staged ? staged_[tile] : f32 ? limbs[tile] : direct[tile];
         for (int64_t want = 1; want <= 16 && want <= nt; want = want < 4 ? want + 1 : want * 2) {
             const int64_t per = (nt + want - 1) / want;
             const int splits = (int)((nt + per - 1) / per);
@@ -62,31 +73,144 @@ ProductPlan make_plan(int64_t P, int64_t Q, int64_t K, bool pt, bool qt, bool st
     return best;
 }
 
-// One product with its plan; everything but the workspace address.
+bool vec_ok(const void *p, int type, int64_t ld) { return al16(p) && ld % (16 / dtype_bytes(type)) == 0; }
+
+// ---- operands as padded 16-bit planes -----------------------------------------
+struct PackJob {
+    const void *src;                    // [rows][cols] of `type`
+    const uint8_t *scales;              // MXFP8
+    int64_t ld, ld_scales, rows;
+    int type, cols, vec;
+    uint16_t *dst;                      // [limbs][rows][ld_dst], zeros past cols
+    int64_t ld_dst;
+    int limbs, half;                    // 3: bf16 limbs of fp32; 1: bf16, or fp16 if half
+    int64_t first;                      // the job's first thread
+};
+struct PackJobs {
+    PackJob job[2];
+    int count;
+    int64_t threads;
+};
+
+__device__ __forceinline__ void store_planes(uint16_t *dst, int64_t plane, int64_t at, int limbs, int half, const float v[8])
+{
+    if (limbs == 1) {
+        Vec<uint16_t, 8> w;
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            w.v[i] = half ? __builtin_bit_cast(uint16_t, (_Float16)v[i]) : __builtin_bit_cast(uint16_t, (__bf16)v[i]);
+        *reinterpret_cast<Vec<uint16_t, 8> *>(dst + at) = w;
+        return;
+    }
+    Vec<uint16_t, 8> w[3];
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        uint16_t limb[3];
+        split_limbs<3>(v[i], limb);
+#pragma unroll
+        for (int l = 0; l < 3; l++) w[l].v[i] = limb[l];
+    }
+#pragma unroll
+    for (int l = 0; l < 3; l++) *reinterpret_cast<Vec<uint16_t, 8> *>(dst + l * plane + at) = w[l];
+}
+
+// A thread per 8 columns of a row.
+__global__ __launch_bounds__(kThreads) void pack_operands(PackJobs jobs)
+{
+    const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (id >= jobs.threads) return;
+    const PackJob j = jobs.count > 1 && id >= jobs.job[1].first ? jobs.job[1] : jobs.job[0];
+    const int64_t groups = j.ld_dst / 8, at = id - j.first, r = at / groups;
+    const int c = (int)(at - r * groups) * 8, valid = min(8, j.cols - c);
+    float v[8];
+    if (j.type == GS_DTYPE_MXFP8) {
+        const uint8_t *b = static_cast<const uint8_t *>(j.src) + r * j.ld + c;
+        const float f = e8m0_value(j.scales[r * j.ld_scales + (c >> 5)]);       // cols is a multiple of 32
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[i] = e4m3_value(b[i]) * f;
+    } else {
+        load8(j.src, j.type, r * j.ld + c, valid, j.vec, v);
+    }
+    store_planes(j.dst, j.rows * j.ld_dst, r * j.ld_dst + c, j.limbs, j.half, v);
+}
+
+void add_job(PackJobs &jobs, const void *src, int type, const uint8_t *scales, int64_t ld, int64_t ld_scales, int64_t rows, int cols,
+             void *dst)
+{
+    PackJob &j = jobs.job[jobs.count++];
+    j.src = src;
+    j.scales = scales;
+    j.ld = ld;
+    j.ld_scales = ld_scales;
+    j.rows = rows;
+    j.type = type;
+    j.cols = cols;
+    j.vec = type != GS_DTYPE_MXFP8 && vec_ok(src, type, ld);
+    j.dst = static_cast<uint16_t *>(dst);
+    j.ld_dst = ((int64_t)cols + 7) & ~(int64_t)7;
+    j.limbs = type == GS_DTYPE_F32 ? 3 : 1;
+    j.half = type == GS_DTYPE_F16;
+    j.first = jobs.threads;
+    jobs.threads += rows * (j.ld_dst / 8);
+}
+
+hipError_t run_jobs(const PackJobs &jobs, hipStream_t s)
+{
+    if (jobs.count == 0) return hipSuccess;
+    pack_operands<<<(unsigned)((jobs.threads + kThreads - 1) / kThreads), kThreads, 0, s>>>(jobs);
+    return hipGetLastError();
+}
+
+size_t packed_bytes(int type, int64_t rows, int64_t cols)
+{
+    return round256((size_t)(type == GS_DTYPE_F32 ? 3 : 1) * rows * ((cols + 7) & ~(int64_t)7) * 2);
+}
+
+// One product with its plan; everything but the workspace addresses.
+enum Way { kDirect, kPacked, kStaged };
+
 struct Product {
     gemm::Args a;
     LinearEpilogue::Args e;
     ProductPlan plan;
-    int kind;                           // gs_dtype of the operands
+    int type;                           // gs_dtype of the operands as given
+    Way way;
+    bool pack_p, pack_q;
     size_t partial_bytes;
 };
 
-bool vec_ok(const void *p, int type, int64_t ld) { return al16(p) && ld % (16 / dtype_bytes(type)) == 0; }
-
-void finish_plan(Product &r, bool direct)
+// The way of a product whose operands can (p_ok, q_ok) or cannot be loaded
+// directly, then its tile and splits.
+void finish_plan(Product &r, bool p_ok, bool q_ok)
 {
-    const int step = direct ? (r.kind == GS_DTYPE_MXFP8 ? 128 : 64) : 32;
-    r.a.p_vec = r.a.p_type != GS_DTYPE_MXFP8 && vec_ok(r.a.p, r.a.p_type, r.a.ldp);
-    r.a.q_vec = r.a.q_type != GS_DTYPE_MXFP8 && vec_ok(r.a.q, r.a.q_type, r.a.ldq);
-    const float work = r.kind == GS_DTYPE_F32 ? 6.0f : r.kind == GS_DTYPE_MXFP8 && direct ? 0.6f : 1.0f;
     const bool pt = r.plan.pt, qt = r.plan.qt;
-    r.plan = make_plan(r.a.P, r.a.Q, r.a.K, pt, qt, !direct, step, work);
+    const int least = r.a.P < r.a.Q ? r.a.P : r.a.Q;
+    r.way = p_ok && q_ok ? kDirect : least <= 64 ? kStaged : kPacked;
+    r.pack_p = r.way == kPacked && (!p_ok || r.type == GS_DTYPE_MXFP8);
+    r.pack_q = r.way == kPacked && (!q_ok || r.type == GS_DTYPE_MXFP8);
+    if (r.way == kStaged) {
+        r.a.p_vec = r.type != GS_DTYPE_MXFP8 && vec_ok(r.a.p, r.a.p_type, r.a.ldp);
+        r.a.q_vec = r.type != GS_DTYPE_MXFP8 && vec_ok(r.a.q, r.a.q_type, r.a.ldq);
+    }
+    const bool mx = r.type == GS_DTYPE_MXFP8 && r.way == kDirect, f32 = r.type == GS_DTYPE_F32;
+    const int step = mx ? 128 : r.way == kStaged || f32 ? 32 : 64;
+    r.plan = make_plan(r.a.P, r.a.Q, r.a.K, pt, qt, r.way == kStaged, f32, step, f32 ? 6.0f : mx ? 0.6f : 1.0f);
     r.e.ld_partial = (r.a.P + 7) & ~7;
     r.e.split_stride = r.e.ld_partial * r.a.Q;
     r.partial_bytes = r.plan.splits > 1 ? (size_t)r.plan.splits * r.e.split_stride * 4 : 0;
-    r.e.vec = (r.e.bias_on_q || al16(r.e.bias)) && vec_ok(r.e.y, r.e.y_type, r.e.ldy) && (!r.e.residual || vec_ok(r.e.residual, r.e.y_type, r.e.ldr)) &&
+    r.e.vec = (r.e.bias_on_q || al16(r.e.bias)) && vec_ok(r.e.y, r.e.y_type, r.e.ldy) &&
+              (!r.e.residual || vec_ok(r.e.residual, r.e.y_type, r.e.ldr)) &&
               (!r.e.z || r.e.z_p != 1 || vec_ok(r.e.z, r.e.z_type, r.e.z_q));
     r.e.exact = r.e.y_type == GS_DTYPE_F32 || (r.e.z && r.e.z_type == GS_DTYPE_F32);
+}
+
+// Points an operand at its packed planes.
+void use_planes(const void *planes, int64_t rows, int64_t cols, const void *&p, int64_t &ld, int64_t &plane, int &extent, bool columns)
+{
+    p = planes;
+    ld = (cols + 7) & ~(int64_t)7;
+    plane = rows * ld;
+    if (columns) extent = (int)ld;
 }
 
 // Sum of the splits in their order, then the epilogue: a thread per 8
@@ -121,10 +245,10 @@ hipError_t run_product(Product &r, void *partial, hipStream_t s)
 {
     r.e.partial = r.plan.splits > 1 ? static_cast<float *>(partial) : nullptr;
     hipError_t err;
-    if (r.kind == GS_DTYPE_MXFP8) err = launch_product_mx8(r.a, r.e, r.plan, s);
-    else if (r.kind == GS_DTYPE_F32) err = launch_product_f32(r.a, r.e, r.plan, s);
-    else if (r.kind == GS_DTYPE_F16) err = launch_product_f16(r.a, r.e, r.plan, s);
-    else err = launch_product_bf16(r.a, r.e, r.plan, s);
+    if (r.type == GS_DTYPE_MXFP8 && r.way == kDirect) err = launch_product_mx8(r.a, r.e, r.plan, s);
+    else if (r.type == GS_DTYPE_F32) err = launch_product_f32(r.a, r.e, r.plan, s);
+    else if (r.type == GS_DTYPE_F16) err = launch_product_f16(r.a, r.e, r.plan, s);
+    else err = launch_product_bf16(r.a, r.e, r.plan, s);        // widened 8-bit operands too
     if (err != hipSuccess || r.plan.splits == 1) return err;
     const bool vec = r.e.vec && r.a.P % 8 == 0;
     const int64_t n = (int64_t)(vec ? r.a.P / 8 : r.a.P) * r.a.Q;
@@ -168,10 +292,16 @@ gs_status linear_fwd_ok(const gs_linear *l)
     return GS_OK;
 }
 
-Product plan_fwd(const gs_linear &l)
+struct FwdPlan {
+    Product product;
+    size_t p_at, q_at, partial_at, bytes;
+};
+
+FwdPlan plan_fwd(const gs_linear &l)
 {
-    Product r;
-    memset(&r, 0, sizeof r);
+    FwdPlan f;
+    memset(&f, 0, sizeof f);
+    Product &r = f.product;
     const int es = dtype_bytes(l.dtype);
     const bool px = l.planes != 0;              // the P operand is x
     gemm::Args &a = r.a;
@@ -187,7 +317,7 @@ Product plan_fwd(const gs_linear &l)
     a.Q = a.Ql = (int)(px ? l.n : l.m);
     a.K = l.k;
     a.p_type = a.q_type = l.dtype;
-    r.kind = l.dtype;
+    r.type = l.dtype;
     LinearEpilogue::Args &e = r.e;
     e.bias = l.bias;
     e.bias_on_q = px;
@@ -201,13 +331,41 @@ Product plan_fwd(const gs_linear &l)
     e.z_type = l.dtype;
     e.z_q = px ? 1 : l.z_stride;
     e.z_p = px ? l.z_stride : 1;
+    bool p_ok = l.dtype != GS_DTYPE_F32 && gemm::direct_ok(a.p, es, a.ldp, a.K), q_ok = l.dtype != GS_DTYPE_F32 && gemm::direct_ok(a.q, es, a.ldq, a.K);
     // 8-bit matrix instructions only for 16-bit results: they keep fewer bits
     // of a sum than fp32 holds
-    bool direct = l.dtype != GS_DTYPE_F32 && gemm::direct_ok(a.p, es, a.ldp, a.K) && gemm::direct_ok(a.q, es, a.ldq, a.K);
     if (l.dtype == GS_DTYPE_MXFP8)
-        direct = direct && l.y_dtype != GS_DTYPE_F32 && a.ldps < (1 << 22) && a.ldqs < (1 << 22);
-    finish_plan(r, direct);
-    return r;
+        p_ok = q_ok = p_ok && q_ok && l.y_dtype != GS_DTYPE_F32 && a.ldps < (1 << 22) && a.ldqs < (1 << 22);
+    finish_plan(r, p_ok, q_ok);
+    if (r.pack_p) {
+        f.p_at = f.bytes;
+        f.bytes += packed_bytes(l.dtype, a.P, l.k);
+    }
+    if (r.pack_q) {
+        f.q_at = f.bytes;
+        f.bytes += packed_bytes(l.dtype, a.Q, l.k);
+    }
+    f.partial_at = f.bytes;
+    f.bytes += r.partial_bytes;
+    return f;
+}
+
+hipError_t run_fwd(const gs_linear &l, FwdPlan &f, char *ws, hipStream_t s)
+{
+    Product &r = f.product;
+    gemm::Args &a = r.a;
+    PackJobs jobs;
+    memset(&jobs, 0, sizeof jobs);
+    if (r.pack_p) {
+        add_job(jobs, a.p, l.dtype, a.ps, a.ldp, a.ldps, a.P, l.k, ws + f.p_at);
+        use_planes(ws + f.p_at, a.P, l.k, a.p, a.ldp, a.plane_p, a.Pl, false);
+    }
+    if (r.pack_q) {
+        add_job(jobs, a.q, l.dtype, a.qs, a.ldq, a.ldqs, a.Q, l.k, ws + f.q_at);
+        use_planes(ws + f.q_at, a.Q, l.k, a.q, a.ldq, a.plane_q, a.Ql, false);
+    }
+    const hipError_t err = run_jobs(jobs, s);
+    return err == hipSuccess ? run_product(r, ws + f.partial_at, s) : err;
 }
 
 // ---- backward: dz and the sums of db -------------------------------------------
@@ -216,6 +374,7 @@ struct DzArgs {
     int64_t lddy, ldz;
     int dy_type, type, act, exact;
     void *dz;                           // [m][ld_dz] of `type`, zeros past n; NULL: not wanted
+    uint16_t *limbs;                    // fp32: [3][m][ld_dz] bf16 limbs of dz; NULL: not wanted
     int64_t ld_dz;
     float *part;                        // [row blocks][n] partial sums of db, or NULL
     int64_t m;
@@ -231,7 +390,7 @@ __global__ __launch_bounds__(kThreads) void dz_rows(DzArgs d, int groups)
     const int cg = threadIdx.x % groups, rl = threadIdx.x / groups, lanes = kThreads / groups;
     const int c0 = (blockIdx.x * groups + cg) * 8, valid = max(0, min(8, d.n - c0));
     const int64_t r0 = (int64_t)blockIdx.y * d.rows_per_block, r1 = min(d.m, r0 + d.rows_per_block);
-    const int room = d.dz ? (int)max((int64_t)0, min((int64_t)8, d.ld_dz - c0)) : 0;
+    const bool room = c0 < d.ld_dz;             // ld_dz is a multiple of 8
     float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     for (int64_t r = r0 + rl; r < r1; r += lanes) {
         float v[8];
@@ -239,17 +398,13 @@ __global__ __launch_bounds__(kThreads) void dz_rows(DzArgs d, int groups)
         if (d.act != GS_ACT_NONE) {
             float z[8];
             load8(d.z, d.type, r * d.ldz + c0, valid, d.vec, z);
-            if (d.exact) {
-#pragma unroll
-                for (int i = 0; i < 8; i++) v[i] = i < valid ? v[i] * activate_slope<true>(z[i], d.act) : 0.0f;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; i++) v[i] = i < valid ? v[i] * activate_slope<false>(z[i], d.act) : 0.0f;
-            }
+            if (d.exact) scale_by_slope<8, true>(v, z, d.act);      // past n: 0 times the slope at 0
+            else scale_by_slope<8, false>(v, z, d.act);
         }
 #pragma unroll
         for (int i = 0; i < 8; i++) acc[i] += v[i];
-        if (room == 8) store8_vec(d.dz, d.type, r * d.ld_dz + c0, v);        // ld_dz is a multiple of 8
+        if (room && d.dz) store8_vec(d.dz, d.type, r * d.ld_dz + c0, v);
+        if (room && d.limbs) store_planes(d.limbs, d.m * d.ld_dz, r * d.ld_dz + c0, 3, 0, v);
     }
     if (!d.part) return;
 #pragma unroll
@@ -285,10 +440,20 @@ __global__ __launch_bounds__(kThreads) void dz_planes(DzArgs d)
             float v = tile[tx][i];
             if (d.act != GS_ACT_NONE && c < d.n) {
                 const float z = load_as_float(d.z, d.type, (r + i) * d.ldz + c);
-                v *= d.exact ? activate_slope<true>(z, d.act) : activate_slope<false>(z, d.act);
+                if (d.exact) scale_by_slope<1, true>(&v, &z, d.act);
+                else scale_by_slope<1, false>(&v, &z, d.act);
             }
             acc += v;
-            if (d.dz && c < d.ld_dz) store_from_float(d.dz, d.type, (r + i) * d.ld_dz + c, v);
+            if (c < d.ld_dz) {
+                const int64_t at = (r + i) * d.ld_dz + c;
+                if (d.dz) store_from_float(d.dz, d.type, at, v);
+                if (d.limbs) {
+                    uint16_t limb[3];
+                    split_limbs<3>(v, limb);
+#pragma unroll
+                    for (int l = 0; l < 3; l++) d.limbs[l * d.m * d.ld_dz + at] = limb[l];
+                }
+            }
         }
         __syncthreads();
     }
@@ -300,11 +465,12 @@ __global__ __launch_bounds__(kThreads) void dz_planes(DzArgs d)
 
 // Everything a backward call does, with its places in the workspace.
 struct BwdPlan {
-    bool own_dz;                        // dz is written to the workspace (else dz is dy)
+    bool own_dz;                        // dz is written to the workspace in `dtype` (else dz is dy where that is read)
+    bool limbs;                         // dz is written as limbs
     bool pass;                          // the dz / db pass runs
     int row_blocks, rows_per_block;
     int64_t ld_dz;
-    size_t dz_at, part_at, dx_at, dw_at, bytes;
+    size_t dz_at, limbs_at, part_at, w_at, x_at, split_at, bytes;
     Product dx, dw;
 };
 
@@ -313,13 +479,40 @@ BwdPlan plan_bwd(const gs_linear &l, const gs_linear_grads &g)
     BwdPlan b;
     memset(&b, 0, sizeof b);
     const int es = dtype_bytes(l.dtype);
-    const bool products = g.dx || g.dw;
-    // dz is dy itself when nothing has to be done to it and it can be loaded
-    // as it stands
-    const bool same = l.activation == GS_ACT_NONE && !l.planes && l.y_dtype == l.dtype;
-    b.own_dz = products && !(same && (l.dtype == GS_DTYPE_F32 || gemm::direct_ok(g.dy, es, g.dy_stride, l.n)));
-    b.pass = b.own_dz || g.db;
+    const bool f32 = l.dtype == GS_DTYPE_F32;
     b.ld_dz = ((int64_t)l.n + 7) & ~(int64_t)7;
+    // dz is dy itself when nothing has to be done to it; a 16-bit dz is always
+    // loadable directly, written that way if dy is not
+    const bool same = l.activation == GS_ACT_NONE && !l.planes && l.y_dtype == l.dtype;
+    const bool as_is = same && (f32 || gemm::direct_ok(g.dy, es, g.dy_stride, l.n));
+
+    auto product = [&](Product &r, const void *p, int64_t ldp, int Q, int K, bool qt, void *y, int64_t ldy, int y_type, bool add) {
+        r.type = l.dtype;
+        r.plan.pt = true;
+        r.plan.qt = qt;
+        r.a.p = p;
+        r.a.ldp = ldp;
+        r.a.p_type = r.a.q_type = l.dtype;
+        r.a.q = as_is ? g.dy : nullptr;                 // else: the workspace, 256-byte aligned
+        r.a.ldq = as_is ? g.dy_stride : b.ld_dz;
+        r.a.P = r.a.Pl = l.k;
+        r.a.Q = r.a.Ql = Q;
+        r.a.K = K;
+        r.e.y = y;
+        r.e.ldy = ldy;
+        r.e.y_type = y_type;
+        r.e.accumulate = add;
+        finish_plan(r, !f32 && gemm::direct_ok(p, es, ldp, l.k), !f32);
+        if (qt && !as_is) r.a.Ql = (int)b.ld_dz;        // its padding may be read
+        r.pack_q = false;                               // dz comes from the pass in the form it is needed in
+    };
+    if (g.dx) product(b.dx, l.w, l.w_stride, (int)l.m, l.n, false, g.dx, g.dx_stride, l.dtype, false);
+    if (g.dw) product(b.dw, l.x, l.x_stride, l.n, (int)l.m, true, g.dw, g.dw_stride, g.dw_dtype, g.accumulate != 0);
+    const bool staged_f32 = f32 && ((g.dx && b.dx.way == kStaged) || (g.dw && b.dw.way == kStaged));
+    b.limbs = f32 && ((g.dx && b.dx.way == kPacked) || (g.dw && b.dw.way == kPacked));
+    b.own_dz = !as_is && (f32 ? staged_f32 : g.dx || g.dw);
+    b.pass = b.own_dz || b.limbs || g.db;
+
     // row blocks of the pass: enough for the device, at most 1024 (the partial
     // sums are read once more)
     const int64_t cols = l.planes ? (l.n + 63) / 64 : (l.n + 511) / 512;
@@ -330,56 +523,18 @@ BwdPlan plan_bwd(const gs_linear &l, const gs_linear_grads &g)
     if (per < 64) per = 64;
     b.rows_per_block = (int)per;
     b.row_blocks = (int)((l.m + per - 1) / per);
-    size_t at = 0;
-    b.dz_at = at;
-    if (b.own_dz) at += round256((size_t)l.m * b.ld_dz * es);
-    b.part_at = at;
-    if (g.db) at += round256((size_t)b.row_blocks * l.n * 4);
-
-    auto common = [&](Product &r) {
-        r.kind = l.dtype;
-        r.a.p_type = r.a.q_type = l.dtype;
-        r.a.q = b.own_dz ? nullptr : g.dy;              // with own_dz: the workspace, 256-byte aligned
-        r.a.ldq = b.own_dz ? b.ld_dz : g.dy_stride;
-        r.plan.pt = true;
-        r.a.P = r.a.Pl = l.k;
+    auto take = [&](size_t bytes) {
+        const size_t at = b.bytes;
+        b.bytes += round256(bytes);
+        return at;
     };
-    const int64_t n_read = b.own_dz ? b.ld_dz : l.n;    // columns of dz that may be read
-    const bool w16 = l.dtype != GS_DTYPE_F32;
-    if (g.dx) {
-        Product &r = b.dx;
-        common(r);
-        r.a.p = l.w;
-        r.a.ldp = l.w_stride;
-        r.a.Q = r.a.Ql = (int)l.m;
-        r.a.K = l.n;
-        r.e.y = g.dx;
-        r.e.ldy = g.dx_stride;
-        r.e.y_type = l.dtype;
-        finish_plan(r, w16 && gemm::direct_ok(l.w, es, l.w_stride, l.k) &&
-                           gemm::direct_ok(r.a.q, es, r.a.ldq, n_read));
-        b.dx_at = at;
-    }
-    if (g.dw) {
-        Product &r = b.dw;
-        common(r);
-        r.plan.qt = true;
-        r.a.p = l.x;
-        r.a.ldp = l.x_stride;
-        r.a.Q = l.n;
-        r.a.Ql = (int)n_read;
-        r.a.K = (int)l.m;
-        r.e.y = g.dw;
-        r.e.ldy = g.dw_stride;
-        r.e.y_type = g.dw_dtype;
-        r.e.accumulate = g.accumulate != 0;
-        finish_plan(r, w16 && gemm::direct_ok(l.x, es, l.x_stride, l.k) &&
-                           gemm::direct_ok(r.a.q, es, r.a.ldq, n_read));
-        b.dw_at = at;
-    }
+    if (b.own_dz) b.dz_at = take((size_t)l.m * b.ld_dz * es);
+    if (b.limbs) b.limbs_at = take((size_t)3 * l.m * b.ld_dz * 2);
+    if (g.db) b.part_at = take((size_t)b.row_blocks * l.n * 4);
+    if (b.dx.pack_p) b.w_at = take(packed_bytes(l.dtype, l.n, l.k));
+    if (b.dw.pack_p) b.x_at = take(packed_bytes(l.dtype, l.m, l.k));
     // the two products run one after the other and share their partial sums' place
-    const size_t parts = b.dx.partial_bytes > b.dw.partial_bytes ? b.dx.partial_bytes : b.dw.partial_bytes;
-    b.bytes = at + round256(parts);
+    b.split_at = take(b.dx.partial_bytes > b.dw.partial_bytes ? b.dx.partial_bytes : b.dw.partial_bytes);
     return b;
 }
 
@@ -434,6 +589,7 @@ hipError_t run_bwd(const gs_linear &l, const gs_linear_grads &g, BwdPlan &b, cha
         d.act = l.activation;
         d.exact = l.dtype == GS_DTYPE_F32;
         d.dz = b.own_dz ? ws + b.dz_at : nullptr;
+        d.limbs = b.limbs ? reinterpret_cast<uint16_t *>(ws + b.limbs_at) : nullptr;
         d.ld_dz = b.ld_dz;
         d.part = g.db ? reinterpret_cast<float *>(ws + b.part_at) : nullptr;
         d.m = l.m;
@@ -452,16 +608,26 @@ hipError_t run_bwd(const gs_linear &l, const gs_linear_grads &g, BwdPlan &b, cha
             if ((err = launch_sum_rows(d.part, g.db, l.n, b.row_blocks, g.accumulate, s)) != hipSuccess) return err;
         }
     }
-    if (g.dx) {
-        if (b.own_dz) b.dx.a.q = ws + b.dz_at;
-        b.dx.a.q_vec = b.own_dz ? 1 : b.dx.a.q_vec;
-        if ((err = run_product(b.dx, ws + b.dx_at, s)) != hipSuccess) return err;
-    }
-    if (g.dw) {
-        if (b.own_dz) b.dw.a.q = ws + b.dz_at;
-        b.dw.a.q_vec = b.own_dz ? 1 : b.dw.a.q_vec;
-        if ((err = run_product(b.dw, ws + b.dw_at, s)) != hipSuccess) return err;
-    }
+    PackJobs jobs;
+    memset(&jobs, 0, sizeof jobs);
+    auto operands = [&](Product &r, bool packed_at, size_t at, int64_t rows, bool qt) {
+        gemm::Args &a = r.a;
+        if (packed_at) {
+            add_job(jobs, a.p, l.dtype, nullptr, a.ldp, 0, rows, l.k, ws + at);
+            use_planes(ws + at, rows, l.k, a.p, a.ldp, a.plane_p, a.Pl, true);
+        }
+        if (b.limbs && r.way == kPacked) {
+            use_planes(ws + b.limbs_at, l.m, l.n, a.q, a.ldq, a.plane_q, a.Ql, qt);
+        } else if (b.own_dz) {
+            a.q = ws + b.dz_at;
+            a.q_vec = 1;
+        }
+    };
+    if (g.dx) operands(b.dx, b.dx.pack_p, b.w_at, l.n, false);
+    if (g.dw) operands(b.dw, b.dw.pack_p, b.x_at, l.m, true);
+    if ((err = run_jobs(jobs, s)) != hipSuccess) return err;
+    if (g.dx && (err = run_product(b.dx, ws + b.split_at, s)) != hipSuccess) return err;
+    if (g.dw && (err = run_product(b.dw, ws + b.split_at, s)) != hipSuccess) return err;
     return hipSuccess;
 }
 
@@ -477,7 +643,7 @@ extern "C" {
 size_t gs_linear_fwd_workspace_bytes(const gs_linear *l)
 {
     if (linear_fwd_ok(l) != GS_OK || l->m == 0) return 0;
-    return plan_fwd(*l).partial_bytes;
+    return plan_fwd(*l).bytes;
 }
 
 gs_status gs_linear_fwd(const gs_linear *l, void *workspace, size_t workspace_bytes, void *stream)
@@ -485,12 +651,12 @@ gs_status gs_linear_fwd(const gs_linear *l, void *workspace, size_t workspace_by
     const gs_status st = linear_fwd_ok(l);
     if (st != GS_OK) return st;
     if (l->m == 0) return GS_OK;
-    Product r = plan_fwd(*l);
-    if (r.partial_bytes > 0) {
-        if (workspace_bytes < r.partial_bytes) return GS_ERR_WORKSPACE;
+    FwdPlan f = plan_fwd(*l);
+    if (f.bytes > 0) {
+        if (workspace_bytes < f.bytes) return GS_ERR_WORKSPACE;
         if (!workspace || !al16(workspace)) return GS_ERR_INVALID_ARG;
     }
-    return from_hip(run_product(r, workspace, (hipStream_t)stream));
+    return from_hip(run_fwd(*l, f, static_cast<char *>(workspace), (hipStream_t)stream));
 }
 
 size_t gs_linear_bwd_workspace_bytes(const gs_linear *l, const gs_linear_grads *g)

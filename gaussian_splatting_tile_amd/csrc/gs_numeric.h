@@ -124,11 +124,11 @@ template <bool EXACT> __device__ __forceinline__ float logistic(float z)
     if constexpr (EXACT) return 1.0f / (1.0f + expf(-z));
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
 }
-template <bool EXACT> __device__ __forceinline__ float activate(float z, int act)
+template <int ACT, bool EXACT> __device__ __forceinline__ float activate(float z)
 {
-    if (act == GS_ACT_RELU) return z < 0.0f ? 0.0f : z;               // a NaN stays one
-    if (act == GS_ACT_SILU) return z * logistic<EXACT>(z);
-    if (act == GS_ACT_GELU) {
+    if constexpr (ACT == GS_ACT_RELU) return z < 0.0f ? 0.0f : z;     // a NaN stays one
+    if constexpr (ACT == GS_ACT_SILU) return z * logistic<EXACT>(z);
+    if constexpr (ACT == GS_ACT_GELU) {
         if constexpr (EXACT) return z * (0.5f * erfcf(-0.70710678118654752f * z));
         // z Phi(z) = max(z, 0) - |z| Phi(-|z|); the bound keeps an infinite z from
         // meeting the tail's 0
@@ -138,20 +138,50 @@ template <bool EXACT> __device__ __forceinline__ float activate(float z, int act
     }
     return z;
 }
-template <bool EXACT> __device__ __forceinline__ float activate_slope(float z, int act)
+template <int ACT, bool EXACT> __device__ __forceinline__ float activate_slope(float z)
 {
-    if (act == GS_ACT_RELU) return z > 0.0f ? 1.0f : z == z ? 0.0f : z;
-    if (act == GS_ACT_SILU) {
+    if constexpr (ACT == GS_ACT_RELU) return z > 0.0f ? 1.0f : z == z ? 0.0f : z;
+    if constexpr (ACT == GS_ACT_SILU) {
         const float s = logistic<EXACT>(z);
         return s * fmaf(z, 1.0f - s, 1.0f);
     }
-    if (act == GS_ACT_GELU) {
+    if constexpr (ACT == GS_ACT_GELU) {
         if constexpr (EXACT) return 0.5f * erfcf(-0.70710678118654752f * z) + z * 0.39894228040143268f * expf(-0.5f * z * z);
         float e;
         const float h = normal_tail(z, e);
         return fmaf(z * 0.39894228040143268f, e, z >= 0.0f ? 1.0f - h : h);
     }
     return 1.0f;
+}
+
+// The choice of activation is made once for N values: a branch in front of
+// each would put their exponentials and reciprocals one after the other.
+template <int N, bool EXACT> __device__ __forceinline__ void activate_all(float v[N], int act)
+{
+    if (act == GS_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < N; i++) v[i] = activate<GS_ACT_RELU, EXACT>(v[i]);
+    } else if (act == GS_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < N; i++) v[i] = activate<GS_ACT_SILU, EXACT>(v[i]);
+    } else if (act == GS_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < N; i++) v[i] = activate<GS_ACT_GELU, EXACT>(v[i]);
+    }
+}
+// v *= act'(z)
+template <int N, bool EXACT> __device__ __forceinline__ void scale_by_slope(float v[N], const float z[N], int act)
+{
+    if (act == GS_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < N; i++) v[i] *= activate_slope<GS_ACT_RELU, EXACT>(z[i]);
+    } else if (act == GS_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < N; i++) v[i] *= activate_slope<GS_ACT_SILU, EXACT>(z[i]);
+    } else if (act == GS_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < N; i++) v[i] *= activate_slope<GS_ACT_GELU, EXACT>(z[i]);
+    }
 }
 
 }  // namespace gsi
