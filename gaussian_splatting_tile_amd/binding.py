@@ -520,38 +520,41 @@ def active_mask_static(scores, n, keep, mask, stream=None):
 # ---- a network head that predicts Gaussians ---------------------------------
 _DTYPES = {torch.float32: GS_DTYPE_F32, torch.float16: GS_DTYPE_F16, torch.bfloat16: GS_DTYPE_BF16,
            torch.float8_e4m3fn: GS_DTYPE_MXFP8}
+_BY_CODE = {code: t for t, code in _DTYPES.items()}
 _SCALES = (torch.uint8, torch.float8_e8m0fnu)
 
 
 def _dtype(t: torch.Tensor) -> int:
-    d = _DTYPES.get(t.dtype)
-    if d is None:
-        raise ValueError(f"unsupported element type {t.dtype}")
-    return d
+    try:
+        return _DTYPES[t.dtype]
+    except KeyError:
+        raise ValueError(f"unsupported element type {t.dtype}") from None
 
 
-def _rows(t: Optional[torch.Tensor], rows: int, cols: int, what: str, dtype=None, device=None):
-    """(pointer, row stride) of an [rows][cols] tensor whose rows are
+def _rows(t: Optional[torch.Tensor], rows: int, cols: int, what: str, dtypes=None, device=None):
+    """(address, row stride) of a [rows][cols] tensor whose rows are
     contiguous; (None, cols) for None."""
     if t is None:
         return None, cols
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise ValueError(f"{what}: expected [{rows}][{cols}], got {tuple(t.shape)}")
-    if dtype is not None and (t.dtype not in dtype if isinstance(dtype, tuple) else t.dtype != dtype):
+    if dtypes is not None and t.dtype not in dtypes:
         raise ValueError(f"{what}: unexpected element type {t.dtype}")
     if device is not None and t.device != device:
-        raise ValueError(f"{what}: on {t.device}, expected {device}")
-    s = t.stride()
-    if (cols > 1 and s[1] != 1) or (rows > 1 and s[0] < cols):
-        raise ValueError(f"{what}: rows must be contiguous and must not overlap (strides {s})")
-    return t.data_ptr(), (s[0] if rows > 1 else cols)
+        raise ValueError(f"{what}: on {t.device}, another device than the others")
+    stride, step = t.stride()
+    if rows <= 1:
+        stride = cols
+    if (step != 1 and cols > 1) or stride < cols:
+        raise ValueError(f"{what}: rows must be contiguous and must not overlap (strides {t.stride()})")
+    return t.data_ptr(), stride
 
 
 def _vector(t: Optional[torch.Tensor], n: int, what: str, device=None):
     if t is None:
         return None
-    if t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous() or (device is not None and t.device != device):
-        raise ValueError(f"{what}: expected {n} contiguous float32 values on {device}")
+    if t.dtype is not torch.float32 or t.numel() != n or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{what}: expected {n} contiguous float32 values on the others' device")
     return t.data_ptr()
 
 
@@ -563,13 +566,11 @@ def rms_norm_fwd(x: torch.Tensor, y: torch.Tensor, gamma: Optional[torch.Tensor]
     bfloat16): y = (x + residual) * rstd * gamma in x's type, or
     torch.float8_e4m3fn with y_scales [m][n / 32] (uint8 or float8_e8m0fnu)."""
     m, n = x.shape
-    a = GsRmsNorm(m=m, n=n, dtype=_dtype(x), y_dtype=_dtype(y), eps=eps)
-    a.x, a.x_stride = _rows(x, m, n, "x")
-    a.residual, a.residual_stride = _rows(residual, m, n, "residual", x.dtype, x.device)
-    a.sum, a.sum_stride = _rows(sum_out, m, n, "sum_out", x.dtype, x.device)
-    a.y, a.y_stride = _rows(y, m, n, "y", (x.dtype, torch.float8_e4m3fn), x.device)
-    a.y_scales, a.y_scales_stride = _rows(y_scales, m, n // 32, "y_scales", _SCALES, x.device)
-    a.gamma, a.rstd = _vector(gamma, n, "gamma", x.device), _vector(rstd, m, "rstd", x.device)
+    own, dev = (x.dtype,), x.device
+    a = GsRmsNorm(m, n, _dtype(x), _dtype(y), eps, *_rows(x, m, n, "x"), *_rows(residual, m, n, "residual", own, dev),
+                  _vector(gamma, n, "gamma", dev), *_rows(sum_out, m, n, "sum_out", own, dev),
+                  *_rows(y, m, n, "y", (x.dtype, torch.float8_e4m3fn), dev),
+                  *_rows(y_scales, m, n // 32, "y_scales", _SCALES, dev), _vector(rstd, m, "rstd", dev))
     _check(lib().gs_rms_norm_fwd(C.byref(a), _stream(stream)), "gs_rms_norm_fwd")
 
 
@@ -585,14 +586,11 @@ def rms_norm_bwd(sum_in: torch.Tensor, rstd: torch.Tensor, dy: torch.Tensor, dx:
     gradient dx of x and residual and, with dgamma and a workspace of
     rms_norm_bwd_workspace_bytes(m, n), that of gamma."""
     m, n = sum_in.shape
-    t, dev = sum_in.dtype, sum_in.device
-    a = GsRmsNormGrads(m=m, n=n, dtype=_dtype(sum_in), accumulate=1 if accumulate else 0)
-    a.sum, a.sum_stride = _rows(sum_in, m, n, "sum_in")
-    a.dy, a.dy_stride = _rows(dy, m, n, "dy", t, dev)
-    a.dsum, a.dsum_stride = _rows(dsum, m, n, "dsum", t, dev)
-    a.dx, a.dx_stride = _rows(dx, m, n, "dx", t, dev)
-    a.rstd, a.gamma = _vector(rstd, m, "rstd", dev), _vector(gamma, n, "gamma", dev)
-    a.dgamma = _vector(dgamma, n, "dgamma", dev)
+    own, dev = (sum_in.dtype,), sum_in.device
+    a = GsRmsNormGrads(m, n, _dtype(sum_in), *_rows(sum_in, m, n, "sum_in"), _vector(rstd, m, "rstd", dev),
+                       _vector(gamma, n, "gamma", dev), *_rows(dy, m, n, "dy", own, dev),
+                       *_rows(dsum, m, n, "dsum", own, dev), *_rows(dx, m, n, "dx", own, dev),
+                       _vector(dgamma, n, "dgamma", dev), 1 if accumulate else 0)
     _check(lib().gs_rms_norm_bwd(C.byref(a), _ptr(workspace), _nbytes(workspace), _stream(stream)), "gs_rms_norm_bwd")
 
 
@@ -600,9 +598,10 @@ def mxfp8_quantize(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, s
     """gs_mxfp8_quantize: x [m][n] -> codes float8_e4m3fn [m][n] and scales
     [m][n / 32] (uint8 or float8_e8m0fnu)."""
     m, n = x.shape
+    dev = x.device
     xp, xs = _rows(x, m, n, "x")
-    cp, cs = _rows(codes, m, n, "codes", torch.float8_e4m3fn, x.device)
-    sp, ss = _rows(scales, m, n // 32, "scales", _SCALES, x.device)
+    cp, cs = _rows(codes, m, n, "codes", (torch.float8_e4m3fn,), dev)
+    sp, ss = _rows(scales, m, n // 32, "scales", _SCALES, dev)
     _check(lib().gs_mxfp8_quantize(xp, _dtype(x), m, n, xs, cp, cs, sp, ss, _stream(stream)), "gs_mxfp8_quantize")
 
 
@@ -615,19 +614,16 @@ def linear_struct(x: torch.Tensor, w: torch.Tensor, y: Optional[torch.Tensor],
     z: the pre-activation kept for the backward, [m][n] of x's type."""
     m, k = x.shape
     n = w.shape[0]
-    a = GsLinear(m=m, n=n, k=k, dtype=_dtype(x), y_dtype=_dtype(x if y is None else y), activation=GS_ACT[act],
-                 planes=1 if planes else 0)
+    own, dev = (x.dtype,), x.device
     rows, cols = (n, m) if planes else (m, n)
-    a.x, a.x_stride = _rows(x, m, k, "x")
-    a.w, a.w_stride = _rows(w, n, k, "w", x.dtype, x.device)
-    if x.dtype == torch.float8_e4m3fn:
-        a.x_scales, a.x_scales_stride = _rows(x_scales, m, k // 32, "x_scales", _SCALES, x.device)
-        a.w_scales, a.w_scales_stride = _rows(w_scales, n, k // 32, "w_scales", _SCALES, x.device)
-    a.bias = _vector(bias, n, "bias", x.device)
-    a.y, a.y_stride = _rows(y, rows, cols, "y", None, x.device)
-    a.residual, a.residual_stride = _rows(residual, rows, cols, "residual", None if y is None else y.dtype, x.device)
-    a.z, a.z_stride = _rows(z, m, n, "z", x.dtype, x.device)
-    return a
+    yt = None if y is None else (y.dtype,)
+    block = x.dtype is torch.float8_e4m3fn
+    return GsLinear(m, n, k, _dtype(x), _dtype(x if y is None else y), GS_ACT[act], 1 if planes else 0,
+                    *_rows(x, m, k, "x"), *_rows(w, n, k, "w", own, dev),
+                    *(_rows(x_scales, m, k // 32, "x_scales", _SCALES, dev) if block else (None, 0)),
+                    *(_rows(w_scales, n, k // 32, "w_scales", _SCALES, dev) if block else (None, 0)),
+                    _vector(bias, n, "bias", dev), *_rows(residual, rows, cols, "residual", yt, dev),
+                    *_rows(y, rows, cols, "y", None, dev), *_rows(z, m, n, "z", own, dev))
 
 
 def linear_fwd_workspace_bytes(a: GsLinear) -> int:
@@ -649,14 +645,11 @@ def linear_grads_struct(a: GsLinear, dy: torch.Tensor, dx: Optional[torch.Tensor
     dy's."""
     rows, cols = (a.n, a.m) if a.planes else (a.m, a.n)
     a.y_dtype = _dtype(dy)
-    own = [t for t, d in _DTYPES.items() if d == a.dtype][0]
-    g = GsLinearGrads(accumulate=1 if accumulate else 0)
-    g.dy, g.dy_stride = _rows(dy, rows, cols, "dy")
-    g.dx, g.dx_stride = _rows(dx, a.m, a.k, "dx", own, dy.device)
-    g.dw, g.dw_stride = _rows(dw, a.n, a.k, "dw", (own, torch.float32), dy.device)
-    g.dw_dtype = GS_DTYPE_F32 if dw is None else _dtype(dw)
-    g.db = _vector(db, a.n, "db", dy.device)
-    return g
+    own, dev = _BY_CODE[a.dtype], dy.device
+    return GsLinearGrads(*_rows(dy, rows, cols, "dy"), *_rows(dx, a.m, a.k, "dx", (own,), dev),
+                         *_rows(dw, a.n, a.k, "dw", (own, torch.float32), dev),
+                         GS_DTYPE_F32 if dw is None else _dtype(dw), 1 if accumulate else 0,
+                         _vector(db, a.n, "db", dev))
 
 
 def linear_bwd_workspace_bytes(a: GsLinear, g: GsLinearGrads) -> int:
@@ -692,13 +685,10 @@ def muon_struct(grad: torch.Tensor, out: Optional[torch.Tensor] = None, momentum
             raise ValueError(f"{what}: expected float32")
     if weight is not None and weight.dtype != weight_out.dtype:
         raise ValueError("weight_out: expected weight's type")
-    a = GsMuon(batch=shape[0] if len(shape) == 3 else 1, rows=shape[-2], cols=shape[-1], grad_dtype=_dtype(grad),
-               out_dtype=_dtype(grad if out is None and weight is None else out if weight is None else weight),
-               steps=steps, a=coeffs[0], b=coeffs[1], c=coeffs[2], eps=eps, lr=lr, beta=beta,
-               weight_decay=weight_decay, scale=scale, nesterov=1 if nesterov else 0)
-    a.grad, a.out, a.momentum, a.momentum_out = _ptr(grad), _ptr(out), _ptr(momentum), _ptr(momentum_out)
-    a.weight, a.weight_out = _ptr(weight), _ptr(weight_out)
-    return a
+    to = weight if weight is not None else out if out is not None else grad
+    return GsMuon(shape[0] if len(shape) == 3 else 1, shape[-2], shape[-1], _dtype(grad), _dtype(to), steps, *coeffs, eps,
+                  lr, beta, weight_decay, scale, 1 if nesterov else 0, _ptr(grad), _ptr(out), _ptr(momentum),
+                  _ptr(momentum_out), _ptr(weight), _ptr(weight_out))
 
 
 def muon_workspace_bytes(a: GsMuon) -> int:

@@ -22,7 +22,7 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgs_hip.so")
 SOURCES = ["gs_api.hip", "gs_project.hip", "gs_sort.hip", "gs_render.hip", "gs_mask.hip", "gs_adam.hip",
            "gs_norm.hip", "gs_linear.hip", "gs_product_bf16.hip", "gs_product_f16.hip", "gs_product_f32.hip",
-           "gs_product_mx8.hip", "gs_muon.hip"]
+           "gs_product_mx8.hip", "gs_product_few.hip", "gs_muon.hip"]
 # the peak-rate microbenchmarks the roofline fractions are also taken against
 # (not part of the rasterizer's ABI)
 PEAKS_LIB = os.path.join(PKG, "libgs_peaks.so")

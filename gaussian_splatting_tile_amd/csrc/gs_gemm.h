@@ -189,8 +189,7 @@ template <class TL, int THREADS, bool T, int ES> struct Direct {
 // Scale bytes of a kMX8 tile: 4 blocks of 32 k per row, each widened to a word
 // in LDS, [BX][4].  Blocks past the end of k read as 0, a finite scale.
 template <int BX, int THREADS> struct Scales {
-    static constexpr int kLoads = BX * 4 / THREADS;
-    static_assert(BX * 4 % THREADS == 0, "tile and block size");
+    static constexpr int kLoads = BX * 4 >= THREADS ? BX * 4 / THREADS : 1;
     uint32_t off[kLoads];
 
     __device__ __forceinline__ void init(int x0, int X, int64_t ld, int tid)
@@ -264,26 +263,31 @@ template <class TL, int THREADS, bool T, int NL, int KIND> struct Staged {
     }
 };
 
-// Which tile a block takes.  Blocks go to the 8 dies in turn, so block b of
-// nb becomes (b % 8)-th die's next tile of a contiguous eighth: the tiles of a
-// die share operands in its L2.  Within that order, 8 tiles down q by all of p.
-__device__ __forceinline__ void tile_of(int b, int tiles_p, int tiles_q, int &tp, int &tq)
+// Which tile and split of k a block takes.  Blocks go to the 8 dies in turn, so
+// block b of nb becomes the (b % 8)-th die's next item of a contiguous eighth of
+// the list of splits and, within each, tiles: a die's blocks share operands in
+// its L2 (with splits, only a range of k of them; 1024 x 1024 x 4096 in 7 splits
+// took 28.8 us where every die read all k).
+__device__ __forceinline__ int die_order(int b, int nb)
 {
-    const int nb = tiles_p * tiles_q, die = b & 7, at = b >> 3, per = nb >> 3, more = nb & 7;
-    const int t = die * per + min(die, more) + at;
+    const int die = b & 7, at = b >> 3, per = nb >> 3, more = nb & 7;
+    return die * per + min(die, more) + at;
+}
+// The t-th tile: 8 tiles down q by all of p, and so on.
+__device__ __forceinline__ void tile_of(int t, int tiles_p, int tiles_q, int &tp, int &tq)
+{
     const int group = 8 * tiles_p, g = t / group, r = t - g * group;
     const int h = min(8, tiles_q - g * 8);
     tp = r / h;
     tq = g * 8 + r - tp * h;
 }
-
-// The b-th tile of the triangle tp <= tq, row by row.
-__device__ __forceinline__ void triangle_of(int b, int &tp, int &tq)
+// The t-th tile of the triangle tp <= tq, row by row.
+__device__ __forceinline__ void triangle_of(int t, int &tp, int &tq)
 {
-    tq = (int)((sqrtf(8.0f * (float)b + 1.0f) - 1.0f) * 0.5f);
-    while ((tq + 1) * (tq + 2) / 2 <= b) tq++;
-    while (tq * (tq + 1) / 2 > b) tq--;
-    tp = b - tq * (tq + 1) / 2;
+    tq = (int)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
+    while ((tq + 1) * (tq + 2) / 2 <= t) tq++;
+    while (tq * (tq + 1) / 2 > t) tq--;
+    tp = t - tq * (tq + 1) / 2;
 }
 
 // Waits until at most LEFT of the wave's loads are outstanding and its LDS
@@ -293,6 +297,9 @@ template <int LEFT> __device__ __forceinline__ void stage_barrier()
     static_assert(LEFT >= 0 && LEFT < 64, "vmcnt");
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LEFT) : "memory");
 }
+
+// The same for LDS reads alone.
+__device__ __forceinline__ void slice_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 // Orders a wave's own LDS writes and reads across its lanes (the lanes run in
 // lockstep and LDS serves a wave in order: only the compiler has to be held).
@@ -311,15 +318,17 @@ constexpr int turn_part(int fp, int waves, int bytes)
 }
 
 // The epilogue takes 8 sums of consecutive p at a time where EPI::vec(e) allows,
-// EPI::store8(e, p, q, v, batch, split, mirror), else single ones,
-// EPI::store1.  mirror: the tile also stands for its transpose.
-template <int KIND, int NL, int NS, int BK, int BP, int BQ, int WP, int WQ, bool PT, bool QT, bool STAGED, class EPI>
+// EPI::store8(e, p, q, v, batch, split), which leaves the final values in v,
+// else single ones, EPI::store1.  A tile that also stands for its transpose
+// (EPI::kMirror) hands those on to EPI::store_mirror.
+template <int KIND, int NL, int NS, int BK, int BP, int BQ, int WP, int WQ, bool PT, bool QT, bool STAGED, bool PING, class EPI>
 __global__ __launch_bounds__(WP *WQ * 64, NL == 3 && BP == 128 ? 1 : 2) void product_kernel(Args a, typename EPI::Args e)
 {
     constexpr int kThreads = WP * WQ * 64;
     constexpr int FP = BP / WP / 16, FQ = BQ / WQ / 16, KK = BK / 32;
     constexpr int ES = KIND == kMX8 ? 1 : 2;
     constexpr int kStepK = KIND == kMX8 ? 2 * BK : BK;  // k per tile
+    static_assert(!PING || (WP * WQ == 8 && !STAGED), "two waves on every SIMD");
     static_assert(KIND != kMX8 || (!PT && !QT && !STAGED && NL == 1 && BK == 64), "8-bit operands");
     using TP = Tile<BP, BK, PT>;
     using TQ = Tile<BQ, BK, QT>;
@@ -336,12 +345,14 @@ __global__ __launch_bounds__(WP *WQ * 64, NL == 3 && BP == 128 ? 1 : 2) void pro
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wp = wave / WQ, wq = wave % WQ;
     int tp, tq;
+    const int item = die_order(blockIdx.y * gridDim.x + blockIdx.x, gridDim.x * gridDim.y);
+    const int split = item / gridDim.x, tile = item - split * gridDim.x;
     if (a.symmetric)
-        triangle_of(blockIdx.x, tp, tq);
+        triangle_of(tile, tp, tq);
     else
-        tile_of(blockIdx.x, a.tiles_p, a.tiles_q, tp, tq);
+        tile_of(tile, a.tiles_p, a.tiles_q, tp, tq);
     const int p0 = tp * BP, q0 = tq * BQ;
-    const int kbeg = blockIdx.y * a.k_split, kend = min(a.K, kbeg + a.k_split);
+    const int kbeg = split * a.k_split, kend = min(a.K, kbeg + a.k_split);
     const char *pb = static_cast<const char *>(a.p), *qb = static_cast<const char *>(a.q);
 
     f4 acc[FP][FQ];
@@ -350,53 +361,57 @@ __global__ __launch_bounds__(WP *WQ * 64, NL == 3 && BP == 128 ? 1 : 2) void pro
 #pragma unroll
         for (int j = 0; j < FQ; j++) acc[i][j] = f4{0, 0, 0, 0};
 
-    // issue() starts the next tile's loads once the first fragments are on their
-    // way: the wave's LDS reads do not queue behind them
-    auto compute = [&](const char *s, auto &&issue) {
-        if constexpr (KIND == kMX8) {
-            const int *sp = reinterpret_cast<const int *>(s + kScaleAt) + (wp * FP * 16 + (lane & 15)) * 4 + (lane >> 4);
-            const int *sq = reinterpret_cast<const int *>(s + kScaleAt + BP * 16) + (wq * FQ * 16 + (lane & 15)) * 4 + (lane >> 4);
-            int sqv[FQ];
+    // A tile's products in slices: 32 k each, or (kMX8, 128 k at once) half of
+    // the P side each.  fetch() reads a slice's fragments, multiply() uses them.
+    constexpr bool MX = KIND == kMX8;
+    constexpr int kSlices = MX ? (FP > 1 ? 2 : 1) : KK, kHalf = MX ? FP / kSlices : FP;
+    i4 pf[MX ? 2 : NL][kHalf], qf[MX ? 2 : NL][FQ];
+    int sp[MX ? kHalf : 1], sq[MX ? FQ : 1];
+    auto fetch = [&](const char *s, int slice) {
+        const char *t = s + NL * TP::kBytes;
+        if constexpr (MX) {
+            const int *cp = reinterpret_cast<const int *>(s + kScaleAt) + (wp * FP * 16 + (lane & 15)) * 4 + (lane >> 4);
+            const int *cq = reinterpret_cast<const int *>(s + kScaleAt + BP * 16) + (wq * FQ * 16 + (lane & 15)) * 4 + (lane >> 4);
+            if (slice == 0) {
 #pragma unroll
-            for (int j = 0; j < FQ; j++) sqv[j] = sq[j * 64];
-            bool issued = false;
-            i4 qf[FQ][2];
+                for (int j = 0; j < FQ; j++) {
+                    sq[j] = cq[j * 64];
 #pragma unroll
-            for (int j = 0; j < FQ; j++)
+                    for (int h = 0; h < 2; h++) qf[h][j] = TQ::frag(t, wq * FQ * 16, j, h, lane);
+                }
+            }
 #pragma unroll
-                for (int h = 0; h < 2; h++) qf[j][h] = TQ::frag(s + TP::kBytes, wq * FQ * 16, j, h, lane);
+            for (int i = 0; i < kHalf; i++) {
+                sp[i] = cp[(slice * kHalf + i) * 64];
 #pragma unroll
-            for (int i = 0; i < FP; i++) {
-                const i4 lo = TP::frag(s, wp * FP * 16, i, 0, lane), hi = TP::frag(s, wp * FP * 16, i, 1, lane);
-                if (!issued) issue();
-                issued = true;
-#pragma unroll
-                for (int j = 0; j < FQ; j++) acc[i][j] = mfma_mx(lo, hi, sp[i * 64], qf[j][0], qf[j][1], sqv[j], acc[i][j]);
+                for (int h = 0; h < 2; h++) pf[h][i] = TP::frag(s, wp * FP * 16, slice * kHalf + i, h, lane);
             }
         } else {
 #pragma unroll
-            for (int kk = 0; kk < KK; kk++) {
-                if (kk) __builtin_amdgcn_sched_barrier(0);      // one slice's fragments in registers at a time
-                i4 pf[NL][FP], qf[NL][FQ];
+            for (int l = 0; l < NL; l++) {
 #pragma unroll
-                for (int l = 0; l < NL; l++) {
+                for (int i = 0; i < FP; i++) pf[l][i] = TP::frag(s + l * TP::kBytes, wp * FP * 16, i, slice, lane);
 #pragma unroll
-                    for (int i = 0; i < FP; i++) pf[l][i] = TP::frag(s + l * TP::kBytes, wp * FP * 16, i, kk, lane);
-#pragma unroll
-                    for (int j = 0; j < FQ; j++)
-                        qf[l][j] = TQ::frag(s + NL * TP::kBytes + l * TQ::kBytes, wq * FQ * 16, j, kk, lane);
-                }
-                if (kk == 0) issue();
-#pragma unroll
-                for (int order = NL - 1; order >= 0; order--)
-#pragma unroll
-                    for (int l = 0; l <= order; l++)
-#pragma unroll
-                        for (int i = 0; i < FP; i++)
-#pragma unroll
-                            for (int j = 0; j < FQ; j++)
-                                acc[i][j] = mfma32<KIND>(pf[l][i], qf[order - l][j], acc[i][j]);
+                for (int j = 0; j < FQ; j++) qf[l][j] = TQ::frag(t + l * TQ::kBytes, wq * FQ * 16, j, slice, lane);
             }
+        }
+    };
+    auto multiply = [&](int slice) {
+        if constexpr (MX) {
+#pragma unroll
+            for (int i = 0; i < kHalf; i++)
+#pragma unroll
+                for (int j = 0; j < FQ; j++)
+                    acc[slice * kHalf + i][j] = mfma_mx(pf[0][i], pf[1][i], sp[i], qf[0][j], qf[1][j], sq[j], acc[slice * kHalf + i][j]);
+        } else {
+#pragma unroll
+            for (int order = NL - 1; order >= 0; order--)
+#pragma unroll
+                for (int l = 0; l <= order; l++)
+#pragma unroll
+                    for (int i = 0; i < FP; i++)
+#pragma unroll
+                        for (int j = 0; j < FQ; j++) acc[i][j] = mfma32<KIND>(pf[l][i], qf[order - l][j], acc[i][j]);
         }
     };
 
@@ -410,6 +425,7 @@ __global__ __launch_bounds__(WP *WQ * 64, NL == 3 && BP == 128 ? 1 : 2) void pro
         dp.init(p0, a.Pl, a.ldp, tid);
         dq.init(q0, a.Ql, a.ldq, tid);
         if constexpr (KIND == kMX8) {
+            static_assert(BP * 4 % kThreads == 0 && BQ * 4 % kThreads == 0, "tile and block size");
             cp.init(p0, a.P, a.ldps, tid);
             cq.init(q0, a.Q, a.ldqs, tid);
         }
@@ -439,13 +455,47 @@ __global__ __launch_bounds__(WP *WQ * 64, NL == 3 && BP == 128 ? 1 : 2) void pro
         // later tiles' are outstanding leaves tile t complete; the barrier then
         // makes it so for every wave, and frees the stage of tile t - 1.  Every
         // tile counts the same loads: past the end they read zeros.
+        //
+        // PING: the block's two halves of waves (one wave of each on every SIMD)
+        // work half a slice apart, so that one half's LDS reads run beside the
+        // other's matrix instructions.  The 256 tile of 16-bit operands gains 1 to
+        // 5 per cent (1024 x 16384 x 4096 110.5 -> 108 us); with 128 tiles or 8-bit
+        // operands it made no difference and is left off.  A half
+        // reads a tile while the other half's pieces must already be there, so
+        // each waits for its own one phase early.
+        constexpr int kAhead = kLoadsPerTile * (NS - 2);
         auto turn_stage = [&](int t, char *now, char *next) {
-            stage_barrier<kLoadsPerTile *(NS - 2)>();
-            compute(now, [&] { issue(t + NS - 1, next); });
+            if constexpr (!PING) stage_barrier<kAhead>();
+#pragma unroll
+            for (int c = 0; c < kSlices; c++) {
+                if (!PING && c) __builtin_amdgcn_sched_barrier(0);      // one slice's fragments in registers at a time
+                fetch(now, c);
+                // the next tile's loads start once the first fragments are on
+                // their way: the wave's LDS reads do not queue behind them
+                if (c == 0) issue(t + NS - 1, next);
+                if constexpr (PING) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (c == kSlices - 1) stage_barrier<kAhead>();
+                    else slice_barrier();
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                multiply(c);
+                if constexpr (PING) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    __builtin_amdgcn_s_barrier();
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
         };
         char *const stage[4] = {lds0, lds1, lds2, lds3};
 #pragma unroll
         for (int t = 0; t < NS - 1; t++) issue(t, stage[t]);
+        const bool late = wave >= WP * WQ / 2;
+        if constexpr (PING) {
+            stage_barrier<kAhead>();
+            if (late) __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+        }
         int t = 0;
         for (; t + NS <= nt; t += NS)
 #pragma unroll
@@ -453,6 +503,7 @@ __global__ __launch_bounds__(WP *WQ * 64, NL == 3 && BP == 128 ? 1 : 2) void pro
         if (t < nt) turn_stage(t, stage[0], stage[NS - 1]);
         if (NS > 2 && t + 1 < nt) turn_stage(t + 1, stage[1], stage[0]);
         if (NS > 3 && t + 2 < nt) turn_stage(t + 2, stage[2], stage[1]);
+        if (PING && !late) __builtin_amdgcn_s_barrier();
     } else {
         Staged<TP, kThreads, PT, NL, KIND> sp;
         Staged<TQ, kThreads, QT, NL, KIND> sq;
@@ -469,7 +520,11 @@ __global__ __launch_bounds__(WP *WQ * 64, NL == 3 && BP == 128 ? 1 : 2) void pro
             sq.write(s + NL * TP::kBytes, tid);
             __syncthreads();                            // also: every wave is done with this stage's last use
             if (k0 + kStepK < kend) load(k0 + kStepK);
-            compute(s, [] {});
+#pragma unroll
+            for (int c = 0; c < kSlices; c++) {
+                fetch(s, c);
+                multiply(c);
+            }
         }
     }
 
@@ -493,7 +548,7 @@ __global__ __launch_bounds__(WP *WQ * 64, NL == 3 && BP == 128 ? 1 : 2) void pro
             }
         wave_fence();
         const int pb0 = p0 + (wp * FP + i0) * 16, qb0 = q0 + (wq * FQ + j) * 16;
-        const bool mirror = a.symmetric && tp != tq;
+        const bool mirror = EPI::kMirror && a.symmetric && tp != tq;
         if (EPI::vec(e)) {
 #pragma unroll 1
             for (int h = 0; h < 16; h += kRowsQ) {
@@ -503,10 +558,25 @@ __global__ __launch_bounds__(WP *WQ * 64, NL == 3 && BP == 128 ? 1 : 2) void pro
                 if (p + 8 <= a.P) {
                     float v[8];
                     load8_vec(turn + qr * kTurnLd + pr, v);
-                    EPI::store8(e, p, q, v, blockIdx.z, blockIdx.y, mirror);
+                    EPI::store8(e, p, q, v, blockIdx.z, split);
+                    if (mirror) store8_vec(turn + qr * kTurnLd + pr, v);
                 } else {
 #pragma unroll 1
-                    for (int i = 0; i < a.P - p; i++) EPI::store1(e, p + i, q, turn[qr * kTurnLd + pr + i], blockIdx.z, blockIdx.y);
+                    for (int i = 0; i < a.P - p; i++) EPI::store1(e, p + i, q, turn[qr * kTurnLd + pr + i], blockIdx.z, split);
+                }
+            }
+            if constexpr (EPI::kMirror) {
+                if (mirror) {               // the transposed tile: 8 q of a p to a lane
+                    wave_fence();
+#pragma unroll 1
+                    for (int x = lane; x < 32 * kPart; x += 64) {
+                        const int pr = x % (16 * kPart), qr = x / (16 * kPart) * 8;
+                        if (pb0 + pr >= a.P || qb0 + qr >= a.Q) continue;
+                        float v[8];
+#pragma unroll
+                        for (int i = 0; i < 8; i++) v[i] = turn[(qr + i) * kTurnLd + pr];
+                        EPI::store_mirror(e, qb0 + qr, pb0 + pr, v, blockIdx.z, split);
+                    }
                 }
             }
         } else {
@@ -514,7 +584,7 @@ __global__ __launch_bounds__(WP *WQ * 64, NL == 3 && BP == 128 ? 1 : 2) void pro
             for (int x = lane; x < 256 * kPart; x += 64) {
                 const int p = pb0 + x % (16 * kPart), q = qb0 + x / (16 * kPart);
                 if (p < a.P && q < a.Q)
-                    EPI::store1(e, p, q, turn[x / (16 * kPart) * kTurnLd + x % (16 * kPart)], blockIdx.z, blockIdx.y);
+                    EPI::store1(e, p, q, turn[x / (16 * kPart) * kTurnLd + x % (16 * kPart)], blockIdx.z, split);
             }
         }
         wave_fence();
@@ -532,7 +602,7 @@ inline bool direct_ok(const void *p, int es, int64_t ld, int64_t extent)
     return al16(p) && ld % per == 0 && extent % per == 0 && ld * es < (1 << 23);
 }
 
-template <int KIND, int NL, int NS, int BK, int BP, int BQ, int WP, int WQ, bool PT, bool QT, bool STAGED, class EPI>
+template <int KIND, int NL, int NS, int BK, int BP, int BQ, int WP, int WQ, bool PT, bool QT, bool STAGED, bool PING, class EPI>
 hipError_t launch(Args a, const typename EPI::Args &e, int splits, int batch, hipStream_t s)
 {
     constexpr int kStepK = KIND == kMX8 ? 2 * BK : BK;
@@ -543,7 +613,7 @@ hipError_t launch(Args a, const typename EPI::Args &e, int splits, int batch, hi
     a.k_split = per * kStepK;
     const int tiles = a.symmetric ? a.tiles_p * (a.tiles_p + 1) / 2 : a.tiles_p * a.tiles_q;
     const dim3 grid((unsigned)tiles, (unsigned)splits, (unsigned)batch);
-    product_kernel<KIND, NL, NS, BK, BP, BQ, WP, WQ, PT, QT, STAGED, EPI><<<grid, WP * WQ * 64, 0, s>>>(a, e);
+    product_kernel<KIND, NL, NS, BK, BP, BQ, WP, WQ, PT, QT, STAGED, PING, EPI><<<grid, WP * WQ * 64, 0, s>>>(a, e);
     return hipGetLastError();
 }
 

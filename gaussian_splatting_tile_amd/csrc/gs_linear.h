@@ -84,7 +84,9 @@ struct LinearEpilogue {
 
     __device__ static __forceinline__ bool vec(const Args &e) { return e.partial || e.vec; }
 
-    __device__ static __forceinline__ void store8(const Args &e, int p, int q, float v[8], int, int split, bool)
+    static constexpr bool kMirror = false;
+
+    __device__ static __forceinline__ void store8(const Args &e, int p, int q, float v[8], int, int split)
     {
         if (e.partial)                                          // rows of partial sums are padded to 8
             store8_vec(e.partial + split * e.split_stride + (int64_t)q * e.ld_partial + p, v);
@@ -115,6 +117,9 @@ hipError_t launch_sum_rows(const float *part, float *out, int n, int rows, int a
 hipError_t launch_product_bf16(const gemm::Args &a, const LinearEpilogue::Args &e, const ProductPlan &plan, hipStream_t s);
 hipError_t launch_product_f16(const gemm::Args &a, const LinearEpilogue::Args &e, const ProductPlan &plan, hipStream_t s);
 hipError_t launch_product_f32(const gemm::Args &a, const LinearEpilogue::Args &e, const ProductPlan &plan, hipStream_t s);
+// At most 64 rows of x, operands readable in 16-byte pieces (fp32: 8 values).
+constexpr int kFewRows = 64;
+hipError_t launch_few_rows(const gs_linear &l, const LinearEpilogue::Args &e, hipStream_t s);
 hipError_t launch_product_mx8(const gemm::Args &a, const LinearEpilogue::Args &e, const ProductPlan &plan, hipStream_t s);
 
 }  // namespace gsi

@@ -41,7 +41,7 @@ double product_cost(const TileRate &t, int64_t P, int64_t Q, int64_t K, int spli
     const double blocks = (double)((P + t.size - 1) / t.size) * (double)((Q + t.size - 1) / t.size) * splits;
     const double per_cu = ceil(blocks / 256.0);
     // fewer blocks than the CU holds leave some of its rate unused
-    const double filled = per_cu < t.resident ? 0.5 + 0.5 * per_cu / t.resident : 1.0;
+    const double filled = per_cu < t.resident ? 0.8 + 0.2 * per_cu / t.resident : 1.0;
     const double tile = 2e-6 * t.size * t.size * (ceil((double)K / splits) + 64.0) * work;
     double us = per_cu * tile / (t.mflop_us * filled);
     if (splits > 1) us += 4.0 + splits * (double)P * (double)Q * 8.0 / 4e6;
@@ -50,7 +50,7 @@ double product_cost(const TileRate &t, int64_t P, int64_t Q, int64_t K, int spli
 
 ProductPlan make_plan(int64_t P, int64_t Q, int64_t K, bool pt, bool qt, bool staged, bool f32, int step_k, float work)
 {
-    static const TileRate direct[3] = {{256, 1, 4.6f}, {128, 2, 4.1f}, {64, 3, 2.4f}};
+    static const TileRate direct[3] = {{256, 1, 4.7f}, {128, 2, 4.2f}, {64, 3, 2.4f}};
     static const TileRate limbs[3] = {{256, 1, 0.0f}, {128, 1, 4.1f}, {64, 2, 3.0f}};
     static const TileRate staged_[3] = {{256, 1, 0.0f}, {128, 1, 0.0f}, {64, 3, 1.2f}};
     ProductPlan best{pt, qt, staged, 2, 1};
@@ -167,7 +167,7 @@ size_t packed_bytes(int type, int64_t rows, int64_t cols)
 }
 
 // One product with its plan; everything but the workspace addresses.
-enum Way { kDirect, kPacked, kStaged };
+enum Way { kDirect, kPacked, kStaged, kFew };
 
 struct Product {
     gemm::Args a;
@@ -336,7 +336,14 @@ FwdPlan plan_fwd(const gs_linear &l)
     // of a sum than fp32 holds
     if (l.dtype == GS_DTYPE_MXFP8)
         p_ok = q_ok = p_ok && q_ok && l.y_dtype != GS_DTYPE_F32 && a.ldps < (1 << 22) && a.ldqs < (1 << 22);
+    const bool few = l.m <= kFewRows && (l.dtype == GS_DTYPE_F32 ? l.k % 8 == 0 && vec_ok(l.x, l.dtype, l.x_stride) && vec_ok(l.w, l.dtype, l.w_stride)
+                                                                 : p_ok && q_ok);
     finish_plan(r, p_ok, q_ok);
+    if (few) {
+        r.way = kFew;
+        r.pack_p = r.pack_q = false;
+        r.partial_bytes = 0;
+    }
     if (r.pack_p) {
         f.p_at = f.bytes;
         f.bytes += packed_bytes(l.dtype, a.P, l.k);
@@ -353,6 +360,7 @@ FwdPlan plan_fwd(const gs_linear &l)
 hipError_t run_fwd(const gs_linear &l, FwdPlan &f, char *ws, hipStream_t s)
 {
     Product &r = f.product;
+    if (r.way == kFew) return launch_few_rows(l, r.e, s);
     gemm::Args &a = r.a;
     PackJobs jobs;
     memset(&jobs, 0, sizeof jobs);

@@ -204,29 +204,21 @@ template <int NL> struct NsEpilogue {
         }
     }
 
-    __device__ static __forceinline__ void store8(const Args &e, int p, int q, float v[8], int batch, int split, bool mirror)
+    static constexpr bool kMirror = true;
+
+    __device__ static __forceinline__ void store8(const Args &e, int p, int q, float v[8], int batch, int split)
     {
         if (e.partial) {
             store8_vec(e.partial + ((int64_t)batch * e.splits + split) * e.split_stride + (int64_t)q * e.ld_partial + p, v);
             return;
         }
         combine(e, p, q, v, batch);
-        if (e.out) {
-            write_result(e, p, q, v, batch);
-            return;
-        }
-        write_limbs(e, p, q, v, batch);
-        if (mirror) {
-            // the transposed tile, 2 bytes at a time: a few per cent of a
-            // triangle's time, where forming it would double it
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                uint16_t limb[NL];
-                split_limbs<NL>(v[i], limb);
-#pragma unroll
-                for (int l = 0; l < NL; l++) e.o[batch * e.batch_o + l * e.plane_o + (int64_t)(p + i) * e.ldo + q] = limb[l];
-            }
-        }
+        if (e.out) write_result(e, p, q, v, batch);
+        else write_limbs(e, p, q, v, batch);
+    }
+    __device__ static __forceinline__ void store_mirror(const Args &e, int p, int q, const float v[8], int batch, int)
+    {
+        if (!e.partial) write_limbs(e, p, q, v, batch);
     }
     __device__ static __forceinline__ void store1(const Args &, int, int, float, int, int) {}  // never: 8 | P
 };
@@ -332,9 +324,9 @@ MuonPlan plan_muon(const gs_muon &m)
     return p;
 }
 
-// Estimated time in microseconds.  A 128 tile of 8 waves takes about 0.42 us
-// per 32 k with three products and twice that with six, a 64 tile 0.19 alone on
-// its CU and 0.10 (0.2) with others beside it; a split costs a launch and its
+// Estimated time in microseconds, from measured steps: a 128 tile of 8 waves
+// takes 0.66 us per 32 k with three products and 1.2 with six, a 64 tile 0.24
+// and 0.38, beside others on its CU as alone; a split costs a launch and its
 // sums' way to memory and back.
 NsProduct choose(int P, int Q, int K, int batch, bool symmetric, int nl)
 {
@@ -347,8 +339,8 @@ NsProduct choose(int P, int Q, int K, int batch, bool symmetric, int nl)
         for (int want = 1; want <= 8 && want <= nt; want++) {
             const int per = (nt + want - 1) / want, splits = (nt + per - 1) / per;
             const double rounds = ceil(tiles * splits / 256.0);
-            const double step = nl == 3 ? (tile == 128 ? 0.84 : rounds > 1 ? 0.2 : 0.26) : tile == 128 ? 0.42 : rounds > 1 ? 0.1 : 0.19;
-            double us = rounds * per * step + 2.0;
+            const double step = nl == 3 ? (tile == 128 ? 1.2 : 0.38) : tile == 128 ? 0.66 : 0.24;
+            double us = rounds * per * step + (tile == 128 ? 5.0 : 4.0);
             if (splits > 1) us += 5.0 + tiles * splits * tile * tile * 8.0 / 6e6;
             if (us < least * 0.97) {
                 least = us;
@@ -370,8 +362,8 @@ hipError_t launch_product(gemm::Args a, typename NsEpilogue<NL>::Args e, float *
     e.partial = c.splits > 1 ? partial : nullptr;
     e.ld_partial = a.P;
     e.split_stride = (int64_t)a.P * a.Q;
-    hipError_t err = c.tile == 128 ? gemm::launch<gemm::kBF16, NL, NL == 3 ? 2 : 3, 32, 128, 128, 2, 4, PT, false, false, E>(a, e, c.splits, batch, s)
-                                   : gemm::launch<gemm::kBF16, NL, 3, 32, 64, 64, 2, 2, PT, false, false, E>(a, e, c.splits, batch, s);
+    hipError_t err = c.tile == 128 ? gemm::launch<gemm::kBF16, NL, 3, 32, 128, 128, 2, 4, PT, false, false, false, E>(a, e, c.splits, batch, s)
+                                   : gemm::launch<gemm::kBF16, NL, 3, 32, 64, 64, 2, 2, PT, false, false, false, E>(a, e, c.splits, batch, s);
     if (err != hipSuccess || c.splits == 1) return err;
     const int tp = (a.P + 63) / 64, tq = (a.Q + 63) / 64;
     reduce_splits<NL><<<dim3((unsigned)(symmetric ? tp * (tp + 1) / 2 : tp * tq), (unsigned)batch), kThreads, 0, s>>>(e, a.P, a.Q, symmetric);

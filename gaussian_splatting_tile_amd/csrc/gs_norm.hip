@@ -226,7 +226,7 @@ struct GradArgs {
 
 // Each workgroup strides over the rows; a thread keeps the dgamma sums of its
 // columns in registers and the workgroup writes one partial row at the end.
-template <typename T, int LANES, int V> __global__ __launch_bounds__(kThreads) void grad_rows(GradArgs a)
+template <typename T, int LANES, int V, bool AHEAD> __global__ __launch_bounds__(kThreads) void grad_rows(GradArgs a)
 {
     constexpr int kRows = kThreads / LANES;
     __shared__ float lds[kThreads / 64];
@@ -237,14 +237,45 @@ template <typename T, int LANES, int V> __global__ __launch_bounds__(kThreads) v
     for (int k = 0; k < V; k++)
 #pragma unroll
         for (int j = 0; j < 8; j++) dg[k][j] = 0.0f;
-    for (int64_t row = (int64_t)blockIdx.x * kRows + sub; row < a.m; row += (int64_t)gridDim.x * kRows) {
-        const float rstd = a.rstd[row];
-        float h[V][8], g[V][8], dot = 0.0f;
+    // AHEAD (whole chunks, aligned): the next row's sum and dy are on their way,
+    // unconverted, while a row is worked on
+    Vec<T, 8> nh[V], ng[V];
+    auto fetch = [&](int64_t row) {
+        if (row >= a.m) return;
 #pragma unroll
         for (int k = 0; k < V; k++) {
-            const int c = (k * LANES + lane) * 8, valid = max(0, min(8, a.n - c));
-            load_chunk(static_cast<const T *>(a.sum), row * a.lds + c, valid, a.vec, h[k]);
-            load_chunk(static_cast<const T *>(a.dy), row * a.ldy + c, valid, a.vec, g[k]);
+            const int c = (k * LANES + lane) * 8;
+            if (c >= a.n) continue;
+            nh[k] = *reinterpret_cast<const Vec<T, 8> *>(static_cast<const T *>(a.sum) + row * a.lds + c);
+            ng[k] = *reinterpret_cast<const Vec<T, 8> *>(static_cast<const T *>(a.dy) + row * a.ldy + c);
+        }
+    };
+    const int64_t step = (int64_t)gridDim.x * kRows;
+    int64_t row = (int64_t)blockIdx.x * kRows + sub;
+    if constexpr (AHEAD) {
+#pragma unroll
+        for (int k = 0; k < V; k++) nh[k] = ng[k] = Vec<T, 8>{};
+        fetch(row);
+    }
+    for (; row < a.m; row += step) {
+        const float rstd = a.rstd[row];
+        float h[V][8], g[V][8], dot = 0.0f;
+        if constexpr (AHEAD) {
+#pragma unroll
+            for (int k = 0; k < V; k++)
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    h[k][j] = (float)nh[k].v[j];
+                    g[k][j] = (float)ng[k].v[j];
+                }
+            fetch(row + step);
+        } else {
+#pragma unroll
+            for (int k = 0; k < V; k++) {
+                const int c = (k * LANES + lane) * 8, valid = max(0, min(8, a.n - c));
+                load_chunk(static_cast<const T *>(a.sum), row * a.lds + c, valid, a.vec, h[k]);
+                load_chunk(static_cast<const T *>(a.dy), row * a.ldy + c, valid, a.vec, g[k]);
+            }
         }
 #pragma unroll
         for (int k = 0; k < V; k++) {
@@ -380,17 +411,24 @@ int grad_blocks(int64_t m, int n)
 {
     if (n > kMaxRegRow) return (int)(m < 64 ? m : 64);
     const int64_t rows = n <= 2048 ? 4 : 1, want = (m + rows - 1) / rows;
-    return (int)(want < 512 ? want : 512);
+    return (int)(want < 1024 ? want : 1024);
+}
+
+template <typename T, int LANES, int V> void launch_rows(const GradArgs &a, unsigned blocks, bool ahead, hipStream_t s)
+{
+    if (ahead) grad_rows<T, LANES, V, true><<<blocks, kThreads, 0, s>>>(a);
+    else grad_rows<T, LANES, V, false><<<blocks, kThreads, 0, s>>>(a);
 }
 
 template <typename T> hipError_t launch_grad(const GradArgs &a, hipStream_t s)
 {
     const unsigned g = (unsigned)grad_blocks(a.m, a.n);
-    if (a.n <= 512) grad_rows<T, 64, 1><<<g, kThreads, 0, s>>>(a);
-    else if (a.n <= 1024) grad_rows<T, 64, 2><<<g, kThreads, 0, s>>>(a);
-    else if (a.n <= 2048) grad_rows<T, 64, 4><<<g, kThreads, 0, s>>>(a);
-    else if (a.n <= 4096) grad_rows<T, 256, 2><<<g, kThreads, 0, s>>>(a);
-    else if (a.n <= kMaxRegRow) grad_rows<T, 256, 4><<<g, kThreads, 0, s>>>(a);
+    const bool ahead = a.vec && a.n % 8 == 0;
+    if (a.n <= 512) launch_rows<T, 64, 1>(a, g, ahead, s);
+    else if (a.n <= 1024) launch_rows<T, 64, 2>(a, g, ahead, s);
+    else if (a.n <= 2048) launch_rows<T, 64, 4>(a, g, ahead, s);
+    else if (a.n <= 4096) launch_rows<T, 256, 2>(a, g, ahead, s);
+    else if (a.n <= kMaxRegRow) launch_rows<T, 256, 4>(a, g, ahead, s);
     else {
         // dgamma first: dx may be written over dy
         if (a.part) dgamma_long<T><<<dim3((unsigned)((a.n + 2047) / 2048), g), kThreads, 0, s>>>(a);
