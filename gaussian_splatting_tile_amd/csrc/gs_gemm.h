@@ -265,9 +265,10 @@ template <class TL, int THREADS, bool T, int NL, int KIND> struct Staged {
 
 // Which tile and split of k a block takes.  Blocks go to the 8 dies in turn, so
 // block b of nb becomes the (b % 8)-th die's next item of a contiguous eighth of
-// the list of splits and, within each, tiles: a die's blocks share operands in
-// its L2 (with splits, only a range of k of them; 1024 x 1024 x 4096 in 7 splits
-// took 28.8 us where every die read all k).
+// the list of matrices of a batch, splits and tiles: a die's blocks share
+// operands in its L2 (with splits, only a range of k of them: half a 1024 x
+// 1024 x 4096 product of two limbs in 7 splits takes 19.5 us, 28.8 us where every
+// die read all k).
 __device__ __forceinline__ int die_order(int b, int nb)
 {
     const int die = b & 7, at = b >> 3, per = nb >> 3, more = nb & 7;
@@ -345,8 +346,9 @@ __global__ __launch_bounds__(WP *WQ * 64, NL == 3 && BP == 128 ? 1 : 2) void pro
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wp = wave / WQ, wq = wave % WQ;
     int tp, tq;
-    const int item = die_order(blockIdx.y * gridDim.x + blockIdx.x, gridDim.x * gridDim.y);
-    const int split = item / gridDim.x, tile = item - split * gridDim.x;
+    const int per_matrix = gridDim.x * gridDim.y;
+    const int item = die_order(blockIdx.z * per_matrix + blockIdx.y * gridDim.x + blockIdx.x, per_matrix * gridDim.z);
+    const int batch = item / per_matrix, split = item % per_matrix / gridDim.x, tile = item % gridDim.x;
     if (a.symmetric)
         triangle_of(tile, tp, tq);
     else
@@ -416,8 +418,8 @@ __global__ __launch_bounds__(WP *WQ * 64, NL == 3 && BP == 128 ? 1 : 2) void pro
     };
 
     if constexpr (!STAGED) {
-        pb += (int64_t)blockIdx.z * a.batch_p * ES;
-        qb += (int64_t)blockIdx.z * a.batch_q * ES;
+        pb += (int64_t)batch * a.batch_p * ES;
+        qb += (int64_t)batch * a.batch_q * ES;
         Direct<TP, kThreads, PT, ES> dp;
         Direct<TQ, kThreads, QT, ES> dq;
         Scales<BP, kThreads> cp;
@@ -507,8 +509,8 @@ __global__ __launch_bounds__(WP *WQ * 64, NL == 3 && BP == 128 ? 1 : 2) void pro
     } else {
         Staged<TP, kThreads, PT, NL, KIND> sp;
         Staged<TQ, kThreads, QT, NL, KIND> sq;
-        pb += (int64_t)blockIdx.z * a.batch_p * dtype_bytes(a.p_type);
-        qb += (int64_t)blockIdx.z * a.batch_q * dtype_bytes(a.q_type);
+        pb += (int64_t)batch * a.batch_p * dtype_bytes(a.p_type);
+        qb += (int64_t)batch * a.batch_q * dtype_bytes(a.q_type);
         auto load = [&](int k0) {
             sp.load(pb, a.p_type, a.p_vec, a.ps, a.ldps, p0, a.P, a.ldp, k0, kend, tid);
             sq.load(qb, a.q_type, a.q_vec, a.qs, a.ldqs, q0, a.Q, a.ldq, k0, kend, tid);
@@ -558,11 +560,11 @@ __global__ __launch_bounds__(WP *WQ * 64, NL == 3 && BP == 128 ? 1 : 2) void pro
                 if (p + 8 <= a.P) {
                     float v[8];
                     load8_vec(turn + qr * kTurnLd + pr, v);
-                    EPI::store8(e, p, q, v, blockIdx.z, split);
+                    EPI::store8(e, p, q, v, batch, split);
                     if (mirror) store8_vec(turn + qr * kTurnLd + pr, v);
                 } else {
 #pragma unroll 1
-                    for (int i = 0; i < a.P - p; i++) EPI::store1(e, p + i, q, turn[qr * kTurnLd + pr + i], blockIdx.z, split);
+                    for (int i = 0; i < a.P - p; i++) EPI::store1(e, p + i, q, turn[qr * kTurnLd + pr + i], batch, split);
                 }
             }
             if constexpr (EPI::kMirror) {
@@ -575,7 +577,7 @@ __global__ __launch_bounds__(WP *WQ * 64, NL == 3 && BP == 128 ? 1 : 2) void pro
                         float v[8];
 #pragma unroll
                         for (int i = 0; i < 8; i++) v[i] = turn[(qr + i) * kTurnLd + pr];
-                        EPI::store_mirror(e, qb0 + qr, pb0 + pr, v, blockIdx.z, split);
+                        EPI::store_mirror(e, qb0 + qr, pb0 + pr, v, batch, split);
                     }
                 }
             }
@@ -584,7 +586,7 @@ __global__ __launch_bounds__(WP *WQ * 64, NL == 3 && BP == 128 ? 1 : 2) void pro
             for (int x = lane; x < 256 * kPart; x += 64) {
                 const int p = pb0 + x % (16 * kPart), q = qb0 + x / (16 * kPart);
                 if (p < a.P && q < a.Q)
-                    EPI::store1(e, p, q, turn[x / (16 * kPart) * kTurnLd + x % (16 * kPart)], blockIdx.z, split);
+                    EPI::store1(e, p, q, turn[x / (16 * kPart) * kTurnLd + x % (16 * kPart)], batch, split);
             }
         }
         wave_fence();

@@ -179,6 +179,8 @@ struct Product {
     size_t partial_bytes;
 };
 
+bool exact_results(const LinearEpilogue::Args &e) { return e.y_type == GS_DTYPE_F32 || (e.z && e.z_type == GS_DTYPE_F32); }
+
 // The way of a product whose operands can (p_ok, q_ok) or cannot be loaded
 // directly, then its tile and splits.
 void finish_plan(Product &r, bool p_ok, bool q_ok)
@@ -201,7 +203,7 @@ void finish_plan(Product &r, bool p_ok, bool q_ok)
     r.e.vec = (r.e.bias_on_q || al16(r.e.bias)) && vec_ok(r.e.y, r.e.y_type, r.e.ldy) &&
               (!r.e.residual || vec_ok(r.e.residual, r.e.y_type, r.e.ldr)) &&
               (!r.e.z || r.e.z_p != 1 || vec_ok(r.e.z, r.e.z_type, r.e.z_q));
-    r.e.exact = r.e.y_type == GS_DTYPE_F32 || (r.e.z && r.e.z_type == GS_DTYPE_F32);
+    r.e.exact = exact_results(r.e);
 }
 
 // Points an operand at its packed planes.
@@ -338,12 +340,12 @@ FwdPlan plan_fwd(const gs_linear &l)
         p_ok = q_ok = p_ok && q_ok && l.y_dtype != GS_DTYPE_F32 && a.ldps < (1 << 22) && a.ldqs < (1 << 22);
     const bool few = l.m <= kFewRows && (l.dtype == GS_DTYPE_F32 ? l.k % 8 == 0 && vec_ok(l.x, l.dtype, l.x_stride) && vec_ok(l.w, l.dtype, l.w_stride)
                                                                  : p_ok && q_ok);
-    finish_plan(r, p_ok, q_ok);
     if (few) {
-        r.way = kFew;
-        r.pack_p = r.pack_q = false;
-        r.partial_bytes = 0;
+        r.way = kFew;                           // one value at a time: no tile, split or vector rule
+        r.e.exact = exact_results(r.e);
+        return f;
     }
+    finish_plan(r, p_ok, q_ok);
     if (r.pack_p) {
         f.p_at = f.bytes;
         f.bytes += packed_bytes(l.dtype, a.P, l.k);

@@ -88,14 +88,19 @@ template <int KIND, int NL, int FQ> __global__ __launch_bounds__(kThreads) void 
     f4 acc[FQ];
 #pragma unroll
     for (int j = 0; j < FQ; j++) acc[j] = f4{0, 0, 0, 0};
-#pragma unroll 4
-    for (int k0 = wave * kStep; k0 < a.k; k0 += kWaves * kStep) {
-        Piece<KIND, NL> w, x;
-        load_piece(w, a.w, a.ldw, a.ws, a.ldws, row, k0, a.k, g);
+    constexpr int kAtOnce = NL == 1 ? 4 : 1;    // pieces of weights on their way together
+    for (int k0 = wave * kStep; k0 < a.k; k0 += kAtOnce * kWaves * kStep) {
+        Piece<KIND, NL> w[kAtOnce];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; u++) load_piece(w[u], a.w, a.ldw, a.ws, a.ldws, row, k0 + u * kWaves * kStep, a.k, g);
 #pragma unroll
         for (int j = 0; j < FQ; j++) {
-            load_piece(x, a.x, a.ldx, a.xs, a.ldxs, min(j * 16 + r, a.m - 1), k0, a.k, g);
-            acc[j] = product(w, x, acc[j]);
+            Piece<KIND, NL> x[kAtOnce];
+#pragma unroll
+            for (int u = 0; u < kAtOnce; u++)
+                load_piece(x[u], a.x, a.ldx, a.xs, a.ldxs, min(j * 16 + r, a.m - 1), k0 + u * kWaves * kStep, a.k, g);
+#pragma unroll
+            for (int u = 0; u < kAtOnce; u++) acc[j] = product(w[u], x[u], acc[j]);
         }
     }
 #pragma unroll
