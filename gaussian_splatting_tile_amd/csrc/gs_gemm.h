@@ -318,12 +318,16 @@ constexpr int turn_part(int fp, int waves, int bytes)
     return fp;
 }
 
+// Waves on a SIMD that the register budget has to leave room for: of two blocks
+// where the LDS holds two.
+constexpr int waves_per_simd(int waves, int lds) { return (2 * lds <= 160 * 1024 ? 2 : 1) * waves / 4; }
+
 // The epilogue takes 8 sums of consecutive p at a time where EPI::vec(e) allows,
 // EPI::store8(e, p, q, v, batch, split), which leaves the final values in v,
 // else single ones, EPI::store1.  A tile that also stands for its transpose
 // (EPI::kMirror) hands those on to EPI::store_mirror.
 template <int KIND, int NL, int NS, int BK, int BP, int BQ, int WP, int WQ, bool PT, bool QT, bool STAGED, bool PING, class EPI>
-__global__ __launch_bounds__(WP *WQ * 64, NL == 3 && BP == 128 ? 1 : 2) void product_kernel(Args a, typename EPI::Args e)
+__global__ __launch_bounds__(WP *WQ * 64, waves_per_simd(WP * WQ, NS * NL * (BP + BQ) * BK * 2)) void product_kernel(Args a, typename EPI::Args e)
 {
     constexpr int kThreads = WP * WQ * 64;
     constexpr int FP = BP / WP / 16, FQ = BQ / WQ / 16, KK = BK / 32;

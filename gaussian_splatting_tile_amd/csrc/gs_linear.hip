@@ -392,6 +392,22 @@ struct DzArgs {
     int vec;
 };
 
+// A block's sums of its columns over its row lanes, in order, to its partial row.
+__device__ __forceinline__ void column_sums(const DzArgs &d, int groups, const float acc[8], float (*sums)[8])
+{
+    if (!d.part) return;
+    const int lanes = kThreads / groups;
+#pragma unroll
+    for (int i = 0; i < 8; i++) sums[threadIdx.x][i] = acc[i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < groups * 8; i += kThreads) {
+        const int c = blockIdx.x * groups * 8 + i;
+        float s = 0.0f;
+        for (int l = 0; l < lanes; l++) s += sums[l * groups + i / 8][i % 8];
+        if (c < d.n) d.part[(int64_t)blockIdx.y * d.n + c] = s;
+    }
+}
+
 // dy in rows.  A block takes `rows_per_block` rows of up to 512 columns: a
 // thread owns 8 columns and every (256 / groups)-th row.
 __global__ __launch_bounds__(kThreads) void dz_rows(DzArgs d, int groups)
@@ -416,16 +432,43 @@ __global__ __launch_bounds__(kThreads) void dz_rows(DzArgs d, int groups)
         if (room && d.dz) store8_vec(d.dz, d.type, r * d.ld_dz + c0, v);
         if (room && d.limbs) store_planes(d.limbs, d.m * d.ld_dz, r * d.ld_dz + c0, 3, 0, v);
     }
-    if (!d.part) return;
+    column_sums(d, groups, acc, sums);
+}
+
+// The same where dy, z and dz are of one 16-bit type in whole, aligned chunks of
+// 8: the next row is on its way, unconverted, while a row is worked on
+// (16384 x 4096 with GELU in bf16: 79 us, 5.1 TB/s; 103 us without).
+template <typename T> __global__ __launch_bounds__(kThreads) void dz_rows_ahead(DzArgs d, int groups)
+{
+    __shared__ float sums[kThreads][8];
+    using Row = Vec<T, 8>;
+    const int cg = threadIdx.x % groups, rl = threadIdx.x / groups, lanes = kThreads / groups;
+    const int c0 = (blockIdx.x * groups + cg) * 8;
+    const int64_t r0 = (int64_t)blockIdx.y * d.rows_per_block, r1 = min(d.m, r0 + d.rows_per_block);
+    const T *dy = static_cast<const T *>(d.dy) + c0, *z = static_cast<const T *>(d.z) + c0;
+    T *dz = static_cast<T *>(d.dz) + c0;
+    float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    Row ny{}, nz{};
+    auto fetch = [&](int64_t r) {
+        if (r >= r1 || c0 >= d.n) return;
+        ny = *reinterpret_cast<const Row *>(dy + r * d.lddy);
+        nz = *reinterpret_cast<const Row *>(z + r * d.ldz);
+    };
+    fetch(r0 + rl);
+    for (int64_t r = r0 + rl; r < r1; r += lanes) {
+        float v[8], w[8];
 #pragma unroll
-    for (int i = 0; i < 8; i++) sums[threadIdx.x][i] = acc[i];
-    __syncthreads();
-    for (int i = threadIdx.x; i < groups * 8; i += kThreads) {
-        const int c = blockIdx.x * groups * 8 + i;
-        float s = 0.0f;
-        for (int l = 0; l < lanes; l++) s += sums[l * groups + i / 8][i % 8];
-        if (c < d.n) d.part[(int64_t)blockIdx.y * d.n + c] = s;
+        for (int i = 0; i < 8; i++) {
+            v[i] = (float)ny.v[i];
+            w[i] = (float)nz.v[i];
+        }
+        fetch(r + lanes);
+        scale_by_slope<8, false>(v, w, d.act);
+#pragma unroll
+        for (int i = 0; i < 8; i++) acc[i] += v[i];
+        if (c0 < d.n) store8_vec(dz + r * d.ld_dz, v);
     }
+    column_sums(d, groups, acc, sums);
 }
 
 // dy in planes [n][m]: tiles of 64 columns x 64 rows turned round in LDS.
@@ -446,6 +489,7 @@ __global__ __launch_bounds__(kThreads) void dz_planes(DzArgs d)
 #pragma unroll
         for (int k = 0; k < 16; k++) tile[ty + 4 * k][tx] = in[k];
         __syncthreads();
+#pragma unroll 4
         for (int i = ty; i < 64 && r + i < r1; i += 4) {
             float v = tile[tx][i];
             if (d.act != GS_ACT_NONE && c < d.n) {
@@ -611,7 +655,11 @@ hipError_t run_bwd(const gs_linear &l, const gs_linear_grads &g, BwdPlan &b, cha
         } else {
             int groups = 1;                     // of 8 columns: a power of two, at most 64
             while (groups < 64 && groups * 8 < l.n) groups *= 2;
-            dz_rows<<<dim3((unsigned)((l.n + groups * 8 - 1) / (groups * 8)), (unsigned)b.row_blocks), kThreads, 0, s>>>(d, groups);
+            const dim3 grid((unsigned)((l.n + groups * 8 - 1) / (groups * 8)), (unsigned)b.row_blocks);
+            const bool ahead = d.dz && !d.limbs && d.vec && l.n % 8 == 0 && l.activation != GS_ACT_NONE && l.y_dtype == l.dtype;
+            if (ahead && l.dtype == GS_DTYPE_BF16) dz_rows_ahead<__bf16><<<grid, kThreads, 0, s>>>(d, groups);
+            else if (ahead && l.dtype == GS_DTYPE_F16) dz_rows_ahead<_Float16><<<grid, kThreads, 0, s>>>(d, groups);
+            else dz_rows<<<grid, kThreads, 0, s>>>(d, groups);
         }
         if ((err = hipGetLastError()) != hipSuccess) return err;
         if (g.db) {
