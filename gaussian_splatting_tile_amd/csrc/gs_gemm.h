@@ -311,11 +311,17 @@ __device__ __forceinline__ void wave_fence()
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// Fragments along p that the waves can turn at once within `bytes` of LDS.
+// Fragments along p that the waves turn at once within `bytes` of LDS, [16 q][16
+// p each]; the 16-byte chunks of row q at c ^ (q & 7), so that neither the
+// writes (16 rows of a chunk) nor the reads (a row) meet in a bank.
 constexpr int turn_part(int fp, int waves, int bytes)
 {
-    while (fp > 1 && waves * 16 * (fp * 16 + 4) * 4 > bytes) fp /= 2;
+    while (fp > 1 && waves * 16 * fp * 16 * 4 > bytes) fp /= 2;
     return fp;
+}
+template <int PART> __device__ __forceinline__ int turn_at(int q, int p)
+{
+    return q * (PART * 16) + (((p >> 2) ^ (q & 7 & (PART * 4 - 1))) << 2) + (p & 3);
 }
 
 // Waves on a SIMD that the register budget has to leave room for: of two blocks
@@ -323,8 +329,9 @@ constexpr int turn_part(int fp, int waves, int bytes)
 constexpr int waves_per_simd(int waves, int lds) { return (2 * lds <= 160 * 1024 ? 2 : 1) * waves / 4; }
 
 // The epilogue takes 8 sums of consecutive p at a time where EPI::vec(e) allows,
-// EPI::store8(e, p, q, v, batch, split), which leaves the final values in v,
-// else single ones, EPI::store1.  A tile that also stands for its transpose
+// EPI::store8(e, p, q, v, part, ahead, batch, split), which leaves the final
+// values in v and finds in `part` and `ahead` what EPI::part(e, p, ..) and
+// EPI::look_ahead(e, p, q, ..) loaded for it, else single ones, EPI::store1.  A tile that also stands for its transpose
 // (EPI::kMirror) hands those on to EPI::store_mirror.
 template <int KIND, int NL, int NS, int BK, int BP, int BQ, int WP, int WQ, bool PT, bool QT, bool STAGED, bool PING, class EPI>
 __global__ __launch_bounds__(WP *WQ * 64, waves_per_simd(WP * WQ, NS * NL * (BP + BQ) * BK * 2)) void product_kernel(Args a, typename EPI::Args e)
@@ -341,7 +348,7 @@ __global__ __launch_bounds__(WP *WQ * 64, waves_per_simd(WP * WQ, NS * NL * (BP 
     constexpr int kStage = kScaleAt + (KIND == kMX8 ? (BP + BQ) * 16 : 0);
     // after the last product each wave turns its sums round in a stage's place,
     // 16 q by as many p as fit there at a time
-    constexpr int kPart = turn_part(FP, WP * WQ, kStage), kTurnLd = kPart * 16 + 4;
+    constexpr int kPart = turn_part(FP, WP * WQ, kStage);
     __shared__ __align__(128) char lds0[kStage];
     __shared__ __align__(128) char lds1[kStage];
     __shared__ __align__(128) char lds2[NS > 2 ? kStage : 16];
@@ -537,38 +544,58 @@ __global__ __launch_bounds__(WP *WQ * 64, waves_per_simd(WP * WQ, NS * NL * (BP 
     // sums to the epilogue, 8 consecutive p at a time; a lane's accumulator holds
     // p = 16 i + 4 g + (0..3) at q = 16 j + r
     stage_barrier<0>();
-    float *turn = reinterpret_cast<float *>(lds0) + wave * (16 * kTurnLd);
+    float *turn = reinterpret_cast<float *>(lds0) + wave * (256 * kPart);
     constexpr int kLanesP = kPart * 2, kRowsQ = 64 / kLanesP;   // lanes along p, q rows at a time
-    constexpr int kParts = FQ * (FP / kPart);
+    constexpr int kParts = FQ * (FP / kPart), kIts = kRowsQ < 16 ? 16 / kRowsQ : 1;
+    const bool mirror = EPI::kMirror && a.symmetric && tp != tq, vec = EPI::vec(e);
+    // what the epilogue reads for a part is on its way while its sums turn
+    typename EPI::Ahead ahead[kIts];
+    auto part_p = [&](int u) { return p0 + (wp * FP + u % (FP / kPart) * kPart) * 16; };
+    auto part_q = [&](int u) { return q0 + (wq * FQ + u / (FP / kPart)) * 16; };
+    auto look_ahead = [&](int u) {
+#pragma unroll
+        for (int it = 0; it < kIts; it++) {
+            const int qr = it * kRowsQ + lane / kLanesP, p = part_p(u) + lane % kLanesP * 8, q = part_q(u) + qr;
+            if (qr < 16 && q < a.Q && p + 8 <= a.P) EPI::look_ahead(e, p, q, batch, ahead[it]);
+        }
+    };
 #pragma unroll 1
     for (int u = 0; u < kParts; u++) {
-        const int j = u / (FP / kPart), i0 = u % (FP / kPart) * kPart;
+        typename EPI::Part part;
+        if (vec) {
+            look_ahead(u);
+            const int p = part_p(u) + lane % kLanesP * 8;
+            if (p + 8 <= a.P) EPI::part(e, p, part);
+        }
         // accumulators have no run-time index: one of kParts branches
 #pragma unroll
         for (int c = 0; c < kParts; c++)
             if (u == c) {
 #pragma unroll
                 for (int i = 0; i < kPart; i++)
-                    *reinterpret_cast<f4 *>(turn + (lane & 15) * kTurnLd + i * 16 + (lane >> 4) * 4) =
+                    *reinterpret_cast<f4 *>(turn + turn_at<kPart>(lane & 15, i * 16 + (lane >> 4) * 4)) =
                         acc[c % (FP / kPart) * kPart + i][c / (FP / kPart)];
             }
         wave_fence();
-        const int pb0 = p0 + (wp * FP + i0) * 16, qb0 = q0 + (wq * FQ + j) * 16;
-        const bool mirror = EPI::kMirror && a.symmetric && tp != tq;
-        if (EPI::vec(e)) {
-#pragma unroll 1
-            for (int h = 0; h < 16; h += kRowsQ) {
-                const int qr = h + lane / kLanesP, pr = lane % kLanesP * 8;
+        const int pb0 = part_p(u), qb0 = part_q(u);
+        if (vec) {
+#pragma unroll
+            for (int it = 0; it < kIts; it++) {
+                const int qr = it * kRowsQ + lane / kLanesP, pr = lane % kLanesP * 8;
                 const int p = pb0 + pr, q = qb0 + qr;
                 if (qr >= 16 || q >= a.Q) continue;     // two lanes a row would reach 32 rows
                 if (p + 8 <= a.P) {
-                    float v[8];
-                    load8_vec(turn + qr * kTurnLd + pr, v);
-                    EPI::store8(e, p, q, v, batch, split);
-                    if (mirror) store8_vec(turn + qr * kTurnLd + pr, v);
+                    f4 *const lo = reinterpret_cast<f4 *>(turn + turn_at<kPart>(qr, pr));
+                    f4 *const hi = reinterpret_cast<f4 *>(turn + turn_at<kPart>(qr, pr + 4));
+                    float v[8] = {(*lo)[0], (*lo)[1], (*lo)[2], (*lo)[3], (*hi)[0], (*hi)[1], (*hi)[2], (*hi)[3]};
+                    EPI::store8(e, p, q, v, part, ahead[it], batch, split);
+                    if (mirror) {
+                        *lo = f4{v[0], v[1], v[2], v[3]};
+                        *hi = f4{v[4], v[5], v[6], v[7]};
+                    }
                 } else {
 #pragma unroll 1
-                    for (int i = 0; i < a.P - p; i++) EPI::store1(e, p + i, q, turn[qr * kTurnLd + pr + i], batch, split);
+                    for (int i = 0; i < a.P - p; i++) EPI::store1(e, p + i, q, turn[turn_at<kPart>(qr, pr + i)], batch, split);
                 }
             }
             if constexpr (EPI::kMirror) {
@@ -580,7 +607,7 @@ __global__ __launch_bounds__(WP *WQ * 64, waves_per_simd(WP * WQ, NS * NL * (BP 
                         if (pb0 + pr >= a.P || qb0 + qr >= a.Q) continue;
                         float v[8];
 #pragma unroll
-                        for (int i = 0; i < 8; i++) v[i] = turn[(qr + i) * kTurnLd + pr];
+                        for (int i = 0; i < 8; i++) v[i] = turn[turn_at<kPart>(qr + i, pr)];
                         EPI::store_mirror(e, qb0 + qr, pb0 + pr, v, batch, split);
                     }
                 }
@@ -590,7 +617,7 @@ __global__ __launch_bounds__(WP *WQ * 64, waves_per_simd(WP * WQ, NS * NL * (BP 
             for (int x = lane; x < 256 * kPart; x += 64) {
                 const int p = pb0 + x % (16 * kPart), q = qb0 + x / (16 * kPart);
                 if (p < a.P && q < a.Q)
-                    EPI::store1(e, p, q, turn[x / (16 * kPart) * kTurnLd + x % (16 * kPart)], batch, split);
+                    EPI::store1(e, p, q, turn[turn_at<kPart>(x / (16 * kPart), x % (16 * kPart))], batch, split);
             }
         }
         wave_fence();

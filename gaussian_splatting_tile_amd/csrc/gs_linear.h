@@ -26,7 +26,8 @@ struct LinearEpilogue {
         void *z;                        // element q * z_q + p * z_p
         int64_t z_q, z_p;
         int z_type;
-        int vec;                        // 8 consecutive p may be read and written as vectors
+        int vec;                        // 8 consecutive p may be read and written as vectors (and no exact silu or gelu:
+                                        // eight library erfs at once take more registers than the rest of a kernel)
     };
 
     // One value, any layout.
@@ -42,8 +43,23 @@ struct LinearEpilogue {
         store_from_float(e.y, e.y_type, at, v);
     }
 
+    struct Part { gemm::f4 bias[2]; };              // of eight p
+    struct Ahead { gemm::i4 residual; };            // of eight values of a 16-bit type, unconverted
+
+    __device__ static __forceinline__ void part(const Args &e, int p, Part &b)
+    {
+        if (e.partial || !e.bias || e.bias_on_q) return;
+        b.bias[0] = *reinterpret_cast<const gemm::f4 *>(e.bias + p);
+        b.bias[1] = *reinterpret_cast<const gemm::f4 *>(e.bias + p + 4);
+    }
+    __device__ static __forceinline__ void look_ahead(const Args &e, int p, int q, int, Ahead &a)
+    {
+        if (!e.partial && e.residual && e.y_type != GS_DTYPE_F32)
+            a.residual = *reinterpret_cast<const gemm::i4 *>(static_cast<const uint16_t *>(e.residual) + (int64_t)q * e.ldr + p);
+    }
+
     // Eight values p .. p + 7, vec set.
-    __device__ static __forceinline__ void finish8(const Args &e, int p, int q, float v[8])
+    __device__ static __forceinline__ void finish8(const Args &e, int p, int q, float v[8], const Part &b, const Ahead &a)
     {
         const int64_t at = (int64_t)q * e.ldy + p;
         if (e.bias) {
@@ -52,10 +68,8 @@ struct LinearEpilogue {
 #pragma unroll
                 for (int i = 0; i < 8; i++) v[i] += b;
             } else {
-                float b[8];
-                load8_vec(e.bias + p, b);
 #pragma unroll
-                for (int i = 0; i < 8; i++) v[i] += b[i];
+                for (int i = 0; i < 8; i++) v[i] += b.bias[i >> 2][i & 3];
             }
         }
         if (e.z) {
@@ -66,13 +80,22 @@ struct LinearEpilogue {
                 for (int i = 0; i < 8; i++) store_from_float(e.z, e.z_type, (int64_t)q * e.z_q + (int64_t)(p + i) * e.z_p, v[i]);
             }
         }
-        if (e.exact) activate_all<8, true>(v, e.act);
-        else activate_all<8, false>(v, e.act);
+        activate_all<8, false>(v, e.act);
         float r[8];
         if (e.residual) {
-            load8_vec(e.residual, e.y_type, (int64_t)q * e.ldr + p, r);
+            if (e.y_type == GS_DTYPE_F32) {
+                load8_vec(static_cast<const float *>(e.residual) + (int64_t)q * e.ldr + p, r);
 #pragma unroll
-            for (int i = 0; i < 8; i++) v[i] += r[i];
+                for (int i = 0; i < 8; i++) v[i] += r[i];
+            } else if (e.y_type == GS_DTYPE_F16) {
+                const gemm::h8 h = __builtin_bit_cast(gemm::h8, a.residual);
+#pragma unroll
+                for (int i = 0; i < 8; i++) v[i] += (float)h[i];
+            } else {
+                const gemm::bf8 h = __builtin_bit_cast(gemm::bf8, a.residual);
+#pragma unroll
+                for (int i = 0; i < 8; i++) v[i] += (float)h[i];
+            }
         }
         if (e.accumulate) {
             load8_vec(e.y, e.y_type, at, r);
@@ -86,12 +109,12 @@ struct LinearEpilogue {
 
     static constexpr bool kMirror = false;
 
-    __device__ static __forceinline__ void store8(const Args &e, int p, int q, float v[8], int, int split)
+    __device__ static __forceinline__ void store8(const Args &e, int p, int q, float v[8], const Part &b, const Ahead &a, int, int split)
     {
         if (e.partial)                                          // rows of partial sums are padded to 8
             store8_vec(e.partial + split * e.split_stride + (int64_t)q * e.ld_partial + p, v);
         else
-            finish8(e, p, q, v);
+            finish8(e, p, q, v, b, a);
     }
     __device__ static __forceinline__ void store1(const Args &e, int p, int q, float v, int, int split)
     {

@@ -200,10 +200,10 @@ void finish_plan(Product &r, bool p_ok, bool q_ok)
     r.e.ld_partial = (r.a.P + 7) & ~7;
     r.e.split_stride = r.e.ld_partial * r.a.Q;
     r.partial_bytes = r.plan.splits > 1 ? (size_t)r.plan.splits * r.e.split_stride * 4 : 0;
-    r.e.vec = (r.e.bias_on_q || al16(r.e.bias)) && vec_ok(r.e.y, r.e.y_type, r.e.ldy) &&
+    r.e.exact = exact_results(r.e);
+    r.e.vec = !(r.e.exact && r.e.act >= GS_ACT_SILU) && (r.e.bias_on_q || al16(r.e.bias)) && vec_ok(r.e.y, r.e.y_type, r.e.ldy) &&
               (!r.e.residual || vec_ok(r.e.residual, r.e.y_type, r.e.ldr)) &&
               (!r.e.z || r.e.z_p != 1 || vec_ok(r.e.z, r.e.z_type, r.e.z_q));
-    r.e.exact = exact_results(r.e);
 }
 
 // Points an operand at its packed planes.
@@ -227,6 +227,11 @@ template <bool VEC> __global__ __launch_bounds__(kReduceThreads) void reduce_spl
     const float *src = e.partial + (int64_t)q * e.ld_partial + p;
     if constexpr (VEC) {
         float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        e.partial = nullptr;
+        LinearEpilogue::Ahead ahead;
+        LinearEpilogue::look_ahead(e, p, q, 0, ahead);
+        LinearEpilogue::Part part;
+        LinearEpilogue::part(e, p, part);
 #pragma unroll 4
         for (int s = 0; s < splits; s++) {
             float w[8];
@@ -234,7 +239,7 @@ template <bool VEC> __global__ __launch_bounds__(kReduceThreads) void reduce_spl
 #pragma unroll
             for (int i = 0; i < 8; i++) v[i] += w[i];
         }
-        LinearEpilogue::finish8(e, p, q, v);
+        LinearEpilogue::finish8(e, p, q, v, part, ahead);
     } else {
         float v = 0.0f;
 #pragma unroll 8

@@ -172,20 +172,28 @@ template <int NL> struct NsEpilogue {
         for (int l = 0; l < NL; l++) *reinterpret_cast<Vec<uint16_t, 8> *>(o + l * e.plane_o) = h[l];
     }
 
+    struct Part {};
+    __device__ static __forceinline__ void part(const Args &, int, Part &) {}
+    struct Ahead { Vec<uint16_t, 8> c[NL]; };   // the limbs of C
+    __device__ static __forceinline__ void look_ahead(const Args &e, int p, int q, int batch, Ahead &a)
+    {
+        if (!e.c || e.partial) return;
+        const uint16_t *c = e.c + batch * e.batch_c + (int64_t)q * e.ldc + p;
+#pragma unroll
+        for (int l = 0; l < NL; l++) a.c[l] = *reinterpret_cast<const Vec<uint16_t, 8> *>(c + l * e.plane_c);
+    }
+
     // v = alpha sum + beta C, in place
-    __device__ static __forceinline__ void combine(const Args &e, int p, int q, float v[8], int batch)
+    __device__ static __forceinline__ void combine(const Args &e, float v[8], const Ahead &a)
     {
 #pragma unroll
         for (int i = 0; i < 8; i++) v[i] *= e.alpha;
         if (!e.c) return;
-        const uint16_t *c = e.c + batch * e.batch_c + (int64_t)q * e.ldc + p;
         float w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-        for (int l = NL - 1; l >= 0; l--) {
-            const Vec<uint16_t, 8> h = *reinterpret_cast<const Vec<uint16_t, 8> *>(c + l * e.plane_c);
+        for (int l = NL - 1; l >= 0; l--)
 #pragma unroll
-            for (int i = 0; i < 8; i++) w[i] += limb_value(h.v[i]);
-        }
+            for (int i = 0; i < 8; i++) w[i] += limb_value(a.c[l].v[i]);
 #pragma unroll
         for (int i = 0; i < 8; i++) v[i] = fmaf(e.beta, w[i], v[i]);
     }
@@ -206,13 +214,13 @@ template <int NL> struct NsEpilogue {
 
     static constexpr bool kMirror = true;
 
-    __device__ static __forceinline__ void store8(const Args &e, int p, int q, float v[8], int batch, int split)
+    __device__ static __forceinline__ void store8(const Args &e, int p, int q, float v[8], const Part &, const Ahead &a, int batch, int split)
     {
         if (e.partial) {
             store8_vec(e.partial + ((int64_t)batch * e.splits + split) * e.split_stride + (int64_t)q * e.ld_partial + p, v);
             return;
         }
-        combine(e, p, q, v, batch);
+        combine(e, v, a);
         if (e.out) write_result(e, p, q, v, batch);
         else write_limbs(e, p, q, v, batch);
     }
@@ -240,12 +248,16 @@ __global__ __launch_bounds__(kThreads) void reduce_splits(typename NsEpilogue<NL
         tq = blockIdx.x / tiles_p;
     }
     const float *part = e.partial + (int64_t)blockIdx.y * e.splits * e.split_stride;
+    typename E::Args whole = e;
+    whole.partial = nullptr;
     const int pl = threadIdx.x % 8 * 8;
 #pragma unroll
     for (int h = 0; h < 64; h += 32) {
         const int ql = h + threadIdx.x / 8, p = tp * 64 + pl, q = tq * 64 + ql;
         if (p >= P || q >= Q) continue;
         float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        typename E::Ahead ahead;
+        E::look_ahead(whole, p, q, blockIdx.y, ahead);
 #pragma unroll 4
         for (int s = 0; s < e.splits; s++) {
             float w[8];
@@ -253,7 +265,7 @@ __global__ __launch_bounds__(kThreads) void reduce_splits(typename NsEpilogue<NL
 #pragma unroll
             for (int i = 0; i < 8; i++) v[i] += w[i];
         }
-        E::combine(e, p, q, v, blockIdx.y);
+        E::combine(e, v, ahead);
         if (e.out) E::write_result(e, p, q, v, blockIdx.y);
         else E::write_limbs(e, p, q, v, blockIdx.y);
 #pragma unroll
