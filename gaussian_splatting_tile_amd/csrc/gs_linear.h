@@ -74,7 +74,7 @@ struct LinearEpilogue {
         }
         if (e.z) {
             if (e.z_p == 1) {
-                store8_vec(e.z, e.z_type, (int64_t)q * e.z_q + p, v);
+                store8_stream(e.z, e.z_type, (int64_t)q * e.z_q + p, v);
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; i++) store_from_float(e.z, e.z_type, (int64_t)q * e.z_q + (int64_t)(p + i) * e.z_p, v[i]);

@@ -44,13 +44,13 @@ double product_cost(const TileRate &t, int64_t P, int64_t Q, int64_t K, int spli
     const double filled = per_cu < t.resident ? 0.8 + 0.2 * per_cu / t.resident : 1.0;
     const double tile = 2e-6 * t.size * t.size * (ceil((double)K / splits) + 64.0) * work;
     double us = per_cu * tile / (t.mflop_us * filled);
-    if (splits > 1) us += 4.0 + splits * (double)P * (double)Q * 8.0 / 4e6;
+    if (splits > 1) us += 3.0 + splits * (double)P * (double)Q * 4.0 / 6e6;
     return us;
 }
 
 ProductPlan make_plan(int64_t P, int64_t Q, int64_t K, bool pt, bool qt, bool staged, bool f32, int step_k, float work)
 {
-    static const TileRate direct[3] = {{256, 1, 4.7f}, {128, 2, 4.2f}, {64, 3, 2.4f}};
+    static const TileRate direct[3] = {{256, 1, 4.9f}, {128, 2, 4.1f}, {64, 3, 2.4f}};
     static const TileRate limbs[3] = {{256, 1, 0.0f}, {128, 1, 4.1f}, {64, 2, 3.0f}};
     static const TileRate staged_[3] = {{256, 1, 0.0f}, {128, 1, 0.0f}, {64, 3, 1.2f}};
     ProductPlan best{pt, qt, staged, 2, 1};

@@ -53,6 +53,27 @@ __device__ __forceinline__ void load8_vec(const void *p, int t, int64_t i, float
     else if (t == GS_DTYPE_F16) load8_vec(static_cast<const _Float16 *>(p) + i, v);
     else load8_vec(static_cast<const __bf16 *>(p) + i, v);
 }
+// The same for results that are not read again soon: written past the caches.
+__device__ __forceinline__ void store8_stream(void *p, int t, int64_t i, const float v[8])
+{
+    typedef int i4 __attribute__((ext_vector_type(4)));
+    if (t == GS_DTYPE_F32) {
+        float *q = static_cast<float *>(p) + i;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const Vec<float, 4> w = {{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]}};
+            __builtin_nontemporal_store(__builtin_bit_cast(i4, w), reinterpret_cast<i4 *>(q + 4 * h));
+        }
+        return;
+    }
+    union { Vec<_Float16, 8> h; Vec<__bf16, 8> b; i4 u; } w;
+#pragma unroll
+    for (int k = 0; k < 8; k++) {
+        if (t == GS_DTYPE_F16) w.h.v[k] = (_Float16)v[k];
+        else w.b.v[k] = (__bf16)v[k];
+    }
+    __builtin_nontemporal_store(w.u, reinterpret_cast<i4 *>(static_cast<uint16_t *>(p) + i));
+}
 __device__ __forceinline__ void store8_vec(void *p, int t, int64_t i, const float v[8])
 {
     if (t == GS_DTYPE_F32) store8_vec(static_cast<float *>(p) + i, v);
