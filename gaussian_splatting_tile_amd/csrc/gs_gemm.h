@@ -39,9 +39,7 @@ struct Args {
     int64_t ldp, ldq, plane_p, plane_q, batch_p, batch_q;
     int P, Q, K;
     int Pl, Ql;                                        // rows that may be read: P, Q, or padded up to a multiple of 8
-    // staged loads only: element types (gs_dtype) and whether 8 consecutive
-    // elements of a row may be read with 16-byte accesses
-    int p_type, q_type, p_vec, q_vec;
+    int p_type, q_type;                                // staged loads only: element types (gs_dtype)
     // kMX8: scale bytes, one per 32 k, and their row strides
     const uint8_t *ps, *qs;
     int64_t ldps, ldqs;
@@ -209,15 +207,19 @@ template <int BX, int THREADS> struct Scales {
     }
 };
 
-// Staged loads: any type, stride, alignment and size; converted (and split
-// into limbs) in registers, then written to LDS.
+// Staged loads: any type, stride, alignment and size.  A chunk waits in
+// registers as it was loaded, so that the loads of the next tile are under way
+// while a tile is multiplied, and is converted (and split into limbs) on its
+// way to LDS.
 template <class TL, int THREADS, bool T, int NL, int KIND> struct Staged {
     static constexpr int kLoads = TL::kChunks / THREADS;
     static_assert(TL::kChunks % THREADS == 0, "tile and block size");
-    float v[kLoads][8];
+    static constexpr int kWords = NL > 1 ? 8 : 4;
+    uint32_t raw[kLoads][kWords];                       // 8 values each: fp32, or in pairs, or (MXFP8) in fours
+    float scale[kLoads];                                // MXFP8
 
-    __device__ __forceinline__ void load(const void *p, int type, bool vec, const uint8_t *scales, int64_t lds_scale,
-                                         int x0, int X, int64_t ld, int k0, int K, int tid)
+    __device__ __forceinline__ void load(const void *p, int type, const uint8_t *scales, int64_t lds_scale, int x0, int X, int64_t ld,
+                                         int k0, int K, int tid)
     {
 #pragma unroll
         for (int j = 0; j < kLoads; j++) {
@@ -227,31 +229,63 @@ template <class TL, int THREADS, bool T, int NL, int KIND> struct Staged {
             int valid = T ? (k < K ? X - x : 0) : (x < X ? K - k : 0);
             valid = max(0, min(8, valid));
             const int64_t i = T ? (int64_t)k * ld + x : (int64_t)x * ld + k;
-            if (type == GS_DTYPE_MXFP8) {
-                const uint8_t *b = static_cast<const uint8_t *>(p);
-                const float s = valid ? e8m0_value(scales[(int64_t)x * lds_scale + (k >> 5)]) : 0.0f;
 #pragma unroll
-                for (int e = 0; e < 8; e++) v[j][e] = e < valid ? e4m3_value(b[i + e]) * s : 0.0f;
+            for (int e = 0; e < kWords; e++) raw[j][e] = 0;
+            if constexpr (NL > 1) {                     // fp32
+                const uint32_t *f = static_cast<const uint32_t *>(p) + i;
+                if (valid == 8) {
+                    const auto v = *reinterpret_cast<const Vec<uint32_t, 8> *>(f);
+#pragma unroll
+                    for (int e = 0; e < 8; e++) raw[j][e] = v.v[e];
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; e++)
+                        if (e < valid) raw[j][e] = f[e];
+                }
+            } else if (type == GS_DTYPE_MXFP8) {        // k is a multiple of 32
+                if (valid == 8) {
+                    const auto v = *reinterpret_cast<const Vec<uint8_t, 8> *>(static_cast<const uint8_t *>(p) + i);
+                    const auto u = __builtin_bit_cast(uint2, v);
+                    raw[j][0] = u.x;
+                    raw[j][1] = u.y;
+                }
+                scale[j] = valid ? e8m0_value(scales[(int64_t)x * lds_scale + (k >> 5)]) : 0.0f;
             } else {
-                load8(p, type, i, valid, vec, v[j]);
+                const uint16_t *h = static_cast<const uint16_t *>(p) + i;
+                if (valid == 8) {
+                    const auto v = *reinterpret_cast<const Vec<uint16_t, 8> *>(h);
+                    const auto u = __builtin_bit_cast(uint4, v);
+                    raw[j][0] = u.x;
+                    raw[j][1] = u.y;
+                    raw[j][2] = u.z;
+                    raw[j][3] = u.w;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; e++)
+                        if (e < valid) raw[j][e >> 1] |= (uint32_t)h[e] << (16 * (e & 1));
+                }
             }
         }
     }
-    __device__ __forceinline__ void write(char *lds, int tid) const
+    __device__ __forceinline__ void write(char *lds, int type, int tid) const
     {
 #pragma unroll
         for (int j = 0; j < kLoads; j++) {
             const int id = j * THREADS + tid;
             const int line = id / TL::CH, c = (id % TL::CH) ^ TL::swz(line);
             union { uint16_t h[8]; uint4 u; } w[NL];
+            if constexpr (NL == 1) {
+                w[0].u = make_uint4(raw[j][0], raw[j][1], raw[j][2], raw[j][3]);
+                if (type == GS_DTYPE_MXFP8) {
 #pragma unroll
-            for (int e = 0; e < 8; e++) {
-                if constexpr (NL == 1) {
-                    w[0].h[e] = KIND == kF16 ? __builtin_bit_cast(uint16_t, (_Float16)v[j][e])
-                                             : __builtin_bit_cast(uint16_t, (__bf16)v[j][e]);
-                } else {
+                    for (int e = 0; e < 8; e++)
+                        w[0].h[e] = __builtin_bit_cast(uint16_t, (__bf16)(e4m3_value((uint8_t)(raw[j][e >> 2] >> (8 * (e & 3)))) * scale[j]));
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; e++) {
                     uint16_t limb[NL];
-                    split_limbs<NL>(v[j][e], limb);
+                    split_limbs<NL>(__uint_as_float(raw[j][e]), limb);
 #pragma unroll
                     for (int l = 0; l < NL; l++) w[l].h[e] = limb[l];
                 }
@@ -523,14 +557,14 @@ __global__ __launch_bounds__(WP *WQ * 64, waves_per_simd(WP * WQ, NS * NL * (BP 
         pb += (int64_t)batch * a.batch_p * dtype_bytes(a.p_type);
         qb += (int64_t)batch * a.batch_q * dtype_bytes(a.q_type);
         auto load = [&](int k0) {
-            sp.load(pb, a.p_type, a.p_vec, a.ps, a.ldps, p0, a.P, a.ldp, k0, kend, tid);
-            sq.load(qb, a.q_type, a.q_vec, a.qs, a.ldqs, q0, a.Q, a.ldq, k0, kend, tid);
+            sp.load(pb, a.p_type, a.ps, a.ldps, p0, a.P, a.ldp, k0, kend, tid);
+            sq.load(qb, a.q_type, a.qs, a.ldqs, q0, a.Q, a.ldq, k0, kend, tid);
         };
         load(kbeg);
         for (int k0 = kbeg; k0 < kend; k0 += kStepK) {
             char *s = ((k0 - kbeg) / kStepK) & 1 ? lds1 : lds0;
-            sp.write(s, tid);
-            sq.write(s + NL * TP::kBytes, tid);
+            sp.write(s, a.p_type, tid);
+            sq.write(s + NL * TP::kBytes, a.q_type, tid);
             __syncthreads();                            // also: every wave is done with this stage's last use
             if (k0 + kStepK < kend) load(k0 + kStepK);
 #pragma unroll

@@ -26,8 +26,8 @@ struct LinearEpilogue {
         void *z;                        // element q * z_q + p * z_p
         int64_t z_q, z_p;
         int z_type;
-        int vec;                        // 8 consecutive p may be read and written as vectors (and no exact silu or gelu:
-                                        // eight library erfs at once take more registers than the rest of a kernel)
+        int vec;                        // 8 consecutive p at a time: unless it takes exact silu or gelu, as eight library
+                                        // erfs at once take more registers than the rest of a kernel
     };
 
     // One value, any layout.
@@ -43,19 +43,18 @@ struct LinearEpilogue {
         store_from_float(e.y, e.y_type, at, v);
     }
 
-    struct Part { gemm::f4 bias[2]; };              // of eight p
-    struct Ahead { gemm::i4 residual; };            // of eight values of a 16-bit type, unconverted
+    struct Part { float bias[8]; };                 // of eight p
+    struct Ahead { Vec<uint16_t, 8> residual; };    // of eight values of a 16-bit type, unconverted
 
     __device__ static __forceinline__ void part(const Args &e, int p, Part &b)
     {
         if (e.partial || !e.bias || e.bias_on_q) return;
-        b.bias[0] = *reinterpret_cast<const gemm::f4 *>(e.bias + p);
-        b.bias[1] = *reinterpret_cast<const gemm::f4 *>(e.bias + p + 4);
+        load8_vec(e.bias + p, b.bias);
     }
     __device__ static __forceinline__ void look_ahead(const Args &e, int p, int q, int, Ahead &a)
     {
         if (!e.partial && e.residual && e.y_type != GS_DTYPE_F32)
-            a.residual = *reinterpret_cast<const gemm::i4 *>(static_cast<const uint16_t *>(e.residual) + (int64_t)q * e.ldr + p);
+            a.residual = *reinterpret_cast<const Vec<uint16_t, 8> *>(static_cast<const uint16_t *>(e.residual) + (int64_t)q * e.ldr + p);
     }
 
     // Eight values p .. p + 7, vec set.
@@ -69,7 +68,7 @@ struct LinearEpilogue {
                 for (int i = 0; i < 8; i++) v[i] += b;
             } else {
 #pragma unroll
-                for (int i = 0; i < 8; i++) v[i] += b.bias[i >> 2][i & 3];
+                for (int i = 0; i < 8; i++) v[i] += b.bias[i];
             }
         }
         if (e.z) {
@@ -140,7 +139,7 @@ hipError_t launch_sum_rows(const float *part, float *out, int n, int rows, int a
 hipError_t launch_product_bf16(const gemm::Args &a, const LinearEpilogue::Args &e, const ProductPlan &plan, hipStream_t s);
 hipError_t launch_product_f16(const gemm::Args &a, const LinearEpilogue::Args &e, const ProductPlan &plan, hipStream_t s);
 hipError_t launch_product_f32(const gemm::Args &a, const LinearEpilogue::Args &e, const ProductPlan &plan, hipStream_t s);
-// At most 64 rows of x, operands readable in 16-byte pieces (fp32: 8 values).
+// At most 64 rows of x (8-bit operands: for a 16-bit y).
 constexpr int kFewRows = 64;
 hipError_t launch_few_rows(const gs_linear &l, const LinearEpilogue::Args &e, hipStream_t s);
 hipError_t launch_product_mx8(const gemm::Args &a, const LinearEpilogue::Args &e, const ProductPlan &plan, hipStream_t s);

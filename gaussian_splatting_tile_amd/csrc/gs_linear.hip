@@ -9,7 +9,7 @@
 // dw[n][k] = dz^T x, whose operands are read by columns where k is theirs.
 //
 // Operands that cannot be loaded into LDS as they stand (fp32, odd sizes,
-// strides or alignments, 8-bit values for an fp32 result) go one of two ways.
+// strides or alignments of 16-bit ones, 8-bit values for an fp32 result) go one of two ways.
 // A result of at most 64 columns or rows reads its long operand once, so the
 // product converts while loading ("staged").  A wider one would convert each
 // element once per tile across it; there one pass first writes both operands
@@ -44,7 +44,7 @@ double product_cost(const TileRate &t, int64_t P, int64_t Q, int64_t K, int spli
     const double filled = per_cu < t.resident ? 0.8 + 0.2 * per_cu / t.resident : 1.0;
     const double tile = 2e-6 * t.size * t.size * (ceil((double)K / splits) + 64.0) * work;
     double us = per_cu * tile / (t.mflop_us * filled);
-    if (splits > 1) us += 3.0 + splits * (double)P * (double)Q * 4.0 / 6e6;
+    if (splits > 1) us += 3.0 + splits * (0.05 + (double)P * (double)Q * 4.0 / 6e6);
     return us;
 }
 
@@ -59,7 +59,7 @@ ProductPlan make_plan(int64_t P, int64_t Q, int64_t K, bool pt, bool qt, bool st
     // three limbs of a 256 tile exceed the LDS
     for (int tile = staged ? 2 : f32 ? 1 : 0; tile < 3; tile++) {
         const TileRate &t = staged ? staged_[tile] : f32 ? limbs[tile] : direct[tile];
-        for (int64_t want = 1; want <= 16 && want <= nt; want = want < 4 ? want + 1 : want * 2) {
+        for (int64_t want = 1; want <= 64 && want <= nt; want = want < 4 ? want + 1 : want * 2) {
             const int64_t per = (nt + want - 1) / want;
             const int splits = (int)((nt + per - 1) / per);
             const double us = product_cost(t, P, Q, K, splits, work);
@@ -73,14 +73,12 @@ ProductPlan make_plan(int64_t P, int64_t Q, int64_t K, bool pt, bool qt, bool st
     return best;
 }
 
-bool vec_ok(const void *p, int type, int64_t ld) { return al16(p) && ld % (16 / dtype_bytes(type)) == 0; }
-
 // ---- operands as padded 16-bit planes -----------------------------------------
 struct PackJob {
     const void *src;                    // [rows][cols] of `type`
     const uint8_t *scales;              // MXFP8
     int64_t ld, ld_scales, rows;
-    int type, cols, vec;
+    int type, cols;
     uint16_t *dst;                      // [limbs][rows][ld_dst], zeros past cols
     int64_t ld_dst;
     int limbs, half;                    // 3: bf16 limbs of fp32; 1: bf16, or fp16 if half
@@ -129,7 +127,7 @@ __global__ __launch_bounds__(kThreads) void pack_operands(PackJobs jobs)
 #pragma unroll
         for (int i = 0; i < 8; i++) v[i] = e4m3_value(b[i]) * f;
     } else {
-        load8(j.src, j.type, r * j.ld + c, valid, j.vec, v);
+        load8(j.src, j.type, r * j.ld + c, valid, v);
     }
     store_planes(j.dst, j.rows * j.ld_dst, r * j.ld_dst + c, j.limbs, j.half, v);
 }
@@ -145,7 +143,6 @@ void add_job(PackJobs &jobs, const void *src, int type, const uint8_t *scales, i
     j.rows = rows;
     j.type = type;
     j.cols = cols;
-    j.vec = type != GS_DTYPE_MXFP8 && vec_ok(src, type, ld);
     j.dst = static_cast<uint16_t *>(dst);
     j.ld_dst = ((int64_t)cols + 7) & ~(int64_t)7;
     j.limbs = type == GS_DTYPE_F32 ? 3 : 1;
@@ -190,20 +187,14 @@ void finish_plan(Product &r, bool p_ok, bool q_ok)
     r.way = p_ok && q_ok ? kDirect : least <= 64 ? kStaged : kPacked;
     r.pack_p = r.way == kPacked && (!p_ok || r.type == GS_DTYPE_MXFP8);
     r.pack_q = r.way == kPacked && (!q_ok || r.type == GS_DTYPE_MXFP8);
-    if (r.way == kStaged) {
-        r.a.p_vec = r.type != GS_DTYPE_MXFP8 && vec_ok(r.a.p, r.a.p_type, r.a.ldp);
-        r.a.q_vec = r.type != GS_DTYPE_MXFP8 && vec_ok(r.a.q, r.a.q_type, r.a.ldq);
-    }
     const bool mx = r.type == GS_DTYPE_MXFP8 && r.way == kDirect, f32 = r.type == GS_DTYPE_F32;
     const int step = mx ? 128 : r.way == kStaged || f32 ? 32 : 64;
-    r.plan = make_plan(r.a.P, r.a.Q, r.a.K, pt, qt, r.way == kStaged, f32, step, f32 ? 6.0f : mx ? 0.6f : 1.0f);
+    r.plan = make_plan(r.a.P, r.a.Q, r.a.K, pt, qt, r.way == kStaged, f32, step, f32 || r.way == kStaged ? 6.0f : mx ? 0.6f : 1.0f);
     r.e.ld_partial = (r.a.P + 7) & ~7;
     r.e.split_stride = r.e.ld_partial * r.a.Q;
     r.partial_bytes = r.plan.splits > 1 ? (size_t)r.plan.splits * r.e.split_stride * 4 : 0;
     r.e.exact = exact_results(r.e);
-    r.e.vec = !(r.e.exact && r.e.act >= GS_ACT_SILU) && (r.e.bias_on_q || al16(r.e.bias)) && vec_ok(r.e.y, r.e.y_type, r.e.ldy) &&
-              (!r.e.residual || vec_ok(r.e.residual, r.e.y_type, r.e.ldr)) &&
-              (!r.e.z || r.e.z_p != 1 || vec_ok(r.e.z, r.e.z_type, r.e.z_q));
+    r.e.vec = !(r.e.exact && r.e.act >= GS_ACT_SILU);
 }
 
 // Points an operand at its packed planes.
@@ -257,7 +248,7 @@ hipError_t run_product(Product &r, void *partial, hipStream_t s)
     else if (r.type == GS_DTYPE_F16) err = launch_product_f16(r.a, r.e, r.plan, s);
     else err = launch_product_bf16(r.a, r.e, r.plan, s);        // widened 8-bit operands too
     if (err != hipSuccess || r.plan.splits == 1) return err;
-    const bool vec = r.e.vec && r.a.P % 8 == 0;
+    const bool vec = r.e.vec && r.a.P % 8 == 0;         // whole chunks
     const int64_t n = (int64_t)(vec ? r.a.P / 8 : r.a.P) * r.a.Q;
     const unsigned blocks = (unsigned)((n + kReduceThreads - 1) / kReduceThreads);
     if (vec) reduce_splits<true><<<blocks, kReduceThreads, 0, s>>>(r.e, r.a.P, r.a.Q, r.plan.splits);
@@ -343,9 +334,7 @@ FwdPlan plan_fwd(const gs_linear &l)
     // of a sum than fp32 holds
     if (l.dtype == GS_DTYPE_MXFP8)
         p_ok = q_ok = p_ok && q_ok && l.y_dtype != GS_DTYPE_F32 && a.ldps < (1 << 22) && a.ldqs < (1 << 22);
-    const bool few = l.m <= kFewRows && (l.dtype == GS_DTYPE_F32 ? l.k % 8 == 0 && vec_ok(l.x, l.dtype, l.x_stride) && vec_ok(l.w, l.dtype, l.w_stride)
-                                                                 : p_ok && q_ok);
-    if (few) {
+    if (l.m <= kFewRows && !(l.dtype == GS_DTYPE_MXFP8 && l.y_dtype == GS_DTYPE_F32)) {
         r.way = kFew;                           // one value at a time: no tile, split or vector rule
         r.e.exact = exact_results(r.e);
         return f;
@@ -394,7 +383,6 @@ struct DzArgs {
     float *part;                        // [row blocks][n] partial sums of db, or NULL
     int64_t m;
     int n, rows_per_block;
-    int vec;
 };
 
 // A block's sums of its columns over its row lanes, in order, to its partial row.
@@ -425,10 +413,10 @@ __global__ __launch_bounds__(kThreads) void dz_rows(DzArgs d, int groups)
     float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     for (int64_t r = r0 + rl; r < r1; r += lanes) {
         float v[8];
-        load8(d.dy, d.dy_type, r * d.lddy + c0, valid, d.vec, v);
+        load8(d.dy, d.dy_type, r * d.lddy + c0, valid, v);
         if (d.act != GS_ACT_NONE) {
             float z[8];
-            load8(d.z, d.type, r * d.ldz + c0, valid, d.vec, z);
+            load8(d.z, d.type, r * d.ldz + c0, valid, z);
             if (d.exact) scale_by_slope<8, true>(v, z, d.act);      // past n: 0 times the slope at 0
             else scale_by_slope<8, false>(v, z, d.act);
         }
@@ -440,8 +428,7 @@ __global__ __launch_bounds__(kThreads) void dz_rows(DzArgs d, int groups)
     column_sums(d, groups, acc, sums);
 }
 
-// The same where dy, z and dz are of one 16-bit type in whole, aligned chunks of
-// 8: the next row is on its way, unconverted, while a row is worked on
+// The same where dy, z and dz are of one 16-bit type in whole chunks of 8: the next row is on its way, unconverted, while a row is worked on
 // (16384 x 4096 with GELU in bf16: 79 us, 5.1 TB/s; 103 us without).
 template <typename T> __global__ __launch_bounds__(kThreads) void dz_rows_ahead(DzArgs d, int groups)
 {
@@ -578,8 +565,9 @@ BwdPlan plan_bwd(const gs_linear &l, const gs_linear_grads &g)
     int64_t want = 2048 / cols;
     want = want < 1 ? 1 : want > 1024 ? 1024 : want;
     int64_t per = (l.m + want - 1) / want;
-    per = (per + 63) & ~(int64_t)63;
-    if (per < 64) per = 64;
+    const int64_t whole = l.planes ? 64 : 8;            // rows that a block works on at a time
+    per = (per + whole - 1) / whole * whole;
+    if (per < whole) per = whole;
     b.rows_per_block = (int)per;
     b.row_blocks = (int)((l.m + per - 1) / per);
     auto take = [&](size_t bytes) {
@@ -654,14 +642,13 @@ hipError_t run_bwd(const gs_linear &l, const gs_linear_grads &g, BwdPlan &b, cha
         d.m = l.m;
         d.n = l.n;
         d.rows_per_block = b.rows_per_block;
-        d.vec = vec_ok(g.dy, l.y_dtype, g.dy_stride) && (l.activation == GS_ACT_NONE || vec_ok(l.z, l.dtype, l.z_stride));
         if (l.planes) {
             dz_planes<<<dim3((unsigned)((l.n + 63) / 64), (unsigned)b.row_blocks), kThreads, 0, s>>>(d);
         } else {
             int groups = 1;                     // of 8 columns: a power of two, at most 64
             while (groups < 64 && groups * 8 < l.n) groups *= 2;
             const dim3 grid((unsigned)((l.n + groups * 8 - 1) / (groups * 8)), (unsigned)b.row_blocks);
-            const bool ahead = d.dz && !d.limbs && d.vec && l.n % 8 == 0 && l.activation != GS_ACT_NONE && l.y_dtype == l.dtype;
+            const bool ahead = d.dz && !d.limbs && l.n % 8 == 0 && l.activation != GS_ACT_NONE && l.y_dtype == l.dtype;
             if (ahead && l.dtype == GS_DTYPE_BF16) dz_rows_ahead<__bf16><<<grid, kThreads, 0, s>>>(d, groups);
             else if (ahead && l.dtype == GS_DTYPE_F16) dz_rows_ahead<_Float16><<<grid, kThreads, 0, s>>>(d, groups);
             else dz_rows<<<grid, kThreads, 0, s>>>(d, groups);
@@ -683,7 +670,6 @@ hipError_t run_bwd(const gs_linear &l, const gs_linear_grads &g, BwdPlan &b, cha
             use_planes(ws + b.limbs_at, l.m, l.n, a.q, a.ldq, a.plane_q, a.Ql, qt);
         } else if (b.own_dz) {
             a.q = ws + b.dz_at;
-            a.q_vec = 1;
         }
     };
     if (g.dx) operands(b.dx, b.dx.pack_p, b.w_at, l.n, false);

@@ -30,7 +30,7 @@ struct Update {
     float *momentum_out;
     int grad_type, nesterov;
     float beta;
-    int vec;                                    // size and alignments are multiples of 4 elements
+    int vec;                                    // size is a multiple of 4
     int64_t size;                               // rows * cols
 };
 
@@ -398,8 +398,7 @@ template <int NL> hipError_t run_muon(const gs_muon &m, bool step, char *ws, hip
     u.nesterov = m.nesterov;
     u.beta = m.beta;
     u.size = (int64_t)m.rows * m.cols;
-    const int es = dtype_bytes(m.grad_dtype) * 4;
-    u.vec = u.size % 4 == 0 && aligned_to(m.grad, es) && (!step || (aligned_to(m.momentum, 16) && aligned_to(m.momentum_out, 16)));
+    u.vec = u.size % 4 == 0;
     momentum_and_norm<<<dim3((unsigned)p.norm_blocks, (unsigned)m.batch), kThreads, 0, s>>>(u, part);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;

@@ -4,9 +4,9 @@
 // HBM-bound: the forward reads x and the residual and writes the sum and y
 // once, the backward reads the sum, dy and dsum and writes dx.  A row is held
 // in registers between its reduction and its outputs, 8 consecutive elements
-// (16 bytes of a 16-bit type) per lane and access: rows of up to 2048 by one
-// wave (4 rows per workgroup, no barrier), up to 8192 by a workgroup, longer
-// ones in two passes.  An 8-bit block of 32 values is 4 neighbouring lanes.
+// (16 bytes of a 16-bit type) per lane and access: rows of up to 128 by 16
+// lanes, up to 2048 by a wave (4 rows per workgroup, no barrier), up to 8192 by
+// a workgroup, longer ones in two passes.  An 8-bit block of 32 values is 4 neighbouring lanes.
 #include "gs_linear.h"
 
 #include <math.h>
@@ -19,7 +19,6 @@ constexpr int kMaxRegRow = 8192;
 
 bool aligned_to(const void *p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
 bool float_type(int t) { return t == GS_DTYPE_F32 || t == GS_DTYPE_F16 || t == GS_DTYPE_BF16; }
-bool vec_ok(const void *p, int type, int64_t ld) { return aligned_to(p, 16) && ld % (16 / dtype_bytes(type)) == 0; }
 gs_status from_hip(hipError_t e) { return e == hipSuccess ? GS_OK : GS_ERR_HIP; }
 
 template <typename T> constexpr int type_of();
@@ -27,18 +26,18 @@ template <> constexpr int type_of<float>() { return GS_DTYPE_F32; }
 template <> constexpr int type_of<_Float16>() { return GS_DTYPE_F16; }
 template <> constexpr int type_of<__bf16>() { return GS_DTYPE_BF16; }
 
-template <typename T> __device__ __forceinline__ void load_chunk(const T *p, int64_t i, int valid, bool vec, float v[8])
+template <typename T> __device__ __forceinline__ void load_chunk(const T *p, int64_t i, int valid, float v[8])
 {
-    if (vec && valid == 8) {
+    if (valid == 8) {
         load8_vec(p + i, v);
         return;
     }
 #pragma unroll
     for (int j = 0; j < 8; j++) v[j] = j < valid ? (float)p[i + j] : 0.0f;
 }
-template <typename T> __device__ __forceinline__ void store_chunk(T *p, int64_t i, int valid, bool vec, const float v[8])
+template <typename T> __device__ __forceinline__ void store_chunk(T *p, int64_t i, int valid, const float v[8])
 {
-    if (vec && valid == 8) {
+    if (valid == 8) {
         store8_vec(p + i, v);
         return;
     }
@@ -47,16 +46,11 @@ template <typename T> __device__ __forceinline__ void store_chunk(T *p, int64_t 
         if (j < valid) p[i + j] = (T)v[j];
 }
 
-__device__ __forceinline__ float wave_sum(float x)
-{
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);
-    return x;
-}
-// Sum over the LANES threads of a row: a wave, or the workgroup by LDS.
+// Sum over the LANES threads of a row: (part of) a wave, or the workgroup by LDS.
 template <int LANES> __device__ __forceinline__ float row_sum(float x, float *lds)
 {
-    x = wave_sum(x);
+#pragma unroll
+    for (int o = min(LANES, 64) / 2; o > 0; o >>= 1) x += __shfl_xor(x, o);
     if constexpr (LANES > 64) {
         __syncthreads();                        // the last use of lds is over
         if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
@@ -72,7 +66,7 @@ template <int LANES> __device__ __forceinline__ float row_sum(float x, float *ld
 // (all of them in the call).  The exponent is the smallest that leaves the
 // block's largest magnitude, 1.m x 2^E, at most 448 = 1.75 x 2^8: E - 8, or
 // E - 7 where 1.m > 1.75.
-__device__ __forceinline__ void quantize_chunk(const float v[8], uint8_t *codes, bool vec, uint8_t *scale)
+__device__ __forceinline__ void quantize_chunk(const float v[8], uint8_t *codes, uint8_t *scale)
 {
     uint32_t top = 0;
 #pragma unroll
@@ -89,12 +83,7 @@ __device__ __forceinline__ void quantize_chunk(const float v[8], uint8_t *codes,
         int x = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h] * inv, v[4 * h + 1] * inv, 0, false);
         w[h] = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h + 2] * inv, v[4 * h + 3] * inv, x, true);
     }
-    if (vec) {
-        *reinterpret_cast<int2 *>(codes) = make_int2(w[0], w[1]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; j++) codes[j] = (uint8_t)(w[j >> 2] >> (8 * (j & 3)));
-    }
+    *reinterpret_cast<Vec<uint8_t, 8> *>(codes) = __builtin_bit_cast(Vec<uint8_t, 8>, make_int2(w[0], w[1]));
     if (scale) *scale = (uint8_t)s;
 }
 
@@ -105,7 +94,7 @@ struct NormArgs {
     uint8_t *scales;
     float *rstd;
     int64_t m, ldx, ldr, lds, ldy, ldsc;
-    int n, vec, gamma_vec, q8, norm;            // norm 0: y is x (quantisation alone)
+    int n, q8, norm;                            // norm 0: y is x (quantisation alone)
     float eps;
 };
 
@@ -116,15 +105,14 @@ __device__ __forceinline__ void emit(const NormArgs &a, int64_t row, int c, int 
 {
     if (a.norm) {
         float g[8];
-        if (a.gamma) load_chunk(a.gamma, c, valid, a.gamma_vec, g);
+        if (a.gamma) load_chunk(a.gamma, c, valid, g);
 #pragma unroll
         for (int j = 0; j < 8; j++) v[j] = a.gamma ? v[j] * rstd * g[j] : v[j] * rstd;
     }
     if (a.q8)
-        quantize_chunk(v, static_cast<uint8_t *>(a.y) + row * a.ldy + c, a.vec,
-                       (threadIdx.x & 3) == 0 ? a.scales + row * a.ldsc + (c >> 5) : nullptr);
+        quantize_chunk(v, static_cast<uint8_t *>(a.y) + row * a.ldy + c, (threadIdx.x & 3) == 0 ? a.scales + row * a.ldsc + (c >> 5) : nullptr);
     else
-        store_chunk(static_cast<T *>(a.y), row * a.ldy + c, valid, a.vec, v);
+        store_chunk(static_cast<T *>(a.y), row * a.ldy + c, valid, v);
 }
 
 // Rows of up to LANES * 8 * V elements.
@@ -133,15 +121,15 @@ template <typename T, int LANES, int V> __global__ __launch_bounds__(kThreads) v
     __shared__ float lds[kThreads / 64];
     const int lane = threadIdx.x % LANES;
     const int64_t row = (int64_t)blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
-    if (row >= a.m) return;                     // whole waves; a workgroup's single row is always there
+    if (row >= a.m) return;                     // a row's lanes together; a workgroup's single row is always there
     float v[V][8], sq = 0.0f;
 #pragma unroll
     for (int k = 0; k < V; k++) {
         const int c = (k * LANES + lane) * 8, valid = max(0, min(8, a.n - c));
-        load_chunk(static_cast<const T *>(a.x), row * a.ldx + c, valid, a.vec, v[k]);
+        load_chunk(static_cast<const T *>(a.x), row * a.ldx + c, valid, v[k]);
         if (a.residual) {
             float r[8];
-            load_chunk(static_cast<const T *>(a.residual), row * a.ldr + c, valid, a.vec, r);
+            load_chunk(static_cast<const T *>(a.residual), row * a.ldr + c, valid, r);
 #pragma unroll
             for (int j = 0; j < 8; j++) v[k][j] += r[j];
         }
@@ -156,7 +144,7 @@ template <typename T, int LANES, int V> __global__ __launch_bounds__(kThreads) v
     for (int k = 0; k < V; k++) {
         const int c = (k * LANES + lane) * 8, valid = max(0, min(8, a.n - c));
         if (valid == 0) continue;               // whole 8-bit blocks: n is a multiple of 32 there
-        if (a.sum) store_chunk(static_cast<T *>(a.sum), row * a.lds + c, valid, a.vec, v[k]);
+        if (a.sum) store_chunk(static_cast<T *>(a.sum), row * a.lds + c, valid, v[k]);
         emit<T>(a, row, c, valid, v[k], rstd);
     }
 }
@@ -167,10 +155,10 @@ template <typename T> __global__ __launch_bounds__(kThreads) void norm_long(Norm
     __shared__ float lds[kThreads / 64];
     const int64_t row = blockIdx.x;
     auto sum_at = [&](int c, int valid, float v[8]) {
-        load_chunk(static_cast<const T *>(a.x), row * a.ldx + c, valid, a.vec, v);
+        load_chunk(static_cast<const T *>(a.x), row * a.ldx + c, valid, v);
         if (a.residual) {
             float r[8];
-            load_chunk(static_cast<const T *>(a.residual), row * a.ldr + c, valid, a.vec, r);
+            load_chunk(static_cast<const T *>(a.residual), row * a.ldr + c, valid, r);
 #pragma unroll
             for (int j = 0; j < 8; j++) v[j] += r[j];
         }
@@ -190,15 +178,16 @@ template <typename T> __global__ __launch_bounds__(kThreads) void norm_long(Norm
         const int valid = min(8, a.n - c);
         float v[8];
         sum_at(c, valid, v);
-        if (a.sum) store_chunk(static_cast<T *>(a.sum), row * a.lds + c, valid, a.vec, v);
+        if (a.sum) store_chunk(static_cast<T *>(a.sum), row * a.lds + c, valid, v);
         emit<T>(a, row, c, valid, v, rstd);
     }
 }
 
 template <typename T> hipError_t launch_norm(const NormArgs &a, hipStream_t s)
 {
-    const unsigned rows4 = (unsigned)((a.m + 3) / 4), rows1 = (unsigned)a.m;
-    if (a.n <= 512) norm_rows<T, 64, 1><<<rows4, kThreads, 0, s>>>(a);
+    const unsigned rows16 = (unsigned)((a.m + 15) / 16), rows4 = (unsigned)((a.m + 3) / 4), rows1 = (unsigned)a.m;
+    if (a.n <= 128) norm_rows<T, 16, 1><<<rows16, kThreads, 0, s>>>(a);
+    else if (a.n <= 512) norm_rows<T, 64, 1><<<rows4, kThreads, 0, s>>>(a);
     else if (a.n <= 1024) norm_rows<T, 64, 2><<<rows4, kThreads, 0, s>>>(a);
     else if (a.n <= 2048) norm_rows<T, 64, 4><<<rows4, kThreads, 0, s>>>(a);
     else if (a.n <= 4096) norm_rows<T, 256, 2><<<rows1, kThreads, 0, s>>>(a);
@@ -221,67 +210,85 @@ struct GradArgs {
     void *dx;
     float *part;                                // [grid][n] partial sums of dgamma, or NULL
     int64_t m, lds, ldy, ldds, ldx;
-    int n, vec, gamma_vec;
+    int n;
 };
 
+template <int LANES> constexpr int kGradThreads = LANES <= 64 ? kThreads : LANES;
+
 // Each workgroup strides over the rows; a thread keeps the dgamma sums of its
-// columns in registers and the workgroup writes one partial row at the end.
-template <typename T, int LANES, int V, bool AHEAD> __global__ __launch_bounds__(kThreads) void grad_rows(GradArgs a)
+// columns in registers and the workgroup writes one partial row at the end.  The
+// next row's sum and dy are on their way, unconverted, while a row is worked on.
+// WIDE, rows of at least 8: the last chunk of a row takes its last 8 elements,
+// so that every load is a whole vector, and leaves those of them that are the
+// chunk's before it alone (62846 x 118 in bf16: 18 us, 27 with loads of single
+// elements there).
+template <typename T, int LANES, int V, bool WIDE> __global__ __launch_bounds__(kGradThreads<LANES>) void grad_rows(GradArgs a)
 {
-    constexpr int kRows = kThreads / LANES;
-    __shared__ float lds[kThreads / 64];
-    __shared__ float turn[LANES == 64 ? kThreads : 1][8];
+    constexpr int kRows = kGradThreads<LANES> / LANES;
+    __shared__ float lds[LANES > 64 ? LANES / 64 : 1];
+    __shared__ float turn[kRows > 1 ? kThreads : 1][8];
     const int lane = threadIdx.x % LANES, sub = threadIdx.x / LANES;
+    auto chunk = [&](int k, int l) { return (k * LANES + l) * 8; };
+    auto start = [&](int c) { return WIDE ? min(c, a.n - 8) : c; };      // of a chunk's 8 elements
+    // element j of a chunk that starts at `at` is its own
+    auto own = [&](int c, int at, int j) { return WIDE ? at + j >= c : c + j < a.n; };
+    auto load = [&](auto *p, int at, float v[8]) {
+        if constexpr (WIDE) load8_vec(p + at, v);
+        else load_chunk(p, at, a.n - at, v);
+    };
     float dg[V][8];
+    Vec<T, 8> nh[V], ng[V];
 #pragma unroll
-    for (int k = 0; k < V; k++)
+    for (int k = 0; k < V; k++) {
+        nh[k] = ng[k] = Vec<T, 8>{};
 #pragma unroll
         for (int j = 0; j < 8; j++) dg[k][j] = 0.0f;
-    // AHEAD (whole chunks, aligned): the next row's sum and dy are on their way,
-    // unconverted, while a row is worked on
-    Vec<T, 8> nh[V], ng[V];
+    }
     auto fetch = [&](int64_t row) {
         if (row >= a.m) return;
 #pragma unroll
         for (int k = 0; k < V; k++) {
-            const int c = (k * LANES + lane) * 8;
+            const int c = chunk(k, lane), at = start(c);
             if (c >= a.n) continue;
-            nh[k] = *reinterpret_cast<const Vec<T, 8> *>(static_cast<const T *>(a.sum) + row * a.lds + c);
-            ng[k] = *reinterpret_cast<const Vec<T, 8> *>(static_cast<const T *>(a.dy) + row * a.ldy + c);
+            const T *h = static_cast<const T *>(a.sum) + row * a.lds + at, *g = static_cast<const T *>(a.dy) + row * a.ldy + at;
+            if constexpr (WIDE) {
+                nh[k] = *reinterpret_cast<const Vec<T, 8> *>(h);
+                ng[k] = *reinterpret_cast<const Vec<T, 8> *>(g);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                    if (c + j < a.n) {
+                        nh[k].v[j] = h[j];
+                        ng[k].v[j] = g[j];
+                    }
+            }
         }
     };
     const int64_t step = (int64_t)gridDim.x * kRows;
     int64_t row = (int64_t)blockIdx.x * kRows + sub;
-    if constexpr (AHEAD) {
-#pragma unroll
-        for (int k = 0; k < V; k++) nh[k] = ng[k] = Vec<T, 8>{};
-        fetch(row);
-    }
+    fetch(row);
     for (; row < a.m; row += step) {
         const float rstd = a.rstd[row];
         float h[V][8], g[V][8], dot = 0.0f;
-        if constexpr (AHEAD) {
 #pragma unroll
-            for (int k = 0; k < V; k++)
+        for (int k = 0; k < V; k++)
 #pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    h[k][j] = (float)nh[k].v[j];
-                    g[k][j] = (float)ng[k].v[j];
-                }
-            fetch(row + step);
-        } else {
-#pragma unroll
-            for (int k = 0; k < V; k++) {
-                const int c = (k * LANES + lane) * 8, valid = max(0, min(8, a.n - c));
-                load_chunk(static_cast<const T *>(a.sum), row * a.lds + c, valid, a.vec, h[k]);
-                load_chunk(static_cast<const T *>(a.dy), row * a.ldy + c, valid, a.vec, g[k]);
+            for (int j = 0; j < 8; j++) {
+                h[k][j] = (float)nh[k].v[j];
+                g[k][j] = (float)ng[k].v[j];
             }
-        }
+        fetch(row + step);
 #pragma unroll
         for (int k = 0; k < V; k++) {
-            const int c = (k * LANES + lane) * 8, valid = max(0, min(8, a.n - c));
+            const int c = chunk(k, lane), at = start(c);
+            if (c >= a.n) continue;
+            if (WIDE && at < c) {
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                    if (!own(c, at, j)) h[k][j] = g[k][j] = 0.0f;
+            }
             float w[8];
-            if (a.gamma) load_chunk(a.gamma, c, valid, a.gamma_vec, w);
+            if (a.gamma) load(a.gamma, at, w);
 #pragma unroll
             for (int j = 0; j < 8; j++) {
                 h[k][j] *= rstd;
@@ -293,36 +300,46 @@ template <typename T, int LANES, int V, bool AHEAD> __global__ __launch_bounds__
         dot = row_sum<LANES>(dot, lds) / (float)a.n;
 #pragma unroll
         for (int k = 0; k < V; k++) {
-            const int c = (k * LANES + lane) * 8, valid = max(0, min(8, a.n - c));
-            if (valid == 0) continue;
+            const int c = chunk(k, lane), at = start(c);
+            if (c >= a.n) continue;
             float d[8];
-            if (a.dsum) load_chunk(static_cast<const T *>(a.dsum), row * a.ldds + c, valid, a.vec, d);
+            if (a.dsum) load(static_cast<const T *>(a.dsum) + row * a.ldds, at, d);
 #pragma unroll
             for (int j = 0; j < 8; j++) {
                 const float v = rstd * fmaf(-h[k][j], dot, g[k][j]);
                 d[j] = a.dsum ? v + d[j] : v;
             }
-            store_chunk(static_cast<T *>(a.dx), row * a.ldx + c, valid, a.vec, d);
+            T *dx = static_cast<T *>(a.dx) + row * a.ldx + at;
+            if (WIDE && at == c) {
+                store8_vec(dx, d);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                    if (own(c, at, j)) dx[j] = (T)d[j];
+            }
         }
     }
     if (!a.part) return;
     float *out = a.part + (int64_t)blockIdx.x * a.n;
 #pragma unroll
     for (int k = 0; k < V; k++) {
-        const int c = (k * LANES + lane) * 8;
-        if constexpr (LANES == 64) {            // the four waves' sums of a column, in order
+        if constexpr (kRows > 1) {              // a column's sums over the workgroup's rows, in order
             __syncthreads();
 #pragma unroll
             for (int j = 0; j < 8; j++) turn[threadIdx.x][j] = dg[k][j];
             __syncthreads();
-            for (int i = threadIdx.x; i < 512; i += kThreads) {
-                const int l = i / 8, j = i % 8, col = k * 512 + i;
-                if (col < a.n) out[col] = turn[l][j] + turn[64 + l][j] + turn[128 + l][j] + turn[192 + l][j];
+            for (int i = threadIdx.x; i < LANES * 8; i += kThreads) {
+                const int c = chunk(k, i / 8), at = start(c);
+                float sum = turn[i / 8][i % 8];
+#pragma unroll
+                for (int r = 1; r < kRows; r++) sum += turn[r * LANES + i / 8][i % 8];
+                if (c < a.n && own(c, at, i % 8)) out[at + i % 8] = sum;
             }
         } else {
+            const int c = chunk(k, lane), at = start(c);
 #pragma unroll
             for (int j = 0; j < 8; j++)
-                if (c + j < a.n) out[c + j] = dg[k][j];
+                if (c < a.n && own(c, at, j)) out[at + j] = dg[k][j];
         }
     }
 }
@@ -336,9 +353,9 @@ template <typename T> __global__ __launch_bounds__(kThreads) void grad_long(Grad
     float dot = 0.0f;
     auto at = [&](int c, int valid, float h[8], float g[8]) {
         float w[8];
-        load_chunk(static_cast<const T *>(a.sum), row * a.lds + c, valid, a.vec, h);
-        load_chunk(static_cast<const T *>(a.dy), row * a.ldy + c, valid, a.vec, g);
-        if (a.gamma) load_chunk(a.gamma, c, valid, a.gamma_vec, w);
+        load_chunk(static_cast<const T *>(a.sum), row * a.lds + c, valid, h);
+        load_chunk(static_cast<const T *>(a.dy), row * a.ldy + c, valid, g);
+        if (a.gamma) load_chunk(a.gamma, c, valid, w);
 #pragma unroll
         for (int j = 0; j < 8; j++) {
             h[j] *= rstd;
@@ -356,13 +373,13 @@ template <typename T> __global__ __launch_bounds__(kThreads) void grad_long(Grad
         const int valid = min(8, a.n - c);
         float h[8], g[8], d[8];
         at(c, valid, h, g);
-        if (a.dsum) load_chunk(static_cast<const T *>(a.dsum), row * a.ldds + c, valid, a.vec, d);
+        if (a.dsum) load_chunk(static_cast<const T *>(a.dsum), row * a.ldds + c, valid, d);
 #pragma unroll
         for (int j = 0; j < 8; j++) {
             const float v = rstd * fmaf(-h[j], dot, g[j]);
             d[j] = a.dsum ? v + d[j] : v;
         }
-        store_chunk(static_cast<T *>(a.dx), row * a.ldx + c, valid, a.vec, d);
+        store_chunk(static_cast<T *>(a.dx), row * a.ldx + c, valid, d);
     }
 }
 
@@ -373,8 +390,8 @@ template <typename T> __global__ __launch_bounds__(kThreads) void dgamma_long(Gr
     float dg[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     for (int64_t row = blockIdx.y; row < a.m; row += gridDim.y) {
         float h[8], g[8];
-        load_chunk(static_cast<const T *>(a.sum), row * a.lds + c, valid, a.vec, h);
-        load_chunk(static_cast<const T *>(a.dy), row * a.ldy + c, valid, a.vec, g);
+        load_chunk(static_cast<const T *>(a.sum), row * a.lds + c, valid, h);
+        load_chunk(static_cast<const T *>(a.dy), row * a.ldy + c, valid, g);
         const float rstd = a.rstd[row];
 #pragma unroll
         for (int j = 0; j < 8; j++) dg[j] = fmaf(g[j], h[j] * rstd, dg[j]);
@@ -406,29 +423,33 @@ __global__ __launch_bounds__(kSumThreads) void sum_rows(const float *part, float
     if (ty == 0 && c < n) out[c] = accumulate ? out[c] + sums[0][tx] : sums[0][tx];
 }
 
-// Workgroups of the backward, each with one partial row of dgamma.
+// Workgroups of the backward, each with one partial row of dgamma: one per CU
+// before any takes a second pass over the rows, then at least two passes each
+// (four of the one row of wide workgroups) while that gives each CU as many as
+// it runs best with.  In bf16 with 512 / 1024: 60000 x 512 takes 75.3 / 53.5 us,
+// 16384 x 1024 37.7 / 32.7, 16384 x 2048 82.5 / 64.2, 16384 x 4096 121 / 128;
+// 2000 x 2048 17.3 with 512 and 20.7 with 1024.
 int grad_blocks(int64_t m, int n)
 {
     if (n > kMaxRegRow) return (int)(m < 64 ? m : 64);
-    const int64_t rows = n <= 2048 ? 4 : 1, want = (m + rows - 1) / rows;
-    return (int)(want < 1024 ? want : 1024);
-}
-
-template <typename T, int LANES, int V> void launch_rows(const GradArgs &a, unsigned blocks, bool ahead, hipStream_t s)
-{
-    if (ahead) grad_rows<T, LANES, V, true><<<blocks, kThreads, 0, s>>>(a);
-    else grad_rows<T, LANES, V, false><<<blocks, kThreads, 0, s>>>(a);
+    const int64_t rows = n <= 128 ? 16 : n <= 256 ? 8 : n <= 1024 ? 4 : 1;
+    const int64_t passes = (m + rows - 1) / rows, most = n <= 2048 ? 1024 : 512;
+    if (passes <= 256) return (int)passes;
+    const int64_t each = n <= 1024 ? 2 : 4, want = passes / each > 256 ? passes / each : 256;
+    return (int)(want < most ? want : most);
 }
 
 template <typename T> hipError_t launch_grad(const GradArgs &a, hipStream_t s)
 {
     const unsigned g = (unsigned)grad_blocks(a.m, a.n);
-    const bool ahead = a.vec && a.n % 8 == 0;
-    if (a.n <= 512) launch_rows<T, 64, 1>(a, g, ahead, s);
-    else if (a.n <= 1024) launch_rows<T, 64, 2>(a, g, ahead, s);
-    else if (a.n <= 2048) launch_rows<T, 64, 4>(a, g, ahead, s);
-    else if (a.n <= 4096) launch_rows<T, 256, 2>(a, g, ahead, s);
-    else if (a.n <= kMaxRegRow) launch_rows<T, 256, 4>(a, g, ahead, s);
+    if (a.n < 8) grad_rows<T, 16, 1, false><<<g, kThreads, 0, s>>>(a);
+    else if (a.n <= 128) grad_rows<T, 16, 1, true><<<g, kThreads, 0, s>>>(a);
+    else if (a.n <= 256) grad_rows<T, 32, 1, true><<<g, kThreads, 0, s>>>(a);
+    else if (a.n <= 512) grad_rows<T, 64, 1, true><<<g, kThreads, 0, s>>>(a);
+    else if (a.n <= 1024) grad_rows<T, 64, 2, true><<<g, kThreads, 0, s>>>(a);
+    else if (a.n <= 2048) grad_rows<T, 256, 1, true><<<g, 256, 0, s>>>(a);
+    else if (a.n <= 4096) grad_rows<T, 512, 1, true><<<g, 512, 0, s>>>(a);
+    else if (a.n <= kMaxRegRow) grad_rows<T, 1024, 1, true><<<g, 1024, 0, s>>>(a);
     else {
         // dgamma first: dx may be written over dy
         if (a.part) dgamma_long<T><<<dim3((unsigned)((a.n + 2047) / 2048), g), kThreads, 0, s>>>(a);
@@ -513,10 +534,6 @@ gs_status gs_rms_norm_fwd(const gs_rms_norm *p, void *stream)
     a.ldy = p->y_stride;
     a.ldsc = p->y_scales_stride;
     a.n = p->n;
-    a.vec = vec_ok(p->x, p->dtype, p->x_stride) && (!p->residual || vec_ok(p->residual, p->dtype, p->residual_stride)) &&
-            (!p->sum || vec_ok(p->sum, p->dtype, p->sum_stride)) &&
-            (q8 ? aligned_to(p->y, 8) && p->y_stride % 8 == 0 : vec_ok(p->y, p->dtype, p->y_stride));
-    a.gamma_vec = aligned_to(p->gamma, 16);
     a.q8 = q8;
     a.norm = 1;
     a.eps = p->eps;
@@ -549,7 +566,6 @@ gs_status gs_mxfp8_quantize(const void *x, int32_t dtype, int64_t m, int32_t n, 
     a.ldy = codes_stride;
     a.ldsc = scales_stride;
     a.n = n;
-    a.vec = vec_ok(x, dtype, x_stride) && aligned_to(codes, 8) && codes_stride % 8 == 0;
     a.q8 = 1;
     return from_hip(launch_norm(a, dtype, (hipStream_t)stream));
 }
@@ -588,9 +604,6 @@ gs_status gs_rms_norm_bwd(const gs_rms_norm_grads *p, void *workspace, size_t wo
     a.ldds = p->dsum_stride;
     a.ldx = p->dx_stride;
     a.n = p->n;
-    a.vec = vec_ok(p->sum, p->dtype, p->sum_stride) && vec_ok(p->dy, p->dtype, p->dy_stride) &&
-            (!p->dsum || vec_ok(p->dsum, p->dtype, p->dsum_stride)) && vec_ok(p->dx, p->dtype, p->dx_stride);
-    a.gamma_vec = aligned_to(p->gamma, 16);
     hipError_t e = p->dtype == GS_DTYPE_F32 ? launch_grad<float>(a, s)
                    : p->dtype == GS_DTYPE_F16 ? launch_grad<_Float16>(a, s) : launch_grad<__bf16>(a, s);
     if (e == hipSuccess && p->dgamma) {

@@ -12,8 +12,10 @@ namespace gsi {
 
 __host__ __device__ constexpr int dtype_bytes(int t) { return t == GS_DTYPE_F32 ? 4 : t == GS_DTYPE_MXFP8 ? 1 : 2; }
 
-// Four or eight consecutive values as one vector access; T: float, _Float16, __bf16.
-template <typename T, int N> struct alignas(sizeof(T) * N > 16 ? 16 : sizeof(T) * N) Vec { T v[N]; };
+// Consecutive values as one vector access of up to 16 bytes.  Only the elements'
+// own alignment is asked for: the hardware takes the wide accesses at any
+// address of global memory, so odd strides and offsets need no other path.
+template <typename T, int N> struct __attribute__((packed, aligned(sizeof(T)))) Vec { T v[N]; };
 
 template <typename T> __device__ __forceinline__ float to_float(T x) { return (float)x; }
 template <typename T> __device__ __forceinline__ T from_float(float x) { return (T)x; }     // rounds to nearest even
@@ -45,8 +47,7 @@ template <typename T> __device__ __forceinline__ void store8_vec(T *p, const flo
     for (int i = 0; i < 8; i++) w.v[i] = (T)v[i];
     *reinterpret_cast<Vec<T, 8> *>(p) = w;
 }
-// Elements i .. i + 7 of an array of type t, i * size a multiple of 16 bytes
-// from an aligned base.
+// Elements i .. i + 7 of an array of type t.
 __device__ __forceinline__ void load8_vec(const void *p, int t, int64_t i, float v[8])
 {
     if (t == GS_DTYPE_F32) load8_vec(static_cast<const float *>(p) + i, v);
@@ -56,23 +57,23 @@ __device__ __forceinline__ void load8_vec(const void *p, int t, int64_t i, float
 // The same for results that are not read again soon: written past the caches.
 __device__ __forceinline__ void store8_stream(void *p, int t, int64_t i, const float v[8])
 {
-    typedef int i4 __attribute__((ext_vector_type(4)));
+    typedef int any4 __attribute__((ext_vector_type(4), aligned(2)));     // at any element's address
     if (t == GS_DTYPE_F32) {
         float *q = static_cast<float *>(p) + i;
 #pragma unroll
         for (int h = 0; h < 2; h++) {
             const Vec<float, 4> w = {{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]}};
-            __builtin_nontemporal_store(__builtin_bit_cast(i4, w), reinterpret_cast<i4 *>(q + 4 * h));
+            __builtin_nontemporal_store(__builtin_bit_cast(any4, w), reinterpret_cast<any4 *>(q + 4 * h));
         }
         return;
     }
-    union { Vec<_Float16, 8> h; Vec<__bf16, 8> b; i4 u; } w;
+    union { Vec<_Float16, 8> h; Vec<__bf16, 8> b; } w;
 #pragma unroll
     for (int k = 0; k < 8; k++) {
         if (t == GS_DTYPE_F16) w.h.v[k] = (_Float16)v[k];
         else w.b.v[k] = (__bf16)v[k];
     }
-    __builtin_nontemporal_store(w.u, reinterpret_cast<i4 *>(static_cast<uint16_t *>(p) + i));
+    __builtin_nontemporal_store(__builtin_bit_cast(any4, w), reinterpret_cast<any4 *>(static_cast<uint16_t *>(p) + i));
 }
 __device__ __forceinline__ void store8_vec(void *p, int t, int64_t i, const float v[8])
 {
@@ -80,11 +81,10 @@ __device__ __forceinline__ void store8_vec(void *p, int t, int64_t i, const floa
     else if (t == GS_DTYPE_F16) store8_vec(static_cast<_Float16 *>(p) + i, v);
     else store8_vec(static_cast<__bf16 *>(p) + i, v);
 }
-// The same without alignment; elements past the first `valid` do not exist and
-// read as 0.
-__device__ __forceinline__ void load8(const void *p, int t, int64_t i, int valid, bool vec, float v[8])
+// Elements past the first `valid` do not exist and read as 0.
+__device__ __forceinline__ void load8(const void *p, int t, int64_t i, int valid, float v[8])
 {
-    if (vec && valid >= 8) {
+    if (valid >= 8) {
         load8_vec(p, t, i, v);
         return;
     }

@@ -35,22 +35,35 @@ template <int KIND, int NL>
 __device__ __forceinline__ void load_piece(Piece<KIND, NL> &f, const void *base, int64_t ld, const uint8_t *scales, int64_t lds, int row,
                                            int k0, int K, int g)
 {
-    const i4 zero = {0, 0, 0, 0};
-    if constexpr (KIND == kMX8) {
+    if constexpr (KIND == kMX8) {                       // k is a multiple of 32
         const uint8_t *p = static_cast<const uint8_t *>(base) + row * ld + k0;
-        f.v[0][0] = k0 + g * 16 < K ? *reinterpret_cast<const i4 *>(p + g * 16) : zero;
-        f.v[0][1] = k0 + 64 + g * 16 < K ? *reinterpret_cast<const i4 *>(p + 64 + g * 16) : zero;
+        using V = Vec<uint8_t, 16>;
+        f.v[0][0] = f.v[0][1] = i4{0, 0, 0, 0};
+        if (k0 + g * 16 < K) f.v[0][0] = __builtin_bit_cast(i4, *reinterpret_cast<const V *>(p + g * 16));
+        if (k0 + 64 + g * 16 < K) f.v[0][1] = __builtin_bit_cast(i4, *reinterpret_cast<const V *>(p + 64 + g * 16));
         f.scale = k0 + g * 32 < K ? scales[row * lds + (k0 >> 5) + g] : 127;
     } else if constexpr (NL == 1) {
-        const uint16_t *p = static_cast<const uint16_t *>(base) + row * ld + k0 + g * 16;
-#pragma unroll
-        for (int h = 0; h < 2; h++) f.v[0][h] = k0 + g * 16 + h * 8 < K ? *reinterpret_cast<const i4 *>(p + h * 8) : zero;
-    } else {
-        const float *p = static_cast<const float *>(base) + row * ld + k0 + g * 16;
+        const uint16_t *p = static_cast<const uint16_t *>(base) + row * ld;
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-            float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (k0 + g * 16 + h * 8 < K) load8_vec(p + h * 8, v);
+            const int k = k0 + g * 16 + h * 8;
+            Vec<uint16_t, 8> v{};
+            if (k + 8 <= K) {
+                v = *reinterpret_cast<const Vec<uint16_t, 8> *>(p + k);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; e++)
+                    if (k + e < K) v.v[e] = p[k + e];
+            }
+            f.v[0][h] = __builtin_bit_cast(i4, v);
+        }
+    } else {
+        const float *p = static_cast<const float *>(base) + row * ld;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const int k = k0 + g * 16 + h * 8;
+            float v[8];
+            load8(p, GS_DTYPE_F32, k, min(8, K - k), v);
             union { uint16_t u[8]; i4 w; } limb[NL];
 #pragma unroll
             for (int e = 0; e < 8; e++) {
