@@ -129,8 +129,9 @@ struct LinearEpilogue {
 struct ProductPlan {
     bool pt, qt;
     bool staged;
-    int tile;                           // 0: 256 x 256, 1: 128 x 128, 2: 64 x 64 (staged: 2; fp32: 1 and 2)
+    int tile;                           // 0: 256 x 256, 1: 128 x 128, 2: 64 x 64 (staged and fp32: 1, 2)
     int splits;                         // of k, each with at least one tile of k
+    double us;                          // estimated time
 };
 
 // out[c] (+)= sum over rows r of part[r][c], in a fixed order (gs_norm.hip).
@@ -139,8 +140,8 @@ hipError_t launch_sum_rows(const float *part, float *out, int n, int rows, int a
 hipError_t launch_product_bf16(const gemm::Args &a, const LinearEpilogue::Args &e, const ProductPlan &plan, hipStream_t s);
 hipError_t launch_product_f16(const gemm::Args &a, const LinearEpilogue::Args &e, const ProductPlan &plan, hipStream_t s);
 hipError_t launch_product_f32(const gemm::Args &a, const LinearEpilogue::Args &e, const ProductPlan &plan, hipStream_t s);
-// At most 64 rows of x (8-bit operands: for a 16-bit y).
-constexpr int kFewRows = 64;
+// At most 16 rows of x (8-bit operands: for a 16-bit y).
+constexpr int kFewRows = 16;
 hipError_t launch_few_rows(const gs_linear &l, const LinearEpilogue::Args &e, hipStream_t s);
 hipError_t launch_product_mx8(const gemm::Args &a, const LinearEpilogue::Args &e, const ProductPlan &plan, hipStream_t s);
 

@@ -9,13 +9,15 @@
 // dw[n][k] = dz^T x, whose operands are read by columns where k is theirs.
 //
 // Operands that cannot be loaded into LDS as they stand (fp32, odd sizes,
-// strides or alignments of 16-bit ones, 8-bit values for an fp32 result) go one of two ways.
-// A result of at most 64 columns or rows reads its long operand once, so the
-// product converts while loading ("staged").  A wider one would convert each
-// element once per tile across it; there one pass first writes both operands
-// as padded 16-bit planes (three bf16 limbs of fp32).  At 692x4032x384 in fp32
-// the backward took 111 us staged and XX packed; at 18846x64x832 the forward
-// takes YY staged and ZZ packed.
+// strides or alignments of 16-bit ones, 8-bit values for an fp32 result) go one
+// of two ways.  Staged, the product converts while loading, once per tile
+// across the result; packed, one pass first writes both operands as padded
+// 16-bit planes (three bf16 limbs of fp32).  Staged is taken where the result's
+// smaller side is at most 256 (8-bit: 128), never for 16-bit operands read by
+// columns.  Staged against packed in us: fp32 72519 x 256 x 832 268 / 319,
+// x 512 463 / 482, 16384 x 1024 x 512 136 / 119; bf16 of odd sizes 72519 x 250 x 830
+// 97 / 132, its transposed products 189 / 133; 8-bit 30000 x 91 x 192 17 / 25,
+// 72519 x 250 x 800 129 / 99.
 #include <string.h>
 
 #include "gs_linear.h"
@@ -33,31 +35,33 @@ size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 // ---- choice of tile and split -----------------------------------------------
 // Estimated time in microseconds of a tile choice: rounds of blocks over the
 // 256 CUs, each CU working through its resident blocks at `rate`, plus what a
-// split of k costs to reduce.  The rates are measured ones at full occupancy.
-struct TileRate { int size, resident; float mflop_us; };        // per CU
+// split of k costs to reduce.  The rates are measured ones at full occupancy;
+// one block by itself reaches `alone` of them.  What a block does before and
+// after its product counts as `around` more of k.
+struct TileRate { int size, resident; float mflop_us, alone; int around; };     // per CU
 
 double product_cost(const TileRate &t, int64_t P, int64_t Q, int64_t K, int splits, float work)
 {
     const double blocks = (double)((P + t.size - 1) / t.size) * (double)((Q + t.size - 1) / t.size) * splits;
     const double per_cu = ceil(blocks / 256.0);
     // fewer blocks than the CU holds leave some of its rate unused
-    const double filled = per_cu < t.resident ? 0.8 + 0.2 * per_cu / t.resident : 1.0;
-    const double tile = 2e-6 * t.size * t.size * (ceil((double)K / splits) + 64.0) * work;
+    const double filled = per_cu < t.resident ? t.alone + (1.0 - t.alone) * (per_cu - 1.0) / (t.resident - 1.0) : 1.0;
+    const double tile = 2e-6 * t.size * t.size * (ceil((double)K / splits) + t.around) * work;
     double us = per_cu * tile / (t.mflop_us * filled);
-    if (splits > 1) us += 3.0 + splits * (0.05 + (double)P * (double)Q * 4.0 / 6e6);
+    if (splits > 1) us += 3.0 + splits * (0.1 + (double)P * (double)Q * 4.0 / 6e6);
     return us;
 }
 
 ProductPlan make_plan(int64_t P, int64_t Q, int64_t K, bool pt, bool qt, bool staged, bool f32, int step_k, float work)
 {
-    static const TileRate direct[3] = {{256, 1, 4.9f}, {128, 2, 4.1f}, {64, 3, 2.4f}};
-    static const TileRate limbs[3] = {{256, 1, 0.0f}, {128, 1, 4.1f}, {64, 2, 3.0f}};
-    static const TileRate staged_[3] = {{256, 1, 0.0f}, {128, 1, 0.0f}, {64, 3, 1.2f}};
-    ProductPlan best{pt, qt, staged, 2, 1};
+    static const TileRate direct[3] = {{256, 1, 4.9f, 1.0f, 64}, {128, 2, 4.1f, 0.9f, 64}, {64, 3, 2.4f, 0.87f, 64}};
+    static const TileRate limbs[3] = {{256, 1, 0.0f, 1.0f, 64}, {128, 1, 4.1f, 1.0f, 64}, {64, 2, 3.0f, 0.9f, 64}};
+    static const TileRate staged_[3] = {{256, 1, 0.0f, 1.0f, 64}, {128, 1, 3.3f, 1.0f, 128}, {64, 3, 2.5f, 0.4f, 64}};
+    ProductPlan best{pt, qt, staged, 2, 1, 0.0};
     double least = 1e30;
     const int64_t nt = (K + step_k - 1) / step_k;
     // three limbs of a 256 tile exceed the LDS
-    for (int tile = staged ? 2 : f32 ? 1 : 0; tile < 3; tile++) {
+    for (int tile = staged || f32 ? 1 : 0; tile < 3; tile++) {
         const TileRate &t = staged ? staged_[tile] : f32 ? limbs[tile] : direct[tile];
         for (int64_t want = 1; want <= 64 && want <= nt; want = want < 4 ? want + 1 : want * 2) {
             const int64_t per = (nt + want - 1) / want;
@@ -70,7 +74,18 @@ ProductPlan make_plan(int64_t P, int64_t Q, int64_t K, bool pt, bool qt, bool st
             }
         }
     }
+    best.us = least;
     return best;
+}
+
+// The same of the way for few rows, as measured: a workgroup takes 16 outputs,
+// so without enough of them for every CU a long k is better split over tiles.
+// One row of 16384 to 64 outputs in bf16 takes 20 us against 9.0 by tiles, to
+// 4096 outputs 26 against 24.5; of 1024 to 4096 4.2 against 6.5.
+double few_rows_cost(const gs_linear &l)
+{
+    const double per_k = l.dtype == GS_DTYPE_F32 ? 3.9e-3 : l.dtype == GS_DTYPE_MXFP8 ? 0.9e-3 : 1.3e-3;
+    return 2.2 + per_k * l.k * (l.n > 4096 ? l.n / 4096.0 : 1.0);
 }
 
 // ---- operands as padded 16-bit planes -----------------------------------------
@@ -184,7 +199,8 @@ void finish_plan(Product &r, bool p_ok, bool q_ok)
 {
     const bool pt = r.plan.pt, qt = r.plan.qt;
     const int least = r.a.P < r.a.Q ? r.a.P : r.a.Q;
-    r.way = p_ok && q_ok ? kDirect : least <= 64 ? kStaged : kPacked;
+    const int staged_up_to = r.type == GS_DTYPE_F32 ? 256 : r.type == GS_DTYPE_MXFP8 ? 128 : pt ? 0 : 256;
+    r.way = p_ok && q_ok ? kDirect : least <= staged_up_to ? kStaged : kPacked;
     r.pack_p = r.way == kPacked && (!p_ok || r.type == GS_DTYPE_MXFP8);
     r.pack_q = r.way == kPacked && (!q_ok || r.type == GS_DTYPE_MXFP8);
     const bool mx = r.type == GS_DTYPE_MXFP8 && r.way == kDirect, f32 = r.type == GS_DTYPE_F32;
@@ -334,12 +350,12 @@ FwdPlan plan_fwd(const gs_linear &l)
     // of a sum than fp32 holds
     if (l.dtype == GS_DTYPE_MXFP8)
         p_ok = q_ok = p_ok && q_ok && l.y_dtype != GS_DTYPE_F32 && a.ldps < (1 << 22) && a.ldqs < (1 << 22);
-    if (l.m <= kFewRows && !(l.dtype == GS_DTYPE_MXFP8 && l.y_dtype == GS_DTYPE_F32)) {
-        r.way = kFew;                           // one value at a time: no tile, split or vector rule
-        r.e.exact = exact_results(r.e);
+    finish_plan(r, p_ok, q_ok);
+    if (l.m <= kFewRows && !(l.dtype == GS_DTYPE_MXFP8 && l.y_dtype == GS_DTYPE_F32) &&
+        few_rows_cost(l) < r.plan.us + 1.8) {
+        r.way = kFew;                           // no workspace
         return f;
     }
-    finish_plan(r, p_ok, q_ok);
     if (r.pack_p) {
         f.p_at = f.bytes;
         f.bytes += packed_bytes(l.dtype, a.P, l.k);

@@ -10,7 +10,10 @@ template <int KIND, bool PT, bool QT>
 hipError_t launch_product_16(const gemm::Args &a, const LinearEpilogue::Args &e, const ProductPlan &plan, hipStream_t s)
 {
     using E = LinearEpilogue;
-    if (plan.staged) return gemm::launch<KIND, 1, 2, 32, 64, 64, 2, 2, PT, QT, true, false, E>(a, e, plan.splits, 1, s);
+    if constexpr (!PT) {
+        if (plan.staged && plan.tile == 1) return gemm::launch<KIND, 1, 2, 32, 128, 128, 2, 4, PT, QT, true, false, E>(a, e, plan.splits, 1, s);
+        if (plan.staged) return gemm::launch<KIND, 1, 2, 32, 64, 64, 2, 2, PT, QT, true, false, E>(a, e, plan.splits, 1, s);
+    }
     if (plan.tile == 0) return gemm::launch<KIND, 1, 2, 64, 256, 256, 2, 4, PT, QT, false, true, E>(a, e, plan.splits, 1, s);
     if (plan.tile == 1) {
         // a block alone on its CU wants a third stage on the way, two blocks

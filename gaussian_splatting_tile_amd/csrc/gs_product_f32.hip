@@ -9,6 +9,7 @@ template <bool PT, bool QT>
 static hipError_t launch_tiles(const gemm::Args &a, const LinearEpilogue::Args &e, const ProductPlan &plan, hipStream_t s)
 {
     using E = LinearEpilogue;
+    if (plan.staged && plan.tile == 1) return gemm::launch<gemm::kBF16, 3, 2, 32, 128, 128, 2, 4, PT, QT, true, false, E>(a, e, plan.splits, 1, s);
     if (plan.staged) return gemm::launch<gemm::kBF16, 3, 2, 32, 64, 64, 2, 2, PT, QT, true, false, E>(a, e, plan.splits, 1, s);
     if (plan.tile == 1) return gemm::launch<gemm::kBF16, 3, 3, 32, 128, 128, 2, 4, PT, QT, false, false, E>(a, e, plan.splits, 1, s);
     return gemm::launch<gemm::kBF16, 3, 3, 32, 64, 64, 2, 2, PT, QT, false, false, E>(a, e, plan.splits, 1, s);
