@@ -286,7 +286,7 @@ __global__ __launch_bounds__(kThreads) void reduce_splits(typename NsEpilogue<NL
 
 // Tile and splits of one product of a batch.
 struct NsProduct {
-    int tile;                                   // 128 or 64
+    int tile;                                   // 128, 64 or 32
     int splits;
 };
 NsProduct choose(int P, int Q, int K, int batch, bool symmetric, int nl);
@@ -336,27 +336,30 @@ MuonPlan plan_muon(const gs_muon &m)
     return p;
 }
 
-// Estimated time in microseconds, from measured steps: a 128 tile of 8 waves
-// takes 0.66 us per 32 k with three products and 1.2 with six, a 64 tile 0.24
-// and 0.38, beside others on its CU as alone; a split costs a launch and its
-// sums' way to memory and back.
+// Estimated time in microseconds: rounds of blocks over the 256 CUs, each with
+// its start and end and so many 64 k; a split costs a launch and its sums' way to
+// memory and back.  A product of the iteration, on average over its three, in
+// us by tiles of 128 / 64 / 32: 256 x 256 in three limbs 16.7 / 7.5 / 5.9, 8 of them
+// 16.8 / 7.7 / 7.2, 1024 x 1024 41.3 / 16.9 / 23.9, 4 of them 46.6 / 52.0 / 68.4; in two
+// limbs 256 x 256 12.0 / 6.0 / 5.0, 4 of 1024 x 1024 29.2 / 34.6 / 42.4.
 NsProduct choose(int P, int Q, int K, int batch, bool symmetric, int nl)
 {
+    static const struct { int tile, step_k; float start, us3, us2; } kTiles[3] = {{128, 32, 3.0f, 2.3f, 1.3f}, {64, 64, 1.2f, 0.77f, 0.46f}, {32, 64, 0.5f, 0.62f, 0.38f}};
     NsProduct best{64, 1};
     double least = 1e30;
-    const int nt = (K + 31) / 32;
-    for (int tile = 128; tile >= 64; tile /= 2) {
-        const int tp = (P + tile - 1) / tile, tq = (Q + tile - 1) / tile;
+    for (const auto &t : kTiles) {
+        const int tp = (P + t.tile - 1) / t.tile, tq = (Q + t.tile - 1) / t.tile, nt = (K + t.step_k - 1) / t.step_k;
         const double tiles = (double)(symmetric ? tp * (tp + 1) / 2 : tp * tq) * batch;
         for (int want = 1; want <= 8 && want <= nt; want++) {
             const int per = (nt + want - 1) / want, splits = (nt + per - 1) / per;
-            const double rounds = ceil(tiles * splits / 256.0);
-            const double step = nl == 3 ? (tile == 128 ? 1.2 : 0.38) : tile == 128 ? 0.66 : 0.24;
-            double us = rounds * per * step + (tile == 128 ? 5.0 : 4.0);
-            if (splits > 1) us += 5.0 + tiles * splits * tile * tile * 8.0 / 6e6;
+            double rounds = tiles * splits / 256.0;
+            // one block a CU, or (32) several that share its time
+            rounds = t.tile > 32 ? ceil(rounds) : rounds > 1.0 ? rounds : 1.0;
+            double us = 3.2 + rounds * (t.start + per * t.step_k / 64.0 * (nl == 3 ? t.us3 : t.us2));
+            if (splits > 1) us += 5.0 + tiles * splits * t.tile * t.tile * 8.0 / 6e6;
             if (us < least * 0.97) {
                 least = us;
-                best.tile = tile;
+                best.tile = t.tile;
                 best.splits = splits;
             }
         }
@@ -374,8 +377,9 @@ hipError_t launch_product(gemm::Args a, typename NsEpilogue<NL>::Args e, float *
     e.partial = c.splits > 1 ? partial : nullptr;
     e.ld_partial = a.P;
     e.split_stride = (int64_t)a.P * a.Q;
-    hipError_t err = c.tile == 128 ? gemm::launch<gemm::kBF16, NL, 3, 32, 128, 128, 2, 4, PT, false, false, false, E>(a, e, c.splits, batch, s)
-                                   : gemm::launch<gemm::kBF16, NL, 3, 32, 64, 64, 2, 2, PT, false, false, false, E>(a, e, c.splits, batch, s);
+    hipError_t err = c.tile == 128  ? gemm::launch<gemm::kBF16, NL, 3, 32, 128, 128, 2, 4, PT, false, false, false, E>(a, e, c.splits, batch, s)
+                     : c.tile == 64 ? gemm::launch<gemm::kBF16, NL, 3, 64, 64, 64, 2, 4, PT, false, false, false, E>(a, e, c.splits, batch, s)
+                                    : gemm::launch<gemm::kBF16, NL, 3, 64, 32, 32, 2, 2, PT, false, false, false, E>(a, e, c.splits, batch, s);
     if (err != hipSuccess || c.splits == 1) return err;
     const int tp = (a.P + 63) / 64, tq = (a.Q + 63) / 64;
     reduce_splits<NL><<<dim3((unsigned)(symmetric ? tp * (tp + 1) / 2 : tp * tq), (unsigned)batch), kThreads, 0, s>>>(e, a.P, a.Q, symmetric);
