@@ -232,8 +232,8 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _stream(stream=None):
     if stream is None:
-        # with the device given, torch looks the stream up in a third of the time
-        stream = torch.cuda.current_stream(torch.cuda.current_device())
+        # the handle alone: making a Stream object of it takes 1.3 us, a tenth of a small call
+        return C.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     return C.c_void_p(stream.cuda_stream)
 
 
@@ -352,7 +352,7 @@ def bin_sort_workspace_bytes(n: int, k_capacity: int, n_tiles: int) -> int:
 
 
 def _nbytes(t):
-    return 0 if t is None else t.numel() * t.element_size()
+    return 0 if t is None else t.nbytes
 
 
 def schedule_words(width: int, height: int) -> int:
