@@ -231,37 +231,34 @@ template <int NL> struct NsEpilogue {
     __device__ static __forceinline__ void store1(const Args &, int, int, float, int, int) {}  // never: 8 | P
 };
 
-// Sum of the splits of k in their order and the epilogue, a 64 x 64 tile a
-// workgroup; a symmetric result is summed on one side of the diagonal and
-// turned round in LDS for the other.
+// Sum of the splits of k in their order and the epilogue, 32 rows q of a 64 x 64
+// tile a workgroup, 8 p a thread; a symmetric result is summed on one side of
+// the diagonal and turned round in LDS for the other.
 template <int NL>
 __global__ __launch_bounds__(kThreads) void reduce_splits(typename NsEpilogue<NL>::Args e, int P, int Q, int symmetric)
 {
     using E = NsEpilogue<NL>;
-    __shared__ float tile[64][65];
+    __shared__ float tile[32][65];
     int tp, tq;
-    const int tiles_p = (P + 63) / 64;
+    const int tiles_p = (P + 63) / 64, t = blockIdx.x / 2, half = blockIdx.x % 2 * 32;
     if (symmetric) {
-        gemm::triangle_of(blockIdx.x, tp, tq);
+        gemm::triangle_of(t, tp, tq);
     } else {
-        tp = blockIdx.x % tiles_p;
-        tq = blockIdx.x / tiles_p;
+        tp = t % tiles_p;
+        tq = t / tiles_p;
     }
-    const float *part = e.partial + (int64_t)blockIdx.y * e.splits * e.split_stride;
-    typename E::Args whole = e;
-    whole.partial = nullptr;
-    const int pl = threadIdx.x % 8 * 8;
-#pragma unroll
-    for (int h = 0; h < 64; h += 32) {
-        const int ql = h + threadIdx.x / 8, p = tp * 64 + pl, q = tq * 64 + ql;
-        if (p >= P || q >= Q) continue;
-        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    const int pl = threadIdx.x % 8 * 8, ql = threadIdx.x / 8, p = tp * 64 + pl, q = tq * 64 + half + ql;
+    if (p < P && q < Q) {
+        const float *part = e.partial + (int64_t)blockIdx.y * e.splits * e.split_stride + (int64_t)q * e.ld_partial + p;
+        typename E::Args whole = e;
+        whole.partial = nullptr;
         typename E::Ahead ahead;
         E::look_ahead(whole, p, q, blockIdx.y, ahead);
-#pragma unroll 4
+        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 8
         for (int s = 0; s < e.splits; s++) {
             float w[8];
-            load8_vec(part + s * e.split_stride + (int64_t)q * e.ld_partial + p, w);
+            load8_vec(part + s * e.split_stride, w);
 #pragma unroll
             for (int i = 0; i < 8; i++) v[i] += w[i];
         }
@@ -273,15 +270,13 @@ __global__ __launch_bounds__(kThreads) void reduce_splits(typename NsEpilogue<NL
     }
     if (!symmetric || tp == tq) return;
     __syncthreads();
+    // the mirrored tile: p and q change places
+    const int mp = tq * 64 + half + threadIdx.x % 4 * 8, mq = tp * 64 + threadIdx.x / 4;
+    if (mp >= P || mq >= Q) return;
+    float v[8];
 #pragma unroll
-    for (int h = 0; h < 64; h += 32) {
-        const int ql = h + threadIdx.x / 8, p = tq * 64 + pl, q = tp * 64 + ql;     // the mirrored tile's
-        if (p >= P || q >= Q) continue;
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; i++) v[i] = tile[pl + i][ql];
-        E::write_limbs(e, p, q, v, blockIdx.y);
-    }
+    for (int i = 0; i < 8; i++) v[i] = tile[threadIdx.x % 4 * 8 + i][threadIdx.x / 4];
+    E::write_limbs(e, mp, mq, v, blockIdx.y);
 }
 
 // Tile and splits of one product of a batch.
@@ -382,7 +377,7 @@ hipError_t launch_product(gemm::Args a, typename NsEpilogue<NL>::Args e, float *
                                     : gemm::launch<gemm::kBF16, NL, 3, 64, 32, 32, 2, 2, PT, false, false, false, E>(a, e, c.splits, batch, s);
     if (err != hipSuccess || c.splits == 1) return err;
     const int tp = (a.P + 63) / 64, tq = (a.Q + 63) / 64;
-    reduce_splits<NL><<<dim3((unsigned)(symmetric ? tp * (tp + 1) / 2 : tp * tq), (unsigned)batch), kThreads, 0, s>>>(e, a.P, a.Q, symmetric);
+    reduce_splits<NL><<<dim3((unsigned)(symmetric ? tp * (tp + 1) : 2 * tp * tq), (unsigned)batch), kThreads, 0, s>>>(e, a.P, a.Q, symmetric);
     return hipGetLastError();
 }
 
