@@ -479,50 +479,55 @@ template <typename T> __global__ __launch_bounds__(kThreads) void dz_rows_ahead(
     column_sums(d, groups, acc, sums);
 }
 
-// dy in planes [n][m]: tiles of 64 columns x 64 rows turned round in LDS.
-__global__ __launch_bounds__(kThreads) void dz_planes(DzArgs d)
+// dy in planes [n][m]: tiles of 64 columns x 32 rows, read 8 rows of a column at
+// a time, turned round in LDS and written 8 columns of a row at a time; the
+// next tile is on its way meanwhile.
+constexpr int kPlaneRows = 32;
+
+template <bool EXACT> __global__ __launch_bounds__(kThreads) void dz_planes(DzArgs d)
 {
-    __shared__ float tile[64][65];
-    const int c0 = blockIdx.x * 64, tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
+    __shared__ float tile[64][kPlaneRows + 1];
+    __shared__ float sums[kThreads][8];
+    constexpr int kGroups = 8;                  // of 8 columns
+    const int cg = threadIdx.x % kGroups, rl = threadIdx.x / kGroups;
+    const int c0 = (blockIdx.x * kGroups + cg) * 8, valid = max(0, min(8, d.n - c0));
+    const int column = blockIdx.x * 64 + threadIdx.x / 4, rows_at = threadIdx.x % 4 * 8;
     const int64_t r0 = (int64_t)blockIdx.y * d.rows_per_block, r1 = min(d.m, r0 + d.rows_per_block);
-    const int c = c0 + tx;                      // this thread's column of dz
-    float acc = 0.0f;
-    for (int64_t r = r0; r < r1; r += 64) {
-        float in[16];                           // all loads under way at once
+    const bool room = c0 < d.ld_dz;             // ld_dz is a multiple of 8
+    float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0}, in[8], z[8];
+    auto fetch = [&](int64_t r) {
+        const int there = column < d.n ? (int)max((int64_t)0, min((int64_t)8, r1 - r - rows_at)) : 0;
+        load8(d.dy, d.dy_type, (int64_t)column * d.lddy + r + rows_at, there, in);
+        if (d.act != GS_ACT_NONE) load8(d.z, d.type, (r + rl) * d.ldz + c0, r + rl < r1 ? valid : 0, z);
+    };
+    fetch(r0);
+    for (int64_t r = r0; r < r1; r += kPlaneRows) {
 #pragma unroll
-        for (int k = 0; k < 16; k++) {
-            const int i = ty + 4 * k;
-            in[k] = c0 + i < d.n && r + tx < r1 ? load_as_float(d.dy, d.dy_type, (int64_t)(c0 + i) * d.lddy + r + tx) : 0.0f;
-        }
-#pragma unroll
-        for (int k = 0; k < 16; k++) tile[ty + 4 * k][tx] = in[k];
+        for (int j = 0; j < 8; j++) tile[threadIdx.x / 4][rows_at + j] = in[j];
         __syncthreads();
-#pragma unroll 4
-        for (int i = ty; i < 64 && r + i < r1; i += 4) {
-            float v = tile[tx][i];
-            if (d.act != GS_ACT_NONE && c < d.n) {
-                const float z = load_as_float(d.z, d.type, (r + i) * d.ldz + c);
-                if (d.exact) scale_by_slope<1, true>(&v, &z, d.act);
-                else scale_by_slope<1, false>(&v, &z, d.act);
-            }
-            acc += v;
-            if (c < d.ld_dz) {
-                const int64_t at = (r + i) * d.ld_dz + c;
-                if (d.dz) store_from_float(d.dz, d.type, at, v);
-                if (d.limbs) {
-                    uint16_t limb[3];
-                    split_limbs<3>(v, limb);
+        float v[8], at_z[8];
 #pragma unroll
-                    for (int l = 0; l < 3; l++) d.limbs[l * d.m * d.ld_dz + at] = limb[l];
-                }
-            }
+        for (int j = 0; j < 8; j++) {
+            v[j] = tile[cg * 8 + j][rl];
+            at_z[j] = z[j];
         }
         __syncthreads();
+        if (r + kPlaneRows < r1) fetch(r + kPlaneRows);
+        if (d.act != GS_ACT_NONE) {
+            if constexpr (EXACT) {              // one at a time: eight library erfs at once take many registers
+#pragma unroll 1
+                for (int j = 0; j < 8; j++) scale_by_slope<1, true>(v + j, at_z + j, d.act);
+            } else {
+                scale_by_slope<8, false>(v, at_z, d.act);       // outside: 0 times the slope at 0
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j++) acc[j] += v[j];
+        if (!room || r + rl >= r1) continue;
+        if (d.dz) store8_vec(d.dz, d.type, (r + rl) * d.ld_dz + c0, v);
+        if (d.limbs) store_planes(d.limbs, d.m * d.ld_dz, (r + rl) * d.ld_dz + c0, 3, 0, v);
     }
-    if (!d.part) return;
-    tile[ty][tx] = acc;
-    __syncthreads();
-    if (ty == 0 && c < d.n) d.part[(int64_t)blockIdx.y * d.n + c] = tile[0][tx] + tile[1][tx] + tile[2][tx] + tile[3][tx];
+    column_sums(d, kGroups, acc, sums);
 }
 
 // Everything a backward call does, with its places in the workspace.
@@ -581,7 +586,7 @@ BwdPlan plan_bwd(const gs_linear &l, const gs_linear_grads &g)
     int64_t want = 2048 / cols;
     want = want < 1 ? 1 : want > 1024 ? 1024 : want;
     int64_t per = (l.m + want - 1) / want;
-    const int64_t whole = l.planes ? 64 : 8;            // rows that a block works on at a time
+    const int64_t whole = l.planes ? kPlaneRows : 8;    // rows that a block works on at a time
     per = (per + whole - 1) / whole * whole;
     if (per < whole) per = whole;
     b.rows_per_block = (int)per;
@@ -659,7 +664,9 @@ hipError_t run_bwd(const gs_linear &l, const gs_linear_grads &g, BwdPlan &b, cha
         d.n = l.n;
         d.rows_per_block = b.rows_per_block;
         if (l.planes) {
-            dz_planes<<<dim3((unsigned)((l.n + 63) / 64), (unsigned)b.row_blocks), kThreads, 0, s>>>(d);
+            const dim3 grid((unsigned)((l.n + 63) / 64), (unsigned)b.row_blocks);
+            if (d.exact) dz_planes<true><<<grid, kThreads, 0, s>>>(d);
+            else dz_planes<false><<<grid, kThreads, 0, s>>>(d);
         } else {
             int groups = 1;                     // of 8 columns: a power of two, at most 64
             while (groups < 64 && groups * 8 < l.n) groups *= 2;
