@@ -530,6 +530,8 @@ template <bool EXACT> __global__ __launch_bounds__(kThreads) void dz_planes(DzAr
     column_sums(d, kGroups, acc, sums);
 }
 
+constexpr int kOneRowBlock = 64;                // rows of x that one row block of the pass takes
+
 // Everything a backward call does, with its places in the workspace.
 struct BwdPlan {
     bool own_dz;                        // dz is written to the workspace in `dtype` (else dz is dy where that is read)
@@ -581,7 +583,8 @@ BwdPlan plan_bwd(const gs_linear &l, const gs_linear_grads &g)
     b.pass = b.own_dz || b.limbs || g.db;
 
     // row blocks of the pass: enough for the device, at most 1024 (the partial
-    // sums are read once more)
+    // sums are read once more); one for few rows, whose sums are then db itself
+    // and save a launch
     const int64_t cols = l.planes ? (l.n + 63) / 64 : (l.n + 511) / 512;
     int64_t want = 2048 / cols;
     want = want < 1 ? 1 : want > 1024 ? 1024 : want;
@@ -589,6 +592,7 @@ BwdPlan plan_bwd(const gs_linear &l, const gs_linear_grads &g)
     const int64_t whole = l.planes ? kPlaneRows : 8;    // rows that a block works on at a time
     per = (per + whole - 1) / whole * whole;
     if (per < whole) per = whole;
+    if (l.m <= kOneRowBlock) per = kOneRowBlock;
     b.rows_per_block = (int)per;
     b.row_blocks = (int)((l.m + per - 1) / per);
     auto take = [&](size_t bytes) {
@@ -659,7 +663,8 @@ hipError_t run_bwd(const gs_linear &l, const gs_linear_grads &g, BwdPlan &b, cha
         d.dz = b.own_dz ? ws + b.dz_at : nullptr;
         d.limbs = b.limbs ? reinterpret_cast<uint16_t *>(ws + b.limbs_at) : nullptr;
         d.ld_dz = b.ld_dz;
-        d.part = g.db ? reinterpret_cast<float *>(ws + b.part_at) : nullptr;
+        const bool sum = g.db && (b.row_blocks > 1 || g.accumulate);
+        d.part = sum ? reinterpret_cast<float *>(ws + b.part_at) : g.db;
         d.m = l.m;
         d.n = l.n;
         d.rows_per_block = b.rows_per_block;
@@ -668,8 +673,10 @@ hipError_t run_bwd(const gs_linear &l, const gs_linear_grads &g, BwdPlan &b, cha
             if (d.exact) dz_planes<true><<<grid, kThreads, 0, s>>>(d);
             else dz_planes<false><<<grid, kThreads, 0, s>>>(d);
         } else {
-            int groups = 1;                     // of 8 columns: a power of two, at most 64
-            while (groups < 64 && groups * 8 < l.n) groups *= 2;
+            // of 8 columns: a power of two, at most 64; few where one block takes all rows
+            const int most = l.m <= kOneRowBlock ? 8 : 64;
+            int groups = 1;
+            while (groups < most && groups * 8 < l.n) groups *= 2;
             const dim3 grid((unsigned)((l.n + groups * 8 - 1) / (groups * 8)), (unsigned)b.row_blocks);
             const bool ahead = d.dz && !d.limbs && l.n % 8 == 0 && l.activation != GS_ACT_NONE && l.y_dtype == l.dtype;
             if (ahead && l.dtype == GS_DTYPE_BF16) dz_rows_ahead<__bf16><<<grid, kThreads, 0, s>>>(d, groups);
@@ -677,9 +684,7 @@ hipError_t run_bwd(const gs_linear &l, const gs_linear_grads &g, BwdPlan &b, cha
             else dz_rows<<<grid, kThreads, 0, s>>>(d, groups);
         }
         if ((err = hipGetLastError()) != hipSuccess) return err;
-        if (g.db) {
-            if ((err = launch_sum_rows(d.part, g.db, l.n, b.row_blocks, g.accumulate, s)) != hipSuccess) return err;
-        }
+        if (sum && (err = launch_sum_rows(d.part, g.db, l.n, b.row_blocks, g.accumulate, s)) != hipSuccess) return err;
     }
     PackJobs jobs;
     memset(&jobs, 0, sizeof jobs);
