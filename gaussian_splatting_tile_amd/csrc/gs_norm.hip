@@ -434,6 +434,7 @@ int grad_blocks(int64_t m, int n)
     if (n > kMaxRegRow) return (int)(m < 64 ? m : 64);
     const int64_t rows = n <= 128 ? 16 : n <= 256 ? 8 : n <= 1024 ? 4 : 1;
     const int64_t passes = (m + rows - 1) / rows, most = n <= 2048 ? 1024 : 512;
+    if (passes <= 4) return 1;                  // its partial row is dgamma: one launch
     if (passes <= 256) return (int)passes;
     const int64_t each = n <= 1024 ? 2 : 4, want = passes / each > 256 ? passes / each : 256;
     return (int)(want < most ? want : most);
@@ -597,7 +598,9 @@ gs_status gs_rms_norm_bwd(const gs_rms_norm_grads *p, void *workspace, size_t wo
     a.rstd = p->rstd;
     a.gamma = p->gamma;
     a.dx = p->dx;
-    a.part = p->dgamma ? static_cast<float *>(workspace) : nullptr;
+    const int blocks = grad_blocks(p->m, p->n);
+    const bool add = p->dgamma && (blocks > 1 || p->accumulate);
+    a.part = add ? static_cast<float *>(workspace) : p->dgamma;
     a.m = p->m;
     a.lds = p->sum_stride;
     a.ldy = p->dy_stride;
@@ -606,9 +609,7 @@ gs_status gs_rms_norm_bwd(const gs_rms_norm_grads *p, void *workspace, size_t wo
     a.n = p->n;
     hipError_t e = p->dtype == GS_DTYPE_F32 ? launch_grad<float>(a, s)
                    : p->dtype == GS_DTYPE_F16 ? launch_grad<_Float16>(a, s) : launch_grad<__bf16>(a, s);
-    if (e == hipSuccess && p->dgamma) {
-        e = launch_sum_rows(a.part, p->dgamma, p->n, grad_blocks(p->m, p->n), p->accumulate, s);
-    }
+    if (e == hipSuccess && add) e = launch_sum_rows(a.part, p->dgamma, p->n, blocks, p->accumulate, s);
     return from_hip(e);
 }
 
