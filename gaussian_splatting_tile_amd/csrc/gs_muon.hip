@@ -10,6 +10,9 @@
 // end.  fp32 results take three limbs, 16-bit results two: an iteration
 // amplifies an error in a weak direction up to |a| times, 2^-16 grows to about
 // 2^-11 in five, where one bf16 limb would lose the direction.
+//
+// A matrix that fits the LDS of a CU is iterated by one workgroup from its
+// gradient to its weight.
 #include <string.h>
 
 #include "gs_gemm.h"
@@ -283,16 +286,270 @@ __global__ __launch_bounds__(kThreads) void reduce_splits(typename NsEpilogue<NL
 struct NsProduct {
     int tile;                                   // 128, 64 or 32
     int splits;
+    double us;                                  // estimated time
 };
 NsProduct choose(int P, int Q, int K, int batch, bool symmetric, int nl);
+
+// Whether a symmetric product's tiles are multiplied on one side of the diagonal
+// only: the sums of splits are taken by 64 x 64, so smaller tiles of them all.
+bool one_side(int tile, int splits) { return tile >= 64 || splits == 1; }
+
+// ---- small matrices: all iterations in one workgroup --------------------------
+// X and A (then B in its place) stay in LDS as limbs, rows padded by 16 bytes so
+// that neither 16 rows of a chunk nor 4 lines of a transposed read meet in a
+// bank.  A wave takes pairs of 16 x 16 results side by side; the sums wait in
+// registers until every wave has read what they replace.
+constexpr int kSmallThreads = 1024, kSmallWaves = kSmallThreads / 64;
+constexpr int kSmallLds = 158 * 1024;
+constexpr int kSmallPairs = 4;                  // pairs of results of X per wave
+
+struct Small {
+    Update u;
+    int rows, cols, tall, r, f, steps;
+    float a, b, c, eps, decay, rate;
+    void *out;
+    const void *weight;
+    int out_type;
+};
+
+struct LdsMatrix {                              // [limbs][rows][pitch]
+    uint16_t *at;
+    int pitch, plane;
+};
+
+// Limbs of rows x0 .. x0 + 15 at k = 32 kk .. 32 kk + 31; T: of columns x0 ..
+template <int NL, bool T> __device__ __forceinline__ void small_fragment(const LdsMatrix &m, int x0, int kk, int lane, gemm::i4 v[NL])
+{
+    const int g = lane >> 4, r = lane & 15;
+#pragma unroll
+    for (int l = 0; l < NL; l++) {
+        const uint16_t *p = m.at + l * m.plane;
+        if constexpr (!T) {
+            v[l] = *reinterpret_cast<const gemm::i4 *>(p + (x0 + r) * m.pitch + kk * 32 + g * 8);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const uint16_t *a = p + (kk * 32 + g * 8 + h * 4 + (r >> 2)) * m.pitch + x0 + (r & 3) * 4;
+                const int2 w = __builtin_bit_cast(
+                    int2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) gemm::s4 *)a));
+                v[l][2 * h] = w.x;
+                v[l][2 * h + 1] = w.y;
+            }
+        }
+    }
+}
+
+// acc[j] = this wave's j-th pair of results, q0[j] .. + 15 by p0[j] .. + 31
+template <int NL, int PAIRS, bool PT>
+__device__ __forceinline__ void small_product(const LdsMatrix &P, const LdsMatrix &Q, int K, int mine, const int p0[PAIRS], const int q0[PAIRS], int lane,
+                                              gemm::f4 acc[PAIRS][2])
+{
+#pragma unroll
+    for (int j = 0; j < PAIRS; j++) acc[j][0] = acc[j][1] = gemm::f4{0, 0, 0, 0};
+    asm volatile("" : "+v"(lane));
+#pragma unroll 1
+    for (int kk = 0; kk < K / 32; kk++) {
+#pragma unroll
+        for (int j = 0; j < PAIRS; j++) {
+            __builtin_amdgcn_sched_barrier(0);          // one pair's fragments in registers at a time
+            if (j >= mine) continue;
+            gemm::i4 q[NL], p[2][NL];
+            small_fragment<NL, false>(Q, q0[j], kk, lane, q);
+            small_fragment<NL, PT>(P, p0[j], kk, lane, p[0]);
+            small_fragment<NL, PT>(P, p0[j] + 16, kk, lane, p[1]);
+#pragma unroll
+            for (int order = NL - 1; order >= 0; order--)
+#pragma unroll
+                for (int l = 0; l <= order; l++)
+#pragma unroll
+                    for (int i = 0; i < 2; i++) acc[j][i] = gemm::mfma32<gemm::kBF16>(p[i][l], q[order - l], acc[j][i]);
+        }
+    }
+}
+
+// A lane's sums hold p + (0..3) of one q.
+template <int NL> __device__ __forceinline__ void small_read(const LdsMatrix &m, int p, int q, float v[4])
+{
+#pragma unroll
+    for (int i = 0; i < 4; i++) v[i] = 0.0f;
+#pragma unroll
+    for (int l = NL - 1; l >= 0; l--) {
+        const gemm::s4 w = *reinterpret_cast<const gemm::s4 *>(m.at + l * m.plane + q * m.pitch + p);
+#pragma unroll
+        for (int i = 0; i < 4; i++) v[i] += limb_value((uint16_t)w[i]);
+    }
+}
+template <int NL> __device__ __forceinline__ void small_write(const LdsMatrix &m, int p, int q, const gemm::f4 &v)
+{
+    gemm::s4 w[NL];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        uint16_t limb[NL];
+        split_limbs<NL>(v[i], limb);
+#pragma unroll
+        for (int l = 0; l < NL; l++) w[l][i] = (short)limb[l];
+    }
+#pragma unroll
+    for (int l = 0; l < NL; l++) *reinterpret_cast<gemm::s4 *>(m.at + l * m.plane + q * m.pitch + p) = w[l];
+}
+
+template <int NL> __global__ __launch_bounds__(kSmallThreads) void small_matrices(Small s)
+{
+    __shared__ __align__(16) uint16_t lds[kSmallLds / 2];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const Update &u = s.u;
+    const int64_t base = (int64_t)blockIdx.x * u.size;
+    const int size = (int)u.size;
+    const LdsMatrix X{lds, s.f + 8, s.r * (s.f + 8)}, A{lds + NL * X.plane, s.r + 8, s.r * (s.r + 8)};
+
+    // momentum and the norm in fp64, as for larger matrices
+    double sq = 0.0;
+#pragma unroll 4
+    for (int i = tid; i < size; i += kSmallThreads) {
+        if (u.momentum) u.momentum_out[base + i] = fmaf(u.beta, u.momentum[base + i], load_as_float(u.grad, u.grad_type, base + i));
+        const double x = update_at(u, base + i);
+        sq = fma(x, x, sq);
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) sq += __shfl_xor(sq, o);
+    double *sums = reinterpret_cast<double *>(A.at);
+    if (lane == 0) sums[wave] = sq;
+    for (int i = tid; i < NL * X.plane / 8; i += kSmallThreads) reinterpret_cast<uint4 *>(X.at)[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    sq = 0.0;
+#pragma unroll
+    for (int w = 0; w < kSmallWaves; w++) sq += sums[w];
+    const double inv = 1.0 / (sqrt(sq) + (double)s.eps);
+#pragma unroll 4
+    for (int i = tid; i < size; i += kSmallThreads) {
+        const int row = i / s.cols, col = i - row * s.cols;
+        uint16_t limb[NL];
+        split_limbs<NL>((float)(update_at(u, base + i) * inv), limb);
+        const int at = s.tall ? col * X.pitch + row : row * X.pitch + col;
+#pragma unroll
+        for (int l = 0; l < NL; l++) X.at[l * X.plane + at] = limb[l];
+    }
+    __syncthreads();
+
+    // this wave's pairs of results of A and of X
+    constexpr int kPairsA = 2;                  // r up to 128
+    int ap[kPairsA], aq[kPairsA], xp[kSmallPairs], xq[kSmallPairs], mine_a = 0, mine_x = 0;
+    const int across_a = s.r / 32, across_x = s.f / 32;
+#pragma unroll
+    for (int j = 0; j < kPairsA; j++) {
+        const int t = wave + j * kSmallWaves;
+        aq[j] = t / across_a * 16;
+        ap[j] = t % across_a * 32;
+        mine_a += aq[j] < s.r;
+    }
+#pragma unroll
+    for (int j = 0; j < kSmallPairs; j++) {
+        const int t = wave + j * kSmallWaves;
+        xq[j] = t / across_x * 16;
+        xp[j] = t % across_x * 32;
+        mine_x += xq[j] < s.r;
+    }
+    int lp = (lane >> 4) * 4, lq = lane & 15;
+    // the last sums take X's place, unsplit
+    float *const result = reinterpret_cast<float *>(lds);
+    const int pitch = s.f + 4;
+    for (int it = 0; it < s.steps; it++) {
+        // addresses are made anew: kept over the iterations they would take the registers of the sums
+        asm volatile("" : "+v"(lp), "+v"(lq));
+        {
+            gemm::f4 acc[kPairsA][2];
+            small_product<NL, kPairsA, false>(X, X, s.f, mine_a, ap, aq, lane, acc);
+#pragma unroll
+            for (int j = 0; j < kPairsA; j++)
+#pragma unroll
+                for (int i = 0; i < 2; i++)
+                    if (j < mine_a) small_write<NL>(A, ap[j] + i * 16 + lp, aq[j] + lq, acc[j][i]);
+            __syncthreads();
+            small_product<NL, kPairsA, false>(A, A, s.r, mine_a, ap, aq, lane, acc);
+#pragma unroll
+            for (int j = 0; j < kPairsA; j++)
+#pragma unroll
+                for (int i = 0; i < 2; i++)
+                    if (j < mine_a) {
+                        float v[4];
+                        small_read<NL>(A, ap[j] + i * 16 + lp, aq[j] + lq, v);
+#pragma unroll
+                        for (int e = 0; e < 4; e++) acc[j][i][e] = fmaf(s.b, v[e], s.c * acc[j][i][e]);
+                    }
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < kPairsA; j++)
+#pragma unroll
+                for (int i = 0; i < 2; i++)
+                    if (j < mine_a) small_write<NL>(A, ap[j] + i * 16 + lp, aq[j] + lq, acc[j][i]);
+            __syncthreads();
+        }
+        gemm::f4 acc[kSmallPairs][2];
+        small_product<NL, kSmallPairs, true>(X, A, s.r, mine_x, xp, xq, lane, acc);
+#pragma unroll
+        for (int j = 0; j < kSmallPairs; j++)
+#pragma unroll
+            for (int i = 0; i < 2; i++)
+                if (j < mine_x) {
+                    float v[4];
+                    small_read<NL>(X, xp[j] + i * 16 + lp, xq[j] + lq, v);
+#pragma unroll
+                    for (int e = 0; e < 4; e++) acc[j][i][e] = fmaf(s.a, v[e], acc[j][i][e]);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+        __syncthreads();
+        if (it < s.steps - 1) {
+#pragma unroll
+            for (int j = 0; j < kSmallPairs; j++)
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (j < mine_x) small_write<NL>(X, xp[j] + i * 16 + lp, xq[j] + lq, acc[j][i]);
+                }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kSmallPairs; j++)
+#pragma unroll
+                for (int i = 0; i < 2; i++)
+                    if (j < mine_x) *reinterpret_cast<gemm::f4 *>(result + (xq[j] + lq) * pitch + xp[j] + i * 16 + lp) = acc[j][i];
+        }
+        __syncthreads();
+    }
+#pragma unroll 4
+    for (int i = tid; i < size; i += kSmallThreads) {
+        const int row = i / s.cols, col = i - row * s.cols;
+        float x = result[s.tall ? col * pitch + row : row * pitch + col];
+        if (s.weight) x = load_as_float(s.weight, s.out_type, base + i) * s.decay - s.rate * x;
+        store_from_float(s.out, s.out_type, base + i, x);
+    }
+}
 
 struct MuonPlan {
     int r, f;                                   // padded
     int nl;
+    bool small;                                 // one workgroup a matrix
     int64_t x_size, a_size;                     // elements of one limb plane
     int norm_blocks;
     size_t part_at, x_at[2], a_at, b_at, split_at, bytes;
 };
+
+// Whether a matrix fits the LDS of one workgroup and that is the faster way: a
+// wave's steps of 32 k in the three products, as measured, against the products'
+// estimates and what their launches cost.  In us, small against products: fp32
+// 64 x 64 35 / 67, 64 x 256 65 / 73, 300 of 64 x 64 72 / 149; 16-bit 96 x 96 51 / 65,
+// 128 x 128 85 / 64, 300 of them 181 / 297.
+bool small_way(const MuonPlan &p, const gs_muon &m)
+{
+    const int64_t lds = 2 * p.nl * ((int64_t)p.r * (p.f + 8) + (int64_t)p.r * (p.r + 8));
+    if (p.r > 128 || p.r * (int64_t)p.f > kSmallWaves * kSmallPairs * 512 || lds > kSmallLds) return false;
+    const int pairs_a = (p.r / 16 * (p.r / 32) + kSmallWaves - 1) / kSmallWaves, pairs_x = (p.r / 16 * (p.f / 32) + kSmallWaves - 1) / kSmallWaves;
+    const int turns = pairs_a * (p.f / 32 + p.r / 32) + pairs_x * (p.r / 32);
+    const double one = 12.0 + m.steps * (0.6 + turns * (p.nl == 3 ? 0.65 : 0.58));
+    const double products = choose(p.r, p.r, p.f, m.batch, true, p.nl).us + choose(p.r, p.r, p.r, m.batch, true, p.nl).us +
+                            choose(p.f, p.r, p.r, m.batch, false, p.nl).us;
+    const double many = 8.0 + m.steps * products, launches = 3.9 * (2 + 3 * m.steps);
+    return one * ((m.batch + 255) / 256) < (many > launches ? many : launches);
+}
 
 MuonPlan plan_muon(const gs_muon &m)
 {
@@ -303,6 +560,7 @@ MuonPlan plan_muon(const gs_muon &m)
     p.nl = m.out_dtype == GS_DTYPE_F32 ? 3 : 2;
     p.x_size = (int64_t)p.r * p.f;
     p.a_size = (int64_t)p.r * p.r;
+    p.small = small_way(p, m);
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t here = at;
@@ -340,13 +598,13 @@ MuonPlan plan_muon(const gs_muon &m)
 NsProduct choose(int P, int Q, int K, int batch, bool symmetric, int nl)
 {
     static const struct { int tile, step_k; float start, us3, us2; } kTiles[3] = {{128, 32, 3.0f, 2.3f, 1.3f}, {64, 64, 1.2f, 0.77f, 0.46f}, {32, 64, 0.5f, 0.62f, 0.38f}};
-    NsProduct best{64, 1};
+    NsProduct best{64, 1, 0.0};
     double least = 1e30;
     for (const auto &t : kTiles) {
         const int tp = (P + t.tile - 1) / t.tile, tq = (Q + t.tile - 1) / t.tile, nt = (K + t.step_k - 1) / t.step_k;
-        const double tiles = (double)(symmetric ? tp * (tp + 1) / 2 : tp * tq) * batch;
         for (int want = 1; want <= 8 && want <= nt; want++) {
             const int per = (nt + want - 1) / want, splits = (nt + per - 1) / per;
+            const double tiles = (double)(symmetric && one_side(t.tile, splits) ? tp * (tp + 1) / 2 : tp * tq) * batch;
             double rounds = tiles * splits / 256.0;
             // one block a CU, or (32) several that share its time
             rounds = t.tile > 32 ? ceil(rounds) : rounds > 1.0 ? rounds : 1.0;
@@ -359,6 +617,7 @@ NsProduct choose(int P, int Q, int K, int batch, bool symmetric, int nl)
             }
         }
     }
+    best.us = least;
     return best;
 }
 
@@ -367,7 +626,7 @@ hipError_t launch_product(gemm::Args a, typename NsEpilogue<NL>::Args e, float *
 {
     using E = NsEpilogue<NL>;
     const NsProduct c = choose(a.P, a.Q, a.K, batch, symmetric, NL);
-    a.symmetric = symmetric;
+    a.symmetric = symmetric && one_side(c.tile, c.splits);
     e.splits = c.splits;
     e.partial = c.splits > 1 ? partial : nullptr;
     e.ld_partial = a.P;
@@ -398,6 +657,27 @@ template <int NL> hipError_t run_muon(const gs_muon &m, bool step, char *ws, hip
     u.beta = m.beta;
     u.size = (int64_t)m.rows * m.cols;
     u.vec = u.size % 4 == 0;
+    if (p.small) {
+        Small q;
+        q.u = u;
+        q.rows = m.rows;
+        q.cols = m.cols;
+        q.tall = tall;
+        q.r = p.r;
+        q.f = p.f;
+        q.steps = m.steps;
+        q.a = m.a;
+        q.b = m.b;
+        q.c = m.c;
+        q.eps = m.eps;
+        q.decay = 1.0f - m.lr * m.weight_decay;
+        q.rate = m.lr * m.scale;
+        q.out = step ? m.weight_out : m.out;
+        q.weight = step ? m.weight : nullptr;
+        q.out_type = m.out_dtype;
+        small_matrices<NL><<<(unsigned)m.batch, kSmallThreads, 0, s>>>(q);
+        return hipGetLastError();
+    }
     momentum_and_norm<<<dim3((unsigned)p.norm_blocks, (unsigned)m.batch), kThreads, 0, s>>>(u, part);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;

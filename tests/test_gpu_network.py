@@ -435,6 +435,14 @@ def test_orthogonalize(e, r, f, t):
             assert err <= (1e-4 if to == "f32" else 2.5e-2 + U[to]), (i, err)
 
 
+# one workgroup a matrix or products by 128, 64 and 32 tiles, with and without splits of a long side
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("e,r,f", [(1, 58, 700), (2, 64, 1500), (1, 32, 1000), (1, 704, 64), (300, 17, 33), (260, 64, 40), (3, 96, 96), (1, 128, 128),
+                                   (2, 64, 384), (1, 260, 900), (5, 190, 30), (1, 20, 3000), (1, 1000, 1030)])
+def test_orthogonalize_by_every_way(e, r, f, t):
+    test_orthogonalize(e, r, f, t)
+
+
 def test_orthogonalize_of_zeros_ranks_and_scales():
     rng = np.random.default_rng(9)
     g = torch.zeros(4, 40, 24, device="cuda")
