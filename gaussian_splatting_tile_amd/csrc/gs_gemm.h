@@ -273,26 +273,23 @@ template <class TL, int THREADS, bool T, int NL, int KIND> struct Staged {
         for (int j = 0; j < kLoads; j++) {
             const int id = j * THREADS + tid;
             const int line = id / TL::CH, c = (id % TL::CH) ^ TL::swz(line);
-            union { uint16_t h[8]; uint4 u; } w[NL];
+            Vec<uint16_t, 8> w[NL];
             if constexpr (NL == 1) {
-                w[0].u = make_uint4(raw[j][0], raw[j][1], raw[j][2], raw[j][3]);
+                w[0] = __builtin_bit_cast(Vec<uint16_t, 8>, make_uint4(raw[j][0], raw[j][1], raw[j][2], raw[j][3]));
                 if (type == GS_DTYPE_MXFP8) {
 #pragma unroll
                     for (int e = 0; e < 8; e++)
-                        w[0].h[e] = __builtin_bit_cast(uint16_t, (__bf16)(e4m3_value((uint8_t)(raw[j][e >> 2] >> (8 * (e & 3)))) * scale[j]));
+                        w[0].v[e] = __builtin_bit_cast(uint16_t, (__bf16)(e4m3_value((uint8_t)(raw[j][e >> 2] >> (8 * (e & 3)))) * scale[j]));
                 }
             } else {
+                float v[8];
 #pragma unroll
-                for (int e = 0; e < 8; e++) {
-                    uint16_t limb[NL];
-                    split_limbs<NL>(__uint_as_float(raw[j][e]), limb);
-#pragma unroll
-                    for (int l = 0; l < NL; l++) w[l].h[e] = limb[l];
-                }
+                for (int e = 0; e < 8; e++) v[e] = __uint_as_float(raw[j][e]);
+                split_all<NL, 8>(v, w);
             }
 #pragma unroll
             for (int l = 0; l < NL; l++)
-                *reinterpret_cast<uint4 *>(lds + l * TL::kBytes + (line * TL::CH + c) * 16) = w[l].u;
+                *reinterpret_cast<uint4 *>(lds + l * TL::kBytes + (line * TL::CH + c) * 16) = __builtin_bit_cast(uint4, w[l]);
         }
     }
 };
@@ -552,25 +549,33 @@ __global__ __launch_bounds__(WP *WQ * 64, waves_per_simd(WP * WQ, NS * NL * (BP 
         if (NS > 3 && t + 2 < nt) turn_stage(t + 2, stage[2], stage[1]);
         if (PING && !late) __builtin_amdgcn_s_barrier();
     } else {
-        Staged<TP, kThreads, PT, NL, KIND> sp;
-        Staged<TQ, kThreads, QT, NL, KIND> sq;
+        // a stage's next tile but one is on its way while it is multiplied
+        constexpr int kSets = 2;
+        Staged<TP, kThreads, PT, NL, KIND> sp[kSets];
+        Staged<TQ, kThreads, QT, NL, KIND> sq[kSets];
         pb += (int64_t)batch * a.batch_p * dtype_bytes(a.p_type);
         qb += (int64_t)batch * a.batch_q * dtype_bytes(a.q_type);
-        auto load = [&](int k0) {
-            sp.load(pb, a.p_type, a.ps, a.ldps, p0, a.P, a.ldp, k0, kend, tid);
-            sq.load(qb, a.q_type, a.qs, a.ldqs, q0, a.Q, a.ldq, k0, kend, tid);
+        auto load = [&](int k0, int set) {
+            if (k0 >= kend) return;
+            sp[set].load(pb, a.p_type, a.ps, a.ldps, p0, a.P, a.ldp, k0, kend, tid);
+            sq[set].load(qb, a.q_type, a.qs, a.ldqs, q0, a.Q, a.ldq, k0, kend, tid);
         };
-        load(kbeg);
-        for (int k0 = kbeg; k0 < kend; k0 += kStepK) {
-            char *s = ((k0 - kbeg) / kStepK) & 1 ? lds1 : lds0;
-            sp.write(s, a.p_type, tid);
-            sq.write(s + NL * TP::kBytes, a.q_type, tid);
-            __syncthreads();                            // also: every wave is done with this stage's last use
-            if (k0 + kStepK < kend) load(k0 + kStepK);
 #pragma unroll
-            for (int c = 0; c < kSlices; c++) {
-                fetch(s, c);
-                multiply(c);
+        for (int i = 0; i < kSets; i++) load(kbeg + i * kStepK, i);
+        for (int k0 = kbeg; k0 < kend; k0 += kSets * kStepK) {
+#pragma unroll
+            for (int i = 0; i < kSets; i++) {
+                if (k0 + i * kStepK >= kend) continue;
+                char *s = i ? lds1 : lds0;
+                sp[i].write(s, a.p_type, tid);
+                sq[i].write(s + NL * TP::kBytes, a.q_type, tid);
+                __syncthreads();                        // also: every wave is done with this stage's last use
+                load(k0 + (i + kSets) * kStepK, i);
+#pragma unroll
+                for (int c = 0; c < kSlices; c++) {
+                    fetch(s, c);
+                    multiply(c);
+                }
             }
         }
     }

@@ -116,13 +116,7 @@ __device__ __forceinline__ void store_planes(uint16_t *dst, int64_t plane, int64
         return;
     }
     Vec<uint16_t, 8> w[3];
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-        uint16_t limb[3];
-        split_limbs<3>(v[i], limb);
-#pragma unroll
-        for (int l = 0; l < 3; l++) w[l].v[i] = limb[l];
-    }
+    split_all<3, 8>(v, w);
 #pragma unroll
     for (int l = 0; l < 3; l++) *reinterpret_cast<Vec<uint16_t, 8> *>(dst + l * plane + at) = w[l];
 }

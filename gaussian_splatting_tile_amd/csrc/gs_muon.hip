@@ -163,13 +163,7 @@ template <int NL> struct NsEpilogue {
     __device__ static __forceinline__ void write_limbs(const Args &e, int p, int q, const float v[8], int batch)
     {
         Vec<uint16_t, 8> h[NL];
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-            uint16_t limb[NL];
-            split_limbs<NL>(v[i], limb);
-#pragma unroll
-            for (int l = 0; l < NL; l++) h[l].v[i] = limb[l];
-        }
+        split_all<NL, 8>(v, h);
         uint16_t *o = e.o + batch * e.batch_o + (int64_t)q * e.ldo + p;
 #pragma unroll
         for (int l = 0; l < NL; l++) *reinterpret_cast<Vec<uint16_t, 8> *>(o + l * e.plane_o) = h[l];
@@ -381,16 +375,11 @@ template <int NL> __device__ __forceinline__ void small_read(const LdsMatrix &m,
 }
 template <int NL> __device__ __forceinline__ void small_write(const LdsMatrix &m, int p, int q, const gemm::f4 &v)
 {
-    gemm::s4 w[NL];
+    const float x[4] = {v[0], v[1], v[2], v[3]};
+    Vec<uint16_t, 4> w[NL];
+    split_all<NL, 4>(x, w);
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        uint16_t limb[NL];
-        split_limbs<NL>(v[i], limb);
-#pragma unroll
-        for (int l = 0; l < NL; l++) w[l][i] = (short)limb[l];
-    }
-#pragma unroll
-    for (int l = 0; l < NL; l++) *reinterpret_cast<gemm::s4 *>(m.at + l * m.plane + q * m.pitch + p) = w[l];
+    for (int l = 0; l < NL; l++) *reinterpret_cast<gemm::s4 *>(m.at + l * m.plane + q * m.pitch + p) = __builtin_bit_cast(gemm::s4, w[l]);
 }
 
 template <int NL> __global__ __launch_bounds__(kSmallThreads) void small_matrices(Small s)

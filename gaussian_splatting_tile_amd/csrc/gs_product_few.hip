@@ -63,16 +63,10 @@ __device__ __forceinline__ void load_piece(Piece<KIND, NL> &f, const void *base,
             const int k = k0 + g * 16 + h * 8;
             float v[8];
             load8(p, GS_DTYPE_F32, k, min(8, K - k), v);
-            union { uint16_t u[8]; i4 w; } limb[NL];
+            Vec<uint16_t, 8> limb[NL];
+            split_all<NL, 8>(v, limb);
 #pragma unroll
-            for (int e = 0; e < 8; e++) {
-                uint16_t l[NL];
-                split_limbs<NL>(v[e], l);
-#pragma unroll
-                for (int i = 0; i < NL; i++) limb[i].u[e] = l[i];
-            }
-#pragma unroll
-            for (int i = 0; i < NL; i++) f.v[i][h] = limb[i].w;
+            for (int i = 0; i < NL; i++) f.v[i][h] = __builtin_bit_cast(i4, limb[i]);
         }
     }
 }
