@@ -13,11 +13,11 @@
 // of two ways.  Staged, the product converts while loading, once per tile
 // across the result; packed, one pass first writes both operands as padded
 // 16-bit planes (three bf16 limbs of fp32).  Staged is taken where the result's
-// smaller side is at most 256 (8-bit: 128), never for 16-bit operands read by
-// columns.  Staged against packed in us: fp32 72519 x 256 x 832 268 / 319,
-// x 512 463 / 482, 16384 x 1024 x 512 136 / 119; bf16 of odd sizes 72519 x 250 x 830
-// 97 / 132, its transposed products 189 / 133; 8-bit 30000 x 91 x 192 17 / 25,
-// 72519 x 250 x 800 129 / 99.
+// smaller side is at most 1024 (fp32; by columns 512), 256 (16 bits; by columns
+// never) or 128 (8 bits).  Staged against packed in us: fp32 16384 x 1024 x 512
+// 112 / 116, 4096 x 4096 x 1024 205 / 189, by columns 72519 x 512 x 832 465 / 466 and
+// 20000 x 768 x 768 182 / 159; bf16 of odd sizes 72519 x 250 x 830 97 / 132, by columns
+// 189 / 133; 8-bit 30000 x 91 x 192 17 / 25, 72519 x 250 x 800 129 / 99.
 #include <string.h>
 
 #include "gs_linear.h"
@@ -56,7 +56,7 @@ ProductPlan make_plan(int64_t P, int64_t Q, int64_t K, bool pt, bool qt, bool st
 {
     static const TileRate direct[3] = {{256, 1, 4.9f, 1.0f, 64}, {128, 2, 4.1f, 0.9f, 64}, {64, 3, 2.4f, 0.87f, 64}};
     static const TileRate limbs[3] = {{256, 1, 0.0f, 1.0f, 64}, {128, 1, 4.1f, 1.0f, 64}, {64, 2, 3.0f, 0.9f, 64}};
-    static const TileRate staged_[3] = {{256, 1, 0.0f, 1.0f, 64}, {128, 1, 3.3f, 1.0f, 128}, {64, 3, 2.5f, 0.4f, 64}};
+    static const TileRate staged_[3] = {{256, 1, 0.0f, 1.0f, 64}, {128, 1, 4.4f, 1.0f, 128}, {64, 3, 3.7f, 0.38f, 64}};
     ProductPlan best{pt, qt, staged, 2, 1, 0.0};
     double least = 1e30;
     const int64_t nt = (K + step_k - 1) / step_k;
@@ -84,7 +84,7 @@ ProductPlan make_plan(int64_t P, int64_t Q, int64_t K, bool pt, bool qt, bool st
 // 4096 outputs 26 against 24.5; of 1024 to 4096 4.2 against 6.5.
 double few_rows_cost(const gs_linear &l)
 {
-    const double per_k = l.dtype == GS_DTYPE_F32 ? 3.9e-3 : l.dtype == GS_DTYPE_MXFP8 ? 0.9e-3 : 1.3e-3;
+    const double per_k = l.dtype == GS_DTYPE_F32 ? 2.6e-3 : l.dtype == GS_DTYPE_MXFP8 ? 0.9e-3 : 1.3e-3;
     return 2.2 + per_k * l.k * (l.n > 4096 ? l.n / 4096.0 : 1.0);
 }
 
@@ -193,13 +193,13 @@ void finish_plan(Product &r, bool p_ok, bool q_ok)
 {
     const bool pt = r.plan.pt, qt = r.plan.qt;
     const int least = r.a.P < r.a.Q ? r.a.P : r.a.Q;
-    const int staged_up_to = r.type == GS_DTYPE_F32 ? 256 : r.type == GS_DTYPE_MXFP8 ? 128 : pt ? 0 : 256;
+    const int staged_up_to = r.type == GS_DTYPE_F32 ? (pt ? 512 : 1024) : r.type == GS_DTYPE_MXFP8 ? 128 : pt ? 0 : 256;
     r.way = p_ok && q_ok ? kDirect : least <= staged_up_to ? kStaged : kPacked;
     r.pack_p = r.way == kPacked && (!p_ok || r.type == GS_DTYPE_MXFP8);
     r.pack_q = r.way == kPacked && (!q_ok || r.type == GS_DTYPE_MXFP8);
     const bool mx = r.type == GS_DTYPE_MXFP8 && r.way == kDirect, f32 = r.type == GS_DTYPE_F32;
     const int step = mx ? 128 : r.way == kStaged || f32 ? 32 : 64;
-    r.plan = make_plan(r.a.P, r.a.Q, r.a.K, pt, qt, r.way == kStaged, f32, step, f32 || r.way == kStaged ? 6.0f : mx ? 0.6f : 1.0f);
+    r.plan = make_plan(r.a.P, r.a.Q, r.a.K, pt, qt, r.way == kStaged, f32, step, f32 ? 6.0f : r.way == kStaged ? 3.0f : mx ? 0.6f : 1.0f);
     r.e.ld_partial = (r.a.P + 7) & ~7;
     r.e.split_stride = r.e.ld_partial * r.a.Q;
     r.partial_bytes = r.plan.splits > 1 ? (size_t)r.plan.splits * r.e.split_stride * 4 : 0;
