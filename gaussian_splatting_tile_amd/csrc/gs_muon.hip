@@ -13,6 +13,11 @@
 //
 // A matrix that fits the LDS of a CU is iterated by one workgroup from its
 // gradient to its weight.
+//
+// 4096 x 1024 in bf16, 5 iterations: 353 us, each A 20 us and its splits' sum 6, B 11
+// and X' 30 (860 TFLOP/s of the three limb products), momentum, norm and first
+// limbs 24.  8 x 256 x 256 in fp32: 110 us, 17 launches of 5 to 7 us; the products are
+// bound by their starts and ends, which 32 x 32 tiles on more CUs shorten.
 #include <string.h>
 
 #include "gs_gemm.h"
@@ -292,7 +297,9 @@ bool one_side(int tile, int splits) { return tile >= 64 || splits == 1; }
 // X and A (then B in its place) stay in LDS as limbs, rows padded by 16 bytes so
 // that neither 16 rows of a chunk nor 4 lines of a transposed read meet in a
 // bank.  A wave takes pairs of 16 x 16 results side by side; the sums wait in
-// registers until every wave has read what they replace.
+// registers until every wave has read what they replace.  Bound by LDS reads (9
+// fragments for 12 products of fp32) and the barriers' latency: 64 x 64 in fp32
+// 35 us, 2 us a product.
 constexpr int kSmallThreads = 1024, kSmallWaves = kSmallThreads / 64;
 constexpr int kSmallLds = 158 * 1024;
 constexpr int kSmallPairs = 4;                  // pairs of results of X per wave

@@ -4,9 +4,15 @@
 // HBM-bound: the forward reads x and the residual and writes the sum and y
 // once, the backward reads the sum, dy and dsum and writes dx.  A row is held
 // in registers between its reduction and its outputs, 8 consecutive elements
-// (16 bytes of a 16-bit type) per lane and access: rows of up to 128 by 16
-// lanes, up to 2048 by a wave (4 rows per workgroup, no barrier), up to 8192 by
-// a workgroup, longer ones in two passes.  An 8-bit block of 32 values is 4 neighbouring lanes.
+// (16 bytes of a 16-bit type) per lane and access.  Forward: rows of up to 128
+// by 16 lanes, up to 2048 by a wave (4 rows per workgroup, no barrier), up to
+// 8192 by a workgroup, longer ones in two passes.  An 8-bit block of 32 values is
+// 4 neighbouring lanes.  Backward: as few elements per lane as cover the row, 8
+// or (512 < n <= 1024) 16, as it also holds the next row and its columns' sums.
+//
+// bf16 with a residual: 16384 x 1024 in 28 us (134 MB, 4.8 TB/s), 100000 x 2048
+// to 8 bits in 269 us (1.44 GB, 5.4 TB/s), the backward of 16384 x 1024 in 33 us
+// (4.1 TB/s, 3 us of them the sum of the partial dgammas).
 #include "gs_linear.h"
 
 #include <math.h>
