@@ -119,6 +119,13 @@ def test_norm_forward_and_backward(m, n, t):
     assert _untouched(dxv, dxb)
 
 
+# the widths of every group of lanes, rows that make the backward's workgroups go round, and one workgroup alone
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+@pytest.mark.parametrize("m,n", [(16, 120), (40, 129), (9000, 7), (4100, 65), (2500, 256), (1500, 600), (700, 1300), (1030, 2047), (300, 3001), (280, 5003)])
+def test_norm_of_every_width(m, n, t):
+    test_norm_forward_and_backward(m, n, t)
+
+
 def test_norm_of_awkward_rows():
     x = torch.zeros(6, 64, device="cuda")
     x[1] = 1e-30
@@ -235,6 +242,14 @@ def test_linear_forward_large_tiles_and_splits(m, n, k, t):
     _linear_case(m, n, k, t, "f32", "none", True, False, False, 0)
 
 
+# few rows by 4 and 16 waves and by tiles, converted while loading by 64 and 128 tiles, packed, long k in many splits
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+@pytest.mark.parametrize("m,n,k", [(1, 70, 8200), (16, 4096, 2100), (16, 4100, 515), (17, 203, 13001), (40, 33, 9000), (3000, 200, 700), (700, 1000, 301),
+                                   (2300, 1030, 64)])
+def test_linear_forward_by_every_way(m, n, k, t):
+    test_linear_forward(m, n, k, t)
+
+
 def test_linear_residual_in_place_empty_and_no_bias():
     rng = np.random.default_rng(1)
     x, w, y = _make(rng, (70, 64), "bf16"), _make(rng, (40, 64), "bf16", 0.1), _make(rng, (70, 40), "bf16")
@@ -341,6 +356,13 @@ def test_linear_backward(m, n, k, t):
             B.linear_bwd(lin, gr, _ws(B.linear_bwd_workspace_bytes(lin, gr)))
         _close(_np(dw), 2 * first.cpu().double().numpy(), 2 * U[tw] * np.abs(2 * _np(first)) + TINY[tw], "dw added to itself")
         _close(_np(db), 2 * db64, ((2 * m + 40) * E + 2 * slack) * a.sum(0) + 1e-30, "db added to itself")
+
+
+# one row block and several, products converted while loading and packed, long sums over rows
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+@pytest.mark.parametrize("m,n,k", [(64, 300, 500), (65, 2048, 40), (9000, 47, 198), (900, 600, 58), (700, 640, 700), (3, 4099, 33)])
+def test_linear_backward_by_every_way(m, n, k, t):
+    test_linear_backward(m, n, k, t)
 
 
 def test_linear_backward_matches_differences_of_the_forward():
