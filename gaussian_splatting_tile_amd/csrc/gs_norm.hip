@@ -5,7 +5,7 @@
 // once, the backward reads the sum, dy and dsum and writes dx.  A row is held
 // in registers between its reduction and its outputs, 8 consecutive elements
 // (16 bytes of a 16-bit type) per lane and access.  Forward: rows of up to 128
-// by 16 lanes, up to 2048 by a wave (4 rows per workgroup, no barrier), up to
+// by 16 lanes, up to 256 by 32, up to 2048 by a wave (4 rows per workgroup, no barrier), up to
 // 8192 by a workgroup, longer ones in two passes.  An 8-bit block of 32 values is
 // 4 neighbouring lanes.  Backward: as few elements per lane as cover the row, 8
 // or (512 < n <= 1024) 16, as it also holds the next row and its columns' sums.
@@ -121,37 +121,48 @@ __device__ __forceinline__ void emit(const NormArgs &a, int64_t row, int c, int 
         store_chunk(static_cast<T *>(a.y), row * a.ldy + c, valid, v);
 }
 
-// Rows of up to LANES * 8 * V elements.
-template <typename T, int LANES, int V> __global__ __launch_bounds__(kThreads) void norm_rows(NormArgs a)
+// Rows of up to LANES * 8 * V elements.  WIDE, rows of at least 8: the last chunk
+// of a row takes its last 8 elements, so that every access is a whole vector;
+// those that are also the chunk's before it count once and are written twice
+// alike, after the whole row was read.
+template <typename T, int LANES, int V, bool WIDE> __global__ __launch_bounds__(kThreads) void norm_rows(NormArgs a)
 {
     __shared__ float lds[kThreads / 64];
     const int lane = threadIdx.x % LANES;
     const int64_t row = (int64_t)blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
     if (row >= a.m) return;                     // a row's lanes together; a workgroup's single row is always there
+    auto chunk = [&](int k) { return (k * LANES + lane) * 8; };
+    auto start = [&](int c) { return WIDE ? min(c, a.n - 8) : c; };
+    auto inside = [&](int at) { return WIDE ? 8 : min(8, a.n - at); };
     float v[V][8], sq = 0.0f;
 #pragma unroll
     for (int k = 0; k < V; k++) {
-        const int c = (k * LANES + lane) * 8, valid = max(0, min(8, a.n - c));
-        load_chunk(static_cast<const T *>(a.x), row * a.ldx + c, valid, v[k]);
+        const int c = chunk(k), at = start(c);
+#pragma unroll
+        for (int j = 0; j < 8; j++) v[k][j] = 0.0f;
+        if (c >= a.n) continue;
+        load_chunk(static_cast<const T *>(a.x), row * a.ldx + at, inside(at), v[k]);
         if (a.residual) {
             float r[8];
-            load_chunk(static_cast<const T *>(a.residual), row * a.ldr + c, valid, r);
+            load_chunk(static_cast<const T *>(a.residual), row * a.ldr + at, inside(at), r);
 #pragma unroll
             for (int j = 0; j < 8; j++) v[k][j] += r[j];
         }
     }
 #pragma unroll
-    for (int k = 0; k < V; k++)
+    for (int k = 0; k < V; k++) {
+        const int shared = WIDE ? max(0, min(8, chunk(k) - (a.n - 8))) : 0;
 #pragma unroll
-        for (int j = 0; j < 8; j++) sq = fmaf(v[k][j], v[k][j], sq);
+        for (int j = 0; j < 8; j++) sq = fmaf(v[k][j], j >= shared ? v[k][j] : 0.0f, sq);
+    }
     const float rstd = inverse_rms(row_sum<LANES>(sq, lds), a.n, a.eps);
     if (a.rstd && lane == 0) a.rstd[row] = rstd;
 #pragma unroll
     for (int k = 0; k < V; k++) {
-        const int c = (k * LANES + lane) * 8, valid = max(0, min(8, a.n - c));
-        if (valid == 0) continue;               // whole 8-bit blocks: n is a multiple of 32 there
-        if (a.sum) store_chunk(static_cast<T *>(a.sum), row * a.lds + c, valid, v[k]);
-        emit<T>(a, row, c, valid, v[k], rstd);
+        const int c = chunk(k), at = start(c);
+        if (c >= a.n) continue;                 // whole 8-bit blocks: n is a multiple of 32 there
+        if (a.sum) store_chunk(static_cast<T *>(a.sum), row * a.lds + at, inside(at), v[k]);
+        emit<T>(a, row, at, inside(at), v[k], rstd);
     }
 }
 
@@ -191,13 +202,15 @@ template <typename T> __global__ __launch_bounds__(kThreads) void norm_long(Norm
 
 template <typename T> hipError_t launch_norm(const NormArgs &a, hipStream_t s)
 {
-    const unsigned rows16 = (unsigned)((a.m + 15) / 16), rows4 = (unsigned)((a.m + 3) / 4), rows1 = (unsigned)a.m;
-    if (a.n <= 128) norm_rows<T, 16, 1><<<rows16, kThreads, 0, s>>>(a);
-    else if (a.n <= 512) norm_rows<T, 64, 1><<<rows4, kThreads, 0, s>>>(a);
-    else if (a.n <= 1024) norm_rows<T, 64, 2><<<rows4, kThreads, 0, s>>>(a);
-    else if (a.n <= 2048) norm_rows<T, 64, 4><<<rows4, kThreads, 0, s>>>(a);
-    else if (a.n <= 4096) norm_rows<T, 256, 2><<<rows1, kThreads, 0, s>>>(a);
-    else if (a.n <= kMaxRegRow) norm_rows<T, 256, 4><<<rows1, kThreads, 0, s>>>(a);
+    const unsigned rows16 = (unsigned)((a.m + 15) / 16), rows8 = (unsigned)((a.m + 7) / 8), rows4 = (unsigned)((a.m + 3) / 4), rows1 = (unsigned)a.m;
+    if (a.n < 8) norm_rows<T, 16, 1, false><<<rows16, kThreads, 0, s>>>(a);
+    else if (a.n <= 128) norm_rows<T, 16, 1, true><<<rows16, kThreads, 0, s>>>(a);
+    else if (a.n <= 256) norm_rows<T, 32, 1, true><<<rows8, kThreads, 0, s>>>(a);
+    else if (a.n <= 512) norm_rows<T, 64, 1, true><<<rows4, kThreads, 0, s>>>(a);
+    else if (a.n <= 1024) norm_rows<T, 64, 2, true><<<rows4, kThreads, 0, s>>>(a);
+    else if (a.n <= 2048) norm_rows<T, 64, 4, true><<<rows4, kThreads, 0, s>>>(a);
+    else if (a.n <= 4096) norm_rows<T, 256, 2, true><<<rows1, kThreads, 0, s>>>(a);
+    else if (a.n <= kMaxRegRow) norm_rows<T, 256, 4, true><<<rows1, kThreads, 0, s>>>(a);
     else norm_long<T><<<rows1, kThreads, 0, s>>>(a);
     return hipGetLastError();
 }
