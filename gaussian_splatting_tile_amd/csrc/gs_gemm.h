@@ -367,11 +367,11 @@ template <int PART> __device__ __forceinline__ int turn_at(int q, int p)
 // where the LDS holds two.
 constexpr int waves_per_simd(int waves, int lds) { return (2 * lds <= 160 * 1024 ? 2 : 1) * waves / 4; }
 
-// The epilogue takes 8 sums of consecutive p at a time where EPI::vec(e) allows,
-// EPI::store8(e, p, q, v, part, ahead, batch, split), which leaves the final
-// values in v and finds in `part` and `ahead` what EPI::part(e, p, ..) and
-// EPI::look_ahead(e, p, q, ..) loaded for it, else single ones, EPI::store1.  A tile that also stands for its transpose
-// (EPI::kMirror) hands those on to EPI::store_mirror.
+// The epilogue takes 8 sums of consecutive p at a time, EPI::store8(e, p, q, v,
+// part, ahead, batch, split), which leaves the final values in v and finds in
+// `part` and `ahead` what EPI::part(e, p, ..) and EPI::look_ahead(e, p, q, ..)
+// loaded for it; at the end of p single ones, EPI::store1.  A tile that also
+// stands for its transpose (EPI::kMirror) hands those on to EPI::store_mirror.
 template <int KIND, int NL, int NS, int BK, int BP, int BQ, int WP, int WQ, bool PT, bool QT, bool STAGED, bool PING, class EPI>
 __global__ __launch_bounds__(WP *WQ * 64, waves_per_simd(WP * WQ, NS * NL * (BP + BQ) * BK * 2)) void product_kernel(Args a, typename EPI::Args e)
 {
@@ -594,7 +594,7 @@ __global__ __launch_bounds__(WP *WQ * 64, waves_per_simd(WP * WQ, NS * NL * (BP 
     float *turn = reinterpret_cast<float *>(lds0) + wave * (256 * kPart);
     constexpr int kLanesP = kPart * 2, kRowsQ = 64 / kLanesP;   // lanes along p, q rows at a time
     constexpr int kParts = FQ * (FP / kPart), kIts = kRowsQ < 16 ? 16 / kRowsQ : 1;
-    const bool mirror = EPI::kMirror && a.symmetric && tp != tq, vec = EPI::vec(e);
+    const bool mirror = EPI::kMirror && a.symmetric && tp != tq;
     // what the epilogue reads for a part is on its way while its sums turn
     typename EPI::Ahead ahead[kIts];
     auto part_p = [&](int u) { return p0 + (wp * FP + u % (FP / kPart) * kPart) * 16; };
@@ -609,11 +609,9 @@ __global__ __launch_bounds__(WP *WQ * 64, waves_per_simd(WP * WQ, NS * NL * (BP 
 #pragma unroll 1
     for (int u = 0; u < kParts; u++) {
         typename EPI::Part part;
-        if (vec) {
-            look_ahead(u);
-            const int p = part_p(u) + lane % kLanesP * 8;
-            if (p + 8 <= a.P) EPI::part(e, p, part);
-        }
+        look_ahead(u);
+        const int part_at = part_p(u) + lane % kLanesP * 8;
+        if (part_at + 8 <= a.P) EPI::part(e, part_at, part);
         // accumulators have no run-time index: one of kParts branches
 #pragma unroll
         for (int c = 0; c < kParts; c++)
@@ -625,46 +623,37 @@ __global__ __launch_bounds__(WP *WQ * 64, waves_per_simd(WP * WQ, NS * NL * (BP 
             }
         wave_fence();
         const int pb0 = part_p(u), qb0 = part_q(u);
-        if (vec) {
 #pragma unroll
-            for (int it = 0; it < kIts; it++) {
-                const int qr = it * kRowsQ + lane / kLanesP, pr = lane % kLanesP * 8;
-                const int p = pb0 + pr, q = qb0 + qr;
-                if (qr >= 16 || q >= a.Q) continue;     // two lanes a row would reach 32 rows
-                if (p + 8 <= a.P) {
-                    f4 *const lo = reinterpret_cast<f4 *>(turn + turn_at<kPart>(qr, pr));
-                    f4 *const hi = reinterpret_cast<f4 *>(turn + turn_at<kPart>(qr, pr + 4));
-                    float v[8] = {(*lo)[0], (*lo)[1], (*lo)[2], (*lo)[3], (*hi)[0], (*hi)[1], (*hi)[2], (*hi)[3]};
-                    EPI::store8(e, p, q, v, part, ahead[it], batch, split);
-                    if (mirror) {
-                        *lo = f4{v[0], v[1], v[2], v[3]};
-                        *hi = f4{v[4], v[5], v[6], v[7]};
-                    }
-                } else {
-#pragma unroll 1
-                    for (int i = 0; i < a.P - p; i++) EPI::store1(e, p + i, q, turn[turn_at<kPart>(qr, pr + i)], batch, split);
+        for (int it = 0; it < kIts; it++) {
+            const int qr = it * kRowsQ + lane / kLanesP, pr = lane % kLanesP * 8;
+            const int p = pb0 + pr, q = qb0 + qr;
+            if (qr >= 16 || q >= a.Q) continue;     // two lanes a row would reach 32 rows
+            if (p + 8 <= a.P) {
+                f4 *const lo = reinterpret_cast<f4 *>(turn + turn_at<kPart>(qr, pr));
+                f4 *const hi = reinterpret_cast<f4 *>(turn + turn_at<kPart>(qr, pr + 4));
+                float v[8] = {(*lo)[0], (*lo)[1], (*lo)[2], (*lo)[3], (*hi)[0], (*hi)[1], (*hi)[2], (*hi)[3]};
+                EPI::store8(e, p, q, v, part, ahead[it], batch, split);
+                if (mirror) {
+                    *lo = f4{v[0], v[1], v[2], v[3]};
+                    *hi = f4{v[4], v[5], v[6], v[7]};
                 }
-            }
-            if constexpr (EPI::kMirror) {
-                if (mirror) {               // the transposed tile: 8 q of a p to a lane
-                    wave_fence();
+            } else {
 #pragma unroll 1
-                    for (int x = lane; x < 32 * kPart; x += 64) {
-                        const int pr = x % (16 * kPart), qr = x / (16 * kPart) * 8;
-                        if (pb0 + pr >= a.P || qb0 + qr >= a.Q) continue;
-                        float v[8];
+                for (int i = 0; i < a.P - p; i++) EPI::store1(e, p + i, q, turn[turn_at<kPart>(qr, pr + i)], batch, split);
+            }
+        }
+        if constexpr (EPI::kMirror) {
+            if (mirror) {               // the transposed tile: 8 q of a p to a lane
+                wave_fence();
+#pragma unroll 1
+                for (int x = lane; x < 32 * kPart; x += 64) {
+                    const int pr = x % (16 * kPart), qr = x / (16 * kPart) * 8;
+                    if (pb0 + pr >= a.P || qb0 + qr >= a.Q) continue;
+                    float v[8];
 #pragma unroll
-                        for (int i = 0; i < 8; i++) v[i] = turn[turn_at<kPart>(qr + i, pr)];
-                        EPI::store_mirror(e, qb0 + qr, pb0 + pr, v, batch, split);
-                    }
+                    for (int i = 0; i < 8; i++) v[i] = turn[turn_at<kPart>(qr + i, pr)];
+                    EPI::store_mirror(e, qb0 + qr, pb0 + pr, v, batch, split);
                 }
-            }
-        } else {
-#pragma unroll 2
-            for (int x = lane; x < 256 * kPart; x += 64) {
-                const int p = pb0 + x % (16 * kPart), q = qb0 + x / (16 * kPart);
-                if (p < a.P && q < a.Q)
-                    EPI::store1(e, p, q, turn[turn_at<kPart>(x / (16 * kPart), x % (16 * kPart))], batch, split);
             }
         }
         wave_fence();

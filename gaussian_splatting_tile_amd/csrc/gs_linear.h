@@ -17,7 +17,7 @@ struct LinearEpilogue {
         int64_t ld_partial, split_stride;
         const float *bias;
         int bias_on_q;                  // bias[q] (planes) or bias[p]
-        int act, exact;                 // exact: fp32 results, library erf and exp
+        int act, exact;                 // exact: fp32 results
         const void *residual;
         int64_t ldr;
         void *y;                        // residual and y: element q * ld + p
@@ -26,8 +26,6 @@ struct LinearEpilogue {
         void *z;                        // element q * z_q + p * z_p
         int64_t z_q, z_p;
         int z_type;
-        int vec;                        // 8 consecutive p at a time: unless it takes exact silu or gelu, as eight library
-                                        // erfs at once take more registers than the rest of a kernel
     };
 
     // One value, any layout.
@@ -57,7 +55,7 @@ struct LinearEpilogue {
             a.residual = *reinterpret_cast<const Vec<uint16_t, 8> *>(static_cast<const uint16_t *>(e.residual) + (int64_t)q * e.ldr + p);
     }
 
-    // Eight values p .. p + 7, vec set.
+    // Eight values p .. p + 7.
     __device__ static __forceinline__ void finish8(const Args &e, int p, int q, float v[8], const Part &b, const Ahead &a)
     {
         const int64_t at = (int64_t)q * e.ldy + p;
@@ -79,7 +77,8 @@ struct LinearEpilogue {
                 for (int i = 0; i < 8; i++) store_from_float(e.z, e.z_type, (int64_t)q * e.z_q + (int64_t)(p + i) * e.z_p, v[i]);
             }
         }
-        activate_all<8, false>(v, e.act);
+        if (e.exact) activate_all<8, true>(v, e.act);
+        else activate_all<8, false>(v, e.act);
         float r[8];
         if (e.residual) {
             if (e.y_type == GS_DTYPE_F32) {
@@ -103,8 +102,6 @@ struct LinearEpilogue {
         }
         store8_vec(e.y, e.y_type, at, v);
     }
-
-    __device__ static __forceinline__ bool vec(const Args &e) { return e.partial || e.vec; }
 
     static constexpr bool kMirror = false;
 

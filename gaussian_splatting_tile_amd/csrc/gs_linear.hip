@@ -204,7 +204,6 @@ void finish_plan(Product &r, bool p_ok, bool q_ok)
     r.e.split_stride = r.e.ld_partial * r.a.Q;
     r.partial_bytes = r.plan.splits > 1 ? (size_t)r.plan.splits * r.e.split_stride * 4 : 0;
     r.e.exact = exact_results(r.e);
-    r.e.vec = !(r.e.exact && r.e.act >= GS_ACT_SILU);
 }
 
 // Points an operand at its packed planes.
@@ -258,7 +257,7 @@ hipError_t run_product(Product &r, void *partial, hipStream_t s)
     else if (r.type == GS_DTYPE_F16) err = launch_product_f16(r.a, r.e, r.plan, s);
     else err = launch_product_bf16(r.a, r.e, r.plan, s);        // widened 8-bit operands too
     if (err != hipSuccess || r.plan.splits == 1) return err;
-    const bool vec = r.e.vec && r.a.P % 8 == 0;         // whole chunks
+    const bool vec = r.a.P % 8 == 0;            // whole chunks
     const int64_t n = (int64_t)(vec ? r.a.P / 8 : r.a.P) * r.a.Q;
     const unsigned blocks = (unsigned)((n + kReduceThreads - 1) / kReduceThreads);
     if (vec) reduce_splits<true><<<blocks, kReduceThreads, 0, s>>>(r.e, r.a.P, r.a.Q, r.plan.splits);
@@ -509,12 +508,7 @@ template <bool EXACT> __global__ __launch_bounds__(kThreads) void dz_planes(DzAr
         __syncthreads();
         if (r + kPlaneRows < r1) fetch(r + kPlaneRows);
         if (d.act != GS_ACT_NONE) {
-            if constexpr (EXACT) {              // one at a time: eight library erfs at once take many registers
-#pragma unroll 1
-                for (int j = 0; j < 8; j++) scale_by_slope<1, true>(v + j, at_z + j, d.act);
-            } else {
-                scale_by_slope<8, false>(v, at_z, d.act);       // outside: 0 times the slope at 0
-            }
+            scale_by_slope<8, EXACT>(v, at_z, d.act);   // outside: 0 times the slope at 0
         }
 #pragma unroll
         for (int j = 0; j < 8; j++) acc[j] += v[j];

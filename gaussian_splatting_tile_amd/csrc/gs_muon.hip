@@ -163,8 +163,6 @@ template <int NL> struct NsEpilogue {
         float decay, rate;                      // weight * decay - rate * v
     };
 
-    __device__ static __forceinline__ bool vec(const Args &) { return true; }   // everything is padded
-
     __device__ static __forceinline__ void write_limbs(const Args &e, int p, int q, const float v[8], int batch)
     {
         Vec<uint16_t, 8> h[NL];

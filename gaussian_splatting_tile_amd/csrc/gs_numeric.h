@@ -161,22 +161,43 @@ __device__ __forceinline__ float e8m0_value(uint32_t s)
 }
 
 // ---- activations -------------------------------------------------------------
-// Phi(-|z|) of the standard normal distribution, for results rounded to 16
-// bits: the five-term approximation of Abramowitz and Stegun 7.1.26 (absolute
-// error 7.5e-8), one reciprocal and one exponential, e = exp(-z^2 / 2); the
-// library's erf takes about three times as long and made up most of the
-// epilogue of a GELU layer.
-__device__ __forceinline__ float normal_tail(float z, float &e)
+// Phi(-|z|) of the standard normal distribution and e = exp(-z^2 / 2): both as t
+// times a polynomial in t = 1 / (1 + p |z| / sqrt 2) times e.
+// For results rounded to 16 bits the five terms of Abramowitz and Stegun 7.1.26
+// (absolute error 7.5e-8).  For fp32 results (EXACT) nine, fitted for this to
+// the scaled complementary error function: relative error 4e-8 before rounding,
+// 7e-7 up to |z| = 4 in fp32, where a sum 1 + erf has lost all of the tail.  The
+// library's erfc, with its branches, took most of an epilogue's time.
+template <bool EXACT> __device__ __forceinline__ float normal_tail(float z, float &e)
 {
+    e = __builtin_amdgcn_exp2f(z * z * -0.72134752044448170f);
+    if constexpr (EXACT) {
+        const float d = fmaf(fminf(fabsf(z), 16.0f), 0.5f * 0.70710678118654752f, 1.0f);
+        float t = __builtin_amdgcn_rcpf(d);
+        t = fmaf(fmaf(-d, t, 1.0f), t, t);
+        constexpr float k[9] = {0.141044193f, 0.141170635f, 0.121674233f, 0.100864183f, -0.0121898435f, 0.137415421f, -0.242194546f, 0.141612519f, -0.0293968155f};
+        float p = k[8];
+#pragma unroll
+        for (int i = 7; i >= 0; i--) p = fmaf(t, p, k[i]);
+        return t * p * e;
+    }
     const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(z), 0.3275911f * 0.70710678118654752f, 1.0f));
     const float p = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 0.5f * 1.061405429f, -0.5f * 1.453152027f), 0.5f * 1.421413741f),
                                      -0.5f * 0.284496736f), 0.5f * 0.254829592f);
-    e = __builtin_amdgcn_exp2f(z * z * -0.72134752044448170f);
     return p * e;
 }
+// 1 / (1 + exp(-z)); EXACT carries what the exponent's product rounds off and
+// corrects the reciprocal once.
 template <bool EXACT> __device__ __forceinline__ float logistic(float z)
 {
-    if constexpr (EXACT) return 1.0f / (1.0f + expf(-z));
+    if constexpr (EXACT) {
+        const float x = -fminf(fmaxf(z, -87.0f), 87.0f), u = x * 1.4426950408889634f;
+        const float rest = fmaf(x, 1.4426950408889634f, -u) + x * 1.9259629911266175e-8f;     // log2 e to 48 bits
+        float e = __builtin_amdgcn_exp2f(u);
+        e = fmaf(e, rest * 0.69314718055994531f, e);
+        const float d = 1.0f + e, s = __builtin_amdgcn_rcpf(d);
+        return z < -87.0f ? 0.0f : fmaf(fmaf(-d, s, 1.0f), s, s);       // under 2^-125
+    }
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
 }
 template <int ACT, bool EXACT> __device__ __forceinline__ float activate(float z)
@@ -184,11 +205,10 @@ template <int ACT, bool EXACT> __device__ __forceinline__ float activate(float z
     if constexpr (ACT == GS_ACT_RELU) return z < 0.0f ? 0.0f : z;     // a NaN stays one
     if constexpr (ACT == GS_ACT_SILU) return z * logistic<EXACT>(z);
     if constexpr (ACT == GS_ACT_GELU) {
-        if constexpr (EXACT) return z * (0.5f * erfcf(-0.70710678118654752f * z));
         // z Phi(z) = max(z, 0) - |z| Phi(-|z|); the bound keeps an infinite z from
         // meeting the tail's 0
         float e;
-        const float h = normal_tail(z, e);
+        const float h = normal_tail<EXACT>(z, e);
         return fmaf(-fminf(fabsf(z), 64.0f), h, fmaxf(z, 0.0f));
     }
     return z;
@@ -201,9 +221,8 @@ template <int ACT, bool EXACT> __device__ __forceinline__ float activate_slope(f
         return s * fmaf(z, 1.0f - s, 1.0f);
     }
     if constexpr (ACT == GS_ACT_GELU) {
-        if constexpr (EXACT) return 0.5f * erfcf(-0.70710678118654752f * z) + z * 0.39894228040143268f * expf(-0.5f * z * z);
         float e;
-        const float h = normal_tail(z, e);
+        const float h = normal_tail<EXACT>(z, e);
         return fmaf(z * 0.39894228040143268f, e, z >= 0.0f ? 1.0f - h : h);
     }
     return 1.0f;

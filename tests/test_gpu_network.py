@@ -276,6 +276,33 @@ def test_linear_keeps_infinities_and_nans_in_their_rows(t):
     np.testing.assert_array_equal(fin, want)
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_activations_in_fp32_over_their_range(act):
+    """y and its slope through a product with 1: absolute errors of fp32's
+    rounding of values near 1, relative ones down the tail (its exponent's
+    product is off by z^2 / 2 ulps), nothing left far below."""
+    from math import erfc
+
+    z = torch.cat([torch.linspace(-14, 14, 100001), torch.tensor([0.0, 1e-30, -1e-30, 300.0, -300.0, 3e38, -3e38])]).cuda().view(-1, 1)
+    w, y, dx = torch.ones(1, 1, device="cuda"), torch.empty_like(z), torch.empty_like(z)
+    lin = B.linear_struct(z, w, y, act=act)
+    B.linear_fwd(lin, _ws(B.linear_fwd_workspace_bytes(lin)))
+    back = B.linear_struct(z, w, None, z=z, act=act)
+    gr = B.linear_grads_struct(back, torch.ones_like(z), dx=dx)
+    B.linear_bwd(back, gr, _ws(B.linear_bwd_workspace_bytes(back, gr)))
+    v = _np(z)[:, 0]
+    if act == "gelu":
+        phi = np.array([0.5 * erfc(-t / 2 ** 0.5) for t in v])
+        want, slope = v * phi, phi + v * np.exp(-0.5 * np.minimum(np.abs(v), 1e3) ** 2) / (2 * np.pi) ** 0.5
+    else:
+        s = 1 / (1 + np.exp(np.minimum(-v, 700)))
+        want, slope = v * s, s * (1 + v * (1 - s))
+    a = np.minimum(np.abs(v), 20.0)
+    # results under 2^-125 may be 0
+    _close(_np(y)[:, 0], want, (8 + a * a) * E * np.abs(want) + 1e-35, "y")
+    _close(_np(dx)[:, 0], slope, (8 + a * a) * E * (1 + a) * np.maximum(np.abs(slope), np.minimum(1, 4 * np.exp(-a))) + 1e-35, "slope")
+
+
 def test_linear_f32_keeps_the_largest_and_smallest_values():
     x = torch.zeros(4, 32, device="cuda")
     w = torch.zeros(16, 32, device="cuda")
