@@ -37,25 +37,29 @@ size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 // 256 CUs, each CU working through its resident blocks at `rate`, plus what a
 // split of k costs to reduce.  The rates are measured ones at full occupancy;
 // one block by itself reaches `alone` of them.  What a block does before and
-// after its product counts as `around` more of k.
+// after its product counts as 64 more of k, or `around` where blocks share or follow
+// one another on a CU and all write at once (40000 x 1000 x 64 in bf16: 43 us by
+// 256 tiles, 32 by 128, 48 by 64; 72519 x 512 x 832: 88, 81, 101).
 struct TileRate { int size, resident; float mflop_us, alone; int around; };     // per CU
 
 double product_cost(const TileRate &t, int64_t P, int64_t Q, int64_t K, int splits, float work)
 {
     const double blocks = (double)((P + t.size - 1) / t.size) * (double)((Q + t.size - 1) / t.size) * splits;
-    const double per_cu = ceil(blocks / 256.0);
-    // fewer blocks than the CU holds leave some of its rate unused
-    const double filled = per_cu < t.resident ? t.alone + (1.0 - t.alone) * (per_cu - 1.0) / (t.resident - 1.0) : 1.0;
-    const double tile = 2e-6 * t.size * t.size * (ceil((double)K / splits) + t.around) * work;
-    double us = per_cu * tile / (t.mflop_us * filled);
+    // many small blocks even out over the CUs
+    const double per_cu = blocks > 512.0 * t.resident ? blocks / 256.0 + 0.5 : ceil(blocks / 256.0);
+    const double tile = 2e-6 * t.size * t.size * (ceil((double)K / splits) + (per_cu >= t.resident ? t.around : 64)) * work;
+    // the last few blocks of a CU leave some of its rate unused
+    const double whole = floor(per_cu / t.resident) * t.resident, rest = per_cu - whole;
+    const double filled = t.resident > 1 ? t.alone + (1.0 - t.alone) * (rest > 1.0 ? rest - 1.0 : 0.0) / (t.resident - 1.0) : 1.0;
+    double us = tile / t.mflop_us * (whole + rest / filled);
     if (splits > 1) us += 3.0 + splits * (0.1 + (double)P * (double)Q * 4.0 / 6e6);
     return us;
 }
 
 ProductPlan make_plan(int64_t P, int64_t Q, int64_t K, bool pt, bool qt, bool staged, bool f32, int step_k, float work)
 {
-    static const TileRate direct[3] = {{256, 1, 4.9f, 1.0f, 64}, {128, 2, 4.1f, 0.9f, 64}, {64, 3, 2.4f, 0.87f, 64}};
-    static const TileRate limbs[3] = {{256, 1, 0.0f, 1.0f, 64}, {128, 1, 4.1f, 1.0f, 64}, {64, 2, 3.0f, 0.9f, 64}};
+    static const TileRate direct[3] = {{256, 1, 4.9f, 1.0f, 350}, {128, 2, 4.1f, 0.68f, 300}, {64, 3, 2.4f, 0.87f, 200}};
+    static const TileRate limbs[3] = {{256, 1, 0.0f, 1.0f, 64}, {128, 1, 4.8f, 1.0f, 64}, {64, 2, 3.9f, 0.6f, 64}};
     static const TileRate staged_[3] = {{256, 1, 0.0f, 1.0f, 64}, {128, 1, 4.4f, 1.0f, 128}, {64, 3, 3.7f, 0.38f, 64}};
     ProductPlan best{pt, qt, staged, 2, 1, 0.0};
     double least = 1e30;
