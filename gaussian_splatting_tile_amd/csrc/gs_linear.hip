@@ -523,7 +523,9 @@ template <bool EXACT> __global__ __launch_bounds__(kThreads) void dz_planes(DzAr
     column_sums(d, kGroups, acc, sums);
 }
 
-constexpr int kOneRowBlock = 64;                // rows of x that one row block of the pass takes
+// Rows of x that one row block of the pass takes: 128 x 256 x 512 12.5 us against
+// 13.9 with partial sums and their own launch, 256 x 1024 x 256 20.4 against 19.2.
+constexpr int kOneRowBlock = 128;
 
 // Everything a backward call does, with its places in the workspace.
 struct BwdPlan {

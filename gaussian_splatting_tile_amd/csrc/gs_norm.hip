@@ -453,7 +453,9 @@ int grad_blocks(int64_t m, int n)
     if (n > kMaxRegRow) return (int)(m < 64 ? m : 64);
     const int64_t rows = n <= 128 ? 16 : n <= 256 ? 8 : n <= 1024 ? 4 : 1;
     const int64_t passes = (m + rows - 1) / rows, most = n <= 2048 ? 1024 : 512;
-    if (passes <= 4) return 1;                  // its partial row is dgamma: one launch
+    // its partial row is dgamma and saves a launch: 4 x 2034 7.8 us against 7.2 on
+    // the GPU, but a call takes 10.7 against 13.1
+    if (passes <= 4) return 1;
     if (passes <= 256) return (int)passes;
     const int64_t each = n <= 1024 ? 2 : 4, want = passes / each > 256 ? passes / each : 256;
     return (int)(want < most ? want : most);
