@@ -379,6 +379,7 @@ __global__ __launch_bounds__(WP *WQ * 64, waves_per_simd(WP * WQ, NS * NL * (BP 
     constexpr int FP = BP / WP / 16, FQ = BQ / WQ / 16, KK = BK / 32;
     constexpr int ES = KIND == kMX8 ? 1 : 2;
     constexpr int kStepK = KIND == kMX8 ? 2 * BK : BK;  // k per tile
+    static_assert(NS == 2 || NS == 3, "stages");
     static_assert(!PING || (WP * WQ == 8 && !STAGED), "two waves on every SIMD");
     static_assert(KIND != kMX8 || (!PT && !QT && !STAGED && NL == 1 && BK == 64), "8-bit operands");
     using TP = Tile<BP, BK, PT>;
@@ -391,7 +392,6 @@ __global__ __launch_bounds__(WP *WQ * 64, waves_per_simd(WP * WQ, NS * NL * (BP 
     __shared__ __align__(128) char lds0[kStage];
     __shared__ __align__(128) char lds1[kStage];
     __shared__ __align__(128) char lds2[NS > 2 ? kStage : 16];
-    __shared__ __align__(128) char lds3[NS > 3 ? kStage : 16];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wp = wave / WQ, wq = wave % WQ;
@@ -539,7 +539,7 @@ __global__ __launch_bounds__(WP *WQ * 64, waves_per_simd(WP * WQ, NS * NL * (BP 
                 }
             }
         };
-        char *const stage[4] = {lds0, lds1, lds2, lds3};
+        char *const stage[3] = {lds0, lds1, lds2};
 #pragma unroll
         for (int t = 0; t < NS - 1; t++) issue(t, stage[t]);
         const bool late = wave >= WP * WQ / 2;
@@ -554,7 +554,6 @@ __global__ __launch_bounds__(WP *WQ * 64, waves_per_simd(WP * WQ, NS * NL * (BP 
             for (int i = 0; i < NS; i++) turn_stage(t + i, stage[i], stage[(i + NS - 1) % NS]);
         if (t < nt) turn_stage(t, stage[0], stage[NS - 1]);
         if (NS > 2 && t + 1 < nt) turn_stage(t + 1, stage[1], stage[0]);
-        if (NS > 3 && t + 2 < nt) turn_stage(t + 2, stage[2], stage[1]);
         if (PING && !late) __builtin_amdgcn_s_barrier();
     } else {
         // a stage's next tile but one is on its way while it is multiplied
