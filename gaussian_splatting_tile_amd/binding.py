@@ -107,6 +107,7 @@ class GsLinearGrads(C.Structure):
     _fields_ = [("dy", C.c_void_p), ("dy_stride", C.c_int64), ("dx", C.c_void_p), ("dx_stride", C.c_int64),
                 ("dw", C.c_void_p), ("dw_stride", C.c_int64), ("dw_dtype", C.c_int32), ("accumulate", C.c_int32),
                 ("db", C.c_void_p)]
+    dy_dtype = None            # gs_dtype of dy (linear_grads_struct)
 
 
 class GsMuon(C.Structure):
@@ -642,24 +643,38 @@ def linear_grads_struct(a: GsLinear, dy: torch.Tensor, dx: Optional[torch.Tensor
                         accumulate: bool = False) -> GsLinearGrads:
     """Descriptor of the gradients of a linear_struct: dy in y's layout; dx
     [m][k] of x's type, dw [n][k] of float32 or x's type, db [n] float32, each
-    optional; accumulate adds to dw and db.  Sets the descriptor's y_dtype to
-    dy's."""
+    optional; accumulate adds to dw and db.  dy is of y's type; a descriptor
+    without y takes dy's."""
     rows, cols = (a.n, a.m) if a.planes else (a.m, a.n)
-    a.y_dtype = _dtype(dy)
+    dy_dtype = _dtype(dy)
+    if a.y and a.y_dtype != dy_dtype:
+        raise ValueError(f"dy: expected y's type, got {dy.dtype}")
+    a.y_dtype = dy_dtype
     own, dev = _BY_CODE[a.dtype], dy.device
-    return GsLinearGrads(*_rows(dy, rows, cols, "dy"), *_rows(dx, a.m, a.k, "dx", (own,), dev),
-                         *_rows(dw, a.n, a.k, "dw", (own, torch.float32), dev),
-                         GS_DTYPE_F32 if dw is None else _dtype(dw), 1 if accumulate else 0,
-                         _vector(db, a.n, "db", dev))
+    g = GsLinearGrads(*_rows(dy, rows, cols, "dy"), *_rows(dx, a.m, a.k, "dx", (own,), dev),
+                      *_rows(dw, a.n, a.k, "dw", (own, torch.float32), dev),
+                      GS_DTYPE_F32 if dw is None else _dtype(dw), 1 if accumulate else 0,
+                      _vector(db, a.n, "db", dev))
+    g.dy_dtype = dy_dtype
+    return g
+
+
+def _for_dy(a: GsLinear, g: GsLinearGrads) -> GsLinear:
+    """The descriptor with dy's type, which another dy may have changed since."""
+    if g.dy_dtype in (None, a.y_dtype):
+        return a
+    b = GsLinear.from_buffer_copy(a)
+    b.y_dtype = g.dy_dtype
+    return b
 
 
 def linear_bwd_workspace_bytes(a: GsLinear, g: GsLinearGrads) -> int:
-    return int(lib().gs_linear_bwd_workspace_bytes(C.byref(a), C.byref(g)))
+    return int(lib().gs_linear_bwd_workspace_bytes(C.byref(_for_dy(a, g)), C.byref(g)))
 
 
 def linear_bwd(a: GsLinear, g: GsLinearGrads, workspace: Optional[torch.Tensor] = None, stream=None):
     """gs_linear_bwd of a linear_struct and its linear_grads_struct."""
-    _check(lib().gs_linear_bwd(C.byref(a), C.byref(g), _ptr(workspace), _nbytes(workspace), _stream(stream)),
+    _check(lib().gs_linear_bwd(C.byref(_for_dy(a, g)), C.byref(g), _ptr(workspace), _nbytes(workspace), _stream(stream)),
            "gs_linear_bwd")
 
 

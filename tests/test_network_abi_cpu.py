@@ -199,3 +199,29 @@ def test_binding_refuses_tensors_that_do_not_fit():
     lin = B.linear_struct(x, w, y)
     with pytest.raises(ValueError):
         B.linear_grads_struct(lin, y, dw=torch.zeros(8, 64, dtype=torch.float16))
+
+
+def test_gradients_leave_the_forward_descriptor_as_it_is():
+    """A y of one type and a dy of another in one descriptor would have the
+    next forward write dy's type into y."""
+    x, w = torch.zeros(40, 64, dtype=torch.bfloat16), torch.zeros(8, 64, dtype=torch.bfloat16)
+    dy, dw = torch.zeros(40, 8, dtype=torch.bfloat16), torch.zeros(8, 64)
+    lin = B.linear_struct(x, w, dy.clone())
+    with pytest.raises(ValueError):
+        B.linear_grads_struct(lin, dy.float(), dw=dw)
+    assert lin.y_dtype == B.GS_DTYPE_BF16
+    B.linear_grads_struct(lin, dy, dw=dw)
+    assert lin.y_dtype == B.GS_DTYPE_BF16
+
+
+def test_a_descriptor_without_y_takes_gradients_of_any_type():
+    """Each of them is used with its own type, whichever was made last: an
+    fp32 dy of bf16 operands has to be converted first, a bf16 one is read as
+    it is."""
+    x, w = torch.zeros(40, 64, dtype=torch.bfloat16), torch.zeros(8, 64, dtype=torch.bfloat16)
+    dy, dw = torch.zeros(40, 8, dtype=torch.bfloat16), torch.zeros(8, 64)
+    size = lambda d: (lambda a: B.linear_bwd_workspace_bytes(a, B.linear_grads_struct(a, d, dw=dw)))(B.linear_struct(x, w, None))
+    assert size(dy) != size(dy.float())
+    lin = B.linear_struct(x, w, None)
+    kept = [B.linear_grads_struct(lin, d, dw=dw) for d in (dy, dy.float(), dy)]
+    assert [B.linear_bwd_workspace_bytes(lin, g) for g in kept] == [size(dy), size(dy.float()), size(dy)]
