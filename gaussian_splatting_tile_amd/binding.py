@@ -699,9 +699,10 @@ def muon_struct(grad: torch.Tensor, out: Optional[torch.Tensor] = None, momentum
     for t, what in ((momentum, "momentum"), (momentum_out, "momentum_out")):
         if t is not None and t.dtype != torch.float32:
             raise ValueError(f"{what}: expected float32")
-    if weight is not None and weight.dtype != weight_out.dtype:
-        raise ValueError("weight_out: expected weight's type")
-    to = weight if weight is not None else out if out is not None else grad
+    results = [t for t in (weight, weight_out, out) if t is not None] or [grad]
+    to = results[0]
+    if any(t.dtype != to.dtype for t in results):
+        raise ValueError("weight, weight_out, out: expected one type")
     return GsMuon(shape[0] if len(shape) == 3 else 1, shape[-2], shape[-1], _dtype(grad), _dtype(to), steps, *coeffs, eps,
                   lr, beta, weight_decay, scale, 1 if nesterov else 0, _ptr(grad), _ptr(out), _ptr(momentum),
                   _ptr(momentum_out), _ptr(weight), _ptr(weight_out))

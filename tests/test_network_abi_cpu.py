@@ -225,3 +225,16 @@ def test_a_descriptor_without_y_takes_gradients_of_any_type():
     lin = B.linear_struct(x, w, None)
     kept = [B.linear_grads_struct(lin, d, dw=dw) for d in (dy, dy.float(), dy)]
     assert [B.linear_bwd_workspace_bytes(lin, g) for g in kept] == [size(dy), size(dy.float()), size(dy)]
+
+
+def test_muon_results_have_one_type():
+    """One type describes out and weight: of two the other would be written in
+    elements of the wrong size."""
+    g = torch.zeros(4, 64)
+    for out, weight in ((torch.bfloat16, torch.float32), (torch.float32, torch.float16)):
+        with pytest.raises(ValueError):
+            B.muon_struct(g, out=g.to(out), momentum=g, weight=g.to(weight))
+    with pytest.raises(ValueError):
+        B.muon_struct(g, out=g.half(), momentum=g, weight_out=g)
+    a = B.muon_struct(g, out=g.half(), momentum=g, weight=g.half())
+    assert a.out_dtype == B.GS_DTYPE_F16 and B.muon_struct(g, out=g.bfloat16()).out_dtype == B.GS_DTYPE_BF16
