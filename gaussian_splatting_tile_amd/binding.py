@@ -101,6 +101,7 @@ class GsLinear(C.Structure):
                 ("w_scales", C.c_void_p), ("w_scales_stride", C.c_int64), ("bias", C.c_void_p),
                 ("residual", C.c_void_p), ("residual_stride", C.c_int64), ("y", C.c_void_p), ("y_stride", C.c_int64),
                 ("z", C.c_void_p), ("z_stride", C.c_int64)]
+    device = None              # of the tensors (linear_struct)
 
 
 class GsLinearGrads(C.Structure):
@@ -117,6 +118,7 @@ class GsMuon(C.Structure):
                 ("scale", C.c_float), ("nesterov", C.c_int32), ("grad", C.c_void_p), ("out", C.c_void_p),
                 ("momentum", C.c_void_p), ("momentum_out", C.c_void_p), ("weight", C.c_void_p),
                 ("weight_out", C.c_void_p)]
+    device = None              # of the tensors (muon_struct)
 
 
 class GsError(RuntimeError):
@@ -236,6 +238,24 @@ def _stream(stream=None):
         # the handle alone: making a Stream object of it takes 1.3 us, a tenth of a small call
         return C.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     return C.c_void_p(stream.cuda_stream)
+
+
+def _stream_for(device: Optional[torch.device], workspace: Optional[torch.Tensor], stream=None):
+    """The stream of a call whose tensors are on `device` (None: not known).
+    Kernels get bare addresses: the host's memory or another GPU's is refused
+    here."""
+    if device is None:
+        return _stream(stream)
+    index = device.index
+    if device.type != "cuda" or index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {device}: expected the current GPU")
+    if workspace is not None and (workspace.device != device or not workspace.is_contiguous()):
+        raise ValueError("workspace: expected contiguous memory on the tensors' device")
+    if stream is None:
+        return C.c_void_p(torch._C._cuda_getCurrentRawStream(index))
+    if stream.device != device:
+        raise ValueError(f"stream of {stream.device} for tensors on {device}")
+    return _stream(stream)
 
 
 def camera_struct(cam) -> GsCamera:
@@ -573,7 +593,7 @@ def rms_norm_fwd(x: torch.Tensor, y: torch.Tensor, gamma: Optional[torch.Tensor]
                   _vector(gamma, n, "gamma", dev), *_rows(sum_out, m, n, "sum_out", own, dev),
                   *_rows(y, m, n, "y", (x.dtype, torch.float8_e4m3fn), dev),
                   *_rows(y_scales, m, n // 32, "y_scales", _SCALES, dev), _vector(rstd, m, "rstd", dev))
-    _check(lib().gs_rms_norm_fwd(C.byref(a), _stream(stream)), "gs_rms_norm_fwd")
+    _check(lib().gs_rms_norm_fwd(C.byref(a), _stream_for(dev, None, stream)), "gs_rms_norm_fwd")
 
 
 def rms_norm_bwd_workspace_bytes(m: int, n: int) -> int:
@@ -593,7 +613,8 @@ def rms_norm_bwd(sum_in: torch.Tensor, rstd: torch.Tensor, dy: torch.Tensor, dx:
                        _vector(gamma, n, "gamma", dev), *_rows(dy, m, n, "dy", own, dev),
                        *_rows(dsum, m, n, "dsum", own, dev), *_rows(dx, m, n, "dx", own, dev),
                        _vector(dgamma, n, "dgamma", dev), 1 if accumulate else 0)
-    _check(lib().gs_rms_norm_bwd(C.byref(a), _ptr(workspace), _nbytes(workspace), _stream(stream)), "gs_rms_norm_bwd")
+    _check(lib().gs_rms_norm_bwd(C.byref(a), _ptr(workspace), _nbytes(workspace), _stream_for(dev, workspace, stream)),
+           "gs_rms_norm_bwd")
 
 
 def mxfp8_quantize(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None):
@@ -604,7 +625,8 @@ def mxfp8_quantize(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, s
     xp, xs = _rows(x, m, n, "x")
     cp, cs = _rows(codes, m, n, "codes", (torch.float8_e4m3fn,), dev)
     sp, ss = _rows(scales, m, n // 32, "scales", _SCALES, dev)
-    _check(lib().gs_mxfp8_quantize(xp, _dtype(x), m, n, xs, cp, cs, sp, ss, _stream(stream)), "gs_mxfp8_quantize")
+    _check(lib().gs_mxfp8_quantize(xp, _dtype(x), m, n, xs, cp, cs, sp, ss, _stream_for(dev, None, stream)),
+           "gs_mxfp8_quantize")
 
 
 def linear_struct(x: torch.Tensor, w: torch.Tensor, y: Optional[torch.Tensor],
@@ -620,12 +642,14 @@ def linear_struct(x: torch.Tensor, w: torch.Tensor, y: Optional[torch.Tensor],
     rows, cols = (n, m) if planes else (m, n)
     yt = None if y is None else (y.dtype,)
     block = x.dtype is torch.float8_e4m3fn
-    return GsLinear(m, n, k, _dtype(x), _dtype(x if y is None else y), GS_ACT[act], 1 if planes else 0,
-                    *_rows(x, m, k, "x"), *_rows(w, n, k, "w", own, dev),
-                    *(_rows(x_scales, m, k // 32, "x_scales", _SCALES, dev) if block else (None, 0)),
-                    *(_rows(w_scales, n, k // 32, "w_scales", _SCALES, dev) if block else (None, 0)),
-                    _vector(bias, n, "bias", dev), *_rows(residual, rows, cols, "residual", yt, dev),
-                    *_rows(y, rows, cols, "y", None, dev), *_rows(z, m, n, "z", own, dev))
+    a = GsLinear(m, n, k, _dtype(x), _dtype(x if y is None else y), GS_ACT[act], 1 if planes else 0,
+                 *_rows(x, m, k, "x"), *_rows(w, n, k, "w", own, dev),
+                 *(_rows(x_scales, m, k // 32, "x_scales", _SCALES, dev) if block else (None, 0)),
+                 *(_rows(w_scales, n, k // 32, "w_scales", _SCALES, dev) if block else (None, 0)),
+                 _vector(bias, n, "bias", dev), *_rows(residual, rows, cols, "residual", yt, dev),
+                 *_rows(y, rows, cols, "y", None, dev), *_rows(z, m, n, "z", own, dev))
+    a.device = dev
+    return a
 
 
 def linear_fwd_workspace_bytes(a: GsLinear) -> int:
@@ -635,7 +659,8 @@ def linear_fwd_workspace_bytes(a: GsLinear) -> int:
 def linear_fwd(a: GsLinear, workspace: Optional[torch.Tensor] = None, stream=None):
     """gs_linear_fwd of a linear_struct; the tensors it was made from must be
     alive."""
-    _check(lib().gs_linear_fwd(C.byref(a), _ptr(workspace), _nbytes(workspace), _stream(stream)), "gs_linear_fwd")
+    _check(lib().gs_linear_fwd(C.byref(a), _ptr(workspace), _nbytes(workspace), _stream_for(a.device, workspace, stream)),
+           "gs_linear_fwd")
 
 
 def linear_grads_struct(a: GsLinear, dy: torch.Tensor, dx: Optional[torch.Tensor] = None,
@@ -650,8 +675,8 @@ def linear_grads_struct(a: GsLinear, dy: torch.Tensor, dx: Optional[torch.Tensor
     if a.y and a.y_dtype != dy_dtype:
         raise ValueError(f"dy: expected y's type, got {dy.dtype}")
     a.y_dtype = dy_dtype
-    own, dev = _BY_CODE[a.dtype], dy.device
-    g = GsLinearGrads(*_rows(dy, rows, cols, "dy"), *_rows(dx, a.m, a.k, "dx", (own,), dev),
+    own, dev = _BY_CODE[a.dtype], dy.device if a.device is None else a.device
+    g = GsLinearGrads(*_rows(dy, rows, cols, "dy", None, dev), *_rows(dx, a.m, a.k, "dx", (own,), dev),
                       *_rows(dw, a.n, a.k, "dw", (own, torch.float32), dev),
                       GS_DTYPE_F32 if dw is None else _dtype(dw), 1 if accumulate else 0,
                       _vector(db, a.n, "db", dev))
@@ -674,8 +699,8 @@ def linear_bwd_workspace_bytes(a: GsLinear, g: GsLinearGrads) -> int:
 
 def linear_bwd(a: GsLinear, g: GsLinearGrads, workspace: Optional[torch.Tensor] = None, stream=None):
     """gs_linear_bwd of a linear_struct and its linear_grads_struct."""
-    _check(lib().gs_linear_bwd(C.byref(_for_dy(a, g)), C.byref(g), _ptr(workspace), _nbytes(workspace), _stream(stream)),
-           "gs_linear_bwd")
+    _check(lib().gs_linear_bwd(C.byref(_for_dy(a, g)), C.byref(g), _ptr(workspace), _nbytes(workspace),
+                               _stream_for(a.device, workspace, stream)), "gs_linear_bwd")
 
 
 def muon_struct(grad: torch.Tensor, out: Optional[torch.Tensor] = None, momentum: Optional[torch.Tensor] = None,
@@ -703,9 +728,11 @@ def muon_struct(grad: torch.Tensor, out: Optional[torch.Tensor] = None, momentum
     to = results[0]
     if any(t.dtype != to.dtype for t in results):
         raise ValueError("weight, weight_out, out: expected one type")
-    return GsMuon(shape[0] if len(shape) == 3 else 1, shape[-2], shape[-1], _dtype(grad), _dtype(to), steps, *coeffs, eps,
-                  lr, beta, weight_decay, scale, 1 if nesterov else 0, _ptr(grad), _ptr(out), _ptr(momentum),
-                  _ptr(momentum_out), _ptr(weight), _ptr(weight_out))
+    a = GsMuon(shape[0] if len(shape) == 3 else 1, shape[-2], shape[-1], _dtype(grad), _dtype(to), steps, *coeffs, eps,
+               lr, beta, weight_decay, scale, 1 if nesterov else 0, _ptr(grad), _ptr(out), _ptr(momentum),
+               _ptr(momentum_out), _ptr(weight), _ptr(weight_out))
+    a.device = grad.device
+    return a
 
 
 def muon_workspace_bytes(a: GsMuon) -> int:
@@ -714,12 +741,14 @@ def muon_workspace_bytes(a: GsMuon) -> int:
 
 def orthogonalize(a: GsMuon, workspace: torch.Tensor, stream=None):
     """gs_orthogonalize: a's out receives the orthogonalised grad."""
-    _check(lib().gs_orthogonalize(C.byref(a), _ptr(workspace), _nbytes(workspace), _stream(stream)), "gs_orthogonalize")
+    _check(lib().gs_orthogonalize(C.byref(a), _ptr(workspace), _nbytes(workspace), _stream_for(a.device, workspace, stream)),
+           "gs_orthogonalize")
 
 
 def muon_step(a: GsMuon, workspace: torch.Tensor, stream=None):
     """gs_muon_step: momentum, orthogonalised update and weight decay."""
-    _check(lib().gs_muon_step(C.byref(a), _ptr(workspace), _nbytes(workspace), _stream(stream)), "gs_muon_step")
+    _check(lib().gs_muon_step(C.byref(a), _ptr(workspace), _nbytes(workspace), _stream_for(a.device, workspace, stream)),
+           "gs_muon_step")
 
 
 # ---- buffers for one view ---------------------------------------------------

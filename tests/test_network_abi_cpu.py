@@ -238,3 +238,43 @@ def test_muon_results_have_one_type():
         B.muon_struct(g, out=g.half(), momentum=g, weight_out=g)
     a = B.muon_struct(g, out=g.half(), momentum=g, weight=g.half())
     assert a.out_dtype == B.GS_DTYPE_F16 and B.muon_struct(g, out=g.bfloat16()).out_dtype == B.GS_DTYPE_BF16
+
+
+def test_calls_refuse_memory_that_the_gpu_must_not_touch(monkeypatch):
+    """Tensors of the host or of another GPU than the current one, and
+    workspaces that are not so many bytes of that GPU's memory."""
+    x, w, v = torch.zeros(4, 64), torch.zeros(8, 64), torch.zeros(4)
+    codes, scales = torch.zeros(4, 64, dtype=torch.float8_e4m3fn), torch.zeros(4, 2, dtype=torch.uint8)
+    lin = B.linear_struct(x, w, torch.zeros(4, 8))
+    gr = B.linear_grads_struct(lin, torch.zeros(4, 8), dx=torch.zeros(4, 64))
+    mu = B.muon_struct(x, out=x, momentum=x, weight=x)
+    ws = torch.zeros(1 << 20, dtype=torch.uint8)
+    calls = [lambda: B.rms_norm_fwd(x, x), lambda: B.rms_norm_bwd(x, v, x, x), lambda: B.mxfp8_quantize(x, codes, scales),
+             lambda: B.linear_fwd(lin, ws), lambda: B.linear_bwd(lin, gr, ws), lambda: B.orthogonalize(mu, ws),
+             lambda: B.muon_step(mu, ws)]
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    for call in calls:
+        with pytest.raises(ValueError):
+            call()
+    gpu, ok = torch.device("cuda", 0), ws.to("meta")
+    for device, workspace, stream in ((torch.device("cuda", 1), None, None), (gpu, ws, None), (gpu, ws[::2], None)):
+        with pytest.raises(ValueError):
+            B._stream_for(device, workspace, stream)
+
+    class Side:
+        device, cuda_stream = gpu, 64
+
+    class Shared(torch.Tensor):                     # a workspace's properties, without one
+        device = gpu
+
+    whole = torch.zeros(16, dtype=torch.uint8).as_subclass(Shared)
+    assert B._stream_for(gpu, whole, Side).value == 64 and B._stream_for(None, ok, Side).value == 64
+    Side.device = torch.device("cuda", 1)
+    with pytest.raises(ValueError):
+        B._stream_for(gpu, whole, Side)
+    Side.device = gpu
+    for bad in (whole[::2], whole[:1].expand(16)):
+        with pytest.raises(ValueError):
+            B._stream_for(gpu, bad, Side)
+    with pytest.raises(ValueError):
+        B.linear_grads_struct(lin, torch.zeros(4, 8, device="meta"))
