@@ -553,6 +553,12 @@ def _dtype(t: torch.Tensor) -> int:
         raise ValueError(f"unsupported element type {t.dtype}") from None
 
 
+def _int32(*sizes: int):
+    """ctypes cuts larger values to their low bits."""
+    if max(sizes) >= 1 << 31:
+        raise ValueError(f"sizes {sizes}: more than 32 bits hold")
+
+
 def _rows(t: Optional[torch.Tensor], rows: int, cols: int, what: str, dtypes=None, device=None):
     """(address, row stride) of a [rows][cols] tensor whose rows are
     contiguous; (None, cols) for None."""
@@ -588,6 +594,7 @@ def rms_norm_fwd(x: torch.Tensor, y: torch.Tensor, gamma: Optional[torch.Tensor]
     bfloat16): y = (x + residual) * rstd * gamma in x's type, or
     torch.float8_e4m3fn with y_scales [m][n / 32] (uint8 or float8_e8m0fnu)."""
     m, n = x.shape
+    _int32(n)
     own, dev = (x.dtype,), x.device
     a = GsRmsNorm(m, n, _dtype(x), _dtype(y), eps, *_rows(x, m, n, "x"), *_rows(residual, m, n, "residual", own, dev),
                   _vector(gamma, n, "gamma", dev), *_rows(sum_out, m, n, "sum_out", own, dev),
@@ -597,6 +604,7 @@ def rms_norm_fwd(x: torch.Tensor, y: torch.Tensor, gamma: Optional[torch.Tensor]
 
 
 def rms_norm_bwd_workspace_bytes(m: int, n: int) -> int:
+    _int32(n)
     return int(lib().gs_rms_norm_bwd_workspace_bytes(m, n))
 
 
@@ -608,6 +616,7 @@ def rms_norm_bwd(sum_in: torch.Tensor, rstd: torch.Tensor, dy: torch.Tensor, dx:
     gradient dx of x and residual and, with dgamma and a workspace of
     rms_norm_bwd_workspace_bytes(m, n), that of gamma."""
     m, n = sum_in.shape
+    _int32(n)
     own, dev = (sum_in.dtype,), sum_in.device
     a = GsRmsNormGrads(m, n, _dtype(sum_in), *_rows(sum_in, m, n, "sum_in"), _vector(rstd, m, "rstd", dev),
                        _vector(gamma, n, "gamma", dev), *_rows(dy, m, n, "dy", own, dev),
@@ -621,6 +630,7 @@ def mxfp8_quantize(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, s
     """gs_mxfp8_quantize: x [m][n] -> codes float8_e4m3fn [m][n] and scales
     [m][n / 32] (uint8 or float8_e8m0fnu)."""
     m, n = x.shape
+    _int32(n)
     dev = x.device
     xp, xs = _rows(x, m, n, "x")
     cp, cs = _rows(codes, m, n, "codes", (torch.float8_e4m3fn,), dev)
@@ -638,6 +648,7 @@ def linear_struct(x: torch.Tensor, w: torch.Tensor, y: Optional[torch.Tensor],
     z: the pre-activation kept for the backward, [m][n] of x's type."""
     m, k = x.shape
     n = w.shape[0]
+    _int32(n, k)
     own, dev = (x.dtype,), x.device
     rows, cols = (n, m) if planes else (m, n)
     yt = None if y is None else (y.dtype,)
@@ -715,6 +726,7 @@ def muon_struct(grad: torch.Tensor, out: Optional[torch.Tensor] = None, momentum
     shape = grad.shape
     if len(shape) not in (2, 3):
         raise ValueError("grad: expected [rows][cols] or [batch][rows][cols]")
+    _int32(*shape)
     momentum_out = momentum if momentum_out is None else momentum_out
     weight_out = weight if weight_out is None else weight_out
     for t, what in ((grad, "grad"), (out, "out"), (momentum, "momentum"), (weight, "weight"),

@@ -278,3 +278,25 @@ def test_calls_refuse_memory_that_the_gpu_must_not_touch(monkeypatch):
             B._stream_for(gpu, bad, Side)
     with pytest.raises(ValueError):
         B.linear_grads_struct(lin, torch.zeros(4, 8, device="meta"))
+
+
+def test_sizes_that_the_descriptors_cannot_hold():
+    """A size of 2^32 + 64 in a 32-bit field would read as 64."""
+    big = (1 << 32) + 64
+    e = lambda *s, t=torch.bfloat16: torch.empty(s, dtype=t, device="meta")
+    too_large = lambda: pytest.raises(ValueError, match="32 bits")
+    with too_large():
+        B.linear_struct(e(1, big), e(8, big), e(1, 8))
+    with too_large():
+        B.linear_struct(e(1, 8), e(big, 8), e(1, big))
+    with too_large():
+        B.rms_norm_fwd(e(1, big), e(1, big))
+    with too_large():
+        B.rms_norm_bwd(e(1, big), e(1, t=torch.float32), e(1, big), e(1, big))
+    with too_large():
+        B.rms_norm_bwd_workspace_bytes(1, big)
+    with too_large():
+        B.mxfp8_quantize(e(1, big), e(1, big, t=torch.float8_e4m3fn), e(1, big // 32, t=torch.uint8))
+    for shape in ((big, 8), (8, big), (big, 1, 8)):
+        with too_large():
+            B.muon_struct(e(*shape), out=e(*shape))
