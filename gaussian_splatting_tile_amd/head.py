@@ -26,8 +26,9 @@ from . import binding as B
 
 
 class GaussianHead:
-    """Weights, activations and buffers for up to `m` tokens.  `width` and
-    `hidden` are multiples of 32 (the 8-bit blocks)."""
+    """Weights, activations and buffers for training on `m` tokens; serve()
+    takes any number.  `width` and `hidden` are multiples of 32 (the 8-bit
+    blocks)."""
 
     def __init__(self, m: int, width: int, hidden: int, blocks: int, sh_degree: int = 3, act: str = "gelu",
                  dtype=torch.bfloat16, device="cuda", seed: int = 0):
@@ -71,6 +72,8 @@ class GaussianHead:
     # ---- training -----------------------------------------------------------
     def forward(self, tokens: torch.Tensor) -> torch.Tensor:
         """The parameter planes [rows][m] (fp32) of tokens [m][width]."""
+        if tokens.shape != (self.m, self.width):
+            raise ValueError(f"tokens: expected [{self.m}][{self.width}], got {tuple(tokens.shape)}")
         self.s[0].copy_(tokens)
         for i in range(self.blocks):
             B.rms_norm_fwd(self.s[i], self.normed[i], gamma=self.gamma[i], rstd=self.rstd[i])
@@ -135,6 +138,8 @@ class GaussianHead:
         """The planes of any number of tokens, the blocks by 8-bit products
         (quantize() first).  The last product stays in the weights' own type:
         a Gaussian's position has to be good to a fraction of its size."""
+        if tokens.dim() != 2 or tokens.shape[1] != self.width:
+            raise ValueError(f"tokens: expected [n][{self.width}], got {tuple(tokens.shape)}")
         n, dev = tokens.shape[0], tokens.device
         codes = lambda w: (torch.empty((n, w), dtype=torch.float8_e4m3fn, device=dev), torch.empty((n, w // 32), dtype=torch.uint8, device=dev))
         s, (y, ys), (hq, hs) = tokens.to(self.w1.dtype).clone(), codes(self.width), codes(self.hidden)
