@@ -246,13 +246,13 @@ def _stream_for(device: Optional[torch.device], workspace: Optional[torch.Tensor
     here."""
     if device is None:
         return _stream(stream)
-    index = device.index
-    if device.type != "cuda" or index != torch.cuda.current_device():
+    index = device.index                                # None: the host; else the GPU is in use and its number at hand
+    if index is None or index != torch._C._cuda_getDevice():
         raise ValueError(f"tensors on {device}: expected the current GPU")
-    if workspace is not None and (workspace.device != device or not workspace.is_contiguous()):
+    if workspace is not None and (workspace.get_device() != index or not workspace.is_contiguous()):
         raise ValueError("workspace: expected contiguous memory on the tensors' device")
     if stream is None:
-        return C.c_void_p(torch._C._cuda_getCurrentRawStream(index))
+        return torch._C._cuda_getCurrentRawStream(index)
     if stream.device != device:
         raise ValueError(f"stream of {stream.device} for tensors on {device}")
     return _stream(stream)
@@ -555,8 +555,9 @@ def _dtype(t: torch.Tensor) -> int:
 
 def _int32(*sizes: int):
     """ctypes cuts larger values to their low bits."""
-    if max(sizes) >= 1 << 31:
-        raise ValueError(f"sizes {sizes}: more than 32 bits hold")
+    for size in sizes:
+        if size >> 31:
+            raise ValueError(f"sizes {sizes}: more than 32 bits hold")
 
 
 def _rows(t: Optional[torch.Tensor], rows: int, cols: int, what: str, dtypes=None, device=None):

@@ -252,7 +252,7 @@ def test_calls_refuse_memory_that_the_gpu_must_not_touch(monkeypatch):
     calls = [lambda: B.rms_norm_fwd(x, x), lambda: B.rms_norm_bwd(x, v, x, x), lambda: B.mxfp8_quantize(x, codes, scales),
              lambda: B.linear_fwd(lin, ws), lambda: B.linear_bwd(lin, gr, ws), lambda: B.orthogonalize(mu, ws),
              lambda: B.muon_step(mu, ws)]
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
     for call in calls:
         with pytest.raises(ValueError):
             call()
@@ -265,7 +265,8 @@ def test_calls_refuse_memory_that_the_gpu_must_not_touch(monkeypatch):
         device, cuda_stream = gpu, 64
 
     class Shared(torch.Tensor):                     # a workspace's properties, without one
-        device = gpu
+        def get_device(self):
+            return 0
 
     whole = torch.zeros(16, dtype=torch.uint8).as_subclass(Shared)
     assert B._stream_for(gpu, whole, Side).value == 64 and B._stream_for(None, ok, Side).value == 64
