@@ -129,8 +129,8 @@ template <typename T, int LANES, int V, bool WIDE> __global__ __launch_bounds__(
 {
     __shared__ float lds[kThreads / 64];
     const int lane = threadIdx.x % LANES;
-    const int64_t row = (int64_t)blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
-    if (row >= a.m) return;                     // a row's lanes together; a workgroup's single row is always there
+    const int64_t row = block_of() * (kThreads / LANES) + threadIdx.x / LANES;
+    if (row >= a.m) return;                     // a row's lanes together
     auto chunk = [&](int k) { return (k * LANES + lane) * 8; };
     auto start = [&](int c) { return WIDE ? min(c, a.n - 8) : c; };
     auto inside = [&](int at) { return WIDE ? 8 : min(8, a.n - at); };
@@ -170,7 +170,8 @@ template <typename T, int LANES, int V, bool WIDE> __global__ __launch_bounds__(
 template <typename T> __global__ __launch_bounds__(kThreads) void norm_long(NormArgs a)
 {
     __shared__ float lds[kThreads / 64];
-    const int64_t row = blockIdx.x;
+    const int64_t row = block_of();
+    if (row >= a.m) return;
     auto sum_at = [&](int c, int valid, float v[8]) {
         load_chunk(static_cast<const T *>(a.x), row * a.ldx + c, valid, v);
         if (a.residual) {
@@ -202,7 +203,8 @@ template <typename T> __global__ __launch_bounds__(kThreads) void norm_long(Norm
 
 template <typename T> hipError_t launch_norm(const NormArgs &a, hipStream_t s)
 {
-    const unsigned rows16 = (unsigned)((a.m + 15) / 16), rows8 = (unsigned)((a.m + 7) / 8), rows4 = (unsigned)((a.m + 3) / 4), rows1 = (unsigned)a.m;
+    const dim3 rows16 = grid_of((a.m + 15) / 16, kThreads), rows8 = grid_of((a.m + 7) / 8, kThreads), rows4 = grid_of((a.m + 3) / 4, kThreads),
+               rows1 = grid_of(a.m, kThreads);
     if (a.n < 8) norm_rows<T, 16, 1, false><<<rows16, kThreads, 0, s>>>(a);
     else if (a.n <= 128) norm_rows<T, 16, 1, true><<<rows16, kThreads, 0, s>>>(a);
     else if (a.n <= 256) norm_rows<T, 32, 1, true><<<rows8, kThreads, 0, s>>>(a);
@@ -367,7 +369,8 @@ template <typename T, int LANES, int V, bool WIDE> __global__ __launch_bounds__(
 template <typename T> __global__ __launch_bounds__(kThreads) void grad_long(GradArgs a)
 {
     __shared__ float lds[kThreads / 64];
-    const int64_t row = blockIdx.x;
+    const int64_t row = block_of();
+    if (row >= a.m) return;
     const float rstd = a.rstd[row];
     float dot = 0.0f;
     auto at = [&](int c, int valid, float h[8], float g[8]) {
@@ -475,7 +478,7 @@ template <typename T> hipError_t launch_grad(const GradArgs &a, hipStream_t s)
     else {
         // dgamma first: dx may be written over dy
         if (a.part) dgamma_long<T><<<dim3((unsigned)((a.n + 2047) / 2048), g), kThreads, 0, s>>>(a);
-        grad_long<T><<<(unsigned)a.m, kThreads, 0, s>>>(a);
+        grad_long<T><<<grid_of(a.m, kThreads), kThreads, 0, s>>>(a);
     }
     return hipGetLastError();
 }

@@ -12,6 +12,15 @@ namespace gsi {
 
 __host__ __device__ constexpr int dtype_bytes(int t) { return t == GS_DTYPE_F32 ? 4 : t == GS_DTYPE_MXFP8 ? 1 : 2; }
 
+// HIP takes fewer than 2^32 threads along a dimension of a launch: more blocks
+// than that are spread over y too, and those past the last find nothing to do.
+inline dim3 grid_of(int64_t blocks, int threads)
+{
+    const int64_t most = 0xFFFFFFFFll / threads, y = (blocks + most - 1) / most;
+    return dim3((unsigned)((blocks + y - 1) / y), (unsigned)y);
+}
+__device__ __forceinline__ int64_t block_of() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
 // Consecutive values as one vector access of up to 16 bytes.  Only the elements'
 // own alignment is asked for: the hardware takes the wide accesses at any
 // address of global memory, so odd strides and offsets need no other path.
