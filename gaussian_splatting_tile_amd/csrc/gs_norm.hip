@@ -153,7 +153,10 @@ template <typename T, int LANES, int V, bool WIDE> __global__ __launch_bounds__(
     for (int k = 0; k < V; k++) {
         const int shared = WIDE ? max(0, min(8, chunk(k) - (a.n - 8))) : 0;
 #pragma unroll
-        for (int j = 0; j < 8; j++) sq = fmaf(v[k][j], j >= shared ? v[k][j] : 0.0f, sq);
+        for (int j = 0; j < 8; j++) {           // not times 0: an infinity would make the row NaN
+            const float own = j >= shared ? v[k][j] : 0.0f;
+            sq = fmaf(own, own, sq);
+        }
     }
     const float rstd = inverse_rms(row_sum<LANES>(sq, lds), a.n, a.eps);
     if (a.rstd && lane == 0) a.rstd[row] = rstd;
