@@ -659,6 +659,10 @@ __global__ __launch_bounds__(WP *WQ * 64, waves_per_simd(WP * WQ, NS * NL * (BP 
     }
 }
 
+// Tiles of one launch: HIP takes fewer than 2^32 threads along a dimension, and
+// blocks have up to 512.
+constexpr int64_t kMaxTiles = (1 << 23) - 1;
+
 inline bool al16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
 // Whether an operand may be loaded directly: 16-byte pieces must not cross
@@ -679,7 +683,8 @@ hipError_t launch(Args a, const typename EPI::Args &e, int splits, int batch, hi
     const int nt = (a.K + kStepK - 1) / kStepK, per = (nt + splits - 1) / splits;
     if ((nt + per - 1) / per != splits) return hipErrorInvalidValue;       // every split has at least one tile
     a.k_split = per * kStepK;
-    const int tiles = a.symmetric ? a.tiles_p * (a.tiles_p + 1) / 2 : a.tiles_p * a.tiles_q;
+    const int64_t tiles = a.symmetric ? (int64_t)a.tiles_p * (a.tiles_p + 1) / 2 : (int64_t)a.tiles_p * a.tiles_q;
+    if (tiles > kMaxTiles || tiles * splits * batch > INT32_MAX) return hipErrorInvalidValue;
     const dim3 grid((unsigned)tiles, (unsigned)splits, (unsigned)batch);
     product_kernel<KIND, NL, NS, BK, BP, BQ, WP, WQ, PT, QT, STAGED, PING, EPI><<<grid, WP * WQ * 64, 0, s>>>(a, e);
     return hipGetLastError();

@@ -128,7 +128,7 @@ __device__ __forceinline__ void store_planes(uint16_t *dst, int64_t plane, int64
 // A thread per 8 columns of a row.
 __global__ __launch_bounds__(kThreads) void pack_operands(PackJobs jobs)
 {
-    const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    const int64_t id = block_of() * kThreads + threadIdx.x;
     if (id >= jobs.threads) return;
     const PackJob j = jobs.count > 1 && id >= jobs.job[1].first ? jobs.job[1] : jobs.job[0];
     const int64_t groups = j.ld_dst / 8, at = id - j.first, r = at / groups;
@@ -167,7 +167,7 @@ void add_job(PackJobs &jobs, const void *src, int type, const uint8_t *scales, i
 hipError_t run_jobs(const PackJobs &jobs, hipStream_t s)
 {
     if (jobs.count == 0) return hipSuccess;
-    pack_operands<<<(unsigned)((jobs.threads + kThreads - 1) / kThreads), kThreads, 0, s>>>(jobs);
+    pack_operands<<<grid_of((jobs.threads + kThreads - 1) / kThreads, kThreads), kThreads, 0, s>>>(jobs);
     return hipGetLastError();
 }
 
@@ -278,8 +278,53 @@ __global__ __launch_bounds__(kReduceThreads) void reduce_splits(LinearEpilogue::
     }
 }
 
+// `count` of the product's columns (along p) or rows (along q) of results, from `at` on.
+Product band_of(const Product &whole, bool along_p, int at, int count)
+{
+    Product r = whole;
+    gemm::Args &a = r.a;
+    LinearEpilogue::Args &e = r.e;
+    const auto move = [](auto &base, int64_t bytes) {
+        if (base) base = reinterpret_cast<std::remove_reference_t<decltype(base)>>(reinterpret_cast<uintptr_t>(base) + (uintptr_t)bytes);
+    };
+    const int es = r.way == kPacked ? 2 : dtype_bytes(r.type), ys = dtype_bytes(e.y_type), zs = dtype_bytes(e.z_type);
+    if (along_p) {
+        move(a.p, (r.plan.pt ? at : at * a.ldp) * es);
+        move(a.ps, at * a.ldps);
+        a.P = count;
+        a.Pl -= at;
+        if (!e.bias_on_q) move(e.bias, at * (int64_t)4);
+        move(e.residual, (int64_t)at * ys);
+        move(e.y, (int64_t)at * ys);
+        move(e.z, at * e.z_p * zs);
+    } else {
+        move(a.q, (r.plan.qt ? at : at * a.ldq) * es);
+        move(a.qs, at * a.ldqs);
+        a.Q = count;
+        a.Ql -= at;
+        if (e.bias_on_q) move(e.bias, at * (int64_t)4);
+        move(e.residual, at * e.ldr * ys);
+        move(e.y, at * e.ldy * ys);
+        move(e.z, at * e.z_q * zs);
+    }
+    return r;
+}
+
 hipError_t run_product(Product &r, void *partial, hipStream_t s, const RowSum &rows = RowSum{})
 {
+    // more tiles than one launch takes: in bands along the longer side
+    const int tile = 256 >> r.plan.tile;
+    const int64_t tiles_p = (r.a.P + tile - 1) / tile, tiles_q = (r.a.Q + tile - 1) / tile;
+    if (tiles_p * tiles_q > gemm::kMaxTiles) {
+        const bool along_p = tiles_p > tiles_q;
+        const int64_t whole = along_p ? r.a.P : r.a.Q, band = gemm::kMaxTiles / (along_p ? tiles_q : tiles_p) * tile;
+        for (int64_t at = 0; at < whole; at += band) {
+            Product part = band_of(r, along_p, (int)at, (int)(band < whole - at ? band : whole - at));
+            const hipError_t err = run_product(part, partial, s, at == 0 ? rows : RowSum{});
+            if (err != hipSuccess) return err;
+        }
+        return hipSuccess;
+    }
     r.e.partial = r.plan.splits > 1 ? static_cast<float *>(partial) : nullptr;
     hipError_t err;
     if (r.type == GS_DTYPE_MXFP8 && r.way == kDirect) err = launch_product_mx8(r.a, r.e, r.plan, s);
@@ -651,7 +696,7 @@ gs_status linear_bwd_ok(const gs_linear *l, const gs_linear_grads *g)
 
 __global__ __launch_bounds__(kThreads) void zero_rows(void *p, int type, int64_t ld, int rows, int cols)
 {
-    const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    const int64_t id = block_of() * kThreads + threadIdx.x;
     if (id >= (int64_t)rows * cols) return;
     store_from_float(p, type, id / cols * ld + id % cols, 0.0f);
 }
@@ -662,7 +707,7 @@ hipError_t run_bwd(const gs_linear &l, const gs_linear_grads &g, BwdPlan &b, cha
     if (l.m == 0) {                             // sums over no rows
         if (g.dw && !g.accumulate) {
             const int64_t blocks = ((int64_t)l.n * l.k + kThreads - 1) / kThreads;
-            zero_rows<<<(unsigned)blocks, kThreads, 0, s>>>(g.dw, g.dw_dtype, g.dw_stride, l.n, l.k);
+            zero_rows<<<grid_of(blocks, kThreads), kThreads, 0, s>>>(g.dw, g.dw_dtype, g.dw_stride, l.n, l.k);
             if ((err = hipGetLastError()) != hipSuccess) return err;
         }
         if (g.db && !g.accumulate) {

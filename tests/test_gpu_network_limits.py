@@ -59,3 +59,39 @@ def test_quantise_of_more_rows_than_a_launch_has_threads():
     # 256 = 2 x 2^7 = 1 x 2^8
     ok = _all(codes.view(torch.uint8) == 0x78), _all(scales[::2] == 127 - 7), _all(scales[1::2] == 127 - 8)
     assert all(ok), ok
+
+
+@pytest.mark.parametrize("planes", [False, True])
+@pytest.mark.parametrize("t", [torch.bfloat16, torch.float32])
+def test_linear_of_more_tiles_than_a_launch_takes(t, planes):
+    """2^30 rows in tiles of 64 by 256 threads or of 128 by 512 are 2^32
+    threads.  Small whole numbers, so every result is exact."""
+    m = 1 << 30
+    say(f"[gpu] linear {m} x 1 x 1 {t} planes={planes}")
+    x = torch.arange(m, dtype=torch.int32, device="cuda").remainder_(63).to(t).view(m, 1)
+    xs = x.view(1, m) if planes else x
+    w, b, y, z = torch.full((1, 1), 2.0, dtype=t, device="cuda"), torch.ones(1, device="cuda"), torch.zeros_like(xs), torch.zeros_like(x)
+    lin = B.linear_struct(x, w, y, bias=b, residual=xs, z=z, planes=planes)
+    _call(lambda: B.linear_fwd(lin, _ws(B.linear_fwd_workspace_bytes(lin))))
+    z -= 1
+    y -= 1
+    ok = _all(z == 2 * x), _all(y == 3 * xs)
+    assert all(ok), ok
+    lin = B.linear_struct(x, w, None, planes=planes)
+    gr = B.linear_grads_struct(lin, xs, dx=z)
+    z.zero_()
+    _call(lambda: B.linear_bwd(lin, gr, _ws(B.linear_bwd_workspace_bytes(lin, gr))))
+    ok = _all(z == 2 * x)
+    assert ok, "dx"
+
+
+def test_linear_backward_of_no_rows_into_a_large_dw():
+    n = 1 << 16
+    say(f"[gpu] dw of {n} x {n} over no rows")
+    x, dy = torch.zeros(0, n, dtype=torch.bfloat16, device="cuda"), torch.zeros(0, n, dtype=torch.bfloat16, device="cuda")
+    dw = torch.ones(n, n, dtype=torch.bfloat16, device="cuda")
+    lin = B.linear_struct(x, dw, None)
+    gr = B.linear_grads_struct(lin, dy, dw=dw)
+    _call(lambda: B.linear_bwd(lin, gr))
+    ok = not bool(dw.any())
+    assert ok, "dw"
