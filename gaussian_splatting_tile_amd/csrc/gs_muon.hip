@@ -14,10 +14,11 @@
 // A matrix that fits the LDS of a CU is iterated by one workgroup from its
 // gradient to its weight.
 //
-// 4096 x 1024 in bf16, 5 iterations: 353 us, each A 20 us and its splits' sum 6, B 11
-// and X' 30 (860 TFLOP/s of the three limb products), momentum, norm and first
-// limbs 24.  8 x 256 x 256 in fp32: 110 us, 17 launches of 5 to 7 us; the products are
-// bound by their starts and ends, which 32 x 32 tiles on more CUs shorten.
+// 4096 x 1024 in bf16, 5 iterations: 352 us (up to 364 with the card's clock; fp16 353, fp32
+// 535), each A 20 us and its splits' sum 6, B 11 and X' 30 (860 TFLOP/s of the three
+// limb products), momentum, norm and first limbs 24.  8 x 256 x 256 in fp32: 106 us (bf16
+// 95), 17 launches of 5 to 7 us; the products are bound by their starts and ends, which
+// 32 x 32 tiles on more CUs shorten.
 #include <string.h>
 
 #include "gs_gemm.h"

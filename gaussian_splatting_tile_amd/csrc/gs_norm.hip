@@ -10,9 +10,10 @@
 // 4 neighbouring lanes.  Backward: as few elements per lane as cover the row, 8
 // or (512 < n <= 1024) 16, as it also holds the next row and its columns' sums.
 //
-// bf16 with a residual: 16384 x 1024 in 28 us (134 MB, 4.8 TB/s), 100000 x 2048
-// to 8 bits in 269 us (1.44 GB, 5.4 TB/s), the backward of 16384 x 1024 in 33 us
-// (4.1 TB/s, 3 us of them the sum of the partial dgammas).
+// bf16 with a residual: 16384 x 1024 in 27.4 us (134 MB, 4.9 TB/s; fp32 53.7), 100000 x
+// 2048 to 8 bits in 264 us (1.44 GB, 5.4 TB/s), the backward of 16384 x 1024 in 33 us
+// (4.1 TB/s, 4 us of them the sum of the partial dgammas; fp32 65).  Quantisation
+// alone: bf16 65536 x 2048 in 76.5 us (5.3 TB/s).
 #include "gs_linear.h"
 
 #include <math.h>
@@ -26,11 +27,6 @@ constexpr int kMaxRegRow = 8192;
 bool aligned_to(const void *p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
 bool float_type(int t) { return t == GS_DTYPE_F32 || t == GS_DTYPE_F16 || t == GS_DTYPE_BF16; }
 gs_status from_hip(hipError_t e) { return e == hipSuccess ? GS_OK : GS_ERR_HIP; }
-
-template <typename T> constexpr int type_of();
-template <> constexpr int type_of<float>() { return GS_DTYPE_F32; }
-template <> constexpr int type_of<_Float16>() { return GS_DTYPE_F16; }
-template <> constexpr int type_of<__bf16>() { return GS_DTYPE_BF16; }
 
 template <typename T> __device__ __forceinline__ void load_chunk(const T *p, int64_t i, int valid, float v[8])
 {

@@ -595,7 +595,8 @@ size_t gs_active_mask_static_scratch_bytes(void);
  * parameter, the [rows][n] layout of gs_gaussians and gs_grads; their
  * gradients; the weights' orthogonalised momentum step; and an 8-bit form
  * for serving.  All matrices are row-major device memory with a row stride in
- * elements; every product and sum is accumulated in fp32. */
+ * elements.  Products and sums are accumulated in fp32, but for the sums of the
+ * 8-bit matrix instruction (see gs_linear) and the update's norm in fp64. */
 
 /* Element types.  GS_DTYPE_MXFP8 is a block format: e4m3 values (largest 448)
  * with one e8m0 scale 2^(s-127) per 32 consecutive values of a row, held in a
@@ -612,7 +613,9 @@ typedef enum gs_activation { GS_ACT_NONE = 0, GS_ACT_RELU = 1, GS_ACT_SILU = 2, 
 /* Root-mean-square norm of the rows of x + residual:
  *     s = x + residual,  rstd = (mean_j s_j^2 + eps)^(-1/2),  y_j = s_j rstd gamma_j
  * in fp32 from the unrounded s; sum receives s rounded to `dtype`.  A row of
- * zeros gives zeros.  y may be x or residual, sum may be x or residual
+ * zeros gives zeros with eps > 0 and NaN with eps = 0 (0 / 0); a row with an
+ * infinity gives zeros around it and NaN in its place, one whose squares pass
+ * fp32's range zeros.  y may be x or residual, sum may be x or residual
  * (each element is read before it is written) with the same stride, unless
  * y is 8-bit.  Strides are in elements (of the scales: bytes). */
 typedef struct gs_rms_norm {
@@ -666,7 +669,8 @@ typedef struct gs_rms_norm_grads {
     int32_t accumulate;         /* nonzero: dgamma += (else dgamma =)          */
 } gs_rms_norm_grads;
 
-/* Workspace of gs_rms_norm_bwd, in bytes (0 without dgamma). */
+/* Workspace of a gs_rms_norm_bwd with dgamma, in bytes; a call without dgamma
+ * needs none. */
 size_t gs_rms_norm_bwd_workspace_bytes(int64_t m, int32_t n);
 
 /* Errors: as gs_rms_norm_fwd; GS_ERR_WORKSPACE. */
@@ -719,15 +723,17 @@ size_t gs_linear_fwd_workspace_bytes(const gs_linear *linear /* host */);
 
 /* Errors: GS_ERR_INVALID_ARG (NULL descriptor or arrays with m > 0, sizes or
  * strides out of range, an unknown type or activation, a misaligned pointer),
- * GS_ERR_UNSUPPORTED (MXFP8 with z kept, or k no multiple of 32; an 8-bit y),
- * GS_ERR_WORKSPACE. */
+ * GS_ERR_UNSUPPORTED (MXFP8 with z kept, or k no multiple of 32; an 8-bit y;
+ * 2^31 or more 64 x 64 tiles of y), GS_ERR_WORKSPACE. */
 gs_status gs_linear_fwd(const gs_linear *linear /* host */, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Gradients of the linear layer, for the gradient dy of y (y's layout and
  * y_dtype).  With an activation z must be the one the forward kept:
  *     dz = dy act'(z),  dx = dz w,  dw (+)= dz^T x,  db (+)= sum over rows of dz
  * (the residual's gradient is dy itself).  For 16-bit operands dz is rounded
- * to `dtype` for the two products; db sums it unrounded.  NULL outputs are
+ * to `dtype` for the two products (a relative error of half an ulp each, of the
+ * size that dx's own rounding has); db sums it unrounded.  fp32 operands keep
+ * it whole.  NULL outputs are
  * not computed.  Sums over rows are reduced in a fixed order.  The outputs
  * must not overlap the inputs. */
 typedef struct gs_linear_grads {
