@@ -121,6 +121,22 @@ class GsMuon(C.Structure):
     device = None              # of the tensors (muon_struct)
 
 
+def _tensor_fields(name):
+    return [(name, C.c_void_p)] + [(f"{name}_{dim}", C.c_int64) for dim in ("batch", "row", "head")]
+
+
+class GsAttention(C.Structure):
+    _fields_ = [("batch", C.c_int32), ("heads", C.c_int32), ("kv_heads", C.c_int32), ("nq", C.c_int32), ("nk", C.c_int32),
+                ("d", C.c_int32), ("dtype", C.c_int32), ("scale", C.c_float), *_tensor_fields("q"), *_tensor_fields("k"),
+                *_tensor_fields("v"), *_tensor_fields("out"), ("lse", C.c_void_p), ("kv_lengths", C.c_void_p),
+                ("kv_mask", C.c_void_p), ("kv_mask_stride", C.c_int64)]
+    device = None              # of the tensors (attention_struct)
+
+
+class GsAttentionGrads(C.Structure):
+    _fields_ = [*_tensor_fields("dout"), *_tensor_fields("dq"), *_tensor_fields("dk"), *_tensor_fields("dv")]
+
+
 class GsError(RuntimeError):
     pass
 
@@ -136,7 +152,8 @@ SYMBOLS = ("gs_project", "gs_bin_sort_workspace_bytes", "gs_schedule_words", "gs
            "gs_sh_q8_bounds_floats", "gs_sh_quantize8", "gs_sh_adam_step", "gs_rms_norm_fwd",
            "gs_rms_norm_bwd_workspace_bytes", "gs_rms_norm_bwd", "gs_mxfp8_quantize", "gs_linear_fwd_workspace_bytes",
            "gs_linear_fwd", "gs_linear_bwd_workspace_bytes", "gs_linear_bwd", "gs_muon_workspace_bytes",
-           "gs_orthogonalize", "gs_muon_step", "gs_status_string",
+           "gs_orthogonalize", "gs_muon_step", "gs_attention_fwd_workspace_bytes", "gs_attention_fwd",
+           "gs_attention_bwd_workspace_bytes", "gs_attention_bwd", "gs_status_string",
            "gs_version")
 
 
@@ -208,6 +225,12 @@ def lib():
     L.gs_muon_workspace_bytes.restype = sz
     L.gs_orthogonalize.argtypes = [C.POINTER(GsMuon), vp, sz, vp]
     L.gs_muon_step.argtypes = [C.POINTER(GsMuon), vp, sz, vp]
+    L.gs_attention_fwd_workspace_bytes.argtypes = [C.POINTER(GsAttention)]
+    L.gs_attention_fwd_workspace_bytes.restype = sz
+    L.gs_attention_fwd.argtypes = [C.POINTER(GsAttention), vp, sz, vp]
+    L.gs_attention_bwd_workspace_bytes.argtypes = [C.POINTER(GsAttention), C.POINTER(GsAttentionGrads)]
+    L.gs_attention_bwd_workspace_bytes.restype = sz
+    L.gs_attention_bwd.argtypes = [C.POINTER(GsAttention), C.POINTER(GsAttentionGrads), vp, sz, vp]
     L.gs_status_string.restype = C.c_char_p
     L.gs_status_string.argtypes = [C.c_int]
     L.gs_version.restype = C.c_int32
@@ -217,7 +240,7 @@ def lib():
                  "gs_render_bwd_screen", "gs_render_bwd_screen_views",
                  "gs_project_bwd", "gs_project_bwd_binned", "gs_active_mask", "gs_active_mask_static",
                  "gs_sh_quantize8", "gs_rms_norm_fwd", "gs_rms_norm_bwd", "gs_mxfp8_quantize", "gs_linear_fwd",
-                 "gs_linear_bwd", "gs_orthogonalize", "gs_muon_step"):
+                 "gs_linear_bwd", "gs_orthogonalize", "gs_muon_step", "gs_attention_fwd", "gs_attention_bwd"):
         getattr(L, name).restype = C.c_int
     _lib = L
     return L
@@ -762,6 +785,85 @@ def muon_step(a: GsMuon, workspace: torch.Tensor, stream=None):
     """gs_muon_step: momentum, orthogonalised update and weight decay."""
     _check(lib().gs_muon_step(C.byref(a), _ptr(workspace), _nbytes(workspace), _stream_for(a.device, workspace, stream)),
            "gs_muon_step")
+
+
+# ---- tokens that read an encoder's states ----------------------------------
+def _heads(t: Optional[torch.Tensor], shape, what: str, like: Optional[torch.Tensor] = None):
+    """(address, strides of batch, row and head) of a [batch][rows][heads][d]
+    tensor whose d is contiguous."""
+    if t is None:
+        return None, 0, 0, 0
+    if t.shape != shape:
+        raise ValueError(f"{what}: expected {list(shape)}, got {list(t.shape)}")
+    if like is not None and (t.dtype is not like.dtype or t.device != like.device):
+        raise ValueError(f"{what}: expected {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
+    sb, sr, sh, sd = t.stride()
+    if sd != 1 and shape[3] > 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous (strides {t.stride()})")
+    return t.data_ptr(), sb, sr, sh
+
+
+def attention_struct(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                     lse: Optional[torch.Tensor] = None, kv_lengths: Optional[torch.Tensor] = None,
+                     kv_mask: Optional[torch.Tensor] = None, scale: Optional[float] = None) -> GsAttention:
+    """Descriptor of cross attention: q and out [batch][nq][heads][d], k and v
+    [batch][nk][kv_heads][d] of one type (float32, float16 or bfloat16; views of
+    any strides but for d), lse [batch][heads][nq] float32 for the backward,
+    kv_lengths [batch] int32, kv_mask [batch][nk] uint8 or bool (0: not
+    attended), scale d^-1/2 unless given."""
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q, k: expected [batch][rows][heads][d]")
+    (b, nq, h, d), (_, nk, kv, _) = q.shape, k.shape
+    _int32(b, nq, h, d, nk, kv)
+    dev, states = q.device, (b, nk, kv, d)
+    if kv_lengths is not None and (kv_lengths.dtype is not torch.int32 or kv_lengths.shape != (b,) or not kv_lengths.is_contiguous()
+                                   or kv_lengths.device != dev):
+        raise ValueError(f"kv_lengths: expected {b} contiguous int32 values on the others' device")
+    mask, stride = None, 0
+    if kv_mask is not None:
+        if kv_mask.dtype not in (torch.uint8, torch.bool) or kv_mask.shape != (b, nk) or kv_mask.device != dev or (nk > 1 and kv_mask.stride(1) != 1):
+            raise ValueError(f"kv_mask: expected uint8 or bool [{b}][{nk}] with contiguous rows on the others' device")
+        mask, stride = kv_mask.data_ptr(), kv_mask.stride(0)
+    if lse is not None and lse.shape != (b, h, nq):
+        raise ValueError(f"lse: expected [{b}][{h}][{nq}], got {list(lse.shape)}")
+    a = GsAttention(b, h, kv, nq, nk, d, _dtype(q), d ** -0.5 if scale is None else scale, *_heads(q, q.shape, "q"),
+                    *_heads(k, states, "k", q), *_heads(v, states, "v", q), *_heads(out, q.shape, "out", q),
+                    _vector(lse, b * h * nq, "lse", dev), None if kv_lengths is None else kv_lengths.data_ptr(), mask, stride)
+    a.device = dev
+    return a
+
+
+def attention_fwd_workspace_bytes(a: GsAttention) -> int:
+    return int(lib().gs_attention_fwd_workspace_bytes(C.byref(a)))
+
+
+def attention_fwd(a: GsAttention, workspace: Optional[torch.Tensor] = None, stream=None):
+    """gs_attention_fwd of an attention_struct; the tensors it was made from
+    must be alive."""
+    _check(lib().gs_attention_fwd(C.byref(a), _ptr(workspace), _nbytes(workspace), _stream_for(a.device, workspace, stream)),
+           "gs_attention_fwd")
+
+
+def attention_grads_struct(a: GsAttention, dout: torch.Tensor, dq: Optional[torch.Tensor] = None,
+                           dk: Optional[torch.Tensor] = None, dv: Optional[torch.Tensor] = None) -> GsAttentionGrads:
+    """Descriptor of the gradients of an attention_struct (whose out and lse the
+    forward has written): dout of out's shape and type, and any of dq, dk, dv of
+    q's, k's and v's shapes and type."""
+    if dout.dtype is not _BY_CODE[a.dtype] or (a.device is not None and dout.device != a.device):
+        raise ValueError(f"dout: expected {_BY_CODE[a.dtype]} on {a.device}, got {dout.dtype} on {dout.device}")
+    rows, states = (a.batch, a.nq, a.heads, a.d), (a.batch, a.nk, a.kv_heads, a.d)
+    return GsAttentionGrads(*_heads(dout, rows, "dout"), *_heads(dq, rows, "dq", dout), *_heads(dk, states, "dk", dout),
+                            *_heads(dv, states, "dv", dout))
+
+
+def attention_bwd_workspace_bytes(a: GsAttention, g: GsAttentionGrads) -> int:
+    return int(lib().gs_attention_bwd_workspace_bytes(C.byref(a), C.byref(g)))
+
+
+def attention_bwd(a: GsAttention, g: GsAttentionGrads, workspace: Optional[torch.Tensor] = None, stream=None):
+    """gs_attention_bwd of an attention_struct and its attention_grads_struct."""
+    _check(lib().gs_attention_bwd(C.byref(a), C.byref(g), _ptr(workspace), _nbytes(workspace),
+                                  _stream_for(a.device, workspace, stream)), "gs_attention_bwd")
 
 
 # ---- buffers for one view ---------------------------------------------------

@@ -22,13 +22,17 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgs_hip.so")
 SOURCES = ["gs_api.hip", "gs_project.hip", "gs_sort.hip", "gs_render.hip", "gs_mask.hip", "gs_adam.hip",
            "gs_norm.hip", "gs_linear.hip", "gs_product_bf16.hip", "gs_product_f16.hip", "gs_product_f32.hip",
-           "gs_product_mx8.hip", "gs_product_few.hip", "gs_muon.hip"]
+           "gs_product_mx8.hip", "gs_product_few.hip", "gs_muon.hip", "gs_attention.hip",
+           "gs_attention_fwd_bf16.hip", "gs_attention_fwd_f16.hip", "gs_attention_fwd_f32.hip",
+           "gs_attention_dq_bf16.hip", "gs_attention_dq_f16.hip", "gs_attention_dq_f32.hip",
+           "gs_attention_dkv_bf16.hip", "gs_attention_dkv_f16.hip", "gs_attention_dkv_f32.hip"]
 # the peak-rate microbenchmarks the roofline fractions are also taken against
 # (not part of the rasterizer's ABI)
 PEAKS_LIB = os.path.join(PKG, "libgs_peaks.so")
 PEAKS_SOURCES = ["peaks.hip"]
 HEADERS = [os.path.join(CSRC, h) for h in ("gs_internal.h", "gs_adam.h", "gs_numeric.h", "gs_gemm.h", "gs_linear.h",
-                                           "gs_product_16.h")] + [os.path.join(INCLUDE, "gs.h")]
+                                           "gs_product_16.h", "gs_attention.h", "gs_attention_fwd.h",
+                                           "gs_attention_bwd.h")] + [os.path.join(INCLUDE, "gs.h")]
 ARCH = os.environ.get("GS_OFFLOAD_ARCH", "gfx950")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

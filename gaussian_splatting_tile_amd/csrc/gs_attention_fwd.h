@@ -1,0 +1,145 @@
+// The forward's kernel, instantiated once per kind of operand.
+#pragma once
+
+#include "gs_attention.h"
+
+namespace gsi {
+namespace attn {
+
+// Online softmax over tiles of keys.  A column's scores are the lane's and its
+// partner's registers; the maximum that is subtracted follows the true one only
+// when that has grown by more than 2^8 (a column's probabilities stay below 2^8,
+// which every type holds, and the sums fp32), so that the sums are rescaled a
+// few times a call and not once a tile.  Probabilities are rounded to the
+// operands' type for the second product (half an ulp each, unbiased); their sum
+// takes them unrounded.
+template <int KIND, int NL, int DP, int NW> __global__ __launch_bounds__(NW * 64, room_for(NL, NW)) void attention_fwd(Args a)
+{
+    constexpr int KT = kTileRows<NL, DP>, KS = KT / 32;
+    using LD = Loader<DP, KT, NW * 64>;
+    constexpr int kStage = 2 * NL * LD::kBytes;
+    __shared__ __align__(128) char lds[2 * kStage];
+
+    Item it;
+    if (!item_of(a, it)) return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int length = length_of(a, it.batch);
+    // this split's tiles
+    const int tiles = (length + KT - 1) / KT, per = (tiles + a.splits - 1) / a.splits;
+    const int t0 = it.split * per, t1 = min(tiles, t0 + per);
+
+    const int row = (it.tile * NW + wave) * 32 + (lane & 31);
+    const bool there = row < a.rows;
+    const int token = there ? row / a.group : 0, head = it.head * a.group + (there ? row - token * a.group : 0);
+    i4 q[NL][DP / 16];
+    load_columns<KIND, NL, DP / 16>(static_cast<const char *>(a.q.p) +
+                                        (it.batch * a.q.sb + token * a.q.sr + head * a.q.sh) * (NL > 1 ? 4 : 2),
+                                    there, a.d, lane, q);
+
+    LD lk, lv;
+    lk.init(a.k.sr, a.d, tid);
+    lv.init(a.v.sr, a.d, tid);
+    const char *kb = a.k.p + it.batch * a.k.sb + it.head * a.k.sh, *vb = a.v.p + it.batch * a.v.sb + it.head * a.v.sh;
+    auto issue = [&](int t, uint64_t seen) {
+        char *s = lds + (t & 1) * kStage;
+#pragma unroll
+        for (int l = 0; l < NL; l++) {
+            lk.issue(kb + l * a.k.plane + (int64_t)t * KT * a.k.sr, s + l * LD::kBytes, seen, wave);
+            lv.issue(vb + l * a.v.plane + (int64_t)t * KT * a.v.sr, s + (NL + l) * LD::kBytes, seen, wave);
+        }
+    };
+    const uint64_t whole = KT == 64 ? ~0ull : 0xFFFFFFFFull;
+    auto byte_of = [&](int t) { return t < t1 ? mask_byte(a, it.batch, (int64_t)t * KT + lane, length) : 0u; };
+    auto seen_in = [&](int t, uint32_t byte) { return t < t1 ? attended(t * KT, length, byte, lane) & whole : 0ull; };
+
+    f16v o[DP / 32];
+#pragma unroll
+    for (int t = 0; t < DP / 32; t++) o[t] = zeros();
+    float m = -INFINITY, base = 0.0f, sum = 0.0f;          // base: m, or 0 before there is one
+    uint64_t seen = seen_in(t0, byte_of(t0)), next = 0;
+    uint32_t byte = byte_of(t0 + 1);
+    if (t0 < t1) issue(t0, seen);
+    for (int t = t0; t < t1; t++, seen = next) {
+        gemm::stage_barrier<0>();
+        next = seen_in(t + 1, byte);
+        byte = byte_of(t + 2);
+        if (t + 1 < t1) issue(t + 1, next);
+        if (!seen) continue;
+        const char *kt = lds + (t & 1) * kStage, *vt = kt + NL * LD::kBytes;
+        f16v s[KS];
+        float top = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < KS; u++) {
+            s[u] = over_d<KIND, NL, DP, LD::kBytes>(kt, u * 32, q, lane);
+            if (seen != whole) {
+                const uint32_t bits = (uint32_t)(seen >> (u * 32)) >> (4 * (lane >> 5));
+#pragma unroll
+                for (int i = 0; i < 16; i++)
+                    if (!((bits >> ((i & 3) + 8 * (i >> 2))) & 1)) s[u][i] = -INFINITY;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; i++) top = fmaxf(top, s[u][i]);
+        }
+        top *= a.c;
+        if (__any(top > m + 8.0f)) {
+            const float up = fmaxf(m, pair_max(top)), now = up == -INFINITY ? 0.0f : up;
+            const float f = __builtin_amdgcn_exp2f(m - now);
+            m = up;
+            base = now;
+            sum *= f;
+#pragma unroll
+            for (int t = 0; t < DP / 32; t++) o[t] *= f;
+        }
+#pragma unroll
+        for (int u = 0; u < KS; u++) {
+            i4 w[2][NL];
+#pragma unroll
+            for (int i = 0; i < 16; i++) {
+                s[u][i] = __builtin_amdgcn_exp2f(fmaf(s[u][i], a.c, -base));
+                sum += s[u][i];
+            }
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 8; i++) v[i] = s[u][j * 8 + i];
+                pack8<KIND, NL>(v, w[j]);
+            }
+            over_rows<KIND, NL, DP, LD::kBytes>(vt, u * 32, w, o, lane);
+        }
+    }
+
+    sum = pair_sum(sum);
+    if (!there) return;
+    const int64_t at = ((int64_t)it.batch * a.heads + head) * a.nq + token;
+    if (a.splits > 1) {                         // sums as they are, for join_fwd
+        const int64_t p = (int64_t)it.split * a.batch * a.heads * a.nq + at;
+        store_columns<DP>(a.part, GS_DTYPE_F32, p * a.d, o, 1.0f, a.d, lane);
+        if (lane < 32) {
+            a.ml[2 * p] = m;
+            a.ml[2 * p + 1] = sum;
+        }
+        return;
+    }
+    const float f = m == -INFINITY && sum == 0.0f ? 0.0f : 1.0f / sum;
+    store_columns<DP>(const_cast<void *>(a.out.p), a.type, it.batch * a.out.sb + token * a.out.sr + head * a.out.sh, o, f, a.d, lane);
+    if (a.lse && lane < 32) a.lse[at] = (m + log2f(sum)) * kLn2;
+}
+
+template <int KIND, int NL, int DP> hipError_t launch_fwd_waves(const Args &a, int waves, hipStream_t s)
+{
+    const dim3 grid = grid_of(a.blocks, waves * 64);
+    if (waves == 1) attention_fwd<KIND, NL, DP, 1><<<grid, 64, 0, s>>>(a);
+    else attention_fwd<KIND, NL, DP, 4><<<grid, 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+template <int KIND, int NL> hipError_t launch_fwd_kind(const Args &a, int waves, hipStream_t s)
+{
+    if (a.d <= 32) return launch_fwd_waves<KIND, NL, 32>(a, waves, s);
+    if (a.d <= 64) return launch_fwd_waves<KIND, NL, 64>(a, waves, s);
+    if (a.d <= 96) return launch_fwd_waves<KIND, NL, 96>(a, waves, s);
+    return launch_fwd_waves<KIND, NL, 128>(a, waves, s);
+}
+
+}  // namespace attn
+}  // namespace gsi

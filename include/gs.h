@@ -799,6 +799,80 @@ size_t gs_muon_workspace_bytes(const gs_muon *muon /* host */);
 gs_status gs_orthogonalize(const gs_muon *muon /* host */, void *workspace, size_t workspace_bytes, void *stream);
 gs_status gs_muon_step(const gs_muon *muon /* host */, void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---------------------------------------------------------------------- */
+/* How such a network's tokens get their content: the feature maps of the
+ * input views pass group norms, and the scene's tokens read the views' states
+ * by cross attention (the GlobalSplat page, steps (2) and (3) of its
+ * pipeline: an encoder of views and global scene tokens). */
+
+/* Cross attention of nq queries to nk states of another length:
+ *     S_ij = scale q_i . k_j,  P = softmax over the attended j,  out_i = sum_j P_ij v_j
+ *     lse_i = log sum_j exp(S_ij)
+ * Tensors are [batch][rows][heads][d] of one type with strides in elements for
+ * batch, row and head (any, 0 included for inputs; d contiguous); query head
+ * h reads k and v of head h / (heads / kv_heads).  State j of batch element b is
+ * attended if j < kv_lengths[b] (taken as within 0 .. nk) and kv_mask[b][j] != 0; what
+ * the others hold, infinities and NaN included, has no effect.  A row with no
+ * attended state gets out = 0 and lse = -infinity.
+ * Scores, maxima and sums are fp32; for 16-bit types exp(S_ij - maximum) is
+ * rounded to the type for its product with v (a relative error of half an ulp each).
+ * fp32 operands are multiplied as three bf16 limbs (see gs_linear). */
+typedef struct gs_attention {
+    int32_t batch;              /* 0 .. 65535                                  */
+    int32_t heads, kv_heads;    /* 1 .. 65535; kv_heads divides heads          */
+    int32_t nq, nk;             /* 0 .. 2^30; nq heads / kv_heads <= 2^30      */
+    int32_t d;                  /* 1 .. 128                                    */
+    int32_t dtype;              /* of q, k, v, out: F32, F16 or BF16           */
+    float scale;                /* > 0, finite                                 */
+    const void *q;              /* [batch][nq][heads][d]                       */
+    int64_t q_batch, q_row, q_head;
+    const void *k;              /* [batch][nk][kv_heads][d]                    */
+    int64_t k_batch, k_row, k_head;
+    const void *v;              /* [batch][nk][kv_heads][d]                    */
+    int64_t v_batch, v_row, v_head;
+    void *out;                  /* [batch][nq][heads][d], overlapping no input */
+    int64_t out_batch, out_row, out_head;
+    float *lse;                 /* [batch][heads][nq] or NULL: not kept        */
+    const int32_t *kv_lengths;  /* [batch] or NULL: nk                         */
+    const uint8_t *kv_mask;     /* [batch][nk] or NULL: ones                   */
+    int64_t kv_mask_stride;     /* bytes between batch elements                */
+} gs_attention;
+
+/* Workspace of gs_attention_fwd, in bytes. */
+size_t gs_attention_fwd_workspace_bytes(const gs_attention *attention /* host */);
+
+/* Errors: GS_ERR_INVALID_ARG (NULL descriptor or arrays with rows, sizes or
+ * strides out of range, an unknown type, a misaligned pointer, elements of out
+ * that share a place), GS_ERR_UNSUPPORTED (d above 128; batch heads max(nq, nk)
+ * above 2^40), GS_ERR_WORKSPACE. */
+gs_status gs_attention_fwd(const gs_attention *attention /* host */, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Gradients of gs_attention_fwd from its inputs, the out and lse that it kept
+ * and the gradient dout of out:
+ *     P_ij = exp(S_ij - lse_i),  delta_i = dout_i . out_i,  dS_ij = P_ij (dout_i . v_j - delta_i)
+ *     dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,  dv_j = sum_i P_ij dout_i
+ * dk and dv are sums over the heads that share k and v, and 0 for states that are
+ * not attended.  For 16-bit types P and dS are rounded to the type for the last
+ * products (fp16 ones times powers of two, so that small ones keep their bits).
+ * Sums are taken in a fixed order.  The outputs must not overlap the inputs. */
+typedef struct gs_attention_grads {
+    const void *dout;           /* [batch][nq][heads][d] of `dtype`, as all    */
+    int64_t dout_batch, dout_row, dout_head;
+    void *dq;                   /* [batch][nq][heads][d], or NULL: not wanted  */
+    int64_t dq_batch, dq_row, dq_head;
+    void *dk;                   /* [batch][nk][kv_heads][d], or NULL           */
+    int64_t dk_batch, dk_row, dk_head;
+    void *dv;                   /* [batch][nk][kv_heads][d], or NULL           */
+    int64_t dv_batch, dv_row, dv_head;
+} gs_attention_grads;
+
+/* Workspace of gs_attention_bwd, in bytes. */
+size_t gs_attention_bwd_workspace_bytes(const gs_attention *attention /* host */, const gs_attention_grads *grads /* host */);
+
+/* Errors: as gs_attention_fwd; GS_ERR_INVALID_ARG for a missing lse or dout. */
+gs_status gs_attention_bwd(const gs_attention *attention /* host */, const gs_attention_grads *grads /* host */, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
 /* Static description of a status code. */
 const char *gs_status_string(gs_status status);
 
