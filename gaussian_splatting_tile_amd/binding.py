@@ -137,6 +137,25 @@ class GsAttentionGrads(C.Structure):
     _fields_ = [*_tensor_fields("dout"), *_tensor_fields("dq"), *_tensor_fields("dk"), *_tensor_fields("dv")]
 
 
+class GsGroupNorm(C.Structure):
+    _fields_ = [("n", C.c_int32), ("c", C.c_int32), ("groups", C.c_int32), ("dtype", C.c_int32), ("activation", C.c_int32),
+                ("eps", C.c_float), ("p", C.c_int64), ("x", C.c_void_p), ("x_image", C.c_int64), ("x_pixel", C.c_int64),
+                ("gamma", C.c_void_p), ("beta", C.c_void_p), ("y", C.c_void_p), ("y_image", C.c_int64),
+                ("y_pixel", C.c_int64), ("mean", C.c_void_p), ("rstd", C.c_void_p), ("kept", C.c_void_p),
+                ("kept_image", C.c_int64), ("kept_pixel", C.c_int64), ("kept_scales", C.c_void_p),
+                ("kept_scales_image", C.c_int64), ("kept_scales_pixel", C.c_int64)]
+
+
+class GsGroupNormGrads(C.Structure):
+    _fields_ = [("n", C.c_int32), ("c", C.c_int32), ("groups", C.c_int32), ("dtype", C.c_int32), ("x_dtype", C.c_int32),
+                ("activation", C.c_int32), ("accumulate", C.c_int32), ("p", C.c_int64), ("x", C.c_void_p),
+                ("x_image", C.c_int64), ("x_pixel", C.c_int64), ("x_scales", C.c_void_p), ("x_scales_image", C.c_int64),
+                ("x_scales_pixel", C.c_int64), ("mean", C.c_void_p), ("rstd", C.c_void_p), ("gamma", C.c_void_p),
+                ("beta", C.c_void_p), ("dy", C.c_void_p), ("dy_image", C.c_int64), ("dy_pixel", C.c_int64),
+                ("dx", C.c_void_p), ("dx_image", C.c_int64), ("dx_pixel", C.c_int64), ("dgamma", C.c_void_p),
+                ("dbeta", C.c_void_p)]
+
+
 class GsError(RuntimeError):
     pass
 
@@ -153,7 +172,8 @@ SYMBOLS = ("gs_project", "gs_bin_sort_workspace_bytes", "gs_schedule_words", "gs
            "gs_rms_norm_bwd_workspace_bytes", "gs_rms_norm_bwd", "gs_mxfp8_quantize", "gs_linear_fwd_workspace_bytes",
            "gs_linear_fwd", "gs_linear_bwd_workspace_bytes", "gs_linear_bwd", "gs_muon_workspace_bytes",
            "gs_orthogonalize", "gs_muon_step", "gs_attention_fwd_workspace_bytes", "gs_attention_fwd",
-           "gs_attention_bwd_workspace_bytes", "gs_attention_bwd", "gs_status_string",
+           "gs_attention_bwd_workspace_bytes", "gs_attention_bwd", "gs_group_norm_fwd_workspace_bytes", "gs_group_norm_fwd",
+           "gs_group_norm_bwd_workspace_bytes", "gs_group_norm_bwd", "gs_status_string",
            "gs_version")
 
 
@@ -231,6 +251,11 @@ def lib():
     L.gs_attention_bwd_workspace_bytes.argtypes = [C.POINTER(GsAttention), C.POINTER(GsAttentionGrads)]
     L.gs_attention_bwd_workspace_bytes.restype = sz
     L.gs_attention_bwd.argtypes = [C.POINTER(GsAttention), C.POINTER(GsAttentionGrads), vp, sz, vp]
+    for name in ("gs_group_norm_fwd_workspace_bytes", "gs_group_norm_bwd_workspace_bytes"):
+        getattr(L, name).argtypes = [i64, i64, C.c_int32, C.c_int32]
+        getattr(L, name).restype = sz
+    L.gs_group_norm_fwd.argtypes = [C.POINTER(GsGroupNorm), vp, sz, vp]
+    L.gs_group_norm_bwd.argtypes = [C.POINTER(GsGroupNormGrads), vp, sz, vp]
     L.gs_status_string.restype = C.c_char_p
     L.gs_status_string.argtypes = [C.c_int]
     L.gs_version.restype = C.c_int32
@@ -240,7 +265,8 @@ def lib():
                  "gs_render_bwd_screen", "gs_render_bwd_screen_views",
                  "gs_project_bwd", "gs_project_bwd_binned", "gs_active_mask", "gs_active_mask_static",
                  "gs_sh_quantize8", "gs_rms_norm_fwd", "gs_rms_norm_bwd", "gs_mxfp8_quantize", "gs_linear_fwd",
-                 "gs_linear_bwd", "gs_orthogonalize", "gs_muon_step", "gs_attention_fwd", "gs_attention_bwd"):
+                 "gs_linear_bwd", "gs_orthogonalize", "gs_muon_step", "gs_attention_fwd", "gs_attention_bwd",
+                 "gs_group_norm_fwd", "gs_group_norm_bwd"):
         getattr(L, name).restype = C.c_int
     _lib = L
     return L
@@ -864,6 +890,81 @@ def attention_bwd(a: GsAttention, g: GsAttentionGrads, workspace: Optional[torch
     """gs_attention_bwd of an attention_struct and its attention_grads_struct."""
     _check(lib().gs_attention_bwd(C.byref(a), C.byref(g), _ptr(workspace), _nbytes(workspace),
                                   _stream_for(a.device, workspace, stream)), "gs_attention_bwd")
+
+
+def _maps(t: Optional[torch.Tensor], shape, what: str, dtypes=None, device=None):
+    """(address, strides of image and pixel) of a [n][p][c] tensor whose c is
+    contiguous."""
+    if t is None:
+        return None, 0, 0
+    if t.shape != shape:
+        raise ValueError(f"{what}: expected {list(shape)}, got {list(t.shape)}")
+    if (dtypes is not None and t.dtype not in dtypes) or (device is not None and t.device != device):
+        raise ValueError(f"{what}: unexpected {t.dtype} on {t.device}")
+    image, pixel, step = t.stride()
+    if step != 1 and shape[2] > 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous (strides {t.stride()})")
+    return t.data_ptr(), image, pixel
+
+
+def group_norm_fwd_workspace_bytes(n: int, p: int, c: int, groups: int) -> int:
+    _int32(c, groups)
+    return int(lib().gs_group_norm_fwd_workspace_bytes(n, p, c, groups))
+
+
+def group_norm_fwd(x: torch.Tensor, y: torch.Tensor, groups: int, gamma: Optional[torch.Tensor] = None,
+                   beta: Optional[torch.Tensor] = None, act: str = "none", mean: Optional[torch.Tensor] = None,
+                   rstd: Optional[torch.Tensor] = None, kept: Optional[torch.Tensor] = None,
+                   kept_scales: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                   workspace: Optional[torch.Tensor] = None, stream=None):
+    """gs_group_norm_fwd over x [n][p][c] (images, pixels, channels; float32,
+    float16 or bfloat16): y = act(gamma h + beta) of x's type.  mean and rstd
+    [n][groups] are kept for the backward, and x itself in 8-bit blocks where
+    kept [n][p][c] (float8_e4m3fn) and kept_scales [n][p][c / 32] (uint8 or
+    float8_e8m0fnu) are given."""
+    if x.dim() != 3:
+        raise ValueError("x: expected [n][p][c]")
+    n, p, c = x.shape
+    _int32(n, c, groups)
+    dev = x.device
+    a = GsGroupNorm(n, c, groups, _dtype(x), GS_ACT[act], eps, p, *_maps(x, x.shape, "x"), _vector(gamma, c, "gamma", dev),
+                    _vector(beta, c, "beta", dev), *_maps(y, x.shape, "y", (x.dtype,), dev),
+                    _vector(mean, n * groups, "mean", dev), _vector(rstd, n * groups, "rstd", dev),
+                    *_maps(kept, x.shape, "kept", (torch.float8_e4m3fn,), dev),
+                    *_maps(kept_scales, (n, p, c // 32), "kept_scales", _SCALES, dev))
+    _check(lib().gs_group_norm_fwd(C.byref(a), _ptr(workspace), _nbytes(workspace), _stream_for(dev, workspace, stream)),
+           "gs_group_norm_fwd")
+
+
+def group_norm_bwd_workspace_bytes(n: int, p: int, c: int, groups: int) -> int:
+    _int32(c, groups)
+    return int(lib().gs_group_norm_bwd_workspace_bytes(n, p, c, groups))
+
+
+def group_norm_bwd(x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor, dy: torch.Tensor, dx: torch.Tensor, groups: int,
+                   gamma: Optional[torch.Tensor] = None, beta: Optional[torch.Tensor] = None, act: str = "none",
+                   dgamma: Optional[torch.Tensor] = None, dbeta: Optional[torch.Tensor] = None,
+                   x_scales: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                   accumulate: bool = False, stream=None):
+    """gs_group_norm_bwd: from x of dy's type, or the checkpoint (kept and, as
+    x_scales, kept_scales) in its place, and the kept mean and rstd, the gradient
+    dx and, if given, dgamma and dbeta [c]; accumulate adds to these two."""
+    if dy.dim() != 3:
+        raise ValueError("dy: expected [n][p][c]")
+    n, p, c = dy.shape
+    _int32(n, c, groups)
+    dev, own = dy.device, (dy.dtype,)
+    block = x.dtype is torch.float8_e4m3fn
+    if block != (x_scales is not None):
+        raise ValueError("x_scales: expected with an 8-bit x alone")
+    a = GsGroupNormGrads(n, c, groups, _dtype(dy), _dtype(x), GS_ACT[act], 1 if accumulate else 0, p,
+                         *_maps(x, dy.shape, "x", (dy.dtype, torch.float8_e4m3fn), dev),
+                         *_maps(x_scales, (n, p, c // 32), "x_scales", _SCALES, dev), _vector(mean, n * groups, "mean", dev),
+                         _vector(rstd, n * groups, "rstd", dev), _vector(gamma, c, "gamma", dev), _vector(beta, c, "beta", dev),
+                         *_maps(dy, dy.shape, "dy"), *_maps(dx, dy.shape, "dx", own, dev), _vector(dgamma, c, "dgamma", dev),
+                         _vector(dbeta, c, "dbeta", dev))
+    _check(lib().gs_group_norm_bwd(C.byref(a), _ptr(workspace), _nbytes(workspace), _stream_for(dev, workspace, stream)),
+           "gs_group_norm_bwd")
 
 
 # ---- buffers for one view ---------------------------------------------------

@@ -1,0 +1,821 @@
+// Group norm with an activation over feature maps whose channels are
+// contiguous, its input kept in 8-bit blocks for the backward, and the backward.
+//
+// HBM-bound: the forward has to read x and write y, the backward to read x (or
+// its 8-bit checkpoint) and dy and write dx; both need sums over a whole image
+// first, so what they read is read twice, the second time out of the last-level
+// cache while it fits.  A thread keeps eight consecutive channels (16 bytes of a
+// 16-bit type) and walks over pixels, so that statistics, gamma and beta stay in
+// registers and any group size costs the same.  Images of up to 64K values are
+// one workgroup's, in one launch; larger ones take three: sums of blocks of
+// pixels, joined per group, then the results.
+//
+// A channel's sums are of differences from a shift, the mean of eight of its
+// pixels spread over the image, which every workgroup forms alike: an offset that
+// is large beside the spread costs no bits, and sums of parts add up.  Channels
+// are joined about their group's mean.  Everything is summed in a fixed order.
+#include "gs_numeric.h"
+
+#include <algorithm>
+
+namespace gsi {
+namespace {
+
+constexpr int kThreads = 256, kOneThreads = 512;
+constexpr int kAhead = 4;                       // pixels a thread loads at once
+constexpr int64_t kOneChunks = 8192;            // of eight channels: an image of one workgroup
+
+bool aligned_to(const void *p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
+bool float_type(int t) { return t == GS_DTYPE_F32 || t == GS_DTYPE_F16 || t == GS_DTYPE_BF16; }
+gs_status from_hip(hipError_t e) { return e == hipSuccess ? GS_OK : GS_ERR_HIP; }
+
+struct Args {
+    const void *x, *dy;
+    const uint8_t *x_scales;                    // x in 8-bit blocks, or NULL
+    void *y;                                    // y, or dx
+    uint8_t *kept, *kept_scales;
+    const float *gamma, *beta;
+    float *mean, *rstd;                         // [n][groups]
+    float *part;                                // [n][blocks][c][2] sums of blocks of pixels
+    float *shift;                               // forward: [n][c] what the sums' values are relative to
+    float *sums;                                // backward: [n][c][2] sums of dz and dz h
+    float *means;                               // backward: [n][groups][2] means of g and g h
+    float *dgamma, *dbeta;
+    int64_t x_image, x_pixel, xs_image, xs_pixel, dy_image, dy_pixel, y_image, y_pixel, k_image, k_pixel, ks_image, ks_pixel;
+    int64_t p, per, per_out;                    // pixels of an image, of a block that sums, of one that writes
+    int n, c, groups, cg, chunks, ct, tiles;    // ct: chunks of a block's channels; tiles of them
+    int blocks, blocks_out, act, accumulate;
+    float eps;
+};
+
+// A thread's place: chunk `chunk` of eight channels from `at` on (`valid` of them exist), pixels
+// sub, sub + step, ..
+struct Place {
+    int at, valid, sub, step;
+    bool works;
+};
+template <int THREADS> __device__ __forceinline__ Place place_of(const Args &a, int tile)
+{
+    Place t;
+    t.step = THREADS / a.ct;
+    t.sub = threadIdx.x / a.ct;
+    t.at = (tile * a.ct + threadIdx.x - t.sub * a.ct) * 8;
+    t.valid = min(8, a.c - t.at);
+    t.works = t.sub < t.step && t.valid > 0;
+    return t;
+}
+
+template <typename T> __device__ __forceinline__ void load(const T *p, int64_t i, int valid, float v[8])
+{
+    if (valid == 8) {
+        load8_vec(p + i, v);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j++) v[j] = j < valid ? (float)p[i + j] : 0.0f;
+}
+template <typename T> __device__ __forceinline__ void store(T *p, int64_t i, int valid, const float v[8])
+{
+    if (valid == 8) {
+        store8_vec(p + i, v);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j++)
+        if (j < valid) p[i + j] = (T)v[j];
+}
+// x of the backward: its own type, or 8-bit blocks.
+template <typename T, bool Q8> __device__ __forceinline__ void load_x(const Args &a, int64_t image, int64_t pixel, const Place &t, float v[8])
+{
+    if constexpr (Q8) {                         // c is a multiple of 32
+        const auto w = __builtin_bit_cast(uint2, *reinterpret_cast<const Vec<uint8_t, 8> *>(static_cast<const uint8_t *>(a.x) + image * a.x_image + pixel * a.x_pixel + t.at));
+        const float s = e8m0_value(a.x_scales[image * a.xs_image + pixel * a.xs_pixel + (t.at >> 5)]);
+#pragma unroll
+        for (int j = 0; j < 8; j++) v[j] = e4m3_value((uint8_t)((j < 4 ? w.x : w.y) >> (8 * (j & 3)))) * s;
+    } else {
+        load(static_cast<const T *>(a.x), image * a.x_image + pixel * a.x_pixel + t.at, t.valid, v);
+    }
+}
+
+// ---- forward -------------------------------------------------------------------
+// What the sums of the thread's channels are relative to.
+template <typename T> __device__ __forceinline__ void shift_of(const Args &a, int64_t image, const Place &t, float shift[8])
+{
+    float v[8][8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) load(static_cast<const T *>(a.x), image * a.x_image + ((a.p * i) >> 3) * a.x_pixel + t.at, t.valid, v[i]);
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        shift[j] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; i++) shift[j] += v[i][j];
+        shift[j] *= 0.125f;
+    }
+}
+
+// Sums of differences from the shift, and of their squares, over the thread's pixels of [p0, p1).
+template <typename T> __device__ __forceinline__ void moments(const Args &a, int64_t image, int64_t p0, int64_t p1, const Place &t, const float shift[8], float s[8], float q[8])
+{
+    const T *x = static_cast<const T *>(a.x) + image * a.x_image + t.at;
+    auto add = [&](const float v[8]) {
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            const float d = v[j] - shift[j];
+            s[j] += d;
+            q[j] = fmaf(d, d, q[j]);
+        }
+    };
+    int64_t p = p0 + t.sub;
+    for (; p + (int64_t)(2 * kAhead - 1) * t.step < p1; p += (int64_t)(2 * kAhead) * t.step) {
+        float v[2 * kAhead][8];
+#pragma unroll
+        for (int i = 0; i < 2 * kAhead; i++) load(x, (p + (int64_t)i * t.step) * a.x_pixel, t.valid, v[i]);
+#pragma unroll
+        for (int i = 0; i < 2 * kAhead; i++) add(v[i]);
+    }
+    for (; p < p1; p += t.step) {
+        float v[8];
+        load(x, p * a.x_pixel, t.valid, v);
+        add(v);
+    }
+}
+
+// Adds what the threads of a workgroup that share a chunk have for its
+// channels: channel i's two sums in LDS out[2 i ..].
+template <int THREADS> __device__ __forceinline__ void join_threads(const Args &a, const Place &t, const float s[8], const float q[8], float (*turn)[16], float *out)
+{
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        turn[threadIdx.x][j] = s[j];
+        turn[threadIdx.x][8 + j] = q[j];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.ct * 8; i += THREADS) {
+        const int chunk = i >> 3, j = i & 7;
+        float u = 0.0f, v = 0.0f;
+        for (int r = 0; r < t.step; r++) {
+            u += turn[r * a.ct + chunk][j];
+            v += turn[r * a.ct + chunk][8 + j];
+        }
+        out[2 * i] = u;
+        out[2 * i + 1] = v;
+    }
+    __syncthreads();
+}
+
+// One block of pixels by one tile of channels.
+struct Part {
+    int64_t image;
+    int block, tile;
+    bool there;
+};
+__device__ __forceinline__ Part part_of(const Args &a, int blocks)
+{
+    int64_t b = block_of();
+    Part w;
+    w.there = b < (int64_t)a.n * blocks * a.tiles;
+    w.tile = (int)(b % a.tiles);
+    b /= a.tiles;
+    w.block = (int)(b % blocks);
+    w.image = b / blocks;
+    return w;
+}
+
+template <typename T> __global__ __launch_bounds__(kThreads) void sum_moments(Args a)
+{
+    __shared__ float turn[kThreads][16], out[kThreads * 16];
+    const Part w = part_of(a, a.blocks);
+    if (!w.there) return;
+    const int64_t p0 = w.block * a.per, p1 = min(a.p, p0 + a.per);
+    const Place t = place_of<kThreads>(a, w.tile);
+    float shift[8], s[8], q[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) s[j] = q[j] = 0.0f;
+    if (t.works) {
+        shift_of<T>(a, w.image, t, shift);
+        moments<T>(a, w.image, p0, p1, t, shift, s, q);
+        if (w.block == 0 && t.sub == 0)
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                if (j < t.valid) a.shift[w.image * a.c + t.at + j] = shift[j];
+    }
+    join_threads<kThreads>(a, t, s, q, turn, out);
+    const int c0 = w.tile * a.ct * 8, wide = 2 * min(a.ct * 8, a.c - c0);
+    float *part = a.part + ((w.image * a.blocks + w.block) * a.c + c0) * 2;
+    for (int i = threadIdx.x; i < wide; i += kThreads) part[i] = out[i];
+}
+
+// Sum over the threads of a workgroup.
+template <int THREADS> __device__ __forceinline__ float block_sum(float x, float *lds)
+{
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);
+    __syncthreads();                            // the last use of lds is over
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
+    __syncthreads();
+    x = 0.0f;
+#pragma unroll
+    for (int w = 0; w < THREADS / 64; w++) x += lds[w];
+    return x;
+}
+
+// Adds a group's channels' two sums over the blocks of pixels, up to 256 channels
+// at a time by as many rows of threads as fit; each(channel, sums) in one thread.
+template <class F> __device__ __forceinline__ void join_blocks(const Args &a, int64_t image, int g, float (*turn)[2], F each)
+{
+    const float *part = a.part + (image * a.blocks * a.c + (int64_t)g * a.cg) * 2;
+    for (int c0 = 0; c0 < a.cg; c0 += kThreads) {
+        const int wide = min(kThreads, a.cg - c0), step = kThreads / wide, sub = threadIdx.x / wide, c = c0 + threadIdx.x - sub * wide;
+        float u = 0.0f, v = 0.0f;
+        if (sub < step)
+            for (int b = sub; b < a.blocks; b += step) {
+                u += part[((int64_t)b * a.c + c) * 2];
+                v += part[((int64_t)b * a.c + c) * 2 + 1];
+            }
+        __syncthreads();
+        turn[threadIdx.x][0] = u;
+        turn[threadIdx.x][1] = v;
+        __syncthreads();
+        if (sub) continue;
+        for (int r = 1; r < step; r++) {
+            u += turn[r * wide + threadIdx.x][0];
+            v += turn[r * wide + threadIdx.x][1];
+        }
+        each(g * a.cg + c, u, v);
+    }
+}
+
+// A group's statistics: its channels' means relative to the first one's shift,
+// then squares about the mean of those.
+__global__ __launch_bounds__(kThreads) void join_groups(Args a)
+{
+    __shared__ float turn[kThreads][2], lds[kThreads / 64];
+    const int64_t item = block_of();
+    if (item >= (int64_t)a.n * a.groups) return;
+    const int64_t image = item / a.groups;
+    const int g = (int)(item - image * a.groups);
+    float *shift = a.shift + image * a.c;
+    const float pixels = (float)a.p, first = shift[(int64_t)g * a.cg];
+    float m = 0.0f, q = 0.0f;
+    __syncthreads();                            // every thread has `first`
+    join_blocks(a, image, g, turn, [&](int c, float s, float sq) {
+        const float d = s / pixels, far = shift[c] - first + d;
+        m += far;
+        q += fmaf(-s, d, sq);
+        shift[c] = far;                         // for this thread, below
+    });
+    m = block_sum<kThreads>(m, lds) / (float)a.cg;
+    for (int c = threadIdx.x; c < a.cg; c += kThreads) {
+        const float d = shift[(int64_t)g * a.cg + c] - m;
+        q = fmaf(pixels * d, d, q);
+    }
+    q = block_sum<kThreads>(q, lds);
+    if (threadIdx.x) return;
+    a.mean[item] = first + m;
+    a.rstd[item] = 1.0f / sqrtf((q < 0.0f ? 0.0f : q) / (pixels * (float)a.cg) + a.eps);
+}
+
+// y (and the 8-bit x) of the thread's pixels of [p0, p1).
+template <typename T> __device__ __forceinline__ void emit(const Args &a, int64_t image, int64_t p0, int64_t p1, const Place &t, const float mean[8],
+                                                           const float scale[8], const float shift[8])
+{
+    const T *x = static_cast<const T *>(a.x);
+    T *y = static_cast<T *>(a.y);
+    int64_t p = p0 + t.sub;
+    auto one = [&](int64_t at, float v[8]) {
+        if (a.kept)
+            quantize_chunk(v, a.kept + image * a.k_image + at * a.k_pixel + t.at,
+                           (threadIdx.x & 3) == 0 ? a.kept_scales + image * a.ks_image + at * a.ks_pixel + (t.at >> 5) : nullptr);
+#pragma unroll
+        for (int j = 0; j < 8; j++) v[j] = fmaf(v[j] - mean[j], scale[j], shift[j]);
+        activate_all<8, sizeof(T) == 4>(v, a.act);
+        store(y, image * a.y_image + at * a.y_pixel + t.at, t.valid, v);
+    };
+    for (; p + (int64_t)(kAhead - 1) * t.step < p1; p += (int64_t)kAhead * t.step) {
+        float v[kAhead][8];
+#pragma unroll
+        for (int i = 0; i < kAhead; i++) load(x, image * a.x_image + (p + (int64_t)i * t.step) * a.x_pixel + t.at, t.valid, v[i]);
+#pragma unroll
+        for (int i = 0; i < kAhead; i++) one(p + (int64_t)i * t.step, v[i]);
+    }
+    for (; p < p1; p += t.step) {
+        float v[8];
+        load(x, image * a.x_image + p * a.x_pixel + t.at, t.valid, v);
+        one(p, v);
+    }
+}
+
+// mean, rstd gamma and beta of the thread's channels.
+__device__ __forceinline__ void coefficients(const Args &a, const float *means, const float *rstds, const Place &t, float mean[8], float scale[8], float shift[8])
+{
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        const int c = min(t.at + j, a.c - 1), g = c / a.cg;
+        mean[j] = means[g];
+        scale[j] = rstds[g] * (a.gamma ? a.gamma[c] : 1.0f);
+        shift[j] = a.beta ? a.beta[c] : 0.0f;
+    }
+}
+
+template <typename T> __global__ __launch_bounds__(kThreads) void write_norm(Args a)
+{
+    const Part w = part_of(a, a.blocks_out);
+    if (!w.there) return;
+    const Place t = place_of<kThreads>(a, w.tile);
+    if (!t.works) return;
+    float mean[8], scale[8], shift[8];
+    coefficients(a, a.mean + w.image * a.groups, a.rstd + w.image * a.groups, t, mean, scale, shift);
+    const int64_t p0 = w.block * a.per_out;
+    emit<T>(a, w.image, p0, min(a.p, p0 + a.per_out), t, mean, scale, shift);
+}
+
+// An image per workgroup.
+template <typename T> __global__ __launch_bounds__(kOneThreads) void norm_image(Args a)
+{
+    __shared__ float turn[kOneThreads][16], out[kOneThreads * 4], shifts[kOneThreads * 2], means[kOneThreads * 2], rstds[kOneThreads * 2];
+    const int64_t image = block_of();
+    if (image >= a.n) return;
+    const Place t = place_of<kOneThreads>(a, 0);
+    float mean[8], scale[8], shift[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) scale[j] = shift[j] = 0.0f;
+    if (t.works) {
+        shift_of<T>(a, image, t, mean);
+        moments<T>(a, image, 0, a.p, t, mean, scale, shift);
+        if (t.sub == 0)
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                if (j < t.valid) shifts[t.at + j] = mean[j];
+    }
+    join_threads<kOneThreads>(a, t, scale, shift, turn, out);
+    // a wave per group, as in join_groups
+    const float pixels = (float)a.p;
+    for (int g = threadIdx.x >> 6; g < a.groups; g += kOneThreads / 64) {
+        const int c0 = g * a.cg;
+        const float first = shifts[c0];
+        float m = 0.0f, q = 0.0f;
+        for (int c = c0 + (threadIdx.x & 63); c < c0 + a.cg; c += 64) m += shifts[c] - first + out[2 * c] / pixels;
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) m += __shfl_xor(m, o);
+        m /= (float)a.cg;
+        for (int c = c0 + (threadIdx.x & 63); c < c0 + a.cg; c += 64) {
+            const float s = out[2 * c], d = shifts[c] - first + s / pixels - m;
+            q += fmaf(pixels * d, d, fmaf(-s, s / pixels, out[2 * c + 1]));
+        }
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) q += __shfl_xor(q, o);
+        if (threadIdx.x & 63) continue;
+        const float r = 1.0f / sqrtf((q < 0.0f ? 0.0f : q) / (pixels * (float)a.cg) + a.eps);
+        means[g] = first + m;
+        rstds[g] = r;
+        if (a.mean) a.mean[image * a.groups + g] = first + m;
+        if (a.rstd) a.rstd[image * a.groups + g] = r;
+    }
+    __syncthreads();
+    if (!t.works) return;
+    coefficients(a, means, rstds, t, mean, scale, shift);
+    emit<T>(a, image, 0, a.p, t, mean, scale, shift);
+}
+
+// ---- backward --------------------------------------------------------------------
+// h and dz of eight values.
+template <typename T, bool Q8> __device__ __forceinline__ void gradient_at(const Args &a, int64_t image, int64_t p, const Place &t, const float mean[8], const float rstd[8],
+                                                                           const float gamma[8], const float beta[8], float h[8], float dz[8])
+{
+    load_x<T, Q8>(a, image, p, t, h);
+    load(static_cast<const T *>(a.dy), image * a.dy_image + p * a.dy_pixel + t.at, t.valid, dz);
+    float z[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        h[j] = (h[j] - mean[j]) * rstd[j];
+        z[j] = fmaf(h[j], gamma[j], beta[j]);
+    }
+    scale_by_slope<8, sizeof(T) == 4>(dz, z, a.act);
+}
+__device__ __forceinline__ void channels(const Args &a, int64_t image, const Place &t, float mean[8], float rstd[8], float gamma[8], float beta[8])
+{
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        const int c = min(t.at + j, a.c - 1), g = c / a.cg;
+        mean[j] = a.mean[image * a.groups + g];
+        rstd[j] = a.rstd[image * a.groups + g];
+        gamma[j] = a.gamma ? a.gamma[c] : 1.0f;
+        beta[j] = a.beta ? a.beta[c] : 0.0f;
+    }
+}
+
+// Sums of dz and dz h of a range, per channel, in LDS out[2 i ..].
+template <typename T, bool Q8, int THREADS> __device__ __forceinline__ void gradient_sums(const Args &a, int64_t image, int64_t p0, int64_t p1, const Place &t, const float mean[8],
+                                                                                          const float rstd[8], const float gamma[8], const float beta[8], float (*turn)[16], float *out)
+{
+    float s[8], sh[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) s[j] = sh[j] = 0.0f;
+    if (t.works) {
+#pragma unroll 4
+        for (int64_t p = p0 + t.sub; p < p1; p += t.step) {
+            float h[8], dz[8];
+            gradient_at<T, Q8>(a, image, p, t, mean, rstd, gamma, beta, h, dz);
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                s[j] += dz[j];
+                sh[j] = fmaf(dz[j], h[j], sh[j]);
+            }
+        }
+    }
+    join_threads<THREADS>(a, t, s, sh, turn, out);
+}
+
+template <typename T, bool Q8> __global__ __launch_bounds__(kThreads) void sum_gradients(Args a)
+{
+    __shared__ float turn[kThreads][16], out[kThreads * 16];
+    const Part w = part_of(a, a.blocks);
+    if (!w.there) return;
+    const int64_t p0 = w.block * a.per, p1 = min(a.p, p0 + a.per);
+    const Place t = place_of<kThreads>(a, w.tile);
+    float mean[8], rstd[8], gamma[8], beta[8];
+    channels(a, w.image, t, mean, rstd, gamma, beta);
+    gradient_sums<T, Q8, kThreads>(a, w.image, p0, p1, t, mean, rstd, gamma, beta, turn, out);
+    const int c0 = w.tile * a.ct * 8, wide = 2 * min(a.ct * 8, a.c - c0);
+    float *part = a.part + ((w.image * a.blocks + w.block) * a.c + c0) * 2;
+    for (int i = threadIdx.x; i < wide; i += kThreads) part[i] = out[i];
+}
+
+// A group's channels' sums over the blocks of pixels, and its means of g and g h.
+__global__ __launch_bounds__(kThreads) void join_gradients(Args a)
+{
+    __shared__ float turn[kThreads][2], lds[kThreads / 64];
+    const int64_t item = block_of();
+    if (item >= (int64_t)a.n * a.groups) return;
+    const int64_t image = item / a.groups;
+    const int g = (int)(item - image * a.groups);
+    float mg = 0.0f, mgh = 0.0f;
+    join_blocks(a, image, g, turn, [&](int c, float s, float sh) {
+        a.sums[(image * a.c + c) * 2] = s;
+        a.sums[(image * a.c + c) * 2 + 1] = sh;
+        const float gamma = a.gamma ? a.gamma[c] : 1.0f;
+        mg = fmaf(gamma, s, mg);
+        mgh = fmaf(gamma, sh, mgh);
+    });
+    const float values = (float)a.p * (float)a.cg;
+    mg = block_sum<kThreads>(mg, lds);
+    mgh = block_sum<kThreads>(mgh, lds);
+    if (threadIdx.x) return;
+    a.means[2 * item] = mg / values;
+    a.means[2 * item + 1] = mgh / values;
+}
+
+// dx = rstd (g - mean g - h mean(g h)) of the thread's pixels of [p0, p1).
+template <typename T, bool Q8> __device__ __forceinline__ void emit_gradient(const Args &a, int64_t image, int64_t p0, int64_t p1, const Place &t, const float mean[8],
+                                                                             const float rstd[8], const float gamma[8], const float beta[8], const float *means)
+{
+    float mg[8], mgh[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        const int g = min(t.at + j, a.c - 1) / a.cg;
+        mg[j] = means[2 * g];
+        mgh[j] = means[2 * g + 1];
+    }
+#pragma unroll 2
+    for (int64_t p = p0 + t.sub; p < p1; p += t.step) {
+        float h[8], dz[8];
+        gradient_at<T, Q8>(a, image, p, t, mean, rstd, gamma, beta, h, dz);
+#pragma unroll
+        for (int j = 0; j < 8; j++) dz[j] = rstd[j] * (fmaf(dz[j], gamma[j], -mg[j]) - h[j] * mgh[j]);
+        store(static_cast<T *>(a.y), image * a.y_image + p * a.y_pixel + t.at, t.valid, dz);
+    }
+}
+
+// dgamma and dbeta of 256 channels: sums over the images.
+__device__ __forceinline__ void sum_images(const Args &a, int64_t block)
+{
+    const int64_t c = block * kThreads + threadIdx.x;
+    if (c >= a.c) return;
+    float s = 0.0f, sh = 0.0f;
+    for (int i = 0; i < a.n; i++) {
+        s += a.sums[((int64_t)i * a.c + c) * 2];
+        sh += a.sums[((int64_t)i * a.c + c) * 2 + 1];
+    }
+    if (a.dbeta) a.dbeta[c] = a.accumulate ? a.dbeta[c] + s : s;
+    if (a.dgamma) a.dgamma[c] = a.accumulate ? a.dgamma[c] + sh : sh;
+}
+
+template <typename T, bool Q8> __global__ __launch_bounds__(kThreads) void write_gradient(Args a)
+{
+    const Part w = part_of(a, a.blocks_out);
+    if (!w.there) {
+        sum_images(a, block_of() - (int64_t)a.n * a.blocks_out * a.tiles);
+        return;
+    }
+    const Place t = place_of<kThreads>(a, w.tile);
+    if (!t.works) return;
+    float mean[8], rstd[8], gamma[8], beta[8];
+    channels(a, w.image, t, mean, rstd, gamma, beta);
+    const int64_t p0 = w.block * a.per_out;
+    emit_gradient<T, Q8>(a, w.image, p0, min(a.p, p0 + a.per_out), t, mean, rstd, gamma, beta, a.means + w.image * a.groups * 2);
+}
+
+// An image per workgroup; dgamma and dbeta of a single image at once.
+template <typename T, bool Q8> __global__ __launch_bounds__(kOneThreads) void gradient_image(Args a)
+{
+    __shared__ float turn[kOneThreads][16], out[kOneThreads * 4], means[kOneThreads * 4];
+    const int64_t image = block_of();
+    if (image >= a.n) return;
+    const Place t = place_of<kOneThreads>(a, 0);
+    float mean[8], rstd[8], gamma[8], beta[8];
+    channels(a, image, t, mean, rstd, gamma, beta);
+    gradient_sums<T, Q8, kOneThreads>(a, image, 0, a.p, t, mean, rstd, gamma, beta, turn, out);
+    const float values = (float)a.p * (float)a.cg;
+    for (int g = threadIdx.x >> 6; g < a.groups; g += kOneThreads / 64) {
+        float mg = 0.0f, mgh = 0.0f;
+        for (int i = threadIdx.x & 63; i < a.cg; i += 64) {
+            const int c = g * a.cg + i;
+            const float w = a.gamma ? a.gamma[c] : 1.0f;
+            mg = fmaf(w, out[2 * c], mg);
+            mgh = fmaf(w, out[2 * c + 1], mgh);
+        }
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) {
+            mg += __shfl_xor(mg, o);
+            mgh += __shfl_xor(mgh, o);
+        }
+        if ((threadIdx.x & 63) == 0) {
+            means[2 * g] = mg / values;
+            means[2 * g + 1] = mgh / values;
+        }
+    }
+    for (int c = threadIdx.x; c < a.c; c += kOneThreads) {
+        if (a.sums) {
+            a.sums[(image * a.c + c) * 2] = out[2 * c];
+            a.sums[(image * a.c + c) * 2 + 1] = out[2 * c + 1];
+        } else {
+            if (a.dbeta) a.dbeta[c] = a.accumulate ? a.dbeta[c] + out[2 * c] : out[2 * c];
+            if (a.dgamma) a.dgamma[c] = a.accumulate ? a.dgamma[c] + out[2 * c + 1] : out[2 * c + 1];
+        }
+    }
+    __syncthreads();
+    if (t.works) emit_gradient<T, Q8>(a, image, 0, a.p, t, mean, rstd, gamma, beta, means);
+}
+
+__global__ __launch_bounds__(kThreads) void sum_images_alone(Args a) { sum_images(a, blockIdx.x); }
+
+__global__ __launch_bounds__(kThreads) void zero_two(float *p, float *q, int n)
+{
+    const int i = blockIdx.x * kThreads + threadIdx.x;
+    if (i >= n) return;
+    if (p) p[i] = 0.0f;
+    if (q) q[i] = 0.0f;
+}
+
+// ---- plan -------------------------------------------------------------------------
+constexpr size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+struct Shape {
+    int64_t n, p;
+    int c, groups;
+};
+struct Plan {
+    bool one;                                   // an image per workgroup
+    int ct, tiles, blocks, blocks_out;
+    int64_t per, per_out;
+};
+// Blocks of pixels so that about `want` workgroups run, each thread with at least
+// `least` pixels.
+void cut(const Shape &s, const Plan &w, int64_t want, int least, int &blocks, int64_t &per)
+{
+    const int64_t step = kThreads / w.ct, rows = (s.p + step * least - 1) / (step * least);
+    const int64_t b = std::max<int64_t>(1, std::min<int64_t>(rows, want / std::max<int64_t>(1, s.n * w.tiles)));
+    per = (s.p + b - 1) / b;
+    blocks = (int)((s.p + per - 1) / per);
+}
+Plan plan_of(const Shape &s)
+{
+    Plan w;
+    const int chunks = (s.c + 7) / 8;
+    w.one = s.p * chunks <= kOneChunks && chunks <= kOneThreads / 4;
+    w.ct = std::min(chunks, w.one ? kOneThreads : kThreads);
+    w.tiles = (chunks + w.ct - 1) / w.ct;
+    if (w.one) {
+        w.blocks = w.blocks_out = 1;
+        w.per = w.per_out = s.p;
+    } else {
+        cut(s, w, 1024, 4 * kAhead, w.blocks, w.per);
+        cut(s, w, 4096, 4, w.blocks_out, w.per_out);
+    }
+    return w;
+}
+
+bool shape_ok(int64_t n, int64_t p, int64_t c, int64_t groups)
+{
+    return n >= 0 && n <= 65535 && p >= 0 && p <= ((int64_t)1 << 30) && c >= 1 && c <= 65536 && groups >= 1 && groups <= c && c % groups == 0;
+}
+
+void set_shape(Args &a, const Shape &s, const Plan &w)
+{
+    a.n = (int)s.n;
+    a.p = s.p;
+    a.c = s.c;
+    a.groups = s.groups;
+    a.cg = s.c / s.groups;
+    a.chunks = (s.c + 7) / 8;
+    a.ct = w.ct;
+    a.tiles = w.tiles;
+    a.blocks = w.blocks;
+    a.blocks_out = w.blocks_out;
+    a.per = w.per;
+    a.per_out = w.per_out;
+}
+
+template <typename T> hipError_t launch_fwd(const Args &a, bool one, hipStream_t s)
+{
+    if (one) {
+        norm_image<T><<<grid_of(a.n, kOneThreads), kOneThreads, 0, s>>>(a);
+        return hipGetLastError();
+    }
+    sum_moments<T><<<grid_of((int64_t)a.n * a.blocks * a.tiles, kThreads), kThreads, 0, s>>>(a);
+    join_groups<<<grid_of((int64_t)a.n * a.groups, kThreads), kThreads, 0, s>>>(a);
+    write_norm<T><<<grid_of((int64_t)a.n * a.blocks_out * a.tiles, kThreads), kThreads, 0, s>>>(a);
+    return hipGetLastError();
+}
+template <typename T, bool Q8> hipError_t launch_bwd(const Args &a, bool one, hipStream_t s)
+{
+    const bool wanted = a.dgamma || a.dbeta;
+    const int sums = (a.c + kThreads - 1) / kThreads;
+    if (one) {
+        gradient_image<T, Q8><<<grid_of(a.n, kOneThreads), kOneThreads, 0, s>>>(a);
+        if (wanted && a.n > 1) sum_images_alone<<<sums, kThreads, 0, s>>>(a);
+        return hipGetLastError();
+    }
+    sum_gradients<T, Q8><<<grid_of((int64_t)a.n * a.blocks * a.tiles, kThreads), kThreads, 0, s>>>(a);
+    join_gradients<<<grid_of((int64_t)a.n * a.groups, kThreads), kThreads, 0, s>>>(a);
+    write_gradient<T, Q8><<<grid_of((int64_t)a.n * a.blocks_out * a.tiles + (wanted ? sums : 0), kThreads), kThreads, 0, s>>>(a);
+    return hipGetLastError();
+}
+template <typename T> hipError_t launch_bwd(const Args &a, bool one, hipStream_t s) { return a.x_scales ? launch_bwd<T, true>(a, one, s) : launch_bwd<T, false>(a, one, s); }
+
+bool strides_ok(const void *p, int es, int64_t image, int64_t pixel) { return aligned_to(p, es) && image >= 0 && pixel >= 0; }
+// Whether the values of a result [n][p][wide] all have places of their own.
+bool apart(int64_t n, int64_t p, int64_t wide, int64_t image, int64_t pixel)
+{
+    __int128 extent = wide;
+    const bool pixels_first = pixel <= image;
+    for (int i = 0; i < 2; i++) {
+        const bool pixels = pixels_first == (i == 0);
+        const int64_t count = pixels ? p : n, stride = pixels ? pixel : image;
+        if (count <= 1) continue;
+        if (stride < extent) return false;
+        extent += (__int128)stride * (count - 1);
+    }
+    return true;
+}
+
+gs_status check(const gs_group_norm *a)
+{
+    if (!a || !shape_ok(a->n, a->p, a->c, a->groups) || !float_type(a->dtype) || a->activation < GS_ACT_NONE || a->activation > GS_ACT_GELU) return GS_ERR_INVALID_ARG;
+    if (!(a->eps >= 0.0f) || !(a->eps < INFINITY)) return GS_ERR_INVALID_ARG;
+    const int es = dtype_bytes(a->dtype);
+    if (!strides_ok(a->x, es, a->x_image, a->x_pixel) || !strides_ok(a->y, es, a->y_image, a->y_pixel) || !apart(a->n, a->p, a->c, a->y_image, a->y_pixel))
+        return GS_ERR_INVALID_ARG;
+    if (!aligned_to(a->gamma, 4) || !aligned_to(a->beta, 4) || !aligned_to(a->mean, 4) || !aligned_to(a->rstd, 4)) return GS_ERR_INVALID_ARG;
+    if (a->n > 0 && a->p > 0 && (!a->x || !a->y)) return GS_ERR_INVALID_ARG;
+    if (!a->kept != !a->kept_scales) return GS_ERR_INVALID_ARG;
+    if (a->kept && (a->c % 32 || !strides_ok(a->kept, 1, a->kept_image, a->kept_pixel) || !strides_ok(a->kept_scales, 1, a->kept_scales_image, a->kept_scales_pixel) ||
+                    !apart(a->n, a->p, a->c, a->kept_image, a->kept_pixel) || !apart(a->n, a->p, a->c / 32, a->kept_scales_image, a->kept_scales_pixel)))
+        return GS_ERR_INVALID_ARG;
+    return GS_OK;
+}
+
+gs_status check(const gs_group_norm_grads *a)
+{
+    if (!a || !shape_ok(a->n, a->p, a->c, a->groups) || !float_type(a->dtype) || a->activation < GS_ACT_NONE || a->activation > GS_ACT_GELU) return GS_ERR_INVALID_ARG;
+    const int es = dtype_bytes(a->dtype);
+    if (a->x_dtype != a->dtype && a->x_dtype != GS_DTYPE_MXFP8) return a->x_dtype >= 0 && a->x_dtype <= GS_DTYPE_MXFP8 ? GS_ERR_UNSUPPORTED : GS_ERR_INVALID_ARG;
+    const bool q8 = a->x_dtype == GS_DTYPE_MXFP8;
+    if (!strides_ok(a->x, q8 ? 1 : es, a->x_image, a->x_pixel) || !strides_ok(a->dy, es, a->dy_image, a->dy_pixel) || !strides_ok(a->dx, es, a->dx_image, a->dx_pixel) ||
+        !apart(a->n, a->p, a->c, a->dx_image, a->dx_pixel))
+        return GS_ERR_INVALID_ARG;
+    if (q8 && (a->c % 32 || !strides_ok(a->x_scales, 1, a->x_scales_image, a->x_scales_pixel))) return GS_ERR_INVALID_ARG;
+    if (!aligned_to(a->gamma, 4) || !aligned_to(a->beta, 4) || !aligned_to(a->mean, 4) || !aligned_to(a->rstd, 4) || !aligned_to(a->dgamma, 4) || !aligned_to(a->dbeta, 4))
+        return GS_ERR_INVALID_ARG;
+    if (a->n > 0 && a->p > 0 && (!a->x || !a->dy || !a->dx || !a->mean || !a->rstd || (q8 && !a->x_scales))) return GS_ERR_INVALID_ARG;
+    return GS_OK;
+}
+
+// Partial sums, and what the calls keep per image: statistics (forward), or sums
+// and means (backward).
+size_t part_bytes(const Shape &s, const Plan &w) { return w.one ? 0 : round256((size_t)s.n * w.blocks * s.c * 8); }
+
+}  // namespace
+}  // namespace gsi
+
+using namespace gsi;
+
+extern "C" {
+
+size_t gs_group_norm_fwd_workspace_bytes(int64_t n, int64_t p, int32_t c, int32_t groups)
+{
+    if (!shape_ok(n, p, c, groups) || n == 0 || p == 0) return 0;
+    const Shape s = {n, p, c, groups};
+    const Plan w = plan_of(s);
+    return w.one ? 0 : part_bytes(s, w) + 2 * round256((size_t)n * groups * 4) + round256((size_t)n * c * 4);
+}
+
+gs_status gs_group_norm_fwd(const gs_group_norm *p, void *workspace, size_t workspace_bytes, void *stream)
+{
+    const gs_status st = check(p);
+    if (st != GS_OK) return st;
+    if (p->n == 0 || p->p == 0) return GS_OK;
+    const Shape shape = {p->n, p->p, p->c, p->groups};
+    const Plan w = plan_of(shape);
+    const size_t need = gs_group_norm_fwd_workspace_bytes(p->n, p->p, p->c, p->groups);
+    if (workspace_bytes < need) return GS_ERR_WORKSPACE;
+    if (need && (!workspace || !aligned_to(workspace, 16))) return GS_ERR_INVALID_ARG;
+    Args a = {};
+    set_shape(a, shape, w);
+    a.x = p->x;
+    a.x_image = p->x_image;
+    a.x_pixel = p->x_pixel;
+    a.y = p->y;
+    a.y_image = p->y_image;
+    a.y_pixel = p->y_pixel;
+    a.kept = p->kept;
+    a.k_image = p->kept_image;
+    a.k_pixel = p->kept_pixel;
+    a.kept_scales = p->kept_scales;
+    a.ks_image = p->kept_scales_image;
+    a.ks_pixel = p->kept_scales_pixel;
+    a.gamma = p->gamma;
+    a.beta = p->beta;
+    a.mean = p->mean;
+    a.rstd = p->rstd;
+    a.act = p->activation;
+    a.eps = p->eps;
+    if (!w.one) {
+        char *ws = static_cast<char *>(workspace);
+        a.part = reinterpret_cast<float *>(ws);
+        const size_t at = part_bytes(shape, w), one = round256((size_t)p->n * p->groups * 4);
+        if (!a.mean) a.mean = reinterpret_cast<float *>(ws + at);
+        if (!a.rstd) a.rstd = reinterpret_cast<float *>(ws + at + one);
+        a.shift = reinterpret_cast<float *>(ws + at + 2 * one);
+    }
+    hipStream_t s = (hipStream_t)stream;
+    return from_hip(p->dtype == GS_DTYPE_F32 ? launch_fwd<float>(a, w.one, s) : p->dtype == GS_DTYPE_F16 ? launch_fwd<_Float16>(a, w.one, s) : launch_fwd<__bf16>(a, w.one, s));
+}
+
+size_t gs_group_norm_bwd_workspace_bytes(int64_t n, int64_t p, int32_t c, int32_t groups)
+{
+    if (!shape_ok(n, p, c, groups) || n == 0 || p == 0) return 0;
+    const Shape s = {n, p, c, groups};
+    const Plan w = plan_of(s);
+    if (w.one && n == 1) return 0;
+    return part_bytes(s, w) + round256((size_t)n * c * 8) + (w.one ? 0 : round256((size_t)n * groups * 8));
+}
+
+gs_status gs_group_norm_bwd(const gs_group_norm_grads *p, void *workspace, size_t workspace_bytes, void *stream)
+{
+    const gs_status st = check(p);
+    if (st != GS_OK) return st;
+    hipStream_t s = (hipStream_t)stream;
+    if (p->n == 0 || p->p == 0) {
+        if (p->accumulate || (!p->dgamma && !p->dbeta)) return GS_OK;
+        zero_two<<<(p->c + kThreads - 1) / kThreads, kThreads, 0, s>>>(p->dgamma, p->dbeta, p->c);
+        return from_hip(hipGetLastError());
+    }
+    const Shape shape = {p->n, p->p, p->c, p->groups};
+    const Plan w = plan_of(shape);
+    const size_t need = gs_group_norm_bwd_workspace_bytes(p->n, p->p, p->c, p->groups);
+    if (workspace_bytes < need) return GS_ERR_WORKSPACE;
+    if (need && (!workspace || !aligned_to(workspace, 16))) return GS_ERR_INVALID_ARG;
+    Args a = {};
+    set_shape(a, shape, w);
+    a.x = p->x;
+    a.x_image = p->x_image;
+    a.x_pixel = p->x_pixel;
+    if (p->x_dtype == GS_DTYPE_MXFP8) {
+        a.x_scales = p->x_scales;
+        a.xs_image = p->x_scales_image;
+        a.xs_pixel = p->x_scales_pixel;
+    }
+    a.dy = p->dy;
+    a.dy_image = p->dy_image;
+    a.dy_pixel = p->dy_pixel;
+    a.y = p->dx;
+    a.y_image = p->dx_image;
+    a.y_pixel = p->dx_pixel;
+    a.gamma = p->gamma;
+    a.beta = p->beta;
+    a.mean = const_cast<float *>(p->mean);
+    a.rstd = const_cast<float *>(p->rstd);
+    a.dgamma = p->dgamma;
+    a.dbeta = p->dbeta;
+    a.act = p->activation;
+    a.accumulate = p->accumulate;
+    char *ws = static_cast<char *>(workspace);
+    const size_t at = part_bytes(shape, w);
+    a.part = reinterpret_cast<float *>(ws);
+    a.sums = need ? reinterpret_cast<float *>(ws + at) : nullptr;
+    a.means = reinterpret_cast<float *>(ws + at + round256((size_t)p->n * p->c * 8));
+    return from_hip(p->dtype == GS_DTYPE_F32 ? launch_bwd<float>(a, w.one, s) : p->dtype == GS_DTYPE_F16 ? launch_bwd<_Float16>(a, w.one, s) : launch_bwd<__bf16>(a, w.one, s));
+}
+
+}  // extern "C"

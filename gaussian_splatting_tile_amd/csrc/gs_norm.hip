@@ -64,31 +64,6 @@ template <int LANES> __device__ __forceinline__ float row_sum(float x, float *ld
     return x;
 }
 
-// One chunk of an 8-bit block row: the scale is shared by 4 neighbouring lanes
-// (all of them in the call).  The exponent is the smallest that leaves the
-// block's largest magnitude, 1.m x 2^E, at most 448 = 1.75 x 2^8: E - 8, or
-// E - 7 where 1.m > 1.75.
-__device__ __forceinline__ void quantize_chunk(const float v[8], uint8_t *codes, uint8_t *scale)
-{
-    uint32_t top = 0;
-#pragma unroll
-    for (int j = 0; j < 8; j++) top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-    top = max(top, (uint32_t)__shfl_xor((int)top, 1));
-    top = max(top, (uint32_t)__shfl_xor((int)top, 2));
-    const bool finite = top < 0x7F800000u;
-    int s = (int)(top >> 23) - 8 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-    s = finite ? max(s, 0) : 255;
-    const float inv = finite ? __uint_as_float((uint32_t)(254 - s) << 23) : 0.0f;      // 2^(127 - s), exact
-    int w[2];
-#pragma unroll
-    for (int h = 0; h < 2; h++) {
-        int x = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h] * inv, v[4 * h + 1] * inv, 0, false);
-        w[h] = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h + 2] * inv, v[4 * h + 3] * inv, x, true);
-    }
-    *reinterpret_cast<Vec<uint8_t, 8> *>(codes) = __builtin_bit_cast(Vec<uint8_t, 8>, make_int2(w[0], w[1]));
-    if (scale) *scale = (uint8_t)s;
-}
-
 struct NormArgs {
     const void *x, *residual;
     const float *gamma;

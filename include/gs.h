@@ -873,6 +873,75 @@ size_t gs_attention_bwd_workspace_bytes(const gs_attention *attention /* host */
 gs_status gs_attention_bwd(const gs_attention *attention /* host */, const gs_attention_grads *grads /* host */, void *workspace,
                            size_t workspace_bytes, void *stream);
 
+/* Group norm with an activation over n images of p pixels by c channels,
+ * channels contiguous: over each image's pixels and each group of c / groups
+ * channels
+ *     mean, var of x,  rstd = (var + eps)^(-1/2),  h = (x - mean) rstd,  y = act(gamma_c h + beta_c)
+ * in fp32.  Strides are in elements (of the scales: bytes).  y may be x with the
+ * same strides.  `kept` receives x as GS_DTYPE_MXFP8, blocks of 32 channels, for
+ * gs_group_norm_bwd: a checkpoint of half a 16-bit x's size. */
+typedef struct gs_group_norm {
+    int32_t n;                  /* images, 0 .. 65535                          */
+    int32_t c, groups;          /* 1 .. 65536 channels; groups divides c; a
+                                   checkpoint: c a multiple of 32              */
+    int32_t dtype;              /* of x and y: F32, F16 or BF16                */
+    int32_t activation;         /* gs_activation                               */
+    float eps;                  /* >= 0, finite                                */
+    int64_t p;                  /* pixels, 0 .. 2^30                           */
+    const void *x;              /* [n][p][c]                                   */
+    int64_t x_image, x_pixel;
+    const float *gamma, *beta;  /* [c] or NULL: ones, zeros                    */
+    void *y;                    /* [n][p][c]                                   */
+    int64_t y_image, y_pixel;
+    float *mean, *rstd;         /* [n][groups] or NULL: not kept               */
+    uint8_t *kept;              /* [n][p][c] or NULL: no checkpoint            */
+    int64_t kept_image, kept_pixel;
+    uint8_t *kept_scales;       /* [n][p][c / 32]                              */
+    int64_t kept_scales_image, kept_scales_pixel;
+} gs_group_norm;
+
+/* Workspace of gs_group_norm_fwd, in bytes. */
+size_t gs_group_norm_fwd_workspace_bytes(int64_t n, int64_t p, int32_t c, int32_t groups);
+
+/* Errors: GS_ERR_INVALID_ARG (NULL descriptor or arrays with n p > 0, sizes or
+ * strides out of range, an unknown type or activation, a misaligned pointer, eps
+ * negative or not finite, elements of a result that share a place),
+ * GS_ERR_WORKSPACE. */
+gs_status gs_group_norm_fwd(const gs_group_norm *norm /* host */, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Backward of gs_group_norm_fwd from x, or its checkpoint in its place, and the
+ * kept mean and rstd, for the gradient dy of y:
+ *     h = (x - mean) rstd,  dz = dy act'(gamma h + beta),  g = dz gamma
+ *     dx = rstd (g - mean(g) - h mean(g h)),  dgamma (+)= sum dz h,  dbeta (+)= sum dz
+ * (means over the image's group, sums over images and pixels, in a fixed
+ * order).  dx may be dy with the same strides, or an x of the same type. */
+typedef struct gs_group_norm_grads {
+    int32_t n;
+    int32_t c, groups;
+    int32_t dtype;              /* of dy and dx: F32, F16 or BF16              */
+    int32_t x_dtype;            /* of x: `dtype` or GS_DTYPE_MXFP8              */
+    int32_t activation;
+    int32_t accumulate;         /* nonzero: dgamma += and dbeta += (else =)    */
+    int64_t p;
+    const void *x;
+    int64_t x_image, x_pixel;
+    const uint8_t *x_scales;    /* MXFP8: [n][p][c / 32]                       */
+    int64_t x_scales_image, x_scales_pixel;
+    const float *mean, *rstd;   /* [n][groups]                                 */
+    const float *gamma, *beta;  /* [c] or NULL: ones, zeros                    */
+    const void *dy;
+    int64_t dy_image, dy_pixel;
+    void *dx;
+    int64_t dx_image, dx_pixel;
+    float *dgamma, *dbeta;      /* [c] or NULL: not wanted                     */
+} gs_group_norm_grads;
+
+/* Workspace of gs_group_norm_bwd, in bytes. */
+size_t gs_group_norm_bwd_workspace_bytes(int64_t n, int64_t p, int32_t c, int32_t groups);
+
+/* Errors: as gs_group_norm_fwd; GS_ERR_UNSUPPORTED for an x of another type. */
+gs_status gs_group_norm_bwd(const gs_group_norm_grads *grads /* host */, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Static description of a status code. */
 const char *gs_status_string(gs_status status);
 

@@ -62,3 +62,61 @@ def attention_grads(q, k, v, scale, seen, out, lse, dout):
             dv[i, js, n // g] += p.T @ gi
             keep[i, n][:, js] = ds
     return dq, dk, dv, keep
+
+
+# ---- group norm -------------------------------------------------------------
+def _phi(z):
+    from math import erfc
+    return 0.5 * np.vectorize(erfc, otypes=[np.float64])(-z / 2 ** 0.5)
+
+
+def act(z, name):
+    if name == "relu":
+        return np.maximum(z, 0.0)
+    if name == "silu":
+        return z / (1.0 + np.exp(np.minimum(-z, 700.0)))
+    return z * _phi(z) if name == "gelu" else z
+
+
+def act_slope(z, name):
+    if name == "relu":
+        return (z > 0) * 1.0
+    if name == "silu":
+        s = 1.0 / (1.0 + np.exp(np.minimum(-z, 700.0)))
+        return s * (1.0 + z * (1.0 - s))
+    if name == "gelu":
+        return _phi(z) + z * np.exp(-0.5 * z * z) / (2 * np.pi) ** 0.5
+    return np.ones_like(z)
+
+
+def _per_channel(v, c):
+    return np.repeat(np.asarray(v, np.float64), c // v.shape[1], axis=1)[:, None]
+
+
+def group_norm(x, groups, gamma=None, beta=None, activation="none", eps=1e-5):
+    """x [n][p][c] -> (mean, rstd) [n][groups], z and y [n][p][c]."""
+    n, p, c = x.shape
+    mean, rstd = np.zeros((n, groups)), np.zeros((n, groups))
+    w = c // groups
+    for i in range(n):
+        for g in range(groups):
+            v = x[i, :, g * w:(g + 1) * w]
+            mean[i, g] = v.mean()
+            rstd[i, g] = 1.0 / np.sqrt(((v - v.mean()) ** 2).mean() + eps)
+    h = (x - _per_channel(mean, c)) * _per_channel(rstd, c)
+    z = h * (1.0 if gamma is None else gamma) + (0.0 if beta is None else beta)
+    return mean, rstd, z, act(z, activation)
+
+
+def group_norm_grads(x, mean, rstd, dy, groups, gamma=None, beta=None, activation="none"):
+    """(dx, dgamma, dbeta) from the kept mean and rstd: of the terms of
+    dy_j/dx_i = gamma_j rstd (delta_ij - 1 / m - h_i h_j / m)."""
+    n, p, c = x.shape
+    m = p * c // groups
+    r = _per_channel(rstd, c)
+    h = (x - _per_channel(mean, c)) * r
+    gam = np.ones(c) if gamma is None else gamma
+    dz = dy * act_slope(h * gam + (0.0 if beta is None else beta), activation)
+    u = dz * gam
+    total = lambda v: _per_channel(v.reshape(n, p, groups, c // groups).sum(axis=(1, 3)), c)
+    return r * (u - total(u) / m - h * total(u * h) / m), (dz * h).sum(axis=(0, 1)), dz.sum(axis=(0, 1))

@@ -39,3 +39,27 @@ def test_gradients_against_differences(g):
             down = f()
             x[at] = keep
             assert abs((up - down) / (2 * h) - dx[at]) < 1e-8
+
+
+@pytest.mark.parametrize("activation", ["none", "relu", "silu", "gelu"])
+def test_group_norm_gradients_against_differences(activation):
+    rng = np.random.default_rng(2)
+    x, gamma, beta = rng.standard_normal((2, 3, 6)) + 1.0, 1 + 0.2 * rng.standard_normal(6), 0.3 * rng.standard_normal(6)
+    w = rng.standard_normal(x.shape)
+    f = lambda: float((A.group_norm(x, 2, gamma, beta, activation, 1e-3)[3] * w).sum())
+    mean, rstd, z, _ = A.group_norm(x, 2, gamma, beta, activation, 1e-3)
+    assert np.abs(z).min() > 1e-3                       # no kink within the differences
+    for v, dv in zip((x, gamma, beta), A.group_norm_grads(x, mean, rstd, w, 2, gamma, beta, activation)):
+        for at in np.ndindex(v.shape):
+            keep, h = v[at], 1e-5
+            v[at] = keep + h
+            up = f()
+            v[at] = keep - h
+            down = f()
+            v[at] = keep
+            assert abs((up - down) / (2 * h) - dv[at]) < 1e-7
+
+
+def test_group_norm_of_one_group_of_equal_values():
+    mean, rstd, z, y = A.group_norm(np.full((1, 4, 2), 3.0), 1, eps=0.25)
+    assert mean[0, 0] == 3.0 and rstd[0, 0] == 2.0 and (y == 0).all()
