@@ -22,7 +22,13 @@ namespace gsi {
 namespace {
 
 constexpr int kThreads = 256, kOneThreads = 512;
-constexpr int kAhead = 4;                       // pixels a thread loads at once
+// Four workgroups to a CU, one round: the backward from 8 bits 65 us, 69 with two
+// rounds; the forward 110 and 114 (and 134 with five for four).
+constexpr int kBlocks = 1024;
+// Results that the second-level caches do not hold are written past them
+// (backward 80 -> 75 us); smaller ones stay for who reads them next.
+constexpr int64_t kStreamBytes = 32 << 20;
+constexpr int kHeld = 4;                        // pixels a thread of a single workgroup keeps
 constexpr int64_t kOneChunks = 8192;            // of eight channels: an image of one workgroup
 
 bool aligned_to(const void *p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
@@ -45,13 +51,15 @@ struct Args {
     int64_t p, per, per_out;                    // pixels of an image, of a block that sums, of one that writes
     int n, c, groups, cg, chunks, ct, tiles;    // ct: chunks of a block's channels; tiles of them
     int blocks, blocks_out, act, accumulate;
+    int stream;                                 // results are written past the caches
     float eps;
 };
 
-// A thread's place: chunk `chunk` of eight channels from `at` on (`valid` of them exist), pixels
-// sub, sub + step, ..
+// A thread's place: eight channels from `at` on, pixels sub, sub + step, ..  The
+// last chunk of c channels (8 or more) takes the last eight, so that every load is
+// a whole vector: its first `skip` are the chunk's before it and go no further.
 struct Place {
-    int at, valid, sub, step;
+    int at, skip, sub, step;
     bool works;
 };
 template <int THREADS> __device__ __forceinline__ Place place_of(const Args &a, int tile)
@@ -59,56 +67,97 @@ template <int THREADS> __device__ __forceinline__ Place place_of(const Args &a, 
     Place t;
     t.step = THREADS / a.ct;
     t.sub = threadIdx.x / a.ct;
-    t.at = (tile * a.ct + threadIdx.x - t.sub * a.ct) * 8;
-    t.valid = min(8, a.c - t.at);
-    t.works = t.sub < t.step && t.valid > 0;
+    const int c = (tile * a.ct + threadIdx.x - t.sub * a.ct) * 8;
+    t.works = t.sub < t.step && c < a.c;
+    t.at = max(0, min(c, a.c - 8));
+    t.skip = t.works ? c - t.at : 0;
     return t;
 }
 
-template <typename T> __device__ __forceinline__ void load(const T *p, int64_t i, int valid, float v[8])
+template <typename T> __device__ __forceinline__ Vec<T, 8> load(const T *p, const Args &a)
 {
-    if (valid == 8) {
-        load8_vec(p + i, v);
-        return;
-    }
+    if (a.c >= 8) return *reinterpret_cast<const Vec<T, 8> *>(p);
+    Vec<T, 8> w = {};
 #pragma unroll
-    for (int j = 0; j < 8; j++) v[j] = j < valid ? (float)p[i + j] : 0.0f;
+    for (int j = 0; j < 8; j++)
+        if (j < a.c) w.v[j] = p[j];
+    return w;
 }
-template <typename T> __device__ __forceinline__ void store(T *p, int64_t i, int valid, const float v[8])
+template <typename T> constexpr int type_of() { return sizeof(T) == 4 ? GS_DTYPE_F32 : __is_same(T, _Float16) ? GS_DTYPE_F16 : GS_DTYPE_BF16; }
+template <typename T> __device__ __forceinline__ void store(T *p, const Place &t, const Args &a, const float v[8])
 {
-    if (valid == 8) {
-        store8_vec(p + i, v);
+    if (t.skip == 0 && a.c >= 8) {
+        if (a.stream) store8_stream(p, type_of<T>(), 0, v);
+        else store8_vec(p, v);
         return;
     }
 #pragma unroll
     for (int j = 0; j < 8; j++)
-        if (j < valid) p[i + j] = (T)v[j];
+        if (j >= t.skip && j < a.c) p[j] = (T)v[j];
 }
-// x of the backward: its own type, or 8-bit blocks.
-template <typename T, bool Q8> __device__ __forceinline__ void load_x(const Args &a, int64_t image, int64_t pixel, const Place &t, float v[8])
-{
-    if constexpr (Q8) {                         // c is a multiple of 32
-        const auto w = __builtin_bit_cast(uint2, *reinterpret_cast<const Vec<uint8_t, 8> *>(static_cast<const uint8_t *>(a.x) + image * a.x_image + pixel * a.x_pixel + t.at));
-        const float s = e8m0_value(a.x_scales[image * a.xs_image + pixel * a.xs_pixel + (t.at >> 5)]);
+// x of the backward as it is stored: its own type, or 8-bit blocks.
+template <typename T, bool Q8> struct Stored {
+    Vec<T, 8> w;
+    __device__ __forceinline__ void values(float v[8]) const
+    {
 #pragma unroll
-        for (int j = 0; j < 8; j++) v[j] = e4m3_value((uint8_t)((j < 4 ? w.x : w.y) >> (8 * (j & 3)))) * s;
-    } else {
-        load(static_cast<const T *>(a.x), image * a.x_image + pixel * a.x_pixel + t.at, t.valid, v);
+        for (int j = 0; j < 8; j++) v[j] = (float)w.v[j];
     }
+};
+template <typename T> struct Stored<T, true> {
+    Vec<uint8_t, 8> w;
+    uint8_t s;
+    __device__ __forceinline__ void values(float v[8]) const
+    {
+        typedef float f2 __attribute__((ext_vector_type(2)));
+        const float scale = e8m0_value(s);
+        const uint2 u = __builtin_bit_cast(uint2, w);
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+            const int x = (int)(j ? u.y : u.x);
+            const f2 lo = __builtin_amdgcn_cvt_pk_f32_fp8(x, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(x, true);
+            v[4 * j] = lo[0] * scale;
+            v[4 * j + 1] = lo[1] * scale;
+            v[4 * j + 2] = hi[0] * scale;
+            v[4 * j + 3] = hi[1] * scale;
+        }
+    }
+};
+
+// For every pixel of the thread in [p0, p1): fetch(pixel) of up to N of them, then
+// use(pixel, what was fetched) of each.
+template <int N, class F, class U> __device__ __forceinline__ void each_pixel(const Place &t, int64_t p0, int64_t p1, F fetch, U use)
+{
+    int64_t p = p0 + t.sub;
+    for (; p + (int64_t)(N - 1) * t.step < p1; p += (int64_t)N * t.step) {
+        decltype(fetch(p)) w[N];
+#pragma unroll
+        for (int i = 0; i < N; i++) w[i] = fetch(p + (int64_t)i * t.step);
+#pragma unroll
+        for (int i = 0; i < N; i++) use(p + (int64_t)i * t.step, w[i]);
+    }
+    if (p >= p1) return;
+    decltype(fetch(p)) w[N];                    // the last ones, fewer than N
+#pragma unroll
+    for (int i = 0; i < N; i++)
+        if (p + (int64_t)i * t.step < p1) w[i] = fetch(p + (int64_t)i * t.step);
+#pragma unroll
+    for (int i = 0; i < N; i++)
+        if (p + (int64_t)i * t.step < p1) use(p + (int64_t)i * t.step, w[i]);
 }
 
 // ---- forward -------------------------------------------------------------------
 // What the sums of the thread's channels are relative to.
 template <typename T> __device__ __forceinline__ void shift_of(const Args &a, int64_t image, const Place &t, float shift[8])
 {
-    float v[8][8];
+    Vec<T, 8> v[8];
 #pragma unroll
-    for (int i = 0; i < 8; i++) load(static_cast<const T *>(a.x), image * a.x_image + ((a.p * i) >> 3) * a.x_pixel + t.at, t.valid, v[i]);
+    for (int i = 0; i < 8; i++) v[i] = load(static_cast<const T *>(a.x) + image * a.x_image + ((a.p * i) >> 3) * a.x_pixel + t.at, a);
 #pragma unroll
     for (int j = 0; j < 8; j++) {
         shift[j] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; i++) shift[j] += v[i][j];
+        for (int i = 0; i < 8; i++) shift[j] += (float)v[i].v[j];
         shift[j] *= 0.125f;
     }
 }
@@ -117,32 +166,20 @@ template <typename T> __device__ __forceinline__ void shift_of(const Args &a, in
 template <typename T> __device__ __forceinline__ void moments(const Args &a, int64_t image, int64_t p0, int64_t p1, const Place &t, const float shift[8], float s[8], float q[8])
 {
     const T *x = static_cast<const T *>(a.x) + image * a.x_image + t.at;
-    auto add = [&](const float v[8]) {
+    each_pixel<8>(t, p0, p1, [&](int64_t p) { return load(x + p * a.x_pixel, a); },
+                  [&](int64_t, const Vec<T, 8> &w) {
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            const float d = v[j] - shift[j];
-            s[j] += d;
-            q[j] = fmaf(d, d, q[j]);
-        }
-    };
-    int64_t p = p0 + t.sub;
-    for (; p + (int64_t)(2 * kAhead - 1) * t.step < p1; p += (int64_t)(2 * kAhead) * t.step) {
-        float v[2 * kAhead][8];
-#pragma unroll
-        for (int i = 0; i < 2 * kAhead; i++) load(x, (p + (int64_t)i * t.step) * a.x_pixel, t.valid, v[i]);
-#pragma unroll
-        for (int i = 0; i < 2 * kAhead; i++) add(v[i]);
-    }
-    for (; p < p1; p += t.step) {
-        float v[8];
-        load(x, p * a.x_pixel, t.valid, v);
-        add(v);
-    }
+                      for (int j = 0; j < 8; j++) {
+                          const float d = (float)w.v[j] - shift[j];
+                          s[j] += d;
+                          q[j] = fmaf(d, d, q[j]);
+                      }
+                  });
 }
 
 // Adds what the threads of a workgroup that share a chunk have for its
 // channels: channel i's two sums in LDS out[2 i ..].
-template <int THREADS> __device__ __forceinline__ void join_threads(const Args &a, const Place &t, const float s[8], const float q[8], float (*turn)[16], float *out)
+template <int THREADS> __device__ __forceinline__ void join_threads(const Args &a, const Place &t, int c0, const float s[8], const float q[8], float (*turn)[16], float *out)
 {
 #pragma unroll
     for (int j = 0; j < 8; j++) {
@@ -150,15 +187,27 @@ template <int THREADS> __device__ __forceinline__ void join_threads(const Args &
         turn[threadIdx.x][8 + j] = q[j];
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < a.ct * 8; i += THREADS) {
-        const int chunk = i >> 3, j = i & 7;
+    // a channel's rows by as many threads as there are to a channel, a power of
+    // two of neighbours
+    const int all = a.ct * 8;
+    int parts = 1;
+    while (parts < 8 && parts * 2 * all <= THREADS) parts *= 2;
+    for (int k = threadIdx.x; k < all * parts; k += THREADS) {
+        const int i = k / parts, chunk = i >> 3, j = (i & 7) + max(0, min(c0 + chunk * 8, a.c) + 8 - max(a.c, 8));
         float u = 0.0f, v = 0.0f;
-        for (int r = 0; r < t.step; r++) {
-            u += turn[r * a.ct + chunk][j];
-            v += turn[r * a.ct + chunk][8 + j];
+        if (c0 + i < a.c)
+            for (int r = k & (parts - 1); r < t.step; r += parts) {
+                u += turn[r * a.ct + chunk][j];
+                v += turn[r * a.ct + chunk][8 + j];
+            }
+        for (int o = parts / 2; o > 0; o >>= 1) {
+            u += __shfl_xor(u, o);
+            v += __shfl_xor(v, o);
         }
-        out[2 * i] = u;
-        out[2 * i + 1] = v;
+        if ((k & (parts - 1)) == 0) {
+            out[2 * i] = u;
+            out[2 * i + 1] = v;
+        }
     }
     __syncthreads();
 }
@@ -181,7 +230,7 @@ __device__ __forceinline__ Part part_of(const Args &a, int blocks)
     return w;
 }
 
-template <typename T> __global__ __launch_bounds__(kThreads) void sum_moments(Args a)
+template <typename T> __global__ __launch_bounds__(kThreads, 4) void sum_moments(Args a)
 {
     __shared__ float turn[kThreads][16], out[kThreads * 16];
     const Part w = part_of(a, a.blocks);
@@ -197,10 +246,10 @@ template <typename T> __global__ __launch_bounds__(kThreads) void sum_moments(Ar
         if (w.block == 0 && t.sub == 0)
 #pragma unroll
             for (int j = 0; j < 8; j++)
-                if (j < t.valid) a.shift[w.image * a.c + t.at + j] = shift[j];
+                if (j >= t.skip && j < a.c) a.shift[w.image * a.c + t.at + j] = shift[j];
     }
-    join_threads<kThreads>(a, t, s, q, turn, out);
     const int c0 = w.tile * a.ct * 8, wide = 2 * min(a.ct * 8, a.c - c0);
+    join_threads<kThreads>(a, t, c0, s, q, turn, out);
     float *part = a.part + ((w.image * a.blocks + w.block) * a.c + c0) * 2;
     for (int i = threadIdx.x; i < wide; i += kThreads) part[i] = out[i];
 }
@@ -275,79 +324,123 @@ __global__ __launch_bounds__(kThreads) void join_groups(Args a)
     a.rstd[item] = 1.0f / sqrtf((q < 0.0f ? 0.0f : q) / (pixels * (float)a.cg) + a.eps);
 }
 
-// y (and the 8-bit x) of the thread's pixels of [p0, p1).
-template <typename T> __device__ __forceinline__ void emit(const Args &a, int64_t image, int64_t p0, int64_t p1, const Place &t, const float mean[8],
+// y (and the 8-bit x) of one pixel's eight channels.
+template <typename T, int G> __device__ __forceinline__ void emit_one(const Args &a, int64_t image, int64_t p, const Place &t, const Vec<T, 8> &w, const float mean[G], const float scale[8], const float shift[8])
+{
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) v[j] = (float)w.v[j];
+    if (a.kept)
+        quantize_chunk(v, a.kept + image * a.k_image + p * a.k_pixel + t.at,
+                       (threadIdx.x & 3) == 0 ? a.kept_scales + image * a.ks_image + p * a.ks_pixel + (t.at >> 5) : nullptr);
+#pragma unroll
+    for (int j = 0; j < 8; j++) v[j] = fmaf(v[j] - mean[j * G / 8], scale[j], shift[j]);
+    activate_all<8, sizeof(T) == 4>(v, a.act);
+    store(static_cast<T *>(a.y) + image * a.y_image + p * a.y_pixel + t.at, t, a, v);
+}
+// Those of the thread's pixels of [p0, p1).
+template <typename T, int G> __device__ __forceinline__ void emit(const Args &a, int64_t image, int64_t p0, int64_t p1, const Place &t, const float mean[G],
                                                            const float scale[8], const float shift[8])
 {
-    const T *x = static_cast<const T *>(a.x);
-    T *y = static_cast<T *>(a.y);
-    int64_t p = p0 + t.sub;
-    auto one = [&](int64_t at, float v[8]) {
-        if (a.kept)
-            quantize_chunk(v, a.kept + image * a.k_image + at * a.k_pixel + t.at,
-                           (threadIdx.x & 3) == 0 ? a.kept_scales + image * a.ks_image + at * a.ks_pixel + (t.at >> 5) : nullptr);
-#pragma unroll
-        for (int j = 0; j < 8; j++) v[j] = fmaf(v[j] - mean[j], scale[j], shift[j]);
-        activate_all<8, sizeof(T) == 4>(v, a.act);
-        store(y, image * a.y_image + at * a.y_pixel + t.at, t.valid, v);
-    };
-    for (; p + (int64_t)(kAhead - 1) * t.step < p1; p += (int64_t)kAhead * t.step) {
-        float v[kAhead][8];
-#pragma unroll
-        for (int i = 0; i < kAhead; i++) load(x, image * a.x_image + (p + (int64_t)i * t.step) * a.x_pixel + t.at, t.valid, v[i]);
-#pragma unroll
-        for (int i = 0; i < kAhead; i++) one(p + (int64_t)i * t.step, v[i]);
-    }
-    for (; p < p1; p += t.step) {
-        float v[8];
-        load(x, image * a.x_image + p * a.x_pixel + t.at, t.valid, v);
-        one(p, v);
-    }
+    const T *x = static_cast<const T *>(a.x) + image * a.x_image + t.at;
+    each_pixel<4>(t, p0, p1, [&](int64_t p) { return load(x + p * a.x_pixel, a); },
+                  [&](int64_t p, const Vec<T, 8> &w) { emit_one<T, G>(a, image, p, t, w, mean, scale, shift); });
 }
 
-// mean, rstd gamma and beta of the thread's channels.
-__device__ __forceinline__ void coefficients(const Args &a, const float *means, const float *rstds, const Place &t, float mean[8], float scale[8], float shift[8])
+// A thread keeps G values of each statistic: 2 where every four channels from a
+// multiple of four on are of one group, else 8; channel j's is number j * G / 8.
+// Each of them, and its group g: f(i, g).
+template <int G, class F> __device__ __forceinline__ void each_group(const Args &a, const Place &t, F f)
+{
+    int g = t.at / a.cg, left = (g + 1) * a.cg - t.at;
+#pragma unroll
+    for (int i = 0; i < G; i++) {
+        f(i, min(g, a.groups - 1));
+        left -= 8 / G;
+        if (left <= 0) {
+            g++;
+            left += a.cg;
+        }
+    }
+}
+// Eight values from p[t.at] on, or `other`.
+__device__ __forceinline__ void load_channels(const Args &a, const float *p, const Place &t, float other, float v[8])
 {
 #pragma unroll
-    for (int j = 0; j < 8; j++) {
-        const int c = min(t.at + j, a.c - 1), g = c / a.cg;
-        mean[j] = means[g];
-        scale[j] = rstds[g] * (a.gamma ? a.gamma[c] : 1.0f);
-        shift[j] = a.beta ? a.beta[c] : 0.0f;
+    for (int j = 0; j < 8; j++) v[j] = other;
+    if (!p) return;
+    if (a.c >= 8) {
+        load8_vec(p + t.at, v);
+        return;
     }
+#pragma unroll
+    for (int j = 0; j < 8; j++)
+        if (j < a.c) v[j] = p[j];
+}
+// mean, rstd gamma and beta of the thread's channels.
+template <int G> __device__ __forceinline__ void coefficients(const Args &a, const float *means, const float *rstds, const Place &t, float mean[G], float scale[8], float shift[8])
+{
+    load_channels(a, a.gamma, t, 1.0f, scale);
+    load_channels(a, a.beta, t, 0.0f, shift);
+    float rstd[G];
+    each_group<G>(a, t, [&](int i, int g) {
+        mean[i] = means[g];
+        rstd[i] = rstds[g];
+    });
+#pragma unroll
+    for (int j = 0; j < 8; j++) scale[j] *= rstd[j * G / 8];
 }
 
-template <typename T> __global__ __launch_bounds__(kThreads) void write_norm(Args a)
+template <typename T, int G> __global__ __launch_bounds__(kThreads, 4) void write_norm(Args a)
 {
     const Part w = part_of(a, a.blocks_out);
     if (!w.there) return;
     const Place t = place_of<kThreads>(a, w.tile);
     if (!t.works) return;
-    float mean[8], scale[8], shift[8];
-    coefficients(a, a.mean + w.image * a.groups, a.rstd + w.image * a.groups, t, mean, scale, shift);
+    float mean[G], scale[8], shift[8];
+    coefficients<G>(a, a.mean + w.image * a.groups, a.rstd + w.image * a.groups, t, mean, scale, shift);
     const int64_t p0 = w.block * a.per_out;
-    emit<T>(a, w.image, p0, min(a.p, p0 + a.per_out), t, mean, scale, shift);
+    emit<T, G>(a, w.image, p0, min(a.p, p0 + a.per_out), t, mean, scale, shift);
 }
 
-// An image per workgroup.
-template <typename T> __global__ __launch_bounds__(kOneThreads) void norm_image(Args a)
+// An image per workgroup; with HELD its values wait in registers, up to kHeld
+// pixels a thread, else they are read again.
+template <typename T, int G, bool HELD> __global__ __launch_bounds__(kOneThreads) void norm_image(Args a)
 {
     __shared__ float turn[kOneThreads][16], out[kOneThreads * 4], shifts[kOneThreads * 2], means[kOneThreads * 2], rstds[kOneThreads * 2];
     const int64_t image = block_of();
     if (image >= a.n) return;
     const Place t = place_of<kOneThreads>(a, 0);
+    const T *x = static_cast<const T *>(a.x) + image * a.x_image + t.at;
+    Vec<T, 8> held[HELD ? kHeld : 1];
     float mean[8], scale[8], shift[8];
 #pragma unroll
     for (int j = 0; j < 8; j++) scale[j] = shift[j] = 0.0f;
     if (t.works) {
-        shift_of<T>(a, image, t, mean);
-        moments<T>(a, image, 0, a.p, t, mean, scale, shift);
+        if constexpr (HELD) {
+#pragma unroll
+            for (int i = 0; i < kHeld; i++)
+                if (t.sub + i * t.step < a.p) held[i] = load(x + (int64_t)(t.sub + i * t.step) * a.x_pixel, a);
+            shift_of<T>(a, image, t, mean);
+#pragma unroll
+            for (int i = 0; i < kHeld; i++)
+                if (t.sub + i * t.step < a.p)
+#pragma unroll
+                    for (int j = 0; j < 8; j++) {
+                        const float d = (float)held[i].v[j] - mean[j];
+                        scale[j] += d;
+                        shift[j] = fmaf(d, d, shift[j]);
+                    }
+        } else {
+            shift_of<T>(a, image, t, mean);
+            moments<T>(a, image, 0, a.p, t, mean, scale, shift);
+        }
         if (t.sub == 0)
 #pragma unroll
             for (int j = 0; j < 8; j++)
-                if (j < t.valid) shifts[t.at + j] = mean[j];
+                if (j >= t.skip && j < a.c) shifts[t.at + j] = mean[j];
     }
-    join_threads<kOneThreads>(a, t, scale, shift, turn, out);
+    join_threads<kOneThreads>(a, t, 0, scale, shift, turn, out);
     // a wave per group, as in join_groups
     const float pixels = (float)a.p;
     for (int g = threadIdx.x >> 6; g < a.groups; g += kOneThreads / 64) {
@@ -373,70 +466,103 @@ template <typename T> __global__ __launch_bounds__(kOneThreads) void norm_image(
     }
     __syncthreads();
     if (!t.works) return;
-    coefficients(a, means, rstds, t, mean, scale, shift);
-    emit<T>(a, image, 0, a.p, t, mean, scale, shift);
+    coefficients<G>(a, means, rstds, t, mean, scale, shift);
+    if constexpr (HELD) {
+#pragma unroll
+        for (int i = 0; i < kHeld; i++)
+            if (t.sub + i * t.step < a.p) emit_one<T, G>(a, image, t.sub + i * t.step, t, held[i], mean, scale, shift);
+    } else {
+        emit<T, G>(a, image, 0, a.p, t, mean, scale, shift);
+    }
 }
 
 // ---- backward --------------------------------------------------------------------
-// h and dz of eight values.
-template <typename T, bool Q8> __device__ __forceinline__ void gradient_at(const Args &a, int64_t image, int64_t p, const Place &t, const float mean[8], const float rstd[8],
-                                                                           const float gamma[8], const float beta[8], float h[8], float dz[8])
-{
-    load_x<T, Q8>(a, image, p, t, h);
-    load(static_cast<const T *>(a.dy), image * a.dy_image + p * a.dy_pixel + t.at, t.valid, dz);
-    float z[8];
-#pragma unroll
-    for (int j = 0; j < 8; j++) {
-        h[j] = (h[j] - mean[j]) * rstd[j];
-        z[j] = fmaf(h[j], gamma[j], beta[j]);
+// What a pixel's eight channels need: x and dy as they are stored.
+template <typename T, bool Q8> struct Pair {
+    Stored<T, Q8> x;
+    Vec<T, 8> dy;
+};
+// The thread's channels, and the first of its values.
+template <typename T, bool Q8, int G> struct Channels {
+    float mean[G], rstd[G], gamma[8], beta[8];
+    const void *x;
+    const uint8_t *scale;
+    const T *dy;
+
+    __device__ __forceinline__ void init(const Args &a, int64_t image, const Place &t)
+    {
+        load_channels(a, a.gamma, t, 1.0f, gamma);
+        load_channels(a, a.beta, t, 0.0f, beta);
+        each_group<G>(a, t, [&](int i, int g) {
+            mean[i] = a.mean[image * a.groups + g];
+            rstd[i] = a.rstd[image * a.groups + g];
+        });
+        dy = static_cast<const T *>(a.dy) + image * a.dy_image + t.at;
+        if constexpr (Q8) {
+            x = static_cast<const uint8_t *>(a.x) + image * a.x_image + t.at;
+            scale = a.x_scales + image * a.xs_image + (t.at >> 5);
+        } else {
+            x = static_cast<const T *>(a.x) + image * a.x_image + t.at;
+        }
     }
-    scale_by_slope<8, sizeof(T) == 4>(dz, z, a.act);
-}
-__device__ __forceinline__ void channels(const Args &a, int64_t image, const Place &t, float mean[8], float rstd[8], float gamma[8], float beta[8])
-{
-#pragma unroll
-    for (int j = 0; j < 8; j++) {
-        const int c = min(t.at + j, a.c - 1), g = c / a.cg;
-        mean[j] = a.mean[image * a.groups + g];
-        rstd[j] = a.rstd[image * a.groups + g];
-        gamma[j] = a.gamma ? a.gamma[c] : 1.0f;
-        beta[j] = a.beta ? a.beta[c] : 0.0f;
+    __device__ __forceinline__ Pair<T, Q8> fetch(const Args &a, int64_t p) const
+    {
+        Pair<T, Q8> w;
+        if constexpr (Q8) {                     // c is a multiple of 32
+            w.x.w = *reinterpret_cast<const Vec<uint8_t, 8> *>(static_cast<const uint8_t *>(x) + p * a.x_pixel);
+            w.x.s = scale[p * a.xs_pixel];
+        } else {
+            w.x.w = load(static_cast<const T *>(x) + p * a.x_pixel, a);
+        }
+        w.dy = load(dy + p * a.dy_pixel, a);
+        return w;
     }
-}
+    // h and dz of a pixel
+    __device__ __forceinline__ void gradient(const Args &a, const Pair<T, Q8> &w, float h[8], float dz[8]) const
+    {
+        float z[8];
+        w.x.values(h);
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            h[j] = (h[j] - mean[j * G / 8]) * rstd[j * G / 8];
+            z[j] = fmaf(h[j], gamma[j], beta[j]);
+            dz[j] = (float)w.dy.v[j];
+        }
+        scale_by_slope<8, sizeof(T) == 4>(dz, z, a.act);
+    }
+};
 
 // Sums of dz and dz h of a range, per channel, in LDS out[2 i ..].
-template <typename T, bool Q8, int THREADS> __device__ __forceinline__ void gradient_sums(const Args &a, int64_t image, int64_t p0, int64_t p1, const Place &t, const float mean[8],
-                                                                                          const float rstd[8], const float gamma[8], const float beta[8], float (*turn)[16], float *out)
+template <typename T, bool Q8, int G, int THREADS> __device__ __forceinline__ void gradient_sums(const Args &a, const Channels<T, Q8, G> &ch, int64_t p0, int64_t p1, const Place &t, int c0, float (*turn)[16], float *out)
 {
     float s[8], sh[8];
 #pragma unroll
     for (int j = 0; j < 8; j++) s[j] = sh[j] = 0.0f;
-    if (t.works) {
-#pragma unroll 4
-        for (int64_t p = p0 + t.sub; p < p1; p += t.step) {
-            float h[8], dz[8];
-            gradient_at<T, Q8>(a, image, p, t, mean, rstd, gamma, beta, h, dz);
+    if (t.works)
+        each_pixel<2>(t, p0, p1, [&](int64_t p) { return ch.fetch(a, p); },
+                      [&](int64_t, const Pair<T, Q8> &w) {
+                          float h[8], dz[8];
+                          ch.gradient(a, w, h, dz);
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
-                s[j] += dz[j];
-                sh[j] = fmaf(dz[j], h[j], sh[j]);
-            }
-        }
-    }
-    join_threads<THREADS>(a, t, s, sh, turn, out);
+                          for (int j = 0; j < 8; j++) {
+                              s[j] += dz[j];
+                              sh[j] = fmaf(dz[j], h[j], sh[j]);
+                          }
+                      });
+    join_threads<THREADS>(a, t, c0, s, sh, turn, out);
 }
 
-template <typename T, bool Q8> __global__ __launch_bounds__(kThreads) void sum_gradients(Args a)
+template <typename T, bool Q8, int G> __global__ __launch_bounds__(kThreads, 4) void sum_gradients(Args a)
 {
     __shared__ float turn[kThreads][16], out[kThreads * 16];
     const Part w = part_of(a, a.blocks);
     if (!w.there) return;
     const int64_t p0 = w.block * a.per, p1 = min(a.p, p0 + a.per);
     const Place t = place_of<kThreads>(a, w.tile);
-    float mean[8], rstd[8], gamma[8], beta[8];
-    channels(a, w.image, t, mean, rstd, gamma, beta);
-    gradient_sums<T, Q8, kThreads>(a, w.image, p0, p1, t, mean, rstd, gamma, beta, turn, out);
+    Channels<T, Q8, G> ch;
+    ch.init(a, w.image, t);
     const int c0 = w.tile * a.ct * 8, wide = 2 * min(a.ct * 8, a.c - c0);
+    gradient_sums<T, Q8, G, kThreads>(a, ch, p0, p1, t, c0, turn, out);
     float *part = a.part + ((w.image * a.blocks + w.block) * a.c + c0) * 2;
     for (int i = threadIdx.x; i < wide; i += kThreads) part[i] = out[i];
 }
@@ -466,24 +592,22 @@ __global__ __launch_bounds__(kThreads) void join_gradients(Args a)
 }
 
 // dx = rstd (g - mean g - h mean(g h)) of the thread's pixels of [p0, p1).
-template <typename T, bool Q8> __device__ __forceinline__ void emit_gradient(const Args &a, int64_t image, int64_t p0, int64_t p1, const Place &t, const float mean[8],
-                                                                             const float rstd[8], const float gamma[8], const float beta[8], const float *means)
+template <typename T, bool Q8, int G> __device__ __forceinline__ void emit_gradient(const Args &a, const Channels<T, Q8, G> &ch, int64_t image, int64_t p0, int64_t p1, const Place &t, const float *means)
 {
-    float mg[8], mgh[8];
+    float mg[G], mgh[G];
+    each_group<G>(a, t, [&](int i, int g) {
+        mg[i] = means[2 * g];
+        mgh[i] = means[2 * g + 1];
+    });
+    T *dx = static_cast<T *>(a.y) + image * a.y_image + t.at;
+    each_pixel<2>(t, p0, p1, [&](int64_t p) { return ch.fetch(a, p); },
+                  [&](int64_t p, const Pair<T, Q8> &w) {
+                      float h[8], dz[8];
+                      ch.gradient(a, w, h, dz);
 #pragma unroll
-    for (int j = 0; j < 8; j++) {
-        const int g = min(t.at + j, a.c - 1) / a.cg;
-        mg[j] = means[2 * g];
-        mgh[j] = means[2 * g + 1];
-    }
-#pragma unroll 2
-    for (int64_t p = p0 + t.sub; p < p1; p += t.step) {
-        float h[8], dz[8];
-        gradient_at<T, Q8>(a, image, p, t, mean, rstd, gamma, beta, h, dz);
-#pragma unroll
-        for (int j = 0; j < 8; j++) dz[j] = rstd[j] * (fmaf(dz[j], gamma[j], -mg[j]) - h[j] * mgh[j]);
-        store(static_cast<T *>(a.y), image * a.y_image + p * a.y_pixel + t.at, t.valid, dz);
-    }
+                      for (int j = 0; j < 8; j++) dz[j] = ch.rstd[j * G / 8] * fmaf(-h[j], mgh[j * G / 8], fmaf(dz[j], ch.gamma[j], -mg[j * G / 8]));
+                      store(dx + p * a.y_pixel, t, a, dz);
+                  });
 }
 
 // dgamma and dbeta of 256 channels: sums over the images.
@@ -500,7 +624,7 @@ __device__ __forceinline__ void sum_images(const Args &a, int64_t block)
     if (a.dgamma) a.dgamma[c] = a.accumulate ? a.dgamma[c] + sh : sh;
 }
 
-template <typename T, bool Q8> __global__ __launch_bounds__(kThreads) void write_gradient(Args a)
+template <typename T, bool Q8, int G> __global__ __launch_bounds__(kThreads, 4) void write_gradient(Args a)
 {
     const Part w = part_of(a, a.blocks_out);
     if (!w.there) {
@@ -509,22 +633,22 @@ template <typename T, bool Q8> __global__ __launch_bounds__(kThreads) void write
     }
     const Place t = place_of<kThreads>(a, w.tile);
     if (!t.works) return;
-    float mean[8], rstd[8], gamma[8], beta[8];
-    channels(a, w.image, t, mean, rstd, gamma, beta);
+    Channels<T, Q8, G> ch;
+    ch.init(a, w.image, t);
     const int64_t p0 = w.block * a.per_out;
-    emit_gradient<T, Q8>(a, w.image, p0, min(a.p, p0 + a.per_out), t, mean, rstd, gamma, beta, a.means + w.image * a.groups * 2);
+    emit_gradient<T, Q8, G>(a, ch, w.image, p0, min(a.p, p0 + a.per_out), t, a.means + w.image * a.groups * 2);
 }
 
 // An image per workgroup; dgamma and dbeta of a single image at once.
-template <typename T, bool Q8> __global__ __launch_bounds__(kOneThreads) void gradient_image(Args a)
+template <typename T, bool Q8, int G> __global__ __launch_bounds__(kOneThreads) void gradient_image(Args a)
 {
     __shared__ float turn[kOneThreads][16], out[kOneThreads * 4], means[kOneThreads * 4];
     const int64_t image = block_of();
     if (image >= a.n) return;
     const Place t = place_of<kOneThreads>(a, 0);
-    float mean[8], rstd[8], gamma[8], beta[8];
-    channels(a, image, t, mean, rstd, gamma, beta);
-    gradient_sums<T, Q8, kOneThreads>(a, image, 0, a.p, t, mean, rstd, gamma, beta, turn, out);
+    Channels<T, Q8, G> ch;
+    ch.init(a, image, t);
+    gradient_sums<T, Q8, G, kOneThreads>(a, ch, 0, a.p, t, 0, turn, out);
     const float values = (float)a.p * (float)a.cg;
     for (int g = threadIdx.x >> 6; g < a.groups; g += kOneThreads / 64) {
         float mg = 0.0f, mgh = 0.0f;
@@ -554,7 +678,7 @@ template <typename T, bool Q8> __global__ __launch_bounds__(kOneThreads) void gr
         }
     }
     __syncthreads();
-    if (t.works) emit_gradient<T, Q8>(a, image, 0, a.p, t, mean, rstd, gamma, beta, means);
+    if (t.works) emit_gradient<T, Q8, G>(a, ch, image, 0, a.p, t, means);
 }
 
 __global__ __launch_bounds__(kThreads) void sum_images_alone(Args a) { sum_images(a, blockIdx.x); }
@@ -592,15 +716,16 @@ Plan plan_of(const Shape &s)
 {
     Plan w;
     const int chunks = (s.c + 7) / 8;
-    w.one = s.p * chunks <= kOneChunks && chunks <= kOneThreads / 4;
+    // one workgroup per image: its values held in registers, or many images
+    w.one = chunks <= kOneThreads / 4 && (s.p <= (int64_t)kHeld * (kOneThreads / chunks) || (s.p * chunks <= kOneChunks && s.n >= 128));
     w.ct = std::min(chunks, w.one ? kOneThreads : kThreads);
     w.tiles = (chunks + w.ct - 1) / w.ct;
     if (w.one) {
         w.blocks = w.blocks_out = 1;
         w.per = w.per_out = s.p;
     } else {
-        cut(s, w, 1024, 4 * kAhead, w.blocks, w.per);
-        cut(s, w, 4096, 4, w.blocks_out, w.per_out);
+        cut(s, w, kBlocks, 2, w.blocks, w.per);
+        cut(s, w, kBlocks, 1, w.blocks_out, w.per_out);
     }
     return w;
 }
@@ -610,7 +735,7 @@ bool shape_ok(int64_t n, int64_t p, int64_t c, int64_t groups)
     return n >= 0 && n <= 65535 && p >= 0 && p <= ((int64_t)1 << 30) && c >= 1 && c <= 65536 && groups >= 1 && groups <= c && c % groups == 0;
 }
 
-void set_shape(Args &a, const Shape &s, const Plan &w)
+void set_shape(Args &a, const Shape &s, const Plan &w, int es)
 {
     a.n = (int)s.n;
     a.p = s.p;
@@ -624,33 +749,40 @@ void set_shape(Args &a, const Shape &s, const Plan &w)
     a.blocks_out = w.blocks_out;
     a.per = w.per;
     a.per_out = w.per_out;
+    a.stream = s.n * s.p * s.c * es > kStreamBytes;
 }
 
-template <typename T> hipError_t launch_fwd(const Args &a, bool one, hipStream_t s)
+template <typename T, int G> hipError_t launch_fwd(const Args &a, bool one, hipStream_t s)
 {
     if (one) {
-        norm_image<T><<<grid_of(a.n, kOneThreads), kOneThreads, 0, s>>>(a);
+        if (a.p <= (int64_t)kHeld * (kOneThreads / a.ct)) norm_image<T, G, true><<<grid_of(a.n, kOneThreads), kOneThreads, 0, s>>>(a);
+        else norm_image<T, G, false><<<grid_of(a.n, kOneThreads), kOneThreads, 0, s>>>(a);
         return hipGetLastError();
     }
     sum_moments<T><<<grid_of((int64_t)a.n * a.blocks * a.tiles, kThreads), kThreads, 0, s>>>(a);
     join_groups<<<grid_of((int64_t)a.n * a.groups, kThreads), kThreads, 0, s>>>(a);
-    write_norm<T><<<grid_of((int64_t)a.n * a.blocks_out * a.tiles, kThreads), kThreads, 0, s>>>(a);
+    write_norm<T, G><<<grid_of((int64_t)a.n * a.blocks_out * a.tiles, kThreads), kThreads, 0, s>>>(a);
     return hipGetLastError();
 }
-template <typename T, bool Q8> hipError_t launch_bwd(const Args &a, bool one, hipStream_t s)
+// Two values of a statistic to a thread, or eight (see each_group).
+bool by_fours(const Args &a) { return a.cg % 4 == 0; }
+template <typename T> hipError_t launch_fwd(const Args &a, bool one, hipStream_t s) { return by_fours(a) ? launch_fwd<T, 2>(a, one, s) : launch_fwd<T, 8>(a, one, s); }
+
+template <typename T, bool Q8, int G> hipError_t launch_bwd(const Args &a, bool one, hipStream_t s)
 {
     const bool wanted = a.dgamma || a.dbeta;
     const int sums = (a.c + kThreads - 1) / kThreads;
     if (one) {
-        gradient_image<T, Q8><<<grid_of(a.n, kOneThreads), kOneThreads, 0, s>>>(a);
+        gradient_image<T, Q8, G><<<grid_of(a.n, kOneThreads), kOneThreads, 0, s>>>(a);
         if (wanted && a.n > 1) sum_images_alone<<<sums, kThreads, 0, s>>>(a);
         return hipGetLastError();
     }
-    sum_gradients<T, Q8><<<grid_of((int64_t)a.n * a.blocks * a.tiles, kThreads), kThreads, 0, s>>>(a);
+    sum_gradients<T, Q8, G><<<grid_of((int64_t)a.n * a.blocks * a.tiles, kThreads), kThreads, 0, s>>>(a);
     join_gradients<<<grid_of((int64_t)a.n * a.groups, kThreads), kThreads, 0, s>>>(a);
-    write_gradient<T, Q8><<<grid_of((int64_t)a.n * a.blocks_out * a.tiles + (wanted ? sums : 0), kThreads), kThreads, 0, s>>>(a);
+    write_gradient<T, Q8, G><<<grid_of((int64_t)a.n * a.blocks_out * a.tiles + (wanted ? sums : 0), kThreads), kThreads, 0, s>>>(a);
     return hipGetLastError();
 }
+template <typename T, bool Q8> hipError_t launch_bwd(const Args &a, bool one, hipStream_t s) { return by_fours(a) ? launch_bwd<T, Q8, 2>(a, one, s) : launch_bwd<T, Q8, 8>(a, one, s); }
 template <typename T> hipError_t launch_bwd(const Args &a, bool one, hipStream_t s) { return a.x_scales ? launch_bwd<T, true>(a, one, s) : launch_bwd<T, false>(a, one, s); }
 
 bool strides_ok(const void *p, int es, int64_t image, int64_t pixel) { return aligned_to(p, es) && image >= 0 && pixel >= 0; }
@@ -731,7 +863,7 @@ gs_status gs_group_norm_fwd(const gs_group_norm *p, void *workspace, size_t work
     if (workspace_bytes < need) return GS_ERR_WORKSPACE;
     if (need && (!workspace || !aligned_to(workspace, 16))) return GS_ERR_INVALID_ARG;
     Args a = {};
-    set_shape(a, shape, w);
+    set_shape(a, shape, w, dtype_bytes(p->dtype));
     a.x = p->x;
     a.x_image = p->x_image;
     a.x_pixel = p->x_pixel;
@@ -787,7 +919,7 @@ gs_status gs_group_norm_bwd(const gs_group_norm_grads *p, void *workspace, size_
     if (workspace_bytes < need) return GS_ERR_WORKSPACE;
     if (need && (!workspace || !aligned_to(workspace, 16))) return GS_ERR_INVALID_ARG;
     Args a = {};
-    set_shape(a, shape, w);
+    set_shape(a, shape, w, dtype_bytes(p->dtype));
     a.x = p->x;
     a.x_image = p->x_image;
     a.x_pixel = p->x_pixel;
