@@ -6,9 +6,9 @@
 // first, so what they read is read twice, the second time out of the last-level
 // cache while it fits.  A thread keeps eight consecutive channels (16 bytes of a
 // 16-bit type) and walks over pixels, so that statistics, gamma and beta stay in
-// registers and any group size costs the same.  Images of up to 64K values are
-// one workgroup's, in one launch; larger ones take three: sums of blocks of
-// pixels, joined per group, then the results.
+// registers and any group size costs the same.  Images of up to 16K values (64K of
+// many) are one workgroup's, in one launch; larger ones take two or three: sums
+// of blocks of pixels, joined per group, then the results.
 //
 // A channel's sums are of differences from a shift, the mean of eight of its
 // pixels spread over the image, which every workgroup forms alike: an offset that
@@ -28,6 +28,7 @@ constexpr int kBlocks = 1024;
 // Results that the second-level caches do not hold are written past them
 // (backward 80 -> 75 us); smaller ones stay for who reads them next.
 constexpr int64_t kStreamBytes = 32 << 20;
+constexpr int kJoinChannels = 1024, kJoinBlocks = 32;
 constexpr int kHeld = 4;                        // pixels a thread of a single workgroup keeps
 constexpr int64_t kOneChunks = 8192;            // of eight channels: an image of one workgroup
 
@@ -377,11 +378,9 @@ __device__ __forceinline__ void load_channels(const Args &a, const float *p, con
     for (int j = 0; j < 8; j++)
         if (j < a.c) v[j] = p[j];
 }
-// mean, rstd gamma and beta of the thread's channels.
-template <int G> __device__ __forceinline__ void coefficients(const Args &a, const float *means, const float *rstds, const Place &t, float mean[G], float scale[8], float shift[8])
+// mean, and rstd gamma in gamma's place, of the thread's channels.
+template <int G> __device__ __forceinline__ void coefficients(const Args &a, const float *means, const float *rstds, const Place &t, float mean[G], float scale[8])
 {
-    load_channels(a, a.gamma, t, 1.0f, scale);
-    load_channels(a, a.beta, t, 0.0f, shift);
     float rstd[G];
     each_group<G>(a, t, [&](int i, int g) {
         mean[i] = means[g];
@@ -391,14 +390,73 @@ template <int G> __device__ __forceinline__ void coefficients(const Args &a, con
     for (int j = 0; j < 8; j++) scale[j] *= rstd[j * G / 8];
 }
 
-template <typename T, int G> __global__ __launch_bounds__(kThreads, 4) void write_norm(Args a)
+// Statistics of an image's groups from its channels' sums, a wave per group, as in
+// join_groups; all in LDS, and in mean and rstd (`keep`).
+template <int THREADS> __device__ __forceinline__ void group_statistics(const Args &a, int64_t image, const float *shifts, const float *sums, float *means, float *rstds, bool keep)
 {
+    const float pixels = (float)a.p;
+    for (int g = threadIdx.x >> 6; g < a.groups; g += THREADS / 64) {
+        const int c0 = g * a.cg;
+        const float first = shifts[c0];
+        float m = 0.0f, q = 0.0f;
+        for (int c = c0 + (threadIdx.x & 63); c < c0 + a.cg; c += 64) m += shifts[c] - first + sums[2 * c] / pixels;
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) m += __shfl_xor(m, o);
+        m /= (float)a.cg;
+        for (int c = c0 + (threadIdx.x & 63); c < c0 + a.cg; c += 64) {
+            const float s = sums[2 * c], d = shifts[c] - first + s / pixels - m;
+            q += fmaf(pixels * d, d, fmaf(-s, s / pixels, sums[2 * c + 1]));
+        }
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) q += __shfl_xor(q, o);
+        if (threadIdx.x & 63) continue;
+        const float r = 1.0f / sqrtf((q < 0.0f ? 0.0f : q) / (pixels * (float)a.cg) + a.eps);
+        means[g] = first + m;
+        rstds[g] = r;
+        if (keep && a.mean) a.mean[image * a.groups + g] = first + m;
+        if (keep && a.rstd) a.rstd[image * a.groups + g] = r;
+    }
+    __syncthreads();
+}
+// An image's channels' sums over its few blocks of pixels, in LDS.
+__device__ __forceinline__ void image_sums(const Args &a, int64_t image, float *sums)
+{
+    for (int c = threadIdx.x; c < a.c; c += kThreads) {
+        float u = 0.0f, v = 0.0f;
+        const float2 *part = reinterpret_cast<const float2 *>(a.part) + image * a.blocks * a.c + c;
+        for (int b = 0; b < a.blocks; b += 8) {            // eight loads on their way at once
+            float2 w[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++) w[i] = b + i < a.blocks ? part[(int64_t)(b + i) * a.c] : float2{0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                u += w[i].x;
+                v += w[i].y;
+            }
+        }
+        sums[2 * c] = u;
+        sums[2 * c + 1] = v;
+    }
+}
+
+// JOIN: every workgroup forms the statistics itself, from few blocks' sums.
+template <typename T, int G, bool JOIN> __global__ __launch_bounds__(kThreads, 4) void write_norm(Args a)
+{
+    __shared__ float sums[JOIN ? 2 * kJoinChannels : 1], shifts[JOIN ? kJoinChannels : 1], means[JOIN ? kJoinChannels : 1], rstds[JOIN ? kJoinChannels : 1];
     const Part w = part_of(a, a.blocks_out);
     if (!w.there) return;
     const Place t = place_of<kThreads>(a, w.tile);
-    if (!t.works) return;
     float mean[G], scale[8], shift[8];
-    coefficients<G>(a, a.mean + w.image * a.groups, a.rstd + w.image * a.groups, t, mean, scale, shift);
+    load_channels(a, a.gamma, t, 1.0f, scale);
+    load_channels(a, a.beta, t, 0.0f, shift);
+    if constexpr (JOIN) {
+        image_sums(a, w.image, sums);
+        for (int c = threadIdx.x; c < a.c; c += kThreads) shifts[c] = a.shift[w.image * a.c + c];
+        __syncthreads();
+        group_statistics<kThreads>(a, w.image, shifts, sums, means, rstds, w.block == 0);
+    }
+    if (!t.works) return;
+    coefficients<G>(a, JOIN ? means : a.mean + w.image * a.groups, JOIN ? rstds : a.rstd + w.image * a.groups, t, mean, scale);
     const int64_t p0 = w.block * a.per_out;
     emit<T, G>(a, w.image, p0, min(a.p, p0 + a.per_out), t, mean, scale, shift);
 }
@@ -413,60 +471,39 @@ template <typename T, int G, bool HELD> __global__ __launch_bounds__(kOneThreads
     const Place t = place_of<kOneThreads>(a, 0);
     const T *x = static_cast<const T *>(a.x) + image * a.x_image + t.at;
     Vec<T, 8> held[HELD ? kHeld : 1];
-    float mean[8], scale[8], shift[8];
+    float near[8], s[8], q[8], scale[8], shift[8], mean[G];
+    load_channels(a, a.gamma, t, 1.0f, scale);              // on their way early
+    load_channels(a, a.beta, t, 0.0f, shift);
 #pragma unroll
-    for (int j = 0; j < 8; j++) scale[j] = shift[j] = 0.0f;
+    for (int j = 0; j < 8; j++) s[j] = q[j] = 0.0f;
     if (t.works) {
         if constexpr (HELD) {
 #pragma unroll
             for (int i = 0; i < kHeld; i++)
                 if (t.sub + i * t.step < a.p) held[i] = load(x + (int64_t)(t.sub + i * t.step) * a.x_pixel, a);
-            shift_of<T>(a, image, t, mean);
+            shift_of<T>(a, image, t, near);
 #pragma unroll
             for (int i = 0; i < kHeld; i++)
                 if (t.sub + i * t.step < a.p)
 #pragma unroll
                     for (int j = 0; j < 8; j++) {
-                        const float d = (float)held[i].v[j] - mean[j];
-                        scale[j] += d;
-                        shift[j] = fmaf(d, d, shift[j]);
+                        const float d = (float)held[i].v[j] - near[j];
+                        s[j] += d;
+                        q[j] = fmaf(d, d, q[j]);
                     }
         } else {
-            shift_of<T>(a, image, t, mean);
-            moments<T>(a, image, 0, a.p, t, mean, scale, shift);
+            shift_of<T>(a, image, t, near);
+            moments<T>(a, image, 0, a.p, t, near, s, q);
         }
         if (t.sub == 0)
 #pragma unroll
             for (int j = 0; j < 8; j++)
-                if (j >= t.skip && j < a.c) shifts[t.at + j] = mean[j];
+                if (j >= t.skip && j < a.c) shifts[t.at + j] = near[j];
     }
-    join_threads<kOneThreads>(a, t, 0, scale, shift, turn, out);
-    // a wave per group, as in join_groups
-    const float pixels = (float)a.p;
-    for (int g = threadIdx.x >> 6; g < a.groups; g += kOneThreads / 64) {
-        const int c0 = g * a.cg;
-        const float first = shifts[c0];
-        float m = 0.0f, q = 0.0f;
-        for (int c = c0 + (threadIdx.x & 63); c < c0 + a.cg; c += 64) m += shifts[c] - first + out[2 * c] / pixels;
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) m += __shfl_xor(m, o);
-        m /= (float)a.cg;
-        for (int c = c0 + (threadIdx.x & 63); c < c0 + a.cg; c += 64) {
-            const float s = out[2 * c], d = shifts[c] - first + s / pixels - m;
-            q += fmaf(pixels * d, d, fmaf(-s, s / pixels, out[2 * c + 1]));
-        }
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) q += __shfl_xor(q, o);
-        if (threadIdx.x & 63) continue;
-        const float r = 1.0f / sqrtf((q < 0.0f ? 0.0f : q) / (pixels * (float)a.cg) + a.eps);
-        means[g] = first + m;
-        rstds[g] = r;
-        if (a.mean) a.mean[image * a.groups + g] = first + m;
-        if (a.rstd) a.rstd[image * a.groups + g] = r;
-    }
-    __syncthreads();
+    join_threads<kOneThreads>(a, t, 0, s, q, turn, out);
+    group_statistics<kOneThreads>(a, image, shifts, out, means, rstds, true);
     if (!t.works) return;
-    coefficients<G>(a, means, rstds, t, mean, scale, shift);
+    coefficients<G>(a, means, rstds, t, mean, scale);
     if constexpr (HELD) {
 #pragma unroll
         for (int i = 0; i < kHeld; i++)
@@ -610,33 +647,65 @@ template <typename T, bool Q8, int G> __device__ __forceinline__ void emit_gradi
                   });
 }
 
-// dgamma and dbeta of 256 channels: sums over the images.
-__device__ __forceinline__ void sum_images(const Args &a, int64_t block)
+// Means of g and g h of an image's groups from its channels' sums, a wave per
+// group, in LDS.
+template <int THREADS> __device__ __forceinline__ void group_means(const Args &a, const float *sums, float *means)
+{
+    const float values = (float)a.p * (float)a.cg;
+    for (int g = threadIdx.x >> 6; g < a.groups; g += THREADS / 64) {
+        float mg = 0.0f, mgh = 0.0f;
+        for (int i = threadIdx.x & 63; i < a.cg; i += 64) {
+            const int c = g * a.cg + i;
+            const float w = a.gamma ? a.gamma[c] : 1.0f;
+            mg = fmaf(w, sums[2 * c], mg);
+            mgh = fmaf(w, sums[2 * c + 1], mgh);
+        }
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) {
+            mg += __shfl_xor(mg, o);
+            mgh += __shfl_xor(mgh, o);
+        }
+        if (threadIdx.x & 63) continue;
+        means[2 * g] = mg / values;
+        means[2 * g + 1] = mgh / values;
+    }
+    __syncthreads();
+}
+
+// dgamma and dbeta of 256 channels: sums over the `rows` of images, or of images'
+// blocks.
+__device__ __forceinline__ void sum_images(const Args &a, const float *sums, int64_t rows, int64_t block)
 {
     const int64_t c = block * kThreads + threadIdx.x;
     if (c >= a.c) return;
     float s = 0.0f, sh = 0.0f;
-    for (int i = 0; i < a.n; i++) {
-        s += a.sums[((int64_t)i * a.c + c) * 2];
-        sh += a.sums[((int64_t)i * a.c + c) * 2 + 1];
+    for (int64_t i = 0; i < rows; i++) {
+        s += sums[(i * a.c + c) * 2];
+        sh += sums[(i * a.c + c) * 2 + 1];
     }
     if (a.dbeta) a.dbeta[c] = a.accumulate ? a.dbeta[c] + s : s;
     if (a.dgamma) a.dgamma[c] = a.accumulate ? a.dgamma[c] + sh : sh;
 }
 
-template <typename T, bool Q8, int G> __global__ __launch_bounds__(kThreads, 4) void write_gradient(Args a)
+template <typename T, bool Q8, int G, bool JOIN> __global__ __launch_bounds__(kThreads, 4) void write_gradient(Args a)
 {
+    __shared__ float sums[JOIN ? 2 * kJoinChannels : 1], means[JOIN ? 2 * kJoinChannels : 1];
     const Part w = part_of(a, a.blocks_out);
     if (!w.there) {
-        sum_images(a, block_of() - (int64_t)a.n * a.blocks_out * a.tiles);
+        sum_images(a, JOIN ? a.part : a.sums, JOIN ? (int64_t)a.n * a.blocks : a.n, block_of() - (int64_t)a.n * a.blocks_out * a.tiles);
         return;
     }
     const Place t = place_of<kThreads>(a, w.tile);
-    if (!t.works) return;
     Channels<T, Q8, G> ch;
     ch.init(a, w.image, t);
+    if constexpr (JOIN) {
+        image_sums(a, w.image, sums);
+        __syncthreads();
+        group_means<kThreads>(a, sums, means);
+    }
+    if (!t.works) return;
     const int64_t p0 = w.block * a.per_out;
-    emit_gradient<T, Q8, G>(a, ch, w.image, p0, min(a.p, p0 + a.per_out), t, a.means + w.image * a.groups * 2);
+    emit_gradient<T, Q8, G>(a, ch, w.image, p0, min(a.p, p0 + a.per_out), t, JOIN ? means : a.means + w.image * a.groups * 2);
 }
 
 // An image per workgroup; dgamma and dbeta of a single image at once.
@@ -649,25 +718,7 @@ template <typename T, bool Q8, int G> __global__ __launch_bounds__(kOneThreads) 
     Channels<T, Q8, G> ch;
     ch.init(a, image, t);
     gradient_sums<T, Q8, G, kOneThreads>(a, ch, 0, a.p, t, 0, turn, out);
-    const float values = (float)a.p * (float)a.cg;
-    for (int g = threadIdx.x >> 6; g < a.groups; g += kOneThreads / 64) {
-        float mg = 0.0f, mgh = 0.0f;
-        for (int i = threadIdx.x & 63; i < a.cg; i += 64) {
-            const int c = g * a.cg + i;
-            const float w = a.gamma ? a.gamma[c] : 1.0f;
-            mg = fmaf(w, out[2 * c], mg);
-            mgh = fmaf(w, out[2 * c + 1], mgh);
-        }
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) {
-            mg += __shfl_xor(mg, o);
-            mgh += __shfl_xor(mgh, o);
-        }
-        if ((threadIdx.x & 63) == 0) {
-            means[2 * g] = mg / values;
-            means[2 * g + 1] = mgh / values;
-        }
-    }
+    group_means<kOneThreads>(a, out, means);
     for (int c = threadIdx.x; c < a.c; c += kOneThreads) {
         if (a.sums) {
             a.sums[(image * a.c + c) * 2] = out[2 * c];
@@ -677,11 +728,10 @@ template <typename T, bool Q8, int G> __global__ __launch_bounds__(kOneThreads) 
             if (a.dgamma) a.dgamma[c] = a.accumulate ? a.dgamma[c] + out[2 * c + 1] : out[2 * c + 1];
         }
     }
-    __syncthreads();
     if (t.works) emit_gradient<T, Q8, G>(a, ch, image, 0, a.p, t, means);
 }
 
-__global__ __launch_bounds__(kThreads) void sum_images_alone(Args a) { sum_images(a, blockIdx.x); }
+__global__ __launch_bounds__(kThreads) void sum_images_alone(Args a) { sum_images(a, a.sums, a.n, blockIdx.x); }
 
 __global__ __launch_bounds__(kThreads) void zero_two(float *p, float *q, int n)
 {
@@ -752,6 +802,10 @@ void set_shape(Args &a, const Shape &s, const Plan &w, int es)
     a.stream = s.n * s.p * s.c * es > kStreamBytes;
 }
 
+// Sums of few blocks are joined by every workgroup that writes: a launch less
+// (JJ), where their reading does not show.
+bool joins(const Args &a) { return a.c <= kJoinChannels && a.blocks <= kJoinBlocks && (int64_t)a.n * a.blocks <= 1024; }
+
 template <typename T, int G> hipError_t launch_fwd(const Args &a, bool one, hipStream_t s)
 {
     if (one) {
@@ -760,8 +814,13 @@ template <typename T, int G> hipError_t launch_fwd(const Args &a, bool one, hipS
         return hipGetLastError();
     }
     sum_moments<T><<<grid_of((int64_t)a.n * a.blocks * a.tiles, kThreads), kThreads, 0, s>>>(a);
+    const dim3 out = grid_of((int64_t)a.n * a.blocks_out * a.tiles, kThreads);
+    if (joins(a)) {
+        write_norm<T, G, true><<<out, kThreads, 0, s>>>(a);
+        return hipGetLastError();
+    }
     join_groups<<<grid_of((int64_t)a.n * a.groups, kThreads), kThreads, 0, s>>>(a);
-    write_norm<T, G><<<grid_of((int64_t)a.n * a.blocks_out * a.tiles, kThreads), kThreads, 0, s>>>(a);
+    write_norm<T, G, false><<<out, kThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 // Two values of a statistic to a thread, or eight (see each_group).
@@ -778,8 +837,13 @@ template <typename T, bool Q8, int G> hipError_t launch_bwd(const Args &a, bool 
         return hipGetLastError();
     }
     sum_gradients<T, Q8, G><<<grid_of((int64_t)a.n * a.blocks * a.tiles, kThreads), kThreads, 0, s>>>(a);
+    const dim3 out = grid_of((int64_t)a.n * a.blocks_out * a.tiles + (wanted ? sums : 0), kThreads);
+    if (joins(a)) {
+        write_gradient<T, Q8, G, true><<<out, kThreads, 0, s>>>(a);
+        return hipGetLastError();
+    }
     join_gradients<<<grid_of((int64_t)a.n * a.groups, kThreads), kThreads, 0, s>>>(a);
-    write_gradient<T, Q8, G><<<grid_of((int64_t)a.n * a.blocks_out * a.tiles + (wanted ? sums : 0), kThreads), kThreads, 0, s>>>(a);
+    write_gradient<T, Q8, G, false><<<out, kThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 template <typename T, bool Q8> hipError_t launch_bwd(const Args &a, bool one, hipStream_t s) { return by_fours(a) ? launch_bwd<T, Q8, 2>(a, one, s) : launch_bwd<T, Q8, 8>(a, one, s); }
