@@ -46,14 +46,16 @@ struct Args {
     Tensor dq, dk, dv;                          // results
     float *lse;                                 // [batch][heads][nq], or NULL
     const float *lse2, *delta;                  // backward: [batch][heads][nq_pad]
-    float *part, *part2;                        // of splits: [split][batch][heads][rows][d] sums
-    float *ml;                                  // [split][batch][heads][nq][2] maximum and sum
+    // of splits, as the waves hold them: sums [split][wave][DP / 8][64][4] and (forward)
+    // maxima and sums of exponentials [split][wave][32][2], wave = (pair * tiles + tile) * waves + wave
+    float *part, *part2, *ml;
     const int32_t *lengths;
     const uint8_t *mask;
     int64_t mask_stride;
     int batch, heads, kv, group, nq, nk, nq_pad, d, rows;       // rows = nq * group
-    int tiles, splits;                          // blocks along the wave columns; splits of the other side
+    int tiles, splits, run;                     // blocks along the wave columns; splits of the other side; tiles of a run
     int64_t blocks;
+    int waves;                                  // of a block
     int type;                                   // gs_dtype of the tensors
     float c, scale;                             // scale * log2 e, scale
 };
@@ -281,6 +283,16 @@ template <int DP> __device__ __forceinline__ void store_columns(void *row, int t
         }
 }
 
+// A wave's sums as they are, for the joining of splits: 16 bytes a lane, in order.
+template <int DP> __device__ __forceinline__ void store_part(float *part, int64_t at, const f16v (&acc)[DP / 32], float f, int lane)
+{
+    gemm::f4 *to = reinterpret_cast<gemm::f4 *>(part) + at * (DP / 8 * 64) + lane;
+#pragma unroll
+    for (int t = 0; t < DP / 32; t++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) to[(t * 4 + i) * 64] = gemm::f4{acc[t][4 * i], acc[t][4 * i + 1], acc[t][4 * i + 2], acc[t][4 * i + 3]} * f;
+}
+
 // Which of 64 keys from k0 on are attended.  `byte`: the lane's mask byte (lane =
 // key), prefetched; 1 without a mask.
 __device__ __forceinline__ uint64_t attended(int k0, int length, uint32_t byte, int lane)
@@ -296,24 +308,29 @@ __device__ __forceinline__ int length_of(const Args &a, int batch)
     return a.lengths ? max(0, min(a.lengths[batch], a.nk)) : a.nk;
 }
 
-// What a block works on: consecutive blocks of a die share a head's operands.
+// What a block works on.  Blocks go to the 8 dies in turn; runs of tiles that share
+// a head's operands and a split stay on one die, whose second-level cache then
+// serves them, and neighbouring runs go to different dies, so that batch elements
+// of different lengths keep all of them busy.
 struct Item {
     int batch, head, split, tile;               // head: of k and v
 };
 __device__ __forceinline__ bool item_of(const Args &a, Item &it)
 {
-    int64_t b = block_of();
-    if (b >= a.blocks) return false;
-    // the die's share of the list, in order (64 bits: up to 2^31 blocks and more)
-    const int64_t per = a.blocks >> 3, more = a.blocks & 7, die = b & 7;
-    b = die * per + min(die, more) + (b >> 3);
-    it.tile = (int)(b % a.tiles);
-    b /= a.tiles;
-    it.split = (int)(b % a.splits);
-    b /= a.splits;
-    it.head = (int)(b % a.kv);
-    it.batch = (int)(b / a.kv);
-    return true;
+    const uint32_t b = (uint32_t)block_of(), at = b >> 3;                   // under 2^31 blocks
+    const uint32_t run = at / (uint32_t)a.run * 8 + (b & 7), parts = ((uint32_t)a.tiles + a.run - 1) / a.run;
+    const uint32_t pair = run / parts, group = pair / (uint32_t)a.splits;
+    it.tile = (int)(run - pair * parts) * a.run + (int)(at % a.run);
+    it.split = (int)(pair - group * a.splits);
+    it.batch = (int)(group / (uint32_t)a.kv);
+    it.head = (int)(group - (uint32_t)it.batch * a.kv);
+    return it.batch < a.batch && it.tile < a.tiles;
+}
+// The wave's place among the partial sums.
+__device__ __forceinline__ int64_t part_at(const Args &a, const Item &it, int wave)
+{
+    const int64_t pairs = (int64_t)a.batch * a.kv;
+    return ((it.split * pairs + (int64_t)it.batch * a.kv + it.head) * a.tiles + it.tile) * a.waves + wave;
 }
 
 }  // namespace attn

@@ -100,100 +100,124 @@ __global__ __launch_bounds__(kThreads) void row_statistics(Args a, float *lse2, 
 }
 
 // ---- splits -----------------------------------------------------------------------
-// Partial softmaxes (sums relative to their own maxima) of SL splits at a time; 16
-// lanes a row.  Sums are taken in a fixed order.
-template <int SL> __global__ __launch_bounds__(kThreads) void join_fwd(Args a)
+// A unit is 16 bytes a lane of the 64 lanes that hold 32 rows' sums; its SW waves
+// take every SW-th split, the first of them adds theirs, in order.
+struct JoinArgs {
+    const float *part, *ml;
+    Tensor to;
+    float *lse;
+    int64_t waves, units;                       // waves' places in a split, units = waves * per
+    int per, rows, tiles, wide, group, heads, splits, d, type;      // per: units of a wave; wide: waves of a block; rows: of a pair
+};
+// Where a unit's lane writes: its row's place in the tensor, or not.
+struct Target {
+    bool there;
+    int at;                                     // first of four d
+    int64_t row, stat;                          // elements; index into lse
+};
+__device__ __forceinline__ Target target_of(const JoinArgs &a, int64_t wave, int unit, int lane)
 {
-    constexpr int kRows = kThreads / 16 / SL;
-    __shared__ float sums[kRows][SL][16][9], tops[kRows][SL];
-    const int lane = threadIdx.x & 15, sub = (threadIdx.x >> 4) % SL, r = threadIdx.x / (16 * SL);
-    const int64_t rows = (int64_t)a.batch * a.heads * a.nq, row = block_of() * kRows + r;
-    const int splits = row < rows ? a.splits : 0;
-    float m = -INFINITY;
-    for (int s = sub; s < splits; s += SL) m = fmaxf(m, a.ml[2 * (s * rows + row)]);
-    if constexpr (SL > 1) {
-        if (lane == 0) tops[r][sub] = m;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < SL; i++) m = fmaxf(m, tops[r][i]);
+    const int64_t tile = wave / a.wide, pair = tile / a.tiles;
+    const int row = (int)((tile - pair * a.tiles) * a.wide + (wave - tile * a.wide)) * 32 + (lane & 31);
+    const int kv = a.heads / a.group;
+    const int64_t batch = pair / kv;
+    const int token = row / a.group, head = (int)(pair - batch * kv) * a.group + row - token * a.group;
+    Target t;
+    t.there = row < a.rows;
+    t.at = (unit >> 2) * 32 + (lane >> 5) * 16 + (unit & 3) * 4;
+    t.row = batch * a.to.sb + token * a.to.sr + head * a.to.sh;
+    t.stat = (batch * a.heads + head) * (a.rows / a.group) + token;
+    return t;
+}
+__device__ __forceinline__ void store4(const JoinArgs &a, const Target &t, const gemm::f4 &v)
+{
+    void *to = const_cast<void *>(a.to.p);
+    if (!t.there) return;
+    if (t.at + 4 <= a.d) {
+        const int64_t i = t.row + t.at;
+        if (a.type == GS_DTYPE_F32) *reinterpret_cast<Vec<float, 4> *>(static_cast<float *>(to) + i) = Vec<float, 4>{{v[0], v[1], v[2], v[3]}};
+        else if (a.type == GS_DTYPE_F16) *reinterpret_cast<Vec<_Float16, 4> *>(static_cast<_Float16 *>(to) + i) = Vec<_Float16, 4>{{(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]}};
+        else *reinterpret_cast<Vec<__bf16, 4> *>(static_cast<__bf16 *>(to) + i) = Vec<__bf16, 4>{{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]}};
+        return;
     }
-    const float base = m == -INFINITY ? 0.0f : m;
-    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, sum = 0.0f;
-    const int valid = a.d - lane * 8;
-    for (int s = sub; s < splits; s += SL) {
-        const int64_t at = s * rows + row;
-        const float ms = a.ml[2 * at], ls = a.ml[2 * at + 1];
-        if (ms == -INFINITY && ls == 0.0f) continue;        // no attended key there
-        const float f = ms == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(ms - base);      // NaN scores have no maximum, but a sum
-        sum = fmaf(ls, f, sum);
-        if (valid > 0) {
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+        if (t.at + j < a.d) store_from_float(to, a.type, t.row + t.at + j, v[j]);
+}
+
+// Partial softmaxes (SOFT: sums relative to their own maxima), or plain sums.
+template <int SW, bool SOFT> __global__ __launch_bounds__(kThreads) void join_splits(JoinArgs a)
+{
+    constexpr int kUnits = kThreads / 64 / SW;
+    __shared__ gemm::f4 turn[SW > 1 ? kThreads : 1];
+    __shared__ float2 stats[SW > 1 ? kThreads : 1];
+    const int lane = threadIdx.x & 63, sub = (threadIdx.x >> 6) % SW;
+    const int64_t u = block_of() * kUnits + (threadIdx.x >> 6) / SW;
+    const bool works = u < a.units;
+    const int64_t wave = works ? u / a.per : 0;
+    const int unit = works ? (int)(u - wave * a.per) : 0, splits = works ? a.splits : 0;
+    const gemm::f4 *part = reinterpret_cast<const gemm::f4 *>(a.part) + (wave * a.per + unit) * 64 + lane;
+    const float2 *ml = reinterpret_cast<const float2 *>(a.ml) + wave * 32 + (lane & 31);
+    const int64_t next = a.waves * a.per * 64, next_ml = a.waves * 32;
+    gemm::f4 v = {0, 0, 0, 0};
+    float sum = 0.0f, m = -INFINITY, base = 0.0f;
+    if constexpr (SOFT) {
+        for (int s = sub; s < splits; s += 8 * SW) {
             float x[8];
-            load8(a.part, GS_DTYPE_F32, at * a.d + lane * 8, valid, x);
 #pragma unroll
-            for (int i = 0; i < 8; i++) v[i] = fmaf(x[i], f, v[i]);
+            for (int i = 0; i < 8; i++) x[i] = s + i * SW < splits ? ml[(s + i * SW) * next_ml].x : -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 8; i++) m = fmaxf(m, x[i]);
         }
-    }
-    if constexpr (SL > 1) {
+        if constexpr (SW > 1) {
+            stats[threadIdx.x].x = m;
+            __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 8; i++) sums[r][sub][lane][i] = v[i];
-        sums[r][sub][lane][8] = sum;
+            for (int i = 0; i < SW; i++) m = fmaxf(m, stats[(threadIdx.x / (64 * SW) * SW + i) * 64 + lane].x);
+            __syncthreads();
+        }
+        base = m == -INFINITY ? 0.0f : m;
+    }
+    for (int s = sub; s < splits; s += 8 * SW) {
+        gemm::f4 x[8];
+        float2 w[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (s + i * SW < splits) {
+                x[i] = part[(s + i * SW) * next];
+                if constexpr (SOFT) w[i] = ml[(s + i * SW) * next_ml];
+            }
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (s + i * SW < splits) {
+                if constexpr (SOFT) {
+                    // NaN scores have no maximum, but a sum: it goes on
+                    const float f = w[i].x == -INFINITY && w[i].y != 0.0f ? 1.0f : __builtin_amdgcn_exp2f(w[i].x - base);
+                    sum = fmaf(w[i].y, f, sum);
+                    v += x[i] * f;
+                } else {
+                    v += x[i];
+                }
+            }
+    }
+    if constexpr (SW > 1) {
+        turn[threadIdx.x] = v;
+        stats[threadIdx.x].y = sum;
         __syncthreads();
         if (sub) return;
 #pragma unroll
-        for (int k = 1; k < SL; k++) {
-#pragma unroll
-            for (int i = 0; i < 8; i++) v[i] += sums[r][k][lane][i];
-            sum += sums[r][k][lane][8];
+        for (int i = 1; i < SW; i++) {
+            v += turn[threadIdx.x + i * 64];
+            sum += stats[threadIdx.x + i * 64].y;
         }
     }
-    if (row >= rows) return;
-    const int64_t pair = row / a.nq, token = row - pair * a.nq, batch = pair / a.heads, head = pair - batch * a.heads;
-    if (a.lse && lane == 0) a.lse[row] = (m + log2f(sum)) * kLn2;
-    if (valid <= 0) return;
-    const float f = m == -INFINITY && sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-    for (int i = 0; i < 8; i++) v[i] *= f;
-    void *out = const_cast<void *>(a.out.p);
-    const int64_t to = batch * a.out.sb + token * a.out.sr + head * a.out.sh + lane * 8;
-    if (valid >= 8) {
-        store8_vec(out, a.type, to, v);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; i++)
-            if (i < valid) store_from_float(out, a.type, to + i, v[i]);
+    if (!works) return;
+    const Target t = target_of(a, wave, unit, lane);
+    if constexpr (SOFT) {
+        v *= m == -INFINITY && sum == 0.0f ? 0.0f : 1.0f / sum;
+        if (a.lse && t.there && unit == 0 && lane < 32) a.lse[t.stat] = (m + log2f(sum)) * kLn2;
     }
-}
-
-// to[batch][n][heads][d] = sum over splits of part [split][batch][heads][n][d]
-struct SumArgs {
-    const float *part;
-    Tensor to;
-    int64_t rows;                               // batch * heads * n
-    int n, heads, d, chunks, splits, type;
-};
-__global__ __launch_bounds__(kThreads) void sum_splits(SumArgs a)
-{
-    const int64_t i = block_of() * kThreads + threadIdx.x;
-    const int64_t row = i / a.chunks;
-    const int at = (int)(i - row * a.chunks) * 8, valid = a.d - at;
-    if (row >= a.rows) return;
-    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (int s = 0; s < a.splits; s++) {
-        float x[8];
-        load8(a.part, GS_DTYPE_F32, (s * a.rows + row) * a.d + at, valid, x);
-#pragma unroll
-        for (int j = 0; j < 8; j++) v[j] += x[j];
-    }
-    const int64_t pair = row / a.n, token = row - pair * a.n, batch = pair / a.heads, head = pair - batch * a.heads;
-    void *p = const_cast<void *>(a.to.p);
-    const int64_t to = batch * a.to.sb + token * a.to.sr + head * a.to.sh + at;
-    if (valid >= 8) {
-        store8_vec(p, a.type, to, v);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; j++)
-            if (j < valid) store_from_float(p, a.type, to + j, v[j]);
-    }
+    store4(a, t, v);
 }
 
 // ---- plan ----------------------------------------------------------------------------
@@ -245,6 +269,11 @@ void place(Plan &w, Piece &piece, const gs_attention *p, const void *t, int64_t 
     if (piece.packed) w.bytes += packed_bytes(p, rows, heads);
 }
 
+// Places of partial sums in a split, and the bytes of all.
+size_t places(const gs_attention *p, const Tiling &t) { return (size_t)p->batch * p->kv_heads * t.tiles * t.waves; }
+int padded(int d) { return (d + 31) / 32 * 32; }
+size_t part_bytes(const gs_attention *p, const Tiling &t) { return t.splits * places(p, t) * 32 * padded(p->d) * 4; }
+
 Plan plan_fwd(const gs_attention *p)
 {
     Plan w = {};
@@ -253,11 +282,10 @@ Plan plan_fwd(const gs_attention *p)
     place(w, w.k, p, p->k, p->k_batch, p->k_row, p->k_head, p->nk, p->kv_heads);
     place(w, w.v, p, p->v, p->v_batch, p->v_row, p->v_head, p->nk, p->kv_heads);
     if (w.t.splits > 1) {
-        const size_t rows = (size_t)w.t.splits * p->batch * p->heads * p->nq;
         w.part = w.bytes;
-        w.bytes += round256(rows * p->d * 4);
+        w.bytes += part_bytes(p, w.t);
         w.ml = w.bytes;
-        w.bytes += round256(rows * 8);
+        w.bytes += (size_t)w.t.splits * places(p, w.t) * 32 * 8;
     }
     return w;
 }
@@ -278,7 +306,7 @@ Plan plan_bwd(const gs_attention *p, const gs_attention_grads *g)
     if (g->dq) {
         place(w, w.k, p, p->k, p->k_batch, p->k_row, p->k_head, p->nk, p->kv_heads);
         place(w, w.v, p, p->v, p->v_batch, p->v_row, p->v_head, p->nk, p->kv_heads);
-        if (w.t.splits > 1) part = round256((size_t)w.t.splits * p->batch * p->heads * p->nq * p->d * 4);
+        if (w.t.splits > 1) part = part_bytes(p, w.t);
     }
     w.part = w.part2 = w.bytes;
     if (g->dk || g->dv) {
@@ -286,7 +314,7 @@ Plan plan_bwd(const gs_attention *p, const gs_attention_grads *g)
         place(w, w.g, p, g->dout, g->dout_batch, g->dout_row, g->dout_head, p->nq, p->heads);
         w.part = w.part2 = w.bytes;
         if (w.tkv.splits > 1) {
-            const size_t one = round256((size_t)w.tkv.splits * p->batch * p->kv_heads * p->nk * p->d * 4);
+            const size_t one = part_bytes(p, w.tkv);
             part = std::max(part, 2 * one);
             w.part2 = w.part + one;
         }
@@ -399,20 +427,26 @@ void tile(Args &a, const Tiling &t)
 {
     a.tiles = t.tiles;
     a.splits = t.splits;
-    a.blocks = (int64_t)a.batch * a.kv * t.tiles * t.splits;
+    a.waves = t.waves;
+    const int64_t pairs = (int64_t)a.batch * a.kv * t.splits, want = (64 + pairs - 1) / pairs;      // runs: 64 or more
+    a.run = (int)((t.tiles + want - 1) / want);
+    const int64_t parts = (t.tiles + a.run - 1) / a.run;
+    a.blocks = (pairs * parts + 7) / 8 * 8 * a.run;
 }
 
-template <int SL> void launch_join(const Args &a, hipStream_t s)
+// Joins the splits of what `t` tiled: `rows` rows of a pair, `group` heads of them
+// to a token, into `to`.
+hipError_t launch_join(const Args &a, const float *part, const float *ml, const Tensor &to, int rows, int group, int heads, hipStream_t s)
 {
-    const int64_t rows = (int64_t)a.batch * a.heads * a.nq;
-    constexpr int kRows = kThreads / 16 / SL;
-    join_fwd<SL><<<grid_of((rows + kRows - 1) / kRows, kThreads), kThreads, 0, s>>>(a);
-}
-
-hipError_t launch_sum(const Args &a, const float *part, const Tensor &to, int n, int heads, hipStream_t s)
-{
-    SumArgs u = {part, to, (int64_t)a.batch * heads * n, n, heads, a.d, (a.d + 7) / 8, a.splits, a.type};
-    sum_splits<<<grid_of((u.rows * u.chunks + kThreads - 1) / kThreads, kThreads), kThreads, 0, s>>>(u);
+    JoinArgs j = {part, ml, to, ml ? a.lse : nullptr, 0, 0, padded(a.d) / 8, rows, a.tiles, a.waves, group, heads, a.splits, a.d, a.type};
+    j.waves = (int64_t)a.batch * a.kv * a.tiles * a.waves;
+    j.units = j.waves * j.per;
+    const bool wide = a.splits > 8;             // four waves to a unit
+    const dim3 grid = grid_of(wide ? j.units : (j.units + 3) / 4, kThreads);
+    if (ml && wide) join_splits<4, true><<<grid, kThreads, 0, s>>>(j);
+    else if (ml) join_splits<1, true><<<grid, kThreads, 0, s>>>(j);
+    else if (wide) join_splits<4, false><<<grid, kThreads, 0, s>>>(j);
+    else join_splits<1, false><<<grid, kThreads, 0, s>>>(j);
     return hipGetLastError();
 }
 
@@ -449,12 +483,7 @@ gs_status gs_attention_fwd(const gs_attention *p, void *workspace, size_t worksp
     a.part = reinterpret_cast<float *>(ws + w.part);
     a.ml = reinterpret_cast<float *>(ws + w.ml);
     e = p->dtype == GS_DTYPE_F32 ? launch_fwd_f32(a, w.t.waves, s) : p->dtype == GS_DTYPE_F16 ? launch_fwd_f16(a, w.t.waves, s) : launch_fwd_bf16(a, w.t.waves, s);
-    if (e == hipSuccess && a.splits > 1) {
-        if (a.splits >= 32) launch_join<16>(a, s);
-        else if (a.splits >= 8) launch_join<4>(a, s);
-        else launch_join<1>(a, s);
-        e = hipGetLastError();
-    }
+    if (e == hipSuccess && a.splits > 1) e = launch_join(a, a.part, a.ml, a.out, a.rows, a.group, a.heads, s);
     return from_hip(e);
 }
 
@@ -495,7 +524,7 @@ gs_status gs_attention_bwd(const gs_attention *p, const gs_attention_grads *g, v
         tile(a, w.t);
         if (e == hipSuccess)
             e = p->dtype == GS_DTYPE_F32 ? launch_dq_f32(a, w.t.waves, s) : p->dtype == GS_DTYPE_F16 ? launch_dq_f16(a, w.t.waves, s) : launch_dq_bf16(a, w.t.waves, s);
-        if (e == hipSuccess && a.splits > 1) e = launch_sum(a, a.part, a.dq, p->nq, p->heads, s);
+        if (e == hipSuccess && a.splits > 1) e = launch_join(a, a.part, nullptr, a.dq, a.rows, a.group, a.heads, s);
     }
     if (e == hipSuccess && (g->dk || g->dv) && p->nk > 0) {
         e = operand(p, a.q, p->nq, p->heads, w.q, ws, a.qt, s);
@@ -504,8 +533,8 @@ gs_status gs_attention_bwd(const gs_attention *p, const gs_attention_grads *g, v
         if (e == hipSuccess)
             e = p->dtype == GS_DTYPE_F32 ? launch_dkv_f32(a, w.tkv.waves, s) : p->dtype == GS_DTYPE_F16 ? launch_dkv_f16(a, w.tkv.waves, s) : launch_dkv_bf16(a, w.tkv.waves, s);
         if (e == hipSuccess && a.splits > 1) {
-            if (g->dk) e = launch_sum(a, a.part, a.dk, p->nk, p->kv_heads, s);
-            if (e == hipSuccess && g->dv) e = launch_sum(a, a.part2, a.dv, p->nk, p->kv_heads, s);
+            if (g->dk) e = launch_join(a, a.part, nullptr, a.dk, p->nk, 1, a.kv, s);
+            if (e == hipSuccess && g->dv) e = launch_join(a, a.part2, nullptr, a.dv, p->nk, 1, a.kv, s);
         }
     }
     return from_hip(e);

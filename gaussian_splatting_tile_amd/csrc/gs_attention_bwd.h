@@ -124,12 +124,10 @@ template <int KIND, int NL, int DP, int NW> __global__ __launch_bounds__(NW * 64
             over_rows<KIND, NL, DP, LD::kBytes>(kt, u * 32, w, acc, lane);
         }
     }
-    if (!there) return;
     const float f = a.scale * scale.inverse() * (KIND == gemm::kF16 ? 1.0f / (float)(1 << (int)kHalfShift) : 1.0f);
     if (a.splits > 1) {
-        const int64_t p = ((int64_t)it.split * a.batch * a.heads + (int64_t)it.batch * a.heads + head) * a.nq + token;
-        store_columns<DP>(a.part, GS_DTYPE_F32, p * a.d, acc, f, a.d, lane);
-    } else {
+        store_part<DP>(a.part, part_at(a, it, wave), acc, f, lane);
+    } else if (there) {
         store_columns<DP>(const_cast<void *>(a.dq.p), a.type, it.batch * a.dq.sb + token * a.dq.sr + head * a.dq.sh, acc, f, a.d, lane);
     }
 }
@@ -227,13 +225,12 @@ template <int KIND, int NL, int DP, int NW> __global__ __launch_bounds__(NW * 64
             over_rows<KIND, NL, DP, LD::kBytes>(qt, u * 32, w, dk, lane);
         }
     }
-    if (!there) return;
     const float down = KIND == gemm::kF16 ? 1.0f / (float)(1 << (int)kHalfShift) : 1.0f, f = a.scale * scale.inverse() * down;
     if (a.splits > 1) {
-        const int64_t p = (((int64_t)it.split * a.batch * a.kv + (int64_t)it.batch * a.kv + it.head) * a.nk + key) * a.d;
-        store_columns<DP>(a.part, GS_DTYPE_F32, p, dk, f, a.d, lane);
-        store_columns<DP>(a.part2, GS_DTYPE_F32, p, dv, down, a.d, lane);
-    } else {
+        const int64_t at = part_at(a, it, wave);
+        store_part<DP>(a.part, at, dk, f, lane);
+        store_part<DP>(a.part2, at, dv, down, lane);
+    } else if (there) {
         if (a.dk.p) store_columns<DP>(const_cast<void *>(a.dk.p), a.type, it.batch * a.dk.sb + key * a.dk.sr + it.head * a.dk.sh, dk, f, a.d, lane);
         if (a.dv.p) store_columns<DP>(const_cast<void *>(a.dv.p), a.type, it.batch * a.dv.sb + key * a.dv.sr + it.head * a.dv.sh, dv, down, a.d, lane);
     }

@@ -110,20 +110,16 @@ template <int KIND, int NL, int DP, int NW> __global__ __launch_bounds__(NW * 64
     }
 
     sum = pair_sum(sum);
-    if (!there) return;
-    const int64_t at = ((int64_t)it.batch * a.heads + head) * a.nq + token;
-    if (a.splits > 1) {                         // sums as they are, for join_fwd
-        const int64_t p = (int64_t)it.split * a.batch * a.heads * a.nq + at;
-        store_columns<DP>(a.part, GS_DTYPE_F32, p * a.d, o, 1.0f, a.d, lane);
-        if (lane < 32) {
-            a.ml[2 * p] = m;
-            a.ml[2 * p + 1] = sum;
-        }
+    if (a.splits > 1) {                         // as they are, for join_fwd
+        const int64_t at = part_at(a, it, wave);
+        store_part<DP>(a.part, at, o, 1.0f, lane);
+        if (lane < 32) *reinterpret_cast<float2 *>(a.ml + (at * 32 + lane) * 2) = float2{m, sum};
         return;
     }
+    if (!there) return;
     const float f = m == -INFINITY && sum == 0.0f ? 0.0f : 1.0f / sum;
     store_columns<DP>(const_cast<void *>(a.out.p), a.type, it.batch * a.out.sb + token * a.out.sr + head * a.out.sh, o, f, a.d, lane);
-    if (a.lse && lane < 32) a.lse[at] = (m + log2f(sum)) * kLn2;
+    if (a.lse && lane < 32) a.lse[((int64_t)it.batch * a.heads + head) * a.nq + token] = (m + log2f(sum)) * kLn2;
 }
 
 template <int KIND, int NL, int DP> hipError_t launch_fwd_waves(const Args &a, int waves, hipStream_t s)
