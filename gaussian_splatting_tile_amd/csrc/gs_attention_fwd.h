@@ -7,12 +7,15 @@ namespace gsi {
 namespace attn {
 
 // Online softmax over tiles of keys.  A column's scores are the lane's and its
-// partner's registers; the maximum that is subtracted follows the true one only
-// when that has grown by more than 2^8 (a column's probabilities stay below 2^8,
-// which every type holds, and the sums fp32), so that the sums are rescaled a
-// few times a call and not once a tile.  Probabilities are rounded to the
-// operands' type for the second product (half an ulp each, unbiased); their sum
-// takes them unrounded.
+// partner's registers.  What is subtracted from them is the maximum of the first
+// tile, and a later one's only where probabilities have grown so large that a
+// tile's sum passes 2^13 (fp16 holds 2^16): then the tile is done again and the
+// sums so far are rescaled.  So the usual tile looks for no maximum.
+// Probabilities are rounded to the operands' type for the second product (half
+// an ulp each, unbiased); their sum takes them unrounded, as lse has to be good to
+// fp32.
+constexpr float kMostSum = 8192.0f;
+
 template <int KIND, int NL, int DP, int NW> __global__ __launch_bounds__(NW * 64, room_for(NL, NW)) void attention_fwd(Args a)
 {
     constexpr int KT = kTileRows<NL, DP>, KS = KT / 32;
@@ -67,7 +70,6 @@ template <int KIND, int NL, int DP, int NW> __global__ __launch_bounds__(NW * 64
         if (!seen) continue;
         const char *kt = lds + (t & 1) * kStage, *vt = kt + NL * LD::kBytes;
         f16v s[KS];
-        float top = -INFINITY;
 #pragma unroll
         for (int u = 0; u < KS; u++) {
             s[u] = over_d<KIND, NL, DP, LD::kBytes>(kt, u * 32, q, lane);
@@ -77,36 +79,46 @@ template <int KIND, int NL, int DP, int NW> __global__ __launch_bounds__(NW * 64
                 for (int i = 0; i < 16; i++)
                     if (!((bits >> ((i & 3) + 8 * (i >> 2))) & 1)) s[u][i] = -INFINITY;
             }
-#pragma unroll
-            for (int i = 0; i < 16; i++) top = fmaxf(top, s[u][i]);
         }
-        top *= a.c;
-        if (__any(top > m + 8.0f)) {
-            const float up = fmaxf(m, pair_max(top)), now = up == -INFINITY ? 0.0f : up;
-            const float f = __builtin_amdgcn_exp2f(m - now);
+        i4 w[KS][2][NL];
+        float more;                             // of this tile's probabilities
+        auto exponentials = [&]() {
+            more = 0.0f;
+#pragma unroll
+            for (int u = 0; u < KS; u++)
+#pragma unroll
+                for (int j = 0; j < 2; j++) {
+                    float v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        v[i] = __builtin_amdgcn_exp2f(fmaf(s[u][j * 8 + i], a.c, -base));
+                        more += v[i];
+                    }
+                    pack8<KIND, NL>(v, w[u][j]);
+                }
+        };
+        bool again = __any(m == -INFINITY);
+        if (!again) {
+            exponentials();
+            again = __any(!(more < kMostSum));
+        }
+        if (again) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < KS; u++)
+#pragma unroll
+                for (int i = 0; i < 16; i++) top = fmaxf(top, s[u][i]);
+            const float up = fmaxf(m, pair_max(top * a.c)), now = up == -INFINITY ? 0.0f : up, f = __builtin_amdgcn_exp2f(m - now);
             m = up;
             base = now;
             sum *= f;
 #pragma unroll
             for (int t = 0; t < DP / 32; t++) o[t] *= f;
+            exponentials();
         }
+        sum += more;
 #pragma unroll
-        for (int u = 0; u < KS; u++) {
-            i4 w[2][NL];
-#pragma unroll
-            for (int i = 0; i < 16; i++) {
-                s[u][i] = __builtin_amdgcn_exp2f(fmaf(s[u][i], a.c, -base));
-                sum += s[u][i];
-            }
-#pragma unroll
-            for (int j = 0; j < 2; j++) {
-                float v[8];
-#pragma unroll
-                for (int i = 0; i < 8; i++) v[i] = s[u][j * 8 + i];
-                pack8<KIND, NL>(v, w[j]);
-            }
-            over_rows<KIND, NL, DP, LD::kBytes>(vt, u * 32, w, o, lane);
-        }
+        for (int u = 0; u < KS; u++) over_rows<KIND, NL, DP, LD::kBytes>(vt, u * 32, w[u], o, lane);
     }
 
     sum = pair_sum(sum);
