@@ -24,8 +24,7 @@ SOURCES = ["gs_api.hip", "gs_project.hip", "gs_sort.hip", "gs_render.hip", "gs_m
            "gs_norm.hip", "gs_linear.hip", "gs_product_bf16.hip", "gs_product_f16.hip", "gs_product_f32.hip",
            "gs_product_mx8.hip", "gs_product_few.hip", "gs_muon.hip", "gs_attention.hip",
            "gs_attention_fwd_bf16.hip", "gs_attention_fwd_f16.hip", "gs_attention_fwd_f32.hip",
-           "gs_attention_dq_bf16.hip", "gs_attention_dq_f16.hip", "gs_attention_dq_f32.hip",
-           "gs_attention_dkv_bf16.hip", "gs_attention_dkv_f16.hip", "gs_attention_dkv_f32.hip",
+           "gs_attention_bwd_bf16.hip", "gs_attention_bwd_f16.hip", "gs_attention_bwd_f32.hip",
            "gs_group_norm.hip"]
 # the peak-rate microbenchmarks the roofline fractions are also taken against
 # (not part of the rasterizer's ABI)

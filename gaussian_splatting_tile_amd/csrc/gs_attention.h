@@ -39,23 +39,29 @@ struct Operand {
     int64_t sb, sr, sh, plane;
 };
 
+// How a kernel's blocks are laid out: tiles of columns of a pair (batch element and
+// head of k and v), each in `splits` of the other side's rows.
+struct Grid {
+    int tiles, splits, run, waves;              // run: tiles that stay on a die; waves of a block
+    uint32_t blocks;                            // a multiple of 8
+};
+
 struct Args {
     Tensor q, out, dout;                        // read as they are, row by row
     Operand k, v, qt, dot;                      // read in tiles
     Tensor kt, vt;                              // k and v row by row (gradients)
     Tensor dq, dk, dv;                          // results
+    Grid t, tk;                                 // of the forward or of dq, and of dk and dv
     float *lse;                                 // [batch][heads][nq], or NULL
     const float *lse2, *delta;                  // backward: [batch][heads][nq_pad]
-    // of splits, as the waves hold them: sums [split][wave][DP / 8][64][4] and (forward)
-    // maxima and sums of exponentials [split][wave][32][2], wave = (pair * tiles + tile) * waves + wave
-    float *part, *part2, *ml;
+    // of splits, as the waves hold them: sums [split][wave][DP / 8][64][4] of out or dq, of
+    // dk and of dv, and (forward) maxima and sums of exponentials [split][wave][32][2];
+    // wave = (pair * tiles + tile) * waves + wave of the block
+    float *part, *part_k, *part_v, *ml;
     const int32_t *lengths;
     const uint8_t *mask;
     int64_t mask_stride;
     int batch, heads, kv, group, nq, nk, nq_pad, d, rows;       // rows = nq * group
-    int tiles, splits, run;                     // blocks along the wave columns; splits of the other side; tiles of a run
-    int64_t blocks;
-    int waves;                                  // of a block
     int type;                                   // gs_dtype of the tensors
     float c, scale;                             // scale * log2 e, scale
 };
@@ -108,7 +114,7 @@ template <int NL, int DP> constexpr int kTileRows = NL > 1 && DP > 32 ? 32 : 64;
 
 // Waves on a SIMD that the register budget leaves room for: the limbs of fp32 and
 // single waves (more loads each) take what there is.
-constexpr int room_for(int limbs, int waves) { return limbs > 1 || waves == 1 ? 1 : 2; }
+constexpr int room_for(int limbs, int waves, int most) { return limbs > 1 || waves == 1 ? 1 : most; }
 
 // Loads of a tile of ROWS rows of one operand, straight into LDS.
 template <int DP, int ROWS, int THREADS> struct Loader {
@@ -315,22 +321,21 @@ __device__ __forceinline__ int length_of(const Args &a, int batch)
 struct Item {
     int batch, head, split, tile;               // head: of k and v
 };
-__device__ __forceinline__ bool item_of(const Args &a, Item &it)
+__device__ __forceinline__ bool item_of(const Args &a, const Grid &g, uint32_t b, Item &it)
 {
-    const uint32_t b = (uint32_t)block_of(), at = b >> 3;                   // under 2^31 blocks
-    const uint32_t run = at / (uint32_t)a.run * 8 + (b & 7), parts = ((uint32_t)a.tiles + a.run - 1) / a.run;
-    const uint32_t pair = run / parts, group = pair / (uint32_t)a.splits;
-    it.tile = (int)(run - pair * parts) * a.run + (int)(at % a.run);
-    it.split = (int)(pair - group * a.splits);
+    const uint32_t at = b >> 3, run = at / (uint32_t)g.run * 8 + (b & 7), parts = ((uint32_t)g.tiles + g.run - 1) / g.run;
+    const uint32_t pair = run / parts, group = pair / (uint32_t)g.splits;
+    it.tile = (int)((run - pair * parts) * g.run + at % g.run);
+    it.split = (int)(pair - group * g.splits);
     it.batch = (int)(group / (uint32_t)a.kv);
     it.head = (int)(group - (uint32_t)it.batch * a.kv);
-    return it.batch < a.batch && it.tile < a.tiles;
+    return it.batch < a.batch && it.tile < g.tiles;
 }
 // The wave's place among the partial sums.
-__device__ __forceinline__ int64_t part_at(const Args &a, const Item &it, int wave)
+__device__ __forceinline__ int64_t part_at(const Args &a, const Grid &g, const Item &it, int wave)
 {
     const int64_t pairs = (int64_t)a.batch * a.kv;
-    return ((it.split * pairs + (int64_t)it.batch * a.kv + it.head) * a.tiles + it.tile) * a.waves + wave;
+    return ((it.split * pairs + (int64_t)it.batch * a.kv + it.head) * g.tiles + it.tile) * g.waves + wave;
 }
 
 }  // namespace attn

@@ -11,103 +11,126 @@
 namespace gsi {
 namespace attn {
 
-hipError_t launch_fwd_bf16(const Args &, int, hipStream_t);
-hipError_t launch_fwd_f16(const Args &, int, hipStream_t);
-hipError_t launch_fwd_f32(const Args &, int, hipStream_t);
-hipError_t launch_dq_bf16(const Args &, int, hipStream_t);
-hipError_t launch_dq_f16(const Args &, int, hipStream_t);
-hipError_t launch_dq_f32(const Args &, int, hipStream_t);
-hipError_t launch_dkv_bf16(const Args &, int, hipStream_t);
-hipError_t launch_dkv_f16(const Args &, int, hipStream_t);
-hipError_t launch_dkv_f32(const Args &, int, hipStream_t);
+hipError_t launch_fwd_bf16(const Args &, hipStream_t);
+hipError_t launch_fwd_f16(const Args &, hipStream_t);
+hipError_t launch_fwd_f32(const Args &, hipStream_t);
+hipError_t launch_bwd_bf16(const Args &, int, hipStream_t);
+hipError_t launch_bwd_f16(const Args &, int, hipStream_t);
+hipError_t launch_bwd_f32(const Args &, int, hipStream_t);
 
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxD = 128;
+constexpr int kCus = 256;
 
 gs_status from_hip(hipError_t e) { return e == hipSuccess ? GS_OK : GS_ERR_HIP; }
 bool aligned_to(const void *p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
 constexpr size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// ---- packed operands ------------------------------------------------------------
-// [limb][batch][heads][n][dp] of 16 bits from a tensor of any strides, d padded
-// with zeros to a multiple of 8; fp32 in three limbs.
-struct PackArgs {
+// ---- what comes before the products ---------------------------------------------
+// One launch for up to four packed operands and the backward's row statistics; a
+// row is 2^lanes lanes', eight values each.
+struct PackJob {                                // [limb][batch][heads][n][dp] of 16 bits from any strides
     Tensor from;
     char *to;
     int64_t plane;                              // values of a limb
-    int n, heads, pairs, d, chunks, type;       // pairs: batch * heads; chunks: of 8 values in a row
+    int n, heads;
+    uint32_t first, per;                        // first block; blocks of a batch element and head
 };
-template <int NL> __global__ __launch_bounds__(kThreads) void pack(PackArgs a)
+struct Prepare {
+    PackJob jobs[4];
+    int count, d, chunks, lanes, type;          // chunks: of eight values in a packed row
+    // statistics: delta = dout . out, and lse in units of log 2 with what keeps P
+    // of an empty or absent row at 0
+    Tensor out, dout;
+    const float *lse;
+    float *lse2, *delta;
+    float shift;
+    int nq, nq_pad, heads;
+    uint32_t first, per, blocks;                // blocks: of the launch
+};
+
+template <int NL> __device__ __forceinline__ void pack_row(const Prepare &a, const PackJob &job, uint32_t block)
 {
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (i >= (int64_t)a.n * a.chunks) return;
-    const int row = (int)(i / a.chunks), at = (int)(i - (int64_t)row * a.chunks) * 8;
-    for (int pair = blockIdx.y; pair < a.pairs; pair += gridDim.y) {
-        const int batch = pair / a.heads, head = pair - batch * a.heads;
-        const int64_t from = batch * a.from.sb + row * a.from.sr + head * a.from.sh + at;
-        const int64_t to = (((int64_t)pair * a.n + row) * a.chunks) * 8 + at;
-        const int valid = min(8, a.d - at);
-        if constexpr (NL > 1) {
-            float v[8];
-            load8(a.from.p, GS_DTYPE_F32, from, valid, v);
-            Vec<uint16_t, 8> w[NL];
-            split_all<NL, 8>(v, w);
+    const uint32_t pair = block / job.per;
+    const int at = (int)(threadIdx.x & ((1u << a.lanes) - 1)) * 8;
+    const int64_t row = (int64_t)(block - pair * job.per) * (kThreads >> a.lanes) + (threadIdx.x >> a.lanes);
+    if (row >= job.n || at >= a.chunks * 8) return;
+    const uint32_t batch = pair / (uint32_t)job.heads, head = pair - batch * job.heads;
+    const int64_t from = batch * job.from.sb + row * job.from.sr + head * job.from.sh + at;
+    const int64_t to = ((int64_t)pair * job.n + row) * a.chunks * 8 + at;
+    const int valid = min(8, a.d - at);
+    if constexpr (NL > 1) {
+        float v[8];
+        load8(job.from.p, GS_DTYPE_F32, from, valid, v);
+        Vec<uint16_t, 8> w[NL];
+        split_all<NL, 8>(v, w);
 #pragma unroll
-            for (int l = 0; l < NL; l++) *reinterpret_cast<Vec<uint16_t, 8> *>(a.to + (l * a.plane + to) * 2) = w[l];
-        } else {
-            Vec<uint16_t, 8> w = {{0, 0, 0, 0, 0, 0, 0, 0}};
-            const uint16_t *p = static_cast<const uint16_t *>(a.from.p) + from;
-            if (valid == 8) w = *reinterpret_cast<const Vec<uint16_t, 8> *>(p);
-            else
+        for (int l = 0; l < NL; l++) *reinterpret_cast<Vec<uint16_t, 8> *>(job.to + (l * job.plane + to) * 2) = w[l];
+    } else {
+        Vec<uint16_t, 8> w = {{0, 0, 0, 0, 0, 0, 0, 0}};
+        const uint16_t *p = static_cast<const uint16_t *>(job.from.p) + from;
+        if (valid == 8) w = *reinterpret_cast<const Vec<uint16_t, 8> *>(p);
+        else
 #pragma unroll
-                for (int j = 0; j < 8; j++)
-                    if (j < valid) w.v[j] = p[j];
-            *reinterpret_cast<Vec<uint16_t, 8> *>(a.to + to * 2) = w;
-        }
+            for (int j = 0; j < 8; j++)
+                if (j < valid) w.v[j] = p[j];
+        *reinterpret_cast<Vec<uint16_t, 8> *>(job.to + to * 2) = w;
     }
 }
 
-// ---- row statistics of the backward ------------------------------------------------
-// delta = dout . out, and lse in units of log 2 with what keeps P of an empty or
-// absent row at 0; 16 lanes a row.
-__global__ __launch_bounds__(kThreads) void row_statistics(Args a, float *lse2, float *delta, float shift)
+__global__ __launch_bounds__(kThreads) void prepare(Prepare a)
 {
-    const int lane = threadIdx.x & 15;
-    const int64_t token = (int64_t)blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4);
-    if (token >= a.nq_pad) return;
-    const int pairs = a.batch * a.heads;
-    for (int pair = blockIdx.y; pair < pairs; pair += gridDim.y) {
-        const int batch = pair / a.heads, head = pair - batch * a.heads;
-        float dot = 0.0f;
-        if (token < a.nq && lane * 8 < a.d) {
-            float x[8], y[8];
-            load8(a.out.p, a.type, batch * a.out.sb + token * a.out.sr + head * a.out.sh + lane * 8, a.d - lane * 8, x);
-            load8(a.dout.p, a.type, batch * a.dout.sb + token * a.dout.sr + head * a.dout.sh + lane * 8, a.d - lane * 8, y);
+    uint32_t b = (uint32_t)block_of();
+    if (b < a.first) {
+        int k = 0;
 #pragma unroll
-            for (int i = 0; i < 8; i++) dot = fmaf(x[i], y[i], dot);
-        }
+        for (int i = 1; i < 4; i++)
+            if (i < a.count && b >= a.jobs[i].first) k = i;
+        const PackJob &job = a.jobs[k];
+        if (a.type == GS_DTYPE_F32) pack_row<3>(a, job, b - job.first);
+        else pack_row<1>(a, job, b - job.first);
+        return;
+    }
+    b -= a.first;
+    if (!a.per) return;
+    const uint32_t pair = b / a.per;
+    const int64_t token = (int64_t)(b - pair * a.per) * (kThreads >> a.lanes) + (threadIdx.x >> a.lanes);
+    const uint32_t batch = pair / (uint32_t)a.heads, head = pair - batch * a.heads;
+    if (token >= a.nq_pad || a.first + b >= a.blocks) return;
+    const int at = (int)(threadIdx.x & ((1u << a.lanes) - 1)) * 8;
+    float dot = 0.0f;
+    if (token < a.nq && at < a.d) {
+        float x[8], y[8];
+        load8(a.out.p, a.type, batch * a.out.sb + token * a.out.sr + head * a.out.sh + at, a.d - at, x);
+        load8(a.dout.p, a.type, batch * a.dout.sb + token * a.dout.sr + head * a.dout.sh + at, a.d - at, y);
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) dot += __shfl_xor(dot, o);
-        if (lane == 0) {
-            const float l = token < a.nq ? a.lse[(int64_t)pair * a.nq + token] : -INFINITY;
-            const int64_t at = (int64_t)pair * a.nq_pad + token;
-            lse2[at] = l == -INFINITY ? INFINITY : fmaf(l, kLog2e, -shift);
-            delta[at] = dot;
-        }
+        for (int i = 0; i < 8; i++) dot = fmaf(x[i], y[i], dot);
+    }
+    for (int o = 1 << a.lanes >> 1; o > 0; o >>= 1) dot += __shfl_xor(dot, o);
+    if (at == 0) {
+        const float l = token < a.nq ? a.lse[(int64_t)pair * a.nq + token] : -INFINITY;
+        const int64_t to = (int64_t)pair * a.nq_pad + token;
+        a.lse2[to] = l == -INFINITY ? INFINITY : fmaf(l, kLog2e, -a.shift);
+        a.delta[to] = dot;
     }
 }
 
 // ---- splits -----------------------------------------------------------------------
 // A unit is 16 bytes a lane of the 64 lanes that hold 32 rows' sums; its SW waves
 // take every SW-th split, the first of them adds theirs, in order.
-struct JoinArgs {
+struct JoinJob {
     const float *part, *ml;
     Tensor to;
     float *lse;
-    int64_t waves, units;                       // waves' places in a split, units = waves * per
-    int per, rows, tiles, wide, group, heads, splits, d, type;      // per: units of a wave; wide: waves of a block; rows: of a pair
+    int64_t waves, first;                       // waves' places in a split; first unit
+    int rows, tiles, wide, group, heads, splits;        // rows of a pair; wide: waves of a block
+};
+struct JoinArgs {
+    JoinJob jobs[3];
+    int64_t units;                              // of all jobs
+    int count, per, d, type;                    // per: units of a wave
 };
 // Where a unit's lane writes: its row's place in the tensor, or not.
 struct Target {
@@ -115,7 +138,7 @@ struct Target {
     int at;                                     // first of four d
     int64_t row, stat;                          // elements; index into lse
 };
-__device__ __forceinline__ Target target_of(const JoinArgs &a, int64_t wave, int unit, int lane)
+__device__ __forceinline__ Target target_of(const JoinJob &a, int64_t wave, int unit, int lane)
 {
     const int64_t tile = wave / a.wide, pair = tile / a.tiles;
     const int row = (int)((tile - pair * a.tiles) * a.wide + (wave - tile * a.wide)) * 32 + (lane & 31);
@@ -129,9 +152,9 @@ __device__ __forceinline__ Target target_of(const JoinArgs &a, int64_t wave, int
     t.stat = (batch * a.heads + head) * (a.rows / a.group) + token;
     return t;
 }
-__device__ __forceinline__ void store4(const JoinArgs &a, const Target &t, const gemm::f4 &v)
+__device__ __forceinline__ void store4(const JoinArgs &a, const Tensor &tensor, const Target &t, const gemm::f4 &v)
 {
-    void *to = const_cast<void *>(a.to.p);
+    void *to = const_cast<void *>(tensor.p);
     if (!t.there) return;
     if (t.at + 4 <= a.d) {
         const int64_t i = t.row + t.at;
@@ -154,11 +177,16 @@ template <int SW, bool SOFT> __global__ __launch_bounds__(kThreads) void join_sp
     const int lane = threadIdx.x & 63, sub = (threadIdx.x >> 6) % SW;
     const int64_t u = block_of() * kUnits + (threadIdx.x >> 6) / SW;
     const bool works = u < a.units;
-    const int64_t wave = works ? u / a.per : 0;
-    const int unit = works ? (int)(u - wave * a.per) : 0, splits = works ? a.splits : 0;
-    const gemm::f4 *part = reinterpret_cast<const gemm::f4 *>(a.part) + (wave * a.per + unit) * 64 + lane;
-    const float2 *ml = reinterpret_cast<const float2 *>(a.ml) + wave * 32 + (lane & 31);
-    const int64_t next = a.waves * a.per * 64, next_ml = a.waves * 32;
+    int k = 0;
+#pragma unroll
+    for (int i = 1; i < 3; i++)
+        if (i < a.count && u >= a.jobs[i].first) k = i;
+    const JoinJob &job = a.jobs[__builtin_amdgcn_readfirstlane(k)];         // a wave is of one unit
+    const int64_t wave = works ? (u - job.first) / a.per : 0;
+    const int unit = works ? (int)(u - job.first - wave * a.per) : 0, splits = works ? job.splits : 0;
+    const gemm::f4 *part = reinterpret_cast<const gemm::f4 *>(job.part) + (wave * a.per + unit) * 64 + lane;
+    const float2 *ml = reinterpret_cast<const float2 *>(job.ml) + wave * 32 + (lane & 31);
+    const int64_t next = job.waves * a.per * 64, next_ml = job.waves * 32;
     gemm::f4 v = {0, 0, 0, 0};
     float sum = 0.0f, m = -INFINITY, base = 0.0f;
     if constexpr (SOFT) {
@@ -212,27 +240,71 @@ template <int SW, bool SOFT> __global__ __launch_bounds__(kThreads) void join_sp
         }
     }
     if (!works) return;
-    const Target t = target_of(a, wave, unit, lane);
+    const Target t = target_of(job, wave, unit, lane);
     if constexpr (SOFT) {
         v *= m == -INFINITY && sum == 0.0f ? 0.0f : 1.0f / sum;
-        if (a.lse && t.there && unit == 0 && lane < 32) a.lse[t.stat] = (m + log2f(sum)) * kLn2;
+        if (job.lse && t.there && unit == 0 && lane < 32) job.lse[t.stat] = (m + log2f(sum)) * kLn2;
     }
-    store4(a, t, v);
+    store4(a, job.to, t, v);
 }
 
 // ---- plan ----------------------------------------------------------------------------
 struct Tiling {
     int waves, tiles, splits;
 };
-// Waves of a block, blocks along the columns, and splits of the `other` tiles
-// where the blocks alone would not fill the card.
-Tiling tile_columns(int64_t columns, int64_t pairs, int64_t other)
+// Time of one tile of the other side's rows on a CU that holds one block, and per
+// tile where it holds two or more (us; blocks of four waves; 64 rows, or 32 of fp32
+// above d = 32), and how many it holds.
+struct Cost {
+    double alone, shared;
+    int hold;
+};
+enum Product { kForward, kQueries, kStates };
+
+Cost cost_of(const gs_attention *p, Product what)
+{
+    static const Cost h[3][4] = {{{0.75, 0.45, 4}, {0.95, 0.65, 4}, {1.25, 0.85, 2}, {1.45, 1.06, 2}},
+                                 {{1.0, 0.7, 4}, {1.28, 0.97, 2}, {1.8, 1.3, 2}, {2.1, 1.6, 2}},
+                                 {{1.3, 0.9, 3}, {1.8, 1.3, 2}, {2.5, 1.9, 2}, {3.0, 2.4, 2}}};
+    static const Cost f[3][4] = {{{2.4, 2.0, 2}, {1.9, 1.45, 2}, {2.5, 2.5, 1}, {3.05, 3.05, 1}},
+                                 {{3.2, 2.7, 2}, {2.6, 2.1, 2}, {3.6, 3.6, 1}, {4.5, 4.5, 1}},
+                                 {{4.2, 3.7, 2}, {3.5, 3.5, 1}, {4.8, 4.8, 1}, {6.2, 6.2, 1}}};
+    const int i = p->d <= 32 ? 0 : p->d <= 64 ? 1 : p->d <= 96 ? 2 : 3;
+    return p->dtype == GS_DTYPE_F32 ? f[what][i] : h[what][i];
+}
+
+int padded(int d) { return (d + 31) / 32 * 32; }
+
+// Waves of a block, blocks along the columns, and splits of the `other` side's tiles
+// where the blocks alone would not fill the card: the number with the least
+// estimated time of rounds of blocks, and of writing and joining partial sums.
+Tiling tile_columns(const gs_attention *p, Product what, int64_t columns, int64_t pairs, int64_t other, int cus)
 {
     Tiling t;
     t.waves = columns <= 32 ? 1 : 4;
     t.tiles = (int)((columns + t.waves * 32 - 1) / (t.waves * 32));
-    const int64_t blocks = std::max<int64_t>(1, pairs * t.tiles), target = t.waves == 1 ? 1024 : 512;
-    t.splits = (int)std::max<int64_t>(1, std::min<int64_t>({target / blocks, other / 2, 256}));
+    t.splits = 1;
+    const int64_t blocks = std::max<int64_t>(1, pairs * t.tiles);
+    const Cost c = cost_of(p, what);
+    const int results = what == kStates ? 2 : 1;
+    // single waves: a block is a quarter of one of four waves and hides less
+    const double alone = t.waves == 1 ? 1.2 : c.alone, shared = t.waves == 1 ? c.shared / 4 : c.shared;
+    const int hold = t.waves == 1 ? 4 : c.hold;
+    double best = 0;
+    for (int64_t want = 1; want <= std::min<int64_t>(other, 256); want += want < 8 ? 1 : want / 4) {
+        const int64_t per = (other + want - 1) / want, s = (other + per - 1) / per;
+        if (s > 1 && blocks * s > 4096) break;
+        const int64_t all = blocks * s, most = (all + cus - 1) / cus;
+        // the CU with the most blocks: full rounds of `hold`, and what is left
+        const int64_t left = most % hold;
+        const double round = std::max(alone, shared * hold), last = left ? std::max(alone, shared * left) : 0.0;
+        double time = (most / hold * round + last) * per + 2.0;
+        if (s > 1) time += 3.5 + 0.03 * s + (double)all * t.waves * 32 * padded(p->d) * 4 * 2 * results / 7e6;
+        if (best == 0 || time < best) {
+            best = time;
+            t.splits = (int)s;
+        }
+    }
     return t;
 }
 
@@ -251,9 +323,9 @@ struct Piece {                                  // an operand of the tiles: in p
 };
 struct Plan {
     Tiling t;                                   // of the forward, or of dq
-    Tiling tkv;
+    Tiling tk;
     Piece k, v, q, g;
-    size_t lse2, delta, part, part2, ml, bytes;
+    size_t lse2, delta, part, part_k, part_v, ml, bytes;
     int nq_pad;
 };
 
@@ -271,14 +343,13 @@ void place(Plan &w, Piece &piece, const gs_attention *p, const void *t, int64_t 
 
 // Places of partial sums in a split, and the bytes of all.
 size_t places(const gs_attention *p, const Tiling &t) { return (size_t)p->batch * p->kv_heads * t.tiles * t.waves; }
-int padded(int d) { return (d + 31) / 32 * 32; }
 size_t part_bytes(const gs_attention *p, const Tiling &t) { return t.splits * places(p, t) * 32 * padded(p->d) * 4; }
 
 Plan plan_fwd(const gs_attention *p)
 {
     Plan w = {};
     const int kt = tile_rows(p);
-    w.t = tile_columns((int64_t)p->nq * (p->heads / p->kv_heads), (int64_t)p->batch * p->kv_heads, (p->nk + kt - 1) / kt);
+    w.t = tile_columns(p, kForward, (int64_t)p->nq * (p->heads / p->kv_heads), (int64_t)p->batch * p->kv_heads, (p->nk + kt - 1) / kt, kCus);
     place(w, w.k, p, p->k, p->k_batch, p->k_row, p->k_head, p->nk, p->kv_heads);
     place(w, w.v, p, p->v, p->v_batch, p->v_row, p->v_head, p->nk, p->kv_heads);
     if (w.t.splits > 1) {
@@ -296,30 +367,28 @@ Plan plan_bwd(const gs_attention *p, const gs_attention_grads *g)
     const int kt = tile_rows(p), group = p->heads / p->kv_heads;
     const int64_t pairs = (int64_t)p->batch * p->kv_heads;
     w.nq_pad = (p->nq + 63) / 64 * 64;
-    w.t = tile_columns((int64_t)p->nq * group, pairs, (p->nk + kt - 1) / kt);
-    w.tkv = tile_columns(p->nk, pairs, (int64_t)(p->nq + kt - 1) / kt * group);
-    w.lse2 = 0;
     const size_t stat = round256((size_t)p->batch * p->heads * w.nq_pad * 4);
     w.delta = stat;
     w.bytes = 2 * stat;
-    size_t part = 0;
-    if (g->dq) {
+    const bool queries = g->dq && p->nq > 0, states = (g->dk || g->dv) && p->nk > 0;
+    const int cus = queries && states ? kCus / 2 : kCus;                // the two kinds of blocks share the card
+    if (queries) {
+        w.t = tile_columns(p, kQueries, (int64_t)p->nq * group, pairs, (p->nk + kt - 1) / kt, cus);
         place(w, w.k, p, p->k, p->k_batch, p->k_row, p->k_head, p->nk, p->kv_heads);
         place(w, w.v, p, p->v, p->v_batch, p->v_row, p->v_head, p->nk, p->kv_heads);
-        if (w.t.splits > 1) part = part_bytes(p, w.t);
+        w.part = w.bytes;
+        if (w.t.splits > 1) w.bytes += part_bytes(p, w.t);
     }
-    w.part = w.part2 = w.bytes;
-    if (g->dk || g->dv) {
+    if (states) {
+        w.tk = tile_columns(p, kStates, p->nk, pairs, (int64_t)(p->nq + kt - 1) / kt * group, cus);
         place(w, w.q, p, p->q, p->q_batch, p->q_row, p->q_head, p->nq, p->heads);
         place(w, w.g, p, g->dout, g->dout_batch, g->dout_row, g->dout_head, p->nq, p->heads);
-        w.part = w.part2 = w.bytes;
-        if (w.tkv.splits > 1) {
-            const size_t one = part_bytes(p, w.tkv);
-            part = std::max(part, 2 * one);
-            w.part2 = w.part + one;
+        w.part_k = w.part_v = w.bytes;
+        if (w.tk.splits > 1) {
+            w.part_v += part_bytes(p, w.tk);
+            w.bytes += 2 * part_bytes(p, w.tk);
         }
     }
-    w.bytes += part;
     return w;
 }
 
@@ -358,7 +427,7 @@ gs_status check(const gs_attention *p)
     if (p->batch > 0 && p->nk > 0 && (!p->k || !p->v)) return GS_ERR_INVALID_ARG;
     if (p->batch > 0 && p->nq > 0 && (!p->q || !p->out)) return GS_ERR_INVALID_ARG;
     if (p->d > kMaxD || (int64_t)p->nq * (p->heads / p->kv_heads) > (1 << 30)) return GS_ERR_UNSUPPORTED;
-    if ((int64_t)p->batch * p->heads * std::max(p->nq, p->nk) > ((int64_t)1 << 40)) return GS_ERR_UNSUPPORTED;
+    if ((int64_t)p->batch * p->heads * std::max(std::max(p->nq, p->nk), 32) > ((int64_t)1 << 33)) return GS_ERR_UNSUPPORTED;   // block numbers have 32 bits
     return GS_OK;
 }
 
@@ -406,45 +475,61 @@ Args args_of(const gs_attention *p)
     return a;
 }
 
-// The operand as the tiles are loaded, packed first where it has to be.
-hipError_t operand(const gs_attention *p, const Tensor &t, int rows, int heads, const Piece &piece, char *ws, Operand &o, hipStream_t s)
+// The operand as the tiles are loaded, with its packing among the jobs where it
+// has to be packed first.
+Operand operand(const gs_attention *p, const Tensor &t, int rows, int heads, const Piece &piece, char *ws, Prepare &pre)
 {
-    if (!piece.packed) {
-        o = {static_cast<const char *>(t.p), t.sb * 2, t.sr * 2, t.sh * 2, 0};
-        return hipSuccess;
-    }
-    const int dp = (p->d + 7) / 8 * 8;
-    const int64_t row = dp * 2, plane = (int64_t)p->batch * heads * rows * row;
-    o = {ws + piece.at, heads * (int64_t)rows * row, row, (int64_t)rows * row, plane};
-    PackArgs a = {t, ws + piece.at, plane / 2, rows, heads, p->batch * heads, p->d, dp / 8, p->dtype};
-    const dim3 grid((unsigned)(((int64_t)rows * a.chunks + kThreads - 1) / kThreads), (unsigned)std::min(a.pairs, 65535));
-    if (p->dtype == GS_DTYPE_F32) pack<3><<<grid, kThreads, 0, s>>>(a);
-    else pack<1><<<grid, kThreads, 0, s>>>(a);
+    if (!piece.packed) return {static_cast<const char *>(t.p), t.sb * 2, t.sr * 2, t.sh * 2, 0};
+    const int64_t row = pre.chunks * 16, plane = (int64_t)p->batch * heads * rows * row, lines = kThreads >> pre.lanes;
+    PackJob &job = pre.jobs[pre.count++];
+    job = {t, ws + piece.at, plane / 2, rows, heads, pre.blocks, (uint32_t)((rows + lines - 1) / lines)};
+    pre.blocks += job.per * (uint32_t)(p->batch * heads);
+    pre.first = pre.blocks;
+    return {ws + piece.at, heads * (int64_t)rows * row, row, (int64_t)rows * row, plane};
+}
+Prepare prepare_of(const gs_attention *p)
+{
+    Prepare pre = {};
+    pre.d = p->d;
+    pre.type = p->dtype;
+    pre.chunks = (p->d + 7) / 8;
+    while ((1 << pre.lanes) < pre.chunks) pre.lanes++;
+    pre.heads = p->heads;
+    return pre;
+}
+hipError_t launch_prepare(const Prepare &pre, hipStream_t s)
+{
+    if (!pre.blocks) return hipSuccess;
+    prepare<<<grid_of(pre.blocks, kThreads), kThreads, 0, s>>>(pre);
     return hipGetLastError();
 }
 
-void tile(Args &a, const Tiling &t)
+Grid grid_for(const gs_attention *p, const Tiling &t)
 {
-    a.tiles = t.tiles;
-    a.splits = t.splits;
-    a.waves = t.waves;
-    const int64_t pairs = (int64_t)a.batch * a.kv * t.splits, want = (64 + pairs - 1) / pairs;      // runs: 64 or more
-    a.run = (int)((t.tiles + want - 1) / want);
-    const int64_t parts = (t.tiles + a.run - 1) / a.run;
-    a.blocks = (pairs * parts + 7) / 8 * 8 * a.run;
+    const int64_t pairs = (int64_t)p->batch * p->kv_heads * t.splits, want = (64 + pairs - 1) / pairs;       // runs: 64 or more
+    Grid g = {t.tiles, t.splits, (int)((t.tiles + want - 1) / want), t.waves, 0};
+    const int64_t parts = (t.tiles + g.run - 1) / g.run;
+    g.blocks = (uint32_t)((pairs * parts + 7) / 8 * 8 * g.run);
+    return g;
 }
 
-// Joins the splits of what `t` tiled: `rows` rows of a pair, `group` heads of them
-// to a token, into `to`.
-hipError_t launch_join(const Args &a, const float *part, const float *ml, const Tensor &to, int rows, int group, int heads, hipStream_t s)
+// Adds the join of what `g` laid out to the jobs: `rows` rows of a pair, `group` heads
+// of them to a token, into `to`.
+void add_join(JoinArgs &j, const Args &a, const Grid &g, const float *part, const float *ml, const Tensor &to, int rows, int group, int heads)
 {
-    JoinArgs j = {part, ml, to, ml ? a.lse : nullptr, 0, 0, padded(a.d) / 8, rows, a.tiles, a.waves, group, heads, a.splits, a.d, a.type};
-    j.waves = (int64_t)a.batch * a.kv * a.tiles * a.waves;
-    j.units = j.waves * j.per;
-    const bool wide = a.splits > 8;             // four waves to a unit
+    if (g.splits <= 1 || !to.p) return;
+    JoinJob &job = j.jobs[j.count++];
+    job = {part, ml, to, ml ? a.lse : nullptr, (int64_t)a.batch * a.kv * g.tiles * g.waves, j.units, rows, g.tiles, g.waves, group, heads, g.splits};
+    j.units += job.waves * j.per;
+}
+hipError_t launch_join(const JoinArgs &j, bool soft, hipStream_t s)
+{
+    if (!j.count) return hipSuccess;
+    bool wide = false;                          // four waves to a unit
+    for (int i = 0; i < j.count; i++) wide = wide || j.jobs[i].splits > 8;
     const dim3 grid = grid_of(wide ? j.units : (j.units + 3) / 4, kThreads);
-    if (ml && wide) join_splits<4, true><<<grid, kThreads, 0, s>>>(j);
-    else if (ml) join_splits<1, true><<<grid, kThreads, 0, s>>>(j);
+    if (soft && wide) join_splits<4, true><<<grid, kThreads, 0, s>>>(j);
+    else if (soft) join_splits<1, true><<<grid, kThreads, 0, s>>>(j);
     else if (wide) join_splits<4, false><<<grid, kThreads, 0, s>>>(j);
     else join_splits<1, false><<<grid, kThreads, 0, s>>>(j);
     return hipGetLastError();
@@ -476,14 +561,20 @@ gs_status gs_attention_fwd(const gs_attention *p, void *workspace, size_t worksp
     hipStream_t s = (hipStream_t)stream;
     char *ws = static_cast<char *>(workspace);
     Args a = args_of(p);
-    hipError_t e = operand(p, a.kt, p->nk, p->kv_heads, w.k, ws, a.k, s);
-    if (e == hipSuccess) e = operand(p, a.vt, p->nk, p->kv_heads, w.v, ws, a.v, s);
-    if (e != hipSuccess) return from_hip(e);
-    tile(a, w.t);
+    Prepare pre = prepare_of(p);
+    a.k = operand(p, a.kt, p->nk, p->kv_heads, w.k, ws, pre);
+    a.v = operand(p, a.vt, p->nk, p->kv_heads, w.v, ws, pre);
+    a.t = grid_for(p, w.t);
     a.part = reinterpret_cast<float *>(ws + w.part);
     a.ml = reinterpret_cast<float *>(ws + w.ml);
-    e = p->dtype == GS_DTYPE_F32 ? launch_fwd_f32(a, w.t.waves, s) : p->dtype == GS_DTYPE_F16 ? launch_fwd_f16(a, w.t.waves, s) : launch_fwd_bf16(a, w.t.waves, s);
-    if (e == hipSuccess && a.splits > 1) e = launch_join(a, a.part, a.ml, a.out, a.rows, a.group, a.heads, s);
+    JoinArgs j = {};
+    j.per = padded(p->d) / 8;
+    j.d = p->d;
+    j.type = p->dtype;
+    add_join(j, a, a.t, a.part, a.ml, a.out, a.rows, a.group, a.heads);
+    hipError_t e = launch_prepare(pre, s);
+    if (e == hipSuccess) e = p->dtype == GS_DTYPE_F32 ? launch_fwd_f32(a, s) : p->dtype == GS_DTYPE_F16 ? launch_fwd_f16(a, s) : launch_fwd_bf16(a, s);
+    if (e == hipSuccess) e = launch_join(j, true, s);
     return from_hip(e);
 }
 
@@ -510,33 +601,54 @@ gs_status gs_attention_bwd(const gs_attention *p, const gs_attention_grads *g, v
     a.lse2 = reinterpret_cast<float *>(ws + w.lse2);
     a.delta = reinterpret_cast<float *>(ws + w.delta);
     a.part = reinterpret_cast<float *>(ws + w.part);
-    a.part2 = reinterpret_cast<float *>(ws + w.part2);
-    hipError_t e = hipSuccess;
+    a.part_k = reinterpret_cast<float *>(ws + w.part_k);
+    a.part_v = reinterpret_cast<float *>(ws + w.part_v);
+    Prepare pre = prepare_of(p);
+    JoinArgs j = {};
+    j.per = padded(p->d) / 8;
+    j.d = p->d;
+    j.type = p->dtype;
+    if (w.t.waves) {
+        a.k = operand(p, a.kt, p->nk, p->kv_heads, w.k, ws, pre);
+        a.v = operand(p, a.vt, p->nk, p->kv_heads, w.v, ws, pre);
+        a.t = grid_for(p, w.t);
+        add_join(j, a, a.t, a.part, nullptr, a.dq, a.rows, a.group, a.heads);
+    }
+    if (w.tk.waves) {
+        a.qt = operand(p, a.q, p->nq, p->heads, w.q, ws, pre);
+        a.dot = operand(p, a.dout, p->nq, p->heads, w.g, ws, pre);
+        a.tk = grid_for(p, w.tk);
+        add_join(j, a, a.tk, a.part_k, nullptr, a.dk, p->nk, 1, a.kv);
+        add_join(j, a, a.tk, a.part_v, nullptr, a.dv, p->nk, 1, a.kv);
+    }
     if (p->nq > 0) {
-        const dim3 grid((unsigned)(a.nq_pad / (kThreads / 16)), (unsigned)std::min<int64_t>((int64_t)p->batch * p->heads, 65535));
-        row_statistics<<<grid, kThreads, 0, s>>>(a, reinterpret_cast<float *>(ws + w.lse2), reinterpret_cast<float *>(ws + w.delta),
-                                                 p->dtype == GS_DTYPE_F16 ? kHalfShift : 0.0f);
-        e = hipGetLastError();
+        const int lines = kThreads >> pre.lanes;
+        pre.out = a.out;
+        pre.dout = a.dout;
+        pre.lse = a.lse;
+        pre.lse2 = reinterpret_cast<float *>(ws + w.lse2);
+        pre.delta = reinterpret_cast<float *>(ws + w.delta);
+        pre.shift = p->dtype == GS_DTYPE_F16 ? kHalfShift : 0.0f;
+        pre.nq = p->nq;
+        pre.nq_pad = a.nq_pad;
+        pre.per = (uint32_t)((a.nq_pad + lines - 1) / lines);
+        pre.blocks += pre.per * (uint32_t)(p->batch * p->heads);
     }
-    if (e == hipSuccess && g->dq && p->nq > 0) {
-        e = operand(p, a.kt, p->nk, p->kv_heads, w.k, ws, a.k, s);
-        if (e == hipSuccess) e = operand(p, a.vt, p->nk, p->kv_heads, w.v, ws, a.v, s);
-        tile(a, w.t);
-        if (e == hipSuccess)
-            e = p->dtype == GS_DTYPE_F32 ? launch_dq_f32(a, w.t.waves, s) : p->dtype == GS_DTYPE_F16 ? launch_dq_f16(a, w.t.waves, s) : launch_dq_bf16(a, w.t.waves, s);
-        if (e == hipSuccess && a.splits > 1) e = launch_join(a, a.part, nullptr, a.dq, a.rows, a.group, a.heads, s);
+    hipError_t e = launch_prepare(pre, s);
+    // both kinds of blocks in one launch where they have as many waves
+    auto blocks = [&](const Args &b, int waves) {
+        return p->dtype == GS_DTYPE_F32 ? launch_bwd_f32(b, waves, s) : p->dtype == GS_DTYPE_F16 ? launch_bwd_f16(b, waves, s) : launch_bwd_bf16(b, waves, s);
+    };
+    if (e == hipSuccess && w.t.waves && w.tk.waves && w.t.waves != w.tk.waves) {
+        Args only = a;
+        only.tk.blocks = 0;
+        e = blocks(only, w.t.waves);
+        a.t.blocks = 0;
+        if (e == hipSuccess) e = blocks(a, w.tk.waves);
+    } else if (e == hipSuccess && (w.t.waves || w.tk.waves)) {
+        e = blocks(a, std::max(w.t.waves, w.tk.waves));
     }
-    if (e == hipSuccess && (g->dk || g->dv) && p->nk > 0) {
-        e = operand(p, a.q, p->nq, p->heads, w.q, ws, a.qt, s);
-        if (e == hipSuccess) e = operand(p, a.dout, p->nq, p->heads, w.g, ws, a.dot, s);
-        tile(a, w.tkv);
-        if (e == hipSuccess)
-            e = p->dtype == GS_DTYPE_F32 ? launch_dkv_f32(a, w.tkv.waves, s) : p->dtype == GS_DTYPE_F16 ? launch_dkv_f16(a, w.tkv.waves, s) : launch_dkv_bf16(a, w.tkv.waves, s);
-        if (e == hipSuccess && a.splits > 1) {
-            if (g->dk) e = launch_join(a, a.part, nullptr, a.dk, p->nk, 1, a.kv, s);
-            if (e == hipSuccess && g->dv) e = launch_join(a, a.part2, nullptr, a.dv, p->nk, 1, a.kv, s);
-        }
-    }
+    if (e == hipSuccess) e = launch_join(j, false, s);
     return from_hip(e);
 }
 

@@ -3,10 +3,11 @@
 //   P = exp(S - lse),  dP = dout v,  dS = P (dP - delta),
 //   dq = scale dS k,   dk = scale dS^T q,   dv = P^T dout
 //
-// in two kernels, each of which forms S and dP itself: one walks over keys and
-// sums dq, the other over queries and sums dk and dv.  Two of seven products
-// are formed twice; in exchange nothing is added to memory from many blocks, so
-// the results do not depend on an order, and no partial dq is written.
+// by two kinds of blocks of one launch, each of which forms S and dP itself: some
+// walk over keys and sum dq, the others over queries and sum dk and dv.  Two of
+// seven products are formed twice; in exchange nothing is added to memory from
+// many blocks, so the results do not depend on an order, and a card that one kind
+// would not fill has the other's blocks too.
 #pragma once
 
 #include "gs_attention.h"
@@ -52,18 +53,17 @@ template <int KIND, int NL> __device__ __forceinline__ void pack16(const float v
 }
 
 // dq: a wave owns 32 queries and walks over tiles of keys.
-template <int KIND, int NL, int DP, int NW> __global__ __launch_bounds__(NW * 64, room_for(NL, NW)) void attention_dq(Args a)
+template <int KIND, int NL, int DP, int NW> __device__ __forceinline__ void dq_block(const Args &a, uint32_t block, char *lds)
 {
     constexpr int KT = kTileRows<NL, DP>, KS = KT / 32;
     using LD = Loader<DP, KT, NW * 64>;
     constexpr int kStage = 2 * NL * LD::kBytes, ES = NL > 1 ? 4 : 2;
-    __shared__ __align__(128) char lds[2 * kStage];
 
     Item it;
-    if (!item_of(a, it)) return;
+    if (!item_of(a, a.t, block, it)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int length = length_of(a, it.batch);
-    const int tiles = (length + KT - 1) / KT, per = (tiles + a.splits - 1) / a.splits;
+    const int tiles = (length + KT - 1) / KT, per = (tiles + a.t.splits - 1) / a.t.splits;
     const int t0 = it.split * per, t1 = min(tiles, t0 + per);
 
     const int row = (it.tile * NW + wave) * 32 + (lane & 31);
@@ -125,8 +125,8 @@ template <int KIND, int NL, int DP, int NW> __global__ __launch_bounds__(NW * 64
         }
     }
     const float f = a.scale * scale.inverse() * (KIND == gemm::kF16 ? 1.0f / (float)(1 << (int)kHalfShift) : 1.0f);
-    if (a.splits > 1) {
-        store_part<DP>(a.part, part_at(a, it, wave), acc, f, lane);
+    if (a.t.splits > 1) {
+        store_part<DP>(a.part, part_at(a, a.t, it, wave), acc, f, lane);
     } else if (there) {
         store_columns<DP>(const_cast<void *>(a.dq.p), a.type, it.batch * a.dq.sb + token * a.dq.sr + head * a.dq.sh, acc, f, a.d, lane);
     }
@@ -134,15 +134,14 @@ template <int KIND, int NL, int DP, int NW> __global__ __launch_bounds__(NW * 64
 
 // dk and dv: a wave owns 32 keys and walks over tiles of queries of every head
 // that shares them.
-template <int KIND, int NL, int DP, int NW> __global__ __launch_bounds__(NW * 64, room_for(NL, NW)) void attention_dkv(Args a)
+template <int KIND, int NL, int DP, int NW> __device__ __forceinline__ void dkv_block(const Args &a, uint32_t block, char *lds)
 {
     constexpr int RT = kTileRows<NL, DP>, RS = RT / 32;
     using LD = Loader<DP, RT, NW * 64>;
     constexpr int kOperands = 2 * NL * LD::kBytes, kStage = kOperands + 512, ES = NL > 1 ? 4 : 2;
-    __shared__ __align__(128) char lds[2 * kStage];
 
     Item it;
-    if (!item_of(a, it)) return;
+    if (!item_of(a, a.tk, block, it)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int length = length_of(a, it.batch);
     const int key = (it.tile * NW + wave) * 32 + (lane & 31);
@@ -153,7 +152,7 @@ template <int KIND, int NL, int DP, int NW> __global__ __launch_bounds__(NW * 64
 
     // tiles of queries of one head after the other
     const int per_head = (a.nq + RT - 1) / RT;
-    const int64_t tiles = any ? (int64_t)per_head * a.group : 0, per = (tiles + a.splits - 1) / a.splits;
+    const int64_t tiles = any ? (int64_t)per_head * a.group : 0, per = (tiles + a.tk.splits - 1) / a.tk.splits;
     const int64_t t0 = it.split * per, t1 = min(tiles, t0 + per);
 
     i4 k[NL][DP / 16], v[NL][DP / 16];
@@ -226,43 +225,39 @@ template <int KIND, int NL, int DP, int NW> __global__ __launch_bounds__(NW * 64
         }
     }
     const float down = KIND == gemm::kF16 ? 1.0f / (float)(1 << (int)kHalfShift) : 1.0f, f = a.scale * scale.inverse() * down;
-    if (a.splits > 1) {
-        const int64_t at = part_at(a, it, wave);
-        store_part<DP>(a.part, at, dk, f, lane);
-        store_part<DP>(a.part2, at, dv, down, lane);
+    if (a.tk.splits > 1) {
+        const int64_t at = part_at(a, a.tk, it, wave);
+        store_part<DP>(a.part_k, at, dk, f, lane);
+        store_part<DP>(a.part_v, at, dv, down, lane);
     } else if (there) {
         if (a.dk.p) store_columns<DP>(const_cast<void *>(a.dk.p), a.type, it.batch * a.dk.sb + key * a.dk.sr + it.head * a.dk.sh, dk, f, a.d, lane);
         if (a.dv.p) store_columns<DP>(const_cast<void *>(a.dv.p), a.type, it.batch * a.dv.sb + key * a.dv.sr + it.head * a.dv.sh, dv, down, a.d, lane);
     }
 }
 
-template <int KIND, int NL, int DP> hipError_t launch_dq_waves(const Args &a, int waves, hipStream_t s)
+template <int KIND, int NL, int DP, int NW> __global__ __launch_bounds__(NW * 64, room_for(NL, NW, DP <= 32 ? 4 : DP <= 64 ? 3 : 2)) void attention_bwd(Args a)
 {
-    const dim3 grid = grid_of(a.blocks, waves * 64);
-    if (waves == 1) attention_dq<KIND, NL, DP, 1><<<grid, 64, 0, s>>>(a);
-    else attention_dq<KIND, NL, DP, 4><<<grid, 256, 0, s>>>(a);
+    using LD = Loader<DP, kTileRows<NL, DP>, NW * 64>;
+    __shared__ __align__(128) char lds[2 * (2 * NL * LD::kBytes + 512)];
+    const uint32_t b = (uint32_t)block_of();
+    if (b < a.tk.blocks) dkv_block<KIND, NL, DP, NW>(a, b, lds);
+    else dq_block<KIND, NL, DP, NW>(a, b - a.tk.blocks, lds);
+}
+
+template <int KIND, int NL, int DP> hipError_t launch_bwd_waves(const Args &a, int waves, hipStream_t s)
+{
+    const dim3 grid = grid_of((int64_t)a.tk.blocks + a.t.blocks, waves * 64);
+    if (waves == 1) attention_bwd<KIND, NL, DP, 1><<<grid, 64, 0, s>>>(a);
+    else attention_bwd<KIND, NL, DP, 4><<<grid, 256, 0, s>>>(a);
     return hipGetLastError();
 }
-template <int KIND, int NL> hipError_t launch_dq_kind(const Args &a, int waves, hipStream_t s)
+// Blocks of `waves` waves, of both kinds or (no blocks of the other) one.
+template <int KIND, int NL> hipError_t launch_bwd_kind(const Args &a, int waves, hipStream_t s)
 {
-    if (a.d <= 32) return launch_dq_waves<KIND, NL, 32>(a, waves, s);
-    if (a.d <= 64) return launch_dq_waves<KIND, NL, 64>(a, waves, s);
-    if (a.d <= 96) return launch_dq_waves<KIND, NL, 96>(a, waves, s);
-    return launch_dq_waves<KIND, NL, 128>(a, waves, s);
-}
-template <int KIND, int NL, int DP> hipError_t launch_dkv_waves(const Args &a, int waves, hipStream_t s)
-{
-    const dim3 grid = grid_of(a.blocks, waves * 64);
-    if (waves == 1) attention_dkv<KIND, NL, DP, 1><<<grid, 64, 0, s>>>(a);
-    else attention_dkv<KIND, NL, DP, 4><<<grid, 256, 0, s>>>(a);
-    return hipGetLastError();
-}
-template <int KIND, int NL> hipError_t launch_dkv_kind(const Args &a, int waves, hipStream_t s)
-{
-    if (a.d <= 32) return launch_dkv_waves<KIND, NL, 32>(a, waves, s);
-    if (a.d <= 64) return launch_dkv_waves<KIND, NL, 64>(a, waves, s);
-    if (a.d <= 96) return launch_dkv_waves<KIND, NL, 96>(a, waves, s);
-    return launch_dkv_waves<KIND, NL, 128>(a, waves, s);
+    if (a.d <= 32) return launch_bwd_waves<KIND, NL, 32>(a, waves, s);
+    if (a.d <= 64) return launch_bwd_waves<KIND, NL, 64>(a, waves, s);
+    if (a.d <= 96) return launch_bwd_waves<KIND, NL, 96>(a, waves, s);
+    return launch_bwd_waves<KIND, NL, 128>(a, waves, s);
 }
 
 }  // namespace attn

@@ -16,7 +16,7 @@ namespace attn {
 // fp32.
 constexpr float kMostSum = 8192.0f;
 
-template <int KIND, int NL, int DP, int NW> __global__ __launch_bounds__(NW * 64, room_for(NL, NW)) void attention_fwd(Args a)
+template <int KIND, int NL, int DP, int NW> __global__ __launch_bounds__(NW * 64, room_for(NL, NW, DP <= 64 ? 4 : 2)) void attention_fwd(Args a)
 {
     constexpr int KT = kTileRows<NL, DP>, KS = KT / 32;
     using LD = Loader<DP, KT, NW * 64>;
@@ -24,11 +24,11 @@ template <int KIND, int NL, int DP, int NW> __global__ __launch_bounds__(NW * 64
     __shared__ __align__(128) char lds[2 * kStage];
 
     Item it;
-    if (!item_of(a, it)) return;
+    if (!item_of(a, a.t, (uint32_t)block_of(), it)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int length = length_of(a, it.batch);
     // this split's tiles
-    const int tiles = (length + KT - 1) / KT, per = (tiles + a.splits - 1) / a.splits;
+    const int tiles = (length + KT - 1) / KT, per = (tiles + a.t.splits - 1) / a.t.splits;
     const int t0 = it.split * per, t1 = min(tiles, t0 + per);
 
     const int row = (it.tile * NW + wave) * 32 + (lane & 31);
@@ -122,8 +122,8 @@ template <int KIND, int NL, int DP, int NW> __global__ __launch_bounds__(NW * 64
     }
 
     sum = pair_sum(sum);
-    if (a.splits > 1) {                         // as they are, for join_fwd
-        const int64_t at = part_at(a, it, wave);
+    if (a.t.splits > 1) {                         // as they are, for join_fwd
+        const int64_t at = part_at(a, a.t, it, wave);
         store_part<DP>(a.part, at, o, 1.0f, lane);
         if (lane < 32) *reinterpret_cast<float2 *>(a.ml + (at * 32 + lane) * 2) = float2{m, sum};
         return;
@@ -134,19 +134,19 @@ template <int KIND, int NL, int DP, int NW> __global__ __launch_bounds__(NW * 64
     if (a.lse && lane < 32) a.lse[((int64_t)it.batch * a.heads + head) * a.nq + token] = (m + log2f(sum)) * kLn2;
 }
 
-template <int KIND, int NL, int DP> hipError_t launch_fwd_waves(const Args &a, int waves, hipStream_t s)
+template <int KIND, int NL, int DP> hipError_t launch_fwd_waves(const Args &a, hipStream_t s)
 {
-    const dim3 grid = grid_of(a.blocks, waves * 64);
-    if (waves == 1) attention_fwd<KIND, NL, DP, 1><<<grid, 64, 0, s>>>(a);
+    const dim3 grid = grid_of(a.t.blocks, a.t.waves * 64);
+    if (a.t.waves == 1) attention_fwd<KIND, NL, DP, 1><<<grid, 64, 0, s>>>(a);
     else attention_fwd<KIND, NL, DP, 4><<<grid, 256, 0, s>>>(a);
     return hipGetLastError();
 }
-template <int KIND, int NL> hipError_t launch_fwd_kind(const Args &a, int waves, hipStream_t s)
+template <int KIND, int NL> hipError_t launch_fwd_kind(const Args &a, hipStream_t s)
 {
-    if (a.d <= 32) return launch_fwd_waves<KIND, NL, 32>(a, waves, s);
-    if (a.d <= 64) return launch_fwd_waves<KIND, NL, 64>(a, waves, s);
-    if (a.d <= 96) return launch_fwd_waves<KIND, NL, 96>(a, waves, s);
-    return launch_fwd_waves<KIND, NL, 128>(a, waves, s);
+    if (a.d <= 32) return launch_fwd_waves<KIND, NL, 32>(a, s);
+    if (a.d <= 64) return launch_fwd_waves<KIND, NL, 64>(a, s);
+    if (a.d <= 96) return launch_fwd_waves<KIND, NL, 96>(a, s);
+    return launch_fwd_waves<KIND, NL, 128>(a, s);
 }
 
 }  // namespace attn

@@ -843,8 +843,8 @@ size_t gs_attention_fwd_workspace_bytes(const gs_attention *attention /* host */
 
 /* Errors: GS_ERR_INVALID_ARG (NULL descriptor or arrays with rows, sizes or
  * strides out of range, an unknown type, a misaligned pointer, elements of out
- * that share a place), GS_ERR_UNSUPPORTED (d above 128; batch heads max(nq, nk)
- * above 2^40), GS_ERR_WORKSPACE. */
+ * that share a place), GS_ERR_UNSUPPORTED (d above 128; batch heads max(nq, nk, 32)
+ * above 2^33), GS_ERR_WORKSPACE. */
 gs_status gs_attention_fwd(const gs_attention *attention /* host */, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Gradients of gs_attention_fwd from its inputs, the out and lse that it kept
