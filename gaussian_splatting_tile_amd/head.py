@@ -1,4 +1,5 @@
-"""A network head that predicts Gaussians, on the library's operators.
+"""A network head that predicts Gaussians, and what gives its tokens their
+content, on the library's operators.
 
 Token features [m][width] pass through residual blocks
 
@@ -10,6 +11,11 @@ components, 1 opacity logit and (degree + 1)^2 x 3 SH coefficients.  The
 rasterizer's gradients come back in the same layout, so nothing is copied
 between the two (the heads of the GlobalSplat page, step (4) of its pipeline).
 
+Before the head, the scene's tokens may read the feature maps of the input
+views (ViewReader): a group norm with SiLU over every map, a product to keys and
+values, and cross attention from the tokens (steps (2) and (3) of that
+pipeline).
+
     python -m gaussian_splatting_tile_amd.head
 
 fits a small head to one view of a scene and renders it again with its blocks
@@ -18,7 +24,7 @@ in 8 bits.
 
 from __future__ import annotations
 
-from typing import Dict
+from typing import Dict, Optional
 
 import torch
 
@@ -157,6 +163,97 @@ class GaussianHead:
         B.rms_norm_fwd(s, s, gamma=self.gamma[self.blocks])
         product(s, self.w_out, planes, bias=self.b_out, planes=True)
         return planes
+
+
+class ViewReader:
+    """Tokens [m][width] read feature maps [views][pixels][channels]:
+
+        f = silu(group_norm(features)),  [k v] = f w_kv^T + b_kv,  q = norm(tokens) w_q^T + b_q
+        tokens' = tokens + attention(q, k, v) w_o^T + b_o
+
+    with `heads` heads of width / heads.  Views whose byte in `seen` is 0 are not
+    attended.  For the backward the maps are kept in 8 bits; `channels` and `width`
+    are multiples of 32."""
+
+    def __init__(self, m: int, width: int, views: int, pixels: int, channels: int, heads: int, groups: int,
+                 dtype=torch.bfloat16, device="cuda", seed: int = 0):
+        assert width % 32 == 0 and channels % 32 == 0 and width % heads == 0
+        self.m, self.width, self.views, self.pixels, self.channels, self.heads, self.groups = m, width, views, pixels, channels, heads, groups
+        gen = torch.Generator(device=device).manual_seed(seed)
+        rand = lambda *s, scale: (torch.randn(s, generator=gen, device=device) * scale).to(dtype)
+        e16 = lambda *s: torch.empty(s, dtype=dtype, device=device)
+        f32 = lambda *s: torch.zeros(s, device=device)
+        n = views * pixels
+        self.w_kv, self.w_q, self.w_o = rand(2 * width, channels, scale=channels ** -0.5), rand(width, width, scale=width ** -0.5), rand(width, width, scale=0.1 * width ** -0.5)
+        self.b_kv, self.b_q, self.b_o = f32(2 * width), f32(width), f32(width)
+        self.gamma_f, self.beta_f, self.gamma = torch.ones(channels, device=device), f32(channels), torch.ones(width, device=device)
+        self.matrices, self.vectors = ("w_kv", "w_q", "w_o"), ("b_kv", "b_q", "b_o", "gamma_f", "beta_f", "gamma")
+        self.grads = {k: torch.zeros_like(getattr(self, k)) for k in self.matrices + self.vectors}
+        # activations
+        self.f, self.mean, self.rstd_f = e16(views, pixels, channels), f32(views, groups), f32(views, groups)
+        self.kept = torch.empty((views, pixels, channels), dtype=torch.float8_e4m3fn, device=device)
+        self.kept_scales = torch.empty((views, pixels, channels // 32), dtype=torch.uint8, device=device)
+        self.kv, self.normed, self.rstd, self.q = e16(n, 2 * width), e16(m, width), f32(m), e16(m, width)
+        self.read, self.lse, self.tokens, self.out = e16(m, width), f32(1, heads, m), e16(m, width), e16(m, width)
+        self.mask = torch.ones((1, n), dtype=torch.uint8, device=device)
+        self.d_out, self.d_read, self.d_q, self.d_kv = e16(m, width), e16(m, width), e16(m, width), e16(n, 2 * width)
+        self.d_normed, self.d_tokens, self.d_features = e16(m, width), e16(m, width), e16(views, pixels, channels)
+        # descriptors once: the buffers stay where they are
+        rows = lambda t: t.view(1, m, heads, width // heads)
+        k, v = (self.kv.view(1, n, 2, heads, width // heads)[:, :, i] for i in range(2))
+        dk, dv = (self.d_kv.view(1, n, 2, heads, width // heads)[:, :, i] for i in range(2))
+        flat, g = self.f.view(n, channels), self.grads
+        self._kv = B.linear_struct(flat, self.w_kv, self.kv, bias=self.b_kv)
+        self._q = B.linear_struct(self.normed, self.w_q, self.q, bias=self.b_q)
+        self._o = B.linear_struct(self.read, self.w_o, self.out, bias=self.b_o, residual=self.tokens)
+        self._read = B.attention_struct(rows(self.q), k, v, rows(self.read), lse=self.lse, kv_mask=self.mask)
+        self._d_kv = B.linear_grads_struct(self._kv, self.d_kv, dx=self.d_features.view(n, channels), dw=g["w_kv"], db=g["b_kv"])
+        self._d_q = B.linear_grads_struct(self._q, self.d_q, dx=self.d_normed, dw=g["w_q"], db=g["b_q"])
+        self._d_o = B.linear_grads_struct(self._o, self.d_out, dx=self.d_read, dw=g["w_o"], db=g["b_o"])
+        self._d_read = B.attention_grads_struct(self._read, rows(self.d_read), dq=rows(self.d_q), dk=dk, dv=dv)
+        need = [B.linear_fwd_workspace_bytes(x) for x in (self._kv, self._q, self._o)]
+        need += [B.linear_bwd_workspace_bytes(x, y) for x, y in ((self._kv, self._d_kv), (self._q, self._d_q), (self._o, self._d_o))]
+        need += [B.attention_fwd_workspace_bytes(self._read), B.attention_bwd_workspace_bytes(self._read, self._d_read)]
+        need += [f(views, pixels, channels, groups) for f in (B.group_norm_fwd_workspace_bytes, B.group_norm_bwd_workspace_bytes)]
+        need += [B.rms_norm_bwd_workspace_bytes(m, width)]
+        self.ws = torch.empty(max(need) + 16, dtype=torch.uint8, device=device)
+
+    def forward(self, tokens: torch.Tensor, features: torch.Tensor, seen: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """tokens' [m][width]; seen [views] uint8 or bool, or None: all."""
+        if tokens.shape != (self.m, self.width) or features.shape != (self.views, self.pixels, self.channels):
+            raise ValueError(f"expected tokens [{self.m}][{self.width}] and features [{self.views}][{self.pixels}][{self.channels}], "
+                             f"got {tuple(tokens.shape)} and {tuple(features.shape)}")
+        if seen is not None and seen.shape != (self.views,):
+            raise ValueError(f"seen: expected [{self.views}], got {tuple(seen.shape)}")
+        mask = self.mask.view(self.views, self.pixels)
+        if seen is None:
+            mask.fill_(1)
+        else:
+            mask.copy_((seen != 0).view(-1, 1).expand_as(mask))
+        self.tokens.copy_(tokens)
+        B.group_norm_fwd(features, self.f, self.groups, gamma=self.gamma_f, beta=self.beta_f, act="silu", mean=self.mean, rstd=self.rstd_f,
+                         kept=self.kept, kept_scales=self.kept_scales, workspace=self.ws)
+        B.linear_fwd(self._kv, self.ws)
+        B.rms_norm_fwd(self.tokens, self.normed, gamma=self.gamma, rstd=self.rstd)
+        B.linear_fwd(self._q, self.ws)
+        B.attention_fwd(self._read, self.ws)
+        B.linear_fwd(self._o, self.ws)
+        return self.out
+
+    def backward(self, d_out: torch.Tensor):
+        """Gradients of every weight; returns those of tokens and features."""
+        if d_out.shape != (self.m, self.width):
+            raise ValueError(f"d_out: expected [{self.m}][{self.width}], got {tuple(d_out.shape)}")
+        self.d_out.copy_(d_out)
+        B.linear_bwd(self._o, self._d_o, self.ws)
+        B.attention_bwd(self._read, self._d_read, self.ws)
+        B.linear_bwd(self._q, self._d_q, self.ws)
+        B.rms_norm_bwd(self.tokens, self.rstd, self.d_normed, self.d_tokens, gamma=self.gamma, dsum=self.d_out, dgamma=self.grads["gamma"],
+                       workspace=self.ws)
+        B.linear_bwd(self._kv, self._d_kv, self.ws)
+        B.group_norm_bwd(self.kept, self.mean, self.rstd_f, self.d_features, self.d_features, self.groups, gamma=self.gamma_f, beta=self.beta_f,
+                         act="silu", dgamma=self.grads["gamma_f"], dbeta=self.grads["beta_f"], x_scales=self.kept_scales, workspace=self.ws)
+        return self.d_tokens, self.d_features
 
 
 def fit(steps: int = 120, n: int = 1000, width: int = 64, hidden: int = 128, blocks: int = 2, say=print):
