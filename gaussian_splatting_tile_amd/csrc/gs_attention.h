@@ -193,31 +193,46 @@ template <int KIND, int NL> __device__ __forceinline__ void pack8(const float v[
     }
 }
 
+template <int NL> struct Elements { typedef float type; };
+template <> struct Elements<1> { typedef uint16_t type; };
+
 // A wave's own 32 columns: lane l holds row `row` (its column), d = 16 s + 8 (l / 32) + (0..7).
+// Loads are whole vectors that no branch waits for (past d: of the last values,
+// unused; a row that is not there is one that is), but for the last values of a d
+// that is no multiple of 8.
 template <int KIND, int NL, int STEPS> __device__ __forceinline__ void load_columns(const char *row, bool there, int d, int lane, i4 f[NL][STEPS])
 {
+    using E = typename Elements<NL>::type;
+    const E *p = reinterpret_cast<const E *>(row);
+    Vec<E, 8> w[STEPS] = {};
+    const int mine = (lane >> 5) * 8, whole = d & ~7;
+    if (whole) {
+#pragma unroll
+        for (int s = 0; s < STEPS; s++) w[s] = *reinterpret_cast<const Vec<E, 8> *>(p + min(s * 16 + mine, whole - 8));
+    }
+#pragma unroll
+    for (int s = 0; s < STEPS; s++)
+#pragma unroll
+        for (int j = 0; j < 8; j++) w[s].v[j] = there && s * 16 + mine < whole ? w[s].v[j] : E(0);
+    if (d != whole) {
+        E last[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++) last[j] = p[min(whole + j, d - 1)];
+#pragma unroll
+        for (int s = 0; s < STEPS; s++)
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                if (there && s * 16 + mine == whole && whole + j < d) w[s].v[j] = last[j];
+    }
 #pragma unroll
     for (int s = 0; s < STEPS; s++) {
-        const int at = s * 16 + (lane >> 5) * 8, valid = there ? min(8, d - at) : 0;
         if constexpr (NL > 1) {
-            float v[8];
-            if (valid > 0) load8(row, GS_DTYPE_F32, at, valid, v);
-            else
+            i4 l[NL];
+            pack8<KIND, NL>(w[s].v, l);
 #pragma unroll
-                for (int j = 0; j < 8; j++) v[j] = 0.0f;
-            i4 w[NL];
-            pack8<KIND, NL>(v, w);
-#pragma unroll
-            for (int l = 0; l < NL; l++) f[l][s] = w[l];
+            for (int i = 0; i < NL; i++) f[i][s] = l[i];
         } else {
-            Vec<uint16_t, 8> w = {{0, 0, 0, 0, 0, 0, 0, 0}};
-            const uint16_t *p = reinterpret_cast<const uint16_t *>(row) + at;
-            if (valid >= 8) w = *reinterpret_cast<const Vec<uint16_t, 8> *>(p);
-            else
-#pragma unroll
-                for (int j = 0; j < 8; j++)
-                    if (j < valid) w.v[j] = p[j];
-            f[0][s] = __builtin_bit_cast(i4, w);
+            f[0][s] = __builtin_bit_cast(i4, w[s]);
         }
     }
 }

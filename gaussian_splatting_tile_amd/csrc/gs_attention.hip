@@ -254,7 +254,7 @@ struct Tiling {
 };
 // Time of one tile of the other side's rows on a CU that holds one block, and per
 // tile where it holds two or more (us; blocks of four waves; 64 rows, or 32 of fp32
-// above d = 32), and how many it holds.
+// above d = 32), and how many it holds.  Measured.
 struct Cost {
     double alone, shared;
     int hold;
@@ -273,39 +273,81 @@ Cost cost_of(const gs_attention *p, Product what)
     return p->dtype == GS_DTYPE_F32 ? f[what][i] : h[what][i];
 }
 
+// A wave has 32 columns.
+int waves_for(int64_t columns) { return columns <= 32 ? 1 : 4; }
+
 int padded(int d) { return (d + 31) / 32 * 32; }
 
-// Waves of a block, blocks along the columns, and splits of the `other` side's tiles
-// where the blocks alone would not fill the card: the number with the least
-// estimated time of rounds of blocks, and of writing and joining partial sums.
-Tiling tile_columns(const gs_attention *p, Product what, int64_t columns, int64_t pairs, int64_t other, int cus)
-{
+// One kind of blocks: `blocks` of them, each of whose splits walks over a share of
+// the `other` side's tiles.
+struct Work {
     Tiling t;
-    t.waves = columns <= 32 ? 1 : 4;
-    t.tiles = (int)((columns + t.waves * 32 - 1) / (t.waves * 32));
-    t.splits = 1;
-    const int64_t blocks = std::max<int64_t>(1, pairs * t.tiles);
-    const Cost c = cost_of(p, what);
-    const int results = what == kStates ? 2 : 1;
-    // single waves: a block is a quarter of one of four waves and hides less
-    const double alone = t.waves == 1 ? 1.2 : c.alone, shared = t.waves == 1 ? c.shared / 4 : c.shared;
-    const int hold = t.waves == 1 ? 4 : c.hold;
-    double best = 0;
-    for (int64_t want = 1; want <= std::min<int64_t>(other, 256); want += want < 8 ? 1 : want / 4) {
-        const int64_t per = (other + want - 1) / want, s = (other + per - 1) / per;
-        if (s > 1 && blocks * s > 4096) break;
-        const int64_t all = blocks * s, most = (all + cus - 1) / cus;
-        // the CU with the most blocks: full rounds of `hold`, and what is left
-        const int64_t left = most % hold;
-        const double round = std::max(alone, shared * hold), last = left ? std::max(alone, shared * left) : 0.0;
-        double time = (most / hold * round + last) * per + 2.0;
-        if (s > 1) time += 3.5 + 0.03 * s + (double)all * t.waves * 32 * padded(p->d) * 4 * 2 * results / 7e6;
-        if (best == 0 || time < best) {
-            best = time;
-            t.splits = (int)s;
+    Cost cost;
+    int64_t blocks, other;
+    double part;                                // us to write and join a split's partial sums
+};
+Work work_of(const gs_attention *p, Product what, int waves, int64_t columns, int64_t pairs, int64_t other)
+{
+    Work w = {};
+    w.t = {waves, (int)((columns + waves * 32 - 1) / (waves * 32)), 1};
+    w.cost = cost_of(p, what);
+    if (waves == 1) w.cost = {1.2, w.cost.shared / 4, 4};               // a quarter of the work, and less to hide it behind
+    w.blocks = pairs * w.t.tiles;
+    w.other = other;
+    w.part = 0.03 + (double)w.blocks * waves * 32 * padded(p->d) * 4 * 2 * (what == kStates ? 2 : 1) / 7e6;
+    return w;
+}
+int64_t tiles_of(int64_t other, int64_t splits) { return (other + splits - 1) / splits; }
+
+// Time of w's blocks in s splits each and then of v's in u: blocks go to the first
+// place that is free, as many to a CU as it holds.
+double time_of(const Work &w, int64_t s, const Work *v, int64_t u)
+{
+    const int64_t n = w.blocks * s, m = v ? v->blocks * u : 0;
+    const int64_t hold = std::min<int64_t>(v ? std::min(w.cost.hold, v->cost.hold) : w.cost.hold, (n + m + kCus - 1) / kCus), places = kCus * std::max<int64_t>(1, hold);
+    auto one = [&](const Work &x, int64_t splits) { return tiles_of(x.other, splits) * (hold <= 1 ? x.cost.alone : std::max(x.cost.alone, x.cost.shared * hold)) + 2.0; };
+    const double dn = one(w, s), dm = v ? one(*v, u) : 0.0;
+    const int64_t rounds = n / places, left = n % places;
+    double early = rounds * dn, late = early + (left ? dn : 0.0);       // when `places - left` and `left` places are free
+    int64_t rest = m;
+    while (rest > 0) {
+        if (left == 0 || early <= late) {
+            rest -= places - left;
+            early += dm;
+        } else {
+            rest -= left;
+            late += dm;
         }
     }
-    return t;
+    double time = std::max(early, late);
+    if (s > 1 || u > 1) time += 3.5;
+    if (s > 1) time += s * w.part;
+    if (u > 1) time += u * v->part;
+    return time;
+}
+
+// Splits of one or both kinds of blocks (v: NULL, or the second kind) where the blocks
+// alone would not fill the card: those of the least estimated time.
+void choose_splits(Work *w, Work *v)
+{
+    static const int tried[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32, 48, 64, 96, 128, 192, 256};
+    constexpr int64_t kMostBlocks = 2048;       // more need no splits
+    double best = 0;
+    const Work a = *w, b = v ? *v : Work{};
+    for (int s : tried) {
+        const int64_t ss = (a.other + tiles_of(a.other, s) - 1) / std::max<int64_t>(1, tiles_of(a.other, s));
+        if (s > 1 && (s > a.other || a.blocks * s > kMostBlocks || (ss != s && s <= 4))) continue;
+        for (int u : tried) {
+            if (u > 1 && (!v || u > b.other || b.blocks * u > kMostBlocks)) break;
+            const int64_t uu = v ? (b.other + tiles_of(b.other, u) - 1) / std::max<int64_t>(1, tiles_of(b.other, u)) : 1;
+            const double time = time_of(a, std::max<int64_t>(1, ss), v ? &b : nullptr, std::max<int64_t>(1, uu));
+            if (best == 0 || time < best) {
+                best = time;
+                w->t.splits = (int)std::max<int64_t>(1, ss);
+                if (v) v->t.splits = (int)std::max<int64_t>(1, uu);
+            }
+        }
+    }
 }
 
 int tile_rows(const gs_attention *p) { return p->dtype == GS_DTYPE_F32 && p->d > 32 ? 32 : 64; }
@@ -349,7 +391,10 @@ Plan plan_fwd(const gs_attention *p)
 {
     Plan w = {};
     const int kt = tile_rows(p);
-    w.t = tile_columns(p, kForward, (int64_t)p->nq * (p->heads / p->kv_heads), (int64_t)p->batch * p->kv_heads, (p->nk + kt - 1) / kt, kCus);
+    const int64_t rows = (int64_t)p->nq * (p->heads / p->kv_heads);
+    Work fwd = work_of(p, kForward, waves_for(rows), rows, (int64_t)p->batch * p->kv_heads, (p->nk + kt - 1) / kt);
+    choose_splits(&fwd, nullptr);
+    w.t = fwd.t;
     place(w, w.k, p, p->k, p->k_batch, p->k_row, p->k_head, p->nk, p->kv_heads);
     place(w, w.v, p, p->v, p->v_batch, p->v_row, p->v_head, p->nk, p->kv_heads);
     if (w.t.splits > 1) {
@@ -371,16 +416,21 @@ Plan plan_bwd(const gs_attention *p, const gs_attention_grads *g)
     w.delta = stat;
     w.bytes = 2 * stat;
     const bool queries = g->dq && p->nq > 0, states = (g->dk || g->dv) && p->nk > 0;
-    const int cus = queries && states ? kCus / 2 : kCus;                // the two kinds of blocks share the card
+    // one launch: blocks of as many waves, first those of dk and dv
+    const int waves = std::max(queries ? waves_for((int64_t)p->nq * group) : 1, states ? waves_for(p->nk) : 1);
+    Work dq = work_of(p, kQueries, waves, (int64_t)p->nq * group, pairs, (p->nk + kt - 1) / kt);
+    Work dkv = work_of(p, kStates, waves, p->nk, pairs, (int64_t)(p->nq + kt - 1) / kt * group);
+    if (states) choose_splits(&dkv, queries ? &dq : nullptr);
+    else if (queries) choose_splits(&dq, nullptr);
     if (queries) {
-        w.t = tile_columns(p, kQueries, (int64_t)p->nq * group, pairs, (p->nk + kt - 1) / kt, cus);
+        w.t = dq.t;
         place(w, w.k, p, p->k, p->k_batch, p->k_row, p->k_head, p->nk, p->kv_heads);
         place(w, w.v, p, p->v, p->v_batch, p->v_row, p->v_head, p->nk, p->kv_heads);
         w.part = w.bytes;
         if (w.t.splits > 1) w.bytes += part_bytes(p, w.t);
     }
     if (states) {
-        w.tk = tile_columns(p, kStates, p->nk, pairs, (int64_t)(p->nq + kt - 1) / kt * group, cus);
+        w.tk = dkv.t;
         place(w, w.q, p, p->q, p->q_batch, p->q_row, p->q_head, p->nq, p->heads);
         place(w, w.g, p, g->dout, g->dout_batch, g->dout_row, g->dout_head, p->nq, p->heads);
         w.part_k = w.part_v = w.bytes;
@@ -634,20 +684,9 @@ gs_status gs_attention_bwd(const gs_attention *p, const gs_attention_grads *g, v
         pre.per = (uint32_t)((a.nq_pad + lines - 1) / lines);
         pre.blocks += pre.per * (uint32_t)(p->batch * p->heads);
     }
+    const int waves = std::max(w.t.waves, w.tk.waves);
     hipError_t e = launch_prepare(pre, s);
-    // both kinds of blocks in one launch where they have as many waves
-    auto blocks = [&](const Args &b, int waves) {
-        return p->dtype == GS_DTYPE_F32 ? launch_bwd_f32(b, waves, s) : p->dtype == GS_DTYPE_F16 ? launch_bwd_f16(b, waves, s) : launch_bwd_bf16(b, waves, s);
-    };
-    if (e == hipSuccess && w.t.waves && w.tk.waves && w.t.waves != w.tk.waves) {
-        Args only = a;
-        only.tk.blocks = 0;
-        e = blocks(only, w.t.waves);
-        a.t.blocks = 0;
-        if (e == hipSuccess) e = blocks(a, w.tk.waves);
-    } else if (e == hipSuccess && (w.t.waves || w.tk.waves)) {
-        e = blocks(a, std::max(w.t.waves, w.tk.waves));
-    }
+    if (e == hipSuccess && a.t.blocks + a.tk.blocks) e = p->dtype == GS_DTYPE_F32 ? launch_bwd_f32(a, waves, s) : p->dtype == GS_DTYPE_F16 ? launch_bwd_f16(a, waves, s) : launch_bwd_bf16(a, waves, s);
     if (e == hipSuccess) e = launch_join(j, false, s);
     return from_hip(e);
 }

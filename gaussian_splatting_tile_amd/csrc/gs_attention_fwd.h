@@ -16,7 +16,7 @@ namespace attn {
 // fp32.
 constexpr float kMostSum = 8192.0f;
 
-template <int KIND, int NL, int DP, int NW> __global__ __launch_bounds__(NW * 64, room_for(NL, NW, DP <= 64 ? 4 : 2)) void attention_fwd(Args a)
+template <int KIND, int NL, int DP, int NW> __global__ __launch_bounds__(NW * 64, room_for(NL, NW, DP <= 32 ? 4 : DP <= 64 ? 3 : 2)) void attention_fwd(Args a)
 {
     constexpr int KT = kTileRows<NL, DP>, KS = KT / 32;
     using LD = Loader<DP, KT, NW * 64>;

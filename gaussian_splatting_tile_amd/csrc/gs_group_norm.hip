@@ -28,6 +28,9 @@ constexpr int kBlocks = 1024;
 // Results that the second-level caches do not hold are written past them
 // (backward 80 -> 75 us); smaller ones stay for who reads them next.
 constexpr int64_t kStreamBytes = 32 << 20;
+// Channels of a workgroup, in eights, where an image is many workgroups': more
+// would leave each few pixels, and sums as large as what they are sums of.
+constexpr int kTileChunks = 32;
 constexpr int kJoinChannels = 1024, kJoinBlocks = 32;
 constexpr int kHeld = 4;                        // pixels a thread of a single workgroup keeps
 constexpr int64_t kOneChunks = 8192;            // of eight channels: an image of one workgroup
@@ -45,7 +48,7 @@ struct Args {
     float *mean, *rstd;                         // [n][groups]
     float *part;                                // [n][blocks][c][2] sums of blocks of pixels
     float *shift;                               // forward: [n][c] what the sums' values are relative to
-    float *sums;                                // backward: [n][c][2] sums of dz and dz h
+    float *sums;                                // [n][c][2] sums of an image
     float *means;                               // backward: [n][groups][2] means of g and g h
     float *dgamma, *dbeta;
     int64_t x_image, x_pixel, xs_image, xs_pixel, dy_image, dy_pixel, y_image, y_pixel, k_image, k_pixel, ks_image, ks_pixel;
@@ -295,8 +298,9 @@ template <class F> __device__ __forceinline__ void join_blocks(const Args &a, in
     }
 }
 
-// A group's statistics: its channels' means relative to the first one's shift,
-// then squares about the mean of those.
+// More channels than a workgroup that writes would join (kJoinChannels): a group's
+// statistics at once, its channels' means relative to the first one's shift, then
+// squares about the mean of those.
 __global__ __launch_bounds__(kThreads) void join_groups(Args a)
 {
     __shared__ float turn[kThreads][2], lds[kThreads / 64];
@@ -672,27 +676,66 @@ template <int THREADS> __device__ __forceinline__ void group_means(const Args &a
     __syncthreads();
 }
 
-// dgamma and dbeta of 256 channels: sums over the `rows` of images, or of images'
-// blocks.
-__device__ __forceinline__ void sum_images(const Args &a, const float *sums, int64_t rows, int64_t block)
+// The sum over rows of [rows][c] pairs of 16 channels, c0 .. : 16 rows of threads,
+// eight loads on their way at once; the result in the first 16 threads.
+__device__ __forceinline__ float2 sum_rows_of(const float2 *part, int64_t rows, int c0, int channels, float2 *turn)
 {
-    const int64_t c = block * kThreads + threadIdx.x;
-    if (c >= a.c) return;
-    float s = 0.0f, sh = 0.0f;
-    for (int64_t i = 0; i < rows; i++) {
-        s += sums[(i * a.c + c) * 2];
-        sh += sums[(i * a.c + c) * 2 + 1];
-    }
-    if (a.dbeta) a.dbeta[c] = a.accumulate ? a.dbeta[c] + s : s;
-    if (a.dgamma) a.dgamma[c] = a.accumulate ? a.dgamma[c] + sh : sh;
+    const int c = c0 + (threadIdx.x & 15);
+    float2 s = {0.0f, 0.0f};
+    if (c < channels)
+        for (int64_t b = threadIdx.x >> 4; b < rows; b += 8 * 16) {
+            float2 w[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++) w[i] = b + i * 16 < rows ? part[(b + i * 16) * channels + c] : float2{0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                s.x += w[i].x;
+                s.y += w[i].y;
+            }
+        }
+    turn[threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.x < 16)
+#pragma unroll
+        for (int r = 1; r < 16; r++) {
+            s.x += turn[r * 16 + threadIdx.x].x;
+            s.y += turn[r * 16 + threadIdx.x].y;
+        }
+    return s;
+}
+
+// A channel's sums over an image's blocks: what the workgroups that write then join
+// as one block's.
+__global__ __launch_bounds__(kThreads) void join_channels(Args a, float *to)
+{
+    __shared__ float2 turn[kThreads];
+    const int64_t slices = (a.c + 15) / 16, item = block_of();
+    if (item >= a.n * slices) return;
+    const int64_t image = item / slices;
+    const int c0 = (int)(item - image * slices) * 16;
+    const float2 s = sum_rows_of(reinterpret_cast<const float2 *>(a.part) + image * a.blocks * a.c, a.blocks, c0, a.c, turn);
+    if (threadIdx.x < 16 && c0 + (int)threadIdx.x < a.c) reinterpret_cast<float2 *>(to)[image * a.c + c0 + threadIdx.x] = s;
+}
+
+// dgamma and dbeta of 16 channels: sums over the `rows` of images, or of images'
+// blocks.
+__device__ __forceinline__ void sum_images(const Args &a, const float *sums, int64_t rows, int64_t block, float2 *turn)
+{
+    if (block * 16 >= a.c) return;
+    const float2 s = sum_rows_of(reinterpret_cast<const float2 *>(sums), rows, (int)block * 16, a.c, turn);
+    const int64_t c = block * 16 + threadIdx.x;
+    if (threadIdx.x >= 16 || c >= a.c) return;
+    if (a.dbeta) a.dbeta[c] = a.accumulate ? a.dbeta[c] + s.x : s.x;
+    if (a.dgamma) a.dgamma[c] = a.accumulate ? a.dgamma[c] + s.y : s.y;
 }
 
 template <typename T, bool Q8, int G, bool JOIN> __global__ __launch_bounds__(kThreads, 4) void write_gradient(Args a)
 {
-    __shared__ float sums[JOIN ? 2 * kJoinChannels : 1], means[JOIN ? 2 * kJoinChannels : 1];
+    __shared__ __align__(8) float sums[JOIN ? 2 * kJoinChannels : 2 * kThreads], means[JOIN ? 2 * kJoinChannels : 1];
     const Part w = part_of(a, a.blocks_out);
     if (!w.there) {
-        sum_images(a, JOIN ? a.part : a.sums, JOIN ? (int64_t)a.n * a.blocks : a.n, block_of() - (int64_t)a.n * a.blocks_out * a.tiles);
+        sum_images(a, JOIN ? a.part : a.sums, JOIN ? (int64_t)a.n * a.blocks : a.n, block_of() - (int64_t)a.n * a.blocks_out * a.tiles,
+                   reinterpret_cast<float2 *>(sums));
         return;
     }
     const Place t = place_of<kThreads>(a, w.tile);
@@ -731,7 +774,11 @@ template <typename T, bool Q8, int G> __global__ __launch_bounds__(kOneThreads) 
     if (t.works) emit_gradient<T, Q8, G>(a, ch, image, 0, a.p, t, means);
 }
 
-__global__ __launch_bounds__(kThreads) void sum_images_alone(Args a) { sum_images(a, a.sums, a.n, blockIdx.x); }
+__global__ __launch_bounds__(kThreads) void sum_images_alone(Args a)
+{
+    __shared__ float2 turn[kThreads];
+    sum_images(a, a.sums, a.n, blockIdx.x, turn);
+}
 
 __global__ __launch_bounds__(kThreads) void zero_two(float *p, float *q, int n)
 {
@@ -768,8 +815,9 @@ Plan plan_of(const Shape &s)
     const int chunks = (s.c + 7) / 8;
     // one workgroup per image: its values held in registers, or many images
     w.one = chunks <= kOneThreads / 4 && (s.p <= (int64_t)kHeld * (kOneThreads / chunks) || (s.p * chunks <= kOneChunks && s.n >= 128));
-    w.ct = std::min(chunks, w.one ? kOneThreads : kThreads);
-    w.tiles = (chunks + w.ct - 1) / w.ct;
+    w.tiles = w.one ? 1 : (chunks + kTileChunks - 1) / kTileChunks;
+    w.ct = (chunks + w.tiles - 1) / w.tiles;
+    if (w.tiles > 1) w.ct = (w.ct + 3) / 4 * 4;                         // whole 8-bit blocks
     if (w.one) {
         w.blocks = w.blocks_out = 1;
         w.per = w.per_out = s.p;
@@ -802,9 +850,21 @@ void set_shape(Args &a, const Shape &s, const Plan &w, int es)
     a.stream = s.n * s.p * s.c * es > kStreamBytes;
 }
 
-// Sums of few blocks are joined by every workgroup that writes: a launch less
-// (JJ), where their reading does not show.
-bool joins(const Args &a) { return a.c <= kJoinChannels && a.blocks <= kJoinBlocks && (int64_t)a.n * a.blocks <= 1024; }
+// Whether the workgroups that write join an image's channels themselves: few blocks'
+// sums as they are (3 x 1001 x 90: 17 -> 14 us for the launch less), or, where groups
+// are too few or too wide to be joined by a workgroup each, added up per channel
+// first.  Else a workgroup joins each group (8 x 65536 x 128: 110 us, 119 by channels).
+bool few_blocks(const Args &a) { return a.blocks <= kJoinBlocks && (int64_t)a.n * a.blocks <= 1024; }
+bool by_channels(const Args &a) { return a.c <= kJoinChannels && (few_blocks(a) || a.cg > 64 || (int64_t)a.n * a.groups < 64); }
+Args joined(const Args &a, hipStream_t s)
+{
+    Args b = a;
+    if (few_blocks(a)) return b;
+    join_channels<<<grid_of((int64_t)a.n * ((a.c + 15) / 16), kThreads), kThreads, 0, s>>>(a, a.sums);
+    b.part = a.sums;
+    b.blocks = 1;
+    return b;
+}
 
 template <typename T, int G> hipError_t launch_fwd(const Args &a, bool one, hipStream_t s)
 {
@@ -815,8 +875,8 @@ template <typename T, int G> hipError_t launch_fwd(const Args &a, bool one, hipS
     }
     sum_moments<T><<<grid_of((int64_t)a.n * a.blocks * a.tiles, kThreads), kThreads, 0, s>>>(a);
     const dim3 out = grid_of((int64_t)a.n * a.blocks_out * a.tiles, kThreads);
-    if (joins(a)) {
-        write_norm<T, G, true><<<out, kThreads, 0, s>>>(a);
+    if (by_channels(a)) {
+        write_norm<T, G, true><<<out, kThreads, 0, s>>>(joined(a, s));
         return hipGetLastError();
     }
     join_groups<<<grid_of((int64_t)a.n * a.groups, kThreads), kThreads, 0, s>>>(a);
@@ -830,7 +890,7 @@ template <typename T> hipError_t launch_fwd(const Args &a, bool one, hipStream_t
 template <typename T, bool Q8, int G> hipError_t launch_bwd(const Args &a, bool one, hipStream_t s)
 {
     const bool wanted = a.dgamma || a.dbeta;
-    const int sums = (a.c + kThreads - 1) / kThreads;
+    const int sums = (a.c + 15) / 16;
     if (one) {
         gradient_image<T, Q8, G><<<grid_of(a.n, kOneThreads), kOneThreads, 0, s>>>(a);
         if (wanted && a.n > 1) sum_images_alone<<<sums, kThreads, 0, s>>>(a);
@@ -838,8 +898,8 @@ template <typename T, bool Q8, int G> hipError_t launch_bwd(const Args &a, bool 
     }
     sum_gradients<T, Q8, G><<<grid_of((int64_t)a.n * a.blocks * a.tiles, kThreads), kThreads, 0, s>>>(a);
     const dim3 out = grid_of((int64_t)a.n * a.blocks_out * a.tiles + (wanted ? sums : 0), kThreads);
-    if (joins(a)) {
-        write_gradient<T, Q8, G, true><<<out, kThreads, 0, s>>>(a);
+    if (by_channels(a)) {
+        write_gradient<T, Q8, G, true><<<out, kThreads, 0, s>>>(joined(a, s));
         return hipGetLastError();
     }
     join_gradients<<<grid_of((int64_t)a.n * a.groups, kThreads), kThreads, 0, s>>>(a);
@@ -913,7 +973,7 @@ size_t gs_group_norm_fwd_workspace_bytes(int64_t n, int64_t p, int32_t c, int32_
     if (!shape_ok(n, p, c, groups) || n == 0 || p == 0) return 0;
     const Shape s = {n, p, c, groups};
     const Plan w = plan_of(s);
-    return w.one ? 0 : part_bytes(s, w) + 2 * round256((size_t)n * groups * 4) + round256((size_t)n * c * 4);
+    return w.one ? 0 : part_bytes(s, w) + 2 * round256((size_t)n * groups * 4) + round256((size_t)n * c * 4) + round256((size_t)n * c * 8);
 }
 
 gs_status gs_group_norm_fwd(const gs_group_norm *p, void *workspace, size_t workspace_bytes, void *stream)
@@ -953,6 +1013,7 @@ gs_status gs_group_norm_fwd(const gs_group_norm *p, void *workspace, size_t work
         if (!a.mean) a.mean = reinterpret_cast<float *>(ws + at);
         if (!a.rstd) a.rstd = reinterpret_cast<float *>(ws + at + one);
         a.shift = reinterpret_cast<float *>(ws + at + 2 * one);
+        a.sums = reinterpret_cast<float *>(ws + at + 2 * one + round256((size_t)p->n * p->c * 4));
     }
     hipStream_t s = (hipStream_t)stream;
     return from_hip(p->dtype == GS_DTYPE_F32 ? launch_fwd<float>(a, w.one, s) : p->dtype == GS_DTYPE_F16 ? launch_fwd<_Float16>(a, w.one, s) : launch_fwd<__bf16>(a, w.one, s));
