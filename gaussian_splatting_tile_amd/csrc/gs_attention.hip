@@ -263,12 +263,12 @@ enum Product { kForward, kQueries, kStates };
 
 Cost cost_of(const gs_attention *p, Product what)
 {
-    static const Cost h[3][4] = {{{0.75, 0.45, 4}, {0.95, 0.65, 4}, {1.25, 0.85, 2}, {1.45, 1.06, 2}},
-                                 {{1.0, 0.7, 4}, {1.28, 0.97, 2}, {1.8, 1.3, 2}, {2.1, 1.6, 2}},
-                                 {{1.3, 0.9, 3}, {1.8, 1.3, 2}, {2.5, 1.9, 2}, {3.0, 2.4, 2}}};
-    static const Cost f[3][4] = {{{2.4, 2.0, 2}, {1.9, 1.45, 2}, {2.5, 2.5, 1}, {3.05, 3.05, 1}},
-                                 {{3.2, 2.7, 2}, {2.6, 2.1, 2}, {3.6, 3.6, 1}, {4.5, 4.5, 1}},
-                                 {{4.2, 3.7, 2}, {3.5, 3.5, 1}, {4.8, 4.8, 1}, {6.2, 6.2, 1}}};
+    static const Cost h[3][4] = {{{0.8, 0.52, 4}, {1.05, 0.7, 3}, {1.3, 0.95, 2}, {1.45, 1.1, 2}},
+                                 {{0.95, 0.63, 4}, {1.25, 0.95, 3}, {1.8, 1.35, 2}, {1.95, 1.63, 2}},
+                                 {{1.35, 0.77, 4}, {2.0, 1.29, 3}, {2.2, 1.6, 2}, {4.7, 2.5, 2}}};
+    static const Cost f[3][4] = {{{2.1, 1.58, 2}, {1.65, 1.32, 2}, {2.25, 2.25, 1}, {2.8, 2.8, 1}},
+                                 {{2.5, 2.1, 2}, {2.2, 2.2, 1}, {3.15, 3.15, 1}, {4.05, 4.05, 1}},
+                                 {{3.7, 2.95, 2}, {3.0, 3.0, 1}, {4.1, 4.1, 1}, {5.1, 5.1, 1}}};
     const int i = p->d <= 32 ? 0 : p->d <= 64 ? 1 : p->d <= 96 ? 2 : 3;
     return p->dtype == GS_DTYPE_F32 ? f[what][i] : h[what][i];
 }
