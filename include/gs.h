@@ -815,7 +815,8 @@ gs_status gs_muon_step(const gs_muon *muon /* host */, void *workspace, size_t w
  * the others hold, infinities and NaN included, has no effect.  A row with no
  * attended state gets out = 0 and lse = -infinity.
  * Scores, maxima and sums are fp32; for 16-bit types exp(S_ij - maximum) is
- * rounded to the type for its product with v (a relative error of half an ulp each).
+ * rounded to the type for its product with v (a relative error of half an ulp each;
+ * of fp16's below 2^-20 an error of 2^-31).
  * fp32 operands are multiplied as three bf16 limbs (see gs_linear). */
 typedef struct gs_attention {
     int32_t batch;              /* 0 .. 65535                                  */
@@ -838,7 +839,8 @@ typedef struct gs_attention {
     int64_t kv_mask_stride;     /* bytes between batch elements                */
 } gs_attention;
 
-/* Workspace of gs_attention_fwd, in bytes. */
+/* Workspace of gs_attention_fwd, in bytes: of this descriptor, with its pointers
+ * and strides (what they do not let be read in place is packed first). */
 size_t gs_attention_fwd_workspace_bytes(const gs_attention *attention /* host */);
 
 /* Errors: GS_ERR_INVALID_ARG (NULL descriptor or arrays with rows, sizes or
@@ -854,7 +856,7 @@ gs_status gs_attention_fwd(const gs_attention *attention /* host */, void *works
  * dk and dv are sums over the heads that share k and v, and 0 for states that are
  * not attended.  For 16-bit types P and dS are rounded to the type for the last
  * products (fp16 ones times powers of two, so that small ones keep their bits).
- * Sums are taken in a fixed order.  The outputs must not overlap the inputs. */
+ * Sums are taken in a fixed order.  The outputs must overlap neither inputs nor one another. */
 typedef struct gs_attention_grads {
     const void *dout;           /* [batch][nq][heads][d] of `dtype`, as all    */
     int64_t dout_batch, dout_row, dout_head;
@@ -866,7 +868,7 @@ typedef struct gs_attention_grads {
     int64_t dv_batch, dv_row, dv_head;
 } gs_attention_grads;
 
-/* Workspace of gs_attention_bwd, in bytes. */
+/* Workspace of gs_attention_bwd, in bytes: of these descriptors. */
 size_t gs_attention_bwd_workspace_bytes(const gs_attention *attention /* host */, const gs_attention_grads *grads /* host */);
 
 /* Errors: as gs_attention_fwd; GS_ERR_INVALID_ARG for a missing lse or dout. */

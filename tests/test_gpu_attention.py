@@ -292,3 +292,21 @@ def test_broadcast_inputs():
         res.append([o, lse] + g)
     for x, y in zip(*res):
         assert torch.equal(x, y)
+
+
+def test_fp16_many_states_of_little_weight():
+    """4095 states 2^-20.5 of the first one's weight make up all of out: as fp16
+    times 1 they would lose 3 % (11.4 steps of 2^-24); times 2^6 half a step
+    is 2^-10.5 of them.  To that come out's rounding, 2^-11, and 2^-12 for 4096
+    additions in fp32.  1024 workgroups, which leave the states in one piece."""
+    nq, h, nk, d, s = 8192, 16, 4096, 8, 14.203125
+    k, v = torch.zeros(1, nk, 1, d), torch.ones(1, nk, 1, d)
+    k[0, 1:, 0, 0], v[0, 0] = -s, 0.0
+    k, v = k.half().cuda(), v.half().cuda()
+    q = torch.ones(1, nq, 1, d, dtype=torch.float16, device="cuda").expand(1, nq, h, d)
+    out = torch.empty(1, nq, h, d, dtype=torch.float16, device="cuda")
+    a = B.attention_struct(q, k, v, out, scale=1.0)
+    B.attention_fwd(a, torch.empty(max(16, B.attention_fwd_workspace_bytes(a)), dtype=torch.uint8, device="cuda"))
+    mass = (nk - 1) * np.exp(-s)
+    want = mass / (1 + mass)
+    assert float((out.double() - want).abs().max()) <= want * (2.0 ** -10.5 + 2.0 ** -11 + 2.0 ** -12)
