@@ -172,8 +172,8 @@ class ViewReader:
         tokens' = tokens + attention(q, k, v) w_o^T + b_o
 
     with `heads` heads of width / heads.  Views whose byte in `seen` is 0 are not
-    attended.  For the backward the maps are kept in 8 bits; `channels` and `width`
-    are multiples of 32."""
+    attended and give no gradient, whatever their maps hold.  For the backward the
+    maps are kept in 8 bits; `channels` and `width` are multiples of 32."""
 
     def __init__(self, m: int, width: int, views: int, pixels: int, channels: int, heads: int, groups: int,
                  dtype=torch.bfloat16, device="cuda", seed: int = 0):
@@ -195,7 +195,7 @@ class ViewReader:
         self.kept_scales = torch.empty((views, pixels, channels // 32), dtype=torch.uint8, device=device)
         self.kv, self.normed, self.rstd, self.q = e16(n, 2 * width), e16(m, width), f32(m), e16(m, width)
         self.read, self.lse, self.tokens, self.out = e16(m, width), f32(1, heads, m), e16(m, width), e16(m, width)
-        self.mask = torch.ones((1, n), dtype=torch.uint8, device=device)
+        self.mask, self.nothing = torch.ones((1, n), dtype=torch.uint8, device=device), torch.zeros((), dtype=dtype, device=device)
         self.d_out, self.d_read, self.d_q, self.d_kv = e16(m, width), e16(m, width), e16(m, width), e16(n, 2 * width)
         self.d_normed, self.d_tokens, self.d_features = e16(m, width), e16(m, width), e16(views, pixels, channels)
         # descriptors once: the buffers stay where they are
@@ -225,11 +225,17 @@ class ViewReader:
                              f"got {tuple(tokens.shape)} and {tuple(features.shape)}")
         if seen is not None and seen.shape != (self.views,):
             raise ValueError(f"seen: expected [{self.views}], got {tuple(seen.shape)}")
+        if features.dtype is not self.f.dtype or features.device != self.f.device:
+            raise ValueError(f"features: expected {self.f.dtype} on {self.f.device}, got {features.dtype} on {features.device}")
         mask = self.mask.view(self.views, self.pixels)
         if seen is None:
             mask.fill_(1)
         else:
-            mask.copy_((seen != 0).view(-1, 1).expand_as(mask))
+            there = (seen != 0).to(mask.device)
+            mask.copy_(there.view(-1, 1).expand_as(mask))
+            # zeros for what is not there: the backward multiplies every view's f and h by
+            # gradients of 0, which NaN and infinities would survive
+            features = torch.where(there.view(-1, 1, 1), features, self.nothing, out=self.f)
         self.tokens.copy_(tokens)
         B.group_norm_fwd(features, self.f, self.groups, gamma=self.gamma_f, beta=self.beta_f, act="silu", mean=self.mean, rstd=self.rstd_f,
                          kept=self.kept, kept_scales=self.kept_scales, workspace=self.ws)
