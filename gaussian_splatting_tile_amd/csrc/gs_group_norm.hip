@@ -10,13 +10,20 @@
 // many) are one workgroup's, in one launch; larger ones take two or three: sums
 // of blocks of pixels, joined per group, then the results.
 //
-// A channel's sums are of differences from a shift, the mean of eight of its
+// A channel's values are taken as differences from a shift, the mean of eight of its
 // pixels spread over the image, which every workgroup forms alike: an offset that
-// is large beside the spread costs no bits, and sums of parts add up.  Channels
-// are joined about their group's mean.  Everything is summed in a fixed order.
+// is large beside the spread costs no bits.  The shift need not be typical (all eight
+// may lie on a border): a part of the pixels is its sum S and its squares M about its own
+// mean, and parts of n_i values with the mean m join as S = sum S_i,
+// M = sum (M_i + n_i (S_i / n_i - m)^2), so that M never holds more than the spread
+// itself; eight values of a thread are the smallest part.  (Sums of squares about the
+// shift, two operations a value less: with those eight pixels at 0 and 65528 at 4096 +- 1
+// rstd was off by 1.2e-3, now by 2e-7; 8 x 65536 x 128 with checkpoint took 110 us, now 112.)
+// Channels are joined about their group's mean.  Everything is summed in a fixed order.
 #include "gs_numeric.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace gsi {
 namespace {
@@ -47,9 +54,9 @@ struct Args {
     uint8_t *kept, *kept_scales;
     const float *gamma, *beta;
     float *mean, *rstd;                         // [n][groups]
-    float *part;                                // [n][blocks][c][2] sums of blocks of pixels
+    float *part;                                // [n][blocks][c][2] sums of blocks of pixels (forward: S and M)
     float *shift;                               // forward: [n][c] what the sums' values are relative to
-    float *sums;                                // [n][c][2] sums of an image
+    float *sums;                                // [n][c][2] those of an image
     float *means;                               // backward: [n][groups][2] means of g and g h
     float *dgamma, *dbeta;
     int64_t x_image, x_pixel, xs_image, xs_pixel, dy_image, dy_pixel, y_image, y_pixel, k_image, k_pixel, ks_image, ks_pixel;
@@ -152,6 +159,41 @@ template <int N, class F, class U> __device__ __forceinline__ void each_pixel(co
 }
 
 // ---- forward -------------------------------------------------------------------
+// One over a number of pixels (of none: 1), to an ulp.
+__device__ __forceinline__ float one_over(float n) { return __builtin_amdgcn_rcpf(fmaxf(n, 1.0f)); }
+
+// A part of the pixels, n of them, or {}: none.
+struct Moments {
+    float s, q, n, mean;
+
+    __device__ __forceinline__ void add(const Moments &w)
+    {
+        const float share = one_over(n + w.n), e = w.mean - mean;
+        q = fmaf(e * (n * w.n * share), e, q + w.q);
+        s += w.s;
+        n += w.n;
+        mean = s * share;
+    }
+    // K parts at once.
+    template <int K> __device__ __forceinline__ void add(const Moments (&w)[K])
+    {
+        Moments t = {};
+#pragma unroll
+        for (int i = 0; i < K; i++) {
+            t.s += w[i].s;
+            t.q += w[i].q;
+            t.n += w[i].n;
+        }
+        t.mean = t.s * one_over(t.n);
+#pragma unroll
+        for (int i = 0; i < K; i++) {
+            const float e = w[i].mean - t.mean;
+            t.q = fmaf(e * w[i].n, e, t.q);
+        }
+        add(t);
+    }
+};
+
 // What the sums of the thread's channels are relative to.
 template <typename T> __device__ __forceinline__ void shift_of(const Args &a, int64_t image, const Place &t, float shift[8])
 {
@@ -167,30 +209,77 @@ template <typename T> __device__ __forceinline__ void shift_of(const Args &a, in
     }
 }
 
-// Sums of differences from the shift, and of their squares, over the thread's pixels of [p0, p1).
+// A channel's first `count` of N pixels as differences from its shift.  share: 1 / count.
+template <int N, typename T> __device__ __forceinline__ Moments moments_of(const Vec<T, 8> *w, int count, float share, int j, float shift)
+{
+    float d[N];
+    Moments m = {};
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        d[i] = i < count ? (float)w[i].v[j] - shift : 0.0f;
+        m.s += d[i];
+    }
+    m.mean = m.s * share;                       // what it is off by changes the squares by its own square
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        const float e = i < count ? d[i] - m.mean : 0.0f;
+        m.q = fmaf(e, e, m.q);
+    }
+    m.n = (float)count;
+    return m;
+}
+
+// S and M of the thread's pixels of [p0, p1).
 template <typename T> __device__ __forceinline__ void moments(const Args &a, int64_t image, int64_t p0, int64_t p1, const Place &t, const float shift[8], float s[8], float q[8])
 {
     const T *x = static_cast<const T *>(a.x) + image * a.x_image + t.at;
-    each_pixel<8>(t, p0, p1, [&](int64_t p) { return load(x + p * a.x_pixel, a); },
-                  [&](int64_t, const Vec<T, 8> &w) {
+    float n = 0.0f;
+    auto add = [&](auto size, const Vec<T, 8> *w, int count, float share) {
+        const float before = one_over(n);
 #pragma unroll
-                      for (int j = 0; j < 8; j++) {
-                          const float d = (float)w.v[j] - shift[j];
-                          s[j] += d;
-                          q[j] = fmaf(d, d, q[j]);
-                      }
-                  });
+        for (int j = 0; j < 8; j++) {
+            const Moments m = moments_of<decltype(size)::value>(w, count, share, j, shift[j]);
+            Moments all = {s[j], q[j], n, s[j] * before};
+            all.add(m);
+            s[j] = all.s;
+            q[j] = all.q;
+        }
+        n += (float)count;
+    };
+    int64_t p = p0 + t.sub;
+    Vec<T, 8> w[8];
+    for (; p + (int64_t)7 * t.step < p1; p += (int64_t)8 * t.step) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) w[i] = load(x + (p + (int64_t)i * t.step) * a.x_pixel, a);
+        add(std::integral_constant<int, 8>(), w, 8, 0.125f);
+    }
+    if (p >= p1) return;
+    int count = 0;                              // the last ones, in twos; past the last it is taken again, and not counted
+#pragma unroll
+    for (int i = 0; i < 8; i++) count += p + (int64_t)i * t.step < p1;
+#pragma unroll
+    for (int k = 0; k < 8; k += 4)
+        if (count > k)
+#pragma unroll
+            for (int i = k; i < k + 4; i++) w[i] = load(x + (p + (int64_t)min(i, count - 1) * t.step) * a.x_pixel, a);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2)
+        if (count > i) add(std::integral_constant<int, 2>(), w + i, min(count - i, 2), count > i + 1 ? 0.5f : 1.0f);
 }
 
 // Adds what the threads of a workgroup that share a chunk have for its
-// channels: channel i's two sums in LDS out[2 i ..].
-template <int THREADS> __device__ __forceinline__ void join_threads(const Args &a, const Place &t, int c0, const float s[8], const float q[8], float (*turn)[kTurn], float *out)
+// channels: channel i's two sums in LDS out[2 i ..].  MOMENTS: they are S and M of the
+// thread's share of `pixels`, and of all of these in the end.
+template <int THREADS, bool MOMENTS> __device__ __forceinline__ void join_threads(const Args &a, const Place &t, int c0, int64_t pixels, const float s[8], const float q[8], float (*turn)[kTurn], float *out)
 {
 #pragma unroll
     for (int j = 0; j < 8; j++) {
         turn[threadIdx.x][j] = s[j];
         turn[threadIdx.x][8 + j] = q[j];
     }
+    // the first `more` rows of threads have one pixel more than the others
+    const int each = (int)pixels / t.step, more = (int)pixels - each * t.step;
+    const float share = one_over((float)each), share_more = one_over((float)(each + 1));
     __syncthreads();
     // a channel's rows by as many threads as there are to a channel, a power of
     // two of neighbours
@@ -199,16 +288,33 @@ template <int THREADS> __device__ __forceinline__ void join_threads(const Args &
     while (parts < 8 && parts * 2 * all <= THREADS) parts *= 2;
     for (int k = threadIdx.x; k < all * parts; k += THREADS) {
         const int i = k / parts, chunk = i >> 3, j = (i & 7) + max(0, min(c0 + chunk * 8, a.c) + 8 - max(a.c, 8));
+        const int rows = c0 + i < a.c ? t.step : 0;
         float u = 0.0f, v = 0.0f;
-        if (c0 + i < a.c)
-            for (int r = k & (parts - 1); r < t.step; r += parts) {
+        if constexpr (MOMENTS) {
+            Moments sum = {};
+            for (int r = k & (parts - 1); r < rows; r += 4 * parts) {
+                Moments w[4] = {};
+#pragma unroll
+                for (int h = 0; h < 4; h++) {
+                    const int row = r + h * parts;
+                    if (row >= rows) continue;
+                    const float x = turn[row * a.ct + chunk][j];
+                    w[h] = {x, turn[row * a.ct + chunk][8 + j], (float)(each + (row < more)), x * (row < more ? share_more : share)};
+                }
+                sum.add(w);
+            }
+            u = sum.s;
+            for (int o = parts / 2; o > 0; o >>= 1) u += __shfl_xor(u, o);
+            const float e = sum.mean - u * one_over((float)(int)pixels);
+            v = fmaf(e * sum.n, e, sum.q);
+        } else {
+            for (int r = k & (parts - 1); r < rows; r += parts) {
                 u += turn[r * a.ct + chunk][j];
                 v += turn[r * a.ct + chunk][8 + j];
             }
-        for (int o = parts / 2; o > 0; o >>= 1) {
-            u += __shfl_xor(u, o);
-            v += __shfl_xor(v, o);
+            for (int o = parts / 2; o > 0; o >>= 1) u += __shfl_xor(u, o);
         }
+        for (int o = parts / 2; o > 0; o >>= 1) v += __shfl_xor(v, o);
         if ((k & (parts - 1)) == 0) {
             out[2 * i] = u;
             out[2 * i + 1] = v;
@@ -254,7 +360,7 @@ template <typename T> __global__ __launch_bounds__(kThreads, 4) void sum_moments
                 if (j >= t.skip && j < a.c) a.shift[w.image * a.c + t.at + j] = shift[j];
     }
     const int c0 = w.tile * a.ct * 8, wide = 2 * min(a.ct * 8, a.c - c0);
-    join_threads<kThreads>(a, t, c0, s, q, turn, out);
+    join_threads<kThreads, true>(a, t, c0, p1 - p0, s, q, turn, out);
     float *part = a.part + ((w.image * a.blocks + w.block) * a.c + c0) * 2;
     for (int i = threadIdx.x; i < wide; i += kThreads) part[i] = out[i];
 }
@@ -271,6 +377,24 @@ template <int THREADS> __device__ __forceinline__ float block_sum(float x, float
 #pragma unroll
     for (int w = 0; w < THREADS / 64; w++) x += lds[w];
     return x;
+}
+
+// S and M of a channel over the blocks of pixels b, b + step, .. , eight loads on their way at once.
+__device__ __forceinline__ Moments block_moments(const Args &a, const float2 *part, int b, int step)
+{
+    const float pixels = (float)(int)a.per, last = (float)(int)(a.p - (a.blocks - 1) * a.per), share = one_over(pixels), share_last = one_over(last);
+    Moments sum = {};
+    for (; b < a.blocks; b += 8 * step) {
+        Moments w[8] = {};
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const int k = b + i * step;
+            const float2 x = k < a.blocks ? part[(int64_t)k * a.c] : float2{0.0f, 0.0f};
+            w[i] = {x.x, x.y, k < a.blocks - 1 ? pixels : k < a.blocks ? last : 0.0f, x.x * (k < a.blocks - 1 ? share : share_last)};
+        }
+        sum.add(w);
+    }
+    return sum;
 }
 
 // Adds a group's channels' two sums over the blocks of pixels, up to 256 channels
@@ -298,13 +422,36 @@ template <class F> __device__ __forceinline__ void join_blocks(const Args &a, in
         each(g * a.cg + c, u, v);
     }
 }
+// Their S and M in the same way.
+template <class F> __device__ __forceinline__ void join_block_moments(const Args &a, int64_t image, int g, Moments *turn, F each)
+{
+    const float2 *part = reinterpret_cast<const float2 *>(a.part) + image * a.blocks * a.c + (int64_t)g * a.cg;
+    for (int c0 = 0; c0 < a.cg; c0 += kThreads) {
+        const int wide = min(kThreads, a.cg - c0), step = min(kThreads / wide, (a.blocks + 7) / 8), sub = threadIdx.x / wide, c = c0 + threadIdx.x - sub * wide;
+        Moments sum = {};
+        if (sub < step) sum = block_moments(a, part + c, sub, step);
+        __syncthreads();
+        turn[threadIdx.x] = sum;
+        __syncthreads();
+        if (sub) continue;
+        for (int r = 1; r < step; r += 4) {
+            Moments w[4] = {};
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                if (r + i < step) w[i] = turn[(r + i) * wide + threadIdx.x];
+            sum.add(w);
+        }
+        each(g * a.cg + c, sum.s, sum.q);
+    }
+}
 
 // More channels than a workgroup that writes would join (kJoinChannels): a group's
 // statistics at once, its channels' means relative to the first one's shift, then
 // squares about the mean of those.
 __global__ __launch_bounds__(kThreads) void join_groups(Args a)
 {
-    __shared__ float turn[kThreads][2], lds[kThreads / 64];
+    __shared__ Moments turn[kThreads];
+    __shared__ float lds[kThreads / 64];
     const int64_t item = block_of();
     if (item >= (int64_t)a.n * a.groups) return;
     const int64_t image = item / a.groups;
@@ -313,10 +460,10 @@ __global__ __launch_bounds__(kThreads) void join_groups(Args a)
     const float pixels = (float)a.p, first = shift[(int64_t)g * a.cg];
     float m = 0.0f, q = 0.0f;
     __syncthreads();                            // every thread has `first`
-    join_blocks(a, image, g, turn, [&](int c, float s, float sq) {
-        const float d = s / pixels, far = shift[c] - first + d;
+    join_block_moments(a, image, g, turn, [&](int c, float s, float sq) {
+        const float far = shift[c] - first + s / pixels;
         m += far;
-        q += fmaf(-s, d, sq);
+        q += sq;
         shift[c] = far;                         // for this thread, below
     });
     m = block_sum<kThreads>(m, lds) / (float)a.cg;
@@ -409,8 +556,8 @@ template <int THREADS> __device__ __forceinline__ void group_statistics(const Ar
         for (int o = 32; o > 0; o >>= 1) m += __shfl_xor(m, o);
         m /= (float)a.cg;
         for (int c = c0 + (threadIdx.x & 63); c < c0 + a.cg; c += 64) {
-            const float s = sums[2 * c], d = shifts[c] - first + s / pixels - m;
-            q += fmaf(pixels * d, d, fmaf(-s, s / pixels, sums[2 * c + 1]));
+            const float d = shifts[c] - first + sums[2 * c] / pixels - m;
+            q += fmaf(pixels * d, d, sums[2 * c + 1]);
         }
 #pragma unroll
         for (int o = 32; o > 0; o >>= 1) q += __shfl_xor(q, o);
@@ -444,6 +591,16 @@ __device__ __forceinline__ void image_sums(const Args &a, int64_t image, float *
     }
 }
 
+// Its channels' S and M over as few.
+__device__ __forceinline__ void image_moments(const Args &a, int64_t image, float *sums)
+{
+    for (int c = threadIdx.x; c < a.c; c += kThreads) {
+        const Moments m = block_moments(a, reinterpret_cast<const float2 *>(a.part) + image * a.blocks * a.c + c, 0, 1);
+        sums[2 * c] = m.s;
+        sums[2 * c + 1] = m.q;
+    }
+}
+
 // JOIN: every workgroup forms the statistics itself, from few blocks' sums.
 template <typename T, int G, bool JOIN> __global__ __launch_bounds__(kThreads, 4) void write_norm(Args a)
 {
@@ -455,7 +612,7 @@ template <typename T, int G, bool JOIN> __global__ __launch_bounds__(kThreads, 4
     load_channels(a, a.gamma, t, 1.0f, scale);
     load_channels(a, a.beta, t, 0.0f, shift);
     if constexpr (JOIN) {
-        image_sums(a, w.image, sums);
+        image_moments(a, w.image, sums);
         for (int c = threadIdx.x; c < a.c; c += kThreads) shifts[c] = a.shift[w.image * a.c + c];
         __syncthreads();
         group_statistics<kThreads>(a, w.image, shifts, sums, means, rstds, w.block == 0);
@@ -484,18 +641,17 @@ template <typename T, int G, bool HELD> __global__ __launch_bounds__(kOneThreads
     if (t.works) {
         if constexpr (HELD) {
 #pragma unroll
-            for (int i = 0; i < kHeld; i++)
-                if (t.sub + i * t.step < a.p) held[i] = load(x + (int64_t)(t.sub + i * t.step) * a.x_pixel, a);
+            for (int i = 0; i < kHeld; i++) held[i] = load(x + (t.sub + i * t.step < a.p ? t.sub + i * t.step : 0) * a.x_pixel, a);
             shift_of<T>(a, image, t, near);
+            int count = 0;
 #pragma unroll
-            for (int i = 0; i < kHeld; i++)
-                if (t.sub + i * t.step < a.p)
+            for (int i = 0; i < kHeld; i++) count += t.sub + i * t.step < a.p;
 #pragma unroll
-                    for (int j = 0; j < 8; j++) {
-                        const float d = (float)held[i].v[j] - near[j];
-                        s[j] += d;
-                        q[j] = fmaf(d, d, q[j]);
-                    }
+            for (int j = 0; j < 8; j++) {
+                const Moments m = moments_of<kHeld>(held, count, one_over((float)count), j, near[j]);
+                s[j] = m.s;
+                q[j] = m.q;
+            }
         } else {
             shift_of<T>(a, image, t, near);
             moments<T>(a, image, 0, a.p, t, near, s, q);
@@ -505,7 +661,7 @@ template <typename T, int G, bool HELD> __global__ __launch_bounds__(kOneThreads
             for (int j = 0; j < 8; j++)
                 if (j >= t.skip && j < a.c) shifts[t.at + j] = near[j];
     }
-    join_threads<kOneThreads>(a, t, 0, s, q, turn, out);
+    join_threads<kOneThreads, true>(a, t, 0, a.p, s, q, turn, out);
     group_statistics<kOneThreads>(a, image, shifts, out, means, rstds, true);
     if (!t.works) return;
     coefficients<G>(a, means, rstds, t, mean, scale);
@@ -591,7 +747,7 @@ template <typename T, bool Q8, int G, int THREADS> __device__ __forceinline__ vo
                               sh[j] = fmaf(dz[j], h[j], sh[j]);
                           }
                       });
-    join_threads<THREADS>(a, t, c0, s, sh, turn, out);
+    join_threads<THREADS, false>(a, t, c0, p1 - p0, s, sh, turn, out);
 }
 
 template <typename T, bool Q8, int G> __global__ __launch_bounds__(kThreads, 4) void sum_gradients(Args a)
@@ -704,17 +860,35 @@ __device__ __forceinline__ float2 sum_rows_of(const float2 *part, int64_t rows, 
         }
     return s;
 }
-
-// A channel's sums over an image's blocks: what the workgroups that write then join
-// as one block's.
-__global__ __launch_bounds__(kThreads) void join_channels(Args a, float *to)
+// S and M of 16 channels over an image's blocks in the same way.
+__device__ __forceinline__ float2 join_rows_of(const Args &a, const float2 *part, int c0, Moments *turn)
 {
-    __shared__ float2 turn[kThreads];
+    const int c = c0 + (threadIdx.x & 15);
+    Moments s = {};
+    if (c < a.c) s = block_moments(a, part + c, threadIdx.x >> 4, 16);
+    turn[threadIdx.x] = s;
+    __syncthreads();
+    Moments sum = {};
+    if (threadIdx.x < 16) {
+        Moments w[16] = {};
+#pragma unroll
+        for (int r = 0; r < 16; r++) w[r] = turn[r * 16 + threadIdx.x];
+        sum.add(w);
+    }
+    return float2{sum.s, sum.q};
+}
+
+// A channel's sums over an image's blocks (MOMENTS: S and M): what the workgroups
+// that write then join as one block's.
+template <bool MOMENTS> __global__ __launch_bounds__(kThreads) void join_channels(Args a, float *to)
+{
+    __shared__ __align__(16) Moments turn[kThreads];
     const int64_t slices = (a.c + 15) / 16, item = block_of();
     if (item >= a.n * slices) return;
     const int64_t image = item / slices;
     const int c0 = (int)(item - image * slices) * 16;
-    const float2 s = sum_rows_of(reinterpret_cast<const float2 *>(a.part) + image * a.blocks * a.c, a.blocks, c0, a.c, turn);
+    const float2 *part = reinterpret_cast<const float2 *>(a.part) + image * a.blocks * a.c;
+    const float2 s = MOMENTS ? join_rows_of(a, part, c0, turn) : sum_rows_of(part, a.blocks, c0, a.c, reinterpret_cast<float2 *>(turn));
     if (threadIdx.x < 16 && c0 + (int)threadIdx.x < a.c) reinterpret_cast<float2 *>(to)[image * a.c + c0 + threadIdx.x] = s;
 }
 
@@ -857,11 +1031,11 @@ void set_shape(Args &a, const Shape &s, const Plan &w, int es)
 // first.  Else a workgroup joins each group (8 x 65536 x 128: 110 us, 119 by channels).
 bool few_blocks(const Args &a) { return a.blocks <= kJoinBlocks && (int64_t)a.n * a.blocks <= 1024; }
 bool by_channels(const Args &a) { return a.c <= kJoinChannels && (few_blocks(a) || a.cg > 64 || (int64_t)a.n * a.groups < 64); }
-Args joined(const Args &a, hipStream_t s)
+template <bool MOMENTS> Args joined(const Args &a, hipStream_t s)
 {
     Args b = a;
     if (few_blocks(a)) return b;
-    join_channels<<<grid_of((int64_t)a.n * ((a.c + 15) / 16), kThreads), kThreads, 0, s>>>(a, a.sums);
+    join_channels<MOMENTS><<<grid_of((int64_t)a.n * ((a.c + 15) / 16), kThreads), kThreads, 0, s>>>(a, a.sums);
     b.part = a.sums;
     b.blocks = 1;
     return b;
@@ -877,7 +1051,7 @@ template <typename T, int G> hipError_t launch_fwd(const Args &a, bool one, hipS
     sum_moments<T><<<grid_of((int64_t)a.n * a.blocks * a.tiles, kThreads), kThreads, 0, s>>>(a);
     const dim3 out = grid_of((int64_t)a.n * a.blocks_out * a.tiles, kThreads);
     if (by_channels(a)) {
-        write_norm<T, G, true><<<out, kThreads, 0, s>>>(joined(a, s));
+        write_norm<T, G, true><<<out, kThreads, 0, s>>>(joined<true>(a, s));
         return hipGetLastError();
     }
     join_groups<<<grid_of((int64_t)a.n * a.groups, kThreads), kThreads, 0, s>>>(a);
@@ -900,7 +1074,7 @@ template <typename T, bool Q8, int G> hipError_t launch_bwd(const Args &a, bool 
     sum_gradients<T, Q8, G><<<grid_of((int64_t)a.n * a.blocks * a.tiles, kThreads), kThreads, 0, s>>>(a);
     const dim3 out = grid_of((int64_t)a.n * a.blocks_out * a.tiles + (wanted ? sums : 0), kThreads);
     if (by_channels(a)) {
-        write_gradient<T, Q8, G, true><<<out, kThreads, 0, s>>>(joined(a, s));
+        write_gradient<T, Q8, G, true><<<out, kThreads, 0, s>>>(joined<false>(a, s));
         return hipGetLastError();
     }
     join_gradients<<<grid_of((int64_t)a.n * a.groups, kThreads), kThreads, 0, s>>>(a);

@@ -1,0 +1,63 @@
+"""Group norm's statistics where a few pixels are unlike the others, as a
+border, padding or dead pixels are.
+
+Tolerances.  e = 2^-24; x is fp32, D the largest difference of two of a
+channel's values and sd the group's spread.  Values are taken as differences d from
+one of a channel's values or a mean of some, so |d| <= D, each rounded by e D.
+A sum of r terms one after the other is off by r / 2 e D at most of the mean
+of its terms.  Eight values (4.4 with the first addition), up to 12 such sums of a
+thread and 12 of threads (6 each, four at a time), blocks of pixels eight at a time,
+rows of 16 (10) and their reciprocals (1.6): a mean is off by 28 e D at most.
+* variance: squares of differences of such means, every one a part of the spread,
+  so 2 x 28 e D / sd of itself (what the mean in the middle is off by counts squared); sums
+  of squares themselves 12 e for eight and less than 20 e for what joins them.
+* rstd is off by half of what the variance is, and the mean by 28 e D and its own
+  rounding.
+"""
+
+import pytest
+import torch
+
+from gaussian_splatting_tile_amd import binding as B
+from tests.test_gpu_attention import E, _close, _ws
+
+pytestmark = pytest.mark.gpu
+
+
+def _statistics(x, groups):
+    n, p, c = x.shape
+    y, mean, rstd = torch.empty_like(x), torch.empty(n, groups, device="cuda"), torch.empty(n, groups, device="cuda")
+    B.group_norm_fwd(x, y, groups, mean=mean, rstd=rstd, workspace=_ws(B.group_norm_fwd_workspace_bytes(n, p, c, groups))[0])
+    return y, mean, rstd
+
+
+# one workgroup's (values held; read again), sums joined by the workgroups that write, by channels first, by groups
+SHAPES = [(1, 64, 32, 8), (128, 1024, 24, 3), (2, 2048, 24, 3), (1, 65536, 16, 2), (2, 65536, 128, 32)]
+
+
+@pytest.mark.parametrize("n,p,c,groups", SHAPES)
+@pytest.mark.parametrize("kind", ["left column", "eight pixels", "first row", "one pixel", "none"])
+def test_variance_of_maps_with_unlike_pixels(n, p, c, groups, kind):
+    """4096 +- 1, and 0 in some pixels: maps of 8 rows or a multiple have an eighth of
+    their pixels apart, in a column, the places that a sample spread evenly would take."""
+    gen = torch.Generator("cuda").manual_seed(p + c)
+    x = 4096.0 + torch.randn(n, p, c, generator=gen, device="cuda")
+    rows = 8 if p < 65536 else 64
+    if kind == "left column":
+        x.view(n, rows, p // rows, c)[:, :, 0] = 0.0
+    elif kind == "eight pixels":
+        x[:, ::p // 8] = 0.0
+    elif kind == "first row":
+        x.view(n, rows, p // rows, c)[:, 0] = 0.0
+    elif kind == "one pixel":
+        x[:, 0] = 0.0
+    y, mean, rstd = _statistics(x, groups)
+    v = x.double().view(n, p, groups, c // groups)
+    m64 = v.mean((1, 3))
+    var = (v - m64[:, None, :, None]).square().mean((1, 3))
+    far = (x.amax(1) - x.amin(1)).double().view(n, groups, -1).amax(2)
+    r64 = 1 / (var + 1e-5).sqrt()
+    tol = (32 + 56 * far / var.sqrt()) * E / 2 * r64
+    host = lambda t: t.double().cpu().numpy()
+    _close(host(rstd), host(r64), host(tol), "rstd")
+    _close(host(mean), host(m64), host(28 * E * far + 2 * E * m64.abs()), "mean")
