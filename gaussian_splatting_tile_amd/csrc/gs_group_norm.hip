@@ -19,7 +19,8 @@
 // itself; eight values of a thread are the smallest part.  (Sums of squares about the
 // shift, two operations a value less: with those eight pixels at 0 and 65528 at 4096 +- 1
 // rstd was off by 1.2e-3, now by 2e-7; 8 x 65536 x 128 with checkpoint took 110 us, now 112.)
-// Channels are joined about their group's mean.  Everything is summed in a fixed order.
+// Channels are joined in fp64, relative to their group's first one.  Everything is summed in
+// a fixed order.
 #include "gs_numeric.h"
 
 #include <algorithm>
@@ -366,18 +367,39 @@ template <typename T> __global__ __launch_bounds__(kThreads, 4) void sum_moments
 }
 
 // Sum over the threads of a workgroup.
-template <int THREADS> __device__ __forceinline__ float block_sum(float x, float *lds)
+template <int THREADS, typename T> __device__ __forceinline__ T block_sum(T x, T *lds)
 {
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);
     __syncthreads();                            // the last use of lds is over
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
     __syncthreads();
-    x = 0.0f;
+    x = 0;
 #pragma unroll
     for (int w = 0; w < THREADS / 64; w++) x += lds[w];
     return x;
 }
+
+// A group's channels: the sums of their means' distances from the first channel's shift and of
+// their squares about it.  In fp64, as channels may lie far apart and the mean is good to
+// its own rounding then (in fp32 it was off by 4e-5 for channels of -1000 to 1000).
+struct Group {
+    double m, q;
+
+    __device__ __forceinline__ void add(float shift, float first, float s, float q1, double pixels, double share)
+    {
+        const double far = (double)shift - (double)first + (double)s * share;
+        m += far;
+        q += fma(far * far, pixels, (double)q1);
+    }
+    // mean and rstd of cg channels
+    __device__ __forceinline__ float2 statistics(float first, int cg, double pixels, double share, float eps) const
+    {
+        const double part = 1.0 / (double)cg, far = m * part;
+        const float var = (float)(fma(q * part, share, -far * far));
+        return float2{(float)((double)first + far), 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + eps)};
+    }
+};
 
 // S and M of a channel over the blocks of pixels b, b + step, .. , eight loads on their way at once.
 __device__ __forceinline__ Moments block_moments(const Args &a, const float2 *part, int b, int step)
@@ -445,36 +467,25 @@ template <class F> __device__ __forceinline__ void join_block_moments(const Args
     }
 }
 
-// More channels than a workgroup that writes would join (kJoinChannels): a group's
-// statistics at once, its channels' means relative to the first one's shift, then
-// squares about the mean of those.
+// A group's statistics by a workgroup, where those that write do not join them themselves.
 __global__ __launch_bounds__(kThreads) void join_groups(Args a)
 {
     __shared__ Moments turn[kThreads];
-    __shared__ float lds[kThreads / 64];
+    __shared__ double lds[kThreads / 64];
     const int64_t item = block_of();
     if (item >= (int64_t)a.n * a.groups) return;
     const int64_t image = item / a.groups;
     const int g = (int)(item - image * a.groups);
-    float *shift = a.shift + image * a.c;
-    const float pixels = (float)a.p, first = shift[(int64_t)g * a.cg];
-    float m = 0.0f, q = 0.0f;
-    __syncthreads();                            // every thread has `first`
-    join_block_moments(a, image, g, turn, [&](int c, float s, float sq) {
-        const float far = shift[c] - first + s / pixels;
-        m += far;
-        q += sq;
-        shift[c] = far;                         // for this thread, below
-    });
-    m = block_sum<kThreads>(m, lds) / (float)a.cg;
-    for (int c = threadIdx.x; c < a.cg; c += kThreads) {
-        const float d = shift[(int64_t)g * a.cg + c] - m;
-        q = fmaf(pixels * d, d, q);
-    }
-    q = block_sum<kThreads>(q, lds);
+    const float *shift = a.shift + image * a.c, first = shift[(int64_t)g * a.cg];
+    const double pixels = (double)a.p, share = 1.0 / pixels;
+    Group sum = {};
+    join_block_moments(a, image, g, turn, [&](int c, float s, float q) { sum.add(shift[c], first, s, q, pixels, share); });
+    sum.m = block_sum<kThreads>(sum.m, lds);
+    sum.q = block_sum<kThreads>(sum.q, lds);
     if (threadIdx.x) return;
-    a.mean[item] = first + m;
-    a.rstd[item] = 1.0f / sqrtf((q < 0.0f ? 0.0f : q) / (pixels * (float)a.cg) + a.eps);
+    const float2 w = sum.statistics(first, a.cg, pixels, share, a.eps);
+    a.mean[item] = w.x;
+    a.rstd[item] = w.y;
 }
 
 // y (and the 8-bit x) of one pixel's eight channels.
@@ -542,31 +553,27 @@ template <int G> __device__ __forceinline__ void coefficients(const Args &a, con
     for (int j = 0; j < 8; j++) scale[j] *= rstd[j * G / 8];
 }
 
-// Statistics of an image's groups from its channels' sums, a wave per group, as in
-// join_groups; all in LDS, and in mean and rstd (`keep`).
+// Statistics of an image's groups from its channels' sums, a wave per group; all in
+// LDS, and in mean and rstd (`keep`).
 template <int THREADS> __device__ __forceinline__ void group_statistics(const Args &a, int64_t image, const float *shifts, const float *sums, float *means, float *rstds, bool keep)
 {
-    const float pixels = (float)a.p;
+    const double pixels = (double)a.p, share = 1.0 / pixels;
     for (int g = threadIdx.x >> 6; g < a.groups; g += THREADS / 64) {
         const int c0 = g * a.cg;
         const float first = shifts[c0];
-        float m = 0.0f, q = 0.0f;
-        for (int c = c0 + (threadIdx.x & 63); c < c0 + a.cg; c += 64) m += shifts[c] - first + sums[2 * c] / pixels;
+        Group sum = {};
+        for (int c = c0 + (threadIdx.x & 63); c < c0 + a.cg; c += 64) sum.add(shifts[c], first, sums[2 * c], sums[2 * c + 1], pixels, share);
 #pragma unroll
-        for (int o = 32; o > 0; o >>= 1) m += __shfl_xor(m, o);
-        m /= (float)a.cg;
-        for (int c = c0 + (threadIdx.x & 63); c < c0 + a.cg; c += 64) {
-            const float d = shifts[c] - first + sums[2 * c] / pixels - m;
-            q += fmaf(pixels * d, d, sums[2 * c + 1]);
+        for (int o = 32; o > 0; o >>= 1) {
+            sum.m += __shfl_xor(sum.m, o);
+            sum.q += __shfl_xor(sum.q, o);
         }
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) q += __shfl_xor(q, o);
         if (threadIdx.x & 63) continue;
-        const float r = 1.0f / sqrtf((q < 0.0f ? 0.0f : q) / (pixels * (float)a.cg) + a.eps);
-        means[g] = first + m;
-        rstds[g] = r;
-        if (keep && a.mean) a.mean[image * a.groups + g] = first + m;
-        if (keep && a.rstd) a.rstd[image * a.groups + g] = r;
+        const float2 w = sum.statistics(first, a.cg, pixels, share, a.eps);
+        means[g] = w.x;
+        rstds[g] = w.y;
+        if (keep && a.mean) a.mean[image * a.groups + g] = w.x;
+        if (keep && a.rstd) a.rstd[image * a.groups + g] = w.y;
     }
     __syncthreads();
 }

@@ -1,5 +1,5 @@
 """Group norm's statistics where a few pixels are unlike the others, as a
-border, padding or dead pixels are.
+border, padding or dead pixels are, and where channels of a group lie far apart.
 
 Tolerances.  e = 2^-24; x is fp32, D the largest difference of two of a
 channel's values and sd the group's spread.  Values are taken as differences d from
@@ -15,10 +15,12 @@ rows of 16 (10) and their reciprocals (1.6): a mean is off by 28 e D at most.
   rounding.
 """
 
+import numpy as np
 import pytest
 import torch
 
 from gaussian_splatting_tile_amd import binding as B
+from oracle import attention as A
 from tests.test_gpu_attention import E, _close, _ws
 
 pytestmark = pytest.mark.gpu
@@ -61,3 +63,18 @@ def test_variance_of_maps_with_unlike_pixels(n, p, c, groups, kind):
     host = lambda t: t.double().cpu().numpy()
     _close(host(rstd), host(r64), host(tol), "rstd")
     _close(host(mean), host(m64), host(28 * E * far + 2 * E * m64.abs()), "mean")
+
+
+@pytest.mark.parametrize("n,p,c,groups", [(1, 64, 60, 4), (128, 1016, 24, 3), (2, 1000, 90, 6), (1, 9001, 24, 2), (2, 8008, 128, 32), (1, 200, 1800, 3)])
+def test_mean_of_channels_that_lie_far_apart(n, p, c, groups):
+    """Values on a grid of 2^-4 on which every channel's sums are exact (below 2^23
+    steps of 2^-7, the grid of a mean of eight): what is left of the mean's error is the
+    joining of the channels, and its own rounding, 2^-24 of itself."""
+    rng = np.random.default_rng(p + c)
+    x = rng.integers(-32, 33, (n, p, c)) / 16.0
+    x += np.round(np.linspace(1000, -1000, c // groups))[np.arange(c) % (c // groups)] + 0.125
+    x = torch.from_numpy(x).float().cuda()
+    _, mean, rstd = _statistics(x, groups)
+    m64, r64, _, _ = A.group_norm(x.double().cpu().numpy(), groups)
+    _close(mean.double().cpu().numpy(), m64, 1.001 * E * np.abs(m64), "mean")
+    _close(rstd.double().cpu().numpy(), r64, 16 * E * r64, "rstd")
