@@ -173,11 +173,12 @@ class ViewReader:
 
     with `heads` heads of width / heads.  Views whose byte in `seen` is 0 are not
     attended and give no gradient, whatever their maps hold.  For the backward the
-    maps are kept in 8 bits; `channels` and `width` are multiples of 32."""
+    maps are kept in 8 bits; `channels` and `width` are multiples of 32, a head has 128
+    channels at most, and `groups` divides `channels`."""
 
     def __init__(self, m: int, width: int, views: int, pixels: int, channels: int, heads: int, groups: int,
                  dtype=torch.bfloat16, device="cuda", seed: int = 0):
-        assert width % 32 == 0 and channels % 32 == 0 and width % heads == 0
+        assert width % 32 == 0 and channels % 32 == 0 and width % heads == 0 and width // heads <= 128 and channels % groups == 0
         self.m, self.width, self.views, self.pixels, self.channels, self.heads, self.groups = m, width, views, pixels, channels, heads, groups
         gen = torch.Generator(device=device).manual_seed(seed)
         rand = lambda *s, scale: (torch.randn(s, generator=gen, device=device) * scale).to(dtype)
