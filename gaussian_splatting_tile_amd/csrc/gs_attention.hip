@@ -294,7 +294,10 @@ Work work_of(const gs_attention *p, Product what, int waves, int64_t columns, in
     Work w = {};
     w.t = {waves, (int)((columns + waves * 32 - 1) / (waves * 32)), 1};
     w.cost = cost_of(p, what);
-    if (waves == 1) w.cost = {1.2, w.cost.shared / 4, 4};               // a quarter of the work, and less to hide it behind
+    // single waves: a quarter of the work, and less to hide it behind.  One estimate for every
+    // type and width, though LDS lets four and more of 16 bits and d <= 64 share a CU, three
+    // of fp32 and d <= 64, two of 16 bits above and one of fp32 above
+    if (waves == 1) w.cost = {1.2, w.cost.shared / 4, 4};
     w.blocks = pairs * w.t.tiles;
     w.other = other;
     w.part = 0.03 + (double)w.blocks * waves * 32 * padded(p->d) * 4 * 2 * (what == kStates ? 2 : 1) / 7e6;

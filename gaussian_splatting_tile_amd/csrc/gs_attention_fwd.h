@@ -132,7 +132,7 @@ template <int KIND, int NL, int DP, int NW> __global__ __launch_bounds__(NW * 64
     }
 
     sum = pair_sum(sum);
-    if (a.t.splits > 1) {                         // as they are, for join_fwd
+    if (a.t.splits > 1) {                         // as they are, for join_splits
         const int64_t at = part_at(a, a.t, it, wave);
         store_part<DP>(a.part, at, o, 1.0f, lane);
         if (lane < 32) *reinterpret_cast<float2 *>(a.ml + (at * 32 + lane) * 2) = float2{m, sum};

@@ -62,7 +62,7 @@ struct Args {
     float *dgamma, *dbeta;
     int64_t x_image, x_pixel, xs_image, xs_pixel, dy_image, dy_pixel, y_image, y_pixel, k_image, k_pixel, ks_image, ks_pixel;
     int64_t p, per, per_out;                    // pixels of an image, of a block that sums, of one that writes
-    int n, c, groups, cg, chunks, ct, tiles;    // ct: chunks of a block's channels; tiles of them
+    int n, c, groups, cg, ct, tiles;            // ct: chunks of a block's channels; tiles of them
     int blocks, blocks_out, act, accumulate;
     int stream;                                 // results are written past the caches
     float eps;
@@ -344,7 +344,7 @@ __device__ __forceinline__ Part part_of(const Args &a, int blocks)
 
 template <typename T> __global__ __launch_bounds__(kThreads, 4) void sum_moments(Args a)
 {
-    __shared__ float turn[kThreads][kTurn], out[kThreads * 16];
+    __shared__ float turn[kThreads][kTurn], out[kTileChunks * 16];
     const Part w = part_of(a, a.blocks);
     if (!w.there) return;
     const int64_t p0 = w.block * a.per, p1 = min(a.p, p0 + a.per);
@@ -759,7 +759,7 @@ template <typename T, bool Q8, int G, int THREADS> __device__ __forceinline__ vo
 
 template <typename T, bool Q8, int G> __global__ __launch_bounds__(kThreads, 4) void sum_gradients(Args a)
 {
-    __shared__ float turn[kThreads][kTurn], out[kThreads * 16];
+    __shared__ float turn[kThreads][kTurn], out[kTileChunks * 16];
     const Part w = part_of(a, a.blocks);
     if (!w.there) return;
     const int64_t p0 = w.block * a.per, p1 = min(a.p, p0 + a.per);
@@ -1022,7 +1022,6 @@ void set_shape(Args &a, const Shape &s, const Plan &w, int es)
     a.c = s.c;
     a.groups = s.groups;
     a.cg = s.c / s.groups;
-    a.chunks = (s.c + 7) / 8;
     a.ct = w.ct;
     a.tiles = w.tiles;
     a.blocks = w.blocks;
