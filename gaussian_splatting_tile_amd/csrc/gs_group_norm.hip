@@ -16,15 +16,14 @@
 // may lie on a border): a part of the pixels is its sum S and its squares M about its own
 // mean, and parts of n_i values with the mean m join as S = sum S_i,
 // M = sum (M_i + n_i (S_i / n_i - m)^2), so that M never holds more than the spread
-// itself; eight values of a thread are the smallest part.  (Sums of squares about the
-// shift, two operations a value less: with those eight pixels at 0 and 65528 at 4096 +- 1
+// itself; single values are the smallest part.  (Sums of squares about the shift, two
+// operations a value less: with those eight pixels at 0 and 65528 at 4096 +- 1
 // rstd was off by 1.2e-3, now by 2e-7; 8 x 65536 x 128 with checkpoint took 110 us, now 112.)
 // Channels are joined in fp64, relative to their group's first one.  Everything is summed in
 // a fixed order.
 #include "gs_numeric.h"
 
 #include <algorithm>
-#include <type_traits>
 
 namespace gsi {
 namespace {
@@ -210,63 +209,25 @@ template <typename T> __device__ __forceinline__ void shift_of(const Args &a, in
     }
 }
 
-// A channel's first `count` of N pixels as differences from its shift.  share: 1 / count.
-template <int N, typename T> __device__ __forceinline__ Moments moments_of(const Vec<T, 8> *w, int count, float share, int j, float shift)
-{
-    float d[N];
-    Moments m = {};
-#pragma unroll
-    for (int i = 0; i < N; i++) {
-        d[i] = i < count ? (float)w[i].v[j] - shift : 0.0f;
-        m.s += d[i];
-    }
-    m.mean = m.s * share;                       // what it is off by changes the squares by its own square
-#pragma unroll
-    for (int i = 0; i < N; i++) {
-        const float e = i < count ? d[i] - m.mean : 0.0f;
-        m.q = fmaf(e, e, m.q);
-    }
-    m.n = (float)count;
-    return m;
-}
+// One more pixel in S and M of a thread's channels: with its difference e from the mean
+// of the n before, M grows by n / (n + 1) e^2.
+template <typename T> struct ThreadMoments {
+    float s[8], q[8], n, share;                 // share: one over n
 
-// S and M of the thread's pixels of [p0, p1).
-template <typename T> __device__ __forceinline__ void moments(const Args &a, int64_t image, int64_t p0, int64_t p1, const Place &t, const float shift[8], float s[8], float q[8])
-{
-    const T *x = static_cast<const T *>(a.x) + image * a.x_image + t.at;
-    float n = 0.0f;
-    auto add = [&](auto size, const Vec<T, 8> *w, int count, float share) {
-        const float before = one_over(n);
+    __device__ __forceinline__ void add(const Vec<T, 8> &w, const float shift[8])
+    {
+        const float before = share;
+        n += 1.0f;
+        share = one_over(n);
+        const float weight = 1.0f - share;
 #pragma unroll
         for (int j = 0; j < 8; j++) {
-            const Moments m = moments_of<decltype(size)::value>(w, count, share, j, shift[j]);
-            Moments all = {s[j], q[j], n, s[j] * before};
-            all.add(m);
-            s[j] = all.s;
-            q[j] = all.q;
+            const float d = (float)w.v[j] - shift[j], e = fmaf(-s[j], before, d);
+            q[j] = fmaf(e * weight, e, q[j]);
+            s[j] += d;
         }
-        n += (float)count;
-    };
-    int64_t p = p0 + t.sub;
-    Vec<T, 8> w[8];
-    for (; p + (int64_t)7 * t.step < p1; p += (int64_t)8 * t.step) {
-#pragma unroll
-        for (int i = 0; i < 8; i++) w[i] = load(x + (p + (int64_t)i * t.step) * a.x_pixel, a);
-        add(std::integral_constant<int, 8>(), w, 8, 0.125f);
     }
-    if (p >= p1) return;
-    int count = 0;                              // the last ones, in twos; past the last it is taken again, and not counted
-#pragma unroll
-    for (int i = 0; i < 8; i++) count += p + (int64_t)i * t.step < p1;
-#pragma unroll
-    for (int k = 0; k < 8; k += 4)
-        if (count > k)
-#pragma unroll
-            for (int i = k; i < k + 4; i++) w[i] = load(x + (p + (int64_t)min(i, count - 1) * t.step) * a.x_pixel, a);
-#pragma unroll
-    for (int i = 0; i < 8; i += 2)
-        if (count > i) add(std::integral_constant<int, 2>(), w + i, min(count - i, 2), count > i + 1 ? 0.5f : 1.0f);
-}
+};
 
 // Adds what the threads of a workgroup that share a chunk have for its
 // channels: channel i's two sums in LDS out[2 i ..].  MOMENTS: they are S and M of the
@@ -349,19 +310,19 @@ template <typename T> __global__ __launch_bounds__(kThreads, 4) void sum_moments
     if (!w.there) return;
     const int64_t p0 = w.block * a.per, p1 = min(a.p, p0 + a.per);
     const Place t = place_of<kThreads>(a, w.tile);
-    float shift[8], s[8], q[8];
-#pragma unroll
-    for (int j = 0; j < 8; j++) s[j] = q[j] = 0.0f;
+    float shift[8];
+    ThreadMoments<T> m = {};
     if (t.works) {
         shift_of<T>(a, w.image, t, shift);
-        moments<T>(a, w.image, p0, p1, t, shift, s, q);
+        const T *x = static_cast<const T *>(a.x) + w.image * a.x_image + t.at;
+        each_pixel<8>(t, p0, p1, [&](int64_t p) { return load(x + p * a.x_pixel, a); }, [&](int64_t, const Vec<T, 8> &v) { m.add(v, shift); });
         if (w.block == 0 && t.sub == 0)
 #pragma unroll
             for (int j = 0; j < 8; j++)
                 if (j >= t.skip && j < a.c) a.shift[w.image * a.c + t.at + j] = shift[j];
     }
     const int c0 = w.tile * a.ct * 8, wide = 2 * min(a.ct * 8, a.c - c0);
-    join_threads<kThreads, true>(a, t, c0, p1 - p0, s, q, turn, out);
+    join_threads<kThreads, true>(a, t, c0, p1 - p0, m.s, m.q, turn, out);
     float *part = a.part + ((w.image * a.blocks + w.block) * a.c + c0) * 2;
     for (int i = threadIdx.x; i < wide; i += kThreads) part[i] = out[i];
 }
@@ -640,35 +601,29 @@ template <typename T, int G, bool HELD> __global__ __launch_bounds__(kOneThreads
     const Place t = place_of<kOneThreads>(a, 0);
     const T *x = static_cast<const T *>(a.x) + image * a.x_image + t.at;
     Vec<T, 8> held[HELD ? kHeld : 1];
-    float near[8], s[8], q[8], scale[8], shift[8], mean[G];
+    float near[8], scale[8], shift[8], mean[G];
+    ThreadMoments<T> m = {};
     load_channels(a, a.gamma, t, 1.0f, scale);              // on their way early
     load_channels(a, a.beta, t, 0.0f, shift);
-#pragma unroll
-    for (int j = 0; j < 8; j++) s[j] = q[j] = 0.0f;
     if (t.works) {
         if constexpr (HELD) {
 #pragma unroll
-            for (int i = 0; i < kHeld; i++) held[i] = load(x + (t.sub + i * t.step < a.p ? t.sub + i * t.step : 0) * a.x_pixel, a);
+            for (int i = 0; i < kHeld; i++)
+                if (t.sub + i * t.step < a.p) held[i] = load(x + (int64_t)(t.sub + i * t.step) * a.x_pixel, a);
             shift_of<T>(a, image, t, near);
-            int count = 0;
 #pragma unroll
-            for (int i = 0; i < kHeld; i++) count += t.sub + i * t.step < a.p;
-#pragma unroll
-            for (int j = 0; j < 8; j++) {
-                const Moments m = moments_of<kHeld>(held, count, one_over((float)count), j, near[j]);
-                s[j] = m.s;
-                q[j] = m.q;
-            }
+            for (int i = 0; i < kHeld; i++)
+                if (t.sub + i * t.step < a.p) m.add(held[i], near);
         } else {
             shift_of<T>(a, image, t, near);
-            moments<T>(a, image, 0, a.p, t, near, s, q);
+            each_pixel<8>(t, 0, a.p, [&](int64_t p) { return load(x + p * a.x_pixel, a); }, [&](int64_t, const Vec<T, 8> &v) { m.add(v, near); });
         }
         if (t.sub == 0)
 #pragma unroll
             for (int j = 0; j < 8; j++)
                 if (j >= t.skip && j < a.c) shifts[t.at + j] = near[j];
     }
-    join_threads<kOneThreads, true>(a, t, 0, a.p, s, q, turn, out);
+    join_threads<kOneThreads, true>(a, t, 0, a.p, m.s, m.q, turn, out);
     group_statistics<kOneThreads>(a, image, shifts, out, means, rstds, true);
     if (!t.works) return;
     coefficients<G>(a, means, rstds, t, mean, scale);

@@ -5,12 +5,12 @@ Tolerances.  e = 2^-24; x is fp32, D the largest difference of two of a
 channel's values and sd the group's spread.  Values are taken as differences d from
 one of a channel's values or a mean of some, so |d| <= D, each rounded by e D.
 A sum of r terms one after the other is off by r / 2 e D at most of the mean
-of its terms.  Eight values (4.4 with the first addition), up to 12 such sums of a
-thread and 12 of threads (6 each, four at a time), blocks of pixels eight at a time,
-rows of 16 (10) and their reciprocals (1.6): a mean is off by 28 e D at most.
+of its terms.  Up to eight values of a thread here (4.4 with the first addition),
+threads four at a time (7), blocks of pixels eight at a time (5), rows of those (10)
+and the reciprocals (1.6): a mean is off by 28 e D at most.
 * variance: squares of differences of such means, every one a part of the spread,
   so 2 x 28 e D / sd of itself (what the mean in the middle is off by counts squared); sums
-  of squares themselves 12 e for eight and less than 20 e for what joins them.
+  of squares themselves 12 e for a thread's and less than 20 e for what joins them.
 * rstd is off by half of what the variance is, and the mean by 28 e D and its own
   rounding.
 """
