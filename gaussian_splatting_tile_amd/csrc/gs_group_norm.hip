@@ -29,17 +29,17 @@ namespace gsi {
 namespace {
 
 constexpr int kThreads = 256, kOneThreads = 512;
-// Four workgroups to a CU, one round: the backward from 8 bits 65 us, 69 with two
-// rounds; the forward 110 and 114 (and 134 with five for four).
+// Four workgroups to a CU, one round (8 x 16384 x 256 backward from 8 bits 66 us, 68 with
+// two; 8 x 65536 x 128 forward 112 and 117, and 151 with five for four).
 constexpr int kBlocks = 1024;
 // Results that the second-level caches do not hold are written past them
-// (backward 80 -> 75 us); smaller ones stay for who reads them next.
+// (8 x 16384 x 256 backward 79 -> 73 us); smaller ones stay for who reads them next.
 constexpr int64_t kStreamBytes = 32 << 20;
 // Channels of a workgroup, in eights, where an image is many workgroups': more
 // would leave each few pixels, and sums as large as what they are sums of.
 constexpr int kTileChunks = 32;
 constexpr int kJoinChannels = 1024, kJoinBlocks = 32;
-constexpr int kTurn = 17;                       // a thread's 16 sums in LDS, in banks of their own (one workgroup, 256 x 64: 8.6 -> 7.7 us)
+constexpr int kTurn = 17;                       // a thread's 16 sums in LDS, in banks of their own (one workgroup, 256 x 64: 9.2 -> 8.8 us)
 constexpr int kHeld = 4;                        // pixels a thread of a single workgroup keeps
 constexpr int64_t kOneChunks = 8192;            // of eight channels: an image of one workgroup
 
@@ -989,7 +989,7 @@ void set_shape(Args &a, const Shape &s, const Plan &w, int es)
 // Whether the workgroups that write join an image's channels themselves: few blocks'
 // sums as they are (3 x 1001 x 90: 17 -> 14 us for the launch less), or, where groups
 // are too few or too wide to be joined by a workgroup each, added up per channel
-// first.  Else a workgroup joins each group (8 x 65536 x 128: 110 us, 119 by channels).
+// first.  Else a workgroup joins each group (8 x 65536 x 128: 112 us, 122 by channels).
 bool few_blocks(const Args &a) { return a.blocks <= kJoinBlocks && (int64_t)a.n * a.blocks <= 1024; }
 bool by_channels(const Args &a) { return a.c <= kJoinChannels && (few_blocks(a) || a.cg > 64 || (int64_t)a.n * a.groups < 64); }
 template <bool MOMENTS> Args joined(const Args &a, hipStream_t s)
