@@ -219,6 +219,7 @@ class ViewReader:
         need += [B.rms_norm_bwd_workspace_bytes(m, width)]
         self.ws = torch.empty(max(need) + 16, dtype=torch.uint8, device=device)
 
+    @torch.no_grad()
     def forward(self, tokens: torch.Tensor, features: torch.Tensor, seen: Optional[torch.Tensor] = None) -> torch.Tensor:
         """tokens' [m][width]; seen [views] uint8 or bool, or None: all."""
         if tokens.shape != (self.m, self.width) or features.shape != (self.views, self.pixels, self.channels):

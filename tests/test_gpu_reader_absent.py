@@ -88,3 +88,16 @@ def test_absent_views_in_a_graph():
         for k, w in want.items():
             assert bool(torch.isfinite(w.float()).all()) and torch.equal(got[k], w), (i, k)
         features[i] = held
+
+
+def test_maps_and_tokens_of_an_encoder_that_torch_differentiates():
+    """The reader's gradients are its own; what comes with a history is taken as it is."""
+    r = H.ViewReader(40, 64, 3, 200, 96, 4, 6, seed=1)
+    tokens, features, d_out = _inputs(torch.bfloat16, 3, 200)
+    seen = torch.tensor([1, 0, 1], dtype=torch.uint8, device="cuda")
+    want = [_step(r, tokens, features, s, d_out) for s in (seen, None)]
+    leaf, scale = features.clone().requires_grad_(), torch.ones((), dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    for s, w in zip((seen, None), want):
+        got = _step(r, tokens * scale, leaf * 1, s, d_out)
+        assert all(torch.equal(got[k], w[k]) for k in w)
+        assert not any(t.requires_grad for t in (r.tokens, r.f, r.out, *got.values()))
