@@ -53,7 +53,7 @@ struct Args {
     Tensor dq, dk, dv;                          // results
     Grid t, tk;                                 // of the forward or of dq, and of dk and dv
     float *lse;                                 // [batch][heads][nq], or NULL
-    const float *lse2, *delta;                  // backward: [batch][heads][nq_pad]
+    const float *lse2, *delta;                  // backward: [batch][heads][nq_pad]; lse times log2 e, of fp32 as it is
     // of splits, as the waves hold them: sums [split][wave][DP / 8][64][4] of out or dq, of
     // dk and of dv, and (forward) maxima and sums of exponentials [split][wave][32][2];
     // wave = (pair * tiles + tile) * waves + wave of the block

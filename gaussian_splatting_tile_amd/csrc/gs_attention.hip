@@ -43,8 +43,8 @@ struct PackJob {                                // [limb][batch][heads][n][dp] o
 struct Prepare {
     PackJob jobs[4];
     int count, d, chunks, lanes, type;          // chunks: of eight values in a packed row
-    // statistics: delta = dout . out, and lse in units of log 2 with what keeps P
-    // of an empty or absent row at 0
+    // statistics: delta = dout . out, and lse (of 16-bit types in units of log 2, times
+    // `shift` powers of it) with what keeps P of an empty or absent row at 0
     Tensor out, dout;
     const float *lse;
     float *lse2, *delta;
@@ -114,7 +114,7 @@ __global__ __launch_bounds__(kThreads) void prepare(Prepare a)
     if (at == 0) {
         const float l = token < a.nq ? a.lse[(int64_t)pair * a.nq + token] : -INFINITY;
         const int64_t to = (int64_t)pair * a.nq_pad + token;
-        a.lse2[to] = l == -INFINITY ? INFINITY : fmaf(l, kLog2e, -a.shift);
+        a.lse2[to] = l == -INFINITY ? INFINITY : a.type == GS_DTYPE_F32 ? l : fmaf(l, kLog2e, -a.shift);
         a.delta[to] = dot;
     }
 }
