@@ -55,7 +55,8 @@ struct Args {
     float *lse;                                 // [batch][heads][nq], or NULL
     const float *lse2, *delta;                  // backward: [batch][heads][nq_pad]; lse times log2 e, of fp32 as it is
     // of splits, as the waves hold them: sums [split][wave][DP / 8][64][4] of out or dq, of
-    // dk and of dv, and (forward) maxima and sums of exponentials [split][wave][32][2];
+    // dk and of dv, and (forward) maxima, as power() takes them, and sums of exponentials
+    // [split][wave][32][2];
     // wave = (pair * tiles + tile) * waves + wave of the block
     float *part, *part_k, *part_v, *ml;
     const int32_t *lengths;
@@ -65,6 +66,17 @@ struct Args {
     int type;                                   // gs_dtype of the tensors
     float c, scale;                             // scale * log2 e, scale
 };
+
+// exp(S - x) of a score s, S = scale s.  x is in units of log 2; fp32's in natural ones: the
+// difference from it is rounded once, and small where the result is not, while the
+// products' own roundings, of the size of S, would go into lse and gradients (S = 60:
+// 5e-6 of them).  The second product costs fp32 1 % (2048 x 8192 x 8 heads x 64 188 -> 191 us, backward
+// over 4096 states 350 -> 354); 16-bit types save it.
+template <int NL> __device__ __forceinline__ float unit(const Args &a) { return NL > 1 ? a.scale : a.c; }
+template <int NL> __device__ __forceinline__ float power(float x) { return __builtin_amdgcn_exp2f(NL > 1 ? x * kLog2e : x); }
+template <int NL> __device__ __forceinline__ float power(const Args &a, float s, float x) { return power<NL>(fmaf(s, unit<NL>(a), -x)); }
+// lse from a maximum in those units and the sum of exponentials of differences from it.
+template <int NL> __device__ __forceinline__ float lse_of(float m, float sum) { return NL > 1 ? fmaf(log2f(sum), kLn2, m) : (m + log2f(sum)) * kLn2; }
 
 // ---- tiles --------------------------------------------------------------------
 // [rows][CH] chunks of 16 bytes (8 values); chunk c of row r sits at c ^ swz(r).

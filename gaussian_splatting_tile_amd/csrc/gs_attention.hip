@@ -171,8 +171,8 @@ __device__ __forceinline__ void store4(const JoinArgs &a, const Tensor &tensor, 
         if (t.at + j < a.d) store_from_float(to, a.type, t.row + t.at + j, v[j]);
 }
 
-// Partial softmaxes (SOFT: sums relative to their own maxima), or plain sums.
-template <int SW, bool SOFT> __global__ __launch_bounds__(kThreads) void join_splits(JoinArgs a)
+// Partial softmaxes (sums relative to their own maxima; NL as power() takes it), or plain sums (NL 0).
+template <int SW, int NL> __global__ __launch_bounds__(kThreads) void join_splits(JoinArgs a)
 {
     constexpr int kUnits = kThreads / 64 / SW;
     __shared__ gemm::f4 turn[SW > 1 ? kThreads : 1];
@@ -191,6 +191,7 @@ template <int SW, bool SOFT> __global__ __launch_bounds__(kThreads) void join_sp
     const float2 *ml = reinterpret_cast<const float2 *>(job.ml) + wave * 32 + (lane & 31);
     const int64_t next = job.waves * a.per * 64, next_ml = job.waves * 32;
     gemm::f4 v = {0, 0, 0, 0};
+    constexpr bool SOFT = NL > 0;
     float sum = 0.0f, m = -INFINITY, base = 0.0f;
     if constexpr (SOFT) {
         for (int s = sub; s < splits; s += 8 * SW) {
@@ -223,7 +224,7 @@ template <int SW, bool SOFT> __global__ __launch_bounds__(kThreads) void join_sp
             if (s + i * SW < splits) {
                 if constexpr (SOFT) {
                     // NaN scores have no maximum, but a sum: it goes on
-                    const float f = w[i].x == -INFINITY && w[i].y != 0.0f ? 1.0f : __builtin_amdgcn_exp2f(w[i].x - base);
+                    const float f = w[i].x == -INFINITY && w[i].y != 0.0f ? 1.0f : power<NL>(w[i].x - base);
                     sum = fmaf(w[i].y, f, sum);
                     v += x[i] * f;
                 } else {
@@ -246,7 +247,7 @@ template <int SW, bool SOFT> __global__ __launch_bounds__(kThreads) void join_sp
     const Target t = target_of(job, wave, unit, lane);
     if constexpr (SOFT) {
         v *= m == -INFINITY && sum == 0.0f ? 0.0f : 1.0f / sum;
-        if (job.lse && t.there && unit == 0 && lane < 32) job.lse[t.stat] = (m + log2f(sum)) * kLn2;
+        if (job.lse && t.there && unit == 0 && lane < 32) job.lse[t.stat] = lse_of<NL>(m, sum);
     }
     store4(a, job.to, t, v);
 }
@@ -584,10 +585,17 @@ hipError_t launch_join(const JoinArgs &j, bool soft, hipStream_t s)
     bool wide = false;                          // four waves to a unit
     for (int i = 0; i < j.count; i++) wide = wide || j.jobs[i].splits > 8;
     const dim3 grid = grid_of(wide ? j.units : (j.units + 3) / 4, kThreads);
-    if (soft && wide) join_splits<4, true><<<grid, kThreads, 0, s>>>(j);
-    else if (soft) join_splits<1, true><<<grid, kThreads, 0, s>>>(j);
-    else if (wide) join_splits<4, false><<<grid, kThreads, 0, s>>>(j);
-    else join_splits<1, false><<<grid, kThreads, 0, s>>>(j);
+    if (soft && j.type == GS_DTYPE_F32) {
+        if (wide) join_splits<4, 3><<<grid, kThreads, 0, s>>>(j);
+        else join_splits<1, 3><<<grid, kThreads, 0, s>>>(j);
+    } else if (soft) {
+        if (wide) join_splits<4, 1><<<grid, kThreads, 0, s>>>(j);
+        else join_splits<1, 1><<<grid, kThreads, 0, s>>>(j);
+    } else if (wide) {
+        join_splits<4, 0><<<grid, kThreads, 0, s>>>(j);
+    } else {
+        join_splits<1, 0><<<grid, kThreads, 0, s>>>(j);
+    }
     return hipGetLastError();
 }
 

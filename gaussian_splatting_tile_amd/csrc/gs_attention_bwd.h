@@ -56,15 +56,6 @@ template <int KIND> struct ColumnScale {
     __device__ __forceinline__ float inverse() const { return KIND == gemm::kF16 ? 1.0f / f : 1.0f; }
 };
 
-// P of a score.  fp32's lse is in natural units: the difference from it is rounded once, and
-// small where P is not; in units of log 2 the products' own roundings, of the size of S
-// and lse, would go into P (S = 60: 5e-6 of it; 2048 x 4096 x 8 heads x 64 350 us, not
-// 354).  16-bit types save the second product.
-template <int NL> __device__ __forceinline__ float probability(const Args &a, float s, float lse)
-{
-    return NL > 1 ? __builtin_amdgcn_exp2f(fmaf(s, a.scale, -lse) * kLog2e) : __builtin_amdgcn_exp2f(fmaf(s, a.c, -lse));
-}
-
 template <int KIND, int NL> __device__ __forceinline__ void pack16(const float v[16], i4 (&w)[2][NL])
 {
 #pragma unroll
@@ -136,7 +127,7 @@ template <int KIND, int NL, int DP, int NW> __device__ __forceinline__ void dq_b
             const f16v dp = over_d<KIND, NL, DP, LD::kBytes>(vt, u * 32, g, lane);
             float v[16];
 #pragma unroll
-            for (int i = 0; i < 16; i++) v[i] = probability<NL>(a, s[i], lse) * (dp[i] - delta);
+            for (int i = 0; i < 16; i++) v[i] = power<NL>(a, s[i], lse) * (dp[i] - delta);
             if (seen != whole) {
                 const uint32_t bits = (uint32_t)(seen >> (u * 32)) >> (4 * (lane >> 5));
 #pragma unroll
@@ -227,7 +218,7 @@ template <int KIND, int NL, int DP, int NW> __device__ __forceinline__ void dkv_
             for (int j = 0; j < 4; j++) {
                 const gemm::f4 l = *reinterpret_cast<const gemm::f4 *>(lse + u * 32 + j * 8 + (lane >> 5) * 4);
 #pragma unroll
-                for (int i = 0; i < 4; i++) p[j * 4 + i] = probability<NL>(a, s[j * 4 + i], l[i]);
+                for (int i = 0; i < 4; i++) p[j * 4 + i] = power<NL>(a, s[j * 4 + i], l[i]);
             }
             const f16v dp = over_d<KIND, NL, DP, LD::kBytes>(gt, u * 32, v, lane);
 #pragma unroll

@@ -103,7 +103,7 @@ template <int KIND, int NL, int DP, int NW> __global__ __launch_bounds__(NW * 64
                     float v[8];
 #pragma unroll
                     for (int i = 0; i < 8; i++) {
-                        v[i] = __builtin_amdgcn_exp2f(fmaf(s[u][j * 8 + i], a.c, -base));
+                        v[i] = power<NL>(a, s[u][j * 8 + i], base);
                         more += v[i];
                     }
                     pack8<KIND, NL>(v, w[u][j]);
@@ -120,7 +120,7 @@ template <int KIND, int NL, int DP, int NW> __global__ __launch_bounds__(NW * 64
             for (int u = 0; u < KS; u++)
 #pragma unroll
                 for (int i = 0; i < 16; i++) top = fmaxf(top, s[u][i]);
-            const float up = fmaxf(m, pair_max(top * a.c) - kBelow<KIND>), now = up == -INFINITY ? 0.0f : up, f = __builtin_amdgcn_exp2f(m - now);
+            const float up = fmaxf(m, pair_max(top * unit<NL>(a)) - kBelow<KIND>), now = up == -INFINITY ? 0.0f : up, f = power<NL>(m - now);
             m = up;
             base = now;
             sum *= f;
@@ -143,7 +143,7 @@ template <int KIND, int NL, int DP, int NW> __global__ __launch_bounds__(NW * 64
     if (!there) return;
     const float f = m == -INFINITY && sum == 0.0f ? 0.0f : 1.0f / sum;
     store_columns<DP>(const_cast<void *>(a.out.p), a.type, it.batch * a.out.sb + token * a.out.sr + head * a.out.sh, o, f, a.d, lane);
-    if (a.lse && lane < 32) a.lse[((int64_t)it.batch * a.heads + head) * a.nq + token] = (m + log2f(sum)) * kLn2;
+    if (a.lse && lane < 32) a.lse[((int64_t)it.batch * a.heads + head) * a.nq + token] = lse_of<NL>(m, sum);
 }
 
 template <int KIND, int NL, int DP> hipError_t launch_fwd_waves(const Args &a, hipStream_t s)
